@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libtq2_gb300.so")
@@ -29,6 +30,7 @@ TQ2_ERR_UNSUPPORTED_DEVICE = 4
 TQ2_ERR_CUDA = 5
 TQ2_ERR_TIMEOUT = 6
 TQ2_ERR_TOO_LARGE = 7
+TQ2_ERR_BAD_BATCH = 8
 TQ2_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 TQ2_KERNEL_AUTO = 0
@@ -40,6 +42,10 @@ TQ2_KERNEL_TC_DIRECT = 5
 TQ2_KERNEL_SKINNY_MMA = 6
 KERNEL_NAMES = {0: "auto", 1: "gemv", 2: "skinny", 3: "tc", 4: "f32ref", 5: "tc_direct", 6: "skinny_mma"}
 
+TQ2_F32 = 0
+TQ2_F16 = 1
+TQ2_BF16 = 2
+
 # Every symbol include/tq2.h declares.
 EXPORTS = (
     "tq2_soa_bytes", "tq2_status_string", "tq2_reformat_aos_to_soa", "tq2_gemv", "tq2_gemv_resident",
@@ -49,6 +55,8 @@ EXPORTS = (
     "tq2_gemm_noalloc", "tq2_quantize_f32", "tq2_gate_up_swiglu", "tq2_gate_up_swiglu_resident",
     "tq2_act16_from_f32",
     "tq2_act16_to_f32", "tq2_gemm_act16", "tq2_attention_f32",
+    "tq2_rope_turns", "tq2_rope_axes", "tq2_kv_append", "tq2_attention_paged",
+    "tq2_attention_paged_workspace_bytes",
 )
 
 
@@ -107,6 +115,18 @@ def _load():
         f = getattr(L, name)
         f.restype = i32
         f.argtypes = [vp, vp, vp, i64, i64, i64, vp]
+    # tq2_heads, tq2_rope, tq2_batch and tq2_kv_cache go as packed bytes (see the functions that make them)
+    ch = ctypes.c_char_p
+    L.tq2_rope_turns.restype = i32
+    L.tq2_rope_turns.argtypes = [vp, vp, i64]
+    L.tq2_rope_axes.restype = i32
+    L.tq2_rope_axes.argtypes = [ch, ch, ch, ch, ch, ch, vp, ch, i64, i64, i32, vp]
+    L.tq2_kv_append.restype = i32
+    L.tq2_kv_append.argtypes = [ch, ch, ch, ch, vp, ch, ch, ch, vp]
+    L.tq2_attention_paged.restype = i32
+    L.tq2_attention_paged.argtypes = [ch, ch, ch, ch, ctypes.c_float, i64, i32, vp, ctypes.c_size_t, vp]
+    L.tq2_attention_paged_workspace_bytes.restype = ctypes.c_size_t
+    L.tq2_attention_paged_workspace_bytes.argtypes = [i64, ch, ch]
     L.tq2_gemm_noalloc.restype = i32
     L.tq2_gemm_noalloc.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
     return L
@@ -250,6 +270,63 @@ def tq2_gemm_with(kernel: int, w_soa, x, residual, out, m: int, n: int, k: int,
 
 
 # ---------------------------------------------------------------------------
+# Positions, key/value cache and its attention.  The C structs are passed as
+# packed bytes: tq2_heads(...), tq2_rope(...), tq2_kv_cache(...) and tq2_batch(...)
+# return them from the fields that include/tq2.h documents.
+
+
+def tq2_heads(data, heads: int, token_stride: int, head_stride: int, dtype: int,
+              _pack=struct.Struct("=qqqqi4x").pack) -> bytes:
+    return _pack(_ptr(data) or 0, heads, token_stride, head_stride, dtype)
+
+
+def tq2_rope(turns, axis, pairs: int, axes: int = 1, interleaved: int = 0,
+             _pack=struct.Struct("=qqqii").pack) -> bytes:
+    return _pack(_ptr(turns) or 0, _ptr(axis) or 0, pairs, axes, interleaved)
+
+
+def tq2_kv_cache(k, v, pages: int, page_size: int, heads: int, dim: int, page_stride: int, slot_stride: int,
+                 head_stride: int, dtype: int, _pack=struct.Struct("=qqqqqqqqqi4x").pack) -> bytes:
+    return _pack(_ptr(k) or 0, _ptr(v) or 0, pages, page_size, heads, dim, page_stride, slot_stride, head_stride,
+                 dtype)
+
+
+def tq2_batch(q_start, kv_len, page_table, seqs: int, tokens: int, max_q: int, max_kv: int, table_stride: int,
+              _pack=struct.Struct("=qqqqqqqq").pack) -> bytes:
+    return _pack(_ptr(q_start) or 0, _ptr(kv_len) or 0, _ptr(page_table) or 0, seqs, tokens, max_q, max_kv,
+                 table_stride)
+
+
+def tq2_rope_turns(inv_freq):
+    """Host: the 64-bit fractions of a turn (numpy uint64) of inv_freq (radians per position, numpy float64)."""
+    import numpy as np
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64).reshape(-1)
+    turns = np.empty(f.size, dtype=np.uint64)
+    _check(lib.tq2_rope_turns(f.ctypes.data, turns.ctypes.data, f.size), "tq2_rope_turns")
+    return turns
+
+
+def tq2_rope_axes(q, q_out, k, k_out, v, v_out, positions, rope: bytes, tokens: int, dim: int, inverse: int = 0,
+                  stream=None) -> None:
+    _check(lib.tq2_rope_axes(q, q_out, k, k_out, v, v_out, _ptr(positions), rope, tokens, dim, inverse,
+                             _stream(stream)), "tq2_rope_axes")
+
+
+def tq2_kv_append(q, q_out, k, v, positions, rope, batch: bytes, cache: bytes, stream=None) -> None:
+    _check(lib.tq2_kv_append(q, q_out, k, v, _ptr(positions), rope, batch, cache, _stream(stream)), "tq2_kv_append")
+
+
+def tq2_attention_paged(q, out, cache: bytes, batch: bytes, scale: float, window: int = 0, causal: int = 1,
+                        workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    _check(lib.tq2_attention_paged(q, out, cache, batch, scale, window, causal, _ptr(workspace), workspace_bytes,
+                                   _stream(stream)), "tq2_attention_paged")
+
+
+def tq2_attention_paged_workspace_bytes(heads: int, cache: bytes, batch: bytes) -> int:
+    return int(lib.tq2_attention_paged_workspace_bytes(heads, cache, batch))
+
+
+# ---------------------------------------------------------------------------
 # Tensor-level conveniences (shape and dtype checks, then the calls above).
 
 
@@ -307,4 +384,162 @@ def matmul(w_soa, x, residual=None, *, n: int, k: int, out=None, kernel: int = T
         tq2_gemm_ws(w_soa, x, residual, out, m, n, k, workspace, workspace.numel(), stream)
     else:
         tq2_gemm_with(kernel, w_soa, x, residual, out, m, n, k, stream)
+    return out
+
+
+# ---------------------------------------------------------------------------
+# Positions, key/value cache and its attention on torch tensors.
+
+_DTYPE = None
+
+
+def _dtype_of(t) -> int:
+    global _DTYPE
+    if _DTYPE is None:
+        import torch
+        _DTYPE = {torch.float32: TQ2_F32, torch.float16: TQ2_F16, torch.bfloat16: TQ2_BF16}
+    try:
+        return _DTYPE[t.dtype]
+    except KeyError:
+        raise ValueError(f"float32, float16 or bfloat16 expected, got {t.dtype}") from None
+
+
+def _heads(t, name: str, tokens: int, dim: int) -> bytes:
+    """The tq2_heads of a [tokens, heads, dim] CUDA tensor (any strides, the last one 1)."""
+    shape, strides = t.shape, t.stride()
+    if not t.is_cuda or len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
+        raise ValueError(f"{name} must be a CUDA tensor [{tokens}, heads, {dim}], got {t.device} {tuple(shape)}")
+    if strides[2] != 1 and dim != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return tq2_heads(t.data_ptr(), shape[1], strides[0], strides[1], _dtype_of(t))
+
+
+def _table(t, name: str, dtype: str, ndim: int):
+    if not t.is_cuda or str(t.dtype) != dtype or t.dim() != ndim or (t.numel() and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be a CUDA {dtype} tensor of {ndim} dimension(s) with a contiguous last one")
+    return t
+
+
+class Rope:
+    """Rotary positions: ``inv_freq`` (radians per position of each pair of a head, host values or a tensor), the axis
+    of each pair (``axis``, default 0 for all) among ``axes`` positions per token, and whether pairs are neighbours
+    (``interleaved``) or lie half the rotated width apart.  Holds the device table; see tq2_rope in include/tq2.h."""
+
+    def __init__(self, inv_freq, axis=None, *, axes: int = 1, interleaved: bool = False, device="cuda"):
+        import numpy as np
+        import torch
+        f = inv_freq.detach().cpu().numpy() if isinstance(inv_freq, torch.Tensor) else inv_freq
+        turns = tq2_rope_turns(np.asarray(f, dtype=np.float64))
+        self.pairs, self.axes, self.interleaved = int(turns.size), int(axes), bool(interleaved)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.axis = None
+        if axis is not None:
+            a = torch.as_tensor(axis).detach().cpu().reshape(-1)
+            if a.numel() != self.pairs or (self.pairs and not 0 <= int(a.min()) <= int(a.max()) < self.axes):
+                raise ValueError(f"axis must hold {self.pairs} values from 0 to {self.axes - 1}")
+            self.axis = a.to(torch.uint8).to(device)
+        self.packed = tq2_rope(self.turns, self.axis, self.pairs, self.axes, int(self.interleaved))
+
+    def positions(self, positions, tokens: int):
+        """``positions`` as checked int64 [tokens, axes] (one axis: [tokens] too), or None."""
+        if positions is None:
+            return None
+        if (not positions.is_cuda or str(positions.dtype) != "torch.int64" or not positions.is_contiguous()
+                or positions.numel() != tokens * self.axes):
+            raise ValueError(f"positions must be a contiguous CUDA int64 tensor [{tokens}, {self.axes}]")
+        return positions
+
+
+class KVCache:
+    """A paged cache: ``k`` and ``v`` of shape [pages, page_size, heads, dim] and the same strides (transposed views of
+    [pages, heads, page_size, dim] included), float16 or bfloat16.  Holds the tensors; see tq2_kv_cache."""
+
+    def __init__(self, k, v):
+        if k.dim() != 4 or k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+            raise ValueError("k and v must be [pages, page_size, heads, dim] tensors of one type, shape and strides")
+        if not (k.is_cuda and v.is_cuda) or (k.stride(3) != 1 and k.shape[3] != 1):
+            raise ValueError("k and v must be CUDA tensors with a contiguous last dimension")
+        self.k, self.v = k, v
+        self.pages, self.page_size, self.heads, self.dim = (int(n) for n in k.shape)
+        self.dtype = k.dtype
+        self.packed = tq2_kv_cache(k, v, self.pages, self.page_size, self.heads, self.dim, *k.stride()[:3],
+                                   _dtype_of(k))
+
+
+class PagedBatch:
+    """The sequences of one step: int32 device tables ``q_start`` [seqs + 1], ``kv_len`` [seqs] (the new tokens'
+    keys included) and ``page_table`` [seqs, entries], with the host's bounds.  Holds the tables, whose values may
+    change between calls (a captured graph reads them anew); see tq2_batch."""
+
+    def __init__(self, q_start, kv_len, page_table, *, tokens: int, max_q: int, max_kv: int):
+        _table(q_start, "q_start", "torch.int32", 1)
+        _table(kv_len, "kv_len", "torch.int32", 1)
+        _table(page_table, "page_table", "torch.int32", 2)
+        seqs = kv_len.numel()
+        if q_start.numel() != seqs + 1 or page_table.shape[0] != seqs:
+            raise ValueError(f"{seqs} sequences need q_start [{seqs + 1}] and page_table [{seqs}, entries]")
+        if seqs > 1 and page_table.stride(0) != page_table.shape[1]:
+            raise ValueError("page_table must be contiguous")
+        self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
+        self.seqs, self.tokens, self.max_q, self.max_kv = int(seqs), int(tokens), int(max_q), int(max_kv)
+        self.packed = tq2_batch(q_start, kv_len, page_table, self.seqs, self.tokens, self.max_q, self.max_kv,
+                                page_table.shape[1])
+
+
+def rope_axes(q, k=None, v=None, *, positions, rope: Rope, out=None, inverse: bool = False, stream=None):
+    """Rotate q and k [tokens, heads, dim] by their positions and copy v, into ``out`` (a sequence of as many tensors,
+    of any layout and another type if wanted; default: new contiguous ones).  Returns the outputs as a tuple.
+    ``inverse`` is the gradient: the gradients of the outputs go in, those of the inputs come out."""
+    import torch
+    tokens, _, dim = q.shape
+    ins = [t for t in (q, k, v) if t is not None]
+    if out is None:
+        out = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ins]
+    if len(out) != len(ins):
+        raise ValueError(f"{len(ins)} outputs expected, got {len(out)}")
+    args, o = [], iter(out)
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        args += [None, None] if t is None else [_heads(t, name, tokens, dim), _heads(next(o), name + "'s output", tokens,
+                                                                                    dim)]
+    tq2_rope_axes(*args, rope.positions(positions, tokens), rope.packed, tokens, dim, int(inverse), stream)
+    return tuple(out)
+
+
+def kv_append(k, v, cache: KVCache, batch: PagedBatch, *, rope: Rope = None, positions=None, q=None, q_out=None,
+              stream=None):
+    """Store a step's k (rotated by ``rope``) and v [tokens, heads, dim] in ``cache``; returns q rotated (in ``q_out``,
+    default: a new tensor of the cache's type), or None without q.  ``positions`` [tokens, axes] default to each
+    token's key index."""
+    import torch
+    tokens, dim = batch.tokens, cache.dim
+    qp = qo = None
+    if q is not None:
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=cache.dtype, device=q.device)
+        qp, qo = _heads(q, "q", tokens, dim), _heads(q_out, "q_out", tokens, dim)
+    pos = rope.positions(positions, tokens) if rope is not None else None
+    tq2_kv_append(qp, qo, _heads(k, "k", tokens, dim), _heads(v, "v", tokens, dim), pos,
+                  None if rope is None else rope.packed, batch.packed, cache.packed, stream)
+    return q_out if q is not None else None
+
+
+def attention_paged_workspace(q, cache: KVCache, batch: PagedBatch):
+    """A device workspace for attention_paged of these arguments (torch uint8 tensor; None if not needed)."""
+    import torch
+    nbytes = tq2_attention_paged_workspace_bytes(q.shape[1], cache.packed, batch.packed)
+    return torch.empty(nbytes, dtype=torch.uint8, device=q.device) if nbytes else None
+
+
+def attention_paged(q, cache: KVCache, batch: PagedBatch, *, out=None, scale: float = None, window: int = 0,
+                    causal: bool = True, workspace=None, stream=None):
+    """Attention of the step's tokens q [tokens, heads, dim] over the paged cache, causal by default and within the
+    last ``window`` keys if given; ``scale`` defaults to 1/sqrt(dim).  Returns ``out`` (default: a new tensor of q's
+    type; a float32 one keeps more of the softmax's bits)."""
+    import torch
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    tokens, dim = batch.tokens, cache.dim
+    tq2_attention_paged(_heads(q, "q", tokens, dim), _heads(out, "out", tokens, dim), cache.packed, batch.packed,
+                        dim ** -0.5 if scale is None else scale, window, int(causal), workspace,
+                        0 if workspace is None else workspace.numel(), stream)
     return out

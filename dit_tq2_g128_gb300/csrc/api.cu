@@ -6,6 +6,7 @@
 // K a multiple of 128.  Unlike the page, every failure is a returned status
 // and there is no CPU fallback.
 #include <atomic>
+#include <cmath>
 #include <initializer_list>
 #include <cstdint>
 #include <cstring>
@@ -16,7 +17,7 @@
 namespace {
 
 // Device status word: kernels OR TQ2_ERR_TIMEOUT into it when a bounded wait
-// gives up.  Static device memory of this module (one word per device).
+// gives up, TQ2_ERR_BAD_BATCH (a bit of its own) when a batch's tables are out of range.  Static device memory of this module (one word per device).
 __device__ unsigned int g_device_status;
 
 std::atomic<uint64_t> g_wait_ns{2000000000ull};
@@ -164,6 +165,7 @@ const char *tq2_status_string(int status) {
         case TQ2_ERR_CUDA: return "TQ2_ERR_CUDA: CUDA launch or runtime error";
         case TQ2_ERR_TIMEOUT: return "TQ2_ERR_TIMEOUT: a bounded device-side wait expired";
         case TQ2_ERR_TOO_LARGE: return "TQ2_ERR_TOO_LARGE: the shape needs more scratch than tq2_gemm_noalloc has";
+        case TQ2_ERR_BAD_BATCH: return "TQ2_ERR_BAD_BATCH: a length, offset or page in a batch's device tables is out of range";
         default: return "unknown tq2 status";
     }
 }
@@ -180,7 +182,8 @@ int tq2_device_status(void *stream) {
     unsigned int v = 0, zero = 0;
     if (cudaMemcpy(&v, d.status, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return TQ2_ERR_CUDA;
     if (cudaMemcpy(d.status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return TQ2_ERR_CUDA;
-    return (v & TQ2_ERR_TIMEOUT) == TQ2_ERR_TIMEOUT ? TQ2_ERR_TIMEOUT : TQ2_OK;
+    if ((v & TQ2_ERR_TIMEOUT) == TQ2_ERR_TIMEOUT) return TQ2_ERR_TIMEOUT;
+    return (v & TQ2_ERR_BAD_BATCH) ? TQ2_ERR_BAD_BATCH : TQ2_OK;
 }
 
 int tq2_select_kernel(int64_t m, int64_t n, int64_t k) {
@@ -454,6 +457,380 @@ int tq2_gemv_resident(const void *w_soa, const float *x, const float *residual, 
 int tq2_gemm_f32ref(const void *w_soa, const float *x, const float *residual, float *out,
                     int64_t m, int64_t n, int64_t k, void *stream) {
     return tq2_gemm_with(TQ2_KERNEL_F32REF, w_soa, x, residual, out, m, n, k, stream);
+}
+
+// ---------------------------------------------------------------------------
+// positions, key/value cache and its attention
+
+namespace {
+
+constexpr int64_t kMaxHeads = 16384;
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+
+size_t dtype_bytes(int dtype) { return dtype == TQ2_F32 ? 4 : 2; }
+bool dtype_ok(int dtype) { return dtype == TQ2_F32 || dtype == TQ2_F16 || dtype == TQ2_BF16; }
+
+// The elements of a view whose innermost `dim` are contiguous are distinct: with
+// the strides in order, each steps over all that lies below it.
+bool distinct(int64_t dim, int64_t n0, int64_t s0, int64_t n1, int64_t s1) {
+    if (n0 == 1) return n1 == 1 || s1 >= dim;
+    if (n1 == 1) return s0 >= dim;
+    if (s0 > s1) return s1 >= dim && s0 >= (n1 - 1) * s1 + dim;
+    return s0 >= dim && s1 >= (n0 - 1) * s0 + dim;
+}
+
+int check_view(const tq2_heads *v, int64_t tokens, int64_t dim, bool output) {
+    if (!v->data || !dtype_ok(v->dtype)) return TQ2_ERR_INVALID_ARG;
+    if (v->heads < 1 || v->heads > kMaxHeads || v->token_stride < 0 || v->head_stride < 0 ||
+        v->token_stride > kMaxStride || v->head_stride > kMaxStride)
+        return TQ2_ERR_INVALID_ARG;
+    if (output && !distinct(dim, tokens, v->token_stride, v->heads, v->head_stride)) return TQ2_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(v->data) % dtype_bytes(v->dtype)) return TQ2_ERR_MISALIGNED;
+    return TQ2_OK;
+}
+
+// A stride along an axis of one element says nothing: such strides become 0.
+tq2_heads plain_view(const tq2_heads *v, int64_t tokens) {
+    tq2_heads r = *v;
+    if (tokens == 1) r.token_stride = 0;
+    if (r.heads == 1) r.head_stride = 0;
+    return r;
+}
+tq2_kv_cache plain_cache(const tq2_kv_cache *c) {
+    tq2_kv_cache r = *c;
+    if (r.pages == 1) r.page_stride = 0;
+    if (r.page_size == 1) r.slot_stride = 0;
+    if (r.heads == 1) r.head_stride = 0;
+    return r;
+}
+
+bool same_view(const tq2_heads *a, const tq2_heads *b) {
+    return a->data == b->data && a->dtype == b->dtype && a->heads == b->heads &&
+           a->token_stride == b->token_stride && a->head_stride == b->head_stride;
+}
+
+// Whether two views share no byte: their extents lie apart, or they are different
+// columns of rows with one stride (slices of one fused projection).
+bool views_apart(const tq2_heads *a, const tq2_heads *b, int64_t tokens, int64_t dim) {
+    const size_t ea = dtype_bytes(a->dtype), eb = dtype_bytes(b->dtype);
+    const size_t wa = size_t((a->heads - 1) * a->head_stride + dim) * ea;
+    const size_t wb = size_t((b->heads - 1) * b->head_stride + dim) * eb;
+    const size_t ra = size_t(a->token_stride) * ea, rb = size_t(b->token_stride) * eb;
+    if (!overlaps(a->data, size_t(tokens - 1) * ra + wa, b->data, size_t(tokens - 1) * rb + wb)) return true;
+    if (ra != rb || wa > ra || wb > ra) return false;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a->data), y = reinterpret_cast<uintptr_t>(b->data);
+    const size_t d = y >= x ? (y - x) % ra : (ra - (x - y) % ra) % ra;  // b's columns, from a's first
+    return d >= wa && d + wb <= ra;
+}
+
+// bytes from the first to the last element of a cache plane
+size_t plane_bytes(const tq2_kv_cache *c) {
+    return size_t((c->pages - 1) * c->page_stride + (c->page_size - 1) * c->slot_stride +
+                  (c->heads - 1) * c->head_stride + c->dim) * 2;
+}
+
+bool view_in_plane(const tq2_heads *v, int64_t tokens, const tq2_kv_cache *c, const void *plane) {
+    const size_t n = size_t((tokens - 1) * v->token_stride + (v->heads - 1) * v->head_stride + c->dim) *
+                     dtype_bytes(v->dtype);
+    return overlaps(v->data, n, plane, plane_bytes(c));
+}
+
+int check_cache(const tq2_kv_cache *c) {
+    if (!c->k || !c->v || (c->dtype != TQ2_F16 && c->dtype != TQ2_BF16)) return TQ2_ERR_INVALID_ARG;
+    if (c->dim < 8 || c->dim > 128 || c->dim % 8 || c->heads < 1 || c->heads > kMaxHeads) return TQ2_ERR_INVALID_ARG;
+    if (c->pages < 1 || c->pages > INT32_MAX || c->page_size < 1 || c->page_size > (1 << 20)) return TQ2_ERR_INVALID_ARG;
+    int64_t n[3] = {c->pages, c->page_size, c->heads}, s[3] = {c->page_stride, c->slot_stride, c->head_stride};
+    for (int i = 0; i < 3; ++i)
+        if (s[i] < 0 || s[i] > kMaxStride / 8 || (s[i] && n[i] > (int64_t(1) << 44) / s[i])) return TQ2_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i)  // ascending strides
+        for (int j = i + 1; j < 3; ++j)
+            if (s[j] < s[i]) {
+                const int64_t tn = n[i], ts = s[i];
+                n[i] = n[j], s[i] = s[j], n[j] = tn, s[j] = ts;
+            }
+    int64_t below = c->dim;
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] == 1) continue;
+        if (s[i] < below) return TQ2_ERR_INVALID_ARG;
+        below += (n[i] - 1) * s[i];
+    }
+    if (!aligned16(c->k) || !aligned16(c->v) || c->page_stride % 8 || c->slot_stride % 8 || c->head_stride % 8)
+        return TQ2_ERR_MISALIGNED;
+    return TQ2_OK;
+}
+
+// shape checks of a batch (its pointers are looked at only where there is work)
+int check_batch_shape(const tq2_batch *b, bool *noop) {
+    *noop = false;
+    if (!b || b->seqs < 0 || b->seqs > (1 << 20) || b->tokens < 0 || b->tokens > kMaxTokens || b->max_q < 0 ||
+        b->max_q > kMaxTokens || b->max_kv < 0 || b->max_kv > kMaxTokens || b->table_stride < 0 ||
+        b->table_stride > INT32_MAX)
+        return TQ2_ERR_INVALID_ARG;
+    if (b->seqs == 0 || b->tokens == 0 || b->max_q == 0) *noop = true;
+    return TQ2_OK;
+}
+
+int check_batch(const tq2_batch *b) {
+    if (!b->q_start || !b->kv_len || (!b->page_table && b->table_stride)) return TQ2_ERR_INVALID_ARG;
+    for (const int32_t *p : {b->q_start, b->kv_len, b->page_table})
+        if (reinterpret_cast<uintptr_t>(p) % 4) return TQ2_ERR_MISALIGNED;
+    return TQ2_OK;
+}
+
+tq2::BatchView batch_view(const tq2_batch *b, const tq2_kv_cache *c) {
+    tq2::BatchView v = {};
+    v.q_start = b->q_start;
+    v.kv_len = b->kv_len;
+    v.page_table = b->page_table;
+    v.tokens = b->tokens;
+    v.table_stride = b->table_stride;
+    v.pages = c->pages;
+    v.seqs = int(b->seqs);
+    v.max_q = int(b->max_q < b->tokens ? b->max_q : b->tokens);
+    v.max_kv = int(b->max_kv);
+    v.page_size = int(c->page_size);
+    return v;
+}
+
+// rope may be NULL (no rotation); positions_needed: NULL positions are refused
+int check_rope(const tq2_rope *r, const int64_t *positions, int64_t dim, bool positions_needed) {
+    if (!r) return TQ2_OK;
+    if (r->pairs < 0 || 2 * r->pairs > dim || r->axes < 1 || r->axes > 16) return TQ2_ERR_INVALID_ARG;
+    if (r->pairs == 0) return TQ2_OK;
+    if (!r->turns || (!positions && (positions_needed || r->axes != 1))) return TQ2_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(r->turns) % 8 || reinterpret_cast<uintptr_t>(positions) % 8)
+        return TQ2_ERR_MISALIGNED;
+    return TQ2_OK;
+}
+
+void set_rope(tq2::RopeArgs *a, const tq2_rope *r, const int64_t *positions, int64_t dim) {
+    a->dim = int(dim);
+    a->axes = 1;
+    if (!r) return;
+    a->positions = positions;
+    a->turns = r->turns;
+    a->axis = r->axis;
+    a->axes = r->axes;
+    a->pairs = int(r->pairs);
+    a->interleaved = r->interleaved != 0;
+}
+
+void add_segment(tq2::RopeArgs *a, const tq2_heads *in, const tq2_heads *out, bool turned) {
+    tq2::RopeSegment &g = a->seg[a->nseg++];
+    g.in = in->data;
+    g.in_token = in->token_stride;
+    g.in_head = in->head_stride;
+    g.heads = int(in->heads);
+    g.turned = turned;
+    if (out) {
+        g.out = out->data;
+        g.out_token = out->token_stride;
+        g.out_head = out->head_stride;
+    }
+}
+
+}  // namespace
+
+int tq2_rope_turns(const double *inv_freq, uint64_t *turns, int64_t pairs) {
+    if (pairs < 0 || (pairs && (!inv_freq || !turns))) return TQ2_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < pairs; ++i)
+        if (!std::isfinite(inv_freq[i])) return TQ2_ERR_INVALID_ARG;
+    for (int64_t i = 0; i < pairs; ++i) {
+        const double t = inv_freq[i] / 6.283185307179586476925286766559;
+        const double f = std::fmod(std::fabs(t), 1.0);  // [0, 1), exact
+        // 2^64 f in two halves (the upper one exact), negated as an integer
+        const double hi = std::floor(f * 0x1p32);
+        const uint64_t u = (uint64_t(hi) << 32) + uint64_t(std::llrint((f * 0x1p32 - hi) * 0x1p32));
+        turns[i] = t < 0 ? 0 - u : u;
+    }
+    return TQ2_OK;
+}
+
+int tq2_rope_axes(const tq2_heads *q, const tq2_heads *q_out, const tq2_heads *k, const tq2_heads *k_out,
+                  const tq2_heads *v, const tq2_heads *v_out, const int64_t *positions, const tq2_rope *rope,
+                  int64_t tokens, int64_t dim, int inverse, void *stream) {
+    if (tokens < 0 || tokens > kMaxTokens || dim < 1 || dim > 65536 || !rope) return TQ2_ERR_INVALID_ARG;
+    if (rope->pairs < 0 || 2 * rope->pairs > dim || rope->axes < 1 || rope->axes > 16) return TQ2_ERR_INVALID_ARG;
+    if (tokens == 0) return TQ2_OK;
+    if (!q || !q_out || !k != !k_out || !v != !v_out) return TQ2_ERR_INVALID_ARG;
+    int st = check_rope(rope, positions, dim, true);
+    if (st != TQ2_OK) return st;
+    tq2_heads plain[6];
+    const tq2_heads *in[3] = {q, k, v}, *out[3] = {q_out, k_out, v_out};
+    for (int i = 0; i < 3; ++i) {
+        if (!in[i]) continue;
+        plain[i] = plain_view(in[i], tokens);
+        plain[3 + i] = plain_view(out[i], tokens);
+        in[i] = &plain[i];
+        out[i] = &plain[3 + i];
+        if ((st = check_view(in[i], tokens, dim, false)) != TQ2_OK) return st;
+        if ((st = check_view(out[i], tokens, dim, true)) != TQ2_OK) return st;
+        if (in[i]->heads != out[i]->heads || in[i]->dtype != q->dtype || out[i]->dtype != q_out->dtype)
+            return TQ2_ERR_INVALID_ARG;
+    }
+    for (int i = 0; i < 3; ++i)
+        for (int j = 0; j < 3; ++j) {
+            if (!in[i] || !in[j]) continue;
+            if (!(i == j && same_view(out[i], in[j])) && !views_apart(out[i], in[j], tokens, dim))
+                return TQ2_ERR_INVALID_ARG;
+            if (i < j && !views_apart(out[i], out[j], tokens, dim)) return TQ2_ERR_INVALID_ARG;
+        }
+    tq2::LaunchCtx ctx;
+    st = prepare(stream, &ctx, {q->data, q_out->data, k ? k->data : nullptr, k ? k_out->data : nullptr,
+                                v ? v->data : nullptr, v ? v_out->data : nullptr,
+                                rope->pairs ? positions : nullptr, rope->pairs ? rope->turns : nullptr,
+                                rope->pairs ? rope->axis : nullptr});
+    if (st != TQ2_OK) return st;
+    tq2::RopeArgs a = {};
+    set_rope(&a, rope, positions, dim);
+    a.tokens = tokens;
+    a.inverse = inverse != 0;
+    for (int i = 0; i < 3; ++i)
+        if (in[i]) add_segment(&a, in[i], out[i], i < 2);
+    return finish(tq2::launch_rope(a, q->dtype, q_out->dtype, ctx));
+}
+
+int tq2_kv_append(const tq2_heads *q, const tq2_heads *q_out, const tq2_heads *k, const tq2_heads *v,
+                  const int64_t *positions, const tq2_rope *rope, const tq2_batch *batch, const tq2_kv_cache *cache,
+                  void *stream) {
+    bool noop = false;
+    int st = check_batch_shape(batch, &noop);
+    if (st != TQ2_OK) return st;
+    if (!cache) return TQ2_ERR_INVALID_ARG;
+    const tq2_kv_cache cv = plain_cache(cache);
+    cache = &cv;
+    if ((st = check_cache(cache)) != TQ2_OK) return st;
+    if ((st = check_rope(rope, positions, cache->dim, false)) != TQ2_OK) return st;
+    if (noop) return TQ2_OK;
+    if ((st = check_batch(batch)) != TQ2_OK) return st;
+    if (!k || !v || !q != !q_out) return TQ2_ERR_INVALID_ARG;
+    const int64_t tokens = batch->tokens, dim = cache->dim;
+    tq2_heads plain[4];
+    int np = 0;
+    for (const tq2_heads **x : {&q, &q_out, &k, &v})
+        if (*x) {
+            plain[np] = plain_view(*x, tokens);
+            *x = &plain[np++];
+        }
+    if ((st = check_view(k, tokens, dim, false)) != TQ2_OK || (st = check_view(v, tokens, dim, false)) != TQ2_OK)
+        return st;
+    if (k->heads != cache->heads || v->heads != cache->heads || k->dtype != v->dtype) return TQ2_ERR_INVALID_ARG;
+    if (q) {
+        if ((st = check_view(q, tokens, dim, false)) != TQ2_OK || (st = check_view(q_out, tokens, dim, true)) != TQ2_OK)
+            return st;
+        if (q->heads != q_out->heads || q->dtype != k->dtype || q_out->dtype != cache->dtype) return TQ2_ERR_INVALID_ARG;
+        if (!same_view(q, q_out) && !views_apart(q, q_out, tokens, dim)) return TQ2_ERR_INVALID_ARG;
+        if (!views_apart(q_out, k, tokens, dim) || !views_apart(q_out, v, tokens, dim)) return TQ2_ERR_INVALID_ARG;
+    }
+    for (const tq2_heads *x : {q, q_out, k, v})
+        if (x && (view_in_plane(x, tokens, cache, cache->k) || view_in_plane(x, tokens, cache, cache->v)))
+            return TQ2_ERR_INVALID_ARG;
+    tq2::LaunchCtx ctx;
+    const bool turns = rope && rope->pairs;
+    st = prepare(stream, &ctx, {q ? q->data : nullptr, q ? q_out->data : nullptr, k->data, v->data,
+                                turns ? positions : nullptr, turns ? rope->turns : nullptr,
+                                turns ? rope->axis : nullptr, batch->q_start, batch->kv_len, batch->page_table,
+                                cache->k, cache->v});
+    if (st != TQ2_OK) return st;
+    tq2::RopeArgs a = {};
+    set_rope(&a, rope, positions, dim);
+    a.tokens = tokens;
+    a.append = 1;
+    a.batch = batch_view(batch, cache);
+    a.page_stride = cache->page_stride;
+    if (q) add_segment(&a, q, q_out, true);
+    for (int i = 0; i < 2; ++i) {
+        add_segment(&a, i ? v : k, nullptr, i == 0);
+        tq2::RopeSegment &g = a.seg[a.nseg - 1];
+        g.out = i ? cache->v : cache->k;
+        g.out_token = cache->slot_stride;
+        g.out_head = cache->head_stride;
+        g.paged = 1;
+    }
+    return finish(tq2::launch_rope(a, k->dtype, cache->dtype, ctx));
+}
+
+size_t tq2_attention_paged_workspace_bytes(int64_t heads, const tq2_kv_cache *cache, const tq2_batch *batch) {
+    bool noop = false;
+    if (check_batch_shape(batch, &noop) != TQ2_OK || noop || !cache || cache->heads < 1 || cache->heads > kMaxHeads ||
+        heads < 1 || heads > kMaxHeads || heads % cache->heads || cache->dim < 8 || cache->dim > 128 || cache->dim % 8)
+        return 0;
+    return tq2::attention_paged_ws_bytes(heads, cache->heads, cache->dim, batch->seqs, batch->tokens, batch->max_q,
+                                         batch->max_kv);
+}
+
+int tq2_attention_paged(const tq2_heads *q, const tq2_heads *out, const tq2_kv_cache *cache, const tq2_batch *batch,
+                        float scale, int64_t window, int causal, void *workspace, size_t workspace_bytes,
+                        void *stream) {
+    bool noop = false;
+    int st = check_batch_shape(batch, &noop);
+    if (st != TQ2_OK) return st;
+    if (!cache) return TQ2_ERR_INVALID_ARG;
+    const tq2_kv_cache cv = plain_cache(cache);
+    cache = &cv;
+    if ((st = check_cache(cache)) != TQ2_OK) return st;
+    if (!std::isfinite(scale) || window < 0) return TQ2_ERR_INVALID_ARG;
+    if (noop) return TQ2_OK;
+    if ((st = check_batch(batch)) != TQ2_OK) return st;
+    if (!q || !out) return TQ2_ERR_INVALID_ARG;
+    const int64_t tokens = batch->tokens, dim = cache->dim;
+    const tq2_heads qv = plain_view(q, tokens), ov = plain_view(out, tokens);
+    q = &qv;
+    out = &ov;
+    if ((st = check_view(q, tokens, dim, false)) != TQ2_OK || (st = check_view(out, tokens, dim, true)) != TQ2_OK)
+        return st;
+    if (q->heads != out->heads || q->heads % cache->heads || q->dtype != cache->dtype ||
+        (out->dtype != cache->dtype && out->dtype != TQ2_F32))
+        return TQ2_ERR_INVALID_ARG;
+    for (const tq2_heads *x : {q, out})
+        if (!aligned16(x->data) || x->token_stride % 8 || x->head_stride % 8) return TQ2_ERR_MISALIGNED;
+    if (!views_apart(q, out, tokens, dim) || view_in_plane(out, tokens, cache, cache->k) ||
+        view_in_plane(out, tokens, cache, cache->v))
+        return TQ2_ERR_INVALID_ARG;
+    const size_t need = tq2_attention_paged_workspace_bytes(q->heads, cache, batch);
+    if (workspace) {
+        if (workspace_bytes < need) return TQ2_ERR_INVALID_ARG;
+        if (!aligned16(workspace)) return TQ2_ERR_MISALIGNED;
+        const size_t nb = size_t((tokens - 1) * q->token_stride + (q->heads - 1) * q->head_stride + dim) * 2;
+        const size_t ob = size_t((tokens - 1) * out->token_stride + (out->heads - 1) * out->head_stride + dim) *
+                          dtype_bytes(out->dtype);
+        if (overlaps(workspace, need, q->data, nb) || overlaps(workspace, need, out->data, ob) ||
+            overlaps(workspace, need, cache->k, plane_bytes(cache)) ||
+            overlaps(workspace, need, cache->v, plane_bytes(cache)))
+            return TQ2_ERR_INVALID_ARG;
+    }
+    tq2::LaunchCtx ctx;
+    st = prepare(stream, &ctx, {q->data, out->data, cache->k, cache->v, batch->q_start, batch->kv_len,
+                                batch->page_table, workspace});
+    if (st != TQ2_OK) return st;
+    tq2::PagedArgs a = {};
+    a.q = q->data;
+    a.out = out->data;
+    a.k = cache->k;
+    a.v = cache->v;
+    a.q_token = q->token_stride;
+    a.q_head = q->head_stride;
+    a.out_token = out->token_stride;
+    a.out_head = out->head_stride;
+    a.page_stride = cache->page_stride;
+    a.slot_stride = cache->slot_stride;
+    a.head_stride = cache->head_stride;
+    a.batch = batch_view(batch, cache);
+    a.window = window;
+    a.scale = scale;
+    a.heads = int(q->heads);
+    a.kv_heads = int(cache->heads);
+    a.dim = int(dim);
+    a.causal = causal != 0;
+    void *ws = workspace;
+    if (need && !ws && cudaMallocAsync(&ws, need, ctx.stream) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TQ2_ERR_CUDA;
+    }
+    const cudaError_t e = tq2::launch_attention_paged(a, cache->dtype, out->dtype == TQ2_F32, ws, ctx);
+    const cudaError_t f = ws != workspace ? cudaFreeAsync(ws, ctx.stream) : cudaSuccess;
+    return finish(e != cudaSuccess ? e : f);
 }
 
 }  // extern "C"

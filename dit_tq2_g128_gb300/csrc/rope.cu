@@ -1,0 +1,236 @@
+// Rotary positions with several axes, and the same on the way into a paged
+// key/value cache.
+//
+// Mathematics: pair (a, b) of a head is the complex number a + ib, multiplied by
+// exp(i position[axis] inv_freq).  The angle is kept as a fraction of a turn in
+// 64-bit integers: phase = position * turns mod 2^64 is exact whatever the
+// position, and only the nearest quarter turn's remainder (32 bits of it) is
+// rounded to f32, at most an eighth of a turn with 24 bits: 2^-25 of a radian or
+// so, the rounding of the f32 sine itself.
+//
+// Bound by memory (each element read once and written once).  A thread owns one
+// unit (VP pairs) of one token: it forms the unit's sines once and turns it in up
+// to `hpg` heads, four heads' loads in flight at a time, 16 bytes a load and lane.
+// Any strides: the vector width falls back to one element where the pointers,
+// strides or pair count do not allow 16 (8) bytes.
+#include <cuda_bf16.h>
+
+#include "tq2_internal.cuh"
+
+namespace tq2 {
+namespace {
+
+constexpr int kRopeThreads = 256;
+
+template <typename T, int VP>
+struct alignas(sizeof(T) * VP) Pack {
+    T e[VP];
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float x, float &y) { y = x; }
+__device__ __forceinline__ void from_f32(float x, __half &y) { y = __float2half_rn(x); }
+__device__ __forceinline__ void from_f32(float x, __nv_bfloat16 &y) { y = __float2bfloat16_rn(x); }
+
+template <typename T, int VP>
+__device__ __forceinline__ void store_pack(T *p, const float (&x)[VP]) {
+    Pack<T, VP> v;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) from_f32(x[i], v.e[i]);
+    *reinterpret_cast<Pack<T, VP> *>(p) = v;
+}
+
+// sine and cosine of 2 pi phase / 2^64
+__device__ __forceinline__ void turn_sincos(uint64_t phase, float &sn, float &cs) {
+    const uint64_t quarter = (phase + (uint64_t(1) << 61)) >> 62;
+    const int64_t rest = int64_t(phase - (quarter << 62));  // [-2^61, 2^61): an eighth of a turn each way
+    float s, c;
+    sincospif(float(int32_t(rest >> 30)) * 0x1p-33f, &s, &c);
+    const bool swap = quarter & 1, neg_s = quarter & 2, neg_c = ((quarter + 1) & 2) != 0;
+    sn = swap ? c : s;
+    cs = swap ? s : c;
+    if (neg_s) sn = -sn;
+    if (neg_c) cs = -cs;
+}
+
+// grid: x = tokens * units / threads, y = head groups of all segments
+template <typename TI, typename TO, int VP>
+__global__ void __launch_bounds__(kRopeThreads)
+rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
+    const int64_t idx = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
+    int64_t t;
+    int u;
+    if (idx <= 0xffffffffll) {
+        t = uint32_t(idx) / uint32_t(units);
+        u = int(uint32_t(idx) - uint32_t(t) * uint32_t(units));
+    } else {
+        t = idx / units;
+        u = int(idx - t * units);
+    }
+    if (t >= a.tokens) return;
+    int s = 0, group = blockIdx.y;
+    for (; s < a.nseg - 1; ++s) {
+        const int n = (a.seg[s].heads + hpg - 1) / hpg;
+        if (group < n) break;
+        group -= n;
+    }
+    const RopeSegment &g = a.seg[s];
+
+    // where this token goes
+    int64_t key = 0;
+    int64_t out_base = t * g.out_token;
+    if (a.append) {
+        const int b = seq_of(a.batch, t);
+        if (b < 0) return;
+        bool bad = false;
+        const SeqSpan sp = seq_span(a.batch, b, bad);
+        report_bad(bad, status);
+        if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
+        key = int64_t(sp.kv) - sp.n + (t - sp.q0);
+        if (g.paged) {
+            if (key < 0) return;
+            const int in_table = int(key) / a.batch.page_size;
+            const int64_t page = page_of(a.batch, b, in_table, bad);
+            report_bad(bad, status);
+            if (page < 0) return;
+            out_base = page * a.page_stride + int64_t(int(key) - in_table * a.batch.page_size) * g.out_token;
+        }
+    }
+
+    // the unit's two packs of VP elements in each head
+    const int ru = a.pairs / VP;  // units that are turned
+    const bool turned = g.turned && u < ru;
+    int e0, e1;
+    if (g.turned && u < ru) {
+        e0 = a.interleaved ? u * 2 * VP : u * VP;
+        e1 = a.interleaved ? e0 + VP : a.pairs + e0;
+    } else {
+        e0 = g.turned ? 2 * a.pairs + (u - ru) * 2 * VP : u * 2 * VP;
+        e1 = e0 + VP;
+    }
+    const bool has0 = e0 < a.dim, has1 = e1 < a.dim;  // (a scalar copy unit may end inside)
+    float sn[VP], cs[VP];
+    if (turned) {
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int p = u * VP + i;
+            int64_t pos = key;
+            if (a.positions) {
+                const int ax = a.axis ? min(int(a.axis[p]), a.axes - 1) : 0;
+                pos = a.positions[t * a.axes + ax];
+            }
+            turn_sincos(uint64_t(pos) * a.turns[p], sn[i], cs[i]);
+            if (a.inverse) sn[i] = -sn[i];
+        }
+    }
+    const TI *in = static_cast<const TI *>(g.in) + t * g.in_token;
+    TO *out = static_cast<TO *>(g.out) + out_base;
+    const int h0 = group * hpg, h1 = min(h0 + hpg, g.heads);
+    for (int h = h0; h < h1; h += 4) {
+        Pack<TI, VP> x[4], y[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (h + j < h1) {
+                const TI *p = in + int64_t(h + j) * g.in_head;
+                if (has0) x[j] = *reinterpret_cast<const Pack<TI, VP> *>(p + e0);
+                if (has1) y[j] = *reinterpret_cast<const Pack<TI, VP> *>(p + e1);
+            }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (h + j < h1) {
+                float f0[VP], f1[VP], r0[VP], r1[VP];
+#pragma unroll
+                for (int i = 0; i < VP; ++i) {
+                    f0[i] = to_f32(x[j].e[i]);
+                    f1[i] = to_f32(y[j].e[i]);
+                }
+                if (!turned) {
+#pragma unroll
+                    for (int i = 0; i < VP; ++i) {
+                        r0[i] = f0[i];
+                        r1[i] = f1[i];
+                    }
+                } else if (VP == 1 || !a.interleaved) {
+#pragma unroll
+                    for (int i = 0; i < VP; ++i) {
+                        r0[i] = fmaf(f0[i], cs[i], -f1[i] * sn[i]);
+                        r1[i] = fmaf(f0[i], sn[i], f1[i] * cs[i]);
+                    }
+                } else {  // pairs lie inside each pack: angles 0 .. VP/2 - 1, then the rest
+#pragma unroll
+                    for (int i = 0; i < VP / 2; ++i) {
+                        const float c0 = cs[i], s0 = sn[i], c1 = cs[VP / 2 + i], s1 = sn[VP / 2 + i];
+                        r0[2 * i] = fmaf(f0[2 * i], c0, -f0[2 * i + 1] * s0);
+                        r0[2 * i + 1] = fmaf(f0[2 * i], s0, f0[2 * i + 1] * c0);
+                        r1[2 * i] = fmaf(f1[2 * i], c1, -f1[2 * i + 1] * s1);
+                        r1[2 * i + 1] = fmaf(f1[2 * i], s1, f1[2 * i + 1] * c1);
+                    }
+                }
+                TO *p = out + int64_t(h + j) * g.out_head;
+                if (has0) store_pack<TO, VP>(p + e0, r0);
+                if (has1) store_pack<TO, VP>(p + e1, r1);
+            }
+    }
+}
+
+// pointers, strides and pair count allow packs of vp elements
+bool packs(const RopeArgs &a, int vp, int in_bytes, int out_bytes) {
+    if (a.pairs % vp || a.dim % (2 * vp)) return false;
+    for (int s = 0; s < a.nseg; ++s) {
+        const RopeSegment &g = a.seg[s];
+        if (reinterpret_cast<uintptr_t>(g.in) % (vp * in_bytes) || reinterpret_cast<uintptr_t>(g.out) % (vp * out_bytes))
+            return false;
+        if (g.in_token % vp || g.in_head % vp || g.out_token % vp || g.out_head % vp) return false;
+        if (g.paged && a.page_stride % vp) return false;
+    }
+    return true;
+}
+
+template <typename TI, typename TO, int VP>
+cudaError_t launch_rope_vp(const RopeArgs &a, const LaunchCtx &ctx) {
+    const int units = VP == 1 ? a.pairs + (a.dim - 2 * a.pairs + 1) / 2 : a.dim / (2 * VP);
+    // heads per thread: as many (up to 8, for the sines' sake) as leave every SM its threads
+    int all = 0;
+    for (int s = 0; s < a.nseg; ++s) all += a.seg[s].heads;
+    int hpg = 8;
+    while (hpg > 1 && a.tokens * units * ((all + hpg - 1) / hpg) < int64_t(ctx.num_sms) * 2048) hpg >>= 1;
+    int groups = 0;
+    for (int s = 0; s < a.nseg; ++s) groups += (a.seg[s].heads + hpg - 1) / hpg;
+    if (groups == 0) return cudaSuccess;
+    const int64_t blocks = (a.tokens * units + kRopeThreads - 1) / kRopeThreads;
+    if (blocks > INT32_MAX || groups > 65535) return cudaErrorInvalidValue;
+    rope_kernel<TI, TO, VP><<<dim3(unsigned(blocks), unsigned(groups)), kRopeThreads, 0, ctx.stream>>>(a, units, hpg,
+                                                                                                       ctx.status);
+    return cudaPeekAtLastError();
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_rope_io(const RopeArgs &a, const LaunchCtx &ctx) {
+    if constexpr (sizeof(TI) == 2 && sizeof(TO) == 2)
+        if (packs(a, 8, 2, 2)) return launch_rope_vp<TI, TO, 8>(a, ctx);
+    if (packs(a, 4, sizeof(TI), sizeof(TO))) return launch_rope_vp<TI, TO, 4>(a, ctx);
+    return launch_rope_vp<TI, TO, 1>(a, ctx);
+}
+
+template <typename TI>
+cudaError_t launch_rope_in(const RopeArgs &a, int out_dtype, const LaunchCtx &ctx) {
+    switch (out_dtype) {
+        case TQ2_F32: return launch_rope_io<TI, float>(a, ctx);
+        case TQ2_F16: return launch_rope_io<TI, __half>(a, ctx);
+        default: return launch_rope_io<TI, __nv_bfloat16>(a, ctx);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeArgs &a, int in_dtype, int out_dtype, const LaunchCtx &ctx) {
+    switch (in_dtype) {
+        case TQ2_F32: return launch_rope_in<float>(a, out_dtype, ctx);
+        case TQ2_F16: return launch_rope_in<__half>(a, out_dtype, ctx);
+        default: return launch_rope_in<__nv_bfloat16>(a, out_dtype, ctx);
+    }
+}
+
+}  // namespace tq2

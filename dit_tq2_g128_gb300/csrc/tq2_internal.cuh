@@ -9,6 +9,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "paged_index.h"
 #include "tq2.h"
 
 namespace tq2 {
@@ -101,6 +102,46 @@ size_t attention_ws_bytes(int64_t H, int64_t S, int64_t D);
 cudaError_t launch_attention(const float *q, const float *k, const float *v, float *out, int64_t H, int64_t S,
                              int64_t D, void *ws, const LaunchCtx &ctx);
 
+// Rotary positions / append (rope.cu).  A segment is one of q, k, v.
+struct RopeSegment {
+    const void *in;
+    void *out;
+    int64_t in_token, in_head;    // strides in elements
+    int64_t out_token, out_head;  // out_token: the slot stride if paged
+    int heads;
+    int turned;  // 0: copied
+    int paged;   // out is a cache plane
+};
+struct RopeArgs {
+    RopeSegment seg[3];
+    const int64_t *positions;  // NULL: the token's key index
+    const uint64_t *turns;
+    const uint8_t *axis;
+    BatchView batch;  // appending only (append != 0)
+    int64_t tokens;
+    int64_t page_stride;
+    int nseg, append, axes, pairs, interleaved, inverse, dim;
+};
+cudaError_t launch_rope(const RopeArgs &a, int in_dtype, int out_dtype, const LaunchCtx &ctx);
+
+// Attention over a paged cache (attention_paged.cu).
+struct PagedArgs {
+    const void *q;
+    void *out;
+    const void *k, *v;  // 16-bit cache planes
+    int64_t q_token, q_head, out_token, out_head;            // strides in elements
+    int64_t page_stride, slot_stride, head_stride;
+    BatchView batch;
+    int64_t window;  // 0: none
+    float scale;
+    int heads, kv_heads, dim;
+    int causal;
+};
+size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens,
+                                int64_t max_q, int64_t max_kv);
+// dtype: the cache's (and q's); out_f32: out is f32 instead
+cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx);
+
 // Skinny-M tensor-core kernel (2 <= m <= 32, k up to the shared-memory limit
 // of its K slices): one launch, no workspace.  cudaErrorNotSupported outside.
 bool skinny_mma_fits(int64_t m, int64_t n, int64_t k);
@@ -112,6 +153,11 @@ constexpr int64_t kSkinnyMaxM = 16;
 
 // ---------------------------------------------------------------------------
 // Device helpers
+
+// Records a clamp of a batch's tables (see paged_index.h).
+__device__ __forceinline__ void report_bad(bool bad, unsigned int *status) {
+    if (bad) atomicOr(status, static_cast<unsigned int>(TQ2_ERR_BAD_BATCH));
+}
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

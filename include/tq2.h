@@ -79,7 +79,9 @@ typedef enum {
     TQ2_ERR_UNSUPPORTED_DEVICE = 4, /* current device is not sm_103 */
     TQ2_ERR_CUDA = 5,               /* launch or runtime error */
     TQ2_ERR_TIMEOUT = 6,            /* a bounded device-side wait expired (see tq2_device_status) */
-    TQ2_ERR_TOO_LARGE = 7           /* tq2_gemm_noalloc: the shape needs more than its fixed scratch */
+    TQ2_ERR_TOO_LARGE = 7,          /* tq2_gemm_noalloc: the shape needs more than its fixed scratch */
+    TQ2_ERR_BAD_BATCH = 8           /* a length, offset or page in a batch's device tables is out of
+                                       range (see tq2_device_status) */
 } tq2_status;
 
 /* Size of the fixed device scratch behind tq2_gemm_noalloc (32 MiB). */
@@ -361,6 +363,152 @@ int tq2_gemm_with(int kernel, const void *w_soa, const float *x, const float *re
 /* The kernel that tq2_gemm picks for this shape (a tq2_kernel value).  Host
  * only; needs no device. */
 int tq2_select_kernel(int64_t m, int64_t n, int64_t k);
+
+/* ---------------------------------------------------------------------------
+ * Positions, key/value cache and its attention (what lies between the
+ * projections of a transformer block).
+ * ------------------------------------------------------------------------- */
+
+/* Element types of activations and caches. */
+typedef enum {
+    TQ2_F32 = 0,
+    TQ2_F16 = 1, /* IEEE binary16 */
+    TQ2_BF16 = 2
+} tq2_dtype;
+
+/* A [tokens, heads, dim] view: element (t, h, d) is element
+ * t * token_stride + h * head_stride + d of `data`.  Strides count elements and
+ * are not negative, so token-major (a slice of a fused projection included) and
+ * head-major tensors are both views.  The elements of an output are distinct.
+ * `data` is aligned to its element. */
+typedef struct {
+    void *data;
+    int64_t heads;
+    int64_t token_stride;
+    int64_t head_stride;
+    int32_t dtype; /* tq2_dtype */
+} tq2_heads;
+
+/* Rotary positions.  Pair i of a head (i < pairs, 2 * pairs <= dim) is its
+ * elements (i, i + pairs), or (2i, 2i + 1) if interleaved; it is turned by
+ * position[axis[i]] * inv_freq[i] radians:
+ *     (a, b) -> (a cos - b sin, a sin + b cos).
+ * Elements from 2 * pairs on are copied.
+ *   turns : device [pairs], made of inv_freq by tq2_rope_turns
+ *   axis  : device [pairs], the axis of each pair, below `axes` (a larger value
+ *           reads the last axis); NULL = axis 0 for all */
+typedef struct {
+    const uint64_t *turns;
+    const uint8_t *axis;
+    int64_t pairs;
+    int32_t axes; /* positions per token, 1 .. 16 */
+    int32_t interleaved;
+} tq2_rope;
+
+/* A paged cache: `pages` pages of `page_size` slots of `heads` x `dim` elements.
+ * Element (page, slot, head, d) of k and of v is element page * page_stride +
+ * slot * slot_stride + head * head_stride + d; so [pages, page_size, heads, dim]
+ * and [pages, heads, page_size, dim] are both caches.  The elements of a cache
+ * are distinct.  k and v are 16-byte aligned and the strides are multiples of 8. */
+typedef struct {
+    void *k;
+    void *v;
+    int64_t pages;
+    int64_t page_size;
+    int64_t heads;
+    int64_t dim; /* a multiple of 8, 8 .. 128 */
+    int64_t page_stride;
+    int64_t slot_stride;
+    int64_t head_stride;
+    int32_t dtype; /* TQ2_F16 or TQ2_BF16 */
+} tq2_kv_cache;
+
+/* The sequences of one step.  Sequence b has the new tokens q_start[b] ..
+ * q_start[b+1] - 1 (n of them) of the step's `tokens`, and kv_len[b] keys, its
+ * new tokens' own included: new token i is key kv_len[b] - n + i.  Key j lies in
+ * slot j % page_size of page page_table[b * table_stride + j / page_size].
+ * Table entries past a sequence's last page are not read.  Tokens outside every
+ * sequence (padding of a captured graph) are left out by every call.
+ * The tables are device memory that a captured graph reads again on each replay;
+ * max_q and max_kv are host bounds of n and kv_len that the launch is sized by.
+ * Lengths are clamped to them and to the table's width, and a page outside the
+ * cache is never touched: TQ2_ERR_BAD_BATCH is then recorded in the device
+ * status word (tq2_device_status), and that sequence's results mean nothing. */
+typedef struct {
+    const int32_t *q_start;    /* device [seqs + 1], not decreasing, from 0 */
+    const int32_t *kv_len;     /* device [seqs] */
+    const int32_t *page_table; /* device [seqs, table_stride] */
+    int64_t seqs;
+    int64_t tokens;
+    int64_t max_q;
+    int64_t max_kv;
+    int64_t table_stride;
+} tq2_batch;
+
+/* Fractions of a turn per position, in units of 2^-64: what tq2_rope.turns holds.
+ * HOST function on host memory.  position * turns[i] modulo 2^64 is then the
+ * angle's exact fraction of a turn in integers, so that far positions lose
+ * nothing: its error is |position| * 2^-65 turns and that of inv_freq / 2pi in
+ * binary64.  inv_freq is in radians per position and finite; scaled frequencies
+ * (interpolated contexts) are given as they are to be used.
+ * (No counterpart on the pages: their `fused_qk_rope` kernel is a name only.) */
+int tq2_rope_turns(const double *inv_freq, uint64_t *turns, int64_t pairs);
+
+/* Rotary positions on q and k [tokens, heads, dim], with v copied on the way:
+ * from the views q, k, v to the views q_out, k_out, v_out, which may have another
+ * layout and type (e.g. from the token-major projection to the head-major
+ * operands of tq2_attention_f32).  k and/or v may be NULL (with their outputs).
+ * inverse != 0 turns by the negated angle, which is the gradient of the
+ * rotation: call it on the gradients, from the layout of the outputs to that of
+ * the inputs.  Products and sums in f32, one rounding to the output's type.
+ *   positions : device [tokens, rope->axes] int64; any sign
+ * q, k and v have one type, and their outputs one.  An output may be its own
+ * input (same view); no other output may overlap an input or another output.
+ * dim is 1 .. 65536.  tokens == 0 is a no-op. */
+int tq2_rope_axes(const tq2_heads *q, const tq2_heads *q_out, const tq2_heads *k, const tq2_heads *k_out,
+                  const tq2_heads *v, const tq2_heads *v_out, const int64_t *positions, const tq2_rope *rope,
+                  int64_t tokens, int64_t dim, int inverse, void *stream);
+
+/* Append a step's keys and values to a paged cache: k rotated, v as it is, both
+ * rounded once to the cache's type (to nearest even; binary16 overflows to Inf).
+ * q, if given, is rotated into q_out in the same launch (q, k and v have one
+ * type; q_out has the cache's, which tq2_attention_paged reads).  A token whose key index is negative
+ * (kv_len smaller than its new tokens) is not stored.  Two tokens of one step may
+ * not share a slot.
+ *   q, q_out  : NULL, or views of [tokens, any heads, cache->dim]
+ *   k, v      : views of [tokens, cache->heads, cache->dim]
+ *   positions : device [tokens, rope->axes] int64, or NULL for each token's key
+ *               index (then rope->axes == 1)
+ *   rope      : NULL for no rotation
+ * q_out may be q (same view); nothing else may overlap. */
+int tq2_kv_append(const tq2_heads *q, const tq2_heads *q_out, const tq2_heads *k, const tq2_heads *v,
+                  const int64_t *positions, const tq2_rope *rope, const tq2_batch *batch, const tq2_kv_cache *cache,
+                  void *stream);
+
+/* Attention of the new tokens over the paged cache:
+ *     out[t, h] = sum_j softmax_j(scale * q[t, h] . k_j) v_j
+ * over the keys j of t's sequence in head h / (heads / cache->heads) that the
+ * token sees.  With pos = its key index: causal, j <= pos; else every j <
+ * kv_len; with window > 0 also j > pos - window.  A token that sees no key gets
+ * zeros.  Slots that a token does not see have no influence, whatever they hold.
+ *   q     : view of the cache's type, 16-byte aligned, strides multiples of 8;
+ *           heads a multiple of cache->heads
+ *   out   : view of the same heads, of the cache's type or f32, 16-byte aligned,
+ *           strides multiples of 8
+ *   scale : finite (usually 1/sqrt(dim))
+ * Scores, softmax statistics and sums are f32; the weights enter the second
+ * product in the cache's type, or, for an f32 out, as a sum of two such terms.
+ * Memory: `workspace` holds partial results of long contexts
+ * (tq2_attention_paged_workspace_bytes of the same arguments, 16-byte aligned);
+ * if NULL, a temporary from the device's pool is taken instead. */
+int tq2_attention_paged(const tq2_heads *q, const tq2_heads *out, const tq2_kv_cache *cache, const tq2_batch *batch,
+                        float scale, int64_t window, int causal, void *workspace, size_t workspace_bytes,
+                        void *stream);
+
+/* Bytes of workspace that tq2_attention_paged uses for `heads` query heads: a
+ * function of heads, the cache's heads and dim, and the batch's seqs, tokens,
+ * max_q and max_kv (0: none is needed, or the arguments are not valid). */
+size_t tq2_attention_paged_workspace_bytes(int64_t heads, const tq2_kv_cache *cache, const tq2_batch *batch);
 
 /* Bounded device-side waits.  Every spin-wait inside a kernel (on an mbarrier)
  * gives up after `ns` nanoseconds of %globaltimer time, records
