@@ -1,85 +1,500 @@
-// Attention of a step's new tokens over a paged key/value cache.
+// Attention of a step's new tokens over a paged key/value cache: few query rows.
 //
-// One warp per (token, head): lanes share the head's elements, keys one after the
-// other with the running maximum and sum of the softmax, all in f32.
+// Mathematics.  The rows of one sequence that share a key head (its new tokens
+// times the query heads of the group, R = n * G of them) read the same keys, so
+// a CTA takes all of them at once: S^T = K Q^T, P = exp2(S log2(e) scale - m),
+// O^T += V^T P^T over tiles of 64 keys, with the running maximum m and sum l of
+// the softmax.  Keys are the rows (M) of both products and the query rows their
+// columns (N = 8 or 16): decoding wastes no tensor rows as it would with the
+// queries in M.
+//
+// Bound by memory: 2 R flops per byte of cache at 16 bits, below the legacy
+// tensor path's rate up to R = 16 (the tcgen05 path of attention_paged_tc.cu
+// needs 128 rows in M and takes over above).
+//
+// A CTA (four consumer warps of 16 keys each a tile, one producer warp) owns one
+// (sequence, key head, chunk of keys).  The producer's lanes look up one page
+// each and copy its rows by tensor copies with the 128-byte swizzle into a ring
+// of three tiles (96 KB at 128 features; two CTAs an SM keep 192 KB in flight).
+// A copy's box is the largest power of two of rows that divides the page size, so
+// a box never crosses a page, whatever the page size; features past dim are
+// filled with zeros by the copy.  Every warp keeps its own m, l and O; they meet
+// once, at the end.  Chunks of a long context leave (m, l, O) in the workspace and
+// a second, dependent launch joins them in a fixed order.
+//
+// Slots that no row sees are never multiplied: their scores are replaced by
+// -inf and their rows of V are zeroed in shared memory (0 * NaN is NaN).  Where
+// some rows see a key and others do not, values of V that are not finite are
+// taken out of the product and added to the rows that see them.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
-#include "tq2_internal.cuh"
+#include "paged_attention.cuh"
 
 namespace tq2 {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kKeys = 64;       // keys of a tile
+constexpr int kStages = 3;
+constexpr int kConsumers = 4;   // warps, 16 keys of a tile each
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kRowsMax = 16;    // query rows per (sequence, key head) that this kernel takes
 
-__device__ __forceinline__ float up(__half x) { return __half2float(x); }
-__device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float x, float *p) { *p = x; }
-__device__ __forceinline__ void put(float x, __half *p) { *p = __float2half_rn(x); }
-__device__ __forceinline__ void put(float x, __nv_bfloat16 *p) { *p = __float2bfloat16_rn(x); }
+template <int DP, int NT>
+struct RowLayout {
+    static constexpr int HALVES = DP / 64;
+    static constexpr int HALF = kKeys * 128;           // one swizzled sub-tile of 64 features
+    static constexpr int PLANE = HALF * HALVES;        // K (or V) of a tile
+    static constexpr int RING = kStages * 2 * PLANE;
+    static constexpr int ROWS = 8 * NT;
+    static constexpr int OPAD = DP + 4;                // f32 row of the final exchange
+    static_assert(kConsumers * ROWS * OPAD * 4 <= RING, "the exchange reuses the ring");
+    static constexpr int OFF_CTL = RING;
+    static constexpr int OFF_ML = OFF_CTL + 128;       // m, l per warp and row
+    static constexpr int OFF_POISON = OFF_ML + 2 * kConsumers * ROWS * 4;
+    static constexpr int BYTES = OFF_POISON + ROWS * DP * 4 + 1024;
+};
 
-template <typename T, typename TO>
-__global__ void __launch_bounds__(32 * kWarps) paged_row_kernel(const PagedArgs a, unsigned int *status) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t t = row / a.heads;
-    const int h = int(row - t * a.heads);
-    if (t >= a.batch.tokens) return;
-    const int b = seq_of(a.batch, t);
-    if (b < 0) return;
+struct RowCtl {
+    uint64_t full[kStages], empty[kStages];
+    int abort, poisoned;
+};
+
+template <typename T>
+__device__ __forceinline__ void mma_16x8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (is_half<T>)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// DP: features padded to 64 or 128; NT: query rows in eights; SPLIT_P: the weights
+// enter the second product as two terms (f32 outputs).
+template <typename T, typename TO, int DP, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                  const PagedArgs a, const RowPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml,
+                  unsigned int *status, uint64_t wait_ns) {
+    using L = RowLayout<DP, NT>;
+    constexpr bool SPLIT_P = sizeof(TO) == 4;
+    extern __shared__ uint8_t rows_raw[];
+    const uint32_t raw = smem_u32(rows_raw), pad = (1024u - (raw & 1023u)) & 1023u, base = raw + pad;
+    uint8_t *smem = rows_raw + pad;
+    RowCtl *ctl = reinterpret_cast<RowCtl *>(smem + L::OFF_CTL);
+    float *poison = reinterpret_cast<float *>(smem + L::OFF_POISON);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = blockIdx.y, b = int(blockIdx.x / unsigned(plan.chunks)), chunk = int(blockIdx.x % unsigned(plan.chunks));
+    const int G = a.heads / a.kv_heads;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], kConsumers);
+        }
+        ctl->abort = 0;
+        ctl->poisoned = 0;
+        fence_mbarrier_init();
+    }
+    // the tables, q and the cache may be written by the kernel before this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool bad = false;
     const SeqSpan sp = seq_span(a.batch, b, bad);
-    if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
-    const KeyRange kr = keys_of(sp, int(t - sp.q0), a.window, a.causal);
-    const T *q = static_cast<const T *>(a.q) + t * a.q_token + int64_t(h) * a.q_head;
-    const int64_t head = int64_t(h / (a.heads / a.kv_heads)) * a.head_stride;
-    float qr[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+    const RowSpan rs = row_span(sp, a.window, a.causal, plan.chunk);
+    if (sp.n == 0 || chunk >= max(rs.chunks, 1)) return;  // (CTA-uniform)
+    const int R = sp.n * G;
+    const int64_t k0 = rs.base + int64_t(chunk) * plan.chunk;
+    const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
+    const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
+    const int tile0 = int(k0) / kKeys, tiles = rs.chunks ? (last + kKeys - 1) / kKeys - tile0 : 0;
+    if (sp.n > 1)  // (one token's keys are seen by all its rows or by none)
+        for (int i = threadIdx.x; i < L::ROWS * DP; i += kThreads) poison[i] = 0.f;
+    __syncthreads();
+
+    if (warp == kConsumers) {
+        report_bad(bad, status);
+        bad = false;
+        // ---- producer: lane = box of a tile (and lane + 32, where boxes are single rows)
+        const int rb = plan.box_rows, boxes = kKeys / rb;
+        int issued = 0;
+        bool ok = true;
+        for (; issued < tiles; ++issued) {
+            const int s = issued % kStages, u = issued / kStages;
+            int64_t page[2];
+            int slot[2];
+            unsigned mask[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) qr[i] = lane + 32 * i < a.dim ? up(q[lane + 32 * i]) : 0.f;
-    for (int j = kr.lo; j < kr.hi; ++j) {
-        const int in_table = j / a.batch.page_size;
-        const int64_t page = page_of(a.batch, b, in_table, bad);
-        if (page < 0) continue;
-        const int64_t at = page * a.page_stride + int64_t(j - in_table * a.batch.page_size) * a.slot_stride + head;
-        const T *k = static_cast<const T *>(a.k) + at, *v = static_cast<const T *>(a.v) + at;
-        float s = 0.f;
+            for (int i = 0; i < 2; ++i) {
+                const int box = lane + 32 * i, key = (tile0 + issued) * kKeys + box * rb;
+                const bool want = box < boxes && key < last && key + rb > first;
+                mask[i] = __ballot_sync(0xffffffffu, want);
+                page[i] = -1;
+                slot[i] = 0;
+                if (want) {
+                    const int entry = key / a.batch.page_size;
+                    page[i] = page_of(a.batch, b, entry, bad);
+                    if (page[i] < 0) page[i] = 0;  // (recorded; any page of the cache will do)
+                    slot[i] = key - entry * a.batch.page_size;
+                }
+            }
+            if (u > 0 && !mbar_wait_spin(&ctl->empty[s], (u - 1) & 1, wait_ns, status)) ok = false;
+            if (__any_sync(0xffffffffu, !ok || *reinterpret_cast<volatile int *>(&ctl->abort))) {
+                ok = false;
+                break;
+            }
+            if (lane == 0)
+                mbar_expect_tx(&ctl->full[s], uint32_t(__popc(mask[0]) + __popc(mask[1])) * uint32_t(rb * 256 * L::HALVES));
+            __syncwarp();
+            const uint32_t stage = base + uint32_t(s * 2 * L::PLANE);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < a.dim) s = fmaf(qr[i], up(k[lane + 32 * i]), s);
+            for (int i = 0; i < 2; ++i)
+                if (mask[i] >> lane & 1) {
+                    const uint32_t row = uint32_t((lane + 32 * i) * rb * 128);
 #pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale;
-        const float mn = fmaxf(m, s);
-        const float c = m == mn ? 1.f : expf(m - mn), p = s == mn ? 1.f : expf(s - mn);
-        l = l * c + p;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < a.dim) o[i] = fmaf(p, up(v[lane + 32 * i]), o[i] * c);
+                    for (int h = 0; h < L::HALVES; ++h) {
+                        tma_cache(stage + uint32_t(h * L::HALF) + row, &kmap, 64 * h, g, slot[i], int(page[i]), &ctl->full[s]);
+                        tma_cache(stage + uint32_t(L::PLANE + h * L::HALF) + row, &vmap, 64 * h, g, slot[i], int(page[i]),
+                                  &ctl->full[s]);
+                    }
+                }
+        }
+        report_bad(bad, status);
+        if (!ok) {
+            if (lane == 0) {  // what was issued lands before the CTA ends
+                *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
+                for (int t = max(0, issued - kStages); t < issued; ++t)
+                    mbar_wait_bounded(&ctl->full[t % kStages], (t / kStages) & 1, drain_ns(wait_ns), status);
+            }
+            __syncwarp();
+        }
     }
-    TO *out = static_cast<TO *>(a.out) + t * a.out_token + int64_t(h) * a.out_head;
-    const float inv = l > 0.f ? 1.f / l : (kr.hi > kr.lo ? l : 0.f);
-    report_bad(bad, status);
+
+    float m[NT][2], l[NT][2], o[NT][DP / 16][4];
+    if (warp < kConsumers) {
+        // ---- consumer: 16 keys of every tile
+        uint32_t q[NT][DP / 16][2];
+        int lo[NT][2], hi[NT][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < a.dim) put(o[i] * inv, out + lane + 32 * i);
+        for (int t = 0; t < NT; ++t) {
+            const int r = t * 8 + (lane >> 2);
+            const T *qr = static_cast<const T *>(a.q) + (int64_t(sp.q0) + r / G) * a.q_token + int64_t(g * G + r % G) * a.q_head;
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int d = kk * 16 + e * 8 + 2 * (lane & 3);
+                    q[t][kk][e] = r < R && d < a.dim ? *reinterpret_cast<const uint32_t *>(qr + d) : 0u;
+                }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int n = t * 8 + 2 * (lane & 3) + c;
+                const KeyRange kr = keys_of(sp, n / G, a.window, a.causal);
+                lo[t][c] = n < R ? kr.lo : 0;
+                hi[t][c] = n < R ? kr.hi : 0;
+                m[t][c] = -INFINITY;
+                l[t][c] = 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < DP / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[t][j][e] = 0.f;
+        }
+        const float scale2 = a.scale * 1.4426950408889634f;
+        const int arow = lane & 15, brow = (lane & 7) + ((lane >> 4) & 1) * 8;
+        bool ok = true;
+        for (int it = 0; it < tiles; ++it) {
+            const int s = it % kStages;
+            if (!mbar_wait_spin(&ctl->full[s], (it / kStages) & 1, wait_ns, status)) *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
+            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&ctl->abort) != 0)) {
+                ok = false;
+                break;
+            }
+            const int key0 = (tile0 + it) * kKeys + warp * 16;
+            const uint32_t ks = base + uint32_t(s * 2 * L::PLANE + warp * 16 * 128), vs = ks + L::PLANE;
+            if (key0 < last && key0 + 16 > first) {
+                const bool clean = key0 >= rs.lo_all && key0 + 16 <= min(rs.hi_all, last) && key0 >= first;
+                if (!clean) {
+                    // rows of V that no query row sees (or that this chunk does not own) become zeros; where only
+                    // some see them, values that are not finite go to those rows' sums apart
+                    uint8_t *vrow = smem + (vs - base) + (lane >> 1) * 128;
+                    const int key = key0 + (lane >> 1);
+                    const bool mine = key >= first && key < last;
+                    for (int c = lane & 1; c < L::HALVES * 8; c += 2) {
+                        uint4 *p = reinterpret_cast<uint4 *>(vrow + (c >> 3) * L::HALF + (((c & 7) ^ ((lane >> 1) & 7)) << 4));
+                        if (!mine) {
+                            *p = make_uint4(0, 0, 0, 0);
+                        } else if (key < rs.lo_all || key >= rs.hi_all) {
+                            uint4 w = *p;
+                            if (any_nonfinite<T>(w)) {
+                                take_nonfinite<T>(w, [&](int e, float x) {
+                                    for (int n = 0; n < R; ++n) {
+                                        const KeyRange kr = keys_of(sp, n / G, a.window, a.causal);
+                                        if (key >= kr.lo && key < kr.hi) atomicAdd(&poison[n * DP + c * 8 + e], x);
+                                    }
+                                });
+                                *p = w;
+                                ctl->poisoned = 1;
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+                // S^T = K Q^T, [16 keys] x [8 NT rows]
+                float sc[NT][4];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[t][e] = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    uint32_t ka[4];
+                    const int c = 2 * (kk & 3) + (lane >> 4);
+                    ldsm4(ka, ks + uint32_t((kk >> 2) * L::HALF + arow * 128 + ((c ^ (arow & 7)) << 4)));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) mma_16x8<T>(sc[t], ka, q[t][kk][0], q[t][kk][1]);
+                }
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        sc[t][e] *= scale2;
+                        if (!clean) {
+                            const int key = key0 + (lane >> 2) + (e >> 1) * 8, c = e & 1;
+                            if (key < max(lo[t][c], first) || key >= min(hi[t][c], last)) sc[t][e] = -INFINITY;
+                        }
+                    }
+                    // lazy rescale: m follows the maximum only when it grows by more than 2^8
+                    const float x0 = fmaxf(sc[t][0], sc[t][2]), x1 = fmaxf(sc[t][1], sc[t][3]);
+                    if (__any_sync(0xffffffffu, x0 > m[t][0] + 8.f || x1 > m[t][1] + 8.f)) {
+                        float y0 = fmaxf(x0, m[t][0]), y1 = fmaxf(x1, m[t][1]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            y0 = fmaxf(y0, __shfl_xor_sync(0xffffffffu, y0, d));
+                            y1 = fmaxf(y1, __shfl_xor_sync(0xffffffffu, y1, d));
+                        }
+                        const float f0 = y0 == m[t][0] ? 1.f : fast_ex2(m[t][0] - y0);
+                        const float f1 = y1 == m[t][1] ? 1.f : fast_ex2(m[t][1] - y1);
+                        m[t][0] = y0;
+                        m[t][1] = y1;
+                        l[t][0] *= f0;
+                        l[t][1] *= f1;
+#pragma unroll
+                        for (int j = 0; j < DP / 16; ++j) {
+                            o[t][j][0] *= f0;
+                            o[t][j][1] *= f1;
+                            o[t][j][2] *= f0;
+                            o[t][j][3] *= f1;
+                        }
+                    }
+                    const float u0 = m[t][0] == -INFINITY ? 0.f : m[t][0], u1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+                    float p[4];
+                    p[0] = fast_ex2(sc[t][0] - u0);
+                    p[1] = fast_ex2(sc[t][1] - u1);
+                    p[2] = fast_ex2(sc[t][2] - u0);
+                    p[3] = fast_ex2(sc[t][3] - u1);
+                    l[t][0] += p[0] + p[2];
+                    l[t][1] += p[1] + p[3];
+                    // the weights in the cache's type (the second product's operands have one type); an f32 output
+                    // keeps their remainder as a second term
+                    const uint32_t w0 = pack16<T>(p[0], p[1]), w1 = pack16<T>(p[2], p[3]);
+                    ph[t][0] = transpose_8x8(w0);
+                    ph[t][1] = transpose_8x8(w1);
+                    if constexpr (SPLIT_P) {
+                        float h[4];
+                        unpack16<T>(w0, h[0], h[1]);
+                        unpack16<T>(w1, h[2], h[3]);
+                        pl[t][0] = transpose_8x8(pack16<T>(p[0] - h[0], p[1] - h[1]));
+                        pl[t][1] = transpose_8x8(pack16<T>(p[2] - h[2], p[3] - h[3]));
+                    }
+                }
+                // O^T += V^T P^T
+#pragma unroll
+                for (int j = 0; j < DP / 16; ++j) {
+                    uint32_t va[4];
+                    const int c = 2 * (j & 3) + ((lane >> 3) & 1);
+                    ldsm4_t(va, vs + uint32_t((j >> 2) * L::HALF + brow * 128 + ((c ^ (brow & 7)) << 4)));
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) {
+                        mma_16x8<T>(o[t][j], va, ph[t][0], ph[t][1]);
+                        if constexpr (SPLIT_P) mma_16x8<T>(o[t][j], va, pl[t][0], pl[t][1]);
+                    }
+                }
+                if (!clean) fence_proxy_async_smem();  // this warp wrote where the next copies land
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->empty[s]);
+        }
+        if (!ok) {
+            if (lane == 0) *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
+        }
+        // m and l of this warp's keys
+        float *wm = reinterpret_cast<float *>(smem + L::OFF_ML), *wl = wm + kConsumers * L::ROWS;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float x = l[t][c];
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
+                if (lane < 4) {
+                    wm[warp * L::ROWS + t * 8 + 2 * lane + c] = m[t][c];
+                    wl[warp * L::ROWS + t * 8 + 2 * lane + c] = x;
+                }
+            }
+    }
+    __syncthreads();
+    if (*reinterpret_cast<volatile int *>(&ctl->abort)) return;
+    const float *wm = reinterpret_cast<const float *>(smem + L::OFF_ML), *wl = wm + kConsumers * L::ROWS;
+    float *ob = reinterpret_cast<float *>(smem);  // [warp][row][OPAD], over the ring
+    if (warp < kConsumers) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int n = t * 8 + 2 * (lane & 3) + c;
+                float top = wm[n];
+#pragma unroll
+                for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, wm[w * L::ROWS + n]);
+                const float f = m[t][c] == top ? 1.f : fast_ex2(m[t][c] - top);
+#pragma unroll
+                for (int j = 0; j < DP / 16; ++j) {
+                    ob[(warp * L::ROWS + n) * L::OPAD + j * 16 + (lane >> 2)] = o[t][j][c] * f;
+                    ob[(warp * L::ROWS + n) * L::OPAD + j * 16 + 8 + (lane >> 2)] = o[t][j][2 + c] * f;
+                }
+            }
+    }
+    __syncthreads();
+    const bool whole = rs.chunks <= 1;
+    const int64_t at = (int64_t(b) * a.kv_heads + g) * plan.chunks + chunk;
+    for (int i = threadIdx.x; i < R * (DP / 4); i += kThreads) {
+        const int n = i / (DP / 4), d = 4 * (i % (DP / 4));
+        if (d >= a.dim) continue;
+        float top = wm[n], sum = 0.f;
+#pragma unroll
+        for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, wm[w * L::ROWS + n]);
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kConsumers; ++w) {
+            const float mw = wm[w * L::ROWS + n];
+            sum += wl[w * L::ROWS + n] * (mw == top ? 1.f : fast_ex2(mw - top));
+            const float4 y = *reinterpret_cast<const float4 *>(&ob[(w * L::ROWS + n) * L::OPAD + d]);
+            x.x += y.x;
+            x.y += y.y;
+            x.z += y.z;
+            x.w += y.w;
+        }
+        if (ctl->poisoned) {
+            x.x += poison[n * DP + d];
+            x.y += poison[n * DP + d + 1];
+            x.z += poison[n * DP + d + 2];
+            x.w += poison[n * DP + d + 3];
+        }
+        if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
+            TO *out = static_cast<TO *>(a.out) + (int64_t(sp.q0) + n / G) * a.out_token + int64_t(g * G + n % G) * a.out_head + d;
+            store4(out, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+        } else {
+            *reinterpret_cast<float4 *>(part_o + (at * plan.rows + n) * a.dim + d) = x;
+            if (d == 0) part_ml[at * plan.rows + n] = make_float2(top, sum);
+        }
+    }
+}
+
+template <typename T, typename TO, int DP, int NT>
+cudaError_t launch_rows(const PagedArgs &a, const RowPlan &plan, const CUtensorMap &km, const CUtensorMap &vm, void *ws,
+                        const LaunchCtx &ctx) {
+    using L = RowLayout<DP, NT>;
+    auto kernel = paged_rows_kernel<T, TO, DP, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    float *po = static_cast<float *>(ws);
+    float2 *pml = reinterpret_cast<float2 *>(po + plan.partials(a) * a.dim);
+    e = launch_dependent(kernel, dim3(unsigned(int64_t(plan.chunks) * a.batch.seqs), unsigned(a.kv_heads)), kThreads,
+                         L::BYTES, ctx.stream, km, vm, a, plan, po, pml, ctx.status, ctx.wait_ns);
+    if (e != cudaSuccess || plan.chunks == 1) return e;
+    return launch_join<TO>(a, plan, po, pml, ctx);
+}
+
+template <typename T, typename TO>
+cudaError_t launch_rows_io(const PagedArgs &a, const RowPlan &plan, void *ws, const LaunchCtx &ctx) {
+    CUtensorMap km, vm;
+    cudaError_t e = cache_maps<T>(a, plan.box_rows, &km, &vm);
+    if (e != cudaSuccess) return e;
+    if (a.dim <= 64)
+        return plan.rows <= 8 ? launch_rows<T, TO, 64, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 64, 2>(a, plan, km, vm, ws, ctx);
+    return plan.rows <= 8 ? launch_rows<T, TO, 128, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 128, 2>(a, plan, km, vm, ws, ctx);
+}
+
+// Keys a chunk: as many chunks as give every SM's two CTAs three turns at the
+// host's bound of the keys (sequences are shorter than the bound), between 256
+// keys, below which a chunk is mostly start and end, and 1024, where a partial
+// result is 1/64 of the chunk's bytes at 8 rows.
+constexpr int kMinChunk = 256, kMaxChunk = 1024, kTurns = 6;
+
+RowPlan row_plan(int64_t heads, int64_t kv_heads, int64_t seqs, int64_t max_q, int64_t max_kv, int64_t window,
+                 int page_size) {
+    RowPlan p = {};
+    p.rows = int(max_q * (heads / kv_heads));
+    // keys from the tile that the first token's window begins in to the last token
+    const int64_t span = window && window < max_kv ? std::min(max_kv, window + max_q + kKeys - 2) : max_kv;
+    const int64_t want = (seqs * kv_heads * span + kTurns * kNumSms - 1) / (kTurns * kNumSms);
+    const int64_t chunk = std::min<int64_t>(kMaxChunk, std::max<int64_t>(kMinChunk, (want + kKeys - 1) / kKeys * kKeys));
+    p.chunk = int(chunk);
+    p.chunks = int(std::max<int64_t>(1, (span + chunk - 1) / chunk));
+    p.box_rows = std::min(page_size & -page_size, kKeys);
+    return p;
+}
+
+// The most chunks that row_plan gives for any window.
+int64_t row_chunks_bound(int64_t kv_heads, int64_t seqs, int64_t max_kv) {
+    const int64_t turns = (kTurns * kNumSms + seqs * kv_heads - 1) / (seqs * kv_heads);
+    return std::min((max_kv + kMinChunk - 1) / kMinChunk, std::max(turns, (max_kv + kMaxChunk - 1) / kMaxChunk));
 }
 
 }  // namespace
 
-size_t attention_paged_ws_bytes(int64_t, int64_t, int64_t, int64_t, int64_t, int64_t, int64_t) { return 0; }
+size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
+                                int64_t max_kv) {
+    const int64_t rows = std::min(max_q, tokens) * (heads / kv_heads);
+    if (rows > kRowsMax) return 0;
+    const int64_t chunks = row_chunks_bound(kv_heads, seqs, max_kv);
+    return chunks > 1 ? size_t(seqs * kv_heads * chunks * rows) * size_t(dim * 4 + 8) : 0;
+}
 
-cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, void *, const LaunchCtx &ctx) {
-    const int64_t blocks = (a.batch.tokens * a.heads + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    const unsigned g = unsigned(blocks), n = 32 * kWarps;
+cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx) {
+    if (int64_t(a.batch.max_q) * (a.heads / a.kv_heads) > kRowsMax) return launch_attention_paged_chunk(a, dtype, out_f32, ws, ctx);
+    const RowPlan p = row_plan(a.heads, a.kv_heads, a.batch.seqs, a.batch.max_q, a.batch.max_kv, a.window, a.batch.page_size);
+    if (int64_t(p.chunks) * a.batch.seqs > INT32_MAX) return cudaErrorInvalidValue;
     if (dtype == TQ2_F16) {
-        if (out_f32) paged_row_kernel<__half, float><<<g, n, 0, ctx.stream>>>(a, ctx.status);
-        else paged_row_kernel<__half, __half><<<g, n, 0, ctx.stream>>>(a, ctx.status);
-    } else {
-        if (out_f32) paged_row_kernel<__nv_bfloat16, float><<<g, n, 0, ctx.stream>>>(a, ctx.status);
-        else paged_row_kernel<__nv_bfloat16, __nv_bfloat16><<<g, n, 0, ctx.stream>>>(a, ctx.status);
+        if (out_f32) return launch_rows_io<__half, float>(a, p, ws, ctx);
+        return launch_rows_io<__half, __half>(a, p, ws, ctx);
     }
-    return cudaPeekAtLastError();
+    if (out_f32) return launch_rows_io<__nv_bfloat16, float>(a, p, ws, ctx);
+    return launch_rows_io<__nv_bfloat16, __nv_bfloat16>(a, p, ws, ctx);
 }
 
 }  // namespace tq2

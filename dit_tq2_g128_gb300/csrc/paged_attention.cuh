@@ -1,0 +1,215 @@
+// What the two paged attention kernels share: the cache's tensor maps and copies,
+// 16-bit packing, values that are not finite, and the join of partial results.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "tq2_internal.cuh"
+
+namespace tq2 {
+
+template <typename T>
+constexpr bool is_half = false;
+template <>
+constexpr bool is_half<__half> = true;
+
+// How a call is cut: chunks of `chunk` keys (a multiple of 64), `chunks` of them at
+// most, `rows` query rows per (sequence, key head, chunk), and the rows of a copy.
+struct RowPlan {
+    int rows;
+    int chunk;
+    int chunks;
+    int box_rows;
+    int64_t partials(const PagedArgs &a) const {
+        return chunks > 1 ? int64_t(a.batch.seqs) * a.kv_heads * chunks * rows : 0;
+    }
+};
+
+// 2^x by the hardware approximation (relative error about 2^-22; 2^-inf = 0)
+__device__ __forceinline__ float fast_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t drain_ns(uint64_t wait_ns) { return wait_ns > 1000000000ull ? wait_ns : 1000000000ull; }
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// rows of one page: feature x (a multiple of 64), head, slot, page
+__device__ __forceinline__ void tma_cache(uint32_t dst, const CUtensorMap *map, int x, int head, int slot, int page,
+                                          uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(slot), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack16(float a, float b) {
+    uint32_t r;
+    if constexpr (is_half<T>)
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    else
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void unpack16(uint32_t w, float &a, float &b) {
+    if constexpr (is_half<T>) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+        a = f.x;
+        b = f.y;
+    } else {
+        a = __uint_as_float(w << 16);
+        b = __uint_as_float(w & 0xffff0000u);
+    }
+}
+
+// Whether one of eight 16-bit values is infinite or NaN.
+template <typename T>
+__device__ __forceinline__ bool any_nonfinite(const uint4 &w) {
+    constexpr uint32_t e = is_half<T> ? 0x7c00u : 0x7f80u;
+    bool found = false;
+    for (uint32_t x : {w.x, w.y, w.z, w.w}) found |= (x & e) == e || ((x >> 16) & e) == e;
+    return found;
+}
+
+// Sets the values of w that are not finite to zero and hands each to add(element, value).
+template <typename T, typename F>
+__device__ __forceinline__ void take_nonfinite(uint4 &w, F add) {
+    constexpr uint32_t e = is_half<T> ? 0x7c00u : 0x7f80u;
+    uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        unpack16<T>(x[i], a, b);
+        if ((x[i] & e) == e) {
+            add(2 * i, a);
+            x[i] &= 0xffff0000u;
+        }
+        if (((x[i] >> 16) & e) == e) {
+            add(2 * i + 1, b);
+            x[i] &= 0x0000ffffu;
+        }
+    }
+    w = make_uint4(x[0], x[1], x[2], x[3]);
+}
+
+__device__ __forceinline__ void store4(float *p, float a, float b, float c, float d) {
+    *reinterpret_cast<float4 *>(p) = make_float4(a, b, c, d);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T *p, float a, float b, float c, float d) {
+    *reinterpret_cast<uint2 *>(p) = make_uint2(pack16<T>(a, b), pack16<T>(c, d));
+}
+
+// Tensor maps of the cache's planes: [pages][slots][heads][dim] in the cache's own
+// strides, boxes of 64 features of `box_rows` slots with the 128-byte swizzle
+// (features past dim are filled with zeros).
+template <typename T>
+cudaError_t cache_maps(const PagedArgs &a, int box_rows, CUtensorMap *km, CUtensorMap *vm) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {cuuint64_t(a.dim), cuuint64_t(a.kv_heads), cuuint64_t(a.batch.page_size),
+                                cuuint64_t(a.batch.pages)};
+    // (a stride along an axis of one element is never used)
+    auto bytes = [&](int64_t s) { return cuuint64_t(s ? s : a.dim) * 2; };
+    const cuuint64_t strides[3] = {bytes(a.head_stride), bytes(a.slot_stride), bytes(a.page_stride)};
+    const cuuint32_t box[4] = {64, 1, cuuint32_t(box_rows), 1}, step[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = is_half<T> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    for (int i = 0; i < 2; ++i)
+        if (enc(i ? vm : km, type, 4, const_cast<void *>(i ? a.v : a.k), dims, strides, box, step,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    return cudaSuccess;
+}
+
+// Launch that may begin before the work ahead of it in the stream has ended (the
+// kernel waits for that work itself before it touches memory).
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(unsigned(threads));
+    cfg.dynamicSmemBytes = size_t(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+constexpr int kJoinWarps = 4;
+
+// Joins the chunks of one (new token, head): out = sum_c 2^(m_c - m) O_c / sum_c
+// 2^(m_c - m) l_c, in the chunks' order within each warp and the warps' order
+// after that.  Reads what the attention launch before it wrote (mostly from L2).
+template <typename TO>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+paged_join_kernel(const PagedArgs a, const RowPlan plan, const float *__restrict__ part_o,
+                  const float2 *__restrict__ part_ml) {
+    __shared__ float sh_o[kJoinWarps][128], sh_l[kJoinWarps];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = int(blockIdx.x / unsigned(a.batch.max_q)), i = int(blockIdx.x % unsigned(a.batch.max_q));
+    bool bad = false;
+    const SeqSpan sp = seq_span(a.batch, b, bad);  // (reported by the launch before)
+    if (i >= sp.n) return;
+    const RowSpan rs = row_span(sp, a.window, a.causal, plan.chunk);
+    if (rs.chunks <= 1) return;
+    const int G = a.heads / a.kv_heads, row = i * G + h % G;
+    const int64_t at = ((int64_t(b) * a.kv_heads + h / G) * plan.chunks) * plan.rows + row;
+    float top = -INFINITY;
+    for (int c = lane; c < rs.chunks; c += 32) top = fmaxf(top, part_ml[at + int64_t(c) * plan.rows].x);
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    const bool mine = 4 * lane < a.dim;
+#pragma unroll 4
+    for (int c = warp; c < rs.chunks; c += kJoinWarps) {
+        const float2 ml = part_ml[at + int64_t(c) * plan.rows];
+        const float f = ml.x == top ? 1.f : fast_ex2(ml.x - top);
+        l = fmaf(f, ml.y, l);
+        if (mine) {
+            const float4 x = *reinterpret_cast<const float4 *>(part_o + (at + int64_t(c) * plan.rows) * a.dim + 4 * lane);
+            // (a chunk that this row sees nothing of has l = 0 and O = 0)
+            o.x = fmaf(f, x.x, o.x);
+            o.y = fmaf(f, x.y, o.y);
+            o.z = fmaf(f, x.z, o.z);
+            o.w = fmaf(f, x.w, o.w);
+        }
+    }
+    if (mine) *reinterpret_cast<float4 *>(&sh_o[warp][4 * lane]) = o;
+    if (lane == 0) sh_l[warp] = l;
+    __syncthreads();
+    if (warp == 0 && mine) {
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) {
+            const float4 x = *reinterpret_cast<const float4 *>(&sh_o[w][4 * lane]);
+            o.x += x.x;
+            o.y += x.y;
+            o.z += x.z;
+            o.w += x.w;
+            l += sh_l[w];
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        store4(static_cast<TO *>(a.out) + (int64_t(sp.q0) + i) * a.out_token + int64_t(h) * a.out_head + 4 * lane, o.x * inv,
+               o.y * inv, o.z * inv, o.w * inv);
+    }
+}
+
+template <typename TO>
+cudaError_t launch_join(const PagedArgs &a, const RowPlan &plan, const float *part_o, const float2 *part_ml,
+                        const LaunchCtx &ctx) {
+    return launch_dependent(paged_join_kernel<TO>, dim3(unsigned(int64_t(a.batch.seqs) * a.batch.max_q), unsigned(a.heads)),
+                            32 * kJoinWarps, 0, ctx.stream, a, plan, part_o, part_ml);
+}
+
+}  // namespace tq2

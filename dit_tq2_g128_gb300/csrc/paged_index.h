@@ -82,4 +82,18 @@ TQ2_HD KeyRange keys_of(const SeqSpan &sp, int i, int64_t window, bool causal) {
     return KeyRange{int(lo), int(hi)};
 }
 
+// What the new tokens of a span see together: some token sees a key only in
+// [lo, hi), every token sees all of [lo_all, hi_all); from `base` (lo, down to a
+// multiple of 64) the keys are cut into `chunks` chunks of `chunk` (0: no key).
+struct RowSpan {
+    int lo, hi, lo_all, hi_all, base, chunks;
+};
+TQ2_HD RowSpan row_span(const SeqSpan &sp, int64_t window, bool causal, int chunk) {
+    if (sp.n == 0) return RowSpan{0, 0, 0, 0, 0, 0};
+    const KeyRange first = keys_of(sp, 0, window, causal), last = keys_of(sp, sp.n - 1, window, causal);
+    RowSpan r{first.lo, last.hi, last.lo, first.hi, first.lo / 64 * 64, 0};
+    if (r.hi > r.lo) r.chunks = int((int64_t(r.hi) - r.base + chunk - 1) / chunk);
+    return r;
+}
+
 }  // namespace tq2

@@ -142,6 +142,9 @@ size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, in
 // dtype: the cache's (and q's); out_f32: out is f32 instead
 cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx);
 
+// The part of it for many rows per (sequence, key head) (attention_paged_chunk.cu).
+cudaError_t launch_attention_paged_chunk(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx);
+
 // Skinny-M tensor-core kernel (2 <= m <= 32, k up to the shared-memory limit
 // of its K slices): one launch, no workspace.  cudaErrorNotSupported outside.
 bool skinny_mma_fits(int64_t m, int64_t n, int64_t k);
@@ -150,6 +153,9 @@ cudaError_t launch_skinny_mma(const void *w_soa, const float *x, const float *re
 
 // Largest M the small-M CUDA-core kernel handles.
 constexpr int64_t kSkinnyMaxM = 16;
+
+// SMs of the part (for plans that are made without a device: workspace sizes).
+constexpr int kNumSms = 152;
 
 // ---------------------------------------------------------------------------
 // Device helpers
