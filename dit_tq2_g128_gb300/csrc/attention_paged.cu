@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
 template <typename T, typename TO, int DP, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const PagedArgs a, const RowPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml,
+                  const PagedArgs a, const KeyPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml,
                   unsigned int *status, uint64_t wait_ns) {
     using L = RowLayout<DP, NT>;
     constexpr bool SPLIT_P = sizeof(TO) == 4;
@@ -123,13 +123,14 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     bool bad = false;
     const SeqSpan sp = seq_span(a.batch, b, bad);
-    const RowSpan rs = row_span(sp, a.window, a.causal, plan.chunk);
-    if (sp.n == 0 || chunk >= max(rs.chunks, 1)) return;  // (CTA-uniform)
+    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
+    if (sp.n == 0 || chunk >= max(cut.chunks, 1)) return;  // (CTA-uniform)
+    const RowSpan rs = rows_see(sp, 0, sp.n - 1, a.window, a.causal);
     const int R = sp.n * G;
-    const int64_t k0 = rs.base + int64_t(chunk) * plan.chunk;
+    const int64_t k0 = cut.base + int64_t(chunk) * plan.chunk;
     const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
     const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
-    const int tile0 = int(k0) / kKeys, tiles = rs.chunks ? (last + kKeys - 1) / kKeys - tile0 : 0;
+    const int tile0 = int(k0) / kKeys, tiles = cut.chunks ? (last + kKeys - 1) / kKeys - tile0 : 0;
     if (sp.n > 1)  // (one token's keys are seen by all its rows or by none)
         for (int i = threadIdx.x; i < L::ROWS * DP; i += kThreads) poison[i] = 0.f;
     __syncthreads();
@@ -388,8 +389,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
     }
     __syncthreads();
-    const bool whole = rs.chunks <= 1;
-    const int64_t at = (int64_t(b) * a.kv_heads + g) * plan.chunks + chunk;
+    const bool whole = cut.chunks <= 1;
     for (int i = threadIdx.x; i < R * (DP / 4); i += kThreads) {
         const int n = i / (DP / 4), d = 4 * (i % (DP / 4));
         if (d >= a.dim) continue;
@@ -418,21 +418,22 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             TO *out = static_cast<TO *>(a.out) + (int64_t(sp.q0) + n / G) * a.out_token + int64_t(g * G + n % G) * a.out_head + d;
             store4(out, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
         } else {
-            *reinterpret_cast<float4 *>(part_o + (at * plan.rows + n) * a.dim + d) = x;
-            if (d == 0) part_ml[at * plan.rows + n] = make_float2(top, sum);
+            const int64_t at = partial_at(a, chunk, int64_t(sp.q0) + n / G, g * G + n % G);
+            *reinterpret_cast<float4 *>(part_o + at * a.dim + d) = x;
+            if (d == 0) part_ml[at] = make_float2(top, sum);
         }
     }
 }
 
 template <typename T, typename TO, int DP, int NT>
-cudaError_t launch_rows(const PagedArgs &a, const RowPlan &plan, const CUtensorMap &km, const CUtensorMap &vm, void *ws,
+cudaError_t launch_rows(const PagedArgs &a, const KeyPlan &plan, const CUtensorMap &km, const CUtensorMap &vm, void *ws,
                         const LaunchCtx &ctx) {
     using L = RowLayout<DP, NT>;
     auto kernel = paged_rows_kernel<T, TO, DP, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
     float *po = static_cast<float *>(ws);
-    float2 *pml = reinterpret_cast<float2 *>(po + plan.partials(a) * a.dim);
+    float2 *pml = reinterpret_cast<float2 *>(po + int64_t(plan.chunks) * a.batch.tokens * a.heads * a.dim);
     e = launch_dependent(kernel, dim3(unsigned(int64_t(plan.chunks) * a.batch.seqs), unsigned(a.kv_heads)), kThreads,
                          L::BYTES, ctx.stream, km, vm, a, plan, po, pml, ctx.status, ctx.wait_ns);
     if (e != cudaSuccess || plan.chunks == 1) return e;
@@ -440,13 +441,14 @@ cudaError_t launch_rows(const PagedArgs &a, const RowPlan &plan, const CUtensorM
 }
 
 template <typename T, typename TO>
-cudaError_t launch_rows_io(const PagedArgs &a, const RowPlan &plan, void *ws, const LaunchCtx &ctx) {
+cudaError_t launch_rows_io(const PagedArgs &a, const KeyPlan &plan, void *ws, const LaunchCtx &ctx) {
     CUtensorMap km, vm;
     cudaError_t e = cache_maps<T>(a, plan.box_rows, &km, &vm);
     if (e != cudaSuccess) return e;
+    const bool few = int64_t(a.batch.max_q) * (a.heads / a.kv_heads) <= 8;
     if (a.dim <= 64)
-        return plan.rows <= 8 ? launch_rows<T, TO, 64, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 64, 2>(a, plan, km, vm, ws, ctx);
-    return plan.rows <= 8 ? launch_rows<T, TO, 128, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 128, 2>(a, plan, km, vm, ws, ctx);
+        return few ? launch_rows<T, TO, 64, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 64, 2>(a, plan, km, vm, ws, ctx);
+    return few ? launch_rows<T, TO, 128, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 128, 2>(a, plan, km, vm, ws, ctx);
 }
 
 // Keys a chunk: as many chunks as give every SM's two CTAs three turns at the
@@ -455,16 +457,12 @@ cudaError_t launch_rows_io(const PagedArgs &a, const RowPlan &plan, void *ws, co
 // result is 1/64 of the chunk's bytes at 8 rows.
 constexpr int kMinChunk = 256, kMaxChunk = 1024, kTurns = 6;
 
-RowPlan row_plan(int64_t heads, int64_t kv_heads, int64_t seqs, int64_t max_q, int64_t max_kv, int64_t window,
-                 int page_size) {
-    RowPlan p = {};
-    p.rows = int(max_q * (heads / kv_heads));
-    // keys from the tile that the first token's window begins in to the last token
-    const int64_t span = window && window < max_kv ? std::min(max_kv, window + max_q + kKeys - 2) : max_kv;
+KeyPlan row_plan(int64_t kv_heads, int64_t seqs, int64_t max_q, int64_t max_kv, int64_t window, int page_size) {
+    KeyPlan p = {};
+    const int64_t span = key_span(max_q, max_kv, window);
     const int64_t want = (seqs * kv_heads * span + kTurns * kNumSms - 1) / (kTurns * kNumSms);
-    const int64_t chunk = std::min<int64_t>(kMaxChunk, std::max<int64_t>(kMinChunk, (want + kKeys - 1) / kKeys * kKeys));
-    p.chunk = int(chunk);
-    p.chunks = int(std::max<int64_t>(1, (span + chunk - 1) / chunk));
+    p.chunk = int(std::min<int64_t>(kMaxChunk, std::max<int64_t>(kMinChunk, (want + 127) / 128 * 128)));
+    p.chunks = int(std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk));
     p.box_rows = std::min(page_size & -page_size, kKeys);
     return p;
 }
@@ -480,14 +478,14 @@ int64_t row_chunks_bound(int64_t kv_heads, int64_t seqs, int64_t max_kv) {
 size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
                                 int64_t max_kv) {
     const int64_t rows = std::min(max_q, tokens) * (heads / kv_heads);
-    if (rows > kRowsMax) return 0;
-    const int64_t chunks = row_chunks_bound(kv_heads, seqs, max_kv);
-    return chunks > 1 ? size_t(seqs * kv_heads * chunks * rows) * size_t(dim * 4 + 8) : 0;
+    const int64_t chunks = rows > kRowsMax ? attention_paged_chunk_bound(heads, kv_heads, seqs, tokens, max_kv)
+                                           : row_chunks_bound(kv_heads, seqs, max_kv);
+    return partial_bytes(chunks, tokens, heads, dim);
 }
 
 cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx) {
     if (int64_t(a.batch.max_q) * (a.heads / a.kv_heads) > kRowsMax) return launch_attention_paged_chunk(a, dtype, out_f32, ws, ctx);
-    const RowPlan p = row_plan(a.heads, a.kv_heads, a.batch.seqs, a.batch.max_q, a.batch.max_kv, a.window, a.batch.page_size);
+    const KeyPlan p = row_plan(a.kv_heads, a.batch.seqs, a.batch.max_q, a.batch.max_kv, a.window, a.batch.page_size);
     if (int64_t(p.chunks) * a.batch.seqs > INT32_MAX) return cudaErrorInvalidValue;
     if (dtype == TQ2_F16) {
         if (out_f32) return launch_rows_io<__half, float>(a, p, ws, ctx);

@@ -1,83 +1,675 @@
-// Attention of a step's new tokens over a paged key/value cache.
+// Attention of a step's new tokens over a paged key/value cache: many query rows
+// per (sequence, key head), on the tcgen05 tensor cores.
 //
-// One warp per (token, head): lanes share the head's elements, keys one after the
-// other with the running maximum and sum of the softmax, all in f32.
+// Mathematics: the online softmax of attention_paged.cu with the query rows in M.
+// The rows of a sequence and key head are its new tokens times the query heads of
+// the group, row = token * G + head, so a 128-row tile of a chunk reads each key
+// for all G heads at once.
+//
+//  * A CTA owns up to 256 consecutive rows (two tiles) of one (sequence, key head)
+//    and a chunk of keys, in blocks of 128.  Warp 0 copies K and V through two-stage
+//    rings by paged tensor copies (lane = box of rows inside one page); warp 1 issues
+//    the MMAs; warps 2-3 look after V (below); warps 4-7 and 8-11 are two softmax
+//    groups, one thread per row (= tensor-memory lane).
+//  * Units: with two tiles, unit n is (block n / 2, tile n % 2); with one tile, block
+//    n.  Unit n uses scores S, weights P, sums O, and softmax group n % 2.  So one tile
+//    keeps both groups busy as well: they hold the even and the odd blocks' softmax
+//    and meet at the end.  MMA order: P V of unit n, then S of unit n + 2 over the
+//    same columns (MMAs of one thread execute in issue order).
+//  * Tensor memory: S of group w at columns 128 w, O at 256 + 128 w.  P overwrites S in
+//    the cache's type, 32 columns a 64 keys; for an f32 output the weights' remainder
+//    follows as a second term, in columns that S has left.
+//  * V stays as it lies in the cache, [key][feature]: the second MMA's B operand is
+//    MN-major, with the feature halves 16 KB apart (leading offset) and 8-key groups 1 KB
+//    apart (stride offset).  No transposed copy of V exists.
+//  * V's slots that no row sees are zeroed in shared memory, and where only some rows
+//    see a key, values that are not finite are zeroed there and added, at the end, to
+//    the rows that see them (0 * NaN is NaN).
+// Every wait is bounded; a timeout sets the device status word and the CTA drains
+// and exits.
+#include <algorithm>
+#include <cmath>
+
 #include <cuda_bf16.h>
 
-#include "tq2_internal.cuh"
+#include "paged_attention.cuh"
 
 namespace tq2 {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kRows = 128;      // rows of a tile (MMA M)
+constexpr int kBlock = 128;     // keys of a block
+constexpr int kCtaRows = 2 * kRows;
+constexpr int kThreads = 384;
+constexpr int kMaxSplits = 64;
+constexpr int kMinBlocks = 4;   // blocks a chunk, at least
+constexpr uint32_t kTmemCols = 512, kOCol = 256;
+constexpr float kLazy = 8.f;    // log2 growth of the maximum that O is rescaled for
+constexpr int W_COPY = 0, W_MMA = 1, W_FIX = 2, W_SOFT = 4;
 
-__device__ __forceinline__ float up(__half x) { return __half2float(x); }
-__device__ __forceinline__ float up(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void put(float x, float *p) { *p = x; }
-__device__ __forceinline__ void put(float x, __half *p) { *p = __float2half_rn(x); }
-__device__ __forceinline__ void put(float x, __nv_bfloat16 *p) { *p = __float2bfloat16_rn(x); }
+template <int DP>
+struct ChunkLayout {
+    static constexpr int HALVES = DP / 64;
+    static constexpr int HALF = 128 * 128;            // 128 rows x 64 features, swizzled
+    static constexpr int TILE = HALF * HALVES;        // Q tile, K block, V block
+    static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + 2 * TILE;
+    static constexpr int OFF_CTL = OFF_V + 2 * TILE;
+    static constexpr int OFF_ML = OFF_CTL + 256;      // m, l of group 1 (one tile)
+    static constexpr int BYTES = OFF_ML + 2 * kRows * 4 + 1024;
+    static constexpr int MPAD = DP + 4;               // f32 row of the groups' exchange, over Q and K
+    static_assert(kRows * MPAD * 4 <= OFF_V, "the exchange reuses Q and K");
+    static_assert(BYTES <= 232448, "shared memory budget");
+};
 
-template <typename T, typename TO>
-__global__ void __launch_bounds__(32 * kWarps) paged_row_kernel(const PagedArgs a, unsigned int *status) {
+struct ChunkCtl {
+    uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_ready[2], v_empty[2];
+    uint64_t s_full[2], p_full[2], o_done[2], drain;
+    uint32_t tmem_base;
+    int abort, poisoned;
+};
+static_assert(sizeof(ChunkCtl) <= 256, "control block");
+
+// Matrix descriptors (128-byte swizzle).  K-major: rows 128 B apart, 8-row groups
+// 1024 B.  MN-major: 64 features contiguous, keys 128 B apart; 8-key groups 1024 B
+// (stride offset), the next 64 features `HALF` bytes on (leading offset).
+__device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+           (uint64_t(2) << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t half) {
+    return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(half >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+           (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], A read from tensor memory (lane = row, column c =
+// elements 2c, 2c + 1)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {  // (a NaN operand is ignored)
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t r, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(r));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The sequence and first row of CTA slot `slot`: sequences and their row tiles from
+// the last to the first (the last tiles of a causal prompt are the longest).  One
+// warp; false if the slot is past the last tile.
+__device__ __forceinline__ bool find_rows(const BatchView &bt, int G, int slot, int &b_out, int &row0, unsigned int *status) {
     const int lane = threadIdx.x & 31;
-    const int64_t row = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t t = row / a.heads;
-    const int h = int(row - t * a.heads);
-    if (t >= a.batch.tokens) return;
-    const int b = seq_of(a.batch, t);
-    if (b < 0) return;
+    for (int top = bt.seqs; top > 0; top -= 32) {
+        const int b = top - 1 - lane;
+        int tiles = 0;
+        if (b >= 0) {
+            bool bad = false;
+            const SeqSpan sp = seq_span(bt, b, bad);
+            report_bad(bad, status);
+            tiles = int((int64_t(sp.n) * G + kCtaRows - 1) / kCtaRows);
+        }
+        int upto = tiles;  // inclusive sums over the lanes
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, slot < upto);
+        if (hit) {
+            const int l = __ffs(hit) - 1;
+            b_out = top - 1 - l;
+            row0 = (__shfl_sync(0xffffffffu, upto, l) - 1 - slot) * kCtaRows;
+            return true;
+        }
+        slot -= __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
+
+template <typename T, typename TO, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a,
+                   const KeyPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml, unsigned int *status,
+                   uint64_t wait_ns) {
+    using L = ChunkLayout<DP>;
+    constexpr bool SPLIT_P = sizeof(TO) == 4;
+    extern __shared__ uint8_t chunk_raw[];
+    const uint32_t raw = smem_u32(chunk_raw), pad = (1024u - (raw & 1023u)) & 1023u, base = raw + pad;
+    uint8_t *smem = chunk_raw + pad;
+    ChunkCtl *ctl = reinterpret_cast<ChunkCtl *>(smem + L::OFF_CTL);
+    volatile int *abort_flag = &ctl->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t sQ = base, sK = base + L::OFF_K, sV = base + L::OFF_V;
+
+    // the tables, q and the cache may be written by the kernel before this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // slot = tile * kv_heads * chunks + head * chunks + chunk: a tile's heads and chunks run together
+    const unsigned per = unsigned(a.kv_heads) * unsigned(plan.chunks);
+    const int slot = int(blockIdx.x / per), g = int(blockIdx.x % per) / plan.chunks, chunk = int(blockIdx.x % per) % plan.chunks;
+    const int G = a.heads / a.kv_heads;
+    int b = 0, row0 = 0;
+    if (!find_rows(a.batch, G, slot, b, row0, status)) return;
     bool bad = false;
     const SeqSpan sp = seq_span(a.batch, b, bad);
-    if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
-    const KeyRange kr = keys_of(sp, int(t - sp.q0), a.window, a.causal);
-    const T *q = static_cast<const T *>(a.q) + t * a.q_token + int64_t(h) * a.q_head;
-    const int64_t head = int64_t(h / (a.heads / a.kv_heads)) * a.head_stride;
-    float qr[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) qr[i] = lane + 32 * i < a.dim ? up(q[lane + 32 * i]) : 0.f;
-    for (int j = kr.lo; j < kr.hi; ++j) {
-        const int in_table = j / a.batch.page_size;
-        const int64_t page = page_of(a.batch, b, in_table, bad);
-        if (page < 0) continue;
-        const int64_t at = page * a.page_stride + int64_t(j - in_table * a.batch.page_size) * a.slot_stride + head;
-        const T *k = static_cast<const T *>(a.k) + at, *v = static_cast<const T *>(a.v) + at;
-        float s = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < a.dim) s = fmaf(qr[i], up(k[lane + 32 * i]), s);
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale;
-        const float mn = fmaxf(m, s);
-        const float c = m == mn ? 1.f : expf(m - mn), p = s == mn ? 1.f : expf(s - mn);
-        l = l * c + p;
-        m = mn;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (lane + 32 * i < a.dim) o[i] = fmaf(p, up(v[lane + 32 * i]), o[i] * c);
+    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
+    const int rows = min(kCtaRows, int(int64_t(sp.n) * G - row0));
+    const RowSpan rs = rows_see(sp, row0 / G, (row0 + rows - 1) / G, a.window, a.causal);
+    const bool whole = cut.chunks <= 1;
+    const int64_t k0 = cut.base + int64_t(chunk) * plan.chunk;
+    const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
+    const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
+    const bool none = cut.chunks == 0 || last <= first;
+    if (none && !(whole && chunk == 0)) return;
+    const int block0 = first / kBlock, nb = none ? 0 : (last + kBlock - 1) / kBlock - block0;
+    const int nt = rows > kRows ? 2 : 1, units = nt * nb;
+    auto block_of = [&](int n) { return nt == 2 ? n >> 1 : n; };
+
+    if (threadIdx.x == 0) {
+        mbar_init(&ctl->q_ready, 2 * kRows);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl->k_full[s], 1);
+            mbar_init(&ctl->k_empty[s], 1);
+            mbar_init(&ctl->v_full[s], 1);
+            mbar_init(&ctl->v_ready[s], 2);
+            mbar_init(&ctl->v_empty[s], 1);
+            mbar_init(&ctl->s_full[s], 1);
+            mbar_init(&ctl->p_full[s], kRows);
+            mbar_init(&ctl->o_done[s], 1);
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort = 0;
+        ctl->poisoned = 0;
+        fence_mbarrier_init();
+        fence_proxy_async_smem();
     }
-    TO *out = static_cast<TO *>(a.out) + t * a.out_token + int64_t(h) * a.out_head;
-    const float inv = l > 0.f ? 1.f / l : (kr.hi > kr.lo ? l : 0.f);
-    report_bad(bad, status);
+    if (warp == W_MMA) {
+        tmem_alloc(&ctl->tmem_base, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+
+    if (warp == W_COPY) {
+        // ---- copies: lane = box of a block (lane + 32 i where boxes are small)
+        const int rb = plan.box_rows, boxes = kBlock / rb;
+        bool ok = true;
+        int ki = 0, vi = 0;  // blocks issued
+        for (int j = 0; j < nb && ok; ++j) {
+            const int s = j & 1, u = j >> 1;
+            int page[4], slot_in[4];
+            unsigned mask[4];
+            uint32_t count = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        if (lane + 32 * i < a.dim) put(o[i] * inv, out + lane + 32 * i);
+            for (int i = 0; i < 4; ++i) {
+                const int box = lane + 32 * i, key = (block0 + j) * kBlock + box * rb;
+                const bool want = box < boxes && key < last && key + rb > first;
+                mask[i] = __ballot_sync(0xffffffffu, want);
+                count += __popc(mask[i]);
+                page[i] = slot_in[i] = 0;
+                if (want) {
+                    const int entry = key / a.batch.page_size;
+                    const int64_t p = page_of(a.batch, b, entry, bad);
+                    page[i] = p < 0 ? 0 : int(p);  // (recorded; any page of the cache will do)
+                    slot_in[i] = key - entry * a.batch.page_size;
+                }
+            }
+            const uint32_t bytes = count * uint32_t(rb * 128 * L::HALVES);
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+                uint64_t *full = kv ? &ctl->v_full[s] : &ctl->k_full[s];
+                if (u > 0 && !mbar_wait_spin(kv ? &ctl->v_empty[s] : &ctl->k_empty[s], (u - 1) & 1, wait_ns, status)) ok = false;
+                ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
+                if (!ok) break;
+                if (lane == 0) mbar_expect_tx(full, bytes);
+                __syncwarp();
+                const uint32_t dst = (kv ? sV : sK) + uint32_t(s * L::TILE);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (mask[i] >> lane & 1)
+#pragma unroll
+                        for (int h = 0; h < L::HALVES; ++h)
+                            tma_cache(dst + uint32_t(h * L::HALF + (lane + 32 * i) * rb * 128), kv ? &vmap : &kmap, 64 * h, g,
+                                      slot_in[i], page[i], full);
+                if (kv) vi = j + 1; else ki = j + 1;
+            }
+        }
+        report_bad(bad, status);
+        if (!ok && lane == 0) *abort_flag = 1;
+        __syncwarp();
+        // every copy issued must land before the CTA exits
+        if (lane == 0) {
+            for (int j = max(0, ki - 2); j < ki; ++j) mbar_wait_bounded(&ctl->k_full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
+            for (int j = max(0, vi - 2); j < vi; ++j) mbar_wait_bounded(&ctl->v_full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
+        }
+        __syncwarp();
+    } else if (warp == W_MMA) {
+        // ---- MMAs: the whole warp waits, lane 0 issues
+        constexpr uint32_t type = is_half<T> ? 0u : (1u << 7) | (1u << 10);
+        const int nd = (a.dim + 15) / 16;  // 16-feature steps that hold anything
+        const uint32_t idesc_s = (1u << 4) | type | (uint32_t(kBlock >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
+        const uint32_t idesc_o = (1u << 4) | type | (1u << 16) | (uint32_t(nd * 2) << 17) | (uint32_t(kRows >> 4) << 24);
+        const bool leader = lane == 0;
+        auto wait_all = [&](uint64_t *bar, uint32_t parity) {
+            const bool got = mbar_wait_spin(bar, parity, wait_ns, status);
+            return __all_sync(0xffffffffu, got && *abort_flag == 0);
+        };
+        auto last_of_block = [&](int n) { return nt == 1 || (n & 1); };
+        auto first_of_block = [&](int n) { return nt == 1 || !(n & 1); };
+        auto issue_s = [&](int n) -> bool {
+            const int j = block_of(n), w = n & 1;
+            if (first_of_block(n) && !wait_all(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
+            tc_fence_after();
+            if (leader) {
+                const uint64_t da = desc_k(sQ + uint32_t(nt == 2 ? w * L::TILE : 0)), db = desc_k(sK + uint32_t((j & 1) * L::TILE));
+                for (int kk = 0; kk < nd; ++kk) {
+                    const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
+                    tc_mma_f16(tmem + uint32_t(w * 128), da + off, db + off, idesc_s, kk > 0);
+                }
+                tc_commit(&ctl->s_full[w]);
+                if (last_of_block(n)) tc_commit(&ctl->k_empty[j & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = units == 0 || wait_all(&ctl->q_ready, 0);
+        for (int n = 0; n < 2 && n < units && ok; ++n) ok = issue_s(n);
+        for (int n = 0; n < units && ok; ++n) {
+            const int j = block_of(n), w = n & 1;
+            if (first_of_block(n) && !wait_all(&ctl->v_ready[j & 1], (j >> 1) & 1)) { ok = false; break; }
+            if (!wait_all(&ctl->p_full[w], (n >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            if (leader) {
+                const uint64_t db = desc_mn(sV + uint32_t((j & 1) * L::TILE), L::HALF);
+                const uint32_t d = tmem + kOCol + uint32_t(w * 128), p = tmem + uint32_t(w * 128);
+#pragma unroll
+                for (int kk = 0; kk < kBlock / 16; ++kk) {
+                    const uint32_t pa = p + uint32_t((kk >> 2) * 64 + (kk & 3) * 8);
+                    const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
+                    mma_ts(d, pa, bk, idesc_o, (n > 1 || kk > 0) ? 1u : 0u);
+                    if constexpr (SPLIT_P) mma_ts(d, pa + 32, bk, idesc_o, 1u);
+                }
+                tc_commit(&ctl->o_done[w]);
+                if (last_of_block(n)) tc_commit(&ctl->v_empty[j & 1]);
+            }
+            __syncwarp();
+            if (n + 2 < units) ok = issue_s(n + 2);
+        }
+        if (!ok && leader) *abort_flag = 1;
+        __syncwarp();
+    } else if (warp < W_SOFT) {
+        // ---- V: slots that some row of the CTA must not multiply
+        const int tid = threadIdx.x - 32 * W_FIX;
+        for (int j = 0; j < nb; ++j) {
+            if (!mbar_wait_spin(&ctl->v_full[j & 1], (j >> 1) & 1, wait_ns, status)) *abort_flag = 1;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const int key0 = (block0 + j) * kBlock;
+            if (key0 < max(first, rs.lo_all) || key0 + kBlock > min(last, rs.hi_all)) {
+                uint8_t *v = smem + L::OFF_V + (j & 1) * L::TILE;
+                for (int i = tid; i < kBlock * L::HALVES * 8; i += 64) {
+                    const int r = i / (L::HALVES * 8), c = i % (L::HALVES * 8), key = key0 + r;
+                    uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * L::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                    if (key < first || key >= last) {
+                        *p = make_uint4(0, 0, 0, 0);
+                    } else if (key < rs.lo_all || key >= rs.hi_all) {
+                        uint4 w = *p;
+                        if (any_nonfinite<T>(w)) {
+                            take_nonfinite<T>(w, [](int, float) {});
+                            *p = w;
+                            ctl->poisoned = 1;  // (read behind the p_full / o_done chain that follows v_ready)
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->v_ready[j & 1]);
+        }
+    } else {
+        // ---- softmax groups; first, both bring the rows of Q into the swizzled tiles
+        const int w = (warp - W_SOFT) >> 2;
+        {
+            const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's sign
+            const T *q = static_cast<const T *>(a.q) + int64_t(sp.q0) * a.q_token;
+            for (int i = threadIdx.x - 32 * W_SOFT; i < nt * kRows * (DP / 8); i += 2 * kRows) {
+                const int r = i / (DP / 8), c = i % (DP / 8), row = row0 + r;
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (r < rows && 8 * c < a.dim) {
+                    x = *reinterpret_cast<const uint4 *>(q + int64_t(row / G) * a.q_token + int64_t(g * G + row % G) * a.q_head + 8 * c);
+                    x.x ^= flip;
+                    x.y ^= flip;
+                    x.z ^= flip;
+                    x.w ^= flip;
+                }
+                *reinterpret_cast<uint4 *>(smem + (r >> 7) * L::TILE + (c >> 3) * L::HALF + (r & 127) * 128 +
+                                           (((c & 7) ^ (r & 7)) << 4)) = x;
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&ctl->q_ready);
+        }
+        const int r = (warp & 3) * 32 + lane;                        // row in the tile = TMEM lane
+        const int row = (nt == 2 ? w * kRows : 0) + r;               // row of the CTA
+        const uint32_t tl = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + tl + uint32_t(w * 128), to = tmem + tl + kOCol + uint32_t(w * 128);
+        // scores stay unscaled; scale2 > 0 enters with the exponential (a zero scale as a tiny one, so that -inf stays)
+        const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        const KeyRange kr = row < rows ? keys_of(sp, (row0 + row) / G, a.window, a.causal) : KeyRange{0, INT32_MAX};  // (rows past the end: never written)
+        const int lo = max(kr.lo, first), hi = min(kr.hi, last);
+        const uint64_t scale22 = pair(scale2, scale2);
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        int done = 0;  // units of this group
+        for (int n = w; n < units; n += 2, ++done) {
+            if (!mbar_wait_spin(&ctl->s_full[w], done & 1, wait_ns, status)) *abort_flag = 1;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+            tc_fence_after();
+            const int key0 = (block0 + block_of(n)) * kBlock;
+            const int from = lo - key0, upto = hi - key0;  // this row's keys of the block: [from, upto)
+            const bool full = __all_sync(0xffffffffu, from <= 0 && upto >= kBlock);
+            float mx = -INFINITY;
+#pragma unroll
+            for (int cp = 0; cp < 2; ++cp) {
+                uint32_t va[32], vb[32];
+                tm_ld32(ts + uint32_t(cp * 64), va);
+                tm_ld32(ts + uint32_t(cp * 64 + 32), vb);
+                tc_wait_ld();
+                if (full) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx = max3(mx, __uint_as_float(va[i]), __uint_as_float(vb[i]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int x = cp * 64 + i, y = x + 32;
+                        if (x >= from && x < upto) mx = fmaxf(mx, __uint_as_float(va[i]));
+                        if (y >= from && y < upto) mx = fmaxf(mx, __uint_as_float(vb[i]));
+                    }
+                }
+            }
+            const bool grow = mx > m && (mx - m) * scale2 > kLazy;
+            const float mu = grow ? mx : m;
+            const float alpha = grow ? fast_ex2((m - mu) * scale2) : 1.f;
+            const float neg = mu == -INFINITY ? 0.f : -mu * scale2;
+            const uint64_t neg2 = pair(neg, neg);
+            uint64_t sum2 = pair(0.f, 0.f);
+#pragma unroll
+            for (int cp = 0; cp < 2; ++cp) {
+                uint32_t va[32], vb[32], hp[32], lp[SPLIT_P ? 32 : 1];
+                tm_ld32(ts + uint32_t(cp * 64), va);
+                tm_ld32(ts + uint32_t(cp * 64 + 32), vb);
+                tc_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int i = 2 * e;  // keys 64 cp + i, + i + 1
+                    float s0 = __uint_as_float(i < 32 ? va[i] : vb[i - 32]);
+                    float s1 = __uint_as_float(i < 32 ? va[i + 1] : vb[i - 31]);
+                    if (!full) {
+                        const int x = cp * 64 + i;
+                        if (x < from || x >= upto) s0 = -INFINITY;
+                        if (x + 1 < from || x + 1 >= upto) s1 = -INFINITY;
+                    }
+                    float d0, d1;
+                    unpair(fma2(pair(s0, s1), scale22, neg2), d0, d1);
+                    const float p0 = fast_ex2(d0), p1 = fast_ex2(d1);
+                    sum2 = add2(sum2, pair(p0, p1));
+                    // the weights in the cache's type (one type for both operands); an f32 output keeps the remainder
+                    hp[e] = pack16<T>(p0, p1);
+                    if constexpr (SPLIT_P) {
+                        float h0, h1;
+                        unpack16<T>(hp[e], h0, h1);
+                        lp[e] = pack16<T>(p0 - h0, p1 - h1);
+                    }
+                }
+                tm_st32(ts + uint32_t(cp * 64), hp);
+                if constexpr (SPLIT_P) tm_st32(ts + uint32_t(cp * 64 + 32), lp);
+            }
+            float sum0, sum1;
+            unpair(sum2, sum0, sum1);
+            if (done > 0 && __any_sync(0xffffffffu, grow)) {
+                // rescale this row of O (rows that keep m by 1) once the unit before has accumulated into it
+                if (!mbar_wait_spin(&ctl->o_done[w], (done - 1) & 1, wait_ns, status)) *abort_flag = 1;
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < (a.dim + 31) / 32; ++c) {
+                    uint32_t o[32];
+                    tm_ld32(to + uint32_t(c * 32), o);
+                    tc_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+                    tm_st32(to + uint32_t(c * 32), o);
+                }
+            }
+            l = l * alpha + (sum0 + sum1);
+            m = mu;
+            tm_wait_st();
+            tc_fence_before();
+            mbar_arrive(&ctl->p_full[w]);
+        }
+        if (ok && done > 0) {
+            if (!mbar_wait_spin(&ctl->o_done[w], (done - 1) & 1, wait_ns, status)) *abort_flag = 1;
+            ok = !__any_sync(0xffffffffu, *abort_flag != 0);
+            tc_fence_after();
+        }
+        // one tile: group 1's rows go to group 0 through shared memory (over Q and K, which no MMA reads any more:
+        // both groups have seen their last MMA end)
+        float *ex = reinterpret_cast<float *>(smem);
+        float *exm = reinterpret_cast<float *>(smem + L::OFF_ML), *exl = exm + kRows;
+        float scale_own = 1.f, scale_other = 0.f;
+        if (nt == 1) {
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            ok = ok && *abort_flag == 0;
+            if (w == 1) {
+                exm[r] = m;
+                exl[r] = l;
+                if (ok && done > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < (a.dim + 31) / 32; ++c) {
+                        uint32_t o[32];
+                        tm_ld32(to + uint32_t(c * 32), o);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            *reinterpret_cast<uint4 *>(&ex[r * L::MPAD + c * 32 + i]) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    }
+                }
+            }
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (w == 0 && units > 1) {
+                const float mo = exm[r], top = fmaxf(m, mo);
+                scale_own = m == top ? 1.f : fast_ex2((m - top) * scale2);
+                scale_other = mo == top ? 1.f : fast_ex2((mo - top) * scale2);
+                l = l * scale_own + exl[r] * scale_other;
+                m = top;
+            }
+        }
+        if (ok && (nt == 2 || w == 0)) {
+            const int64_t t = int64_t(sp.q0) + (row0 + row) / G;
+            const int h = g * G + (row0 + row) % G;
+            const bool mine = row < rows;
+            const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // no key: zeros
+            const int64_t at = whole ? 0 : partial_at(a, chunk, t, h);
+            TO *out = static_cast<TO *>(a.out) + t * a.out_token + int64_t(h) * a.out_head;
+            if (!whole && mine) part_ml[at] = make_float2(m == -INFINITY ? m : m * scale2, l);
+            const bool poisoned = *reinterpret_cast<volatile int *>(&ctl->poisoned) != 0;
+#pragma unroll 1
+            for (int c = 0; c < (a.dim + 31) / 32; ++c) {
+                uint32_t o[32];
+                if (done > 0) {
+                    tm_ld32(to + uint32_t(c * 32), o);
+                    tc_wait_ld();
+                }
+                if (!mine) continue;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    float x = done > 0 ? __uint_as_float(o[i]) : 0.f;
+                    if (nt == 1 && units > 1) x = x * scale_own + ex[r * L::MPAD + c * 32 + i] * scale_other;
+                    o[i] = __float_as_uint(x);
+                }
+                if (poisoned) {  // values that are not finite, of keys that this row sees and another row does not
+                    for (int key = lo; key < hi; ++key) {
+                        if (key >= rs.lo_all && key < rs.hi_all) {
+                            key = rs.hi_all - 1;
+                            continue;
+                        }
+                        const int entry = key / a.batch.page_size;
+                        bool ignore = false;
+                        const int64_t p = page_of(a.batch, b, entry, ignore);
+                        const T *v = static_cast<const T *>(a.v) + (p < 0 ? 0 : p) * a.page_stride +
+                                     int64_t(key - entry * a.batch.page_size) * a.slot_stride + int64_t(g) * a.head_stride + c * 32;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c * 32 + i < a.dim) {
+                                const float x = float(v[i]);
+                                if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
+                            }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 4)
+                    if (c * 32 + i < a.dim) {
+                        const float x0 = __uint_as_float(o[i]) * inv, x1 = __uint_as_float(o[i + 1]) * inv;
+                        const float x2 = __uint_as_float(o[i + 2]) * inv, x3 = __uint_as_float(o[i + 3]) * inv;
+                        if (whole) store4(out + c * 32 + i, x0, x1, x2, x3);
+                        else store4(part_o + at * a.dim + c * 32 + i, x0, x1, x2, x3);
+                    }
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == W_MMA) {
+        if (lane == 0) {
+            // every issued MMA must be complete before TMEM is released
+            tc_commit(&ctl->drain);
+            mbar_wait_bounded(&ctl->drain, 0, drain_ns(wait_ns), status);
+        }
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// CTA slots of row tiles, at most
+int64_t tile_bound(int64_t group, int64_t seqs, int64_t tokens) {
+    return tokens * group / kCtaRows + std::min(seqs, tokens);
+}
+
+// The most chunks worth having: four turns of every SM.
+int64_t split_bound(int64_t ctas, int64_t max_kv) {
+    const int64_t blocks = (max_kv + kBlock - 1) / kBlock;
+    return std::max<int64_t>(1, std::min({(4 * kNumSms + ctas - 1) / ctas, (blocks + kMinBlocks - 1) / kMinBlocks,
+                                          int64_t(kMaxSplits)}));
+}
+
+// Chunks of keys: the number for which turns of the SMs x (blocks a CTA + the
+// cost of a CTA's start and end, in blocks) is least.
+KeyPlan chunk_plan(int64_t ctas, int64_t max_q, int64_t max_kv, int64_t window, int page_size) {
+    KeyPlan p = {};
+    const int64_t span = key_span(max_q, max_kv, window), blocks = std::max<int64_t>(1, (span + kBlock - 1) / kBlock);
+    int64_t best = 1;
+    double least = 0;
+    for (int64_t s = 1; s <= split_bound(ctas, span); ++s) {
+        const double turns = double((ctas * s + kNumSms - 1) / kNumSms);
+        const double cost = turns * (double((blocks + s - 1) / s) + (s > 1 ? 4.5 : 3.0)) + (s > 1 ? 2.0 : 0.0);
+        if (s == 1 || cost < least) {
+            best = s;
+            least = cost;
+        }
+    }
+    p.chunk = int((blocks + best - 1) / best * kBlock);
+    p.chunks = int((blocks * kBlock + p.chunk - 1) / p.chunk);
+    p.box_rows = std::min(page_size & -page_size, kBlock);
+    return p;
+}
+
+template <typename T, typename TO, int DP>
+cudaError_t launch_chunk(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
+    using L = ChunkLayout<DP>;
+    const int64_t tiles = tile_bound(a.heads / a.kv_heads, a.batch.seqs, a.batch.tokens);
+    const KeyPlan plan = chunk_plan(tiles * a.kv_heads, a.batch.max_q, a.batch.max_kv, a.window, a.batch.page_size);
+    const int64_t ctas = tiles * a.kv_heads * plan.chunks;
+    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
+    CUtensorMap km, vm;
+    cudaError_t e = cache_maps<T>(a, plan.box_rows, &km, &vm);
+    if (e != cudaSuccess) return e;
+    auto kernel = paged_chunk_kernel<T, TO, DP>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    float *po = static_cast<float *>(ws);
+    float2 *pml = reinterpret_cast<float2 *>(po + int64_t(plan.chunks) * a.batch.tokens * a.heads * a.dim);
+    e = launch_dependent(kernel, dim3(unsigned(ctas)), kThreads, L::BYTES, ctx.stream, km, vm, a, plan, po, pml, ctx.status,
+                         ctx.wait_ns);
+    if (e != cudaSuccess || plan.chunks == 1) return e;
+    return launch_join<TO>(a, plan, po, pml, ctx);
+}
+
+template <typename T, typename TO>
+cudaError_t launch_chunk_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
+    return a.dim <= 64 ? launch_chunk<T, TO, 64>(a, ws, ctx) : launch_chunk<T, TO, 128>(a, ws, ctx);
 }
 
 }  // namespace
 
-cudaError_t launch_attention_paged_chunk(const PagedArgs &a, int dtype, bool out_f32, void *, const LaunchCtx &ctx) {
-    const int64_t blocks = (a.batch.tokens * a.heads + kWarps - 1) / kWarps;
-    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-    const unsigned g = unsigned(blocks), n = 32 * kWarps;
+int64_t attention_paged_chunk_bound(int64_t heads, int64_t kv_heads, int64_t seqs, int64_t tokens, int64_t max_kv) {
+    return split_bound(tile_bound(heads / kv_heads, seqs, tokens) * kv_heads, max_kv);
+}
+
+cudaError_t launch_attention_paged_chunk(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx) {
     if (dtype == TQ2_F16) {
-        if (out_f32) paged_row_kernel<__half, float><<<g, n, 0, ctx.stream>>>(a, ctx.status);
-        else paged_row_kernel<__half, __half><<<g, n, 0, ctx.stream>>>(a, ctx.status);
-    } else {
-        if (out_f32) paged_row_kernel<__nv_bfloat16, float><<<g, n, 0, ctx.stream>>>(a, ctx.status);
-        else paged_row_kernel<__nv_bfloat16, __nv_bfloat16><<<g, n, 0, ctx.stream>>>(a, ctx.status);
+        if (out_f32) return launch_chunk_io<__half, float>(a, ws, ctx);
+        return launch_chunk_io<__half, __half>(a, ws, ctx);
     }
-    return cudaPeekAtLastError();
+    if (out_f32) return launch_chunk_io<__nv_bfloat16, float>(a, ws, ctx);
+    return launch_chunk_io<__nv_bfloat16, __nv_bfloat16>(a, ws, ctx);
 }
 
 }  // namespace tq2

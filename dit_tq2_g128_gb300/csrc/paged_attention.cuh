@@ -2,6 +2,8 @@
 // 16-bit packing, values that are not finite, and the join of partial results.
 #pragma once
 
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "tq2_internal.cuh"
@@ -13,17 +15,25 @@ constexpr bool is_half = false;
 template <>
 constexpr bool is_half<__half> = true;
 
-// How a call is cut: chunks of `chunk` keys (a multiple of 64), `chunks` of them at
-// most, `rows` query rows per (sequence, key head, chunk), and the rows of a copy.
-struct RowPlan {
-    int rows;
+// How a call is cut: at most `chunks` chunks of `chunk` keys (a multiple of 128) a
+// sequence, and the rows of a copy.  With more than one chunk, (m, l, O) of token
+// t, head h and chunk c is partial (c * tokens + t) * heads + h.
+struct KeyPlan {
     int chunk;
     int chunks;
     int box_rows;
-    int64_t partials(const PagedArgs &a) const {
-        return chunks > 1 ? int64_t(a.batch.seqs) * a.kv_heads * chunks * rows : 0;
-    }
 };
+__device__ __forceinline__ int64_t partial_at(const PagedArgs &a, int c, int64_t t, int h) {
+    return (int64_t(c) * a.batch.tokens + t) * a.heads + h;
+}
+inline size_t partial_bytes(int64_t chunks, int64_t tokens, int64_t heads, int64_t dim) {
+    return chunks > 1 ? size_t(chunks * tokens * heads) * size_t(dim * 4 + 8) : 0;
+}
+
+// Keys from the chunk base of the first token's window to the last token, at most.
+inline int64_t key_span(int64_t max_q, int64_t max_kv, int64_t window) {
+    return window && window < max_kv ? std::min(max_kv, window + max_q + 126) : max_kv;
+}
 
 // 2^x by the hardware approximation (relative error about 2^-22; 2^-inf = 0)
 __device__ __forceinline__ float fast_ex2(float x) {
@@ -152,34 +162,38 @@ constexpr int kJoinWarps = 4;
 // after that.  Reads what the attention launch before it wrote (mostly from L2).
 template <typename TO>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-paged_join_kernel(const PagedArgs a, const RowPlan plan, const float *__restrict__ part_o,
+paged_join_kernel(const PagedArgs a, const KeyPlan plan, const float *__restrict__ part_o,
                   const float2 *__restrict__ part_ml) {
     __shared__ float sh_o[kJoinWarps][128], sh_l[kJoinWarps];
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t t = blockIdx.x;
     const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = int(blockIdx.x / unsigned(a.batch.max_q)), i = int(blockIdx.x % unsigned(a.batch.max_q));
+    const int b = seq_of(a.batch, t);
+    if (b < 0) return;
     bool bad = false;
     const SeqSpan sp = seq_span(a.batch, b, bad);  // (reported by the launch before)
-    if (i >= sp.n) return;
-    const RowSpan rs = row_span(sp, a.window, a.causal, plan.chunk);
-    if (rs.chunks <= 1) return;
-    const int G = a.heads / a.kv_heads, row = i * G + h % G;
-    const int64_t at = ((int64_t(b) * a.kv_heads + h / G) * plan.chunks) * plan.rows + row;
+    if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
+    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
+    if (cut.chunks <= 1) return;
+    // the chunks that this token sees a key in
+    const KeyRange kr = keys_of(sp, int(t - sp.q0), a.window, a.causal);
+    const int c0 = kr.hi > kr.lo ? (kr.lo - cut.base) / plan.chunk : 0;
+    const int c1 = kr.hi > kr.lo ? (kr.hi - 1 - cut.base) / plan.chunk + 1 : 0;
     float top = -INFINITY;
-    for (int c = lane; c < rs.chunks; c += 32) top = fmaxf(top, part_ml[at + int64_t(c) * plan.rows].x);
+    for (int c = c0 + lane; c < c1; c += 32) top = fmaxf(top, part_ml[partial_at(a, c, t, h)].x);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     const bool mine = 4 * lane < a.dim;
 #pragma unroll 4
-    for (int c = warp; c < rs.chunks; c += kJoinWarps) {
-        const float2 ml = part_ml[at + int64_t(c) * plan.rows];
+    for (int c = c0 + warp; c < c1; c += kJoinWarps) {
+        const int64_t at = partial_at(a, c, t, h);
+        const float2 ml = part_ml[at];
         const float f = ml.x == top ? 1.f : fast_ex2(ml.x - top);
         l = fmaf(f, ml.y, l);
         if (mine) {
-            const float4 x = *reinterpret_cast<const float4 *>(part_o + (at + int64_t(c) * plan.rows) * a.dim + 4 * lane);
-            // (a chunk that this row sees nothing of has l = 0 and O = 0)
+            const float4 x = *reinterpret_cast<const float4 *>(part_o + at * a.dim + 4 * lane);
             o.x = fmaf(f, x.x, o.x);
             o.y = fmaf(f, x.y, o.y);
             o.z = fmaf(f, x.z, o.z);
@@ -200,16 +214,16 @@ paged_join_kernel(const PagedArgs a, const RowPlan plan, const float *__restrict
             l += sh_l[w];
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        store4(static_cast<TO *>(a.out) + (int64_t(sp.q0) + i) * a.out_token + int64_t(h) * a.out_head + 4 * lane, o.x * inv,
-               o.y * inv, o.z * inv, o.w * inv);
+        store4(static_cast<TO *>(a.out) + t * a.out_token + int64_t(h) * a.out_head + 4 * lane, o.x * inv, o.y * inv, o.z * inv,
+               o.w * inv);
     }
 }
 
 template <typename TO>
-cudaError_t launch_join(const PagedArgs &a, const RowPlan &plan, const float *part_o, const float2 *part_ml,
+cudaError_t launch_join(const PagedArgs &a, const KeyPlan &plan, const float *part_o, const float2 *part_ml,
                         const LaunchCtx &ctx) {
-    return launch_dependent(paged_join_kernel<TO>, dim3(unsigned(int64_t(a.batch.seqs) * a.batch.max_q), unsigned(a.heads)),
-                            32 * kJoinWarps, 0, ctx.stream, a, plan, part_o, part_ml);
+    return launch_dependent(paged_join_kernel<TO>, dim3(unsigned(a.batch.tokens), unsigned(a.heads)), 32 * kJoinWarps, 0,
+                            ctx.stream, a, plan, part_o, part_ml);
 }
 
 }  // namespace tq2

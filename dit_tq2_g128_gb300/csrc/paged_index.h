@@ -82,18 +82,27 @@ TQ2_HD KeyRange keys_of(const SeqSpan &sp, int i, int64_t window, bool causal) {
     return KeyRange{int(lo), int(hi)};
 }
 
-// What the new tokens of a span see together: some token sees a key only in
-// [lo, hi), every token sees all of [lo_all, hi_all); from `base` (lo, down to a
-// multiple of 64) the keys are cut into `chunks` chunks of `chunk` (0: no key).
+// What new tokens i0 .. i1 of a span see together: some of them sees a key only in
+// [lo, hi), every one of them sees all of [lo_all, hi_all) (which may be empty).
 struct RowSpan {
-    int lo, hi, lo_all, hi_all, base, chunks;
+    int lo, hi, lo_all, hi_all;
 };
-TQ2_HD RowSpan row_span(const SeqSpan &sp, int64_t window, bool causal, int chunk) {
-    if (sp.n == 0) return RowSpan{0, 0, 0, 0, 0, 0};
-    const KeyRange first = keys_of(sp, 0, window, causal), last = keys_of(sp, sp.n - 1, window, causal);
-    RowSpan r{first.lo, last.hi, last.lo, first.hi, first.lo / 64 * 64, 0};
-    if (r.hi > r.lo) r.chunks = int((int64_t(r.hi) - r.base + chunk - 1) / chunk);
-    return r;
+TQ2_HD RowSpan rows_see(const SeqSpan &sp, int i0, int i1, int64_t window, bool causal) {
+    const KeyRange first = keys_of(sp, i0, window, causal), last = keys_of(sp, i1, window, causal);
+    return RowSpan{first.lo, last.hi, last.lo, first.hi};
+}
+
+// A sequence's keys are cut into chunks of `chunk` (a multiple of 128) from `base`
+// on: its first visible key, down to a multiple of 128.
+struct KeyCut {
+    int base, chunks;  // chunks: 0 if no token sees a key
+};
+TQ2_HD KeyCut cut_keys(const SeqSpan &sp, int64_t window, bool causal, int chunk) {
+    if (sp.n == 0) return KeyCut{0, 0};
+    const RowSpan r = rows_see(sp, 0, sp.n - 1, window, causal);
+    if (r.hi <= r.lo) return KeyCut{0, 0};
+    const int base = r.lo / 128 * 128;
+    return KeyCut{base, int((int64_t(r.hi) - base + chunk - 1) / chunk)};
 }
 
 }  // namespace tq2
