@@ -11,14 +11,16 @@
 //    rings by paged tensor copies (lane = box of rows inside one page); warp 1 issues
 //    the MMAs; warps 2-3 look after V (below); warps 4-7 and 8-11 are two softmax
 //    groups, one thread per row (= tensor-memory lane).
-//  * Units: with two tiles, unit n is (block n / 2, tile n % 2); with one tile, block
-//    n.  Unit n uses scores S, weights P, sums O, and softmax group n % 2.  So one tile
-//    keeps both groups busy as well: they hold the even and the odd blocks' softmax
-//    and meet at the end.  MMA order: P V of unit n, then S of unit n + 2 over the
-//    same columns (MMAs of one thread execute in issue order).
-//  * Tensor memory: S of group w at columns 128 w, O at 256 + 128 w.  P overwrites S in
-//    the cache's type, 32 columns a 64 keys; for an f32 output the weights' remainder
-//    follows as a second term, in columns that S has left.
+//  * Lanes: with two tiles, lane w is tile w and walks every block; with one tile, lane
+//    w walks the blocks 2i + w, so one tile keeps both softmax groups busy as well (they
+//    meet at the end).  A lane walks in steps of 64 keys (half a block), each step with
+//    its own half of the lane's score columns: the softmax of step u runs while the
+//    MMAs of step u + 1 are queued, and neither waits for the other's round trip.  MMA
+//    order a step: P V of lane 0's step u, its S of step u + 2 over the same columns
+//    (MMAs of one thread execute in issue order), then lane 1's.
+//  * Tensor memory: S of lane w, step u at columns 128 w + 64 (u & 1), O of lane w at
+//    256 + 128 w.  P overwrites S in the cache's type (32 columns); for an f32 output the
+//    weights' remainder follows as a second term in the other 32.
 //  * V stays as it lies in the cache, [key][feature]: the second MMA's B operand is
 //    MN-major, with the feature halves 16 KB apart (leading offset) and 8-key groups 1 KB
 //    apart (stride offset).  No transposed copy of V exists.
@@ -38,7 +40,8 @@ namespace tq2 {
 namespace {
 
 constexpr int kRows = 128;      // rows of a tile (MMA M)
-constexpr int kBlock = 128;     // keys of a block
+constexpr int kBlock = 128;     // keys of a block (copies)
+constexpr int kStep = 64;       // keys of a step (MMAs, softmax)
 constexpr int kCtaRows = 2 * kRows;
 constexpr int kThreads = 384;
 constexpr int kMaxSplits = 64;
@@ -63,7 +66,7 @@ struct ChunkLayout {
 
 struct ChunkCtl {
     uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_ready[2], v_empty[2];
-    uint64_t s_full[2], p_full[2], o_done[2], drain;
+    uint64_t s_full[2][2], p_full[2][2], o_done[2], drain;  // [lane][step & 1]
     uint32_t tmem_base;
     int abort, poisoned;
 };
@@ -114,6 +117,17 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32])
         "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
+}
+// Waits for this thread's loads; ties the registers to the wait, so that nothing that
+// uses them moves ahead of it.
+__device__ __forceinline__ void tm_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :
+                 : "memory");
 }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -173,6 +187,46 @@ __device__ __forceinline__ bool find_rows(const BatchView &bt, int G, int slot, 
     return false;
 }
 
+// Bounded wait that also ends when another role of the CTA has given up; false (with
+// the flag set) then.  A phase that is complete already costs one poll.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint64_t wait_ns,
+                                           unsigned int *status) {
+    const uint32_t addr = smem_u32(bar);
+    auto poll = [&]() {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        return ok != 0;
+    };
+    if (poll()) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (uint32_t it = 0;; ++it) {
+        if (poll()) return true;
+        if ((it & 63u) == 63u) {
+            if (*abort_flag) return false;
+            if (globaltimer_ns() - t0 >= wait_ns) {
+                atomicOr(status, static_cast<unsigned int>(TQ2_ERR_TIMEOUT));
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
+// A value that every lane of the warp holds, told to the compiler to be so.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 template <typename T, typename TO, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a,
@@ -185,7 +239,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     uint8_t *smem = chunk_raw + pad;
     ChunkCtl *ctl = reinterpret_cast<ChunkCtl *>(smem + L::OFF_CTL);
     volatile int *abort_flag = &ctl->abort;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t sQ = base, sK = base + L::OFF_K, sV = base + L::OFF_V;
 
     // the tables, q and the cache may be written by the kernel before this one
@@ -209,8 +263,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const bool none = cut.chunks == 0 || last <= first;
     if (none && !(whole && chunk == 0)) return;
     const int block0 = first / kBlock, nb = none ? 0 : (last + kBlock - 1) / kBlock - block0;
-    const int nt = rows > kRows ? 2 : 1, units = nt * nb;
-    auto block_of = [&](int n) { return nt == 2 ? n >> 1 : n; };
+    const int nt = rows > kRows ? 2 : 1;
+    // lane w: steps 0 .. steps_of(w) - 1; step u is half u & 1 of block block_of(w, u)
+    auto steps_of = [&](int w) { return nt == 2 ? 2 * nb : 2 * ((nb + 1 - w) >> 1); };
+    auto block_of = [&](int w, int u) { return nt == 2 ? u >> 1 : (u & ~1) + w; };
 
     if (threadIdx.x == 0) {
         mbar_init(&ctl->q_ready, 2 * kRows);
@@ -220,8 +276,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             mbar_init(&ctl->v_full[s], 1);
             mbar_init(&ctl->v_ready[s], 2);
             mbar_init(&ctl->v_empty[s], 1);
-            mbar_init(&ctl->s_full[s], 1);
-            mbar_init(&ctl->p_full[s], kRows);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&ctl->s_full[s][h], 1);
+                mbar_init(&ctl->p_full[s][h], kRows / 32);
+            }
             mbar_init(&ctl->o_done[s], 1);
         }
         mbar_init(&ctl->drain, 1);
@@ -237,54 +295,52 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = ctl->tmem_base;
+    const uint32_t tmem = uint32_t(uniform(int(ctl->tmem_base)));
 
     if (warp == W_COPY) {
         // ---- copies: lane = box of a block (lane + 32 i where boxes are small)
         const int rb = plan.box_rows, boxes = kBlock / rb;
         bool ok = true;
         int ki = 0, vi = 0;  // blocks issued
-        for (int j = 0; j < nb && ok; ++j) {
-            const int s = j & 1, u = j >> 1;
+        // K of two blocks, then V of the two: with one tile, the S of a block is issued while P V of the block before it
+        // in the other lane, which frees V's slot, still waits for its weights
+        for (int i = 0; 4 * (i >> 2) < 2 * nb && ok; ++i) {
+            const int kv = (i >> 1) & 1, j = 2 * (i >> 2) + (i & 1), s = j & 1, u = j >> 1;
+            if (j >= nb) continue;
+            uint64_t *full = kv ? &ctl->v_full[s] : &ctl->k_full[s];
+            if (u > 0)
+                ok = __all_sync(0xffffffffu, wait_phase(kv ? &ctl->v_empty[s] : &ctl->k_empty[s], (u - 1) & 1, abort_flag, wait_ns, status));
+            if (!ok) break;
+            const uint32_t dst = (kv ? sV : sK) + uint32_t(s * L::TILE);
             int page[4], slot_in[4];
             unsigned mask[4];
             uint32_t count = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int box = lane + 32 * i, key = (block0 + j) * kBlock + box * rb;
+            for (int x = 0; x < 4; ++x) {
+                const int box = lane + 32 * x, key = (block0 + j) * kBlock + box * rb;
                 const bool want = box < boxes && key < last && key + rb > first;
-                mask[i] = __ballot_sync(0xffffffffu, want);
-                count += __popc(mask[i]);
-                page[i] = slot_in[i] = 0;
+                mask[x] = __ballot_sync(0xffffffffu, want);
+                count += __popc(mask[x]);
+                page[x] = slot_in[x] = 0;
                 if (want) {
                     const int entry = key / a.batch.page_size;
                     const int64_t p = page_of(a.batch, b, entry, bad);
-                    page[i] = p < 0 ? 0 : int(p);  // (recorded; any page of the cache will do)
-                    slot_in[i] = key - entry * a.batch.page_size;
+                    page[x] = p < 0 ? 0 : int(p);  // (recorded; any page of the cache will do)
+                    slot_in[x] = key - entry * a.batch.page_size;
                 }
             }
-            const uint32_t bytes = count * uint32_t(rb * 128 * L::HALVES);
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-                uint64_t *full = kv ? &ctl->v_full[s] : &ctl->k_full[s];
-                if (u > 0 && !mbar_wait_spin(kv ? &ctl->v_empty[s] : &ctl->k_empty[s], (u - 1) & 1, wait_ns, status)) ok = false;
-                ok = __all_sync(0xffffffffu, ok && *abort_flag == 0);
-                if (!ok) break;
-                if (lane == 0) mbar_expect_tx(full, bytes);
-                __syncwarp();
-                const uint32_t dst = (kv ? sV : sK) + uint32_t(s * L::TILE);
+            if (lane == 0) mbar_expect_tx(full, count * uint32_t(rb * 128 * L::HALVES));
+            __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (mask[i] >> lane & 1)
+            for (int x = 0; x < 4; ++x)
+                if (mask[x] >> lane & 1)
 #pragma unroll
-                        for (int h = 0; h < L::HALVES; ++h)
-                            tma_cache(dst + uint32_t(h * L::HALF + (lane + 32 * i) * rb * 128), kv ? &vmap : &kmap, 64 * h, g,
-                                      slot_in[i], page[i], full);
-                if (kv) vi = j + 1; else ki = j + 1;
-            }
+                    for (int h = 0; h < L::HALVES; ++h)
+                        tma_cache(dst + uint32_t(h * L::HALF + (lane + 32 * x) * rb * 128), kv ? &vmap : &kmap, 64 * h, g,
+                                  slot_in[x], page[x], full);
+            if (kv) vi = j + 1; else ki = j + 1;
         }
         report_bad(bad, status);
-        if (!ok && lane == 0) *abort_flag = 1;
-        __syncwarp();
         // every copy issued must land before the CTA exits
         if (lane == 0) {
             for (int j = max(0, ki - 2); j < ki; ++j) mbar_wait_bounded(&ctl->k_full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
@@ -292,65 +348,68 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         __syncwarp();
     } else if (warp == W_MMA) {
-        // ---- MMAs: the whole warp waits, lane 0 issues
+        // ---- MMAs, by one lane
         constexpr uint32_t type = is_half<T> ? 0u : (1u << 7) | (1u << 10);
-        const int nd = (a.dim + 15) / 16;  // 16-feature steps that hold anything
-        const uint32_t idesc_s = (1u << 4) | type | (uint32_t(kBlock >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
+        const int nb_u = uniform(nb), nt_u = uniform(nt), nd = uniform((a.dim + 15) / 16);  // nd: 16-feature steps that hold anything
+        const uint32_t idesc_s = (1u << 4) | type | (uint32_t(kStep >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
         const uint32_t idesc_o = (1u << 4) | type | (1u << 16) | (uint32_t(nd * 2) << 17) | (uint32_t(kRows >> 4) << 24);
-        const bool leader = lane == 0;
-        auto wait_all = [&](uint64_t *bar, uint32_t parity) {
-            const bool got = mbar_wait_spin(bar, parity, wait_ns, status);
-            return __all_sync(0xffffffffu, got && *abort_flag == 0);
-        };
-        auto last_of_block = [&](int n) { return nt == 1 || (n & 1); };
-        auto first_of_block = [&](int n) { return nt == 1 || !(n & 1); };
-        auto issue_s = [&](int n) -> bool {
-            const int j = block_of(n), w = n & 1;
-            if (first_of_block(n) && !wait_all(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
+        auto wait_on = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, wait_ns, status); };
+        auto steps_u = [&](int w) { return nt_u == 2 ? 2 * nb_u : 2 * ((nb_u + 1 - w) >> 1); };
+        auto block_u = [&](int w, int u) { return nt_u == 2 ? u >> 1 : (u & ~1) + w; };
+        // the last lane of a block frees it (with one tile, a block has one lane)
+        auto frees = [&](int w, int u) { return (u & 1) && (nt_u == 1 || w == 1); };
+        // uniform values and an elected lane: with values that the compiler takes for divergent, an MMA's issue took 100
+        // cycles instead of the 48 (N = 64) or 64 that it runs for; offsets never carry out of a descriptor's address field
+        const uint64_t dq[2] = {desc_k(sQ), desc_k(sQ + uint32_t(nt_u == 2 ? L::TILE : 0))};
+        const uint64_t dk[2] = {desc_k(sK), desc_k(sK + L::TILE)};
+        const uint64_t dv[2] = {desc_mn(sV, L::HALF), desc_mn(sV + L::TILE, L::HALF)};
+        auto issue_s = [&](int w, int u) -> bool {
+            const int j = block_u(w, u);
+            if (!(u & 1) && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
             tc_fence_after();
-            if (leader) {
-                const uint64_t da = desc_k(sQ + uint32_t(nt == 2 ? w * L::TILE : 0)), db = desc_k(sK + uint32_t((j & 1) * L::TILE));
-                for (int kk = 0; kk < nd; ++kk) {
-                    const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
-                    tc_mma_f16(tmem + uint32_t(w * 128), da + off, db + off, idesc_s, kk > 0);
-                }
-                tc_commit(&ctl->s_full[w]);
-                if (last_of_block(n)) tc_commit(&ctl->k_empty[j & 1]);
+            const uint64_t da = w ? dq[1] : dq[0];
+            const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t((u & 1) * (kStep * 128 >> 4));
+            const uint32_t d = tmem + uint32_t(w * 128 + (u & 1) * 64);
+#pragma unroll
+            for (int kk = 0; kk < DP / 16; ++kk) {
+                const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
+                if (kk < nd) tc_mma_f16(d, da + off, db + off, idesc_s, kk > 0);
             }
-            __syncwarp();
+            tc_commit(&ctl->s_full[w][u & 1]);
+            if (frees(w, u)) tc_commit(&ctl->k_empty[j & 1]);
             return true;
         };
-        bool ok = units == 0 || wait_all(&ctl->q_ready, 0);
-        for (int n = 0; n < 2 && n < units && ok; ++n) ok = issue_s(n);
-        for (int n = 0; n < units && ok; ++n) {
-            const int j = block_of(n), w = n & 1;
-            if (first_of_block(n) && !wait_all(&ctl->v_ready[j & 1], (j >> 1) & 1)) { ok = false; break; }
-            if (!wait_all(&ctl->p_full[w], (n >> 1) & 1)) { ok = false; break; }
-            tc_fence_after();
-            if (leader) {
-                const uint64_t db = desc_mn(sV + uint32_t((j & 1) * L::TILE), L::HALF);
-                const uint32_t d = tmem + kOCol + uint32_t(w * 128), p = tmem + uint32_t(w * 128);
+        if (elect_one()) {
+            bool ok = nb_u == 0 || wait_on(&ctl->q_ready, 0);
+            for (int u = 0; u < 2 && ok; ++u)
+                for (int w = 0; w < 2 && ok; ++w)
+                    if (u < steps_u(w)) ok = issue_s(w, u);
+            for (int u = 0; u < steps_u(0) && ok; ++u)
+                for (int w = 0; w < 2 && ok; ++w) {
+                    if (u >= steps_u(w)) continue;
+                    const int j = block_u(w, u);
+                    ok = ((u & 1) || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1)) && wait_on(&ctl->p_full[w][u & 1], (u >> 1) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t((u & 1) * (kStep * 128 >> 4));
+                    const uint32_t d = tmem + kOCol + uint32_t(w * 128), p = tmem + uint32_t(w * 128 + (u & 1) * 64);
 #pragma unroll
-                for (int kk = 0; kk < kBlock / 16; ++kk) {
-                    const uint32_t pa = p + uint32_t((kk >> 2) * 64 + (kk & 3) * 8);
-                    const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
-                    mma_ts(d, pa, bk, idesc_o, (n > 1 || kk > 0) ? 1u : 0u);
-                    if constexpr (SPLIT_P) mma_ts(d, pa + 32, bk, idesc_o, 1u);
+                    for (int kk = 0; kk < kStep / 16; ++kk) {
+                        const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
+                        mma_ts(d, p + uint32_t(kk * 8), bk, idesc_o, kk > 0 ? 1u : uint32_t(u > 0));
+                        if constexpr (SPLIT_P) mma_ts(d, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
+                    }
+                    tc_commit(&ctl->o_done[w]);
+                    if (frees(w, u)) tc_commit(&ctl->v_empty[j & 1]);
+                    if (u + 2 < steps_u(w)) ok = issue_s(w, u + 2);
                 }
-                tc_commit(&ctl->o_done[w]);
-                if (last_of_block(n)) tc_commit(&ctl->v_empty[j & 1]);
-            }
-            __syncwarp();
-            if (n + 2 < units) ok = issue_s(n + 2);
         }
-        if (!ok && leader) *abort_flag = 1;
         __syncwarp();
     } else if (warp < W_SOFT) {
         // ---- V: slots that some row of the CTA must not multiply
         const int tid = threadIdx.x - 32 * W_FIX;
         for (int j = 0; j < nb; ++j) {
-            if (!mbar_wait_spin(&ctl->v_full[j & 1], (j >> 1) & 1, wait_ns, status)) *abort_flag = 1;
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (!__all_sync(0xffffffffu, wait_phase(&ctl->v_full[j & 1], (j >> 1) & 1, abort_flag, wait_ns, status))) break;
             const int key0 = (block0 + j) * kBlock;
             if (key0 < max(first, rs.lo_all) || key0 + kBlock > min(last, rs.hi_all)) {
                 uint8_t *v = smem + L::OFF_V + (j & 1) * L::TILE;
@@ -406,96 +465,83 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint64_t scale22 = pair(scale2, scale2);
         float m = -INFINITY, l = 0.f;
         bool ok = true;
-        int done = 0;  // units of this group
-        for (int n = w; n < units; n += 2, ++done) {
-            if (!mbar_wait_spin(&ctl->s_full[w], done & 1, wait_ns, status)) *abort_flag = 1;
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+        const int done = steps_of(w);
+        for (int u = 0; u < done; ++u) {
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->s_full[w][u & 1], (u >> 1) & 1, abort_flag, wait_ns, status));
+            if (!ok) break;
             tc_fence_after();
-            const int key0 = (block0 + block_of(n)) * kBlock;
-            const int from = lo - key0, upto = hi - key0;  // this row's keys of the block: [from, upto)
-            const bool full = __all_sync(0xffffffffu, from <= 0 && upto >= kBlock);
-            float mx = -INFINITY;
+            const int key0 = (block0 + block_of(w, u)) * kBlock + (u & 1) * kStep;
+            const int from = lo - key0, upto = hi - key0;  // this row's keys of the step: [from, upto)
+            uint32_t va[32], vb[32];
+            tm_ld32(ts + uint32_t((u & 1) * 64), va);
+            tm_ld32(ts + uint32_t((u & 1) * 64 + 32), vb);
+            tm_wait_ld(va);
+            tm_wait_ld(vb);
+            if (!__all_sync(0xffffffffu, from <= 0 && upto >= kStep)) {
 #pragma unroll
-            for (int cp = 0; cp < 2; ++cp) {
-                uint32_t va[32], vb[32];
-                tm_ld32(ts + uint32_t(cp * 64), va);
-                tm_ld32(ts + uint32_t(cp * 64 + 32), vb);
-                tc_wait_ld();
-                if (full) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mx = max3(mx, __uint_as_float(va[i]), __uint_as_float(vb[i]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int x = cp * 64 + i, y = x + 32;
-                        if (x >= from && x < upto) mx = fmaxf(mx, __uint_as_float(va[i]));
-                        if (y >= from && y < upto) mx = fmaxf(mx, __uint_as_float(vb[i]));
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    if (i < from || i >= upto) va[i] = 0xff800000u;  // -inf
+                    if (i + 32 < from || i + 32 >= upto) vb[i] = 0xff800000u;
                 }
             }
-            const bool grow = mx > m && (mx - m) * scale2 > kLazy;
-            const float mu = grow ? mx : m;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx[i & 3] = max3(mx[i & 3], __uint_as_float(va[i]), __uint_as_float(vb[i]));
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+            const bool grow = top > m && (top - m) * scale2 > kLazy;
+            const float mu = grow ? top : m;
             const float alpha = grow ? fast_ex2((m - mu) * scale2) : 1.f;
             const float neg = mu == -INFINITY ? 0.f : -mu * scale2;
             const uint64_t neg2 = pair(neg, neg);
-            uint64_t sum2 = pair(0.f, 0.f);
+            uint64_t sum2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+            uint32_t hp[32], lp[SPLIT_P ? 32 : 1];
 #pragma unroll
-            for (int cp = 0; cp < 2; ++cp) {
-                uint32_t va[32], vb[32], hp[32], lp[SPLIT_P ? 32 : 1];
-                tm_ld32(ts + uint32_t(cp * 64), va);
-                tm_ld32(ts + uint32_t(cp * 64 + 32), vb);
-                tc_wait_ld();
-#pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int i = 2 * e;  // keys 64 cp + i, + i + 1
-                    float s0 = __uint_as_float(i < 32 ? va[i] : vb[i - 32]);
-                    float s1 = __uint_as_float(i < 32 ? va[i + 1] : vb[i - 31]);
-                    if (!full) {
-                        const int x = cp * 64 + i;
-                        if (x < from || x >= upto) s0 = -INFINITY;
-                        if (x + 1 < from || x + 1 >= upto) s1 = -INFINITY;
-                    }
-                    float d0, d1;
-                    unpair(fma2(pair(s0, s1), scale22, neg2), d0, d1);
-                    const float p0 = fast_ex2(d0), p1 = fast_ex2(d1);
-                    sum2 = add2(sum2, pair(p0, p1));
-                    // the weights in the cache's type (one type for both operands); an f32 output keeps the remainder
-                    hp[e] = pack16<T>(p0, p1);
-                    if constexpr (SPLIT_P) {
-                        float h0, h1;
-                        unpack16<T>(hp[e], h0, h1);
-                        lp[e] = pack16<T>(p0 - h0, p1 - h1);
-                    }
+            for (int e = 0; e < 32; ++e) {  // keys 2e, 2e + 1 of the step
+                const float s0 = __uint_as_float(e < 16 ? va[2 * e] : vb[2 * e - 32]);
+                const float s1 = __uint_as_float(e < 16 ? va[2 * e + 1] : vb[2 * e - 31]);
+                float d0, d1;
+                unpair(fma2(pair(s0, s1), scale22, neg2), d0, d1);
+                const float p0 = fast_ex2(d0), p1 = fast_ex2(d1);
+                sum2[e & 1] = add2(sum2[e & 1], pair(p0, p1));
+                // the weights in the cache's type (one type for both operands); an f32 output keeps the remainder
+                hp[e] = pack16<T>(p0, p1);
+                if constexpr (SPLIT_P) {
+                    float h0, h1;
+                    unpack16<T>(hp[e], h0, h1);
+                    lp[e] = pack16<T>(p0 - h0, p1 - h1);
                 }
-                tm_st32(ts + uint32_t(cp * 64), hp);
-                if constexpr (SPLIT_P) tm_st32(ts + uint32_t(cp * 64 + 32), lp);
             }
-            float sum0, sum1;
-            unpair(sum2, sum0, sum1);
-            if (done > 0 && __any_sync(0xffffffffu, grow)) {
-                // rescale this row of O (rows that keep m by 1) once the unit before has accumulated into it
-                if (!mbar_wait_spin(&ctl->o_done[w], (done - 1) & 1, wait_ns, status)) *abort_flag = 1;
-                if (__any_sync(0xffffffffu, *abort_flag != 0)) { ok = false; break; }
+            tm_st32(ts + uint32_t((u & 1) * 64), hp);
+            if constexpr (SPLIT_P) tm_st32(ts + uint32_t((u & 1) * 64 + 32), lp);
+            if (u > 0 && __any_sync(0xffffffffu, grow)) {
+                // rescale this row of O (rows that keep m by 1) once the step before has accumulated into it
+                ok = __all_sync(0xffffffffu, wait_phase(&ctl->o_done[w], (u - 1) & 1, abort_flag, wait_ns, status));
+                if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < (a.dim + 31) / 32; ++c) {
                     uint32_t o[32];
                     tm_ld32(to + uint32_t(c * 32), o);
-                    tc_wait_ld();
+                    tm_wait_ld(o);
 #pragma unroll
                     for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
                     tm_st32(to + uint32_t(c * 32), o);
                 }
             }
-            l = l * alpha + (sum0 + sum1);
-            m = mu;
             tm_wait_st();
             tc_fence_before();
-            mbar_arrive(&ctl->p_full[w]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->p_full[w][u & 1]);
+            float s0, s1;
+            unpair(add2(sum2[0], sum2[1]), s0, s1);
+            l = l * alpha + (s0 + s1);
+            m = mu;
         }
         if (ok && done > 0) {
-            if (!mbar_wait_spin(&ctl->o_done[w], (done - 1) & 1, wait_ns, status)) *abort_flag = 1;
-            ok = !__any_sync(0xffffffffu, *abort_flag != 0);
+            // (a lane has an even number of steps; the last one's S told that P V up to step done - 3 has ended, and a
+            // parity tells a phase only from its neighbours)
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->o_done[w], (done - 2) & 1, abort_flag, wait_ns, status) &&
+                                             wait_phase(&ctl->o_done[w], (done - 1) & 1, abort_flag, wait_ns, status));
             tc_fence_after();
         }
         // one tile: group 1's rows go to group 0 through shared memory (over Q and K, which no MMA reads any more:
@@ -514,7 +560,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     for (int c = 0; c < (a.dim + 31) / 32; ++c) {
                         uint32_t o[32];
                         tm_ld32(to + uint32_t(c * 32), o);
-                        tc_wait_ld();
+                        tm_wait_ld(o);
 #pragma unroll
                         for (int i = 0; i < 32; i += 4)
                             *reinterpret_cast<uint4 *>(&ex[r * L::MPAD + c * 32 + i]) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
@@ -522,8 +568,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
             }
             asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (w == 0 && units > 1) {
-                const float mo = exm[r], top = fmaxf(m, mo);
+            if (w == 0 && nb > 1) {
+                const float mo = exm[r], top = fmaxf(m, mo);  // (m == top holds where both are -inf)
                 scale_own = m == top ? 1.f : fast_ex2((m - top) * scale2);
                 scale_other = mo == top ? 1.f : fast_ex2((mo - top) * scale2);
                 l = l * scale_own + exl[r] * scale_other;
@@ -544,13 +590,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 uint32_t o[32];
                 if (done > 0) {
                     tm_ld32(to + uint32_t(c * 32), o);
-                    tc_wait_ld();
+                    tm_wait_ld(o);
                 }
                 if (!mine) continue;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     float x = done > 0 ? __uint_as_float(o[i]) : 0.f;
-                    if (nt == 1 && units > 1) x = x * scale_own + ex[r * L::MPAD + c * 32 + i] * scale_other;
+                    if (nt == 1 && nb > 1) x = x * scale_own + ex[r * L::MPAD + c * 32 + i] * scale_other;
                     o[i] = __float_as_uint(x);
                 }
                 if (poisoned) {  // values that are not finite, of keys that this row sees and another row does not
@@ -598,9 +644,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     }
 }
 
-// CTA slots of row tiles, at most
+// CTA slots of row tiles, at most: each sequence leaves less than one tile unfilled.
 int64_t tile_bound(int64_t group, int64_t seqs, int64_t tokens) {
-    return tokens * group / kCtaRows + std::min(seqs, tokens);
+    return (tokens * group + std::min(seqs, tokens) * (kCtaRows - 1)) / kCtaRows;
 }
 
 // The most chunks worth having: four turns of every SM.
