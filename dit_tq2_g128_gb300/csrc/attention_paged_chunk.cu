@@ -8,16 +8,18 @@
 //
 //  * A CTA owns up to 256 consecutive rows (two tiles) of one (sequence, key head)
 //    and a chunk of keys, in blocks of 128.  Warp 0 copies K and V through two-stage
-//    rings by paged tensor copies (lane = box of rows inside one page); warp 1 issues
-//    the MMAs; warps 2-3 look after V (below); warps 4-7 and 8-11 are two softmax
-//    groups, one thread per row (= tensor-memory lane).
+//    rings by paged tensor copies (lane = box of rows inside one page); warps 1 and 2
+//    issue the MMAs of lane 0 and 1 (below); warp 3 looks after V; warps 4-7 and 8-11 are
+//    the lanes' softmax groups, one thread per row (= tensor-memory lane).
 //  * Lanes: with two tiles, lane w is tile w and walks every block; with one tile, lane
 //    w walks the blocks 2i + w, so one tile keeps both softmax groups busy as well (they
 //    meet at the end).  A lane walks in steps of 64 keys (half a block), each step with
 //    its own half of the lane's score columns: the softmax of step u runs while the
-//    MMAs of step u + 1 are queued, and neither waits for the other's round trip.  MMA
-//    order a step: P V of lane 0's step u, its S of step u + 2 over the same columns
-//    (MMAs of one thread execute in issue order), then lane 1's.
+//    MMAs of step u + 1 are queued, and neither waits for the other's round trip.  A
+//    lane's MMAs, a step: P V of step u, then S of step u + 2 over the same columns
+//    (MMAs of one thread execute in issue order).  Each lane has an issuing warp of its
+//    own, so that the tensor core runs one lane's MMAs while the other's thread waits
+//    (a wait takes 80 to 200 cycles even where its phase is complete).
 //  * Tensor memory: S of lane w, step u at columns 128 w + 64 (u & 1), O of lane w at
 //    256 + 128 w.  P overwrites S in the cache's type (32 columns); for an f32 output the
 //    weights' remainder follows as a second term in the other 32.
@@ -48,7 +50,7 @@ constexpr int kMaxSplits = 64;
 constexpr int kMinBlocks = 4;   // blocks a chunk, at least
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr float kLazy = 8.f;    // log2 growth of the maximum that O is rescaled for
-constexpr int W_COPY = 0, W_MMA = 1, W_FIX = 2, W_SOFT = 4;
+constexpr int W_COPY = 0, W_MMA = 1, W_SOFT = 4;  // W_MMA + lane; warp 3 looks after V
 
 template <int DP>
 struct ChunkLayout {
@@ -272,17 +274,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         mbar_init(&ctl->q_ready, 2 * kRows);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl->k_full[s], 1);
-            mbar_init(&ctl->k_empty[s], 1);
+            mbar_init(&ctl->k_empty[s], nt);
             mbar_init(&ctl->v_full[s], 1);
-            mbar_init(&ctl->v_ready[s], 2);
-            mbar_init(&ctl->v_empty[s], 1);
+            mbar_init(&ctl->v_ready[s], 1);
+            mbar_init(&ctl->v_empty[s], nt);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&ctl->s_full[s][h], 1);
                 mbar_init(&ctl->p_full[s][h], kRows / 32);
             }
             mbar_init(&ctl->o_done[s], 1);
         }
-        mbar_init(&ctl->drain, 1);
+        mbar_init(&ctl->drain, 2);
         ctl->abort = 0;
         ctl->poisoned = 0;
         fence_mbarrier_init();
@@ -347,83 +349,80 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             for (int j = max(0, vi - 2); j < vi; ++j) mbar_wait_bounded(&ctl->v_full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
         }
         __syncwarp();
-    } else if (warp == W_MMA) {
-        // ---- MMAs, by one lane
+    } else if (warp == W_MMA || warp == W_MMA + 1) {
+        // ---- MMAs of lane w, by one thread
+        const int w = warp - W_MMA;
         constexpr uint32_t type = is_half<T> ? 0u : (1u << 7) | (1u << 10);
         const int nb_u = uniform(nb), nt_u = uniform(nt), nd = uniform((a.dim + 15) / 16);  // nd: 16-feature steps that hold anything
         const uint32_t idesc_s = (1u << 4) | type | (uint32_t(kStep >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
         const uint32_t idesc_o = (1u << 4) | type | (1u << 16) | (uint32_t(nd * 2) << 17) | (uint32_t(kRows >> 4) << 24);
         auto wait_on = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, wait_ns, status); };
-        auto steps_u = [&](int w) { return nt_u == 2 ? 2 * nb_u : 2 * ((nb_u + 1 - w) >> 1); };
-        auto block_u = [&](int w, int u) { return nt_u == 2 ? u >> 1 : (u & ~1) + w; };
-        // the last lane of a block frees it (with one tile, a block has one lane)
-        auto frees = [&](int w, int u) { return (u & 1) && (nt_u == 1 || w == 1); };
+        const int steps = nt_u == 2 ? 2 * nb_u : 2 * ((nb_u + 1 - w) >> 1);
+        auto block_u = [&](int u) { return nt_u == 2 ? u >> 1 : (u & ~1) + w; };
         // uniform values and an elected lane: with values that the compiler takes for divergent, an MMA's issue took 100
         // cycles instead of the 48 (N = 64) or 64 that it runs for; offsets never carry out of a descriptor's address field
-        const uint64_t dq[2] = {desc_k(sQ), desc_k(sQ + uint32_t(nt_u == 2 ? L::TILE : 0))};
+        const uint64_t dq = desc_k(sQ + uint32_t(nt_u == 2 ? w * L::TILE : 0));
         const uint64_t dk[2] = {desc_k(sK), desc_k(sK + L::TILE)};
         const uint64_t dv[2] = {desc_mn(sV, L::HALF), desc_mn(sV + L::TILE, L::HALF)};
-        auto issue_s = [&](int w, int u) -> bool {
-            const int j = block_u(w, u);
+        const uint32_t t_s = tmem + uint32_t(w * 128), t_o = tmem + kOCol + uint32_t(w * 128);
+        auto issue_s = [&](int u) -> bool {
+            const int j = block_u(u);
             if (!(u & 1) && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
             tc_fence_after();
-            const uint64_t da = w ? dq[1] : dq[0];
             const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t((u & 1) * (kStep * 128 >> 4));
-            const uint32_t d = tmem + uint32_t(w * 128 + (u & 1) * 64);
 #pragma unroll
             for (int kk = 0; kk < DP / 16; ++kk) {
                 const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
-                if (kk < nd) tc_mma_f16(d, da + off, db + off, idesc_s, kk > 0);
+                if (kk < nd) tc_mma_f16(t_s + uint32_t((u & 1) * 64), dq + off, db + off, idesc_s, kk > 0);
             }
             tc_commit(&ctl->s_full[w][u & 1]);
-            if (frees(w, u)) tc_commit(&ctl->k_empty[j & 1]);
+            if (u & 1) tc_commit(&ctl->k_empty[j & 1]);
             return true;
         };
         if (elect_one()) {
-            bool ok = nb_u == 0 || wait_on(&ctl->q_ready, 0);
-            for (int u = 0; u < 2 && ok; ++u)
-                for (int w = 0; w < 2 && ok; ++w)
-                    if (u < steps_u(w)) ok = issue_s(w, u);
-            for (int u = 0; u < steps_u(0) && ok; ++u)
-                for (int w = 0; w < 2 && ok; ++w) {
-                    if (u >= steps_u(w)) continue;
-                    const int j = block_u(w, u);
-                    ok = ((u & 1) || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1)) && wait_on(&ctl->p_full[w][u & 1], (u >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t((u & 1) * (kStep * 128 >> 4));
-                    const uint32_t d = tmem + kOCol + uint32_t(w * 128), p = tmem + uint32_t(w * 128 + (u & 1) * 64);
+            bool ok = steps == 0 || wait_on(&ctl->q_ready, 0);
+            for (int u = 0; u < 2 && u < steps && ok; ++u) ok = issue_s(u);
+            for (int u = 0; u < steps && ok; ++u) {
+                const int j = block_u(u);
+                ok = ((u & 1) || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1)) && wait_on(&ctl->p_full[w][u & 1], (u >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t((u & 1) * (kStep * 128 >> 4));
+                const uint32_t p = t_s + uint32_t((u & 1) * 64);
 #pragma unroll
-                    for (int kk = 0; kk < kStep / 16; ++kk) {
-                        const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
-                        mma_ts(d, p + uint32_t(kk * 8), bk, idesc_o, kk > 0 ? 1u : uint32_t(u > 0));
-                        if constexpr (SPLIT_P) mma_ts(d, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
-                    }
-                    tc_commit(&ctl->o_done[w]);
-                    if (frees(w, u)) tc_commit(&ctl->v_empty[j & 1]);
-                    if (u + 2 < steps_u(w)) ok = issue_s(w, u + 2);
+                for (int kk = 0; kk < kStep / 16; ++kk) {
+                    const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
+                    mma_ts(t_o, p + uint32_t(kk * 8), bk, idesc_o, kk > 0 ? 1u : uint32_t(u > 0));
+                    if constexpr (SPLIT_P) mma_ts(t_o, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
                 }
+                tc_commit(&ctl->o_done[w]);
+                if (u & 1) tc_commit(&ctl->v_empty[j & 1]);
+                if (u + 2 < steps) ok = issue_s(u + 2);
+            }
+            tc_commit(&ctl->drain);  // when all of this thread's MMAs have ended
         }
         __syncwarp();
     } else if (warp < W_SOFT) {
         // ---- V: slots that some row of the CTA must not multiply
-        const int tid = threadIdx.x - 32 * W_FIX;
         for (int j = 0; j < nb; ++j) {
             if (!__all_sync(0xffffffffu, wait_phase(&ctl->v_full[j & 1], (j >> 1) & 1, abort_flag, wait_ns, status))) break;
             const int key0 = (block0 + j) * kBlock;
-            if (key0 < max(first, rs.lo_all) || key0 + kBlock > min(last, rs.hi_all)) {
+            // rows [0, r0) and [r1, 128) of the block
+            const int r0 = min(kBlock, max(0, max(first, rs.lo_all) - key0)), r1 = max(r0, min(kBlock, min(last, rs.hi_all) - key0));
+            if (r0 > 0 || r1 < kBlock) {
                 uint8_t *v = smem + L::OFF_V + (j & 1) * L::TILE;
-                for (int i = tid; i < kBlock * L::HALVES * 8; i += 64) {
-                    const int r = i / (L::HALVES * 8), c = i % (L::HALVES * 8), key = key0 + r;
+                constexpr int CH = L::HALVES * 8;  // 16-byte pieces of a row
+                for (int i = lane; i < (r0 + kBlock - r1) * CH; i += 32) {
+                    const int x = i / CH, c = i % CH, r = x < r0 ? x : x - r0 + r1, key = key0 + r;
                     uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * L::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
                     if (key < first || key >= last) {
                         *p = make_uint4(0, 0, 0, 0);
-                    } else if (key < rs.lo_all || key >= rs.hi_all) {
+                    } else {
                         uint4 w = *p;
                         if (any_nonfinite<T>(w)) {
                             take_nonfinite<T>(w, [](int, float) {});
                             *p = w;
-                            ctl->poisoned = 1;  // (read behind the p_full / o_done chain that follows v_ready)
+                            ctl->poisoned = 1;  // (read behind the MMAs that follow v_ready)
                         }
                     }
                 }
@@ -633,11 +632,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     tc_fence_before();
     __syncthreads();
     if (warp == W_MMA) {
-        if (lane == 0) {
-            // every issued MMA must be complete before TMEM is released
-            tc_commit(&ctl->drain);
-            mbar_wait_bounded(&ctl->drain, 0, drain_ns(wait_ns), status);
-        }
+        // every issued MMA must be complete before TMEM is released
+        if (lane == 0) mbar_wait_bounded(&ctl->drain, 0, drain_ns(wait_ns), status);
         __syncwarp();
         tc_fence_after();
         tmem_dealloc(tmem, kTmemCols);
