@@ -143,15 +143,27 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_torch = None
+_current_raw_stream = None
+
+
 def _stream(stream):
+    global _torch, _current_raw_stream
     if stream is None:
-        try:
-            import torch
-            if torch.cuda.is_available() and torch.cuda.is_initialized():
-                return torch.cuda.current_stream().cuda_stream
-        except ImportError:  # pragma: no cover
-            pass
-        return None
+        if _torch is None:
+            try:
+                import torch
+            except ImportError:  # pragma: no cover
+                return None
+            _torch = torch
+            # the raw handle without a Stream object around it (4 us of a call otherwise)
+            _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        cuda = _torch.cuda
+        if not cuda.is_initialized():
+            return None
+        if _current_raw_stream is not None:
+            return _current_raw_stream(cuda.current_device())
+        return cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -390,28 +402,27 @@ def matmul(w_soa, x, residual=None, *, n: int, k: int, out=None, kernel: int = T
 # ---------------------------------------------------------------------------
 # Positions, key/value cache and its attention on torch tensors.
 
-_DTYPE = None
+_DTYPE = {}
 
 
 def _dtype_of(t) -> int:
-    global _DTYPE
-    if _DTYPE is None:
+    if not _DTYPE:
         import torch
-        _DTYPE = {torch.float32: TQ2_F32, torch.float16: TQ2_F16, torch.bfloat16: TQ2_BF16}
+        _DTYPE.update({torch.float32: TQ2_F32, torch.float16: TQ2_F16, torch.bfloat16: TQ2_BF16})
     try:
         return _DTYPE[t.dtype]
     except KeyError:
         raise ValueError(f"float32, float16 or bfloat16 expected, got {t.dtype}") from None
 
 
-def _heads(t, name: str, tokens: int, dim: int) -> bytes:
+def _heads(t, name: str, tokens: int, dim: int, _pack=struct.Struct("=qqqqi4x").pack) -> bytes:
     """The tq2_heads of a [tokens, heads, dim] CUDA tensor (any strides, the last one 1)."""
     shape, strides = t.shape, t.stride()
-    if not t.is_cuda or len(shape) != 3 or shape[0] != tokens or shape[2] != dim:
+    if len(shape) != 3 or shape[0] != tokens or shape[2] != dim or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor [{tokens}, heads, {dim}], got {t.device} {tuple(shape)}")
     if strides[2] != 1 and dim != 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return tq2_heads(t.data_ptr(), shape[1], strides[0], strides[1], _dtype_of(t))
+    return _pack(t.data_ptr(), shape[1], strides[0], strides[1], _DTYPE[t.dtype] if t.dtype in _DTYPE else _dtype_of(t))
 
 
 def _table(t, name: str, dtype: str, ndim: int):
@@ -438,13 +449,14 @@ class Rope:
             if a.numel() != self.pairs or (self.pairs and not 0 <= int(a.min()) <= int(a.max()) < self.axes):
                 raise ValueError(f"axis must hold {self.pairs} values from 0 to {self.axes - 1}")
             self.axis = a.to(torch.uint8).to(device)
+        self._int64 = torch.int64
         self.packed = tq2_rope(self.turns, self.axis, self.pairs, self.axes, int(self.interleaved))
 
     def positions(self, positions, tokens: int):
         """``positions`` as checked int64 [tokens, axes] (one axis: [tokens] too), or None."""
         if positions is None:
             return None
-        if (not positions.is_cuda or str(positions.dtype) != "torch.int64" or not positions.is_contiguous()
+        if (positions.dtype is not self._int64 or not positions.is_cuda or not positions.is_contiguous()
                 or positions.numel() != tokens * self.axes):
             raise ValueError(f"positions must be a contiguous CUDA int64 tensor [{tokens}, {self.axes}]")
         return positions
@@ -490,18 +502,20 @@ def rope_axes(q, k=None, v=None, *, positions, rope: Rope, out=None, inverse: bo
     """Rotate q and k [tokens, heads, dim] by their positions and copy v, into ``out`` (a sequence of as many tensors,
     of any layout and another type if wanted; default: new contiguous ones).  Returns the outputs as a tuple.
     ``inverse`` is the gradient: the gradients of the outputs go in, those of the inputs come out."""
-    import torch
     tokens, _, dim = q.shape
     ins = [t for t in (q, k, v) if t is not None]
     if out is None:
+        import torch
         out = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ins]
     if len(out) != len(ins):
         raise ValueError(f"{len(ins)} outputs expected, got {len(out)}")
-    args, o = [], iter(out)
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        args += [None, None] if t is None else [_heads(t, name, tokens, dim), _heads(next(o), name + "'s output", tokens,
-                                                                                    dim)]
-    tq2_rope_axes(*args, rope.positions(positions, tokens), rope.packed, tokens, dim, int(inverse), stream)
+    qi, qo = _heads(q, "q", tokens, dim), _heads(out[0], "q's output", tokens, dim)
+    ki = ko = vi = vo = None
+    if k is not None:
+        ki, ko = _heads(k, "k", tokens, dim), _heads(out[1], "k's output", tokens, dim)
+    if v is not None:
+        vi, vo = _heads(v, "v", tokens, dim), _heads(out[-1], "v's output", tokens, dim)
+    tq2_rope_axes(qi, qo, ki, ko, vi, vo, rope.positions(positions, tokens), rope.packed, tokens, dim, int(inverse), stream)
     return tuple(out)
 
 
@@ -510,11 +524,11 @@ def kv_append(k, v, cache: KVCache, batch: PagedBatch, *, rope: Rope = None, pos
     """Store a step's k (rotated by ``rope``) and v [tokens, heads, dim] in ``cache``; returns q rotated (in ``q_out``,
     default: a new tensor of the cache's type), or None without q.  ``positions`` [tokens, axes] default to each
     token's key index."""
-    import torch
     tokens, dim = batch.tokens, cache.dim
     qp = qo = None
     if q is not None:
         if q_out is None:
+            import torch
             q_out = torch.empty(q.shape, dtype=cache.dtype, device=q.device)
         qp, qo = _heads(q, "q", tokens, dim), _heads(q_out, "q_out", tokens, dim)
     pos = rope.positions(positions, tokens) if rope is not None else None
@@ -535,8 +549,8 @@ def attention_paged(q, cache: KVCache, batch: PagedBatch, *, out=None, scale: fl
     """Attention of the step's tokens q [tokens, heads, dim] over the paged cache, causal by default and within the
     last ``window`` keys if given; ``scale`` defaults to 1/sqrt(dim).  Returns ``out`` (default: a new tensor of q's
     type; a float32 one keeps more of the softmax's bits)."""
-    import torch
     if out is None:
+        import torch
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     tokens, dim = batch.tokens, cache.dim
     tq2_attention_paged(_heads(q, "q", tokens, dim), _heads(out, "out", tokens, dim), cache.packed, batch.packed,

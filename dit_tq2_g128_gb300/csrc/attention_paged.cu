@@ -130,7 +130,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     const int64_t k0 = cut.base + int64_t(chunk) * plan.chunk;
     const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
     const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
-    const int tile0 = int(k0) / kKeys, tiles = cut.chunks ? (last + kKeys - 1) / kKeys - tile0 : 0;
+    const int tile0 = first / kKeys, tiles = cut.chunks ? (last + kKeys - 1) / kKeys - tile0 : 0;  // (each holds a key)
     if (sp.n > 1)  // (one token's keys are seen by all its rows or by none)
         for (int i = threadIdx.x; i < L::ROWS * DP; i += kThreads) poison[i] = 0.f;
     __syncthreads();
@@ -139,48 +139,28 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         report_bad(bad, status);
         bad = false;
         // ---- producer: lane = box of a tile (and lane + 32, where boxes are single rows)
-        const int rb = plan.box_rows, boxes = kKeys / rb;
+        BoxPages boxes(a, b, tile0 * kKeys, kKeys, plan.box_rows, first, last);
         int issued = 0;
         bool ok = true;
         for (; issued < tiles; ++issued) {
             const int s = issued % kStages, u = issued / kStages;
-            int64_t page[2];
-            int slot[2];
-            unsigned mask[2];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int box = lane + 32 * i, key = (tile0 + issued) * kKeys + box * rb;
-                const bool want = box < boxes && key < last && key + rb > first;
-                mask[i] = __ballot_sync(0xffffffffu, want);
-                page[i] = -1;
-                slot[i] = 0;
-                if (want) {
-                    const int entry = key / a.batch.page_size;
-                    page[i] = page_of(a.batch, b, entry, bad);
-                    if (page[i] < 0) page[i] = 0;  // (recorded; any page of the cache will do)
-                    slot[i] = key - entry * a.batch.page_size;
-                }
-            }
+            boxes.seek(issued);
             if (u > 0 && !mbar_wait_spin(&ctl->empty[s], (u - 1) & 1, wait_ns, status)) ok = false;
             if (__any_sync(0xffffffffu, !ok || *reinterpret_cast<volatile int *>(&ctl->abort))) {
                 ok = false;
                 break;
             }
-            if (lane == 0)
-                mbar_expect_tx(&ctl->full[s], uint32_t(__popc(mask[0]) + __popc(mask[1])) * uint32_t(rb * 256 * L::HALVES));
-            __syncwarp();
             const uint32_t stage = base + uint32_t(s * 2 * L::PLANE);
+            const BoxRange br = boxes.range(issued);
+            if (lane == 0) mbar_expect_tx(&ctl->full[s], uint32_t((br.hi - br.lo) * boxes.rows * 256 * L::HALVES));
+            __syncwarp();
+            boxes.each(issued, br, bad, [&](int row, int slot, int page) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (mask[i] >> lane & 1) {
-                    const uint32_t row = uint32_t((lane + 32 * i) * rb * 128);
-#pragma unroll
-                    for (int h = 0; h < L::HALVES; ++h) {
-                        tma_cache(stage + uint32_t(h * L::HALF) + row, &kmap, 64 * h, g, slot[i], int(page[i]), &ctl->full[s]);
-                        tma_cache(stage + uint32_t(L::PLANE + h * L::HALF) + row, &vmap, 64 * h, g, slot[i], int(page[i]),
-                                  &ctl->full[s]);
-                    }
+                for (int h = 0; h < L::HALVES; ++h) {
+                    tma_cache(stage + uint32_t(h * L::HALF + row * 128), &kmap, 64 * h, g, slot, page, &ctl->full[s]);
+                    tma_cache(stage + uint32_t(L::PLANE + h * L::HALF + row * 128), &vmap, 64 * h, g, slot, page, &ctl->full[s]);
                 }
+            });
         }
         report_bad(bad, status);
         if (!ok) {
@@ -264,25 +244,25 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     __syncwarp();
                 }
                 // S^T = K Q^T, [16 keys] x [8 NT rows]
-                float sc[NT][4];
+                float sc[NT][4], sd[NT][4];  // (two sums, of the even and odd steps: half the chain of dependent MMAs)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[t][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) sc[t][e] = sd[t][e] = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < DP / 16; ++kk) {
                     uint32_t ka[4];
                     const int c = 2 * (kk & 3) + (lane >> 4);
                     ldsm4(ka, ks + uint32_t((kk >> 2) * L::HALF + arow * 128 + ((c ^ (arow & 7)) << 4)));
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) mma_16x8<T>(sc[t], ka, q[t][kk][0], q[t][kk][1]);
+                    for (int t = 0; t < NT; ++t) mma_16x8<T>(kk & 1 ? sd[t] : sc[t], ka, q[t][kk][0], q[t][kk][1]);
                 }
                 uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        sc[t][e] *= scale2;
+                        sc[t][e] = (sc[t][e] + sd[t][e]) * scale2;
                         if (!clean) {
                             const int key = key0 + (lane >> 2) + (e >> 1) * 8, c = e & 1;
                             if (key < max(lo[t][c], first) || key >= min(hi[t][c], last)) sc[t][e] = -INFINITY;

@@ -301,7 +301,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 
     if (warp == W_COPY) {
         // ---- copies: lane = box of a block (lane + 32 i where boxes are small)
-        const int rb = plan.box_rows, boxes = kBlock / rb;
+        BoxPages boxes(a, b, block0 * kBlock, kBlock, plan.box_rows, first, last);
         bool ok = true;
         int ki = 0, vi = 0;  // blocks issued
         // K of two blocks, then V of the two: with one tile, the S of a block is issued while P V of the block before it
@@ -309,37 +309,20 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         for (int i = 0; 4 * (i >> 2) < 2 * nb && ok; ++i) {
             const int kv = (i >> 1) & 1, j = 2 * (i >> 2) + (i & 1), s = j & 1, u = j >> 1;
             if (j >= nb) continue;
+            boxes.seek(j);
             uint64_t *full = kv ? &ctl->v_full[s] : &ctl->k_full[s];
             if (u > 0)
                 ok = __all_sync(0xffffffffu, wait_phase(kv ? &ctl->v_empty[s] : &ctl->k_empty[s], (u - 1) & 1, abort_flag, wait_ns, status));
             if (!ok) break;
             const uint32_t dst = (kv ? sV : sK) + uint32_t(s * L::TILE);
-            int page[4], slot_in[4];
-            unsigned mask[4];
-            uint32_t count = 0;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const int box = lane + 32 * x, key = (block0 + j) * kBlock + box * rb;
-                const bool want = box < boxes && key < last && key + rb > first;
-                mask[x] = __ballot_sync(0xffffffffu, want);
-                count += __popc(mask[x]);
-                page[x] = slot_in[x] = 0;
-                if (want) {
-                    const int entry = key / a.batch.page_size;
-                    const int64_t p = page_of(a.batch, b, entry, bad);
-                    page[x] = p < 0 ? 0 : int(p);  // (recorded; any page of the cache will do)
-                    slot_in[x] = key - entry * a.batch.page_size;
-                }
-            }
-            if (lane == 0) mbar_expect_tx(full, count * uint32_t(rb * 128 * L::HALVES));
+            const BoxRange br = boxes.range(j);
+            if (lane == 0) mbar_expect_tx(full, uint32_t((br.hi - br.lo) * boxes.rows * 128 * L::HALVES));
             __syncwarp();
+            boxes.each(j, br, bad, [&](int row, int slot_in, int page) {
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                if (mask[x] >> lane & 1)
-#pragma unroll
-                    for (int h = 0; h < L::HALVES; ++h)
-                        tma_cache(dst + uint32_t(h * L::HALF + (lane + 32 * x) * rb * 128), kv ? &vmap : &kmap, 64 * h, g,
-                                  slot_in[x], page[x], full);
+                for (int h = 0; h < L::HALVES; ++h)
+                    tma_cache(dst + uint32_t(h * L::HALF + row * 128), kv ? &vmap : &kmap, 64 * h, g, slot_in, page, full);
+            });
             if (kv) vi = j + 1; else ki = j + 1;
         }
         report_bad(bad, status);

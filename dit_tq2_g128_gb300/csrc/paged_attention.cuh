@@ -58,6 +58,50 @@ __device__ __forceinline__ void tma_cache(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// The boxes (rows inside one page) of successive tiles of `keys` keys from key0 on, as
+// one warp copies them.  The table is read 32 boxes at a time, one window ahead of
+// its use: read tile by tile, its latency paced the copies (0.9 us a 64-key tile).
+// Tiles of more than 16 boxes (boxes of one or two rows) are looked up as they come.
+struct BoxPages {
+    const PagedArgs &a;
+    const int b, key0, keys, rows, first, last, per, lane;
+    int window = -1, now = 0, next = 0;  // table entries of this lane's box in windows `window` and `window` + 1
+
+    __device__ __forceinline__ BoxPages(const PagedArgs &args, int seq, int key_from, int tile_keys, int box_rows, int first_key,
+                                        int last_key)
+        : a(args), b(seq), key0(key_from), keys(tile_keys), rows(box_rows), first(first_key), last(last_key),
+          per(tile_keys / box_rows), lane(int(threadIdx.x & 31)) {}
+    __device__ __forceinline__ int entry_of(int box) const {
+        const int key = key0 + box * rows;
+        return key < last && key + rows > first ? a.batch.page_table[int64_t(b) * a.batch.table_stride + key / a.batch.page_size] : 0;
+    }
+    // Makes the entries of a tile ready (whole warp; tiles in any order within a window, windows forward).
+    __device__ __forceinline__ void seek(int tile) {
+        if (per > 16) return;
+        const int w = tile * per >> 5;
+        if (w == window) return;
+        now = window >= 0 && w == window + 1 ? next : entry_of(32 * w + lane);
+        next = entry_of(32 * w + 32 + lane);
+        window = w;
+    }
+    __device__ __forceinline__ BoxRange range(int tile) const { return boxes_of(key0 + tile * keys, keys, rows, first, last); }
+    // copy(row in the tile, slot in the page, page) for each box of the range, spread over the lanes
+    template <typename F>
+    __device__ __forceinline__ void each(int tile, BoxRange r, bool &bad, F copy) const {
+        for (int i0 = 0; i0 < per; i0 += 32) {
+            const int i = i0 + lane, box = tile * per + i;
+            const bool mine = i >= r.lo && i < r.hi;
+            int page = per > 16 ? (mine ? entry_of(box) : 0) : __shfl_sync(0xffffffffu, now, box & 31);
+            if (!mine) continue;
+            if (page < 0 || int64_t(page) >= a.batch.pages) {  // (recorded; any page of the cache will do)
+                bad = true;
+                page = 0;
+            }
+            copy(i * rows, (key0 + box * rows) % a.batch.page_size, page);
+        }
+    }
+};
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack16(float a, float b) {
     uint32_t r;

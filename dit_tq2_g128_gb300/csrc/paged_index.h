@@ -105,4 +105,17 @@ TQ2_HD KeyCut cut_keys(const SeqSpan &sp, int64_t window, bool causal, int chunk
     return KeyCut{base, int((int64_t(r.hi) - base + chunk - 1) / chunk)};
 }
 
+// Boxes (rows inside one page) of a tile of keys [from, from + keys) that hold a key
+// of [first, last): box i is keys from + i * rows on, i in [lo, hi).
+struct BoxRange {
+    int lo, hi;
+};
+TQ2_HD BoxRange boxes_of(int from, int keys, int rows, int first, int last) {
+    const int per = keys / rows;
+    int lo = first > from ? (first - from) / rows : 0, hi = last - from < keys ? (last - from + rows - 1) / rows : per;
+    if (lo > per) lo = per;
+    if (hi < lo || last <= first) hi = lo;
+    return BoxRange{lo, hi};
+}
+
 }  // namespace tq2

@@ -136,6 +136,10 @@ void keys(int n, int kv, int i, long long window, int causal, int *out) {
     const KeyRange r = keys_of(SeqSpan{0, n, kv}, i, window, causal);
     out[0] = r.lo, out[1] = r.hi;
 }
+void boxes(int from, int keys, int rows, int first, int last, int *out) {
+    const BoxRange r = boxes_of(from, keys, rows, first, last);
+    out[0] = r.lo, out[1] = r.hi;
+}
 }
 """)
     lib = d / "probe.so"
@@ -200,6 +204,22 @@ def test_visible_keys(index):
                     pos = kv - n + i
                     want = [j for j in range(kv) if (j <= pos or not causal) and (j > pos - window or not window)]
                     assert list(range(out[0], out[1])) == want
+
+
+def test_boxes_of_a_tile(index):
+    """The boxes that are counted are those that hold a key, in tiles that hold none too."""
+    rng = np.random.default_rng(5)
+    for _ in range(4000):
+        keys = int(rng.choice([64, 128]))
+        rows = 1 << int(rng.integers(0, 7 if keys == 64 else 8))
+        first = int(rng.integers(0, 700))
+        last = first + int(rng.integers(0, 500))
+        start = int(rng.integers(0, 10)) * keys
+        out = (ctypes.c_int * 2)()
+        index.boxes(start, keys, rows, first, last, out)
+        want = [i for i in range(keys // rows)
+                if any(first <= k < last for k in range(start + i * rows, start + (i + 1) * rows))]
+        assert list(range(out[0], out[1])) == want
 
 
 # ---------------------------------------------------------------------------
