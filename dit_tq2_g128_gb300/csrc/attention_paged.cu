@@ -145,11 +145,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         for (; issued < tiles; ++issued) {
             const int s = issued % kStages, u = issued / kStages;
             boxes.seek(issued);
-            if (u > 0 && !mbar_wait_spin(&ctl->empty[s], (u - 1) & 1, wait_ns, status)) ok = false;
-            if (__any_sync(0xffffffffu, !ok || *reinterpret_cast<volatile int *>(&ctl->abort))) {
-                ok = false;
-                break;
-            }
+            if (u > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->empty[s], (u - 1) & 1, &ctl->abort, wait_ns, status));
+            if (!ok) break;
             const uint32_t stage = base + uint32_t(s * 2 * L::PLANE);
             const BoxRange br = boxes.range(issued);
             if (lane == 0) mbar_expect_tx(&ctl->full[s], uint32_t((br.hi - br.lo) * boxes.rows * 256 * L::HALVES));
@@ -165,7 +162,6 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         report_bad(bad, status);
         if (!ok) {
             if (lane == 0) {  // what was issued lands before the CTA ends
-                *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
                 for (int t = max(0, issued - kStages); t < issued; ++t)
                     mbar_wait_bounded(&ctl->full[t % kStages], (t / kStages) & 1, drain_ns(wait_ns), status);
             }
@@ -205,14 +201,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         const float scale2 = a.scale * 1.4426950408889634f;
         const int arow = lane & 15, brow = (lane & 7) + ((lane >> 4) & 1) * 8;
-        bool ok = true;
         for (int it = 0; it < tiles; ++it) {
             const int s = it % kStages;
-            if (!mbar_wait_spin(&ctl->full[s], (it / kStages) & 1, wait_ns, status)) *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
-            if (__any_sync(0xffffffffu, *reinterpret_cast<volatile int *>(&ctl->abort) != 0)) {
-                ok = false;
-                break;
-            }
+            if (!__all_sync(0xffffffffu, wait_phase(&ctl->full[s], (it / kStages) & 1, &ctl->abort, wait_ns, status))) break;
             const int key0 = (tile0 + it) * kKeys + warp * 16;
             const uint32_t ks = base + uint32_t(s * 2 * L::PLANE + warp * 16 * 128), vs = ks + L::PLANE;
             if (key0 < last && key0 + 16 > first) {
@@ -328,9 +319,6 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&ctl->empty[s]);
-        }
-        if (!ok) {
-            if (lane == 0) *reinterpret_cast<volatile int *>(&ctl->abort) = 1;
         }
         // m and l of this warp's keys
         float *wm = reinterpret_cast<float *>(smem + L::OFF_ML), *wl = wm + kConsumers * L::ROWS;

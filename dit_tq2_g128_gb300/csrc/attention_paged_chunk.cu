@@ -189,37 +189,6 @@ __device__ __forceinline__ bool find_rows(const BatchView &bt, int G, int slot, 
     return false;
 }
 
-// Bounded wait that also ends when another role of the CTA has given up; false (with
-// the flag set) then.  A phase that is complete already costs one poll.
-__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint64_t wait_ns,
-                                           unsigned int *status) {
-    const uint32_t addr = smem_u32(bar);
-    auto poll = [&]() {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(addr), "r"(parity)
-            : "memory");
-        return ok != 0;
-    };
-    if (poll()) return true;
-    const uint64_t t0 = globaltimer_ns();
-    for (uint32_t it = 0;; ++it) {
-        if (poll()) return true;
-        if ((it & 63u) == 63u) {
-            if (*abort_flag) return false;
-            if (globaltimer_ns() - t0 >= wait_ns) {
-                atomicOr(status, static_cast<unsigned int>(TQ2_ERR_TIMEOUT));
-                *abort_flag = 1;
-                return false;
-            }
-        }
-    }
-}
-
 // A value that every lane of the warp holds, told to the compiler to be so.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 

@@ -48,6 +48,36 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
+// Bounded wait that also ends when another role of the CTA has given up; false (with
+// the flag set) then.  The timer is read from the 64th poll on only: its read costs
+// more than a usual wait.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint64_t wait_ns,
+                                           unsigned int *status) {
+    const uint32_t addr = smem_u32(bar);
+    uint64_t t0 = 0;
+    for (uint32_t it = 0;; ++it) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if ((it & 63u) == 63u) {
+            if (*abort_flag) return false;
+            const uint64_t t = globaltimer_ns();
+            if (t0 == 0) t0 = t;
+            if (t - t0 >= wait_ns) {
+                atomicOr(status, static_cast<unsigned int>(TQ2_ERR_TIMEOUT));
+                *abort_flag = 1;
+                return false;
+            }
+        }
+    }
+}
+
 // rows of one page: feature x (a multiple of 64), head, slot, page
 __device__ __forceinline__ void tma_cache(uint32_t dst, const CUtensorMap *map, int x, int head, int slot, int page,
                                           uint64_t *bar) {
