@@ -105,7 +105,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     uint8_t *smem = rows_raw + pad;
     RowCtl *ctl = reinterpret_cast<RowCtl *>(smem + L::OFF_CTL);
     float *poison = reinterpret_cast<float *>(smem + L::OFF_POISON);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const int g = blockIdx.y, b = int(blockIdx.x / unsigned(plan.chunks)), chunk = int(blockIdx.x % unsigned(plan.chunks));
     const int G = a.heads / a.kv_heads;
 
@@ -138,11 +138,12 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     if (warp == kConsumers) {
         report_bad(bad, status);
         bad = false;
-        // ---- producer: lane = box of a tile (and lane + 32, where boxes are single rows)
+        // ---- producer
         BoxPages boxes(a, b, tile0 * kKeys, kKeys, plan.box_rows, first, last);
+        const int tiles_u = uniform(tiles);
         int issued = 0;
         bool ok = true;
-        for (; issued < tiles; ++issued) {
+        for (; issued < tiles_u; ++issued) {
             const int s = issued % kStages, u = issued / kStages;
             boxes.seek(issued);
             if (u > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->empty[s], (u - 1) & 1, &ctl->abort, wait_ns, status));

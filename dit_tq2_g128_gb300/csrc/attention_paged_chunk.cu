@@ -7,10 +7,10 @@
 // for all G heads at once.
 //
 //  * A CTA owns up to 256 consecutive rows (two tiles) of one (sequence, key head)
-//    and a chunk of keys, in blocks of 128.  Warp 0 copies K and V through two-stage
-//    rings by paged tensor copies (lane = box of rows inside one page); warps 1 and 2
-//    issue the MMAs of lane 0 and 1 (below); warp 3 looks after V; warps 4-7 and 8-11 are
-//    the lanes' softmax groups, one thread per row (= tensor-memory lane).
+//    and a chunk of keys, in blocks of 128.  Warps 0 and 12 copy K and V through
+//    two-stage rings by paged tensor copies (boxes of rows inside one page); warps 1 and
+//    2 issue the MMAs of lane 0 and 1 (below); warp 3 looks after V; warps 4-7 and 8-11
+//    are the lanes' softmax groups, one thread per row (= tensor-memory lane).
 //  * Lanes: with two tiles, lane w is tile w and walks every block; with one tile, lane
 //    w walks the blocks 2i + w, so one tile keeps both softmax groups busy as well (they
 //    meet at the end).  A lane walks in steps of 64 keys (half a block), each step with
@@ -45,12 +45,12 @@ constexpr int kRows = 128;      // rows of a tile (MMA M)
 constexpr int kBlock = 128;     // keys of a block (copies)
 constexpr int kStep = 64;       // keys of a step (MMAs, softmax)
 constexpr int kCtaRows = 2 * kRows;
-constexpr int kThreads = 384;
+constexpr int kThreads = 416;
 constexpr int kMaxSplits = 64;
 constexpr int kMinBlocks = 4;   // blocks a chunk, at least
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr float kLazy = 8.f;    // log2 growth of the maximum that O is rescaled for
-constexpr int W_COPY = 0, W_MMA = 1, W_SOFT = 4;  // W_MMA + lane; warp 3 looks after V
+constexpr int W_K = 0, W_MMA = 1, W_SOFT = 4, W_V = 12;  // W_MMA + lane; warp 3 looks after V
 
 template <int DP>
 struct ChunkLayout {
@@ -189,15 +189,6 @@ __device__ __forceinline__ bool find_rows(const BatchView &bt, int G, int slot, 
     return false;
 }
 
-// A value that every lane of the warp holds, told to the compiler to be so.
-__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-__device__ __forceinline__ bool elect_one() {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
-    return ok != 0;
-}
-
 template <typename T, typename TO, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a,
@@ -268,38 +259,33 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(ctl->tmem_base)));
 
-    if (warp == W_COPY) {
-        // ---- copies: lane = box of a block (lane + 32 i where boxes are small)
+    if (warp == W_K || warp == W_V) {
+        // ---- copies of one plane (a warp each: K's slots and V's are freed at different times)
+        const bool v = warp == W_V;
+        const CUtensorMap *map = v ? &vmap : &kmap;
+        uint64_t *const full = v ? ctl->v_full : ctl->k_full, *const empty = v ? ctl->v_empty : ctl->k_empty;
+        const int nb_u = uniform(nb), g_u = uniform(g);
         BoxPages boxes(a, b, block0 * kBlock, kBlock, plan.box_rows, first, last);
-        bool ok = true;
-        int ki = 0, vi = 0;  // blocks issued
-        // K of two blocks, then V of the two: with one tile, the S of a block is issued while P V of the block before it
-        // in the other lane, which frees V's slot, still waits for its weights
-        for (int i = 0; 4 * (i >> 2) < 2 * nb && ok; ++i) {
-            const int kv = (i >> 1) & 1, j = 2 * (i >> 2) + (i & 1), s = j & 1, u = j >> 1;
-            if (j >= nb) continue;
-            boxes.seek(j);
-            uint64_t *full = kv ? &ctl->v_full[s] : &ctl->k_full[s];
-            if (u > 0)
-                ok = __all_sync(0xffffffffu, wait_phase(kv ? &ctl->v_empty[s] : &ctl->k_empty[s], (u - 1) & 1, abort_flag, wait_ns, status));
-            if (!ok) break;
-            const uint32_t dst = (kv ? sV : sK) + uint32_t(s * L::TILE);
-            const BoxRange br = boxes.range(j);
-            if (lane == 0) mbar_expect_tx(full, uint32_t((br.hi - br.lo) * boxes.rows * 128 * L::HALVES));
+        int issued = 0;
+        for (; issued < nb_u; ++issued) {
+            const int s = issued & 1, u = issued >> 1;
+            boxes.seek(issued);
+            if (u > 0 && !__all_sync(0xffffffffu, wait_phase(&empty[s], (u - 1) & 1, abort_flag, wait_ns, status))) break;
+            const uint32_t dst = (v ? sV : sK) + uint32_t(s * L::TILE);
+            const BoxRange br = boxes.range(issued);
+            if (lane == 0) mbar_expect_tx(&full[s], uint32_t((br.hi - br.lo) * boxes.rows * 128 * L::HALVES));
             __syncwarp();
-            boxes.each(j, br, bad, [&](int row, int slot_in, int page) {
+            boxes.each(issued, br, bad, [&](int row, int slot_in, int page) {
 #pragma unroll
                 for (int h = 0; h < L::HALVES; ++h)
-                    tma_cache(dst + uint32_t(h * L::HALF + row * 128), kv ? &vmap : &kmap, 64 * h, g, slot_in, page, full);
+                    tma_cache(dst + uint32_t(h * L::HALF + row * 128), map, 64 * h, g_u, slot_in, page, &full[s]);
             });
-            if (kv) vi = j + 1; else ki = j + 1;
         }
         report_bad(bad, status);
         // every copy issued must land before the CTA exits
-        if (lane == 0) {
-            for (int j = max(0, ki - 2); j < ki; ++j) mbar_wait_bounded(&ctl->k_full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
-            for (int j = max(0, vi - 2); j < vi; ++j) mbar_wait_bounded(&ctl->v_full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
-        }
+        if (lane == 0)
+            for (int j = max(0, issued - 2); j < issued; ++j)
+                mbar_wait_bounded(&full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
         __syncwarp();
     } else if (warp == W_MMA || warp == W_MMA + 1) {
         // ---- MMAs of lane w, by one thread
@@ -354,7 +340,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             tc_commit(&ctl->drain);  // when all of this thread's MMAs have ended
         }
         __syncwarp();
-    } else if (warp < W_SOFT) {
+    } else if (warp == W_SOFT - 1) {
         // ---- V: slots that some row of the CTA must not multiply
         for (int j = 0; j < nb; ++j) {
             if (!__all_sync(0xffffffffu, wait_phase(&ctl->v_full[j & 1], (j >> 1) & 1, abort_flag, wait_ns, status))) break;

@@ -48,6 +48,15 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t *bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
+// A value that every lane of the warp holds, told to the compiler to be so.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+
 // Bounded wait that also ends when another role of the CTA has given up; false (with
 // the flag set) then.  The timer is read from the 64th poll on only: its read costs
 // more than a usual wait.
@@ -88,6 +97,8 @@ __device__ __forceinline__ void tma_cache(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
+// One lane issues the copies, from values that the compiler knows to be uniform: spread
+// over the lanes, a copy's issue took 50 cycles more.
 // The boxes (rows inside one page) of successive tiles of `keys` keys from key0 on, as
 // one warp copies them.  The table is read 32 boxes at a time, one window ahead of
 // its use: read tile by tile, its latency paced the copies (0.9 us a 64-key tile).
@@ -99,8 +110,8 @@ struct BoxPages {
 
     __device__ __forceinline__ BoxPages(const PagedArgs &args, int seq, int key_from, int tile_keys, int box_rows, int first_key,
                                         int last_key)
-        : a(args), b(seq), key0(key_from), keys(tile_keys), rows(box_rows), first(first_key), last(last_key),
-          per(tile_keys / box_rows), lane(int(threadIdx.x & 31)) {}
+        : a(args), b(seq), key0(uniform(key_from)), keys(tile_keys), rows(box_rows), first(uniform(first_key)),
+          last(uniform(last_key)), per(tile_keys / box_rows), lane(int(threadIdx.x & 31)) {}
     __device__ __forceinline__ int entry_of(int box) const {
         const int key = key0 + box * rows;
         return key < last && key + rows > first ? a.batch.page_table[int64_t(b) * a.batch.table_stride + key / a.batch.page_size] : 0;
@@ -115,20 +126,23 @@ struct BoxPages {
         window = w;
     }
     __device__ __forceinline__ BoxRange range(int tile) const { return boxes_of(key0 + tile * keys, keys, rows, first, last); }
-    // copy(row in the tile, slot in the page, page) for each box of the range, spread over the lanes
+    // copy(row in the tile, slot in the page, page) for each box of the range, by one lane
     template <typename F>
     __device__ __forceinline__ void each(int tile, BoxRange r, bool &bad, F copy) const {
-        for (int i0 = 0; i0 < per; i0 += 32) {
-            const int i = i0 + lane, box = tile * per + i;
-            const bool mine = i >= r.lo && i < r.hi;
-            int page = per > 16 ? (mine ? entry_of(box) : 0) : __shfl_sync(0xffffffffu, now, box & 31);
-            if (!mine) continue;
+        const bool one = elect_one();
+        int slot = (key0 + (tile * per + r.lo) * rows) % a.batch.page_size;
+        for (int i = r.lo; i < r.hi; ++i) {
+            const int box = tile * per + i;
+            int page = per > 16 ? uniform(entry_of(box)) : __shfl_sync(0xffffffffu, now, box & 31);
             if (page < 0 || int64_t(page) >= a.batch.pages) {  // (recorded; any page of the cache will do)
                 bad = true;
                 page = 0;
             }
-            copy(i * rows, (key0 + box * rows) % a.batch.page_size, page);
+            if (one) copy(i * rows, slot, page);
+            slot += rows;
+            if (slot >= a.batch.page_size) slot = 0;  // (a box ends with its page or before it)
         }
+        __syncwarp();
     }
 };
 
