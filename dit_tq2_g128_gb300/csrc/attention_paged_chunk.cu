@@ -33,6 +33,7 @@
 // and exits.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 
@@ -204,40 +205,15 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     const uint32_t sQ = base, sK = base + L::OFF_K, sV = base + L::OFF_V;
 
-    // the tables, q and the cache may be written by the kernel before this one
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // slot = tile * kv_heads * chunks + head * chunks + chunk: a tile's heads and chunks run together
-    const unsigned per = unsigned(a.kv_heads) * unsigned(plan.chunks);
-    const int slot = int(blockIdx.x / per), g = int(blockIdx.x % per) / plan.chunks, chunk = int(blockIdx.x % per) % plan.chunks;
-    const int G = a.heads / a.kv_heads;
-    int b = 0, row0 = 0;
-    if (!find_rows(a.batch, G, slot, b, row0, status)) return;
-    bool bad = false;
-    const SeqSpan sp = seq_span(a.batch, b, bad);
-    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
-    const int rows = min(kCtaRows, int(int64_t(sp.n) * G - row0));
-    const RowSpan rs = rows_see(sp, row0 / G, (row0 + rows - 1) / G, a.window, a.causal);
-    const bool whole = cut.chunks <= 1;
-    const int64_t k0 = cut.base + int64_t(chunk) * plan.chunk;
-    const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
-    const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
-    const bool none = cut.chunks == 0 || last <= first;
-    if (none && !(whole && chunk == 0)) return;
-    const int block0 = first / kBlock, nb = none ? 0 : (last + kBlock - 1) / kBlock - block0;
-    const int nt = rows > kRows ? 2 : 1;
-    // lane w: steps 0 .. steps_of(w) - 1; step u is half u & 1 of block block_of(w, u)
-    auto steps_of = [&](int w) { return nt == 2 ? 2 * nb : 2 * ((nb + 1 - w) >> 1); };
-    auto block_of = [&](int w, int u) { return nt == 2 ? u >> 1 : (u & ~1) + w; };
-
+    // set-up that touches no memory of the launch before: barriers and tensor memory
     if (threadIdx.x == 0) {
         mbar_init(&ctl->q_ready, 2 * kRows);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl->k_full[s], 1);
-            mbar_init(&ctl->k_empty[s], nt);
+            mbar_init(&ctl->k_empty[s], 2);  // both lanes (one tile: its block's lane, twice)
             mbar_init(&ctl->v_full[s], 1);
             mbar_init(&ctl->v_ready[s], 1);
-            mbar_init(&ctl->v_empty[s], nt);
+            mbar_init(&ctl->v_empty[s], 2);
             for (int h = 0; h < 2; ++h) {
                 mbar_init(&ctl->s_full[s][h], 1);
                 mbar_init(&ctl->p_full[s][h], kRows / 32);
@@ -254,10 +230,40 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         tmem_alloc(&ctl->tmem_base, kTmemCols);
         tmem_relinquish();
     }
+    // the tables, q and the cache may be written by the kernel before this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // slot = tile * kv_heads * chunks + head * chunks + chunk: a tile's heads and chunks run together
+    const unsigned per = unsigned(a.kv_heads) * unsigned(plan.chunks);
+    const int slot = int(blockIdx.x / per), g = int(blockIdx.x % per) / plan.chunks, chunk = int(blockIdx.x % per) % plan.chunks;
+    const int G = a.heads / a.kv_heads;
+    int b = 0, row0 = 0;
+    bool bad = false;
+    const bool found = find_rows(a.batch, G, slot, b, row0, status);
+    const SeqSpan sp = found ? seq_span(a.batch, b, bad) : SeqSpan{0, 0, 0};
+    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
+    const int rows = min(kCtaRows, int(int64_t(sp.n) * G - row0));
+    const RowSpan rs = rows > 0 ? rows_see(sp, row0 / G, (row0 + rows - 1) / G, a.window, a.causal) : RowSpan{0, 0, 0, 0};
+    const bool whole = cut.chunks <= 1;
+    const int64_t k0 = cut.base + int64_t(chunk) * plan.chunk;
+    const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
+    const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
+    const bool none = cut.chunks == 0 || last <= first;
+    const bool idle = !found || (none && !(whole && chunk == 0));  // (CTA-uniform: nothing to write)
+    const int block0 = first / kBlock, nb = none || idle ? 0 : (last + kBlock - 1) / kBlock - block0;
+    const int nt = rows > kRows ? 2 : 1;
+    // lane w: steps 0 .. steps_of(w) - 1; step u is half u & 1 of block block_of(w, u)
+    auto steps_of = [&](int w) { return nt == 2 ? 2 * nb : 2 * ((nb + 1 - w) >> 1); };
+    auto block_of = [&](int w, int u) { return nt == 2 ? u >> 1 : (u & ~1) + w; };
+
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(ctl->tmem_base)));
+    if (idle) {
+        if (warp == W_MMA) tmem_dealloc(tmem, kTmemCols);
+        return;
+    }
 
     if (warp == W_K || warp == W_V) {
         // ---- copies of one plane (a warp each: K's slots and V's are freed at different times)
@@ -314,7 +320,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (kk < nd) tc_mma_f16(t_s + uint32_t((u & 1) * 64), dq + off, db + off, idesc_s, kk > 0);
             }
             tc_commit(&ctl->s_full[w][u & 1]);
-            if (u & 1) tc_commit(&ctl->k_empty[j & 1]);
+            if (u & 1) {
+                tc_commit(&ctl->k_empty[j & 1]);
+                if (nt_u == 1) tc_commit(&ctl->k_empty[j & 1]);
+            }
             return true;
         };
         if (elect_one()) {
@@ -334,7 +343,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if constexpr (SPLIT_P) mma_ts(t_o, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
                 }
                 tc_commit(&ctl->o_done[w]);
-                if (u & 1) tc_commit(&ctl->v_empty[j & 1]);
+                if (u & 1) {
+                    tc_commit(&ctl->v_empty[j & 1]);
+                    if (nt_u == 1) tc_commit(&ctl->v_empty[j & 1]);
+                }
                 if (u + 2 < steps) ok = issue_s(u + 2);
             }
             tc_commit(&ctl->drain);  // when all of this thread's MMAs have ended
@@ -375,18 +387,23 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         {
             const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's sign
             const T *q = static_cast<const T *>(a.q) + int64_t(sp.q0) * a.q_token;
-            for (int i = threadIdx.x - 32 * W_SOFT; i < nt * kRows * (DP / 8); i += 2 * kRows) {
-                const int r = i / (DP / 8), c = i % (DP / 8), row = row0 + r;
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (r < rows && 8 * c < a.dim) {
-                    x = *reinterpret_cast<const uint4 *>(q + int64_t(row / G) * a.q_token + int64_t(g * G + row % G) * a.q_head + 8 * c);
-                    x.x ^= flip;
-                    x.y ^= flip;
-                    x.z ^= flip;
-                    x.w ^= flip;
+            constexpr int CH = DP / 8, IT = CH / 2;  // 16-byte pieces of a row; rows of a tile a thread brings
+            const int tid = threadIdx.x - 32 * W_SOFT, c = tid % CH;
+            for (int t = 0; t < nt; ++t) {
+                uint4 x[IT];  // all of a tile's loads in flight
+#pragma unroll
+                for (int k = 0; k < IT; ++k) {
+                    const int r = t * kRows + tid / CH + k * (2 * kRows / CH), row = row0 + r;
+                    x[k] = make_uint4(0, 0, 0, 0);
+                    if (r < rows && 8 * c < a.dim)
+                        x[k] = *reinterpret_cast<const uint4 *>(q + int64_t(row / G) * a.q_token + int64_t(g * G + row % G) * a.q_head + 8 * c);
                 }
-                *reinterpret_cast<uint4 *>(smem + (r >> 7) * L::TILE + (c >> 3) * L::HALF + (r & 127) * 128 +
-                                           (((c & 7) ^ (r & 7)) << 4)) = x;
+#pragma unroll
+                for (int k = 0; k < IT; ++k) {
+                    const int r = tid / CH + k * (2 * kRows / CH);
+                    *reinterpret_cast<uint4 *>(smem + t * L::TILE + (c >> 3) * L::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
+                }
             }
             fence_proxy_async_smem();
             mbar_arrive(&ctl->q_ready);
@@ -513,57 +530,89 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 m = top;
             }
         }
+        auto to_cols = [&](int c) { return to + uint32_t(c * 32); };
+        // values that are not finite, of keys that this row sees and another row of the CTA does not (columns 32 c ..)
+        auto add_hidden = [&](int c, uint32_t (&o)[32]) {
+            for (int key = lo; key < hi; ++key) {
+                if (key >= rs.lo_all && key < rs.hi_all) {
+                    key = rs.hi_all - 1;
+                    continue;
+                }
+                const int entry = key / a.batch.page_size;
+                bool ignore = false;
+                const int64_t p = page_of(a.batch, b, entry, ignore);
+                const T *v = static_cast<const T *>(a.v) + (p < 0 ? 0 : p) * a.page_stride +
+                             int64_t(key - entry * a.batch.page_size) * a.slot_stride + int64_t(g) * a.head_stride + c * 32;
+#pragma unroll 1
+                for (int i = 0; i < 32 && c * 32 + i < a.dim; ++i) {
+                    const float x = float(v[i]);
+                    if (!isfinite(x))
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)  // (o stays in registers)
+                            if (e == i) o[e] = __float_as_uint(__uint_as_float(o[e]) + x);
+                }
+            }
+        };
         if (ok && (nt == 2 || w == 0)) {
             const int64_t t = int64_t(sp.q0) + (row0 + row) / G;
             const int h = g * G + (row0 + row) % G;
             const bool mine = row < rows;
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // no key: zeros
-            const int64_t at = whole ? 0 : partial_at(a, chunk, t, h);
-            TO *out = static_cast<TO *>(a.out) + t * a.out_token + int64_t(h) * a.out_head;
-            if (!whole && mine) part_ml[at] = make_float2(m == -INFINITY ? m : m * scale2, l);
+            if (!whole && mine) part_ml[partial_at(a, chunk, t, h)] = make_float2(m == -INFINITY ? m : m * scale2, l);
             const bool poisoned = *reinterpret_cast<volatile int *>(&ctl->poisoned) != 0;
-#pragma unroll 1
-            for (int c = 0; c < (a.dim + 31) / 32; ++c) {
-                uint32_t o[32];
-                if (done > 0) {
-                    tm_ld32(to + uint32_t(c * 32), o);
-                    tm_wait_ld(o);
-                }
-                if (!mine) continue;
+            // Rows leave through shared memory, 128 bytes of each at a time, so that eight lanes store one row's piece.
+            // A warp's 4 KB lie over the lane's Q tile, which its last MMA has left; with one tile (whose Q the other
+            // group's exchange lies over) over V, which nothing reads any more.
+            uint8_t *stage = smem + (nt == 2 ? w * L::TILE : L::OFF_V) + (warp & 3) * 4096;
+            auto put = [&](bool partial, auto *to, int64_t t_stride, int64_t h_stride) {
+                using E = typename std::remove_pointer<decltype(to)>::type;
+                constexpr int W = 128 / sizeof(E);  // columns of a piece: 32 in f32, 64 in 16 bits
+                for (int c0 = 0; c0 < a.dim; c0 += W) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float x = done > 0 ? __uint_as_float(o[i]) : 0.f;
-                    if (nt == 1 && nb > 1) x = x * scale_own + ex[r * L::MPAD + c * 32 + i] * scale_other;
-                    o[i] = __float_as_uint(x);
-                }
-                if (poisoned) {  // values that are not finite, of keys that this row sees and another row does not
-                    for (int key = lo; key < hi; ++key) {
-                        if (key >= rs.lo_all && key < rs.hi_all) {
-                            key = rs.hi_all - 1;
-                            continue;
+                    for (int part = 0; part < W / 32; ++part) {
+                        const int c = c0 / 32 + part;
+                        uint32_t o[32];
+                        if (nb > 0) {
+                            tm_ld32(to_cols(c), o);
+                            tm_wait_ld(o);
                         }
-                        const int entry = key / a.batch.page_size;
-                        bool ignore = false;
-                        const int64_t p = page_of(a.batch, b, entry, ignore);
-                        const T *v = static_cast<const T *>(a.v) + (p < 0 ? 0 : p) * a.page_stride +
-                                     int64_t(key - entry * a.batch.page_size) * a.slot_stride + int64_t(g) * a.head_stride + c * 32;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c * 32 + i < a.dim) {
-                                const float x = float(v[i]);
-                                if (!isfinite(x)) o[i] = __float_as_uint(__uint_as_float(o[i]) + x);
-                            }
+                        for (int i = 0; i < 32; ++i) {
+                            float x = nb > 0 ? __uint_as_float(o[i]) : 0.f;
+                            if (nt == 1 && nb > 1) x = x * scale_own + ex[r * L::MPAD + c * 32 + i] * scale_other;
+                            o[i] = __float_as_uint(x);
+                        }
+                        if (poisoned && mine) add_hidden(c, o);
+#pragma unroll
+                        for (int i = 0; i < 32; i += 16 / int(sizeof(E))) {
+                            uint4 v;
+                            auto f = [&](int e) { return __uint_as_float(o[i + e]) * inv; };
+                            if constexpr (sizeof(E) == 4)
+                                v = make_uint4(__float_as_uint(f(0)), __float_as_uint(f(1)), __float_as_uint(f(2)), __float_as_uint(f(3)));
+                            else
+                                v = make_uint4(pack16<E>(f(0), f(1)), pack16<E>(f(2), f(3)), pack16<E>(f(4), f(5)), pack16<E>(f(6), f(7)));
+                            const int piece = (part * 32 + i) * int(sizeof(E)) / 16;
+                            *reinterpret_cast<uint4 *>(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
+                        }
                     }
+                    __syncwarp();
+                    const int piece = lane & 7, col = c0 + piece * (16 / int(sizeof(E)));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int rr = k * 4 + (lane >> 3), out_row = row - lane + rr;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
+                        if (out_row < rows && col < a.dim) {
+                            const int64_t tt = int64_t(sp.q0) + (row0 + out_row) / G;
+                            const int hh = g * G + (row0 + out_row) % G;
+                            const int64_t at = partial ? partial_at(a, chunk, tt, hh) * a.dim : tt * t_stride + int64_t(hh) * h_stride;
+                            *reinterpret_cast<uint4 *>(to + at + col) = v;
+                        }
+                    }
+                    __syncwarp();
                 }
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                    if (c * 32 + i < a.dim) {
-                        const float x0 = __uint_as_float(o[i]) * inv, x1 = __uint_as_float(o[i + 1]) * inv;
-                        const float x2 = __uint_as_float(o[i + 2]) * inv, x3 = __uint_as_float(o[i + 3]) * inv;
-                        if (whole) store4(out + c * 32 + i, x0, x1, x2, x3);
-                        else store4(part_o + at * a.dim + c * 32 + i, x0, x1, x2, x3);
-                    }
-            }
+            };
+            if (whole) put(false, static_cast<TO *>(a.out), a.out_token, a.out_head);
+            else put(true, part_o, 0, 0);
         }
     }
 

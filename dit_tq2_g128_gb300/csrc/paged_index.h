@@ -118,4 +118,16 @@ TQ2_HD BoxRange boxes_of(int from, int keys, int rows, int first, int last) {
     return BoxRange{lo, hi};
 }
 
+// Of the `tiles` tiles of `rows` query rows (row = token * group + head) of a span, how
+// many have their last visible key past key x - 1 (x < 0: all of them): the last ones,
+// since a causal token's keys end with itself.
+TQ2_HD int tiles_past(const SeqSpan &sp, int group, int rows, int tiles, bool causal, int64_t x) {
+    if (x < 0) return tiles;
+    if (sp.kv <= x) return 0;
+    const int64_t y = x - (int64_t(sp.kv) - sp.n);  // causal: from the token after the y-th on
+    if (!causal || y <= 0) return tiles;
+    const int64_t t = y * group / rows;
+    return t < tiles ? int(tiles - t) : 0;
+}
+
 }  // namespace tq2

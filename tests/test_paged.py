@@ -140,6 +140,9 @@ void boxes(int from, int keys, int rows, int first, int last, int *out) {
     const BoxRange r = boxes_of(from, keys, rows, first, last);
     out[0] = r.lo, out[1] = r.hi;
 }
+int past(int n, int kv, int group, int rows, int tiles, int causal, long long x) {
+    return tiles_past(SeqSpan{0, n, kv}, group, rows, tiles, causal, x);
+}
 }
 """)
     lib = d / "probe.so"
@@ -220,6 +223,20 @@ def test_boxes_of_a_tile(index):
         want = [i for i in range(keys // rows)
                 if any(first <= k < last for k in range(start + i * rows, start + (i + 1) * rows))]
         assert list(range(out[0], out[1])) == want
+
+
+def test_tiles_past_a_key(index):
+    rng = np.random.default_rng(6)
+    for _ in range(2000):
+        n, kv, group = int(rng.integers(1, 900)), int(rng.integers(0, 1200)), int(rng.integers(1, 17))
+        rows = 256
+        tiles = -(-n * group // rows)
+        for causal in (0, 1):
+            ends = [max(0, kv - n + min(n * group - 1, (t + 1) * rows - 1) // group + 1) if causal else kv
+                    for t in range(tiles)]
+            for x in (-1, 0, 1, int(rng.integers(0, 1300)), kv - 1, kv):
+                want = tiles if x < 0 else sum(e > x for e in ends)
+                assert index.past(n, kv, group, rows, tiles, causal, ctypes.c_longlong(x)) == want, (n, kv, group, x)
 
 
 # ---------------------------------------------------------------------------
