@@ -387,24 +387,34 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         {
             const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's sign
             const T *q = static_cast<const T *>(a.q) + int64_t(sp.q0) * a.q_token;
-            constexpr int CH = DP / 8, IT = CH / 2;  // 16-byte pieces of a row; rows of a tile a thread brings
-            const int tid = threadIdx.x - 32 * W_SOFT, c = tid % CH;
-            for (int t = 0; t < nt; ++t) {
-                uint4 x[IT];  // all of a tile's loads in flight
+            // a group brings its tile, or half of the only one; all of a thread's loads are in flight together
+            constexpr int CH = DP / 8, STEP = kRows / CH;  // 16-byte pieces of a row; rows between a thread's pieces
+            const int tid = threadIdx.x & (kRows - 1), c = tid % CH;
+            const int r_first = tid / CH + (nt == 2 ? 0 : w * (kRows / 2)), count = nt == 2 ? CH : CH / 2;
+            const int row_from = row0 + (nt == 2 ? w * kRows : 0) + r_first;
+            int i = row_from / G, hh = row_from % G;
+            const int i_step = STEP / G, h_step = STEP % G;
+            uint4 x[CH];
 #pragma unroll
-                for (int k = 0; k < IT; ++k) {
-                    const int r = t * kRows + tid / CH + k * (2 * kRows / CH), row = row0 + r;
-                    x[k] = make_uint4(0, 0, 0, 0);
-                    if (r < rows && 8 * c < a.dim)
-                        x[k] = *reinterpret_cast<const uint4 *>(q + int64_t(row / G) * a.q_token + int64_t(g * G + row % G) * a.q_head + 8 * c);
-                }
-#pragma unroll
-                for (int k = 0; k < IT; ++k) {
-                    const int r = tid / CH + k * (2 * kRows / CH);
-                    *reinterpret_cast<uint4 *>(smem + t * L::TILE + (c >> 3) * L::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4)) =
-                        make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
+            for (int k = 0; k < CH; ++k) {
+                x[k] = make_uint4(0, 0, 0, 0);
+                if (k < count && row_from + k * STEP < row0 + rows && 8 * c < a.dim)
+                    x[k] = *reinterpret_cast<const uint4 *>(q + int64_t(i) * a.q_token + int64_t(g * G + hh) * a.q_head + 8 * c);
+                i += i_step;
+                hh += h_step;
+                if (hh >= G) {
+                    hh -= G;
+                    ++i;
                 }
             }
+#pragma unroll
+            for (int k = 0; k < CH; ++k)
+                if (k < count) {
+                    const int r = r_first + k * STEP;
+                    *reinterpret_cast<uint4 *>(smem + (nt == 2 ? w * L::TILE : 0) + (c >> 3) * L::HALF + r * 128 +
+                                               (((c & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
+                }
             fence_proxy_async_smem();
             mbar_arrive(&ctl->q_ready);
         }
@@ -567,6 +577,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             auto put = [&](bool partial, auto *to, int64_t t_stride, int64_t h_stride) {
                 using E = typename std::remove_pointer<decltype(to)>::type;
                 constexpr int W = 128 / sizeof(E);  // columns of a piece: 32 in f32, 64 in 16 bits
+                int64_t at[8];                      // where the rows that this lane stores a part of go
+                const int r_out = row - lane + (lane >> 3);
+                int i = (row0 + r_out) / G, hh = (row0 + r_out) % G;
+                const int i_step = 4 / G, h_step = 4 % G;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int64_t tt = int64_t(sp.q0) + i;
+                    at[k] = partial ? partial_at(a, chunk, tt, g * G + hh) * a.dim : tt * t_stride + int64_t(g * G + hh) * h_stride;
+                    i += i_step;
+                    hh += h_step;
+                    if (hh >= G) {
+                        hh -= G;
+                        ++i;
+                    }
+                }
                 for (int c0 = 0; c0 < a.dim; c0 += W) {
 #pragma unroll
                     for (int part = 0; part < W / 32; ++part) {
@@ -599,14 +624,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     const int piece = lane & 7, col = c0 + piece * (16 / int(sizeof(E)));
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int rr = k * 4 + (lane >> 3), out_row = row - lane + rr;
+                        const int rr = k * 4 + (lane >> 3);
                         const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
-                        if (out_row < rows && col < a.dim) {
-                            const int64_t tt = int64_t(sp.q0) + (row0 + out_row) / G;
-                            const int hh = g * G + (row0 + out_row) % G;
-                            const int64_t at = partial ? partial_at(a, chunk, tt, hh) * a.dim : tt * t_stride + int64_t(hh) * h_stride;
-                            *reinterpret_cast<uint4 *>(to + at + col) = v;
-                        }
+                        if (r_out + 4 * k < rows && col < a.dim) *reinterpret_cast<uint4 *>(to + at[k] + col) = v;
                     }
                     __syncwarp();
                 }
