@@ -12,15 +12,21 @@
 // tensor path's rate up to R = 16 (the tcgen05 path of attention_paged_tc.cu
 // needs 128 rows in M and takes over above).
 //
-// A CTA (four consumer warps of 16 keys each a tile, one producer warp) owns one
-// (sequence, key head, chunk of keys).  The producer's lanes look up one page
-// each and copy its rows by tensor copies with the 128-byte swizzle into a ring
-// of three tiles (96 KB at 128 features; two CTAs an SM keep 192 KB in flight).
-// A copy's box is the largest power of two of rows that divides the page size, so
-// a box never crosses a page, whatever the page size; features past dim are
-// filled with zeros by the copy.  Every warp keeps its own m, l and O; they meet
-// once, at the end.  Chunks of a long context leave (m, l, O) in the workspace and
-// a second, dependent launch joins them in a fixed order.
+// Work is shared out evenly: the (sequence, key head) pairs' tiles, in one line, are
+// cut into as many equal runs as there are CTAs (two an SM), wherever that falls; a
+// pair that is cut leaves (m, l, O) of its pieces in the workspace and a second,
+// dependent launch joins them in order.  So a batch of very different lengths keeps
+// every SM busy to the end, and a CTA starts once.  (Cut into chunks of 1024 keys, 64
+// sequences of 3000 keys took 135 us and 121 in one chunk each; shared out: DESIGN.)
+//
+// A CTA has four consumer warps of 16 keys each a tile and one producer warp, which
+// runs ahead through all of the CTA's pairs.  It looks pages up 32 boxes at a time and
+// copies rows by tensor copies with the 128-byte swizzle into a ring of three tiles (96
+// KB at 128 features; two CTAs an SM keep 192 KB in flight).  A copy's box is the
+// largest power of two of rows that divides the page size, so a box never crosses a
+// page, whatever the page size; features past dim are filled with zeros by the copy.
+// Every warp keeps its own m, l and O; they meet at the end of a pair, in the ring's
+// slot of its last tile.
 //
 // Slots that no row sees are never multiplied: their scores are replaced by
 // -inf and their rows of V are zeroed in shared memory (0 * NaN is NaN).  Where
@@ -39,6 +45,9 @@ constexpr int kKeys = 64;       // keys of a tile
 constexpr int kStages = 3;
 constexpr int kConsumers = 4;   // warps, 16 keys of a tile each
 constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kCtas = 2 * kNumSms;
+constexpr int kMinTiles = 4;    // units of a run, at least, where pairs may be cut
+constexpr int kWholeKeys = 512; // up to so many keys a pair stays whole (a join costs more than a CTA saves)
 constexpr int kRowsMax = 16;    // query rows per (sequence, key head) that this kernel takes
 
 template <int DP, int NT>
@@ -48,18 +57,23 @@ struct RowLayout {
     static constexpr int PLANE = HALF * HALVES;        // K (or V) of a tile
     static constexpr int RING = kStages * 2 * PLANE;
     static constexpr int ROWS = 8 * NT;
-    static constexpr int OPAD = DP + 4;                // f32 row of the final exchange
-    static_assert(kConsumers * ROWS * OPAD * 4 <= RING, "the exchange reuses the ring");
+    static constexpr int OPAD = DP + 4;                // f32 row of the warps' exchange
+    static_assert(kConsumers * 8 * OPAD * 4 <= 2 * PLANE, "eight rows' exchange lies in a slot");
     static constexpr int OFF_CTL = RING;
-    static constexpr int OFF_ML = OFF_CTL + 128;       // m, l per warp and row
-    static constexpr int OFF_POISON = OFF_ML + 2 * kConsumers * ROWS * 4;
+    static constexpr int OFF_ML = OFF_CTL + 128;       // m, l per warp and row, twice (pairs in turn)
+    static constexpr int OFF_POISON = OFF_ML + 4 * kConsumers * ROWS * 4;
     static constexpr int BYTES = OFF_POISON + ROWS * DP * 4 + 1024;
 };
 
 struct RowCtl {
     uint64_t full[kStages], empty[kStages];
     int abort, poisoned;
+    int b, g, t, left;  // where this CTA's run begins: sequence, key head, unit; its units
 };
+static_assert(sizeof(RowCtl) <= 128, "control block");
+
+__device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+static_assert(32 * kConsumers == 128, "consumer_sync");
 
 template <typename T>
 __device__ __forceinline__ void mma_16x8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -91,13 +105,124 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     return y;
 }
 
+// How a call is shared out: `rows` query rows a pair at most, the rows of a copy, and
+// whether pairs may be cut.
+struct RowPlan {
+    int rows;
+    int box_rows;
+    int split;
+};
+
+// The run of this CTA (one warp): `left` units from unit t of (b, g) on.  Block 0 also
+// leaves each sequence's first unit and the units of a run for the join.
+__device__ __forceinline__ void find_run(const PagedArgs &a, const RowPlan &plan, RowCtl *ctl, int *__restrict__ starts,
+                                         unsigned int *status) {
+    const int lane = threadIdx.x & 31;
+    int total = 0;
+    for (int base = 0; base < a.batch.seqs; base += 32) {
+        const int b = base + lane;
+        int units = 0;
+        if (b < a.batch.seqs) {
+            bool bad = false;
+            units = tiles_of(seq_span(a.batch, b, bad), a.window, a.causal, kKeys, plan.split).units * a.kv_heads;
+            report_bad(bad, status);
+        }
+        total += int(__reduce_add_sync(0xffffffffu, unsigned(units)));
+    }
+    const int ctas = int(gridDim.x), least = plan.split ? kMinTiles : 1;
+    const int share = max(least, (total + ctas - 1) / ctas);
+    const bool write = blockIdx.x == 0 && starts != nullptr;
+    const int64_t from = int64_t(blockIdx.x) * share;
+    int before = 0;
+    if (lane == 0) {
+        ctl->left = from < total ? int(min(int64_t(share), total - from)) : 0;
+        if (write) starts[a.batch.seqs] = share;
+    }
+    if (from >= total && !write) return;
+    for (int base = 0; base < a.batch.seqs; base += 32) {
+        const int b = base + lane;
+        int per = 0, units = 0;
+        if (b < a.batch.seqs) {
+            bool ignore = false;
+            per = tiles_of(seq_span(a.batch, b, ignore), a.window, a.causal, kKeys, plan.split).units;
+            units = per * a.kv_heads;
+        }
+        int upto = units;  // inclusive over the lanes
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += x;
+        }
+        upto += before;
+        if (write && b < a.batch.seqs) starts[b] = upto - units;
+        if (units > 0 && from >= upto - units && from < upto) {
+            const int at = int(from) - (upto - units);
+            ctl->b = b;
+            ctl->g = at / per;
+            ctl->t = at % per;
+        }
+        before = __shfl_sync(0xffffffffu, upto, 31);
+        if (!write && from < before) return;
+    }
+}
+
+// A CTA's run, pair by pair: every role walks it by itself.
+struct RowWalk {
+    const PagedArgs &a;
+    const RowPlan &plan;
+    int b, g, t, left;
+    SeqSpan sp;
+    RowSpan rs;
+    TileSpan ts;
+    // the current pair's part
+    int first, last, tile0, tiles, take;
+
+    __device__ __forceinline__ RowWalk(const PagedArgs &args, const RowPlan &p, const RowCtl *ctl)
+        : a(args), plan(p), b(uniform(ctl->b)), g(uniform(ctl->g)), t(uniform(ctl->t)), left(uniform(ctl->left)) {
+        if (left > 0) load();
+    }
+    __device__ __forceinline__ void load() {
+        bool ignore = false;
+        const SeqSpan s = seq_span(a.batch, b, ignore);  // (reported by find_run)
+        sp = SeqSpan{uniform(s.q0), uniform(s.n), uniform(s.kv)};
+        if (sp.n == 0) return;
+        rs = rows_see(sp, 0, sp.n - 1, a.window, a.causal);
+        ts = tiles_of(sp, a.window, a.causal, kKeys, plan.split);
+    }
+    __device__ __forceinline__ bool more() {
+        if (left <= 0) return false;
+        take = min(left, ts.units - t);
+        const bool cut = ts.units > 1;  // units are tiles
+        tile0 = ts.tile0 + (cut ? t : 0);
+        tiles = cut ? take : ts.tiles;
+        first = max(rs.lo, tile0 * kKeys);
+        last = min(rs.hi, (tile0 + tiles) * kKeys);
+        return true;
+    }
+    __device__ __forceinline__ bool whole() const { return t == 0 && take == ts.units; }
+    // where a cut pair's piece goes: a run's first piece, begun by the run before, or its last
+    __device__ __forceinline__ int slot() const { return 2 * int(blockIdx.x) + (t == 0); }
+    __device__ __forceinline__ void next() {
+        left -= take;
+        t += take;
+        if (t < ts.units) return;
+        t = 0;
+        if (++g < a.kv_heads) return;
+        g = 0;
+        while (left > 0 && ++b < a.batch.seqs) {
+            load();
+            if (sp.n > 0) break;
+        }
+    }
+};
+
 // DP: features padded to 64 or 128; NT: query rows in eights; SPLIT_P: the weights
 // enter the second product as two terms (f32 outputs).
 template <typename T, typename TO, int DP, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                  const PagedArgs a, const KeyPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml,
-                  unsigned int *status, uint64_t wait_ns) {
+                  const PagedArgs a, const RowPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml,
+                  int *__restrict__ starts, unsigned int *status, uint64_t wait_ns) {
     using L = RowLayout<DP, NT>;
     constexpr bool SPLIT_P = sizeof(TO) == 4;
     extern __shared__ uint8_t rows_raw[];
@@ -106,7 +231,6 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     RowCtl *ctl = reinterpret_cast<RowCtl *>(smem + L::OFF_CTL);
     float *poison = reinterpret_cast<float *>(smem + L::OFF_POISON);
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
-    const int g = blockIdx.y, b = int(blockIdx.x / unsigned(plan.chunks)), chunk = int(blockIdx.x % unsigned(plan.chunks));
     const int G = a.heads / a.kv_heads;
 
     if (threadIdx.x == 0) {
@@ -121,58 +245,57 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
     // the tables, q and the cache may be written by the kernel before this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    bool bad = false;
-    const SeqSpan sp = seq_span(a.batch, b, bad);
-    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
-    if (sp.n == 0 || chunk >= max(cut.chunks, 1)) return;  // (CTA-uniform)
-    const RowSpan rs = rows_see(sp, 0, sp.n - 1, a.window, a.causal);
-    const int R = sp.n * G;
-    const int64_t k0 = cut.base + int64_t(chunk) * plan.chunk;
-    const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
-    const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
-    const int tile0 = first / kKeys, tiles = cut.chunks ? (last + kKeys - 1) / kKeys - tile0 : 0;  // (each holds a key)
-    if (sp.n > 1)  // (one token's keys are seen by all its rows or by none)
-        for (int i = threadIdx.x; i < L::ROWS * DP; i += kThreads) poison[i] = 0.f;
+    if (warp == 0) find_run(a, plan, ctl, starts, status);
     __syncthreads();
+    RowWalk walk(a, plan, ctl);
+    int ring = 0;  // tiles so far, over all pairs
 
     if (warp == kConsumers) {
-        report_bad(bad, status);
-        bad = false;
-        // ---- producer
-        BoxPages boxes(a, b, tile0 * kKeys, kKeys, plan.box_rows, first, last);
-        const int tiles_u = uniform(tiles);
-        int issued = 0;
-        bool ok = true;
-        for (; issued < tiles_u; ++issued) {
-            const int s = issued % kStages, u = issued / kStages;
-            boxes.seek(issued);
-            if (u > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->empty[s], (u - 1) & 1, &ctl->abort, wait_ns, status));
-            if (!ok) break;
-            const uint32_t stage = base + uint32_t(s * 2 * L::PLANE);
-            const BoxRange br = boxes.range(issued);
-            if (lane == 0) mbar_expect_tx(&ctl->full[s], uint32_t((br.hi - br.lo) * boxes.rows * 256 * L::HALVES));
-            __syncwarp();
-            boxes.each(issued, br, bad, [&](int row, int slot, int page) {
+        // ---- producer: ahead through the run, as far as the ring has room
+        bool bad = false, ok = true;
+        for (; ok && walk.more(); walk.next()) {
+            BoxPages boxes(a, walk.b, walk.tile0 * kKeys, kKeys, plan.box_rows, walk.first, walk.last);
+            const int tiles = walk.tiles, g = walk.g;
+            for (int it = 0; it < tiles; ++it, ++ring) {
+                const int s = ring % kStages, u = ring / kStages;
+                boxes.seek(it);
+                if (u > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->empty[s], (u - 1) & 1, &ctl->abort, wait_ns, status));
+                if (!ok) break;
+                const uint32_t stage = base + uint32_t(s * 2 * L::PLANE);
+                const BoxRange br = boxes.range(it);
+                if (lane == 0) mbar_expect_tx(&ctl->full[s], uint32_t((br.hi - br.lo) * boxes.rows * 256 * L::HALVES));
+                __syncwarp();
+                boxes.each(it, br, bad, [&](int row, int slot, int page) {
 #pragma unroll
-                for (int h = 0; h < L::HALVES; ++h) {
-                    tma_cache(stage + uint32_t(h * L::HALF + row * 128), &kmap, 64 * h, g, slot, page, &ctl->full[s]);
-                    tma_cache(stage + uint32_t(L::PLANE + h * L::HALF + row * 128), &vmap, 64 * h, g, slot, page, &ctl->full[s]);
-                }
-            });
+                    for (int h = 0; h < L::HALVES; ++h) {
+                        tma_cache(stage + uint32_t(h * L::HALF + row * 128), &kmap, 64 * h, g, slot, page, &ctl->full[s]);
+                        tma_cache(stage + uint32_t(L::PLANE + h * L::HALF + row * 128), &vmap, 64 * h, g, slot, page, &ctl->full[s]);
+                    }
+                });
+            }
         }
         report_bad(bad, status);
-        if (!ok) {
-            if (lane == 0) {  // what was issued lands before the CTA ends
-                for (int t = max(0, issued - kStages); t < issued; ++t)
-                    mbar_wait_bounded(&ctl->full[t % kStages], (t / kStages) & 1, drain_ns(wait_ns), status);
-            }
-            __syncwarp();
-        }
+        // what was issued lands before the CTA ends (given up: nobody else waits for it)
+        if (!ok && lane == 0)
+            for (int t = max(0, ring - kStages); t < ring; ++t)
+                mbar_wait_bounded(&ctl->full[t % kStages], (t / kStages) & 1, drain_ns(wait_ns), status);
+        return;
     }
 
-    float m[NT][2], l[NT][2], o[NT][DP / 16][4];
-    if (warp < kConsumers) {
-        // ---- consumer: 16 keys of every tile
+    // ---- consumers: 16 keys of every tile.  After a wait that was given up a warp walks on without waiting or
+    // computing, so that every warp meets every barrier.
+    bool ok = true;
+    for (int pairs = 0; walk.more(); walk.next(), ++pairs) {
+        const SeqSpan sp = walk.sp;
+        const RowSpan rs = walk.rs;
+        const int g = walk.g, R = sp.n * G, first = walk.first, last = walk.last, tiles = walk.tiles;
+        if (sp.n > 1) {  // (one token's keys are seen by all its rows or by none)
+            consumer_sync();  // the pair before has been written
+            for (int i = threadIdx.x; i < L::ROWS * DP; i += 32 * kConsumers) poison[i] = 0.f;
+            if (threadIdx.x == 0) ctl->poisoned = 0;
+            consumer_sync();
+        }
+        float m[NT][2], l[NT][2], o[NT][DP / 16][4];
         uint32_t q[NT][DP / 16][2];
         int lo[NT][2], hi[NT][2];
 #pragma unroll
@@ -202,10 +325,11 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         }
         const float scale2 = a.scale * 1.4426950408889634f;
         const int arow = lane & 15, brow = (lane & 7) + ((lane >> 4) & 1) * 8;
-        for (int it = 0; it < tiles; ++it) {
-            const int s = it % kStages;
-            if (!__all_sync(0xffffffffu, wait_phase(&ctl->full[s], (it / kStages) & 1, &ctl->abort, wait_ns, status))) break;
-            const int key0 = (tile0 + it) * kKeys + warp * 16;
+        for (int it = 0; it < tiles && ok; ++it, ++ring) {
+            const int s = ring % kStages;
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->full[s], (ring / kStages) & 1, &ctl->abort, wait_ns, status));
+            if (!ok) break;
+            const int key0 = (walk.tile0 + it) * kKeys + warp * 16;
             const uint32_t ks = base + uint32_t(s * 2 * L::PLANE + warp * 16 * 128), vs = ks + L::PLANE;
             if (key0 < last && key0 + 16 > first) {
                 const bool clean = key0 >= rs.lo_all && key0 + 16 <= min(rs.hi_all, last) && key0 >= first;
@@ -319,10 +443,11 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                 if (!clean) fence_proxy_async_smem();  // this warp wrote where the next copies land
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->empty[s]);
+            if (it + 1 < tiles && lane == 0) mbar_arrive(&ctl->empty[s]);  // the last tile's slot is kept for the exchange
         }
         // m and l of this warp's keys
-        float *wm = reinterpret_cast<float *>(smem + L::OFF_ML), *wl = wm + kConsumers * L::ROWS;
+        float *wm = reinterpret_cast<float *>(smem + L::OFF_ML) + (pairs & 1) * 2 * kConsumers * L::ROWS;
+        float *wl = wm + kConsumers * L::ROWS;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -335,111 +460,139 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     wl[warp * L::ROWS + t * 8 + 2 * lane + c] = x;
                 }
             }
-    }
-    __syncthreads();
-    if (*reinterpret_cast<volatile int *>(&ctl->abort)) return;
-    const float *wm = reinterpret_cast<const float *>(smem + L::OFF_ML), *wl = wm + kConsumers * L::ROWS;
-    float *ob = reinterpret_cast<float *>(smem);  // [warp][row][OPAD], over the ring
-    if (warp < kConsumers) {
+        const int kept = tiles > 0 ? (ring + kStages - 1) % kStages : 0;  // slot of the last tile
+        float *ob = reinterpret_cast<float *>(smem + kept * 2 * L::PLANE);  // [warp][8 rows][OPAD]
+        const bool whole = walk.whole();
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+        for (int t = 0; t < NT; ++t) {  // eight rows at a time
+            consumer_sync();
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int n = t * 8 + 2 * (lane & 3) + c;
-                float top = wm[n];
+            for (int c = 0; c < 2 && tiles > 0; ++c) {  // (a pair without keys has no slot, and zeros)
+                const int n = 2 * (lane & 3) + c;
+                float top = wm[t * 8 + n];
 #pragma unroll
-                for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, wm[w * L::ROWS + n]);
+                for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, wm[w * L::ROWS + t * 8 + n]);
                 const float f = m[t][c] == top ? 1.f : fast_ex2(m[t][c] - top);
 #pragma unroll
                 for (int j = 0; j < DP / 16; ++j) {
-                    ob[(warp * L::ROWS + n) * L::OPAD + j * 16 + (lane >> 2)] = o[t][j][c] * f;
-                    ob[(warp * L::ROWS + n) * L::OPAD + j * 16 + 8 + (lane >> 2)] = o[t][j][2 + c] * f;
+                    ob[(warp * 8 + n) * L::OPAD + j * 16 + (lane >> 2)] = o[t][j][c] * f;
+                    ob[(warp * 8 + n) * L::OPAD + j * 16 + 8 + (lane >> 2)] = o[t][j][2 + c] * f;
                 }
             }
-    }
-    __syncthreads();
-    const bool whole = cut.chunks <= 1;
-    for (int i = threadIdx.x; i < R * (DP / 4); i += kThreads) {
-        const int n = i / (DP / 4), d = 4 * (i % (DP / 4));
-        if (d >= a.dim) continue;
-        float top = wm[n], sum = 0.f;
+            consumer_sync();
+            for (int i = threadIdx.x; ok && i < min(8, R - 8 * t) * (DP / 4); i += 32 * kConsumers) {
+                const int r = i / (DP / 4), n = t * 8 + r, d = 4 * (i % (DP / 4));
+                if (d >= a.dim) continue;
+                float top = wm[n], sum = 0.f;
 #pragma unroll
-        for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, wm[w * L::ROWS + n]);
-        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = 1; w < kConsumers; ++w) top = fmaxf(top, wm[w * L::ROWS + n]);
+                float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kConsumers; ++w) {
-            const float mw = wm[w * L::ROWS + n];
-            sum += wl[w * L::ROWS + n] * (mw == top ? 1.f : fast_ex2(mw - top));
-            const float4 y = *reinterpret_cast<const float4 *>(&ob[(w * L::ROWS + n) * L::OPAD + d]);
-            x.x += y.x;
-            x.y += y.y;
-            x.z += y.z;
-            x.w += y.w;
+                for (int w = 0; w < kConsumers && tiles > 0; ++w) {
+                    const float mw = wm[w * L::ROWS + n];
+                    sum += wl[w * L::ROWS + n] * (mw == top ? 1.f : fast_ex2(mw - top));
+                    const float4 y = *reinterpret_cast<const float4 *>(&ob[(w * 8 + r) * L::OPAD + d]);
+                    x.x += y.x;
+                    x.y += y.y;
+                    x.z += y.z;
+                    x.w += y.w;
+                }
+                if (sp.n > 1 && ctl->poisoned) {
+                    x.x += poison[n * DP + d];
+                    x.y += poison[n * DP + d + 1];
+                    x.z += poison[n * DP + d + 2];
+                    x.w += poison[n * DP + d + 3];
+                }
+                if (whole) {
+                    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
+                    TO *out = static_cast<TO *>(a.out) + (int64_t(sp.q0) + n / G) * a.out_token + int64_t(g * G + n % G) * a.out_head + d;
+                    store4(out, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+                } else {
+                    const int64_t at = int64_t(walk.slot()) * plan.rows + n;
+                    *reinterpret_cast<float4 *>(part_o + at * a.dim + d) = x;
+                    if (d == 0) part_ml[at] = make_float2(top, sum);
+                }
+            }
         }
-        if (ctl->poisoned) {
-            x.x += poison[n * DP + d];
-            x.y += poison[n * DP + d + 1];
-            x.z += poison[n * DP + d + 2];
-            x.w += poison[n * DP + d + 3];
-        }
-        if (whole) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key: zeros
-            TO *out = static_cast<TO *>(a.out) + (int64_t(sp.q0) + n / G) * a.out_token + int64_t(g * G + n % G) * a.out_head + d;
-            store4(out, x.x * inv, x.y * inv, x.z * inv, x.w * inv);
-        } else {
-            const int64_t at = partial_at(a, chunk, int64_t(sp.q0) + n / G, g * G + n % G);
-            *reinterpret_cast<float4 *>(part_o + at * a.dim + d) = x;
-            if (d == 0) part_ml[at] = make_float2(top, sum);
+        if (tiles > 0 && ok) {
+            fence_proxy_async_smem();  // the exchange lay where the next copy lands
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->empty[kept]);
         }
     }
 }
 
+// Joins the pieces of a cut pair for one (new token, head): runs c0 .. c1 hold it, c0's
+// piece in its last slot, the others' in their first.
+template <typename TO>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+rows_join_kernel(const PagedArgs a, const RowPlan plan, const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
+                 const int *__restrict__ starts) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t t = blockIdx.x;
+    const int h = blockIdx.y, G = a.heads / a.kv_heads;
+    const int b = seq_of(a.batch, t);
+    if (b < 0) return;
+    bool ignore = false;
+    const SeqSpan sp = seq_span(a.batch, b, ignore);  // (reported by the launch before)
+    if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
+    const int share = starts[a.batch.seqs], units = tiles_of(sp, a.window, a.causal, kKeys, true).units;
+    const int from = starts[b] + (h / G) * units, c0 = from / share, c1 = (from + units - 1) / share;
+    if (c0 == c1) return;
+    const int row = int(t - sp.q0) * G + h % G;
+    join_partials(a, t, h, c1 - c0 + 1, part_o, part_ml,
+                  [&](int i) { return int64_t(i == 0 ? 2 * c0 + 1 : 2 * (c0 + i)) * plan.rows + row; }, static_cast<TO *>(a.out));
+}
+
+struct RowLaunch {
+    RowPlan plan;
+    int ctas;
+};
+
+RowLaunch row_launch(int64_t kv_heads, int64_t seqs, int64_t rows, int64_t span, int page_size) {
+    RowLaunch r = {};
+    r.plan.rows = int(rows);
+    r.plan.box_rows = std::min(page_size & -page_size, kKeys);
+    r.plan.split = span > kWholeKeys;
+    const int64_t tiles = r.plan.split ? (span + kKeys - 1) / kKeys + 1 : 1;  // (a window may begin inside a tile)
+    const int64_t units = seqs * kv_heads * tiles, least = r.plan.split ? kMinTiles : 1;
+    r.ctas = int(std::min<int64_t>(kCtas, (units + least - 1) / least));
+    return r;
+}
+
+size_t row_ws_bytes(int64_t seqs, int64_t rows, int64_t dim, int64_t ctas) {
+    return size_t(2 * ctas * rows) * size_t(dim * 4 + 8) + size_t(seqs + 1) * 4;
+}
+
 template <typename T, typename TO, int DP, int NT>
-cudaError_t launch_rows(const PagedArgs &a, const KeyPlan &plan, const CUtensorMap &km, const CUtensorMap &vm, void *ws,
+cudaError_t launch_rows(const PagedArgs &a, const RowLaunch &r, const CUtensorMap &km, const CUtensorMap &vm, void *ws,
                         const LaunchCtx &ctx) {
     using L = RowLayout<DP, NT>;
     auto kernel = paged_rows_kernel<T, TO, DP, NT>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
-    float *po = static_cast<float *>(ws);
-    float2 *pml = reinterpret_cast<float2 *>(po + int64_t(plan.chunks) * a.batch.tokens * a.heads * a.dim);
-    e = launch_dependent(kernel, dim3(unsigned(int64_t(plan.chunks) * a.batch.seqs), unsigned(a.kv_heads)), kThreads,
-                         L::BYTES, ctx.stream, km, vm, a, plan, po, pml, ctx.status, ctx.wait_ns);
-    if (e != cudaSuccess || plan.chunks == 1) return e;
-    return launch_join<TO>(a, plan, po, pml, ctx);
+    const int64_t slots = 2 * int64_t(r.ctas) * r.plan.rows;
+    float *po = r.plan.split ? static_cast<float *>(ws) : nullptr;
+    float2 *pml = r.plan.split ? reinterpret_cast<float2 *>(po + slots * a.dim) : nullptr;
+    int *starts = r.plan.split ? reinterpret_cast<int *>(pml + slots) : nullptr;
+    e = launch_dependent(kernel, dim3(unsigned(r.ctas)), kThreads, L::BYTES, ctx.stream, km, vm, a, r.plan, po, pml, starts,
+                         ctx.status, ctx.wait_ns);
+    if (e != cudaSuccess || !r.plan.split) return e;
+    return launch_dependent(rows_join_kernel<TO>, dim3(unsigned(a.batch.tokens), unsigned(a.heads)), 32 * kJoinWarps, 0,
+                            ctx.stream, a, r.plan, po, pml, starts);
 }
 
 template <typename T, typename TO>
-cudaError_t launch_rows_io(const PagedArgs &a, const KeyPlan &plan, void *ws, const LaunchCtx &ctx) {
+cudaError_t launch_rows_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
+    const int64_t rows = int64_t(a.batch.max_q) * (a.heads / a.kv_heads);
+    const int64_t span = key_span(a.batch.max_q, a.batch.max_kv, a.window);
+    if (int64_t(a.batch.seqs) * a.kv_heads * (span / kKeys + 2) > INT32_MAX) return cudaErrorInvalidValue;
+    const RowLaunch r = row_launch(a.kv_heads, a.batch.seqs, rows, span, a.batch.page_size);
     CUtensorMap km, vm;
-    cudaError_t e = cache_maps<T>(a, plan.box_rows, &km, &vm);
+    cudaError_t e = cache_maps<T>(a, r.plan.box_rows, &km, &vm);
     if (e != cudaSuccess) return e;
-    const bool few = int64_t(a.batch.max_q) * (a.heads / a.kv_heads) <= 8;
-    if (a.dim <= 64)
-        return few ? launch_rows<T, TO, 64, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 64, 2>(a, plan, km, vm, ws, ctx);
-    return few ? launch_rows<T, TO, 128, 1>(a, plan, km, vm, ws, ctx) : launch_rows<T, TO, 128, 2>(a, plan, km, vm, ws, ctx);
-}
-
-// Keys a chunk: as many chunks as give every SM's two CTAs three turns at the
-// host's bound of the keys (sequences are shorter than the bound), between 256
-// keys, below which a chunk is mostly start and end, and 1024, where a partial
-// result is 1/64 of the chunk's bytes at 8 rows.
-constexpr int kMinChunk = 256, kMaxChunk = 1024, kTurns = 6;
-
-KeyPlan row_plan(int64_t kv_heads, int64_t seqs, int64_t max_q, int64_t max_kv, int64_t window, int page_size) {
-    KeyPlan p = {};
-    const int64_t span = key_span(max_q, max_kv, window);
-    const int64_t want = (seqs * kv_heads * span + kTurns * kNumSms - 1) / (kTurns * kNumSms);
-    p.chunk = int(std::min<int64_t>(kMaxChunk, std::max<int64_t>(kMinChunk, (want + 127) / 128 * 128)));
-    p.chunks = int(std::max<int64_t>(1, (span + p.chunk - 1) / p.chunk));
-    p.box_rows = std::min(page_size & -page_size, kKeys);
-    return p;
-}
-
-// The most chunks that row_plan gives for any window.
-int64_t row_chunks_bound(int64_t kv_heads, int64_t seqs, int64_t max_kv) {
-    const int64_t turns = (kTurns * kNumSms + seqs * kv_heads - 1) / (seqs * kv_heads);
-    return std::min((max_kv + kMinChunk - 1) / kMinChunk, std::max(turns, (max_kv + kMaxChunk - 1) / kMaxChunk));
+    if (a.dim <= 64) return rows <= 8 ? launch_rows<T, TO, 64, 1>(a, r, km, vm, ws, ctx) : launch_rows<T, TO, 64, 2>(a, r, km, vm, ws, ctx);
+    return rows <= 8 ? launch_rows<T, TO, 128, 1>(a, r, km, vm, ws, ctx) : launch_rows<T, TO, 128, 2>(a, r, km, vm, ws, ctx);
 }
 
 }  // namespace
@@ -447,21 +600,19 @@ int64_t row_chunks_bound(int64_t kv_heads, int64_t seqs, int64_t max_kv) {
 size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
                                 int64_t max_kv) {
     const int64_t rows = std::min(max_q, tokens) * (heads / kv_heads);
-    const int64_t chunks = rows > kRowsMax ? attention_paged_chunk_bound(heads, kv_heads, seqs, tokens, max_kv)
-                                           : row_chunks_bound(kv_heads, seqs, max_kv);
-    return partial_bytes(chunks, tokens, heads, dim);
+    if (rows > kRowsMax) return partial_bytes(attention_paged_chunk_bound(heads, kv_heads, seqs, tokens, max_kv), tokens, heads, dim);
+    const RowLaunch r = row_launch(kv_heads, seqs, rows, max_kv, 1);  // (a window only shortens the span)
+    return r.plan.split ? row_ws_bytes(seqs, rows, dim, r.ctas) : 0;
 }
 
 cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx) {
     if (int64_t(a.batch.max_q) * (a.heads / a.kv_heads) > kRowsMax) return launch_attention_paged_chunk(a, dtype, out_f32, ws, ctx);
-    const KeyPlan p = row_plan(a.kv_heads, a.batch.seqs, a.batch.max_q, a.batch.max_kv, a.window, a.batch.page_size);
-    if (int64_t(p.chunks) * a.batch.seqs > INT32_MAX) return cudaErrorInvalidValue;
     if (dtype == TQ2_F16) {
-        if (out_f32) return launch_rows_io<__half, float>(a, p, ws, ctx);
-        return launch_rows_io<__half, __half>(a, p, ws, ctx);
+        if (out_f32) return launch_rows_io<__half, float>(a, ws, ctx);
+        return launch_rows_io<__half, __half>(a, ws, ctx);
     }
-    if (out_f32) return launch_rows_io<__nv_bfloat16, float>(a, p, ws, ctx);
-    return launch_rows_io<__nv_bfloat16, __nv_bfloat16>(a, p, ws, ctx);
+    if (out_f32) return launch_rows_io<__nv_bfloat16, float>(a, ws, ctx);
+    return launch_rows_io<__nv_bfloat16, __nv_bfloat16>(a, ws, ctx);
 }
 
 }  // namespace tq2

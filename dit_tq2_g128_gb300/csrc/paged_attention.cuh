@@ -245,38 +245,25 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int s
 
 constexpr int kJoinWarps = 4;
 
-// Joins the chunks of one (new token, head): out = sum_c 2^(m_c - m) O_c / sum_c
-// 2^(m_c - m) l_c, in the chunks' order within each warp and the warps' order
-// after that.  Reads what the attention launch before it wrote (mostly from L2).
-template <typename TO>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-paged_join_kernel(const PagedArgs a, const KeyPlan plan, const float *__restrict__ part_o,
-                  const float2 *__restrict__ part_ml) {
+// Joins `count` partial results of (new token t, head h), the i-th at index place(i):
+// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, in order within each warp and
+// the warps' sums in their order after that.  Reads what the launch before wrote
+// (mostly from L2).  The whole block.
+template <typename TO, typename F>
+__device__ __forceinline__ void join_partials(const PagedArgs &a, int64_t t, int h, int count, const float *__restrict__ part_o,
+                                              const float2 *__restrict__ part_ml, F place, TO *out) {
     __shared__ float sh_o[kJoinWarps][128], sh_l[kJoinWarps];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = seq_of(a.batch, t);
-    if (b < 0) return;
-    bool bad = false;
-    const SeqSpan sp = seq_span(a.batch, b, bad);  // (reported by the launch before)
-    if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
-    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
-    if (cut.chunks <= 1) return;
-    // the chunks that this token sees a key in
-    const KeyRange kr = keys_of(sp, int(t - sp.q0), a.window, a.causal);
-    const int c0 = kr.hi > kr.lo ? (kr.lo - cut.base) / plan.chunk : 0;
-    const int c1 = kr.hi > kr.lo ? (kr.hi - 1 - cut.base) / plan.chunk + 1 : 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float top = -INFINITY;
-    for (int c = c0 + lane; c < c1; c += 32) top = fmaxf(top, part_ml[partial_at(a, c, t, h)].x);
+    for (int c = lane; c < count; c += 32) top = fmaxf(top, part_ml[place(c)].x);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
     const bool mine = 4 * lane < a.dim;
 #pragma unroll 4
-    for (int c = c0 + warp; c < c1; c += kJoinWarps) {
-        const int64_t at = partial_at(a, c, t, h);
+    for (int c = warp; c < count; c += kJoinWarps) {
+        const int64_t at = place(c);
         const float2 ml = part_ml[at];
         const float f = ml.x == top ? 1.f : fast_ex2(ml.x - top);
         l = fmaf(f, ml.y, l);
@@ -302,9 +289,29 @@ paged_join_kernel(const PagedArgs a, const KeyPlan plan, const float *__restrict
             l += sh_l[w];
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        store4(static_cast<TO *>(a.out) + t * a.out_token + int64_t(h) * a.out_head + 4 * lane, o.x * inv, o.y * inv, o.z * inv,
-               o.w * inv);
+        store4(out + t * a.out_token + int64_t(h) * a.out_head + 4 * lane, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
+}
+
+// Joins the chunks that one (new token, head) sees a key in.
+template <typename TO>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+paged_join_kernel(const PagedArgs a, const KeyPlan plan, const float *__restrict__ part_o,
+                  const float2 *__restrict__ part_ml) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t t = blockIdx.x;
+    const int h = blockIdx.y;
+    const int b = seq_of(a.batch, t);
+    if (b < 0) return;
+    bool bad = false;
+    const SeqSpan sp = seq_span(a.batch, b, bad);  // (reported by the launch before)
+    if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
+    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
+    if (cut.chunks <= 1) return;
+    const KeyRange kr = keys_of(sp, int(t - sp.q0), a.window, a.causal);
+    const int c0 = kr.hi > kr.lo ? (kr.lo - cut.base) / plan.chunk : 0;
+    const int c1 = kr.hi > kr.lo ? (kr.hi - 1 - cut.base) / plan.chunk + 1 : 0;
+    join_partials(a, t, h, c1 - c0, part_o, part_ml, [&](int i) { return partial_at(a, c0 + i, t, h); }, static_cast<TO *>(a.out));
 }
 
 template <typename TO>

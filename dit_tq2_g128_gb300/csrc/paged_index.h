@@ -130,4 +130,17 @@ TQ2_HD int tiles_past(const SeqSpan &sp, int group, int rows, int tiles, bool ca
     return t < tiles ? int(tiles - t) : 0;
 }
 
+// The tiles of `keys` keys that hold a key some token of a span sees, and the units of
+// work that the span's (sequence, key head) pairs are shared out in: tiles if they
+// may be split among CTAs, else whole pairs.
+struct TileSpan {
+    int tile0, tiles, units;
+};
+TQ2_HD TileSpan tiles_of(const SeqSpan &sp, int64_t window, bool causal, int keys, bool split) {
+    if (sp.n == 0) return TileSpan{0, 0, 0};
+    const RowSpan r = rows_see(sp, 0, sp.n - 1, window, causal);
+    const int tile0 = r.lo / keys, tiles = r.hi > r.lo ? (r.hi + keys - 1) / keys - tile0 : 0;
+    return TileSpan{tile0, tiles, split && tiles > 1 ? tiles : 1};
+}
+
 }  // namespace tq2

@@ -140,6 +140,10 @@ void boxes(int from, int keys, int rows, int first, int last, int *out) {
     const BoxRange r = boxes_of(from, keys, rows, first, last);
     out[0] = r.lo, out[1] = r.hi;
 }
+void tiles(int n, int kv, long long window, int causal, int keys, int split, int *out) {
+    const TileSpan t = tiles_of(SeqSpan{0, n, kv}, window, causal, keys, split);
+    out[0] = t.tile0, out[1] = t.tiles, out[2] = t.units;
+}
 int past(int n, int kv, int group, int rows, int tiles, int causal, long long x) {
     return tiles_past(SeqSpan{0, n, kv}, group, rows, tiles, causal, x);
 }
@@ -223,6 +227,21 @@ def test_boxes_of_a_tile(index):
         want = [i for i in range(keys // rows)
                 if any(first <= k < last for k in range(start + i * rows, start + (i + 1) * rows))]
         assert list(range(out[0], out[1])) == want
+
+
+def test_tiles_of_a_span(index):
+    rng = np.random.default_rng(7)
+    for _ in range(2000):
+        n, kv, window = int(rng.integers(0, 40)), int(rng.integers(0, 600)), int(rng.choice([0, 1, 5, 64, 65, 300, 10 ** 9]))
+        for causal in (0, 1):
+            seen = sorted({j for i in range(n) for j in range(kv)
+                           if (j <= kv - n + i or not causal) and (j > kv - n + i - window or not window)})
+            for split in (0, 1):
+                out = (ctypes.c_int * 3)()
+                index.tiles(n, kv, ctypes.c_longlong(window), causal, 64, split, out)
+                want = sorted({j // 64 for j in seen})
+                assert out[1] == len(want) and (not want or out[0] == want[0])
+                assert out[2] == (0 if n == 0 else max(1, len(want)) if split else 1)
 
 
 def test_tiles_past_a_key(index):
