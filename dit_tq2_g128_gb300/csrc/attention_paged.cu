@@ -118,17 +118,16 @@ struct RowPlan {
 __device__ __forceinline__ void find_run(const PagedArgs &a, const RowPlan &plan, RowCtl *ctl, int *__restrict__ starts,
                                          unsigned int *status) {
     const int lane = threadIdx.x & 31;
-    int total = 0;
-    for (int base = 0; base < a.batch.seqs; base += 32) {
-        const int b = base + lane;
-        int units = 0;
-        if (b < a.batch.seqs) {
-            bool bad = false;
-            units = tiles_of(seq_span(a.batch, b, bad), a.window, a.causal, kKeys, plan.split).units * a.kv_heads;
-            report_bad(bad, status);
-        }
-        total += int(__reduce_add_sync(0xffffffffu, unsigned(units)));
-    }
+    auto units_of = [&](int b) {  // of one key head
+        bool bad = false;
+        const int n = b < a.batch.seqs ? tiles_of(seq_span(a.batch, b, bad), a.window, a.causal, kKeys, plan.split).units : 0;
+        report_bad(bad, status);
+        return n;
+    };
+    const int head = units_of(lane);
+    int total = int(__reduce_add_sync(0xffffffffu, unsigned(head))) * a.kv_heads;
+    for (int base = 32; base < a.batch.seqs; base += 32)
+        total += int(__reduce_add_sync(0xffffffffu, unsigned(units_of(base + lane)))) * a.kv_heads;
     const int ctas = int(gridDim.x), least = plan.split ? kMinTiles : 1;
     const int share = max(least, (total + ctas - 1) / ctas);
     const bool write = blockIdx.x == 0 && starts != nullptr;
@@ -141,12 +140,7 @@ __device__ __forceinline__ void find_run(const PagedArgs &a, const RowPlan &plan
     if (from >= total && !write) return;
     for (int base = 0; base < a.batch.seqs; base += 32) {
         const int b = base + lane;
-        int per = 0, units = 0;
-        if (b < a.batch.seqs) {
-            bool ignore = false;
-            per = tiles_of(seq_span(a.batch, b, ignore), a.window, a.causal, kKeys, plan.split).units;
-            units = per * a.kv_heads;
-        }
+        const int per = base == 0 ? head : units_of(b), units = per * a.kv_heads;
         int upto = units;  // inclusive over the lanes
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -528,15 +522,16 @@ template <typename TO>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 rows_join_kernel(const PagedArgs a, const RowPlan plan, const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
                  const int *__restrict__ starts) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // before the wait: the tables (see paged_join_kernel)
     const int64_t t = blockIdx.x;
     const int h = blockIdx.y, G = a.heads / a.kv_heads;
     const int b = seq_of(a.batch, t);
-    if (b < 0) return;
     bool ignore = false;
-    const SeqSpan sp = seq_span(a.batch, b, ignore);  // (reported by the launch before)
+    const SeqSpan sp = b < 0 ? SeqSpan{0, 0, 0} : seq_span(a.batch, b, ignore);  // (reported by the launch before)
+    const int units = tiles_of(sp, a.window, a.causal, kKeys, true).units;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
-    const int share = starts[a.batch.seqs], units = tiles_of(sp, a.window, a.causal, kKeys, true).units;
+    const int share = starts[a.batch.seqs];
     const int from = starts[b] + (h / G) * units, c0 = from / share, c1 = (from + units - 1) / share;
     if (c0 == c1) return;
     const int row = int(t - sp.q0) * G + h % G;

@@ -246,47 +246,71 @@ cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, int s
 constexpr int kJoinWarps = 4;
 
 // Joins `count` partial results of (new token t, head h), the i-th at index place(i):
-// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i, in order within each warp and
-// the warps' sums in their order after that.  Reads what the launch before wrote
-// (mostly from L2).  The whole block.
+// out = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i.  A warp takes every
+// kJoinWarps-th of them with a running maximum, four in flight, and the warps meet in
+// their order: the same bits on every call.  Reads what the launch before wrote (mostly
+// from L2).  The whole block.
 template <typename TO, typename F>
 __device__ __forceinline__ void join_partials(const PagedArgs &a, int64_t t, int h, int count, const float *__restrict__ part_o,
                                               const float2 *__restrict__ part_ml, F place, TO *out) {
-    __shared__ float sh_o[kJoinWarps][128], sh_l[kJoinWarps];
+    __shared__ float sh_o[kJoinWarps][128], sh_m[kJoinWarps], sh_l[kJoinWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float top = -INFINITY;
-    for (int c = lane; c < count; c += 32) top = fmaxf(top, part_ml[place(c)].x);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
     const bool mine = 4 * lane < a.dim;
-#pragma unroll 4
-    for (int c = warp; c < count; c += kJoinWarps) {
-        const int64_t at = place(c);
-        const float2 ml = part_ml[at];
-        const float f = ml.x == top ? 1.f : fast_ex2(ml.x - top);
-        l = fmaf(f, ml.y, l);
-        if (mine) {
-            const float4 x = *reinterpret_cast<const float4 *>(part_o + at * a.dim + 4 * lane);
+    float top = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c0 = warp; c0 < count; c0 += 4 * kJoinWarps) {
+        float2 ml[4];
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = c0 + i * kJoinWarps;
+            ml[i] = make_float2(-INFINITY, 0.f);
+            x[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (c < count) {
+                const int64_t at = place(c);
+                ml[i] = part_ml[at];
+                if (mine) x[i] = *reinterpret_cast<const float4 *>(part_o + at * a.dim + 4 * lane);
+            }
+        }
+        const float next = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), top);
+        const float keep = top == next ? 1.f : fast_ex2(top - next);
+        l *= keep;
+        o.x *= keep;
+        o.y *= keep;
+        o.z *= keep;
+        o.w *= keep;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float f = ml[i].x == next ? 1.f : fast_ex2(ml[i].x - next);
+            l = fmaf(f, ml[i].y, l);
+            o.x = fmaf(f, x[i].x, o.x);
+            o.y = fmaf(f, x[i].y, o.y);
+            o.z = fmaf(f, x[i].z, o.z);
+            o.w = fmaf(f, x[i].w, o.w);
+        }
+        top = next;
+    }
+    if (mine) *reinterpret_cast<float4 *>(&sh_o[warp][4 * lane]) = o;
+    if (lane == 0) {
+        sh_m[warp] = top;
+        sh_l[warp] = l;
+    }
+    __syncthreads();
+    if (warp == 0 && mine) {
+        float all = sh_m[0];
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) all = fmaxf(all, sh_m[w]);
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) {
+            const float f = sh_m[w] == all ? 1.f : fast_ex2(sh_m[w] - all);
+            const float4 x = *reinterpret_cast<const float4 *>(&sh_o[w][4 * lane]);
             o.x = fmaf(f, x.x, o.x);
             o.y = fmaf(f, x.y, o.y);
             o.z = fmaf(f, x.z, o.z);
             o.w = fmaf(f, x.w, o.w);
-        }
-    }
-    if (mine) *reinterpret_cast<float4 *>(&sh_o[warp][4 * lane]) = o;
-    if (lane == 0) sh_l[warp] = l;
-    __syncthreads();
-    if (warp == 0 && mine) {
-#pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) {
-            const float4 x = *reinterpret_cast<const float4 *>(&sh_o[w][4 * lane]);
-            o.x += x.x;
-            o.y += x.y;
-            o.z += x.z;
-            o.w += x.w;
-            l += sh_l[w];
+            l = fmaf(f, sh_l[w], l);
         }
         const float inv = l == 0.f ? 0.f : 1.f / l;
         store4(out + t * a.out_token + int64_t(h) * a.out_head + 4 * lane, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
@@ -298,13 +322,14 @@ template <typename TO>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 paged_join_kernel(const PagedArgs a, const KeyPlan plan, const float *__restrict__ part_o,
                   const float2 *__restrict__ part_ml) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Before the wait: the tables.  (This block runs only once every block of the launch before has passed its own wait,
+    // so whatever wrote the tables has ended.)
     const int64_t t = blockIdx.x;
     const int h = blockIdx.y;
     const int b = seq_of(a.batch, t);
-    if (b < 0) return;
     bool bad = false;
-    const SeqSpan sp = seq_span(a.batch, b, bad);  // (reported by the launch before)
+    const SeqSpan sp = b < 0 ? SeqSpan{0, 0, 0} : seq_span(a.batch, b, bad);  // (reported by the launch before)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
     const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
     if (cut.chunks <= 1) return;
