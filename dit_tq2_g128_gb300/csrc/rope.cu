@@ -6,7 +6,8 @@
 // 64-bit integers: phase = position * turns mod 2^64 is exact whatever the
 // position, and only the nearest quarter turn's remainder (32 bits of it) is
 // rounded to f32, at most an eighth of a turn with 24 bits: 2^-25 of a radian or
-// so, the rounding of the f32 sine itself.
+// so, the rounding of the f32 sine itself.  (Its own short series: with the library's
+// sine the 16-bit forms were bound by instructions, 15 an element.)
 //
 // Bound by memory (each element read once and written once).  A thread owns one
 // unit (VP pairs) of one token: it forms the unit's sines once and turns it in up
@@ -27,37 +28,95 @@ struct alignas(sizeof(T) * VP) Pack {
     T e[VP];
 };
 
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ void from_f32(float x, float &y) { y = x; }
-__device__ __forceinline__ void from_f32(float x, __half &y) { y = __float2half_rn(x); }
-__device__ __forceinline__ void from_f32(float x, __nv_bfloat16 &y) { y = __float2bfloat16_rn(x); }
-
-template <typename T, int VP>
-__device__ __forceinline__ void store_pack(T *p, const float (&x)[VP]) {
-    Pack<T, VP> v;
+// The pack's elements in f32, and back with one rounding each, two at a time where
+// there are two (a conversion instruction makes a pair).
+template <int VP>
+__device__ __forceinline__ void unpack(const Pack<float, VP> &v, float (&x)[VP]) {
 #pragma unroll
-    for (int i = 0; i < VP; ++i) from_f32(x[i], v.e[i]);
-    *reinterpret_cast<Pack<T, VP> *>(p) = v;
+    for (int i = 0; i < VP; ++i) x[i] = v.e[i];
+}
+template <int VP>
+__device__ __forceinline__ void unpack(const Pack<__half, VP> &v, float (&x)[VP]) {
+    if constexpr (VP == 1) {
+        x[0] = __half2float(v.e[0]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VP; i += 2) {
+            const float2 f = __half22float2(__halves2half2(v.e[i], v.e[i + 1]));
+            x[i] = f.x;
+            x[i + 1] = f.y;
+        }
+    }
+}
+template <int VP>
+__device__ __forceinline__ void unpack(const Pack<__nv_bfloat16, VP> &v, float (&x)[VP]) {
+    if constexpr (VP == 1) {
+        x[0] = __bfloat162float(v.e[0]);
+    } else {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(&v);
+#pragma unroll
+        for (int i = 0; i < VP; i += 2) {
+            x[i] = __uint_as_float(w[i / 2] << 16);
+            x[i + 1] = __uint_as_float(w[i / 2] & 0xffff0000u);
+        }
+    }
+}
+template <int VP>
+__device__ __forceinline__ void store_pack(float *p, const float (&x)[VP]) {
+    Pack<float, VP> v;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) v.e[i] = x[i];
+    *reinterpret_cast<Pack<float, VP> *>(p) = v;
+}
+template <int VP>
+__device__ __forceinline__ void store_pack(__half *p, const float (&x)[VP]) {
+    if constexpr (VP == 1) {
+        *p = __float2half_rn(x[0]);
+    } else {
+        Pack<__half2, VP / 2> v;
+#pragma unroll
+        for (int i = 0; i < VP; i += 2) v.e[i / 2] = __floats2half2_rn(x[i], x[i + 1]);
+        *reinterpret_cast<Pack<__half2, VP / 2> *>(p) = v;
+    }
+}
+template <int VP>
+__device__ __forceinline__ void store_pack(__nv_bfloat16 *p, const float (&x)[VP]) {
+    if constexpr (VP == 1) {
+        *p = __float2bfloat16_rn(x[0]);
+    } else {
+        Pack<__nv_bfloat162, VP / 2> v;
+#pragma unroll
+        for (int i = 0; i < VP; i += 2) v.e[i / 2] = __floats2bfloat162_rn(x[i], x[i + 1]);
+        *reinterpret_cast<Pack<__nv_bfloat162, VP / 2> *>(p) = v;
+    }
 }
 
-// sine and cosine of 2 pi phase / 2^64
+// Sine and cosine of 2 pi phase / 2^64.  After the nearest quarter turn is taken off
+// as an integer the angle x is within pi/4, where the series to x^9 and x^10 are off
+// by at most x^11/11! = 2e-9 and x^12/12! = 2e-10: f32 rounding decides.
 __device__ __forceinline__ void turn_sincos(uint64_t phase, float &sn, float &cs) {
     const uint64_t quarter = (phase + (uint64_t(1) << 61)) >> 62;
     const int64_t rest = int64_t(phase - (quarter << 62));  // [-2^61, 2^61): an eighth of a turn each way
-    float s, c;
-    sincospif(float(int32_t(rest >> 30)) * 0x1p-33f, &s, &c);
-    const bool swap = quarter & 1, neg_s = quarter & 2, neg_c = ((quarter + 1) & 2) != 0;
-    sn = swap ? c : s;
-    cs = swap ? s : c;
-    if (neg_s) sn = -sn;
-    if (neg_c) cs = -cs;
+    const float x = float(int32_t(rest >> 30)) * (6.28318530717958648f * 0x1p-34f), z = x * x;
+    const float s = fmaf(x * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f), x);
+    const float c = fmaf(z, fmaf(z, fmaf(z, fmaf(z, fmaf(z, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f), -0.5f), 1.f);
+    const uint32_t q = uint32_t(quarter);
+    const bool swap = q & 1;
+    // sine's sign is the second bit of q, cosine's that of q + 1
+    sn = __uint_as_float(__float_as_uint(swap ? c : s) ^ ((q & 2) << 30));
+    cs = __uint_as_float(__float_as_uint(swap ? s : c) ^ (((q + 1) & 2) << 30));
+}
+
+// (a, b) times cos + i sin
+__device__ __forceinline__ void turn(float &a, float &b, float cs, float sn) {
+    const float x = a;
+    a = fmaf(x, cs, -b * sn);
+    b = fmaf(x, sn, b * cs);
 }
 
 // grid: x = tokens * units / threads, y = head groups of all segments
 template <typename TI, typename TO, int VP>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 4)
 rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
     const int64_t idx = int64_t(blockIdx.x) * kRopeThreads + threadIdx.x;
     int64_t t;
@@ -111,66 +170,61 @@ rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
         e1 = e0 + VP;
     }
     const bool has0 = e0 < a.dim, has1 = e1 < a.dim;  // (a scalar copy unit may end inside)
-    float sn[VP], cs[VP];
-    if (turned) {
-#pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            const int p = u * VP + i;
-            int64_t pos = key;
-            if (a.positions) {
-                const int ax = a.axis ? min(int(a.axis[p]), a.axes - 1) : 0;
-                pos = a.positions[t * a.axes + ax];
-            }
-            turn_sincos(uint64_t(pos) * a.turns[p], sn[i], cs[i]);
-            if (a.inverse) sn[i] = -sn[i];
-        }
-    }
     const TI *in = static_cast<const TI *>(g.in) + t * g.in_token;
     TO *out = static_cast<TO *>(g.out) + out_base;
     const int h0 = group * hpg, h1 = min(h0 + hpg, g.heads);
-    for (int h = h0; h < h1; h += 4) {
-        Pack<TI, VP> x[4], y[4];
+    constexpr int HF = sizeof(TI) * VP >= 16 ? 2 : 4;  // heads in flight
+    Pack<TI, VP> x[HF], y[HF];
+    auto load = [&](int h) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < HF; ++j)
             if (h + j < h1) {
                 const TI *p = in + int64_t(h + j) * g.in_head;
                 if (has0) x[j] = *reinterpret_cast<const Pack<TI, VP> *>(p + e0);
                 if (has1) y[j] = *reinterpret_cast<const Pack<TI, VP> *>(p + e1);
             }
+    };
+    load(h0);
+    float sn[VP], cs[VP];
+    if (turned) {
+        int64_t pos = a.positions ? 0 : key;
+        int axis = -1;
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int i = 0; i < VP; ++i) {
+            const int p = u * VP + i;
+            if (a.positions) {
+                const int ax = a.axis ? min(int(a.axis[p]), a.axes - 1) : 0;
+                if (ax != axis) pos = a.positions[t * a.axes + ax];
+                axis = ax;
+            }
+            turn_sincos(uint64_t(pos) * a.turns[p], sn[i], cs[i]);
+            if (a.inverse) sn[i] = -sn[i];
+        }
+    }
+#pragma unroll 1
+    for (int h = h0; h < h1; h += HF) {
+        if (h > h0) load(h);
+#pragma unroll
+        for (int j = 0; j < HF; ++j)
             if (h + j < h1) {
-                float f0[VP], f1[VP], r0[VP], r1[VP];
+                float r0[VP], r1[VP];
+                unpack(x[j], r0);
+                unpack(y[j], r1);
+                if (turned) {
+                    if (VP == 1 || !a.interleaved) {
 #pragma unroll
-                for (int i = 0; i < VP; ++i) {
-                    f0[i] = to_f32(x[j].e[i]);
-                    f1[i] = to_f32(y[j].e[i]);
-                }
-                if (!turned) {
+                        for (int i = 0; i < VP; ++i) turn(r0[i], r1[i], cs[i], sn[i]);
+                    } else {  // pairs lie inside each pack: angles 0 .. VP/2 - 1, then the rest
 #pragma unroll
-                    for (int i = 0; i < VP; ++i) {
-                        r0[i] = f0[i];
-                        r1[i] = f1[i];
-                    }
-                } else if (VP == 1 || !a.interleaved) {
-#pragma unroll
-                    for (int i = 0; i < VP; ++i) {
-                        r0[i] = fmaf(f0[i], cs[i], -f1[i] * sn[i]);
-                        r1[i] = fmaf(f0[i], sn[i], f1[i] * cs[i]);
-                    }
-                } else {  // pairs lie inside each pack: angles 0 .. VP/2 - 1, then the rest
-#pragma unroll
-                    for (int i = 0; i < VP / 2; ++i) {
-                        const float c0 = cs[i], s0 = sn[i], c1 = cs[VP / 2 + i], s1 = sn[VP / 2 + i];
-                        r0[2 * i] = fmaf(f0[2 * i], c0, -f0[2 * i + 1] * s0);
-                        r0[2 * i + 1] = fmaf(f0[2 * i], s0, f0[2 * i + 1] * c0);
-                        r1[2 * i] = fmaf(f1[2 * i], c1, -f1[2 * i + 1] * s1);
-                        r1[2 * i + 1] = fmaf(f1[2 * i], s1, f1[2 * i + 1] * c1);
+                        for (int i = 0; i < VP / 2; ++i) {
+                            turn(r0[2 * i], r0[2 * i + 1], cs[i], sn[i]);
+                            turn(r1[2 * i], r1[2 * i + 1], cs[VP / 2 + i], sn[VP / 2 + i]);
+                        }
                     }
                 }
                 TO *p = out + int64_t(h + j) * g.out_head;
-                if (has0) store_pack<TO, VP>(p + e0, r0);
-                if (has1) store_pack<TO, VP>(p + e1, r1);
+                if (has0) store_pack<VP>(p + e0, r0);
+                if (has1) store_pack<VP>(p + e1, r1);
             }
     }
 }
@@ -191,10 +245,10 @@ bool packs(const RopeArgs &a, int vp, int in_bytes, int out_bytes) {
 template <typename TI, typename TO, int VP>
 cudaError_t launch_rope_vp(const RopeArgs &a, const LaunchCtx &ctx) {
     const int units = VP == 1 ? a.pairs + (a.dim - 2 * a.pairs + 1) / 2 : a.dim / (2 * VP);
-    // heads per thread: as many (up to 8, for the sines' sake) as leave every SM its threads
+    // heads per thread: as many (up to 16, for the sines' sake) as leave every SM its threads
     int all = 0;
     for (int s = 0; s < a.nseg; ++s) all += a.seg[s].heads;
-    int hpg = 8;
+    int hpg = 16;
     while (hpg > 1 && a.tokens * units * ((all + hpg - 1) / hpg) < int64_t(ctx.num_sms) * 2048) hpg >>= 1;
     int groups = 0;
     for (int s = 0; s < a.nseg; ++s) groups += (a.seg[s].heads + hpg - 1) / hpg;
