@@ -169,22 +169,25 @@ rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
         e0 = g.turned ? 2 * a.pairs + (u - ru) * 2 * VP : u * 2 * VP;
         e1 = e0 + VP;
     }
-    const bool has0 = e0 < a.dim, has1 = e1 < a.dim;  // (a scalar copy unit may end inside)
-    const TI *in = static_cast<const TI *>(g.in) + t * g.in_token;
-    TO *out = static_cast<TO *>(g.out) + out_base;
-    const int h0 = group * hpg, h1 = min(h0 + hpg, g.heads);
+    const bool has0 = VP > 1 || e0 < a.dim, has1 = VP > 1 || e1 < a.dim;  // (a scalar copy unit may end inside)
+    const int h0 = group * hpg, count = min(hpg, g.heads - h0);
+    const TI *in = static_cast<const TI *>(g.in) + t * g.in_token + int64_t(h0) * g.in_head + e0;
+    TO *out = static_cast<TO *>(g.out) + out_base + int64_t(h0) * g.out_head + e0;
+    const int64_t in_step = g.in_head, out_step = g.out_head;
+    const int gap = e1 - e0;
     constexpr int HF = sizeof(TI) * VP >= 16 ? 2 : 4;  // heads in flight
     Pack<TI, VP> x[HF], y[HF];
-    auto load = [&](int h) {
+    auto load = [&](int left) {  // the next heads, `in` past them
 #pragma unroll
-        for (int j = 0; j < HF; ++j)
-            if (h + j < h1) {
-                const TI *p = in + int64_t(h + j) * g.in_head;
-                if (has0) x[j] = *reinterpret_cast<const Pack<TI, VP> *>(p + e0);
-                if (has1) y[j] = *reinterpret_cast<const Pack<TI, VP> *>(p + e1);
+        for (int j = 0; j < HF; ++j) {
+            if (j < left) {
+                if (has0) x[j] = *reinterpret_cast<const Pack<TI, VP> *>(in);
+                if (has1) y[j] = *reinterpret_cast<const Pack<TI, VP> *>(in + gap);
             }
+            in += in_step;
+        }
     };
-    load(h0);
+    load(count);
     float sn[VP], cs[VP];
     if (turned) {
         int64_t pos = a.positions ? 0 : key;
@@ -202,11 +205,11 @@ rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
         }
     }
 #pragma unroll 1
-    for (int h = h0; h < h1; h += HF) {
-        if (h > h0) load(h);
+    for (int left = count; left > 0; left -= HF) {
+        if (left < count) load(left);
 #pragma unroll
-        for (int j = 0; j < HF; ++j)
-            if (h + j < h1) {
+        for (int j = 0; j < HF; ++j) {
+            if (j < left) {
                 float r0[VP], r1[VP];
                 unpack(x[j], r0);
                 unpack(y[j], r1);
@@ -222,10 +225,11 @@ rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
                         }
                     }
                 }
-                TO *p = out + int64_t(h + j) * g.out_head;
-                if (has0) store_pack<VP>(p + e0, r0);
-                if (has1) store_pack<VP>(p + e1, r1);
+                if (has0) store_pack<VP>(out, r0);
+                if (has1) store_pack<VP>(out + gap, r1);
             }
+            out += out_step;
+        }
     }
 }
 
