@@ -781,7 +781,7 @@ int tq2_attention_paged(const tq2_heads *q, const tq2_heads *out, const tq2_kv_c
     if ((st = check_view(q, tokens, dim, false)) != TQ2_OK || (st = check_view(out, tokens, dim, true)) != TQ2_OK)
         return st;
     if (q->heads != out->heads || q->heads % cache->heads || q->dtype != cache->dtype ||
-        (out->dtype != cache->dtype && out->dtype != TQ2_F32) || tokens * (q->heads / cache->heads) > INT32_MAX)
+        (out->dtype != cache->dtype && out->dtype != TQ2_F32) || tokens * (q->heads / cache->heads) > INT32_MAX - 1024)
         return TQ2_ERR_INVALID_ARG;
     for (const tq2_heads *x : {q, out})
         if (!aligned16(x->data) || x->token_stride % 8 || x->head_stride % 8) return TQ2_ERR_MISALIGNED;

@@ -522,7 +522,8 @@ template <typename TO>
 __global__ void __launch_bounds__(32 * kJoinWarps)
 rows_join_kernel(const PagedArgs a, const RowPlan plan, const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
                  const int *__restrict__ starts) {
-    // before the wait: the tables (see paged_join_kernel)
+    // Before the wait: the tables.  (This block runs only once every block of the launch before has passed its own wait,
+    // so whatever wrote the tables has ended.)
     const int64_t t = blockIdx.x;
     const int h = blockIdx.y, G = a.heads / a.kv_heads;
     const int b = seq_of(a.batch, t);
@@ -595,7 +596,7 @@ cudaError_t launch_rows_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
 size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
                                 int64_t max_kv) {
     const int64_t rows = std::min(max_q, tokens) * (heads / kv_heads);
-    if (rows > kRowsMax) return partial_bytes(attention_paged_chunk_bound(heads, kv_heads, seqs, tokens, max_kv), tokens, heads, dim);
+    if (rows > kRowsMax) return attention_paged_chunk_ws_bytes(heads, kv_heads, dim, seqs, tokens, max_kv);
     const RowLaunch r = row_launch(kv_heads, seqs, rows, max_kv, 1);  // (a window only shortens the span)
     return r.plan.split ? row_ws_bytes(seqs, rows, dim, r.ctas) : 0;
 }

@@ -6,11 +6,17 @@
 // the group, row = token * G + head, so a 128-row tile of a chunk reads each key
 // for all G heads at once.
 //
-//  * A CTA owns up to 256 consecutive rows (two tiles) of one (sequence, key head)
-//    and a chunk of keys, in blocks of 128.  Warps 0 and 12 copy K and V through
-//    two-stage rings by paged tensor copies (boxes of rows inside one page); warps 1 and
-//    2 issue the MMAs of lane 0 and 1 (below); warp 3 looks after V; warps 4-7 and 8-11
-//    are the lanes' softmax groups, one thread per row (= tensor-memory lane).
+//  * Work is shared out evenly.  An item is up to 256 consecutive rows (two tiles) of
+//    one (sequence, key head); the items' blocks of 128 keys, in one line with the cost
+//    of an item's start and end, are cut into as many equal runs as there are SMs, and a
+//    CTA takes a run.  Pieces of a cut item go to the workspace and a second, dependent
+//    launch joins them in order.  A CTA starts once, copies ahead into its next item,
+//    and its next Q comes as soon as the last S that reads the old one has ended.  (One CTA
+//    an item and chunk spent 7 us of its own on each.)
+//  * Warps 0 and 12 copy K and V through two-stage rings by paged tensor copies (boxes
+//    of rows inside one page), warp 0 Q too; warps 1 and 2 issue the MMAs of lane 0 and
+//    1 (below); warp 3 looks after V; warps 4-7 and 8-11 are the lanes' softmax groups,
+//    one thread per row (= tensor-memory lane).
 //  * Lanes: with two tiles, lane w is tile w and walks every block; with one tile, lane
 //    w walks the blocks 2i + w, so one tile keeps both softmax groups busy as well (they
 //    meet at the end).  A lane walks in steps of 64 keys (half a block), each step with
@@ -47,8 +53,11 @@ constexpr int kBlock = 128;     // keys of a block (copies)
 constexpr int kStep = 64;       // keys of a step (MMAs, softmax)
 constexpr int kCtaRows = 2 * kRows;
 constexpr int kThreads = 416;
-constexpr int kMaxSplits = 64;
-constexpr int kMinBlocks = 4;   // blocks a chunk, at least
+constexpr int kStartUnits = 2;  // an item's start and end, in blocks, for the shares
+constexpr int kMinUnits = 4;    // units of a run, at least, where items may be cut
+constexpr int kWholeKeys = 512; // up to so many keys an item stays whole
+constexpr int kJoinRows = 4;    // rows of a warp of the join
+constexpr int kJoinParts = kCtaRows / (kJoinRows * kJoinWarps);  // its blocks per cut item
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr float kLazy = 8.f;    // log2 growth of the maximum that O is rescaled for
 constexpr int W_K = 0, W_MMA = 1, W_SOFT = 4, W_V = 12;  // W_MMA + lane; warp 3 looks after V
@@ -59,19 +68,20 @@ struct ChunkLayout {
     static constexpr int HALF = 128 * 128;            // 128 rows x 64 features, swizzled
     static constexpr int TILE = HALF * HALVES;        // Q tile, K block, V block
     static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + 2 * TILE;
-    static constexpr int OFF_CTL = OFF_V + 2 * TILE;
-    static constexpr int OFF_ML = OFF_CTL + 256;      // m, l of group 1 (one tile)
-    static constexpr int BYTES = OFF_ML + 2 * kRows * 4 + 1024;
-    static constexpr int MPAD = DP + 4;               // f32 row of the groups' exchange, over Q and K
-    static_assert(kRows * MPAD * 4 <= OFF_V, "the exchange reuses Q and K");
+    static constexpr int OFF_STAGE = OFF_V + 2 * TILE; // 4 KB a softmax warp, for rows on their way out
+    static constexpr int OFF_CTL = OFF_STAGE + 8 * 4096;
+    static constexpr int BYTES = OFF_CTL + 256 + 1024;
     static_assert(BYTES <= 232448, "shared memory budget");
 };
 
 struct ChunkCtl {
-    uint64_t q_ready, k_full[2], k_empty[2], v_full[2], v_ready[2], v_empty[2];
+    uint64_t q_ready, q_free, k_full[2], k_empty[2], v_full[2], v_ready[2], v_empty[2];
     uint64_t s_full[2][2], p_full[2][2], o_done[2], drain;  // [lane][step & 1]
+    uint64_t item_done[2];   // a lane's last P V of an item has ended
     uint32_t tmem_base;
-    int abort, poisoned;
+    int abort;
+    int poisoned[4];         // by item (of those with blocks, from 1 on) modulo 4: the last whose V had values taken out
+    int b, row0, g, u, left; // where this CTA's run begins: sequence, rows, key head, unit; its units
 };
 static_assert(sizeof(ChunkCtl) <= 256, "control block");
 
@@ -85,6 +95,17 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {
 __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t half) {
     return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(half >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+__device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // both softmax groups
+
+// 64 features of a tile's rows of Q: feature x, head, token
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int x, int head, int token, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem], A read from tensor memory (lane = row, column c =
@@ -158,42 +179,182 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     return r;
 }
 
-// The sequence and first row of CTA slot `slot`: sequences and their row tiles from
-// the last to the first (the last tiles of a causal prompt are the longest).  One
-// warp; false if the slot is past the last tile.
-__device__ __forceinline__ bool find_rows(const BatchView &bt, int G, int slot, int &b_out, int &row0, unsigned int *status) {
-    const int lane = threadIdx.x & 31;
-    for (int top = bt.seqs; top > 0; top -= 32) {
-        const int b = top - 1 - lane;
-        int tiles = 0;
-        if (b >= 0) {
+// How a call is shared out: the rows of a copy, whether items may be cut, and whether
+// Q's tiles are copied by tensor copies (the group divides a tile, the scale is not
+// negative).
+struct ChunkPlan {
+    int box_rows;
+    int split;
+    int q_copies;
+};
+
+// What a cut item's piece says to the join: sequence + 1 (0: no piece), first row, key
+// head, 1 if the item's last key is in it.
+using Piece = int4;
+
+__device__ __forceinline__ int tiles_in(const SeqSpan &sp, int G) { return int((int64_t(sp.n) * G + kCtaRows - 1) / kCtaRows); }
+
+__device__ __forceinline__ ItemSpan item_of(const PagedArgs &a, const SeqSpan &sp, int row0) {
+    return item_span(sp, a.heads / a.kv_heads, row0, kCtaRows, a.window, a.causal, kBlock);
+}
+
+// The run of this CTA (one warp): `left` units from unit u of item (b, row0, g) on.
+__device__ __forceinline__ void find_run(const PagedArgs &a, const ChunkPlan &plan, ChunkCtl *ctl, unsigned int *status) {
+    const BatchView &bt = a.batch;
+    const int lane = threadIdx.x & 31, G = a.heads / a.kv_heads;
+    auto weight = [&](const SeqSpan &sp, int tile) { return plan.split ? kStartUnits + max(1, item_of(a, sp, tile * kCtaRows).blocks) : 1; };
+    // units of sequences base + lane, of one key head
+    auto units_of = [&](int base) {
+        SeqSpan sp{0, 0, 0};
+        if (base + lane < bt.seqs) {
             bool bad = false;
-            const SeqSpan sp = seq_span(bt, b, bad);
+            sp = seq_span(bt, base + lane, bad);
             report_bad(bad, status);
-            tiles = int((int64_t(sp.n) * G + kCtaRows - 1) / kCtaRows);
         }
-        int upto = tiles;  // inclusive sums over the lanes
+        const int tiles = tiles_in(sp, G);
+        int units = 0;
+        if (__reduce_max_sync(0xffffffffu, unsigned(tiles)) <= 4) {
+            for (int t = 0; t < tiles; ++t) units += weight(sp, t);
+        } else {  // long prompts: a sequence's tiles over the lanes
+            for (int l = 0; l < 32 && base + l < bt.seqs; ++l) {
+                const SeqSpan x{__shfl_sync(0xffffffffu, sp.q0, l), __shfl_sync(0xffffffffu, sp.n, l), __shfl_sync(0xffffffffu, sp.kv, l)};
+                const int n = tiles_in(x, G);
+                int sum = 0;
+                for (int t = lane; t < n; t += 32) sum += weight(x, t);
+                sum = int(__reduce_add_sync(0xffffffffu, unsigned(sum)));
+                if (lane == l) units = sum;
+            }
+        }
+        return units;
+    };
+    const int head = units_of(0);
+    int total = int(__reduce_add_sync(0xffffffffu, unsigned(head))) * a.kv_heads;
+    for (int base = 32; base < bt.seqs; base += 32)
+        total += int(__reduce_add_sync(0xffffffffu, unsigned(units_of(base)))) * a.kv_heads;
+    const int ctas = int(gridDim.x), share = max(plan.split ? kMinUnits : 1, (total + ctas - 1) / ctas);
+    const int64_t start = int64_t(blockIdx.x) * share;
+    if (lane == 0) ctl->left = start < total ? int(min(int64_t(share), total - start)) : 0;
+    if (start >= total) return;
+    int from = int(start);  // units left to pass
+    for (int base = 0; base < bt.seqs; base += 32) {
+        const int units = (base == 0 ? head : units_of(base)) * a.kv_heads;
+        int upto = units;  // inclusive over the lanes
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, upto, d);
             if (lane >= d) upto += x;
         }
-        const unsigned hit = __ballot_sync(0xffffffffu, slot < upto);
-        if (hit) {
-            const int l = __ffs(hit) - 1;
-            b_out = top - 1 - l;
-            row0 = (__shfl_sync(0xffffffffu, upto, l) - 1 - slot) * kCtaRows;
-            return true;
+        const unsigned hit = __ballot_sync(0xffffffffu, from < upto);
+        if (!hit) {
+            from -= __shfl_sync(0xffffffffu, upto, 31);
+            continue;
         }
-        slot -= __shfl_sync(0xffffffffu, upto, 31);
+        const int l = __ffs(hit) - 1, b = base + l;
+        from -= __shfl_sync(0xffffffffu, upto - units, l);
+        bool ignore = false;
+        const SeqSpan sp = seq_span(bt, b, ignore);
+        const int tiles = tiles_in(sp, G);
+        for (int t0 = 0; t0 < tiles; t0 += 32) {
+            const int w = t0 + lane < tiles ? weight(sp, t0 + lane) : 0;
+            int sum = w * a.kv_heads;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, d);
+                if (lane >= d) sum += x;
+            }
+            const unsigned found = __ballot_sync(0xffffffffu, from < sum);
+            if (found) {
+                if (lane == __ffs(found) - 1) {
+                    const int at = from - (sum - w * a.kv_heads);
+                    ctl->b = b;
+                    ctl->row0 = (t0 + lane) * kCtaRows;
+                    ctl->g = at / w;
+                    ctl->u = at % w;
+                }
+                return;
+            }
+            from -= __shfl_sync(0xffffffffu, sum, 31);
+        }
+        return;
     }
-    return false;
 }
+
+// A CTA's run, item by item: every role walks it by itself (whole warps).
+struct ChunkWalk {
+    const PagedArgs &a;
+    const ChunkPlan &plan;
+    const int G;
+    int b, row0, g, u, left;
+    SeqSpan sp;
+    ItemSpan it;
+    int units, take;
+    // the current item's part: rows, lanes' tiles, blocks from block0 on, keys [first, last)
+    int rows, nt, block0, nb, first, last;
+
+    __device__ __forceinline__ ChunkWalk(const PagedArgs &args, const ChunkPlan &p, const ChunkCtl *ctl)
+        : a(args), plan(p), G(args.heads / args.kv_heads), b(uniform(ctl->b)), row0(uniform(ctl->row0)), g(uniform(ctl->g)),
+          u(uniform(ctl->u)), left(uniform(ctl->left)) {
+        if (left > 0) {
+            load();
+            tile();
+        }
+    }
+    __device__ __forceinline__ void load() {
+        bool ignore = false;
+        const SeqSpan s = seq_span(a.batch, b, ignore);  // (reported by find_run)
+        sp = SeqSpan{uniform(s.q0), uniform(s.n), uniform(s.kv)};
+    }
+    __device__ __forceinline__ void tile() {
+        it = item_of(a, sp, row0);
+        units = plan.split ? kStartUnits + max(1, it.blocks) : 1;
+    }
+    __device__ __forceinline__ bool more() {
+        if (left <= 0) return false;
+        take = min(left, units - u);
+        // unit kStartUnits + k is block k
+        const int k0 = plan.split ? max(0, u - kStartUnits) : 0;
+        const int k1 = plan.split ? min(it.blocks, max(0, u + take - kStartUnits)) : it.blocks;
+        rows = it.rows;
+        nt = rows > kRows ? 2 : 1;
+        block0 = it.block0 + k0;
+        nb = max(0, k1 - k0);
+        first = max(it.see.lo, block0 * kBlock);
+        last = min(it.see.hi, (block0 + nb) * kBlock);
+        return true;
+    }
+    __device__ __forceinline__ bool begins() const { return u <= kStartUnits; }  // its first block (and something of it)
+    __device__ __forceinline__ bool whole() const { return nb == it.blocks; }
+    // nothing of this item falls to this run (only a part of its start does)
+    __device__ __forceinline__ bool skip() const { return nb == 0 && !(it.blocks == 0 && u + take == units); }
+    // where a cut item's piece goes: a run's first piece, begun by the run before, or its last
+    __device__ __forceinline__ int slot() const { return 2 * int(blockIdx.x) + begins(); }
+    __device__ __forceinline__ int steps(int w) const { return nt == 2 ? 2 * nb : 2 * ((nb + 1 - w) >> 1); }
+    // step s of lane w is half s & 1 of block:
+    __device__ __forceinline__ int block(int w, int s) const { return nt == 2 ? s >> 1 : (s & ~1) + w; }
+    __device__ __forceinline__ void next() {
+        left -= take;
+        u += take;
+        if (u < units) return;
+        u = 0;
+        if (++g < a.kv_heads || left <= 0) return;
+        g = 0;
+        row0 += kCtaRows;
+        if (int64_t(row0) >= int64_t(sp.n) * G) {
+            row0 = 0;
+            while (++b < a.batch.seqs) {
+                load();
+                if (sp.n > 0) break;
+            }
+        }
+        tile();
+    }
+};
 
 template <typename T, typename TO, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
-paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, const PagedArgs a,
-                   const KeyPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml, unsigned int *status,
+paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap qmap, const PagedArgs a, const ChunkPlan plan,
+                   float *__restrict__ part_o, float2 *__restrict__ part_ml, Piece *__restrict__ pieces, unsigned int *status,
                    uint64_t wait_ns) {
     using L = ChunkLayout<DP>;
     constexpr bool SPLIT_P = sizeof(TO) == 4;
@@ -203,11 +364,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     ChunkCtl *ctl = reinterpret_cast<ChunkCtl *>(smem + L::OFF_CTL);
     volatile int *abort_flag = &ctl->abort;
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
+    const int G = a.heads / a.kv_heads;
     const uint32_t sQ = base, sK = base + L::OFF_K, sV = base + L::OFF_V;
 
     // set-up that touches no memory of the launch before: barriers and tensor memory
     if (threadIdx.x == 0) {
-        mbar_init(&ctl->q_ready, 2 * kRows);
+        mbar_init(&ctl->q_ready, 1);
+        mbar_init(&ctl->q_free, 2);
         for (int s = 0; s < 2; ++s) {
             mbar_init(&ctl->k_full[s], 1);
             mbar_init(&ctl->k_empty[s], 2);  // both lanes (one tile: its block's lane, twice)
@@ -219,10 +382,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 mbar_init(&ctl->p_full[s][h], kRows / 32);
             }
             mbar_init(&ctl->o_done[s], 1);
+            mbar_init(&ctl->item_done[s], 1);
         }
         mbar_init(&ctl->drain, 2);
         ctl->abort = 0;
-        ctl->poisoned = 0;
+        for (int &p : ctl->poisoned) p = 0;
         fence_mbarrier_init();
         fence_proxy_async_smem();
     }
@@ -233,158 +397,204 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     // the tables, q and the cache may be written by the kernel before this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // slot = tile * kv_heads * chunks + head * chunks + chunk: a tile's heads and chunks run together
-    const unsigned per = unsigned(a.kv_heads) * unsigned(plan.chunks);
-    const int slot = int(blockIdx.x / per), g = int(blockIdx.x % per) / plan.chunks, chunk = int(blockIdx.x % per) % plan.chunks;
-    const int G = a.heads / a.kv_heads;
-    int b = 0, row0 = 0;
-    bool bad = false;
-    const bool found = find_rows(a.batch, G, slot, b, row0, status);
-    const SeqSpan sp = found ? seq_span(a.batch, b, bad) : SeqSpan{0, 0, 0};
-    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
-    const int rows = min(kCtaRows, int(int64_t(sp.n) * G - row0));
-    const RowSpan rs = rows > 0 ? rows_see(sp, row0 / G, (row0 + rows - 1) / G, a.window, a.causal) : RowSpan{0, 0, 0, 0};
-    const bool whole = cut.chunks <= 1;
-    const int64_t k0 = cut.base + int64_t(chunk) * plan.chunk;
-    const int first = int(k0 > rs.lo ? k0 : rs.lo);                                      // keys [first, last)
-    const int last = int(k0 + plan.chunk < rs.hi ? k0 + plan.chunk : int64_t(rs.hi));
-    const bool none = cut.chunks == 0 || last <= first;
-    const bool idle = !found || (none && !(whole && chunk == 0));  // (CTA-uniform: nothing to write)
-    const int block0 = first / kBlock, nb = none || idle ? 0 : (last + kBlock - 1) / kBlock - block0;
-    const int nt = rows > kRows ? 2 : 1;
-    // lane w: steps 0 .. steps_of(w) - 1; step u is half u & 1 of block block_of(w, u)
-    auto steps_of = [&](int w) { return nt == 2 ? 2 * nb : 2 * ((nb + 1 - w) >> 1); };
-    auto block_of = [&](int w, int u) { return nt == 2 ? u >> 1 : (u & ~1) + w; };
-
+    if (warp == 0) {
+        find_run(a, plan, ctl, status);
+        if (lane < 2 && pieces) pieces[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
+    }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(ctl->tmem_base)));
-    if (idle) {
-        if (warp == W_MMA) tmem_dealloc(tmem, kTmemCols);
-        return;
-    }
+    ChunkWalk walk(a, plan, ctl);
+    // Counters that run on over the items: blocks copied (slot = parity), this lane's steps (even an item), and the
+    // items that have blocks (Q's phases).
+    int blocks = 0, qi = 0;
 
     if (warp == W_K || warp == W_V) {
-        // ---- copies of one plane (a warp each: K's slots and V's are freed at different times)
+        // ---- copies of one plane (a warp each: K's slots and V's are freed at different times), and Q by K's warp
         const bool v = warp == W_V;
         const CUtensorMap *map = v ? &vmap : &kmap;
         uint64_t *const full = v ? ctl->v_full : ctl->k_full, *const empty = v ? ctl->v_empty : ctl->k_empty;
-        const int nb_u = uniform(nb), g_u = uniform(g);
-        BoxPages boxes(a, b, block0 * kBlock, kBlock, plan.box_rows, first, last);
-        int issued = 0;
-        for (; issued < nb_u; ++issued) {
-            const int s = issued & 1, u = issued >> 1;
-            boxes.seek(issued);
-            if (u > 0 && !__all_sync(0xffffffffu, wait_phase(&empty[s], (u - 1) & 1, abort_flag, wait_ns, status))) break;
-            const uint32_t dst = (v ? sV : sK) + uint32_t(s * L::TILE);
-            const BoxRange br = boxes.range(issued);
-            if (lane == 0) mbar_expect_tx(&full[s], uint32_t((br.hi - br.lo) * boxes.rows * 128 * L::HALVES));
-            __syncwarp();
-            boxes.each(issued, br, bad, [&](int row, int slot_in, int page) {
+        bool bad = false, ok = true;
+        for (; ok && walk.more(); walk.next()) {
+            if (walk.nb == 0) continue;
+            const int nb = walk.nb, g = walk.g;
+            if (!v && plan.q_copies) {
+                if (qi > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->q_free, (qi - 1) & 1, abort_flag, wait_ns, status));
+                if (!ok) break;
+                if (elect_one()) {
+                    mbar_expect_tx(&ctl->q_ready, uint32_t(walk.nt * L::TILE));
+                    for (int t = 0; t < walk.nt; ++t)
 #pragma unroll
-                for (int h = 0; h < L::HALVES; ++h)
-                    tma_cache(dst + uint32_t(h * L::HALF + row * 128), map, 64 * h, g_u, slot_in, page, &full[s]);
-            });
+                        for (int h = 0; h < L::HALVES; ++h)
+                            tma_rows(sQ + uint32_t(t * L::TILE + h * L::HALF), &qmap, 64 * h, g * G,
+                                     walk.sp.q0 + (walk.row0 + t * kRows) / G, &ctl->q_ready);
+                }
+                __syncwarp();
+            }
+            ++qi;
+            BoxPages boxes(a, walk.b, walk.block0 * kBlock, kBlock, plan.box_rows, walk.first, walk.last);
+            for (int j = 0; j < nb; ++j, ++blocks) {
+                const int s = blocks & 1, u = blocks >> 1;
+                boxes.seek(j);
+                if (u > 0) ok = __all_sync(0xffffffffu, wait_phase(&empty[s], (u - 1) & 1, abort_flag, wait_ns, status));
+                if (!ok) break;
+                const uint32_t dst = (v ? sV : sK) + uint32_t(s * L::TILE);
+                const BoxRange br = boxes.range(j);
+                if (lane == 0) mbar_expect_tx(&full[s], uint32_t((br.hi - br.lo) * boxes.rows * 128 * L::HALVES));
+                __syncwarp();
+                boxes.each(j, br, bad, [&](int row, int slot_in, int page) {
+#pragma unroll
+                    for (int h = 0; h < L::HALVES; ++h)
+                        tma_cache(dst + uint32_t(h * L::HALF + row * 128), map, 64 * h, g, slot_in, page, &full[s]);
+                });
+            }
         }
         report_bad(bad, status);
         // every copy issued must land before the CTA exits
-        if (lane == 0)
-            for (int j = max(0, issued - 2); j < issued; ++j)
+        if (lane == 0) {
+            for (int j = max(0, blocks - 2); j < blocks; ++j)
                 mbar_wait_bounded(&full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
+            if (!v && plan.q_copies && qi > 0) mbar_wait_bounded(&ctl->q_ready, (qi - 1) & 1, drain_ns(wait_ns), status);
+        }
         __syncwarp();
     } else if (warp == W_MMA || warp == W_MMA + 1) {
         // ---- MMAs of lane w, by one thread
         const int w = warp - W_MMA;
         constexpr uint32_t type = is_half<T> ? 0u : (1u << 7) | (1u << 10);
-        const int nb_u = uniform(nb), nt_u = uniform(nt), nd = uniform((a.dim + 15) / 16);  // nd: 16-feature steps that hold anything
+        const int nd = uniform((a.dim + 15) / 16);  // 16-feature steps that hold anything
         const uint32_t idesc_s = (1u << 4) | type | (uint32_t(kStep >> 3) << 17) | (uint32_t(kRows >> 4) << 24);
         const uint32_t idesc_o = (1u << 4) | type | (1u << 16) | (uint32_t(nd * 2) << 17) | (uint32_t(kRows >> 4) << 24);
         auto wait_on = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, wait_ns, status); };
-        const int steps = nt_u == 2 ? 2 * nb_u : 2 * ((nb_u + 1 - w) >> 1);
-        auto block_u = [&](int u) { return nt_u == 2 ? u >> 1 : (u & ~1) + w; };
         // uniform values and an elected lane: with values that the compiler takes for divergent, an MMA's issue took 100
         // cycles instead of the 48 (N = 64) or 64 that it runs for; offsets never carry out of a descriptor's address field
-        const uint64_t dq = desc_k(sQ + uint32_t(nt_u == 2 ? w * L::TILE : 0));
         const uint64_t dk[2] = {desc_k(sK), desc_k(sK + L::TILE)};
         const uint64_t dv[2] = {desc_mn(sV, L::HALF), desc_mn(sV + L::TILE, L::HALF)};
         const uint32_t t_s = tmem + uint32_t(w * 128), t_o = tmem + kOCol + uint32_t(w * 128);
-        auto issue_s = [&](int u) -> bool {
-            const int j = block_u(u);
-            if (!(u & 1) && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
-            tc_fence_after();
-            const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t((u & 1) * (kStep * 128 >> 4));
-#pragma unroll
-            for (int kk = 0; kk < DP / 16; ++kk) {
-                const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
-                if (kk < nd) tc_mma_f16(t_s + uint32_t((u & 1) * 64), dq + off, db + off, idesc_s, kk > 0);
-            }
-            tc_commit(&ctl->s_full[w][u & 1]);
-            if (u & 1) {
-                tc_commit(&ctl->k_empty[j & 1]);
-                if (nt_u == 1) tc_commit(&ctl->k_empty[j & 1]);
-            }
-            return true;
-        };
-        if (elect_one()) {
-            bool ok = steps == 0 || wait_on(&ctl->q_ready, 0);
-            for (int u = 0; u < 2 && u < steps && ok; ++u) ok = issue_s(u);
-            for (int u = 0; u < steps && ok; ++u) {
-                const int j = block_u(u);
-                ok = ((u & 1) || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1)) && wait_on(&ctl->p_full[w][u & 1], (u >> 1) & 1);
-                if (!ok) break;
+        int done = 0;  // this lane's steps before the item
+        bool ok = true;
+        for (; ok && walk.more(); walk.next()) {
+            if (walk.nb == 0) continue;
+            const int nt = walk.nt, steps = walk.steps(w);
+            const uint64_t dq = desc_k(sQ + uint32_t(nt == 2 ? w * L::TILE : 0));
+            auto issue_s = [&](int u) -> bool {
+                const int j = blocks + walk.block(w, u), h = u & 1;
+                if (!h && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
                 tc_fence_after();
-                const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t((u & 1) * (kStep * 128 >> 4));
-                const uint32_t p = t_s + uint32_t((u & 1) * 64);
+                const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t(h * (kStep * 128 >> 4));
 #pragma unroll
-                for (int kk = 0; kk < kStep / 16; ++kk) {
-                    const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
-                    mma_ts(t_o, p + uint32_t(kk * 8), bk, idesc_o, kk > 0 ? 1u : uint32_t(u > 0));
-                    if constexpr (SPLIT_P) mma_ts(t_o, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
+                    if (kk < nd) tc_mma_f16(t_s + uint32_t(h * 64), dq + off, db + off, idesc_s, kk > 0);
                 }
-                tc_commit(&ctl->o_done[w]);
-                if (u & 1) {
-                    tc_commit(&ctl->v_empty[j & 1]);
-                    if (nt_u == 1) tc_commit(&ctl->v_empty[j & 1]);
+                tc_commit(&ctl->s_full[w][h]);
+                if (h) {
+                    tc_commit(&ctl->k_empty[j & 1]);
+                    if (nt == 1) tc_commit(&ctl->k_empty[j & 1]);
                 }
-                if (u + 2 < steps) ok = issue_s(u + 2);
-            }
-            tc_commit(&ctl->drain);  // when all of this thread's MMAs have ended
-        }
-        __syncwarp();
-    } else if (warp == W_SOFT - 1) {
-        // ---- V: slots that some row of the CTA must not multiply
-        for (int j = 0; j < nb; ++j) {
-            if (!__all_sync(0xffffffffu, wait_phase(&ctl->v_full[j & 1], (j >> 1) & 1, abort_flag, wait_ns, status))) break;
-            const int key0 = (block0 + j) * kBlock;
-            // rows [0, r0) and [r1, 128) of the block
-            const int r0 = min(kBlock, max(0, max(first, rs.lo_all) - key0)), r1 = max(r0, min(kBlock, min(last, rs.hi_all) - key0));
-            if (r0 > 0 || r1 < kBlock) {
-                uint8_t *v = smem + L::OFF_V + (j & 1) * L::TILE;
-                constexpr int CH = L::HALVES * 8;  // 16-byte pieces of a row
-                for (int i = lane; i < (r0 + kBlock - r1) * CH; i += 32) {
-                    const int x = i / CH, c = i % CH, r = x < r0 ? x : x - r0 + r1, key = key0 + r;
-                    uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * L::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-                    if (key < first || key >= last) {
-                        *p = make_uint4(0, 0, 0, 0);
-                    } else {
-                        uint4 w = *p;
-                        if (any_nonfinite<T>(w)) {
-                            take_nonfinite<T>(w, [](int, float) {});
-                            *p = w;
-                            ctl->poisoned = 1;  // (read behind the MMAs that follow v_ready)
-                        }
+                if (u == steps - 1) tc_commit(&ctl->q_free);
+                return true;
+            };
+            bool lane_ok = true;
+            if (elect_one()) {
+                lane_ok = wait_on(&ctl->q_ready, qi & 1);
+                if (steps == 0) tc_commit(&ctl->q_free);
+                for (int u = 0; u < 2 && u < steps && lane_ok; ++u) lane_ok = issue_s(u);
+                for (int u = 0; u < steps && lane_ok; ++u) {
+                    const int j = blocks + walk.block(w, u), h = u & 1;
+                    // (P first: its groups have then seen the whole item before end, so that V's parity, whose slot the other
+                    // lane may have used last, is read no earlier than one phase before)
+                    lane_ok = wait_on(&ctl->p_full[w][h], ((done + u) >> 1) & 1) && (h || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1));
+                    if (!lane_ok) break;
+                    tc_fence_after();
+                    const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t(h * (kStep * 128 >> 4));
+                    const uint32_t p = t_s + uint32_t(h * 64);
+#pragma unroll
+                    for (int kk = 0; kk < kStep / 16; ++kk) {
+                        const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
+                        mma_ts(t_o, p + uint32_t(kk * 8), bk, idesc_o, kk > 0 ? 1u : uint32_t(u > 0));
+                        if constexpr (SPLIT_P) mma_ts(t_o, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
                     }
+                    tc_commit(&ctl->o_done[w]);
+                    if (u == steps - 1) tc_commit(&ctl->item_done[w]);
+                    if (h) {
+                        tc_commit(&ctl->v_empty[j & 1]);
+                        if (nt == 1) tc_commit(&ctl->v_empty[j & 1]);
+                    }
+                    if (u + 2 < steps) lane_ok = issue_s(u + 2);
                 }
-                fence_proxy_async_smem();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl->v_ready[j & 1]);
+            ok = __all_sync(0xffffffffu, lane_ok);
+            blocks += walk.nb;
+            done += steps;
+            ++qi;
+        }
+        if (elect_one()) tc_commit(&ctl->drain);  // when all of this lane's MMAs have ended
+        __syncwarp();
+    } else if (warp == W_SOFT - 1) {
+        // ---- V: slots that some row of the item must not multiply
+        bool ok = true;
+        for (; ok && walk.more(); walk.next()) {
+            if (walk.nb == 0) continue;
+            ++qi;
+            const RowSpan rs = walk.it.see;
+            const int first = walk.first, last = walk.last;
+            for (int j = 0; j < walk.nb; ++j, ++blocks) {
+                const int slot = blocks & 1;
+                ok = __all_sync(0xffffffffu, wait_phase(&ctl->v_full[slot], (blocks >> 1) & 1, abort_flag, wait_ns, status));
+                if (!ok) break;
+                const int key0 = (walk.block0 + j) * kBlock;
+                // rows [0, r0) and [r1, 128) of the block
+                const int r0 = min(kBlock, max(0, max(first, rs.lo_all) - key0)), r1 = max(r0, min(kBlock, min(last, rs.hi_all) - key0));
+                if (r0 > 0 || r1 < kBlock) {
+                    uint8_t *v = smem + L::OFF_V + slot * L::TILE;
+                    constexpr int CH = L::HALVES * 8;  // 16-byte pieces of a row
+                    for (int i = lane; i < (r0 + kBlock - r1) * CH; i += 32) {
+                        const int x = i / CH, c = i % CH, r = x < r0 ? x : x - r0 + r1, key = key0 + r;
+                        uint4 *p = reinterpret_cast<uint4 *>(v + (c >> 3) * L::HALF + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+                        if (key < first || key >= last) {
+                            *p = make_uint4(0, 0, 0, 0);
+                        } else {
+                            uint4 w = *p;
+                            if (any_nonfinite<T>(w)) {
+                                take_nonfinite<T>(w, [](int, float) {});
+                                *p = w;
+                                ctl->poisoned[qi & 3] = qi;  // (read behind the MMAs that follow v_ready)
+                            }
+                        }
+                    }
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->v_ready[slot]);
+            }
         }
     } else {
-        // ---- softmax groups; first, both bring the rows of Q into the swizzled tiles
+        // ---- softmax groups.  After a wait that was given up a warp walks on without waiting or computing, so that every
+        // warp meets every barrier.
         const int w = (warp - W_SOFT) >> 2;
-        {
+        const uint32_t tl = uint32_t((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + tl + uint32_t(w * 128), to = tmem + tl + kOCol + uint32_t(w * 128);
+        const int r = (warp & 3) * 32 + lane;                        // row in the tile = TMEM lane
+        uint8_t *const stage = smem + L::OFF_STAGE + (warp - W_SOFT) * 4096;
+        // scores stay unscaled; scale2 > 0 enters with the exponential (a zero scale as a tiny one, so that -inf stays)
+        const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+        const uint64_t scale22 = pair(scale2, scale2);
+        int done = 0, ended = 0;  // this lane's steps, and its items with steps, before the item
+        bool ok = true;
+        for (; walk.more(); walk.next()) {
+        if (walk.skip()) continue;
+        const SeqSpan sp = walk.sp;
+        const RowSpan rs = walk.it.see;
+        const int b = walk.b, g = walk.g, row0 = walk.row0, rows = walk.rows, nt = walk.nt, nb = walk.nb, steps = walk.steps(w);
+        const int first = walk.first, last = walk.last;
+        const int row = (nt == 2 ? w * kRows : 0) + r;               // row of the item
+        const KeyRange kr = row < rows ? keys_of(sp, (row0 + row) / G, a.window, a.causal) : KeyRange{0, INT32_MAX};  // (rows past the end: never written)
+        const int lo = max(kr.lo, first), hi = min(kr.hi, last);
+        if (nb > 0 && !plan.q_copies) {
+            // both groups bring the rows of Q into the swizzled tiles, once no S of the item before reads them
+            if (ok && qi > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->q_free, (qi - 1) & 1, abort_flag, wait_ns, status));
             const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;  // a negative scale turns q's sign
             const T *q = static_cast<const T *>(a.q) + int64_t(sp.q0) * a.q_token;
             // a group brings its tile, or half of the only one; all of a thread's loads are in flight together
@@ -410,31 +620,22 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 #pragma unroll
             for (int k = 0; k < CH; ++k)
                 if (k < count) {
-                    const int r = r_first + k * STEP;
-                    *reinterpret_cast<uint4 *>(smem + (nt == 2 ? w * L::TILE : 0) + (c >> 3) * L::HALF + r * 128 +
-                                               (((c & 7) ^ (r & 7)) << 4)) =
+                    const int rr = r_first + k * STEP;
+                    *reinterpret_cast<uint4 *>(smem + (nt == 2 ? w * L::TILE : 0) + (c >> 3) * L::HALF + rr * 128 +
+                                               (((c & 7) ^ (rr & 7)) << 4)) =
                         make_uint4(x[k].x ^ flip, x[k].y ^ flip, x[k].z ^ flip, x[k].w ^ flip);
                 }
             fence_proxy_async_smem();
-            mbar_arrive(&ctl->q_ready);
+            groups_sync();
+            if (ok && threadIdx.x == 32 * W_SOFT) mbar_arrive(&ctl->q_ready);
         }
-        const int r = (warp & 3) * 32 + lane;                        // row in the tile = TMEM lane
-        const int row = (nt == 2 ? w * kRows : 0) + r;               // row of the CTA
-        const uint32_t tl = uint32_t((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + tl + uint32_t(w * 128), to = tmem + tl + kOCol + uint32_t(w * 128);
-        // scores stay unscaled; scale2 > 0 enters with the exponential (a zero scale as a tiny one, so that -inf stays)
-        const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-        const KeyRange kr = row < rows ? keys_of(sp, (row0 + row) / G, a.window, a.causal) : KeyRange{0, INT32_MAX};  // (rows past the end: never written)
-        const int lo = max(kr.lo, first), hi = min(kr.hi, last);
-        const uint64_t scale22 = pair(scale2, scale2);
+        if (nb > 0) ++qi;
         float m = -INFINITY, l = 0.f;
-        bool ok = true;
-        const int done = steps_of(w);
-        for (int u = 0; u < done; ++u) {
-            ok = __all_sync(0xffffffffu, wait_phase(&ctl->s_full[w][u & 1], (u >> 1) & 1, abort_flag, wait_ns, status));
+        for (int u = 0; u < steps && ok; ++u) {
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->s_full[w][u & 1], ((done + u) >> 1) & 1, abort_flag, wait_ns, status));
             if (!ok) break;
             tc_fence_after();
-            const int key0 = (block0 + block_of(w, u)) * kBlock + (u & 1) * kStep;
+            const int key0 = (walk.block0 + walk.block(w, u)) * kBlock + (u & 1) * kStep;
             const int from = lo - key0, upto = hi - key0;  // this row's keys of the step: [from, upto)
             uint32_t va[32], vb[32];
             tm_ld32(ts + uint32_t((u & 1) * 64), va);
@@ -479,7 +680,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             if constexpr (SPLIT_P) tm_st32(ts + uint32_t((u & 1) * 64 + 32), lp);
             if (u > 0 && __any_sync(0xffffffffu, grow)) {
                 // rescale this row of O (rows that keep m by 1) once the step before has accumulated into it
-                ok = __all_sync(0xffffffffu, wait_phase(&ctl->o_done[w], (u - 1) & 1, abort_flag, wait_ns, status));
+                ok = __all_sync(0xffffffffu, wait_phase(&ctl->o_done[w], (done + u - 1) & 1, abort_flag, wait_ns, status));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -501,46 +702,34 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             l = l * alpha + (s0 + s1);
             m = mu;
         }
-        if (ok && done > 0) {
-            // (a lane has an even number of steps; the last one's S told that P V up to step done - 3 has ended, and a
-            // parity tells a phase only from its neighbours)
-            ok = __all_sync(0xffffffffu, wait_phase(&ctl->o_done[w], (done - 2) & 1, abort_flag, wait_ns, status) &&
-                                             wait_phase(&ctl->o_done[w], (done - 1) & 1, abort_flag, wait_ns, status));
+        if (ok && steps > 0) {
+            // (a barrier of its own: P V of the last two steps may both have ended by now, and a parity tells a phase only
+            // from its neighbours)
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->item_done[w], ended & 1, abort_flag, wait_ns, status));
+            ++ended;
             tc_fence_after();
         }
-        // one tile: group 1's rows go to group 0 through shared memory (over Q and K, which no MMA reads any more:
-        // both groups have seen their last MMA end)
-        float *ex = reinterpret_cast<float *>(smem);
-        float *exm = reinterpret_cast<float *>(smem + L::OFF_ML), *exl = exm + kRows;
+        done += steps;
+        // one tile: the groups hold the softmax of the even and odd blocks of the same rows (and tensor-memory lanes);
+        // each learns the other's m and l, and they take the output's pieces in turn
         float scale_own = 1.f, scale_other = 0.f;
         if (nt == 1) {
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            ok = ok && *abort_flag == 0;
-            if (w == 1) {
-                exm[r] = m;
-                exl[r] = l;
-                if (ok && done > 0) {
-#pragma unroll 1
-                    for (int c = 0; c < (a.dim + 31) / 32; ++c) {
-                        uint32_t o[32];
-                        tm_ld32(to + uint32_t(c * 32), o);
-                        tm_wait_ld(o);
-#pragma unroll
-                        for (int i = 0; i < 32; i += 4)
-                            *reinterpret_cast<uint4 *>(&ex[r * L::MPAD + c * 32 + i]) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    }
-                }
-            }
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (w == 0 && nb > 1) {
-                const float mo = exm[r], top = fmaxf(m, mo);  // (m == top holds where both are -inf)
-                scale_own = m == top ? 1.f : fast_ex2((m - top) * scale2);
-                scale_other = mo == top ? 1.f : fast_ex2((mo - top) * scale2);
-                l = l * scale_own + exl[r] * scale_other;
-                m = top;
-            }
+            float2 *mine = reinterpret_cast<float2 *>(stage);
+            const float2 *other = reinterpret_cast<const float2 *>(smem + L::OFF_STAGE + (((warp - W_SOFT) + 4) & 7) * 4096);
+            tc_fence_before();
+            mine[lane] = make_float2(m, l);
+            groups_sync();
+            tc_fence_after();
+            const float2 x = other[lane];
+            groups_sync();
+            const float top = fmaxf(m, x.x);  // (m == top holds where both are -inf)
+            scale_own = m == top ? 1.f : fast_ex2((m - top) * scale2);
+            scale_other = x.x == top ? 1.f : fast_ex2((x.x - top) * scale2);
+            l = l * scale_own + x.y * scale_other;
+            m = top;
         }
-        auto to_cols = [&](int c) { return to + uint32_t(c * 32); };
+        const bool has_own = steps > 0, has_other = nt == 1 && walk.steps(1 - w) > 0;
+        const uint32_t to_other = tmem + tl + kOCol + uint32_t((1 - w) * 128);
         // values that are not finite, of keys that this row sees and another row of the CTA does not (columns 32 c ..)
         auto add_hidden = [&](int c, uint32_t (&o)[32]) {
             for (int key = lo; key < hi; ++key) {
@@ -563,19 +752,19 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
             }
         };
-        if (ok && (nt == 2 || w == 0)) {
-            const int64_t t = int64_t(sp.q0) + (row0 + row) / G;
-            const int h = g * G + (row0 + row) % G;
-            const bool mine = row < rows;
+        if (ok) {
+            const bool mine = row < rows, whole = walk.whole();
             const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;  // no key: zeros
-            if (!whole && mine) part_ml[partial_at(a, chunk, t, h)] = make_float2(m == -INFINITY ? m : m * scale2, l);
-            const bool poisoned = *reinterpret_cast<volatile int *>(&ctl->poisoned) != 0;
+            const int64_t part = int64_t(walk.slot()) * kCtaRows;
+            if (!whole) {
+                if (mine && (nt == 2 || w == 0)) part_ml[part + row] = make_float2(m == -INFINITY ? m : m * scale2, l);
+                if (threadIdx.x == 32 * W_SOFT)
+                    pieces[walk.slot()] = make_int4(b + 1, row0, g, walk.u + walk.take == walk.units);
+            }
+            const bool poisoned = nb > 0 && *reinterpret_cast<volatile int *>(&ctl->poisoned[qi & 3]) == qi;
             // Rows leave through shared memory, 128 bytes of each at a time, so that eight lanes store one row's piece.
-            // A warp's 4 KB lie over the lane's Q tile, which its last MMA has left; with one tile (whose Q the other
-            // group's exchange lies over) over V, which nothing reads any more.
-            uint8_t *stage = smem + (nt == 2 ? w * L::TILE : L::OFF_V) + (warp & 3) * 4096;
-            auto put = [&](bool partial, auto *to, int64_t t_stride, int64_t h_stride) {
-                using E = typename std::remove_pointer<decltype(to)>::type;
+            auto put = [&](auto *to_rows, int64_t t_stride, int64_t h_stride, bool partial) {
+                using E = typename std::remove_pointer<decltype(to_rows)>::type;
                 constexpr int W = 128 / sizeof(E);  // columns of a piece: 32 in f32, 64 in 16 bits
                 int64_t at[8];                      // where the rows that this lane stores a part of go
                 const int r_out = row - lane + (lane >> 3);
@@ -583,8 +772,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const int i_step = 4 / G, h_step = 4 % G;
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int64_t tt = int64_t(sp.q0) + i;
-                    at[k] = partial ? partial_at(a, chunk, tt, g * G + hh) * a.dim : tt * t_stride + int64_t(g * G + hh) * h_stride;
+                    at[k] = partial ? (part + r_out + 4 * k) * a.dim : (int64_t(sp.q0) + i) * t_stride + int64_t(g * G + hh) * h_stride;
                     i += i_step;
                     hh += h_step;
                     if (hh >= G) {
@@ -592,31 +780,35 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                         ++i;
                     }
                 }
-                for (int c0 = 0; c0 < a.dim; c0 += W) {
+                for (int c0 = nt == 1 ? w * W : 0; c0 < a.dim; c0 += nt == 1 ? 2 * W : W) {
 #pragma unroll
-                    for (int part = 0; part < W / 32; ++part) {
-                        const int c = c0 / 32 + part;
+                    for (int half = 0; half < W / 32; ++half) {
+                        const int c = c0 / 32 + half;
                         uint32_t o[32];
-                        if (nb > 0) {
-                            tm_ld32(to_cols(c), o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                        if (has_own) {
+                            tm_ld32(to + uint32_t(c * 32), o);
                             tm_wait_ld(o);
                         }
+                        if (has_other) {
+                            uint32_t x[32];
+                            tm_ld32(to_other + uint32_t(c * 32), x);
+                            tm_wait_ld(x);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            float x = nb > 0 ? __uint_as_float(o[i]) : 0.f;
-                            if (nt == 1 && nb > 1) x = x * scale_own + ex[r * L::MPAD + c * 32 + i] * scale_other;
-                            o[i] = __float_as_uint(x);
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint((has_own ? __uint_as_float(o[e]) * scale_own : 0.f) + __uint_as_float(x[e]) * scale_other);
                         }
                         if (poisoned && mine) add_hidden(c, o);
 #pragma unroll
-                        for (int i = 0; i < 32; i += 16 / int(sizeof(E))) {
+                        for (int e0 = 0; e0 < 32; e0 += 16 / int(sizeof(E))) {
                             uint4 v;
-                            auto f = [&](int e) { return __uint_as_float(o[i + e]) * inv; };
+                            auto f = [&](int e) { return __uint_as_float(o[e0 + e]) * inv; };
                             if constexpr (sizeof(E) == 4)
                                 v = make_uint4(__float_as_uint(f(0)), __float_as_uint(f(1)), __float_as_uint(f(2)), __float_as_uint(f(3)));
                             else
                                 v = make_uint4(pack16<E>(f(0), f(1)), pack16<E>(f(2), f(3)), pack16<E>(f(4), f(5)), pack16<E>(f(6), f(7)));
-                            const int piece = (part * 32 + i) * int(sizeof(E)) / 16;
+                            const int piece = (half * 32 + e0) * int(sizeof(E)) / 16;
                             *reinterpret_cast<uint4 *>(stage + lane * 128 + ((piece ^ (lane & 7)) << 4)) = v;
                         }
                     }
@@ -626,13 +818,17 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     for (int k = 0; k < 8; ++k) {
                         const int rr = k * 4 + (lane >> 3);
                         const uint4 v = *reinterpret_cast<const uint4 *>(stage + rr * 128 + ((piece ^ (rr & 7)) << 4));
-                        if (r_out + 4 * k < rows && col < a.dim) *reinterpret_cast<uint4 *>(to + at[k] + col) = v;
+                        if (r_out + 4 * k < rows && col < a.dim) *reinterpret_cast<uint4 *>(to_rows + at[k] + col) = v;
                     }
                     __syncwarp();
                 }
             };
-            if (whole) put(false, static_cast<TO *>(a.out), a.out_token, a.out_head);
-            else put(true, part_o, 0, 0);
+            if (whole) put(static_cast<TO *>(a.out), a.out_token, a.out_head, false);
+            else put(part_o, 0, 0, true);
+        }
+        // the next item's first P V writes over O: not before this group (one tile: both groups) has read it
+        tc_fence_before();
+        if (nt == 1) groups_sync();
         }
     }
 
@@ -647,58 +843,155 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     }
 }
 
-// CTA slots of row tiles, at most: each sequence leaves less than one tile unfilled.
+// Joins the pieces of the item that run `blockIdx.x` begins and does not end: its own last
+// one, and the first ones of the runs after it up to the one that ends it, in that
+// order.  A warp takes four rows, with four pieces of each in flight.
+template <typename TO>
+__global__ void __launch_bounds__(32 * kJoinWarps)
+chunk_join_kernel(const PagedArgs a, const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
+                  const Piece *__restrict__ pieces, int ctas) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c0 = blockIdx.x, G = a.heads / a.kv_heads, lane = threadIdx.x & 31;
+    const Piece p = pieces[2 * c0 + 1];
+    if (p.x == 0) return;
+    int c1 = ctas;  // the run that ends the item
+    for (int c = c0 + 1; c < ctas; c += 32) {
+        const unsigned ends = __ballot_sync(0xffffffffu, c + lane < ctas && pieces[2 * (c + lane)].w != 0);
+        if (ends) {
+            c1 = c + __ffs(ends) - 1;
+            break;
+        }
+    }
+    if (c1 == ctas) return;
+    const int b = p.x - 1, row0 = p.y, g = p.z, count = c1 - c0 + 1;
+    bool ignore = false;
+    const SeqSpan sp = seq_span(a.batch, b, ignore);  // (reported by the launch before)
+    const int rows = min(kCtaRows, int(int64_t(sp.n) * G - row0));
+    const int r0 = (blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kJoinRows;
+    if (r0 >= rows) return;
+    const bool mine = 4 * lane < a.dim;
+    float m[kJoinRows], l[kJoinRows];
+    float4 o[kJoinRows];
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r) {
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+        o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    constexpr int AHEAD = 4;
+    for (int k0 = 0; k0 < count; k0 += AHEAD) {
+        float2 ml[AHEAD][kJoinRows];
+        float4 x[AHEAD][kJoinRows];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+            for (int r = 0; r < kJoinRows; ++r) {
+                ml[k][r] = make_float2(-INFINITY, 0.f);
+                x[k][r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k0 + k < count && r0 + r < rows) {
+                    const int64_t at = int64_t(k0 + k == 0 ? 2 * c0 + 1 : 2 * (c0 + k0 + k)) * kCtaRows + r0 + r;
+                    ml[k][r] = part_ml[at];
+                    if (mine) x[k][r] = *reinterpret_cast<const float4 *>(part_o + at * a.dim + 4 * lane);
+                }
+            }
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            float next = m[r];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) next = fmaxf(next, ml[k][r].x);
+            const float keep = m[r] == next ? 1.f : fast_ex2(m[r] - next);
+            l[r] *= keep;
+            o[r].x *= keep;
+            o[r].y *= keep;
+            o[r].z *= keep;
+            o[r].w *= keep;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float f = ml[k][r].x == next ? 1.f : fast_ex2(ml[k][r].x - next);
+                l[r] = fmaf(f, ml[k][r].y, l[r]);
+                o[r].x = fmaf(f, x[k][r].x, o[r].x);
+                o[r].y = fmaf(f, x[k][r].y, o[r].y);
+                o[r].z = fmaf(f, x[k][r].z, o[r].z);
+                o[r].w = fmaf(f, x[k][r].w, o[r].w);
+            }
+            m[r] = next;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kJoinRows; ++r)
+        if (mine && r0 + r < rows) {
+            const int i = (row0 + r0 + r) / G, h = g * G + (row0 + r0 + r) % G;
+            const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+            store4(static_cast<TO *>(a.out) + (int64_t(sp.q0) + i) * a.out_token + int64_t(h) * a.out_head + 4 * lane, o[r].x * inv,
+                   o[r].y * inv, o[r].z * inv, o[r].w * inv);
+        }
+}
+
+struct ChunkLaunch {
+    ChunkPlan plan;
+    int ctas;
+};
+
+// tiles: at most, each sequence leaves less than one unfilled
 int64_t tile_bound(int64_t group, int64_t seqs, int64_t tokens) {
     return (tokens * group + std::min(seqs, tokens) * (kCtaRows - 1)) / kCtaRows;
 }
 
-// The most chunks worth having: four turns of every SM.
-int64_t split_bound(int64_t ctas, int64_t max_kv) {
-    const int64_t blocks = (max_kv + kBlock - 1) / kBlock;
-    return std::max<int64_t>(1, std::min({(4 * kNumSms + ctas - 1) / ctas, (blocks + kMinBlocks - 1) / kMinBlocks,
-                                          int64_t(kMaxSplits)}));
+ChunkLaunch chunk_launch(int64_t items, int64_t span) {
+    ChunkLaunch r = {};
+    r.plan.split = span > kWholeKeys;
+    const int64_t units = items * (r.plan.split ? kStartUnits + span / kBlock + 2 : 1), least = r.plan.split ? kMinUnits : 1;
+    r.ctas = int(std::min<int64_t>(kNumSms, (units + least - 1) / least));
+    return r;
 }
 
-// Chunks of keys: the number for which turns of the SMs x (blocks a CTA + the
-// cost of a CTA's start and end, in blocks) is least.
-KeyPlan chunk_plan(int64_t ctas, int64_t max_q, int64_t max_kv, int64_t window, int page_size) {
-    KeyPlan p = {};
-    const int64_t span = key_span(max_q, max_kv, window), blocks = std::max<int64_t>(1, (span + kBlock - 1) / kBlock);
-    int64_t best = 1;
-    double least = 0;
-    for (int64_t s = 1; s <= split_bound(ctas, span); ++s) {
-        const double turns = double((ctas * s + kNumSms - 1) / kNumSms);
-        const double cost = turns * (double((blocks + s - 1) / s) + (s > 1 ? 4.5 : 3.0)) + (s > 1 ? 2.0 : 0.0);
-        if (s == 1 || cost < least) {
-            best = s;
-            least = cost;
-        }
-    }
-    p.chunk = int((blocks + best - 1) / best * kBlock);
-    p.chunks = int((blocks * kBlock + p.chunk - 1) / p.chunk);
-    p.box_rows = std::min(page_size & -page_size, kBlock);
-    return p;
+size_t chunk_ws_bytes(int64_t ctas, int64_t dim) {
+    return size_t(2 * ctas * kCtaRows) * size_t(dim * 4 + 8) + size_t(2 * ctas) * sizeof(Piece);
+}
+
+// Tensor map of q whose boxes are a 128-row tile's 64 features: G heads of 128 / G tokens.
+template <typename T>
+cudaError_t q_map(const PagedArgs &a, CUtensorMap *map) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const int G = a.heads / a.kv_heads;
+    const cuuint64_t dims[3] = {cuuint64_t(a.dim), cuuint64_t(a.heads), cuuint64_t(a.batch.tokens)};
+    auto bytes = [&](int64_t s) { return cuuint64_t(s ? s : a.dim) * 2; };  // (0: an axis of one element)
+    const cuuint64_t strides[2] = {bytes(a.q_head), bytes(a.q_token)};
+    const cuuint32_t box[3] = {64, cuuint32_t(G), cuuint32_t(kRows / G)}, step[3] = {1, 1, 1};
+    if (enc(map, is_half<T> ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(a.q), dims,
+            strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    return cudaSuccess;
 }
 
 template <typename T, typename TO, int DP>
 cudaError_t launch_chunk(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
     using L = ChunkLayout<DP>;
-    const int64_t tiles = tile_bound(a.heads / a.kv_heads, a.batch.seqs, a.batch.tokens);
-    const KeyPlan plan = chunk_plan(tiles * a.kv_heads, a.batch.max_q, a.batch.max_kv, a.window, a.batch.page_size);
-    const int64_t ctas = tiles * a.kv_heads * plan.chunks;
-    if (ctas > INT32_MAX) return cudaErrorInvalidValue;
-    CUtensorMap km, vm;
-    cudaError_t e = cache_maps<T>(a, plan.box_rows, &km, &vm);
+    const int64_t G = a.heads / a.kv_heads, items = tile_bound(G, a.batch.seqs, a.batch.tokens) * a.kv_heads;
+    const int64_t span = key_span(a.batch.max_q, a.batch.max_kv, a.window);
+    if (items > INT32_MAX / (span / kBlock + 8)) return cudaErrorInvalidValue;
+    ChunkLaunch r = chunk_launch(items, span);
+    r.plan.box_rows = std::min(a.batch.page_size & -a.batch.page_size, kBlock);
+    // a stride of 0 along more than one head or token (a broadcast q) has no tensor map
+    r.plan.q_copies = kRows % G == 0 && a.scale >= 0.f && (a.q_head || a.heads == 1) && (a.q_token || a.batch.tokens == 1);
+    CUtensorMap km, vm, qm = {};
+    cudaError_t e = cache_maps<T>(a, r.plan.box_rows, &km, &vm);
+    if (e == cudaSuccess && r.plan.q_copies) e = q_map<T>(a, &qm);
     if (e != cudaSuccess) return e;
     auto kernel = paged_chunk_kernel<T, TO, DP>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
-    float *po = static_cast<float *>(ws);
-    float2 *pml = reinterpret_cast<float2 *>(po + int64_t(plan.chunks) * a.batch.tokens * a.heads * a.dim);
-    e = launch_dependent(kernel, dim3(unsigned(ctas)), kThreads, L::BYTES, ctx.stream, km, vm, a, plan, po, pml, ctx.status,
-                         ctx.wait_ns);
-    if (e != cudaSuccess || plan.chunks == 1) return e;
-    return launch_join<TO>(a, plan, po, pml, ctx);
+    const int64_t slots = 2 * int64_t(r.ctas) * kCtaRows;
+    float *po = r.plan.split ? static_cast<float *>(ws) : nullptr;
+    float2 *pml = r.plan.split ? reinterpret_cast<float2 *>(po + slots * a.dim) : nullptr;
+    Piece *pieces = r.plan.split ? reinterpret_cast<Piece *>(pml + slots) : nullptr;
+    e = launch_dependent(kernel, dim3(unsigned(r.ctas)), kThreads, L::BYTES, ctx.stream, km, vm, qm, a, r.plan, po, pml, pieces,
+                         ctx.status, ctx.wait_ns);
+    if (e != cudaSuccess || !r.plan.split) return e;
+    return launch_dependent(chunk_join_kernel<TO>, dim3(unsigned(r.ctas), kJoinParts), 32 * kJoinWarps, 0, ctx.stream, a,
+                            static_cast<const float *>(po), static_cast<const float2 *>(pml), static_cast<const Piece *>(pieces), r.ctas);
 }
 
 template <typename T, typename TO>
@@ -708,8 +1001,9 @@ cudaError_t launch_chunk_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) 
 
 }  // namespace
 
-int64_t attention_paged_chunk_bound(int64_t heads, int64_t kv_heads, int64_t seqs, int64_t tokens, int64_t max_kv) {
-    return split_bound(tile_bound(heads / kv_heads, seqs, tokens) * kv_heads, max_kv);
+size_t attention_paged_chunk_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_kv) {
+    const ChunkLaunch r = chunk_launch(tile_bound(heads / kv_heads, seqs, tokens) * kv_heads, max_kv);  // (a window only shortens the span)
+    return r.plan.split ? chunk_ws_bytes(r.ctas, dim) : 0;
 }
 
 cudaError_t launch_attention_paged_chunk(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx) {

@@ -15,22 +15,8 @@ constexpr bool is_half = false;
 template <>
 constexpr bool is_half<__half> = true;
 
-// How a call is cut: at most `chunks` chunks of `chunk` keys (a multiple of 128) a
-// sequence, and the rows of a copy.  With more than one chunk, (m, l, O) of token
-// t, head h and chunk c is partial (c * tokens + t) * heads + h.
-struct KeyPlan {
-    int chunk;
-    int chunks;
-    int box_rows;
-};
-__device__ __forceinline__ int64_t partial_at(const PagedArgs &a, int c, int64_t t, int h) {
-    return (int64_t(c) * a.batch.tokens + t) * a.heads + h;
-}
-inline size_t partial_bytes(int64_t chunks, int64_t tokens, int64_t heads, int64_t dim) {
-    return chunks > 1 ? size_t(chunks * tokens * heads) * size_t(dim * 4 + 8) : 0;
-}
-
-// Keys from the chunk base of the first token's window to the last token, at most.
+// Keys from the first token's window to the last token, at most, with what a block of 128
+// may hold before them.
 inline int64_t key_span(int64_t max_q, int64_t max_kv, int64_t window) {
     return window && window < max_kv ? std::min(max_kv, window + max_q + 126) : max_kv;
 }
@@ -315,35 +301,6 @@ __device__ __forceinline__ void join_partials(const PagedArgs &a, int64_t t, int
         const float inv = l == 0.f ? 0.f : 1.f / l;
         store4(out + t * a.out_token + int64_t(h) * a.out_head + 4 * lane, o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
-}
-
-// Joins the chunks that one (new token, head) sees a key in.
-template <typename TO>
-__global__ void __launch_bounds__(32 * kJoinWarps)
-paged_join_kernel(const PagedArgs a, const KeyPlan plan, const float *__restrict__ part_o,
-                  const float2 *__restrict__ part_ml) {
-    // Before the wait: the tables.  (This block runs only once every block of the launch before has passed its own wait,
-    // so whatever wrote the tables has ended.)
-    const int64_t t = blockIdx.x;
-    const int h = blockIdx.y;
-    const int b = seq_of(a.batch, t);
-    bool bad = false;
-    const SeqSpan sp = b < 0 ? SeqSpan{0, 0, 0} : seq_span(a.batch, b, bad);  // (reported by the launch before)
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
-    const KeyCut cut = cut_keys(sp, a.window, a.causal, plan.chunk);
-    if (cut.chunks <= 1) return;
-    const KeyRange kr = keys_of(sp, int(t - sp.q0), a.window, a.causal);
-    const int c0 = kr.hi > kr.lo ? (kr.lo - cut.base) / plan.chunk : 0;
-    const int c1 = kr.hi > kr.lo ? (kr.hi - 1 - cut.base) / plan.chunk + 1 : 0;
-    join_partials(a, t, h, c1 - c0, part_o, part_ml, [&](int i) { return partial_at(a, c0 + i, t, h); }, static_cast<TO *>(a.out));
-}
-
-template <typename TO>
-cudaError_t launch_join(const PagedArgs &a, const KeyPlan &plan, const float *part_o, const float2 *part_ml,
-                        const LaunchCtx &ctx) {
-    return launch_dependent(paged_join_kernel<TO>, dim3(unsigned(a.batch.tokens), unsigned(a.heads)), 32 * kJoinWarps, 0,
-                            ctx.stream, a, plan, part_o, part_ml);
 }
 
 }  // namespace tq2

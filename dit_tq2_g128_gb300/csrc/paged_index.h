@@ -92,19 +92,6 @@ TQ2_HD RowSpan rows_see(const SeqSpan &sp, int i0, int i1, int64_t window, bool 
     return RowSpan{first.lo, last.hi, last.lo, first.hi};
 }
 
-// A sequence's keys are cut into chunks of `chunk` (a multiple of 128) from `base`
-// on: its first visible key, down to a multiple of 128.
-struct KeyCut {
-    int base, chunks;  // chunks: 0 if no token sees a key
-};
-TQ2_HD KeyCut cut_keys(const SeqSpan &sp, int64_t window, bool causal, int chunk) {
-    if (sp.n == 0) return KeyCut{0, 0};
-    const RowSpan r = rows_see(sp, 0, sp.n - 1, window, causal);
-    if (r.hi <= r.lo) return KeyCut{0, 0};
-    const int base = r.lo / 128 * 128;
-    return KeyCut{base, int((int64_t(r.hi) - base + chunk - 1) / chunk)};
-}
-
 // Boxes (rows inside one page) of a tile of keys [from, from + keys) that hold a key
 // of [first, last): box i is keys from + i * rows on, i in [lo, hi).
 struct BoxRange {
@@ -118,16 +105,21 @@ TQ2_HD BoxRange boxes_of(int from, int keys, int rows, int first, int last) {
     return BoxRange{lo, hi};
 }
 
-// Of the `tiles` tiles of `rows` query rows (row = token * group + head) of a span, how
-// many have their last visible key past key x - 1 (x < 0: all of them): the last ones,
-// since a causal token's keys end with itself.
-TQ2_HD int tiles_past(const SeqSpan &sp, int group, int rows, int tiles, bool causal, int64_t x) {
-    if (x < 0) return tiles;
-    if (sp.kv <= x) return 0;
-    const int64_t y = x - (int64_t(sp.kv) - sp.n);  // causal: from the token after the y-th on
-    if (!causal || y <= 0) return tiles;
-    const int64_t t = y * group / rows;
-    return t < tiles ? int(tiles - t) : 0;
+// An item: rows [row0, row0 + rows) of a span (row = token * group + head, at most `most`),
+// what they see, and the blocks of `keys` keys that hold it (0: no key).
+struct ItemSpan {
+    RowSpan see;
+    int rows, block0, blocks;
+};
+TQ2_HD ItemSpan item_span(const SeqSpan &sp, int group, int row0, int most, int64_t window, bool causal, int keys) {
+    const int64_t left = int64_t(sp.n) * group - row0;
+    ItemSpan it{};
+    it.rows = int(left < most ? left : most);
+    it.see = rows_see(sp, row0 / group, (row0 + it.rows - 1) / group, window, causal);
+    if (it.see.hi <= it.see.lo) return it;
+    it.block0 = it.see.lo / keys;
+    it.blocks = (it.see.hi + keys - 1) / keys - it.block0;
+    return it;
 }
 
 // The tiles of `keys` keys that hold a key some token of a span sees, and the units of

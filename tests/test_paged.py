@@ -144,8 +144,11 @@ void tiles(int n, int kv, long long window, int causal, int keys, int split, int
     const TileSpan t = tiles_of(SeqSpan{0, n, kv}, window, causal, keys, split);
     out[0] = t.tile0, out[1] = t.tiles, out[2] = t.units;
 }
-int past(int n, int kv, int group, int rows, int tiles, int causal, long long x) {
-    return tiles_past(SeqSpan{0, n, kv}, group, rows, tiles, causal, x);
+int item(int n, int kv, int group, int row0, int most, long long window, int causal, int keys, int *out) {
+    const ItemSpan t = item_span(SeqSpan{0, n, kv}, group, row0, most, window, causal, keys);
+    out[0] = t.rows, out[1] = t.block0, out[2] = t.blocks;
+    out[3] = t.see.lo, out[4] = t.see.hi, out[5] = t.see.lo_all, out[6] = t.see.hi_all;
+    return 0;
 }
 }
 """)
@@ -244,18 +247,26 @@ def test_tiles_of_a_span(index):
                 assert out[2] == (0 if n == 0 else max(1, len(want)) if split else 1)
 
 
-def test_tiles_past_a_key(index):
+def test_items_of_a_span(index):
     rng = np.random.default_rng(6)
-    for _ in range(2000):
-        n, kv, group = int(rng.integers(1, 900)), int(rng.integers(0, 1200)), int(rng.integers(1, 17))
-        rows = 256
-        tiles = -(-n * group // rows)
+    for _ in range(1500):
+        n, kv, group = int(rng.integers(1, 60)), int(rng.integers(0, 600)), int(rng.integers(1, 17))
+        window = int(rng.choice([0, 1, 7, 128, 300]))
+        most = 64
         for causal in (0, 1):
-            ends = [max(0, kv - n + min(n * group - 1, (t + 1) * rows - 1) // group + 1) if causal else kv
-                    for t in range(tiles)]
-            for x in (-1, 0, 1, int(rng.integers(0, 1300)), kv - 1, kv):
-                want = tiles if x < 0 else sum(e > x for e in ends)
-                assert index.past(n, kv, group, rows, tiles, causal, ctypes.c_longlong(x)) == want, (n, kv, group, x)
+            for row0 in range(0, n * group, most):
+                out = (ctypes.c_int * 7)()
+                index.item(n, kv, group, row0, most, ctypes.c_longlong(window), causal, 128, out)
+                rows = range(row0, min(n * group, row0 + most))
+                assert out[0] == len(rows)
+                see = [{j for j in range(kv) if (j <= kv - n + i or not causal) and (j > kv - n + i - window or not window)}
+                       for i in sorted({r // group for r in rows})]
+                some, every = set().union(*see), set.intersection(*see)
+                assert set(range(out[3], out[4])) == some or (not some and out[2] == 0)
+                if all(see):
+                    assert set(range(out[5], out[6])) == every
+                want = sorted({j // 128 for j in some})
+                assert out[2] == len(want) and (not want or out[1] == want[0])
 
 
 # ---------------------------------------------------------------------------
