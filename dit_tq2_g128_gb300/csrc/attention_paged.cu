@@ -596,7 +596,7 @@ cudaError_t launch_rows_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
 size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
                                 int64_t max_kv) {
     const int64_t rows = std::min(max_q, tokens) * (heads / kv_heads);
-    if (rows > kRowsMax) return attention_paged_chunk_ws_bytes(heads, kv_heads, dim, seqs, tokens, max_kv);
+    if (rows > kRowsMax) return attention_paged_chunk_ws_bytes(heads, kv_heads, dim, seqs, tokens, std::min(max_q, tokens), max_kv);
     const RowLaunch r = row_launch(kv_heads, seqs, rows, max_kv, 1);  // (a window only shortens the span)
     return r.plan.split ? row_ws_bytes(seqs, rows, dim, r.ctas) : 0;
 }

@@ -6,13 +6,14 @@
 // the group, row = token * G + head, so a 128-row tile of a chunk reads each key
 // for all G heads at once.
 //
-//  * Work is shared out evenly.  An item is up to 256 consecutive rows (two tiles) of
-//    one (sequence, key head); the items' blocks of 128 keys, in one line with the cost
-//    of an item's start and end, are cut into as many equal runs as there are SMs, and a
-//    CTA takes a run.  Pieces of a cut item go to the workspace and a second, dependent
-//    launch joins them in order.  A CTA starts once, copies ahead into its next item,
-//    and its next Q comes as soon as the last S that reads the old one has ended.  (One CTA
-//    an item and chunk spent 7 us of its own on each.)
+//  * An item is up to 256 consecutive rows (two tiles) of one (sequence, key head).
+//    Where the items fill the SMs a CTA takes one, the longest first.  Where they are few
+//    and long their blocks of 128 keys, in one line with the cost of an item's start
+//    and end, are cut into as many equal runs as there are SMs, and a CTA takes a run: it
+//    starts once, copies ahead into its next item, and its next Q comes as soon as the
+//    last S that reads the old one has ended; pieces of a cut item go to the workspace
+//    and a second, dependent launch joins them in order.  (The rule and both sides'
+//    times: chunk_launch.)
 //  * Warps 0 and 12 copy K and V through two-stage rings by paged tensor copies (boxes
 //    of rows inside one page), warp 0 Q too; warps 1 and 2 issue the MMAs of lane 0 and
 //    1 (below); warp 3 looks after V; warps 4-7 and 8-11 are the lanes' softmax groups,
@@ -53,9 +54,9 @@ constexpr int kBlock = 128;     // keys of a block (copies)
 constexpr int kStep = 64;       // keys of a step (MMAs, softmax)
 constexpr int kCtaRows = 2 * kRows;
 constexpr int kThreads = 416;
-constexpr int kStartUnits = 2;  // an item's start and end, in blocks, for the shares
+constexpr int kStartUnits = 4;  // an item's start and end, in blocks, for the shares (2: 207 and 277 us, 4: 207 and 248, 8: 213 and 271
+                                // for 512 tokens over 32768 keys and for ragged prompts)
 constexpr int kMinUnits = 4;    // units of a run, at least, where items may be cut
-constexpr int kWholeKeys = 512; // up to so many keys an item stays whole
 constexpr int kJoinRows = 4;    // rows of a warp of the join
 constexpr int kJoinParts = kCtaRows / (kJoinRows * kJoinWarps);  // its blocks per cut item
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
@@ -81,6 +82,7 @@ struct ChunkCtl {
     uint32_t tmem_base;
     int abort;
     int poisoned[4];         // by item (of those with blocks, from 1 on) modulo 4: the last whose V had values taken out
+    int item;                // the item that q_ready announces: twice its blocks, one more for two tiles; 0: the run is over
     int b, row0, g, u, left; // where this CTA's run begins: sequence, rows, key head, unit; its units
 };
 static_assert(sizeof(ChunkCtl) <= 256, "control block");
@@ -202,7 +204,40 @@ __device__ __forceinline__ ItemSpan item_of(const PagedArgs &a, const SeqSpan &s
 __device__ __forceinline__ void find_run(const PagedArgs &a, const ChunkPlan &plan, ChunkCtl *ctl, unsigned int *status) {
     const BatchView &bt = a.batch;
     const int lane = threadIdx.x & 31, G = a.heads / a.kv_heads;
-    auto weight = [&](const SeqSpan &sp, int tile) { return plan.split ? kStartUnits + max(1, item_of(a, sp, tile * kCtaRows).blocks) : 1; };
+    if (!plan.split) {  // item blockIdx.x of all: from the last sequence's last tile (the longest of a prompt) on
+        int from = int(blockIdx.x);
+        if (lane == 0) ctl->left = 0;
+        for (int top = bt.seqs; top > 0; top -= 32) {
+            const int b = top - 1 - lane;
+            int tiles = 0;
+            if (b >= 0) {
+                bool bad = false;
+                tiles = tiles_in(seq_span(bt, b, bad), G);
+                report_bad(bad, status);
+            }
+            int upto = tiles * a.kv_heads;  // inclusive over the lanes
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, d);
+                if (lane >= d) upto += x;
+            }
+            const unsigned hit = __ballot_sync(0xffffffffu, from < upto);
+            if (hit) {
+                if (lane == __ffs(hit) - 1) {
+                    const int at = from - (upto - tiles * a.kv_heads);
+                    ctl->b = b;
+                    ctl->row0 = (tiles - 1 - at / a.kv_heads) * kCtaRows;
+                    ctl->g = at % a.kv_heads;
+                    ctl->u = 0;
+                    ctl->left = 1;
+                }
+                return;
+            }
+            from -= __shfl_sync(0xffffffffu, upto, 31);
+        }
+        return;
+    }
+    auto weight = [&](const SeqSpan &sp, int tile) { return kStartUnits + max(1, item_of(a, sp, tile * kCtaRows).blocks); };
     // units of sequences base + lane, of one key head
     auto units_of = [&](int base) {
         SeqSpan sp{0, 0, 0};
@@ -231,7 +266,7 @@ __device__ __forceinline__ void find_run(const PagedArgs &a, const ChunkPlan &pl
     int total = int(__reduce_add_sync(0xffffffffu, unsigned(head))) * a.kv_heads;
     for (int base = 32; base < bt.seqs; base += 32)
         total += int(__reduce_add_sync(0xffffffffu, unsigned(units_of(base)))) * a.kv_heads;
-    const int ctas = int(gridDim.x), share = max(plan.split ? kMinUnits : 1, (total + ctas - 1) / ctas);
+    const int ctas = int(gridDim.x), share = max(kMinUnits, (total + ctas - 1) / ctas);
     const int64_t start = int64_t(blockIdx.x) * share;
     if (lane == 0) ctl->left = start < total ? int(min(int64_t(share), total - start)) : 0;
     if (start >= total) return;
@@ -423,6 +458,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (qi > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->q_free, (qi - 1) & 1, abort_flag, wait_ns, status));
                 if (!ok) break;
                 if (elect_one()) {
+                    *reinterpret_cast<volatile int *>(&ctl->item) = 2 * nb + (walk.nt == 2);
                     mbar_expect_tx(&ctl->q_ready, uint32_t(walk.nt * L::TILE));
                     for (int t = 0; t < walk.nt; ++t)
 #pragma unroll
@@ -451,11 +487,19 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             }
         }
         report_bad(bad, status);
+        if (!v && plan.q_copies && ok) {  // the run is over
+            if (qi > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->q_free, (qi - 1) & 1, abort_flag, wait_ns, status));
+            if (ok && elect_one()) {
+                *reinterpret_cast<volatile int *>(&ctl->item) = 0;
+                mbar_arrive(&ctl->q_ready);
+            }
+            __syncwarp();
+        }
         // every copy issued must land before the CTA exits
         if (lane == 0) {
             for (int j = max(0, blocks - 2); j < blocks; ++j)
                 mbar_wait_bounded(&full[j & 1], (j >> 1) & 1, drain_ns(wait_ns), status);
-            if (!v && plan.q_copies && qi > 0) mbar_wait_bounded(&ctl->q_ready, (qi - 1) & 1, drain_ns(wait_ns), status);
+            if (!v && plan.q_copies && qi > 0 && !ok) mbar_wait_bounded(&ctl->q_ready, (qi - 1) & 1, drain_ns(wait_ns), status);
         }
         __syncwarp();
     } else if (warp == W_MMA || warp == W_MMA + 1) {
@@ -471,41 +515,43 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint64_t dk[2] = {desc_k(sK), desc_k(sK + L::TILE)};
         const uint64_t dv[2] = {desc_mn(sV, L::HALF), desc_mn(sV + L::TILE, L::HALF)};
         const uint32_t t_s = tmem + uint32_t(w * 128), t_o = tmem + kOCol + uint32_t(w * 128);
-        int done = 0;  // this lane's steps before the item
-        bool ok = true;
-        for (; ok && walk.more(); walk.next()) {
-            if (walk.nb == 0) continue;
-            const int nt = walk.nt, steps = walk.steps(w);
-            const uint64_t dq = desc_k(sQ + uint32_t(nt == 2 ? w * L::TILE : 0));
-            auto issue_s = [&](int u) -> bool {
-                const int j = blocks + walk.block(w, u), h = u & 1;
-                if (!h && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
-                tc_fence_after();
-                const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t(h * (kStep * 128 >> 4));
+        // One thread from here on; items come with Q (nb blocks, nt tiles), so that nothing but MMAs and waits stands here.
+        if (elect_one()) {
+            int done = 0;  // this lane's steps before the item
+            for (;; ++qi) {
+                bool ok = wait_on(&ctl->q_ready, qi & 1);
+                const int item = ok ? *reinterpret_cast<volatile int *>(&ctl->item) : 0, nb = item >> 1;
+                if (nb == 0) break;
+                const bool two = item & 1;
+                const int steps = two ? 2 * nb : 2 * ((nb + 1 - w) >> 1);
+                const uint64_t dq = desc_k(sQ + uint32_t(two ? w * L::TILE : 0));
+                auto block = [&](int u) { return blocks + (two ? u >> 1 : (u & ~1) + w); };
+                auto issue_s = [&](int u) -> bool {
+                    const int j = block(u), h = u & 1;
+                    if (!h && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
+                    tc_fence_after();
+                    const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t(h * (kStep * 128 >> 4));
 #pragma unroll
-                for (int kk = 0; kk < DP / 16; ++kk) {
-                    const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
-                    if (kk < nd) tc_mma_f16(t_s + uint32_t(h * 64), dq + off, db + off, idesc_s, kk > 0);
-                }
-                tc_commit(&ctl->s_full[w][h]);
-                if (h) {
-                    tc_commit(&ctl->k_empty[j & 1]);
-                    if (nt == 1) tc_commit(&ctl->k_empty[j & 1]);
-                }
-                if (u == steps - 1) tc_commit(&ctl->q_free);
-                return true;
-            };
-            bool lane_ok = true;
-            if (elect_one()) {
-                lane_ok = wait_on(&ctl->q_ready, qi & 1);
+                    for (int kk = 0; kk < DP / 16; ++kk) {
+                        const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
+                        if (kk < nd) tc_mma_f16(t_s + uint32_t(h * 64), dq + off, db + off, idesc_s, kk > 0);
+                    }
+                    tc_commit(&ctl->s_full[w][h]);
+                    if (h) {
+                        tc_commit(&ctl->k_empty[j & 1]);
+                        if (!two) tc_commit(&ctl->k_empty[j & 1]);
+                    }
+                    if (u == steps - 1) tc_commit(&ctl->q_free);
+                    return true;
+                };
                 if (steps == 0) tc_commit(&ctl->q_free);
-                for (int u = 0; u < 2 && u < steps && lane_ok; ++u) lane_ok = issue_s(u);
-                for (int u = 0; u < steps && lane_ok; ++u) {
-                    const int j = blocks + walk.block(w, u), h = u & 1;
+                for (int u = 0; u < 2 && u < steps && ok; ++u) ok = issue_s(u);
+                for (int u = 0; u < steps && ok; ++u) {
+                    const int j = block(u), h = u & 1;
                     // (P first: its groups have then seen the whole item before end, so that V's parity, whose slot the other
                     // lane may have used last, is read no earlier than one phase before)
-                    lane_ok = wait_on(&ctl->p_full[w][h], ((done + u) >> 1) & 1) && (h || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1));
-                    if (!lane_ok) break;
+                    ok = wait_on(&ctl->p_full[w][h], ((done + u) >> 1) & 1) && (h || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1));
+                    if (!ok) break;
                     tc_fence_after();
                     const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t(h * (kStep * 128 >> 4));
                     const uint32_t p = t_s + uint32_t(h * 64);
@@ -519,18 +565,16 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                     if (u == steps - 1) tc_commit(&ctl->item_done[w]);
                     if (h) {
                         tc_commit(&ctl->v_empty[j & 1]);
-                        if (nt == 1) tc_commit(&ctl->v_empty[j & 1]);
+                        if (!two) tc_commit(&ctl->v_empty[j & 1]);
                     }
-                    if (u + 2 < steps) lane_ok = issue_s(u + 2);
+                    if (u + 2 < steps) ok = issue_s(u + 2);
                 }
+                if (!ok) break;
+                blocks += nb;
+                done += steps;
             }
-            __syncwarp();
-            ok = __all_sync(0xffffffffu, lane_ok);
-            blocks += walk.nb;
-            done += steps;
-            ++qi;
+            tc_commit(&ctl->drain);  // when all of this lane's MMAs have ended
         }
-        if (elect_one()) tc_commit(&ctl->drain);  // when all of this lane's MMAs have ended
         __syncwarp();
     } else if (warp == W_SOFT - 1) {
         // ---- V: slots that some row of the item must not multiply
@@ -627,7 +671,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
             fence_proxy_async_smem();
             groups_sync();
-            if (ok && threadIdx.x == 32 * W_SOFT) mbar_arrive(&ctl->q_ready);
+            if (ok && threadIdx.x == 32 * W_SOFT) {
+                *reinterpret_cast<volatile int *>(&ctl->item) = 2 * nb + (nt == 2);
+                mbar_arrive(&ctl->q_ready);
+            }
         }
         if (nb > 0) ++qi;
         float m = -INFINITY, l = 0.f;
@@ -830,6 +877,13 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         tc_fence_before();
         if (nt == 1) groups_sync();
         }
+        if (!plan.q_copies && warp == W_SOFT && ok) {  // the run is over
+            if (qi > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->q_free, (qi - 1) & 1, abort_flag, wait_ns, status));
+            if (ok && lane == 0) {
+                *reinterpret_cast<volatile int *>(&ctl->item) = 0;
+                mbar_arrive(&ctl->q_ready);
+            }
+        }
     }
 
     tc_fence_before();
@@ -845,9 +899,9 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
 
 // Joins the pieces of the item that run `blockIdx.x` begins and does not end: its own last
 // one, and the first ones of the runs after it up to the one that ends it, in that
-// order.  A warp takes four rows, with four pieces of each in flight.
+// order.  A warp takes four rows, with two pieces of each in flight.
 template <typename TO>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+__global__ void __launch_bounds__(32 * kJoinWarps, 6)
 chunk_join_kernel(const PagedArgs a, const float *__restrict__ part_o, const float2 *__restrict__ part_ml,
                   const Piece *__restrict__ pieces, int ctas) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -878,7 +932,7 @@ chunk_join_kernel(const PagedArgs a, const float *__restrict__ part_o, const flo
         l[r] = 0.f;
         o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    constexpr int AHEAD = 4;
+    constexpr int AHEAD = 2;
     for (int k0 = 0; k0 < count; k0 += AHEAD) {
         float2 ml[AHEAD][kJoinRows];
         float4 x[AHEAD][kJoinRows];
@@ -937,11 +991,19 @@ int64_t tile_bound(int64_t group, int64_t seqs, int64_t tokens) {
     return (tokens * group + std::min(seqs, tokens) * (kCtaRows - 1)) / kCtaRows;
 }
 
-ChunkLaunch chunk_launch(int64_t items, int64_t span) {
+// Items are cut where one CTA an item would leave the SMs idle for longer than cutting
+// costs: with fewer than two turns of items, the last turn's idle share times an item's
+// blocks (1.7 us each), against about 14 us for the partial results and the join.  Measured:
+// 512 tokens over 32768 keys, 8 key heads (64 items of 256 blocks) 207 us cut and 229
+// chunked without; 1216 tokens over 8192 (152 items) 131 cut, 101 whole; 1024 of a
+// prompt (128 items of up to 8 blocks) 34 cut, 23 whole.
+ChunkLaunch chunk_launch(int64_t items, int64_t max_q, int64_t span) {
     ChunkLaunch r = {};
-    r.plan.split = span > kWholeKeys;
-    const int64_t units = items * (r.plan.split ? kStartUnits + span / kBlock + 2 : 1), least = r.plan.split ? kMinUnits : 1;
-    r.ctas = int(std::min<int64_t>(kNumSms, (units + least - 1) / least));
+    const int64_t blocks = std::max<int64_t>(1, (span - std::min(max_q, span) / 2) / kBlock);
+    const int64_t idle = (items + kNumSms - 1) / kNumSms * kNumSms - items;
+    r.plan.split = items < 2 * kNumSms && idle * blocks > 8 * kNumSms;
+    const int64_t units = items * (kStartUnits + span / kBlock + 2);
+    r.ctas = int(r.plan.split ? std::min<int64_t>(kNumSms, (units + kMinUnits - 1) / kMinUnits) : items);
     return r;
 }
 
@@ -972,7 +1034,7 @@ cudaError_t launch_chunk(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
     const int64_t G = a.heads / a.kv_heads, items = tile_bound(G, a.batch.seqs, a.batch.tokens) * a.kv_heads;
     const int64_t span = key_span(a.batch.max_q, a.batch.max_kv, a.window);
     if (items > INT32_MAX / (span / kBlock + 8)) return cudaErrorInvalidValue;
-    ChunkLaunch r = chunk_launch(items, span);
+    ChunkLaunch r = chunk_launch(items, a.batch.max_q, span);
     r.plan.box_rows = std::min(a.batch.page_size & -a.batch.page_size, kBlock);
     // a stride of 0 along more than one head or token (a broadcast q) has no tensor map
     r.plan.q_copies = kRows % G == 0 && a.scale >= 0.f && (a.q_head || a.heads == 1) && (a.q_token || a.batch.tokens == 1);
@@ -1001,8 +1063,9 @@ cudaError_t launch_chunk_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) 
 
 }  // namespace
 
-size_t attention_paged_chunk_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_kv) {
-    const ChunkLaunch r = chunk_launch(tile_bound(heads / kv_heads, seqs, tokens) * kv_heads, max_kv);  // (a window only shortens the span)
+size_t attention_paged_chunk_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
+                                      int64_t max_kv) {
+    const ChunkLaunch r = chunk_launch(tile_bound(heads / kv_heads, seqs, tokens) * kv_heads, max_q, max_kv);  // (a window only shortens the span)
     return r.plan.split ? chunk_ws_bytes(r.ctas, dim) : 0;
 }
 

@@ -144,7 +144,8 @@ cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, 
 
 // The part of it for many rows per (sequence, key head) (attention_paged_chunk.cu),
 // and its workspace.
-size_t attention_paged_chunk_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_kv);
+size_t attention_paged_chunk_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
+                                      int64_t max_kv);
 cudaError_t launch_attention_paged_chunk(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx);
 
 // Skinny-M tensor-core kernel (2 <= m <= 32, k up to the shared-memory limit
