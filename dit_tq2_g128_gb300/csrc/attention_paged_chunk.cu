@@ -385,6 +385,11 @@ struct ChunkWalk {
     }
 };
 
+template <bool B>
+struct bool_c {
+    static constexpr bool value = B;
+};
+
 template <typename T, typename TO, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -515,66 +520,76 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const uint64_t dk[2] = {desc_k(sK), desc_k(sK + L::TILE)};
         const uint64_t dv[2] = {desc_mn(sV, L::HALF), desc_mn(sV + L::TILE, L::HALF)};
         const uint32_t t_s = tmem + uint32_t(w * 128), t_o = tmem + kOCol + uint32_t(w * 128);
-        // One thread from here on; items come with Q (nb blocks, nt tiles), so that nothing but MMAs and waits stands here.
-        if (elect_one()) {
-            int done = 0;  // this lane's steps before the item
-            for (;; ++qi) {
-                bool ok = wait_on(&ctl->q_ready, qi & 1);
-                const int item = ok ? *reinterpret_cast<volatile int *>(&ctl->item) : 0, nb = item >> 1;
-                if (nb == 0) break;
-                const bool two = item & 1;
-                const int steps = two ? 2 * nb : 2 * ((nb + 1 - w) >> 1);
-                const uint64_t dq = desc_k(sQ + uint32_t(two ? w * L::TILE : 0));
-                auto block = [&](int u) { return blocks + (two ? u >> 1 : (u & ~1) + w); };
-                auto issue_s = [&](int u) -> bool {
-                    const int j = block(u), h = u & 1;
-                    if (!h && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
-                    tc_fence_after();
-                    const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t(h * (kStep * 128 >> 4));
+        // the MMAs of one item by this lane
+        auto issue_item = [&](auto both, int steps, uint64_t dq, int done) -> bool {
+            constexpr bool TWO = decltype(both)::value;
+            const int from = blocks + (TWO ? 0 : w);
+            bool ok = true;
+            auto issue_s = [&](int u) -> bool {
+                const int j = from + (TWO ? u >> 1 : u & ~1), h = u & 1;
+                if (!h && !wait_on(&ctl->k_full[j & 1], (j >> 1) & 1)) return false;
+                tc_fence_after();
+                const uint64_t db = ((j & 1) ? dk[1] : dk[0]) + uint64_t(h * (kStep * 128 >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < DP / 16; ++kk) {
-                        const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
-                        if (kk < nd) tc_mma_f16(t_s + uint32_t(h * 64), dq + off, db + off, idesc_s, kk > 0);
-                    }
-                    tc_commit(&ctl->s_full[w][h]);
-                    if (h) {
-                        tc_commit(&ctl->k_empty[j & 1]);
-                        if (!two) tc_commit(&ctl->k_empty[j & 1]);
-                    }
-                    if (u == steps - 1) tc_commit(&ctl->q_free);
-                    return true;
-                };
-                if (steps == 0) tc_commit(&ctl->q_free);
-                for (int u = 0; u < 2 && u < steps && ok; ++u) ok = issue_s(u);
-                for (int u = 0; u < steps && ok; ++u) {
-                    const int j = block(u), h = u & 1;
-                    // (P first: its groups have then seen the whole item before end, so that V's parity, whose slot the other
-                    // lane may have used last, is read no earlier than one phase before)
-                    ok = wait_on(&ctl->p_full[w][h], ((done + u) >> 1) & 1) && (h || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t(h * (kStep * 128 >> 4));
-                    const uint32_t p = t_s + uint32_t(h * 64);
-#pragma unroll
-                    for (int kk = 0; kk < kStep / 16; ++kk) {
-                        const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
-                        mma_ts(t_o, p + uint32_t(kk * 8), bk, idesc_o, kk > 0 ? 1u : uint32_t(u > 0));
-                        if constexpr (SPLIT_P) mma_ts(t_o, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
-                    }
-                    tc_commit(&ctl->o_done[w]);
-                    if (u == steps - 1) tc_commit(&ctl->item_done[w]);
-                    if (h) {
-                        tc_commit(&ctl->v_empty[j & 1]);
-                        if (!two) tc_commit(&ctl->v_empty[j & 1]);
-                    }
-                    if (u + 2 < steps) ok = issue_s(u + 2);
+                for (int kk = 0; kk < DP / 16; ++kk) {
+                    const uint64_t off = uint64_t((((kk >> 2) * L::HALF) >> 4) + 2 * (kk & 3));
+                    if (kk < nd) tc_mma_f16(t_s + uint32_t(h * 64), dq + off, db + off, idesc_s, kk > 0);
                 }
+                tc_commit(&ctl->s_full[w][h]);
+                if (h) {
+                    tc_commit(&ctl->k_empty[j & 1]);
+                    if (!TWO) tc_commit(&ctl->k_empty[j & 1]);
+                }
+                if (u == steps - 1) tc_commit(&ctl->q_free);
+                return true;
+            };
+            for (int u = 0; u < 2 && u < steps && ok; ++u) ok = issue_s(u);
+            for (int u = 0; u < steps && ok; ++u) {
+                const int j = from + (TWO ? u >> 1 : u & ~1), h = u & 1;
+                // (P first: its groups have then seen the whole item before end, so that V's parity, whose slot the other
+                // lane may have used last, is read no earlier than one phase before)
+                ok = wait_on(&ctl->p_full[w][h], ((done + u) >> 1) & 1) && (h || wait_on(&ctl->v_ready[j & 1], (j >> 1) & 1));
                 if (!ok) break;
-                blocks += nb;
-                done += steps;
+                tc_fence_after();
+                const uint64_t db = ((j & 1) ? dv[1] : dv[0]) + uint64_t(h * (kStep * 128 >> 4));
+                const uint32_t p = t_s + uint32_t(h * 64);
+#pragma unroll
+                for (int kk = 0; kk < kStep / 16; ++kk) {
+                    const uint64_t bk = db + uint64_t(kk * 2048 >> 4);
+                    mma_ts(t_o, p + uint32_t(kk * 8), bk, idesc_o, kk > 0 ? 1u : uint32_t(u > 0));
+                    if constexpr (SPLIT_P) mma_ts(t_o, p + uint32_t(32 + kk * 8), bk, idesc_o, 1u);
+                }
+                tc_commit(&ctl->o_done[w]);
+                if (u == steps - 1) tc_commit(&ctl->item_done[w]);
+                if (h) {
+                    tc_commit(&ctl->v_empty[j & 1]);
+                    if (!TWO) tc_commit(&ctl->v_empty[j & 1]);
+                }
+                if (u + 2 < steps) ok = issue_s(u + 2);
             }
-            tc_commit(&ctl->drain);  // when all of this lane's MMAs have ended
+            return ok;
+        };
+        // Items come with Q (nb blocks, one or two tiles), so that nothing but MMAs and waits stands here; the warp takes them,
+        // one lane issues.
+        int done = 0;  // this lane's steps before the item
+        for (;; ++qi) {
+            bool ok = __all_sync(0xffffffffu, wait_on(&ctl->q_ready, qi & 1));
+            const int item = ok ? uniform(*reinterpret_cast<volatile int *>(&ctl->item)) : 0, nb = item >> 1;
+            if (nb == 0) break;
+            const bool two = item & 1;
+            const int steps = two ? 2 * nb : 2 * ((nb + 1 - w) >> 1);
+            const uint64_t dq = desc_k(sQ + uint32_t(two ? w * L::TILE : 0));
+            if (elect_one()) {
+                if (steps == 0) tc_commit(&ctl->q_free);
+                ok = two ? issue_item(bool_c<true>{}, steps, dq, done) : issue_item(bool_c<false>{}, steps, dq, done);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            blocks = uniform(blocks + nb);
+            done = uniform(done + steps);
         }
+        if (elect_one()) tc_commit(&ctl->drain);  // when all of this lane's MMAs have ended
         __syncwarp();
     } else if (warp == W_SOFT - 1) {
         // ---- V: slots that some row of the item must not multiply
