@@ -249,7 +249,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
         bool bad = false, ok = true;
         for (; ok && walk.more(); walk.next()) {
             BoxPages boxes(a, walk.b, walk.tile0 * kKeys, kKeys, plan.box_rows, walk.first, walk.last);
-            const int tiles = walk.tiles, g = walk.g;
+            const int tiles = uniform(walk.tiles), g = uniform(walk.g);
+            ring = uniform(ring);
             for (int it = 0; it < tiles; ++it, ++ring) {
                 const int s = ring % kStages, u = ring / kStages;
                 boxes.seek(it);

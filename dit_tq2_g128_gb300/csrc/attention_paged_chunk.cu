@@ -458,23 +458,25 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         bool bad = false, ok = true;
         for (; ok && walk.more(); walk.next()) {
             if (walk.nb == 0) continue;
-            const int nb = walk.nb, g = walk.g;
+            const int nb = uniform(walk.nb), g = uniform(walk.g), nt = uniform(walk.nt);
+            const int q_token = uniform(walk.sp.q0 + walk.row0 / G);
             if (!v && plan.q_copies) {
                 if (qi > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->q_free, (qi - 1) & 1, abort_flag, wait_ns, status));
                 if (!ok) break;
                 if (elect_one()) {
-                    *reinterpret_cast<volatile int *>(&ctl->item) = 2 * nb + (walk.nt == 2);
-                    mbar_expect_tx(&ctl->q_ready, uint32_t(walk.nt * L::TILE));
-                    for (int t = 0; t < walk.nt; ++t)
+                    *reinterpret_cast<volatile int *>(&ctl->item) = 2 * nb + (nt == 2);
+                    mbar_expect_tx(&ctl->q_ready, uint32_t(nt * L::TILE));
+                    for (int t = 0; t < nt; ++t)
 #pragma unroll
                         for (int h = 0; h < L::HALVES; ++h)
-                            tma_rows(sQ + uint32_t(t * L::TILE + h * L::HALF), &qmap, 64 * h, g * G,
-                                     walk.sp.q0 + (walk.row0 + t * kRows) / G, &ctl->q_ready);
+                            tma_rows(sQ + uint32_t(t * L::TILE + h * L::HALF), &qmap, 64 * h, g * G, q_token + t * (kRows / G),
+                                     &ctl->q_ready);
                 }
                 __syncwarp();
             }
             ++qi;
             BoxPages boxes(a, walk.b, walk.block0 * kBlock, kBlock, plan.box_rows, walk.first, walk.last);
+            blocks = uniform(blocks);
             for (int j = 0; j < nb; ++j, ++blocks) {
                 const int s = blocks & 1, u = blocks >> 1;
                 boxes.seek(j);
