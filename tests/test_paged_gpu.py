@@ -555,3 +555,50 @@ def test_operands_off_the_device_are_refused(tq2):
     off = tq2.tq2_batch(step.tables[0], at, step.tables[2], 1, 2, 2, 20, step.table.shape[1])
     assert L.tq2_attention_paged(here, H(step.queries(2).data_ptr(), 2, 128, 64, 1), step.cache.packed, off, 0.1, 0, 1,
                                  None, 0, None) == bad
+
+
+# ---------------------------------------------------------------------------
+# waits that give up, and the operators together
+
+
+@pytest.mark.parametrize("q_len,kv", [(1, 3000), (4, 100), (70, 900), (300, 300), (40, 9000)])
+def test_a_wait_that_runs_out_is_reported_and_the_context_goes_on(tq2, q_len, kv):
+    step = Step(tq2, [q_len, q_len], [kv, kv // 2 + 1], 2, 128, 16)
+    q = step.queries(6)
+    good = tq2.attention_paged(q, step.cache, step.batch)
+    torch.cuda.synchronize()
+    limit = tq2.tq2_set_wait_timeout_ns(0)
+    try:
+        for _ in range(3):
+            tq2.attention_paged(q, step.cache, step.batch)
+        assert tq2.tq2_device_status() in (tq2.TQ2_ERR_TIMEOUT, tq2.TQ2_OK)  # (a wait may find its phase in time)
+    finally:
+        tq2.tq2_set_wait_timeout_ns(limit)
+    again = tq2.attention_paged(q, step.cache, step.batch)
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
+    assert torch.equal(again, good)
+
+
+def test_a_decoder_of_ternary_layers(tq2):
+    """Prompts in chunks and decoding by graph replays give the logits of one pass over everything."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "ternary_decoder.py")
+    spec = importlib.util.spec_from_file_location("ternary_decoder", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    model = ex.Decoder(layers=2, ffn=512, vocab=256)
+    rng = np.random.default_rng(0)
+    prompts = [rng.integers(0, 256, n).tolist() for n in (70, 5, 33)]
+    tokens, _ = ex.generate(model, prompts, 6, chunk=32)
+    tokens = tokens.tolist()
+    # each sequence alone, prompt and continuation in one step: the token after each position is the same, but where
+    # the two best logits are nearer than the activations' binary16 and the cache's bf16 roundings move them
+    for p, row in zip(prompts, tokens):
+        text = p + row
+        seqs = ex.Sequences(1, len(text))
+        logits = model.step(torch.tensor(text, device="cuda"), model.new_caches(seqs.pages), seqs.batch([len(text)]))
+        for i, got in enumerate(row):
+            at = logits[len(p) - 1 + i].double()
+            assert at.max() - at[got] <= 0.05 * at.std(), (len(p), i)
+    assert torch.isfinite(ex.joint_tokens(torch.randn(77 + 64, 3 * 4 * 64, device="cuda"), 4, 64, 77, 8)).all()
