@@ -211,14 +211,14 @@ struct RowWalk {
 };
 
 // DP: features padded to 64 or 128; NT: query rows in eights; SPLIT_P: the weights
-// enter the second product as two terms (f32 outputs).
+// enter the second product as two terms, of bf16 as three (f32 outputs).
 template <typename T, typename TO, int DP, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
 paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                   const PagedArgs a, const RowPlan plan, float *__restrict__ part_o, float2 *__restrict__ part_ml,
                   int *__restrict__ starts, unsigned int *status, uint64_t wait_ns) {
     using L = RowLayout<DP, NT>;
-    constexpr bool SPLIT_P = sizeof(TO) == 4;
+    constexpr bool SPLIT_P = sizeof(TO) == 4, THIRD = SPLIT_P && !is_half<T>;  // (three terms of bf16's 8 bits)
     extern __shared__ uint8_t rows_raw[];
     const uint32_t raw = smem_u32(rows_raw), pad = (1024u - (raw & 1023u)) & 1023u, base = raw + pad;
     uint8_t *smem = rows_raw + pad;
@@ -368,7 +368,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma_16x8<T>(kk & 1 ? sd[t] : sc[t], ka, q[t][kk][0], q[t][kk][1]);
                 }
-                uint32_t ph[NT][2], pl[NT][2];
+                uint32_t ph[NT][2], pl[NT][2], pt[NT][2];
 #pragma unroll
                 for (int t = 0; t < NT; ++t) {
 #pragma unroll
@@ -411,7 +411,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     l[t][0] += p[0] + p[2];
                     l[t][1] += p[1] + p[3];
                     // the weights in the cache's type (the second product's operands have one type); an f32 output
-                    // keeps their remainder as a second term
+                    // keeps their remainder as a second term, and in bf16 a third
                     const uint32_t w0 = pack16<T>(p[0], p[1]), w1 = pack16<T>(p[2], p[3]);
                     ph[t][0] = transpose_8x8(w0);
                     ph[t][1] = transpose_8x8(w1);
@@ -419,8 +419,16 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         float h[4];
                         unpack16<T>(w0, h[0], h[1]);
                         unpack16<T>(w1, h[2], h[3]);
-                        pl[t][0] = transpose_8x8(pack16<T>(p[0] - h[0], p[1] - h[1]));
-                        pl[t][1] = transpose_8x8(pack16<T>(p[2] - h[2], p[3] - h[3]));
+                        const uint32_t l0 = pack16<T>(p[0] - h[0], p[1] - h[1]), l1 = pack16<T>(p[2] - h[2], p[3] - h[3]);
+                        pl[t][0] = transpose_8x8(l0);
+                        pl[t][1] = transpose_8x8(l1);
+                        if constexpr (THIRD) {
+                            float x[4];
+                            unpack16<T>(l0, x[0], x[1]);
+                            unpack16<T>(l1, x[2], x[3]);
+                            pt[t][0] = transpose_8x8(pack16<T>(p[0] - h[0] - x[0], p[1] - h[1] - x[1]));
+                            pt[t][1] = transpose_8x8(pack16<T>(p[2] - h[2] - x[2], p[3] - h[3] - x[3]));
+                        }
                     }
                 }
                 // O^T += V^T P^T
@@ -433,6 +441,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                     for (int t = 0; t < NT; ++t) {
                         mma_16x8<T>(o[t][j], va, ph[t][0], ph[t][1]);
                         if constexpr (SPLIT_P) mma_16x8<T>(o[t][j], va, pl[t][0], pl[t][1]);
+                        if constexpr (THIRD) mma_16x8<T>(o[t][j], va, pt[t][0], pt[t][1]);
                     }
                 }
                 if (!clean) fence_proxy_async_smem();  // this warp wrote where the next copies land

@@ -497,7 +497,8 @@ int tq2_kv_append(const tq2_heads *q, const tq2_heads *q_out, const tq2_heads *k
  *           strides multiples of 8
  *   scale : finite (usually 1/sqrt(dim))
  * Scores, softmax statistics and sums are f32; the weights enter the second
- * product in the cache's type, or, for an f32 out, as a sum of two such terms.
+ * product in the cache's type, or, for an f32 out, as a sum of two such terms (of
+ * three in bf16 where a sequence and key head have at most 16 query rows).
  * Memory: `workspace` holds partial results of long contexts
  * (tq2_attention_paged_workspace_bytes of the same arguments, 16-byte aligned);
  * if NULL, a temporary from the device's pool is taken instead. */
