@@ -5,19 +5,20 @@
 // a CTA takes all of them at once: S^T = K Q^T, P = exp2(S log2(e) scale - m),
 // O^T += V^T P^T over tiles of 64 keys, with the running maximum m and sum l of
 // the softmax.  Keys are the rows (M) of both products and the query rows their
-// columns (N = 8 or 16): decoding wastes no tensor rows as it would with the
+// columns (N = 8 to 32): decoding wastes no tensor rows as it would with the
 // queries in M.
 //
-// Bound by memory: 2 R flops per byte of cache at 16 bits, below the legacy
-// tensor path's rate up to R = 16 (the tcgen05 path of attention_paged_tc.cu
-// needs 128 rows in M and takes over above).
+// Bound by memory: 2 R flops per byte of cache at 16 bits, below the warp-level
+// tensor path's rate for few rows.  The tcgen05 path (attention_paged_chunk.cu) needs
+// 128 rows in M and takes over above rows_max.
 //
 // Work is shared out evenly: the (sequence, key head) pairs' tiles, in one line, are
 // cut into as many equal runs as there are CTAs (two an SM), wherever that falls; a
 // pair that is cut leaves (m, l, O) of its pieces in the workspace and a second,
 // dependent launch joins them in order.  So a batch of very different lengths keeps
 // every SM busy to the end, and a CTA starts once.  (Cut into chunks of 1024 keys, 64
-// sequences of 3000 keys took 135 us and 121 in one chunk each; shared out: DESIGN.)
+// sequences of 3000 keys, eight key heads of 128, took 135 us; shared out 123 us, 94 %
+// of the copy rate.)
 //
 // A CTA has four consumer warps of 16 keys each a tile and one producer warp, which
 // runs ahead through all of the CTA's pairs.  It looks pages up 32 boxes at a time and
@@ -48,7 +49,15 @@ constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kCtas = 2 * kNumSms;
 constexpr int kMinTiles = 4;    // units of a run, at least, where pairs may be cut
 constexpr int kWholeKeys = 512; // up to so many keys a pair stays whole (a join costs more than a CTA saves)
-constexpr int kRowsMax = 16;    // query rows per (sequence, key head) that this kernel takes
+
+// Query rows per (sequence, key head) that this kernel takes; more go to the tcgen05
+// kernel.  The limit is where O and S of a warp's 16 keys stop fitting its registers (168
+// a thread at two CTAs an SM): 32 rows of 64 features, 16 of 128.  Measured, this kernel
+// against that one: 28 rows of 64, 16 sequences of 1000 keys 13.7 / 16.2 us, 32 rows, 64
+// of 2000 keys 90 / 100, 21 rows, 16 of 1000 11.5 / 16.2 (8 of 200 keys, 32 rows: 9.8 /
+// 8.9); 40 rows of 64, spilled, 64 of 2000 keys 126 / 100; 16 rows of 128, 64 of 2000
+// keys 100 / 123; 24 rows of 128, spilled, 153 / 123.
+constexpr int64_t rows_max(int64_t dim) { return dim <= 64 ? 32 : 16; }
 
 template <int DP, int NT>
 struct RowLayout {
@@ -597,8 +606,14 @@ cudaError_t launch_rows_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
     CUtensorMap km, vm;
     cudaError_t e = cache_maps<T>(a, r.plan.box_rows, &km, &vm);
     if (e != cudaSuccess) return e;
-    if (a.dim <= 64) return rows <= 8 ? launch_rows<T, TO, 64, 1>(a, r, km, vm, ws, ctx) : launch_rows<T, TO, 64, 2>(a, r, km, vm, ws, ctx);
-    return rows <= 8 ? launch_rows<T, TO, 128, 1>(a, r, km, vm, ws, ctx) : launch_rows<T, TO, 128, 2>(a, r, km, vm, ws, ctx);
+    if (a.dim <= 64) {
+        if (rows <= 8) return launch_rows<T, TO, 64, 1>(a, r, km, vm, ws, ctx);
+        if (rows <= 16) return launch_rows<T, TO, 64, 2>(a, r, km, vm, ws, ctx);
+        if (rows <= 24) return launch_rows<T, TO, 64, 3>(a, r, km, vm, ws, ctx);
+        return launch_rows<T, TO, 64, 4>(a, r, km, vm, ws, ctx);
+    }
+    if (rows <= 8) return launch_rows<T, TO, 128, 1>(a, r, km, vm, ws, ctx);
+    return launch_rows<T, TO, 128, 2>(a, r, km, vm, ws, ctx);
 }
 
 }  // namespace
@@ -606,13 +621,13 @@ cudaError_t launch_rows_io(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
 size_t attention_paged_ws_bytes(int64_t heads, int64_t kv_heads, int64_t dim, int64_t seqs, int64_t tokens, int64_t max_q,
                                 int64_t max_kv) {
     const int64_t rows = std::min(max_q, tokens) * (heads / kv_heads);
-    if (rows > kRowsMax) return attention_paged_chunk_ws_bytes(heads, kv_heads, dim, seqs, tokens, std::min(max_q, tokens), max_kv);
+    if (rows > rows_max(dim)) return attention_paged_chunk_ws_bytes(heads, kv_heads, dim, seqs, tokens, std::min(max_q, tokens), max_kv);
     const RowLaunch r = row_launch(kv_heads, seqs, rows, max_kv, 1);  // (a window only shortens the span)
     return r.plan.split ? row_ws_bytes(seqs, rows, dim, r.ctas) : 0;
 }
 
 cudaError_t launch_attention_paged(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx) {
-    if (int64_t(a.batch.max_q) * (a.heads / a.kv_heads) > kRowsMax) return launch_attention_paged_chunk(a, dtype, out_f32, ws, ctx);
+    if (int64_t(a.batch.max_q) * (a.heads / a.kv_heads) > rows_max(a.dim)) return launch_attention_paged_chunk(a, dtype, out_f32, ws, ctx);
     if (dtype == TQ2_F16) {
         if (out_f32) return launch_rows_io<__half, float>(a, ws, ctx);
         return launch_rows_io<__half, __half>(a, ws, ctx);

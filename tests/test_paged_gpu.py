@@ -355,6 +355,15 @@ def test_long_contexts_are_split_and_joined(tq2):
             assert torch.equal(again, o), "another run gives other bits"
 
 
+@pytest.mark.parametrize("new,heads", [(8, 1), (3, 3), (16, 1), (17, 1), (3, 8), (5, 5), (4, 8), (11, 3)], ids=str)
+@pytest.mark.parametrize("dim", [64, 48, 128])
+@pytest.mark.parametrize("types", [("f16", "f16"), ("bf16", "f32")], ids=str)
+def test_row_counts_about_the_kernels_limits(tq2, new, heads, dim, types):
+    for kv_len, window in (([40, new, 700], 0), ([3000, 5, 64], 150)):
+        step = Step(tq2, [new] * 3, kv_len, 1, dim, 16, dtype=types[0], seed=new + heads)
+        attend(tq2, step, heads, types[1], window, sharp=2.0)
+
+
 def attend_again(tq2, step, q, o):
     """The same call with a temporary instead of a workspace."""
     again = torch.empty_like(o)
