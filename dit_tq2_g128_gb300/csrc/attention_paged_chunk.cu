@@ -7,8 +7,12 @@
 // for all G heads at once.
 //
 //  * An item is up to 256 consecutive rows (two tiles) of one (sequence, key head).
-//    Where the items fill the SMs a CTA takes one, the longest first.  Where they are few
-//    and long their blocks of 128 keys, in one line with the cost of an item's start
+//    Where the items fill the SMs they stay whole, a CTA of the grid for each, a
+//    sequence's longest first; a CTA near its item's end takes over one that has not started
+//    (a cluster launch control request), so that copies, lookups and set-up of the next item run
+//    under this one's end: 8 us between items became 6 (one prompt of 4096 tokens 117 -> 107
+//    us, 16 of 512 101 -> 86, ragged prompts 242 -> 227).  Where they are few and long their
+//    blocks of 128 keys, in one line with the cost of an item's start
 //    and end, are cut into as many equal runs as there are SMs, and a CTA takes a run: it
 //    starts once, copies ahead into its next item, and its next Q comes as soon as the
 //    last S that reads the old one has ended; pieces of a cut item go to the workspace
@@ -17,7 +21,7 @@
 //  * Warps 0 and 12 copy K and V through two-stage rings by paged tensor copies (boxes
 //    of rows inside one page), warp 0 Q too; warps 1 and 2 issue the MMAs of lane 0 and
 //    1 (below); warp 3 looks after V; warps 4-7 and 8-11 are the lanes' softmax groups,
-//    one thread per row (= tensor-memory lane).
+//    one thread per row (= tensor-memory lane).  Warp 13 claims whole items.
 //  * Lanes: with two tiles, lane w is tile w and walks every block; with one tile, lane
 //    w walks the blocks 2i + w, so one tile keeps both softmax groups busy as well (they
 //    meet at the end).  A lane walks in steps of 64 keys (half a block), each step with
@@ -55,15 +59,17 @@ constexpr int kRows = 128;      // rows of a tile (MMA M)
 constexpr int kBlock = 128;     // keys of a block (copies)
 constexpr int kStep = 64;       // keys of a step (MMAs, softmax)
 constexpr int kCtaRows = 2 * kRows;
-constexpr int kThreads = 416;
-constexpr int kStartUnits = 4;  // an item's start and end, in blocks, for the shares (2: 207 and 277 us, 4: 207 and 248, 8: 213 and 271
-                                // for 512 tokens over 32768 keys and for ragged prompts)
+constexpr int kThreads = 448;
+constexpr int kClaimAhead = 4;  // blocks before an item's end at which the CTA asks for its next one
+// An item's start and end, in blocks, for the shares of cut items (512 tokens over 32768 keys, and ragged prompts if cut:
+// 2 took 207 and 277 us, 4 207 and 248, 8 213 and 271 when measured, the former 195 since).
+constexpr int kStartUnits = 4;
 constexpr int kMinUnits = 4;    // units of a run, at least, where items may be cut
 constexpr int kJoinRows = 4;    // rows of a warp of the join
 constexpr int kJoinParts = kCtaRows / (kJoinRows * kJoinWarps);  // its blocks per cut item
 constexpr uint32_t kTmemCols = 512, kOCol = 256;
 constexpr float kLazy = 8.f;    // log2 growth of the maximum that O is rescaled for
-constexpr int W_K = 0, W_MMA = 1, W_SOFT = 4, W_V = 12;  // W_MMA + lane; warp 3 looks after V
+constexpr int W_K = 0, W_MMA = 1, W_SOFT = 4, W_V = 12, W_CLAIM = 13;  // W_MMA + lane; warp 3 looks after V
 
 template <int DP>
 struct ChunkLayout {
@@ -73,11 +79,20 @@ struct ChunkLayout {
     static constexpr int OFF_K = 2 * TILE, OFF_V = OFF_K + 2 * TILE;
     static constexpr int OFF_STAGE = OFF_V + 2 * TILE; // 4 KB a softmax warp, for rows on their way out
     static constexpr int OFF_CTL = OFF_STAGE + 8 * 4096;
-    static constexpr int BYTES = OFF_CTL + 256 + 1024;
+    static constexpr int BYTES = OFF_CTL + 512 + 1024;
     static_assert(BYTES <= 232448, "shared memory budget");
 };
 
+// An item of a prompt: rows from row0 on of a sequence (its first token, its new tokens, its keys) and a key head; left:
+// 1, or 0 where there is none.
+struct alignas(16) Item {
+    int b, row0, g, left, q0, n, kv, unused;
+};
+
 struct ChunkCtl {
+    uint4 answer;            // to the request for another CTA's item
+    Item next[3];            // whole items: the first in [2], those after it in [0] and [1] in turn
+    uint64_t answered, want, item_full[2], item_free[2];
     uint64_t q_ready, q_free, k_full[2], k_empty[2], v_full[2], v_ready[2], v_empty[2];
     uint64_t s_full[2][2], p_full[2][2], o_done[2], drain;  // [lane][step & 1]
     uint64_t item_done[2];   // a lane's last P V of an item has ended
@@ -85,9 +100,10 @@ struct ChunkCtl {
     int abort;
     int poisoned[4];         // by item (of those with blocks, from 1 on) modulo 4: the last whose V had values taken out
     int item;                // the item that q_ready announces: twice its blocks, one more for two tiles; 0: the run is over
+    int soft_go[2];          // the softmax groups go on with next[.]
     int b, row0, g, u, left; // where this CTA's run begins: sequence, rows, key head, unit; its units
 };
-static_assert(sizeof(ChunkCtl) <= 256, "control block");
+static_assert(sizeof(ChunkCtl) <= 512, "control block");
 
 // Matrix descriptors (128-byte swizzle).  K-major: rows 128 B apart, 8-row groups
 // 1024 B.  MN-major: 64 features contiguous, keys 128 B apart; 8-key groups 1024 B
@@ -102,6 +118,53 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t saddr, uint32_t half) {
 }
 
 __device__ __forceinline__ void groups_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }  // both softmax groups
+
+// A wait as wait_phase's for what takes an item's time: it leaves the schedulers alone.
+__device__ __forceinline__ bool doze_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint64_t wait_ns, unsigned int *status) {
+    const uint32_t addr = smem_u32(bar);
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(addr), "r"(parity)
+            : "memory");
+        if (ok) return true;
+        if (*abort_flag) return false;
+        if (globaltimer_ns() - t0 >= wait_ns) {
+            atomicOr(status, static_cast<unsigned int>(TQ2_ERR_TIMEOUT));
+            *abort_flag = 1;
+            return false;
+        }
+        __nanosleep(500);
+    }
+}
+
+// Asks for a CTA of this grid that has not started, to be done here in its place; the answer comes by bulk copy.
+__device__ __forceinline__ void request_cta(uint4 *answer, uint64_t *bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// Its index, or -1: there is none left (no request may follow).
+__device__ __forceinline__ int requested_cta(const uint4 *answer) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t"
+        "mov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return got ? int(x) : -1;
+}
 
 // 64 features of a tile's rows of Q: feature x, head, token
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap *map, int x, int head, int token, uint64_t *bar) {
@@ -202,40 +265,62 @@ __device__ __forceinline__ ItemSpan item_of(const PagedArgs &a, const SeqSpan &s
     return item_span(sp, a.heads / a.kv_heads, row0, kCtaRows, a.window, a.causal, kBlock);
 }
 
-// The run of this CTA (one warp): `left` units from unit u of item (b, row0, g) on.
-__device__ __forceinline__ void find_run(const PagedArgs &a, const ChunkPlan &plan, ChunkCtl *ctl, unsigned int *status) {
-    const BatchView &bt = a.batch;
-    const int lane = threadIdx.x & 31, G = a.heads / a.kv_heads;
-    if (!plan.split) {  // item blockIdx.x of all: from the last sequence's last tile (the longest of a prompt) on
-        int from = int(blockIdx.x);
-        if (lane == 0) ctl->left = 0;
-        for (int top = bt.seqs; top > 0; top -= 32) {
+// Items in the order of a grid that takes them whole (one warp): from the last sequence's last tile (the longest of a
+// prompt) on, key heads innermost.  Successive indices mostly rise: the search goes on from where it stands.
+struct ItemFinder {
+    const PagedArgs &a;
+    const int G;
+    int top, passed;  // sequences below top are left; the others' items
+
+    __device__ __forceinline__ explicit ItemFinder(const PagedArgs &args) : a(args), G(args.heads / args.kv_heads), top(args.batch.seqs), passed(0) {}
+    __device__ __forceinline__ Item find(int index, unsigned int *status) {
+        const BatchView &bt = a.batch;
+        const int lane = threadIdx.x & 31;
+        if (index < passed) {
+            top = bt.seqs;
+            passed = 0;
+        }
+        for (; top > 0; top -= 32) {
             const int b = top - 1 - lane;
-            int tiles = 0;
+            SeqSpan sp{0, 0, 0};
             if (b >= 0) {
                 bool bad = false;
-                tiles = tiles_in(seq_span(bt, b, bad), G);
+                sp = seq_span(bt, b, bad);
                 report_bad(bad, status);
             }
+            const int tiles = tiles_in(sp, G);
             int upto = tiles * a.kv_heads;  // inclusive over the lanes
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, upto, d);
                 if (lane >= d) upto += x;
             }
-            const unsigned hit = __ballot_sync(0xffffffffu, from < upto);
+            const unsigned hit = __ballot_sync(0xffffffffu, index - passed < upto);
             if (hit) {
-                if (lane == __ffs(hit) - 1) {
-                    const int at = from - (upto - tiles * a.kv_heads);
-                    ctl->b = b;
-                    ctl->row0 = (tiles - 1 - at / a.kv_heads) * kCtaRows;
-                    ctl->g = at % a.kv_heads;
-                    ctl->u = 0;
-                    ctl->left = 1;
-                }
-                return;
+                const int l = __ffs(hit) - 1, at = index - passed - __shfl_sync(0xffffffffu, upto - tiles * a.kv_heads, l);
+                return Item{top - 1 - l, (__shfl_sync(0xffffffffu, tiles, l) - 1 - at / a.kv_heads) * kCtaRows, at % a.kv_heads, 1,
+                            __shfl_sync(0xffffffffu, sp.q0, l), __shfl_sync(0xffffffffu, sp.n, l), __shfl_sync(0xffffffffu, sp.kv, l), 0};
             }
-            from -= __shfl_sync(0xffffffffu, upto, 31);
+            passed += __shfl_sync(0xffffffffu, upto, 31);
+        }
+        return Item{0, 0, 0, 0, 0, 0, 0, 0};
+    }
+};
+
+// The run of this CTA (one warp): `left` units from unit u of item (b, row0, g) on.
+template <bool SPLIT>
+__device__ __forceinline__ void find_run(const PagedArgs &a, ChunkCtl *ctl, unsigned int *status) {
+    const BatchView &bt = a.batch;
+    const int lane = threadIdx.x & 31, G = a.heads / a.kv_heads;
+    if (!SPLIT) {  // item blockIdx.x of all
+        const Item it = ItemFinder(a).find(int(blockIdx.x), status);
+        if (lane == 0) {
+            ctl->b = it.b;
+            ctl->row0 = it.row0;
+            ctl->g = it.g;
+            ctl->u = 0;
+            ctl->left = it.left;
+            ctl->next[2] = it;
         }
         return;
     }
@@ -316,7 +401,7 @@ __device__ __forceinline__ void find_run(const PagedArgs &a, const ChunkPlan &pl
     }
 }
 
-// A CTA's run, item by item: every role walks it by itself (whole warps).
+// A CTA's run of cut items, or a whole item, part by part: every role walks it by itself (whole warps).
 struct ChunkWalk {
     const PagedArgs &a;
     const ChunkPlan &plan;
@@ -340,6 +425,16 @@ struct ChunkWalk {
         bool ignore = false;
         const SeqSpan s = seq_span(a.batch, b, ignore);  // (reported by find_run)
         sp = SeqSpan{uniform(s.q0), uniform(s.n), uniform(s.kv)};
+    }
+    // another whole item
+    __device__ __forceinline__ void begin(const Item *next) {
+        b = uniform(next->b);
+        row0 = uniform(next->row0);
+        g = uniform(next->g);
+        u = 0;
+        left = uniform(next->left);
+        sp = SeqSpan{uniform(next->q0), uniform(next->n), uniform(next->kv)};
+        if (left > 0) tile();
     }
     __device__ __forceinline__ void tile() {
         it = item_of(a, sp, row0);
@@ -392,7 +487,7 @@ struct bool_c {
     static constexpr bool value = B;
 };
 
-template <typename T, typename TO, int DP>
+template <typename T, typename TO, int DP, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, const PagedArgs a, const ChunkPlan plan,
@@ -427,6 +522,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             mbar_init(&ctl->item_done[s], 1);
         }
         mbar_init(&ctl->drain, 2);
+        mbar_init(&ctl->answered, 1);
+        mbar_init(&ctl->want, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl->item_full[s], 1);
+            mbar_init(&ctl->item_free[s], 2 + 1 + 2 * kRows / 32);  // K's, V's and V's second warp, the softmax groups
+        }
         ctl->abort = 0;
         for (int &p : ctl->poisoned) p = 0;
         fence_mbarrier_init();
@@ -440,7 +541,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (warp == 0) {
-        find_run(a, plan, ctl, status);
+        find_run<SPLIT>(a, ctl, status);
         if (lane < 2 && pieces) pieces[2 * blockIdx.x + lane] = make_int4(0, 0, 0, 0);
     }
     tc_fence_before();
@@ -450,7 +551,21 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     ChunkWalk walk(a, plan, ctl);
     // Counters that run on over the items: blocks copied (slot = parity), this lane's steps (even an item), and the
     // items that have blocks (Q's phases).
-    int blocks = 0, qi = 0;
+    int blocks = 0, qi = 0, claims = 0;
+    // The item after the current one, for the roles of one warp: of the run, or as the claiming warp says.
+    auto next_item = [&](bool &ok) {
+        walk.next();
+        if constexpr (!SPLIT) {
+            if (!ok) return;
+            const int slot = claims & 1;
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->item_full[slot], (claims >> 1) & 1, abort_flag, wait_ns, status));
+            if (!ok) return;
+            walk.begin(&ctl->next[slot]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->item_free[slot]);
+            ++claims;
+        }
+    };
 
     if (warp == W_K || warp == W_V) {
         // ---- copies of one plane (a warp each: K's slots and V's are freed at different times), and Q by K's warp
@@ -458,8 +573,12 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         const CUtensorMap *map = v ? &vmap : &kmap;
         uint64_t *const full = v ? ctl->v_full : ctl->k_full, *const empty = v ? ctl->v_empty : ctl->k_empty;
         bool bad = false, ok = true;
-        for (; ok && walk.more(); walk.next()) {
-            if (walk.nb == 0) continue;
+        for (; ok && walk.more(); next_item(ok)) {
+            const int claim = !v && !SPLIT ? max(0, walk.nb - kClaimAhead) : -1;
+            if (walk.nb == 0) {
+                if (claim == 0 && lane == 0) mbar_arrive(&ctl->want);
+                continue;
+            }
             const int nb = uniform(walk.nb), g = uniform(walk.g), nt = uniform(walk.nt);
             const int q_token = uniform(walk.sp.q0 + walk.row0 / G);
             if (!v && plan.q_copies) {
@@ -482,6 +601,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             for (int j = 0; j < nb; ++j, ++blocks) {
                 const int s = blocks & 1, u = blocks >> 1;
                 boxes.seek(j);
+                if (j == claim && lane == 0) mbar_arrive(&ctl->want);
                 if (u > 0) ok = __all_sync(0xffffffffu, wait_phase(&empty[s], (u - 1) & 1, abort_flag, wait_ns, status));
                 if (!ok) break;
                 const uint32_t dst = (v ? sV : sK) + uint32_t(s * L::TILE);
@@ -598,7 +718,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
     } else if (warp == W_SOFT - 1) {
         // ---- V: slots that some row of the item must not multiply
         bool ok = true;
-        for (; ok && walk.more(); walk.next()) {
+        for (; ok && walk.more(); next_item(ok)) {
             if (walk.nb == 0) continue;
             ++qi;
             const RowSpan rs = walk.it.see;
@@ -633,6 +753,45 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 if (lane == 0) mbar_arrive(&ctl->v_ready[slot]);
             }
         }
+    } else if (warp == W_CLAIM) {
+        // ---- claims whole items, one at a time: CTAs of this grid that have not started are taken over, so that the next
+        // item's copies run under this one's end
+        if constexpr (!SPLIT) if (walk.left > 0) {
+            ItemFinder finder(a);
+            uint32_t asked = 0;
+            for (;; ++claims) {
+                const int slot = claims & 1;
+                bool ok = __all_sync(0xffffffffu, doze_phase(&ctl->want, claims & 1, abort_flag, wait_ns, status));
+                if (ok && claims >= 2)
+                    ok = __all_sync(0xffffffffu, wait_phase(&ctl->item_free[slot], ((claims >> 1) - 1) & 1, abort_flag, wait_ns, status));
+                if (!ok) break;
+                Item it = {};
+                for (int index = 0; index >= 0 && it.left == 0; ++asked) {  // (indices past the last item have none)
+                    if (lane == 0) {
+                        mbar_expect_tx(&ctl->answered, 16);
+                        request_cta(&ctl->answer, &ctl->answered);
+                    }
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, wait_phase(&ctl->answered, asked & 1, abort_flag, wait_ns, status));
+                    if (!ok) break;
+                    index = uniform(requested_cta(&ctl->answer));
+                    fence_proxy_async_smem();  // (read before the next answer is written)
+                    __syncwarp();
+                    if (index >= 0) it = finder.find(index, status);
+                }
+                if (!ok) {  // the answer must not come after the CTA has left
+                    if (lane == 0) mbar_wait_bounded(&ctl->answered, asked & 1, drain_ns(wait_ns), status);
+                    __syncwarp();
+                    break;
+                }
+                if (lane == 0) {
+                    ctl->next[slot] = it;
+                    mbar_arrive(&ctl->item_full[slot]);
+                }
+                __syncwarp();
+                if (it.left == 0) break;
+            }
+        }
     } else {
         // ---- softmax groups.  After a wait that was given up a warp walks on without waiting or computing, so that every
         // warp meets every barrier.
@@ -644,9 +803,34 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         // scores stay unscaled; scale2 > 0 enters with the exponential (a zero scale as a tiny one, so that -inf stays)
         const float scale2 = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
         const uint64_t scale22 = pair(scale2, scale2);
-        int done = 0, ended = 0;  // this lane's steps, and its items with steps, before the item
+        uint32_t phase = 0;  // bit 0: this lane's pairs of steps before the item (they are even), bit 1: its items with steps, modulo 2
         bool ok = true;
-        for (; walk.more(); walk.next()) {
+        // one warp's wait decides for both groups whether there is a next item: all of them meet the same barriers
+        auto next_of_groups = [&]() {
+            if constexpr (SPLIT) {
+                walk.next();
+            } else {
+                const int slot = claims & 1;
+                if (warp == W_SOFT) {
+                    const bool got = __all_sync(0xffffffffu, wait_phase(&ctl->item_full[slot], (claims >> 1) & 1, abort_flag, wait_ns, status));
+                    if (lane == 0) ctl->soft_go[slot] = got;
+                    __syncwarp();
+                }
+                groups_sync();
+                if (claims > 0 && lane == 0) mbar_arrive(&ctl->item_free[slot ^ 1]);  // (the one before is done with)
+                if (*reinterpret_cast<volatile int *>(&ctl->soft_go[slot])) ++claims;
+                else claims = -1;
+            }
+        };
+        for (;; next_of_groups()) {
+        if constexpr (!SPLIT) {
+            if (claims < 0) {
+                ok = false;
+                break;
+            }
+            walk.begin(&ctl->next[claims == 0 ? 2 : (claims - 1) & 1]);
+        }
+        if (!walk.more()) break;
         if (walk.skip()) continue;
         const SeqSpan sp = walk.sp;
         const RowSpan rs = walk.it.see;
@@ -698,7 +882,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (nb > 0) ++qi;
         float m = -INFINITY, l = 0.f;
         for (int u = 0; u < steps && ok; ++u) {
-            ok = __all_sync(0xffffffffu, wait_phase(&ctl->s_full[w][u & 1], ((done + u) >> 1) & 1, abort_flag, wait_ns, status));
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->s_full[w][u & 1], (phase ^ uint32_t(u >> 1)) & 1, abort_flag, wait_ns, status));
             if (!ok) break;
             tc_fence_after();
             const int key0 = (walk.block0 + walk.block(w, u)) * kBlock + (u & 1) * kStep;
@@ -746,7 +930,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             if constexpr (SPLIT_P) tm_st32(ts + uint32_t((u & 1) * 64 + 32), lp);
             if (u > 0 && __any_sync(0xffffffffu, grow)) {
                 // rescale this row of O (rows that keep m by 1) once the step before has accumulated into it
-                ok = __all_sync(0xffffffffu, wait_phase(&ctl->o_done[w], (done + u - 1) & 1, abort_flag, wait_ns, status));
+                ok = __all_sync(0xffffffffu, wait_phase(&ctl->o_done[w], (u - 1) & 1, abort_flag, wait_ns, status));
                 if (!ok) break;
                 tc_fence_after();
 #pragma unroll 1
@@ -771,11 +955,11 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         if (ok && steps > 0) {
             // (a barrier of its own: P V of the last two steps may both have ended by now, and a parity tells a phase only
             // from its neighbours)
-            ok = __all_sync(0xffffffffu, wait_phase(&ctl->item_done[w], ended & 1, abort_flag, wait_ns, status));
-            ++ended;
+            ok = __all_sync(0xffffffffu, wait_phase(&ctl->item_done[w], phase >> 1, abort_flag, wait_ns, status));
+            phase ^= 2;
             tc_fence_after();
         }
-        done += steps;
+        phase ^= uint32_t(steps >> 1) & 1;
         // one tile: the groups hold the softmax of the even and odd blocks of the same rows (and tensor-memory lanes);
         // each learns the other's m and l, and they take the output's pieces in turn
         float scale_own = 1.f, scale_other = 0.f;
@@ -894,7 +1078,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
         }
         // the next item's first P V writes over O: not before this group (one tile: both groups) has read it
         tc_fence_before();
-        if (nt == 1) groups_sync();
+        if (nt == 1 && SPLIT) groups_sync();  // (whole items: they meet before the next one)
         }
         if (!plan.q_copies && warp == W_SOFT && ok) {  // the run is over
             if (qi > 0) ok = __all_sync(0xffffffffu, wait_phase(&ctl->q_free, (qi - 1) & 1, abort_flag, wait_ns, status));
@@ -1013,8 +1197,8 @@ int64_t tile_bound(int64_t group, int64_t seqs, int64_t tokens) {
 // Items are cut where one CTA an item would leave the SMs idle for longer than cutting
 // costs: with fewer than two turns of items, the last turn's idle share times an item's
 // blocks (1.7 us each), against about 14 us for the partial results and the join.  Measured:
-// 512 tokens over 32768 keys, 8 key heads (64 items of 256 blocks) 207 us cut and 229
-// chunked without; 1216 tokens over 8192 (152 items) 131 cut, 101 whole; 1024 of a
+// 512 tokens over 32768 keys, 8 key heads (64 items of 256 blocks) 207 us cut (195 since)
+// and 229 in chunks of keys; 1216 tokens over 8192 (152 items) 131 cut, 101 whole (97 since); 1024 of a
 // prompt (128 items of up to 8 blocks) 34 cut, 23 whole.
 ChunkLaunch chunk_launch(int64_t items, int64_t max_q, int64_t span) {
     ChunkLaunch r = {};
@@ -1061,7 +1245,7 @@ cudaError_t launch_chunk(const PagedArgs &a, void *ws, const LaunchCtx &ctx) {
     cudaError_t e = cache_maps<T>(a, r.plan.box_rows, &km, &vm);
     if (e == cudaSuccess && r.plan.q_copies) e = q_map<T>(a, &qm);
     if (e != cudaSuccess) return e;
-    auto kernel = paged_chunk_kernel<T, TO, DP>;
+    auto kernel = r.plan.split ? paged_chunk_kernel<T, TO, DP, true> : paged_chunk_kernel<T, TO, DP, false>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
     if (e != cudaSuccess) return e;
     const int64_t slots = 2 * int64_t(r.ctas) * kCtaRows;

@@ -364,6 +364,47 @@ def test_row_counts_about_the_kernels_limits(tq2, new, heads, dim, types):
         attend(tq2, step, heads, types[1], window, sharp=2.0)
 
 
+# more items than SMs, so that CTAs go on from one to the next: short and long, one tile and two, without keys, of no token
+MANY = [
+    # new tokens, kv lengths, heads, kv heads, dim, window
+    ([70, 1, 0, 129, 33, 300] * 7, [70, 500, 9, 129, 40, 700] * 7, 8, 8, 64, 0),
+    ([300, 40] * 12, [100, 390] * 12, 24, 8, 128, 0),    # three heads a group, tokens that see no key
+    ([65] * 70, [64 + i % 90 for i in range(70)], 16, 4, 40, 50),
+    ([1100, 5, 900], [1100, 5, 1500], 40, 10, 64, 0),
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"{len(c[0])}x{c[3]}x{c[4]}")
+@pytest.mark.parametrize("types", [("f16", "f16"), ("bf16", "f32")], ids=str)
+def test_more_items_than_sms(tq2, case, types):
+    q_len, kv_len, heads, kv_heads, dim, window = case
+    step = Step(tq2, q_len, kv_len, kv_heads, dim, 16, dtype=types[0], seed=dim)
+    q, o = attend(tq2, step, heads, types[1], window, sharp=2.0)
+    again = torch.empty_like(o)
+    for _ in range(5):
+        again.fill_(float("nan"))
+        tq2.attention_paged(q, step.cache, step.batch, out=again, window=window)
+        assert torch.equal(again, o), "another run gives other bits"
+
+
+@pytest.mark.parametrize("limit_ns", [0, 20_000])
+def test_waits_that_run_out_between_items(tq2, limit_ns):
+    step = Step(tq2, [260, 70, 300] * 20, [700, 70, 5000] * 20, 4, 64, 16)
+    q = step.queries(12)
+    good = tq2.attention_paged(q, step.cache, step.batch)
+    torch.cuda.synchronize()
+    limit = tq2.tq2_set_wait_timeout_ns(limit_ns)
+    try:
+        for _ in range(3):
+            tq2.attention_paged(q, step.cache, step.batch)
+        assert tq2.tq2_device_status() in (tq2.TQ2_ERR_TIMEOUT, tq2.TQ2_OK)  # (a wait may find its phase in time)
+    finally:
+        tq2.tq2_set_wait_timeout_ns(limit)
+    again = tq2.attention_paged(q, step.cache, step.batch)
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
+    assert torch.equal(again, good)
+
+
 def attend_again(tq2, step, q, o):
     """The same call with a temporary instead of a workspace."""
     again = torch.empty_like(o)
