@@ -279,8 +279,9 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
             }
         }
         report_bad(bad, status);
-        // what was issued lands before the CTA ends (given up: nobody else waits for it)
-        if (!ok && lane == 0)
+        // What was issued lands before the CTA ends, whoever gave up: with three tiles or fewer this warp has waited for
+        // nothing, so a consumer's wait may have run out unseen here.  (Else the consumers wait for the same phases.)
+        if (lane == 0)
             for (int t = max(0, ring - kStages); t < ring; ++t)
                 mbar_wait_bounded(&ctl->full[t % kStages], (t / kStages) & 1, drain_ns(wait_ns), status);
         return;

@@ -1,0 +1,55 @@
+"""GPU tests of the paged operators where calls go wrong or nearly so: waits that run out, tables that contradict one
+another, weights near the end of a type's range, layouts that interleave.  Tolerances as in test_paged_gpu.py; where a
+test needs a tighter one, its derivation stands beside it."""
+
+import numpy as np
+import pytest
+
+from oracle import paged
+from test_paged_gpu import DT, Step, attention_tol, check, half_step, host
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tq2():
+    import dit_tq2_g128_gb300 as m
+    return m
+
+
+@pytest.fixture(autouse=True)
+def status_is_clean(tq2):
+    yield
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
+
+
+class Limit:
+    """A limit on the device's waits, put back at the end."""
+
+    def __init__(self, tq2, ns):
+        self.tq2, self.ns = tq2, ns
+
+    def __enter__(self):
+        torch.cuda.synchronize()
+        self.before = self.tq2.tq2_set_wait_timeout_ns(self.ns)
+
+    def __exit__(self, *_):
+        self.tq2.tq2_set_wait_timeout_ns(self.before)
+
+
+@pytest.mark.parametrize("kv", [40, 100, 190])
+def test_copies_land_before_a_cta_that_gave_up_is_gone(tq2, kv):
+    """Runs of one to three tiles, whose producer never waits: what they copied must not land in the shared memory of
+    the CTAs that come next."""
+    few = Step(tq2, [4] * 40, [kv] * 40, 8, 128, 16)
+    many = Step(tq2, [130, 40], [200, 90], 4, 128, 16, seed=1)
+    q, r = few.queries(16), many.queries(4)
+    good, next_good = tq2.attention_paged(q, few.cache, few.batch), tq2.attention_paged(r, many.cache, many.batch)
+    for _ in range(20):
+        with Limit(tq2, 0):
+            for _ in range(3):
+                tq2.attention_paged(q, few.cache, few.batch)
+        assert torch.equal(tq2.attention_paged(r, many.cache, many.batch), next_good)
+        assert torch.equal(tq2.attention_paged(q, few.cache, few.batch), good)
+    tq2.tq2_device_status()
