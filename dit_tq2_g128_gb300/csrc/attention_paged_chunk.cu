@@ -349,10 +349,24 @@ __device__ __forceinline__ void find_run(const PagedArgs &a, ChunkCtl *ctl, unsi
         }
         return units;
     };
+    // The host has checked that the units of the step's tokens fit 32 bits; sequences of a bad batch that claim the same
+    // tokens may pass that, and then nothing is done.
+    auto sum_of = [](int units) {
+        return (int64_t(__reduce_add_sync(0xffffffffu, unsigned(units) >> 16)) << 16) +
+               __reduce_add_sync(0xffffffffu, unsigned(units) & 0xffffu);
+    };
     const int head = units_of(0);
-    int total = int(__reduce_add_sync(0xffffffffu, unsigned(head))) * a.kv_heads;
-    for (int base = 32; base < bt.seqs; base += 32)
-        total += int(__reduce_add_sync(0xffffffffu, unsigned(units_of(base)))) * a.kv_heads;
+    int64_t sum = sum_of(head);
+    for (int base = 32; base < bt.seqs; base += 32) sum += sum_of(units_of(base));
+    sum *= a.kv_heads;
+    if (sum > INT32_MAX - kNumSms) {
+        if (lane == 0) {
+            report_bad(true, status);
+            ctl->left = 0;
+        }
+        return;
+    }
+    const int total = int(sum);
     const int ctas = int(gridDim.x), share = max(kMinUnits, (total + ctas - 1) / ctas);
     const int64_t start = int64_t(blockIdx.x) * share;
     if (lane == 0) ctl->left = start < total ? int(min(int64_t(share), total - start)) : 0;

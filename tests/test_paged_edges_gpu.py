@@ -53,3 +53,14 @@ def test_copies_land_before_a_cta_that_gave_up_is_gone(tq2, kv):
         assert torch.equal(tq2.attention_paged(r, many.cache, many.batch), next_good)
         assert torch.equal(tq2.attention_paged(q, few.cache, few.batch), good)
     tq2.tq2_device_status()
+
+
+def test_sequences_that_claim_the_same_tokens(tq2):
+    """Fifty of a hundred sequences claim the same 3000 tokens over 2^30 keys each: more work than 32 bits count."""
+    ints = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    k = torch.zeros((1, 1 << 20, 1, 8), device="cuda", dtype=torch.float16)
+    q = torch.ones((3000, 1, 8), device="cuda", dtype=torch.float16)
+    table = torch.zeros((100, 1 << 10), dtype=torch.int32, device="cuda")
+    batch = tq2.PagedBatch(ints(*([0, 3000] * 50 + [0])), ints(*[1 << 30] * 100), table, tokens=3000, max_q=3000, max_kv=1 << 30)
+    tq2.attention_paged(q, tq2.KVCache(k, k.clone()), batch)
+    assert tq2.tq2_device_status() == tq2.TQ2_ERR_BAD_BATCH
