@@ -154,7 +154,7 @@ rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
         if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
         key = int64_t(sp.kv) - sp.n + (t - sp.q0);
         if (g.paged) {
-            if (key < 0) return;
+            if (bad || key < 0) return;  // (clamped lengths would name the slots of older keys)
             const int in_table = int(key) / a.batch.page_size;
             const int64_t page = page_of(a.batch, b, in_table, bad);
             report_bad(bad, status);

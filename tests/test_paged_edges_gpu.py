@@ -64,3 +64,27 @@ def test_sequences_that_claim_the_same_tokens(tq2):
     batch = tq2.PagedBatch(ints(*([0, 3000] * 50 + [0])), ints(*[1 << 30] * 100), table, tokens=3000, max_q=3000, max_kv=1 << 30)
     tq2.attention_paged(q, tq2.KVCache(k, k.clone()), batch)
     assert tq2.tq2_device_status() == tq2.TQ2_ERR_BAD_BATCH
+
+
+@pytest.mark.parametrize("what", ["more keys than max_kv", "more keys than the table", "more tokens than max_q"])
+def test_append_of_a_bad_batch_stores_nothing_of_its_sequence(tq2, what):
+    step = Step(tq2, [2, 3, 1], [48, 40, 17], 2, 64, 16, rest=0.0)
+    k, v = step.queries(2), step.queries(2)
+    tables, max_q, max_kv, bad = [t.clone() for t in step.tables], 3, 48, 0
+    if what == "more keys than max_kv":
+        tables[1][0] = 49
+    elif what == "more keys than the table":
+        tables[1][0], max_kv = 60, 1000
+    else:
+        max_q, bad = 2, 1
+    want = [step.k.clone(), step.v.clone()]
+    for b in range(3):
+        for i in range(step.q_len[b]):
+            if b != bad:
+                at = step.slot(b, step.kv_len[b] - step.q_len[b] + i)
+                for plane, x in zip(want, (k, v)):
+                    plane[at] = x[int(step.q_start[b]) + i]
+    batch = tq2.PagedBatch(*tables, tokens=step.tokens, max_q=max_q, max_kv=max_kv)
+    tq2.kv_append(k, v, step.cache, batch)
+    assert tq2.tq2_device_status() == tq2.TQ2_ERR_BAD_BATCH
+    assert torch.equal(step.k, want[0]) and torch.equal(step.v, want[1])
