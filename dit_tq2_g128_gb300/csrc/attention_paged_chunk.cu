@@ -1004,7 +1004,8 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 const int entry = key / a.batch.page_size;
                 bool ignore = false;
                 const int64_t p = page_of(a.batch, b, entry, ignore);
-                const T *v = static_cast<const T *>(a.v) + (p < 0 ? 0 : p) * a.page_stride +
+                if (p < 0) continue;  // (read as zeros)
+                const T *v = static_cast<const T *>(a.v) + p * a.page_stride +
                              int64_t(key - entry * a.batch.page_size) * a.slot_stride + int64_t(g) * a.head_stride + c * 32;
 #pragma unroll 1
                 for (int i = 0; i < 32 && c * 32 + i < a.dim; ++i) {

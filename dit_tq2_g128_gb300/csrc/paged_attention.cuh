@@ -120,9 +120,9 @@ struct BoxPages {
         for (int i = r.lo; i < r.hi; ++i) {
             const int box = tile * per + i;
             int page = per > 16 ? uniform(entry_of(box)) : __shfl_sync(0xffffffffu, now, box & 31);
-            if (page < 0 || int64_t(page) >= a.batch.pages) {  // (recorded; any page of the cache will do)
+            if (page < 0 || int64_t(page) >= a.batch.pages) {  // (recorded; past the last page the copy fills in zeros)
                 bad = true;
-                page = 0;
+                page = int(a.batch.pages);
             }
             if (one) copy(i * rows, slot, page);
             slot += rows;

@@ -432,10 +432,10 @@ typedef struct {
  * The tables are device memory that a captured graph reads again on each replay;
  * max_q and max_kv are host bounds of n and kv_len that the launch is sized by.
  * Lengths are clamped to them and to the table's width, and a page outside the
- * cache is never touched: TQ2_ERR_BAD_BATCH is then recorded in the device
- * status word (tq2_device_status), and that sequence's results mean nothing;
- * nothing of it is stored in the cache where its lengths are out of range, nor
- * any of its tokens whose page is. */
+ * cache is never touched (attention reads it as zeros): TQ2_ERR_BAD_BATCH is then
+ * recorded in the device status word (tq2_device_status), and that sequence's
+ * results mean nothing; nothing of it is stored in the cache where its lengths
+ * are out of range, nor any of its tokens whose page is. */
 typedef struct {
     const int32_t *q_start;    /* device [seqs + 1], not decreasing, from 0 */
     const int32_t *kv_len;     /* device [seqs] */

@@ -88,3 +88,21 @@ def test_append_of_a_bad_batch_stores_nothing_of_its_sequence(tq2, what):
     tq2.kv_append(k, v, step.cache, batch)
     assert tq2.tq2_device_status() == tq2.TQ2_ERR_BAD_BATCH
     assert torch.equal(step.k, want[0]) and torch.equal(step.v, want[1])
+
+
+@pytest.mark.parametrize("q_len", [1, 6, 40, 300])
+@pytest.mark.parametrize("entry", [-1, 1 << 20])
+def test_a_page_outside_the_cache_reads_as_zeros(tq2, q_len, entry):
+    step = Step(tq2, [q_len, q_len], [310, 300], 2, 64, 16)
+    q = step.queries(4)
+    tables = [t.clone() for t in step.tables]
+    tables[2][0, 3] = entry
+    tables[2][0, 19] = entry
+    out = tq2.attention_paged(q, step.cache, tq2.PagedBatch(*tables, tokens=step.tokens, max_q=q_len, max_kv=310))
+    assert tq2.tq2_device_status() == tq2.TQ2_ERR_BAD_BATCH
+    pages = step.k.shape[0]
+    k, v = (np.concatenate([host(p), np.zeros((1, *p.shape[1:]))]) for p in (step.k, step.v))
+    table = step.table.copy()
+    table[0, [3, 19]] = pages
+    want, weight, spread = paged.attention(host(q), k, v, step.q_start, step.kv_len, table, 0.125)
+    check(out, want, attention_tol(step, want, weight, spread, "f16"))
