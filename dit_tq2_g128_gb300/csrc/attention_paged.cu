@@ -412,7 +412,8 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                             o[t][j][3] *= f1;
                         }
                     }
-                    const float u0 = m[t][0] == -INFINITY ? 0.f : m[t][0], u1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+                    const float u0 = m[t][0] == -INFINITY ? 0.f : m[t][0] - weight_lift<T>;
+                    const float u1 = m[t][1] == -INFINITY ? 0.f : m[t][1] - weight_lift<T>;
                     float p[4];
                     p[0] = fast_ex2(sc[t][0] - u0);
                     p[1] = fast_ex2(sc[t][1] - u1);

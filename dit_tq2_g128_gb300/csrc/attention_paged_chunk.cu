@@ -920,7 +920,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             const bool grow = top > m && (top - m) * scale2 > kLazy;
             const float mu = grow ? top : m;
             const float alpha = grow ? fast_ex2((m - mu) * scale2) : 1.f;
-            const float neg = mu == -INFINITY ? 0.f : -mu * scale2;
+            const float neg = mu == -INFINITY ? 0.f : fmaf(-mu, scale2, weight_lift<T>);
             const uint64_t neg2 = pair(neg, neg);
             uint64_t sum2[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
             uint32_t hp[32], lp[SPLIT_P ? 32 : 1];

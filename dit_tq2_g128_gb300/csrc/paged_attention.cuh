@@ -15,6 +15,13 @@ constexpr bool is_half = false;
 template <>
 constexpr bool is_half<__half> = true;
 
+// log2 of what the softmax's weights are multiplied by before they are rounded to T for the second product (l sums the
+// same multiples, so it cancels).  binary16 holds 2^-24 to 65504: weights as they are, at most 2^8 where the maximum
+// lags, lose bits below 2^-14 and are gone below 2^-25 of the largest; 2^7 more uses the range to its end.  (A weight of
+// 2^-19 was off by 1.8 %, in an f32 output too.)  bf16 has f32's range.
+template <typename T>
+constexpr float weight_lift = is_half<T> ? 7.f : 0.f;
+
 // Keys from the first token's window to the last token, at most, with what a block of 128
 // may hold before them.
 inline int64_t key_span(int64_t max_q, int64_t max_kv, int64_t window) {

@@ -106,3 +106,27 @@ def test_a_page_outside_the_cache_reads_as_zeros(tq2, q_len, entry):
     table[0, [3, 19]] = pages
     want, weight, spread = paged.attention(host(q), k, v, step.q_start, step.kv_len, table, 0.125)
     check(out, want, attention_tol(step, want, weight, spread, "f16"))
+
+
+@pytest.mark.parametrize("q_len", [1, 4, 40, 300])
+@pytest.mark.parametrize("out", ["f16", "f32"])
+@pytest.mark.parametrize("low", [9.0, 11.0, 13.3984375])
+def test_small_weights_beside_large_ones(tq2, q_len, out, low):
+    """Every 16th key has weight 1 and v = 0, the others e^-low (down to 2^-19) and v = 1000: the result is theirs alone.
+    Weights keep half a step of binary16 (f32 outputs: its square, 2^-22), or 2^-32 of the largest; scores up to 20 in log2
+    units leave the exponential 2^-19."""
+    step = Step(tq2, [q_len], [400], 1, 64, 16, rest=0.0)
+    j = torch.arange(400, device="cuda")
+    p, o = torch.from_numpy(step.table[0].astype(np.int64)).cuda()[j // 16], j % 16
+    step.k.zero_()
+    step.v.zero_()
+    large = (j % 16 == 0)
+    step.k[p, o, 0, 0] = torch.where(large, low, 0.0).half()
+    step.v[p, o, 0, :] = torch.where(large, 0.0, 1000.0).half()[:, None]
+    q = torch.zeros((q_len, 4, 64), device="cuda", dtype=torch.float16)
+    q[..., 0] = 1
+    got = torch.empty(q.shape, device="cuda", dtype=DT[out])
+    tq2.attention_paged(q, step.cache, step.batch, out=got, scale=1.0, causal=False)
+    want, weight, _ = paged.attention(host(q), host(step.k), host(step.v), [0, q_len], [400], step.table, 1.0, causal=False)
+    w = 2.0 ** -11 if out == "f16" else 2.0 ** -22
+    check(got, want, half_step(out) * np.abs(want) + (w + 2.0 ** -19) * weight + 400 * 2.0 ** -32 * 1000)
