@@ -76,8 +76,7 @@ struct KeyRange {
 };
 TQ2_HD KeyRange keys_of(const SeqSpan &sp, int i, int64_t window, bool causal) {
     const int64_t pos = int64_t(sp.kv) - sp.n + i;  // below kv
-    int64_t hi = causal ? pos + 1 : int64_t(sp.kv), lo = window ? pos + 1 - window : 0;
-    if (lo < 0) lo = 0;
+    int64_t hi = causal ? pos + 1 : int64_t(sp.kv), lo = window && window <= pos ? pos + 1 - window : 0;  // (any window)
     if (hi < lo) hi = lo;
     return KeyRange{int(lo), int(hi)};
 }
