@@ -483,7 +483,8 @@ bool distinct(int64_t dim, int64_t n0, int64_t s0, int64_t n1, int64_t s1) {
 int check_view(const tq2_heads *v, int64_t tokens, int64_t dim, bool output) {
     if (!v->data || !dtype_ok(v->dtype)) return TQ2_ERR_INVALID_ARG;
     if (v->heads < 1 || v->heads > kMaxHeads || v->token_stride < 0 || v->head_stride < 0 ||
-        v->token_stride > kMaxStride || v->head_stride > kMaxStride)
+        v->token_stride > kMaxStride || v->head_stride > kMaxStride ||
+        (v->token_stride && tokens > (int64_t(1) << 44) / v->token_stride))
         return TQ2_ERR_INVALID_ARG;
     if (output && !distinct(dim, tokens, v->token_stride, v->heads, v->head_stride)) return TQ2_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(v->data) % dtype_bytes(v->dtype)) return TQ2_ERR_MISALIGNED;
@@ -510,18 +511,38 @@ bool same_view(const tq2_heads *a, const tq2_heads *b) {
            a->token_stride == b->token_stride && a->head_stride == b->head_stride;
 }
 
-// Whether two views share no byte: their extents lie apart, or they are different
-// columns of rows with one stride (slices of one fused projection).
+// Whether two views share no byte: their extents lie apart, or they are different columns of rows with one stride
+// (slices of one fused projection), or, stepping alike, no piece of one head meets one of the other (q, k and v
+// interleaved by head).  Views that mesh with strides of their own count as overlapping.
 bool views_apart(const tq2_heads *a, const tq2_heads *b, int64_t tokens, int64_t dim) {
     const size_t ea = dtype_bytes(a->dtype), eb = dtype_bytes(b->dtype);
     const size_t wa = size_t((a->heads - 1) * a->head_stride + dim) * ea;
     const size_t wb = size_t((b->heads - 1) * b->head_stride + dim) * eb;
     const size_t ra = size_t(a->token_stride) * ea, rb = size_t(b->token_stride) * eb;
     if (!overlaps(a->data, size_t(tokens - 1) * ra + wa, b->data, size_t(tokens - 1) * rb + wb)) return true;
-    if (ra != rb || wa > ra || wb > ra) return false;
+    if (ra != rb) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a->data), y = reinterpret_cast<uintptr_t>(b->data);
-    const size_t d = y >= x ? (y - x) % ra : (ra - (x - y) % ra) % ra;  // b's columns, from a's first
-    return d >= wa && d + wb <= ra;
+    if (wa <= ra && wb <= ra) {
+        const size_t d = y >= x ? (y - x) % ra : (ra - (x - y) % ra) % ra;  // b's columns, from a's first
+        if (d >= wa && d + wb <= ra) return true;
+    }
+    const int64_t sa = a->head_stride * int64_t(ea), sb = b->head_stride * int64_t(eb);
+    if (a->heads > 1 && b->heads > 1 && sa != sb) return false;
+    const int64_t pa = dim * int64_t(ea), pb = dim * int64_t(eb), s = a->heads > 1 ? sa : sb, r = int64_t(ra);
+    // a piece of b starts at (its head - a's head) * s + (its token - a's token) * r + y - x from one of a: within -pb and pa
+    // they meet
+    const int64_t base = y >= x ? int64_t(y - x) : -int64_t(x - y);
+    auto floor_div = [](int64_t n, int64_t d) { return n / d - (n % d < 0); };
+    for (int64_t h = 1 - a->heads; h < b->heads; ++h) {
+        const int64_t at = base + h * s;
+        if (r == 0) {
+            if (at > -pb && at < pa) return false;
+        } else {
+            const int64_t lo = floor_div(-pb - at, r) + 1, hi = floor_div(pa - 1 - at, r);  // token differences that meet
+            if (lo <= hi && lo < tokens && hi > -tokens) return false;
+        }
+    }
+    return true;
 }
 
 // bytes from the first to the last element of a cache plane

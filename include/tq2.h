@@ -466,6 +466,9 @@ int tq2_rope_turns(const double *inv_freq, uint64_t *turns, int64_t pairs);
  *   positions : device [tokens, rope->axes] int64; any sign
  * q, k and v have one type, and their outputs one.  An output may be its own
  * input (same view); no other output may overlap an input or another output.
+ * (Views that mesh without sharing an element are apart where they step alike, as
+ * q, k and v side by side in each head of one projection; where their strides
+ * differ they count as overlapping.)
  * dim is 1 .. 65536.  tokens == 0 is a no-op. */
 int tq2_rope_axes(const tq2_heads *q, const tq2_heads *q_out, const tq2_heads *k, const tq2_heads *k_out,
                   const tq2_heads *v, const tq2_heads *v_out, const int64_t *positions, const tq2_rope *rope,

@@ -2,6 +2,7 @@
 
 import ctypes
 
+import numpy as np
 import pytest
 
 from test_paged import fake, index, tq2  # noqa: F401 (fixtures)
@@ -22,3 +23,49 @@ def test_windows_up_to_64_bits(index, window):  # noqa: F811
             some = set().union(*see)
             assert out[0] == n * group and out[2] == len({j // 128 for j in some}) and min(out[3:7]) >= 0
             assert set(range(out[3], out[4])) == some or not some
+
+
+def refused(tq2, q, k, tokens, dim):  # noqa: F811
+    """Whether q and k in place, (bytes from a base, heads, token stride, head stride) each, are refused."""
+    H, base = tq2.tq2_heads, fake(0)
+    rope = tq2.tq2_rope(fake(3), None, dim // 2, 1)
+    q, k = (H(base + 4 * at, h, ts, hs, 0) for at, h, ts, hs in (q, k))
+    st = tq2.lib.tq2_rope_axes(q, q, k, k, None, None, fake(2), rope, tokens, dim, 0, None)
+    assert st != tq2.TQ2_OK and st != tq2.TQ2_ERR_MISALIGNED
+    return st == tq2.TQ2_ERR_INVALID_ARG
+
+
+def cells(view, tokens, dim):
+    at, heads, ts, hs = view
+    return {at + t * ts + h * hs + d for t in range(tokens) for h in range(heads) for d in range(dim)}
+
+
+def test_views_that_share_nothing_are_taken_and_others_refused(tq2):  # noqa: F811
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are made up")
+    # q, k, v of each head side by side, [tokens, heads, 3, dim], and heads first, [heads, tokens, 3, dim]
+    for ts, hs in ((4 * 3 * 64, 3 * 64), (3 * 64, 10 * 3 * 64)):
+        q = (0, 4, ts, hs)
+        for at in (64, 128):
+            assert not refused(tq2, q, (at, 4, ts, hs), 10, 64)
+        assert refused(tq2, q, (63, 4, ts, hs), 10, 64) and refused(tq2, q, (129, 4, ts, hs), 10, 64)
+    # grouped: one key head beside every four query heads has no view of one stride; one key head in all has
+    assert not refused(tq2, (0, 4, 640, 128), (64, 1, 640, 0), 10, 64)
+    rng = np.random.default_rng(9)
+    taken = 0
+    for _ in range(4000):
+        dim, tokens = 2 * int(rng.integers(1, 4)), int(rng.integers(1, 5))
+        heads = [int(rng.integers(1, 5)) for _ in range(2)]
+        ts, hs = int(rng.integers(0, 40)), int(rng.integers(0, 40))
+        views = [(0, heads[0], ts, hs), (int(rng.integers(0, 60)), heads[1], ts, hs)]
+        if any(len(cells(v, tokens, dim)) < v[1] * tokens * dim for v in views):
+            continue
+        if any((tokens > 1 and ts < dim) or (v[1] > 1 and hs < dim) for v in views):
+            continue   # (outputs' strides step over what lies below them)
+        if any(tokens > 1 and v[1] > 1 and not (ts >= (v[1] - 1) * hs + dim or hs >= (tokens - 1) * ts + dim) for v in views):
+            continue
+        meet = bool(cells(views[0], tokens, dim) & cells(views[1], tokens, dim))
+        assert refused(tq2, *views, tokens, dim) == meet, (views, tokens, dim)
+        taken += not meet
+    assert taken > 300

@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import paged
-from test_paged_gpu import DT, Step, attention_tol, check, half_step, host
+from test_paged_gpu import DT, Step, attention_tol, check, frequencies, half_step, host, rope_tol
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -130,3 +130,16 @@ def test_small_weights_beside_large_ones(tq2, q_len, out, low):
     want, weight, _ = paged.attention(host(q), host(step.k), host(step.v), [0, q_len], [400], step.table, 1.0, causal=False)
     w = 2.0 ** -11 if out == "f16" else 2.0 ** -22
     check(got, want, half_step(out) * np.abs(want) + (w + 2.0 ** -19) * weight + 400 * 2.0 ** -32 * 1000)
+
+
+def test_interleaved_projection_in_place(tq2):
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    f, _ = frequencies(64, 1, np.random.default_rng(5), False)
+    fused = torch.randn((9, 4, 3, 128), device="cuda", generator=gen)
+    before = host(fused)
+    pos = np.arange(9).reshape(9, 1) * 7
+    rope, at = tq2.Rope(f), torch.from_numpy(pos).cuda()
+    tq2.rope_axes(fused[:, :, 0], fused[:, :, 1], positions=at, rope=rope, out=(fused[:, :, 0], fused[:, :, 1]))
+    for i, turned in enumerate((True, True, False)):
+        want = paged.rotate(before[:, :, i], pos, f if turned else [], [0] * 64)
+        check(fused[:, :, i], want, rope_tol(before[:, :, i], 64 if turned else 0, False, want, "f32"), str(i))
