@@ -775,7 +775,10 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
             uint32_t asked = 0;
             for (;; ++claims) {
                 const int slot = claims & 1;
-                bool ok = __all_sync(0xffffffffu, doze_phase(&ctl->want, claims & 1, abort_flag, wait_ns, status));
+                // (blocks are copied meanwhile, the last of the item before and this one's, each of which may take the limit)
+                walk.more();
+                const uint64_t limit = wait_ns >> 32 ? wait_ns : wait_ns * uint64_t(walk.nb + 8);
+                bool ok = __all_sync(0xffffffffu, doze_phase(&ctl->want, claims & 1, abort_flag, limit, status));
                 if (ok && claims >= 2)
                     ok = __all_sync(0xffffffffu, wait_phase(&ctl->item_free[slot], ((claims >> 1) - 1) & 1, abort_flag, wait_ns, status));
                 if (!ok) break;
@@ -804,6 +807,7 @@ paged_chunk_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_consta
                 }
                 __syncwarp();
                 if (it.left == 0) break;
+                walk.begin(&it);
             }
         }
     } else {

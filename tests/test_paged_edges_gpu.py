@@ -143,3 +143,30 @@ def test_interleaved_projection_in_place(tq2):
     for i, turned in enumerate((True, True, False)):
         want = paged.rotate(before[:, :, i], pos, f if turned else [], [0] * 64)
         check(fused[:, :, i], want, rope_tol(before[:, :, i], 64 if turned else 0, False, want, "f32"), str(i))
+
+
+def test_a_long_item_is_not_a_wait_that_ran_out(tq2):
+    """152 whole items of 800 blocks each take a millisecond, each block little more than one microsecond."""
+    step = Step(tq2, [1216], [102_400], 8, 64, 64)
+    q = step.queries(32)
+    good = tq2.attention_paged(q, step.cache, step.batch)
+    with Limit(tq2, 100_000):
+        got = tq2.attention_paged(q, step.cache, step.batch)
+        assert tq2.tq2_device_status() == tq2.TQ2_OK
+    assert torch.equal(got, good)
+
+
+def long_items(tq2):
+    """Whole items of up to 40 blocks: the next one is claimed near the end, which no limit of 0 waits for."""
+    return Step(tq2, [260, 70, 300] * 20, [1700, 70, 5000] * 20, 4, 64, 16)
+
+
+def test_a_wait_that_cannot_be_met_is_reported(tq2):
+    step = long_items(tq2)
+    q = step.queries(12)
+    good = tq2.attention_paged(q, step.cache, step.batch)
+    for _ in range(5):
+        with Limit(tq2, 0):
+            tq2.attention_paged(q, step.cache, step.batch)
+            assert tq2.tq2_device_status() == tq2.TQ2_ERR_TIMEOUT
+        assert torch.equal(tq2.attention_paged(q, step.cache, step.batch), good)
