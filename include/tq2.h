@@ -520,7 +520,9 @@ size_t tq2_attention_paged_workspace_bytes(int64_t heads, const tq2_kv_cache *ca
  * gives up after `ns` nanoseconds of %globaltimer time, records
  * TQ2_ERR_TIMEOUT in a device status word and lets the kernel exit cleanly
  * (draining its own in-flight work first).  Default 2e9 (2 s).  Applies to
- * launches issued after the call.  Returns the previous value. */
+ * launches issued after the call.  The paged attention looks at the limit about
+ * four times a millisecond: a shorter wait does not run out, whatever the limit.
+ * Returns the previous value. */
 uint64_t tq2_set_wait_timeout_ns(uint64_t ns);
 
 /* Synchronises `stream`, then reads and clears the device status word of the

@@ -170,3 +170,20 @@ def test_a_wait_that_cannot_be_met_is_reported(tq2):
             tq2.attention_paged(q, step.cache, step.batch)
             assert tq2.tq2_device_status() == tq2.TQ2_ERR_TIMEOUT
         assert torch.equal(tq2.attention_paged(q, step.cache, step.batch), good)
+
+
+def test_a_wait_of_few_rows_that_runs_out_is_reported(tq2):
+    """The first of 24 tiles, where some rows see a key and others do not, holds nothing but infinities, which the
+    consumers hand to the rows one by one for tens of microseconds; the copies of the fourth tile wait for them."""
+    step = Step(tq2, [16], [2000], 1, 64, 16)
+    j = torch.arange(512, device="cuda")
+    p, o = torch.from_numpy(step.table[0].astype(np.int64)).cuda()[j // 16], j % 16
+    q = step.queries(2)
+    step.v[p, o] = float("inf")
+    good = tq2.attention_paged(q, step.cache, step.batch, window=1500)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        with Limit(tq2, 0):
+            tq2.attention_paged(q, step.cache, step.batch, window=1500)
+            assert tq2.tq2_device_status() == tq2.TQ2_ERR_TIMEOUT
+        assert torch.equal(tq2.attention_paged(q, step.cache, step.batch, window=1500).view(torch.int16), good.view(torch.int16))
