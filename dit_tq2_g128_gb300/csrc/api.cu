@@ -179,11 +179,13 @@ int tq2_device_status(void *stream) {
     int st = current_device(&d);
     if (st != TQ2_OK) return st;
     if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return TQ2_ERR_CUDA;
-    unsigned int v = 0, zero = 0;
+    unsigned int v = 0;
     if (cudaMemcpy(&v, d.status, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return TQ2_ERR_CUDA;
-    if (cudaMemcpy(d.status, &zero, sizeof(zero), cudaMemcpyHostToDevice) != cudaSuccess) return TQ2_ERR_CUDA;
-    if ((v & TQ2_ERR_TIMEOUT) == TQ2_ERR_TIMEOUT) return TQ2_ERR_TIMEOUT;
-    return (v & TQ2_ERR_BAD_BATCH) ? TQ2_ERR_BAD_BATCH : TQ2_OK;
+    // what is reported is cleared; the other kind waits for the next call
+    st = (v & TQ2_ERR_TIMEOUT) == TQ2_ERR_TIMEOUT ? TQ2_ERR_TIMEOUT : v & TQ2_ERR_BAD_BATCH ? TQ2_ERR_BAD_BATCH : TQ2_OK;
+    const unsigned int left = st == TQ2_ERR_TIMEOUT ? v & TQ2_ERR_BAD_BATCH : 0;
+    if (cudaMemcpy(d.status, &left, sizeof(left), cudaMemcpyHostToDevice) != cudaSuccess) return TQ2_ERR_CUDA;
+    return st;
 }
 
 int tq2_select_kernel(int64_t m, int64_t n, int64_t k) {

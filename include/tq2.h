@@ -525,9 +525,12 @@ size_t tq2_attention_paged_workspace_bytes(int64_t heads, const tq2_kv_cache *ca
  * Returns the previous value. */
 uint64_t tq2_set_wait_timeout_ns(uint64_t ns);
 
-/* Synchronises `stream`, then reads and clears the device status word of the
- * current device: TQ2_OK, or TQ2_ERR_TIMEOUT if any kernel since the last
- * check gave up on a wait; TQ2_ERR_CUDA if the synchronisation itself failed. */
+/* Synchronises `stream`, then reads the device status word of the current
+ * device: TQ2_OK, or TQ2_ERR_TIMEOUT if any kernel since the last check gave up
+ * on a wait, or TQ2_ERR_BAD_BATCH if one found a batch's tables out of range;
+ * TQ2_ERR_CUDA if the synchronisation itself failed.  What is returned is
+ * cleared; where both happened the timeout comes first and the next call returns
+ * the other. */
 int tq2_device_status(void *stream);
 
 /* Library version, e.g. 0x000100 for 0.1.0. */

@@ -187,3 +187,16 @@ def test_a_wait_of_few_rows_that_runs_out_is_reported(tq2):
             tq2.attention_paged(q, step.cache, step.batch, window=1500)
             assert tq2.tq2_device_status() == tq2.TQ2_ERR_TIMEOUT
         assert torch.equal(tq2.attention_paged(q, step.cache, step.batch, window=1500).view(torch.int16), good.view(torch.int16))
+
+
+def test_the_status_reports_both_kinds_one_after_the_other(tq2):
+    step = long_items(tq2)
+    q = step.queries(12)
+    tables = [t.clone() for t in step.tables]
+    tables[1][0] = -1
+    bad = tq2.PagedBatch(*tables, tokens=step.tokens, max_q=300, max_kv=5000)
+    with Limit(tq2, 0):
+        tq2.attention_paged(q, step.cache, bad)
+        assert tq2.tq2_device_status() == tq2.TQ2_ERR_TIMEOUT
+    assert tq2.tq2_device_status() == tq2.TQ2_ERR_BAD_BATCH
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
