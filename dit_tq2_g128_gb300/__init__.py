@@ -15,6 +15,7 @@ legacy default stream).
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -339,7 +340,16 @@ def tq2_attention_paged_workspace_bytes(heads: int, cache: bytes, batch: bytes) 
 
 
 # ---------------------------------------------------------------------------
-# Tensor-level conveniences (shape and dtype checks, then the calls above).
+# Tensor-level conveniences (shape and dtype checks, then the calls above).  A tensor that a function makes belongs to
+# the stream it runs on: to ``stream`` if given, as if made under ``torch.cuda.stream(stream)``.
+
+
+def _on(stream):
+    """Context whose allocations are ordered with the work of ``stream`` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    import torch
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
 
 
 def _check_tensor(t, name, dtype, numel):
@@ -365,8 +375,9 @@ def upload_weight(w_aos_host, n: int, k: int, stream=None):
         if not isinstance(w_aos_host, torch.Tensor) else w_aos_host.reshape(-1)
     if src.numel() != nbytes:
         raise ValueError(f"weight has {src.numel()} bytes, expected {nbytes}")
-    aos = src.to("cuda", non_blocking=False)
-    soa = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    with _on(stream):
+        aos = src.to("cuda", non_blocking=False)
+        soa = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     tq2_reformat_aos_to_soa(aos, soa, n, k, stream)
     return soa
 
@@ -390,7 +401,8 @@ def matmul(w_soa, x, residual=None, *, n: int, k: int, out=None, kernel: int = T
     if residual is not None:
         _check_tensor(residual, "residual", "torch.float32", m * n)
     if out is None:
-        out = torch.empty((m, n), dtype=torch.float32, device=x.device)
+        with _on(stream):
+            out = torch.empty((m, n), dtype=torch.float32, device=x.device)
     _check_tensor(out, "out", "torch.float32", m * n)
     if workspace is not None and kernel == TQ2_KERNEL_AUTO:
         tq2_gemm_ws(w_soa, x, residual, out, m, n, k, workspace, workspace.numel(), stream)
@@ -506,7 +518,8 @@ def rope_axes(q, k=None, v=None, *, positions, rope: Rope, out=None, inverse: bo
     ins = [t for t in (q, k, v) if t is not None]
     if out is None:
         import torch
-        out = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ins]
+        with _on(stream):
+            out = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in ins]
     if len(out) != len(ins):
         raise ValueError(f"{len(ins)} outputs expected, got {len(out)}")
     qi, qo = _heads(q, "q", tokens, dim), _heads(out[0], "q's output", tokens, dim)
@@ -529,7 +542,8 @@ def kv_append(k, v, cache: KVCache, batch: PagedBatch, *, rope: Rope = None, pos
     if q is not None:
         if q_out is None:
             import torch
-            q_out = torch.empty(q.shape, dtype=cache.dtype, device=q.device)
+            with _on(stream):
+                q_out = torch.empty(q.shape, dtype=cache.dtype, device=q.device)
         qp, qo = _heads(q, "q", tokens, dim), _heads(q_out, "q_out", tokens, dim)
     pos = rope.positions(positions, tokens) if rope is not None else None
     tq2_kv_append(qp, qo, _heads(k, "k", tokens, dim), _heads(v, "v", tokens, dim), pos,
@@ -551,7 +565,8 @@ def attention_paged(q, cache: KVCache, batch: PagedBatch, *, out=None, scale: fl
     type; a float32 one keeps more of the softmax's bits)."""
     if out is None:
         import torch
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with _on(stream):
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     tokens, dim = batch.tokens, cache.dim
     tq2_attention_paged(_heads(q, "q", tokens, dim), _heads(out, "out", tokens, dim), cache.packed, batch.packed,
                         dim ** -0.5 if scale is None else scale, window, int(causal), workspace,

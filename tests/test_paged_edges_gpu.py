@@ -200,3 +200,37 @@ def test_the_status_reports_both_kinds_one_after_the_other(tq2):
         assert tq2.tq2_device_status() == tq2.TQ2_ERR_TIMEOUT
     assert tq2.tq2_device_status() == tq2.TQ2_ERR_BAD_BATCH
     assert tq2.tq2_device_status() == tq2.TQ2_OK
+
+
+def pool_stream(t):
+    for seg in torch.cuda.memory_snapshot():
+        if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+            return seg["stream"]
+
+
+@pytest.mark.parametrize("as_int", [False, True])
+def test_results_belong_to_the_stream_that_writes_them(tq2, as_int):
+    step = Step(tq2, [3], [40], 2, 64, 16, rest=0.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    s = side.cuda_stream if as_int else side
+    q, k, v = step.queries(4), step.queries(2), step.queries(2)
+    rope = tq2.Rope([1.0, 0.1])
+    w = torch.zeros(tq2.tq2_soa_bytes(64, 128), dtype=torch.uint8, device="cuda")
+    x = torch.zeros((2, 128), device="cuda")
+    torch.cuda.synchronize()
+    got = [tq2.attention_paged(q, step.cache, step.batch, stream=s),
+           tq2.kv_append(k, v, step.cache, step.batch, q=q, stream=s),
+           *tq2.rope_axes(q, k, v, positions=torch.arange(3, device="cuda"), rope=rope, stream=s),
+           tq2.matmul(w, x, n=64, k=128, stream=s)]
+    side.synchronize()
+    assert [pool_stream(t) for t in got] == [side.cuda_stream] * len(got)
+
+
+def test_an_uploaded_weight_belongs_to_its_stream(tq2):
+    w = np.random.default_rng(0).integers(0, 256, tq2.tq2_soa_bytes(64, 128), dtype=np.uint8)
+    want = tq2.upload_weight(w, 64, 128)
+    side = torch.cuda.Stream()
+    got = tq2.upload_weight(w, 64, 128, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want) and pool_stream(got) == side.cuda_stream
