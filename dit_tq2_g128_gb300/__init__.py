@@ -438,9 +438,14 @@ def _heads(t, name: str, tokens: int, dim: int, _pack=struct.Struct("=qqqqi4x").
 
 
 def _table(t, name: str, dtype: str, ndim: int):
-    if not t.is_cuda or str(t.dtype) != dtype or t.dim() != ndim or (t.numel() and t.stride(-1) != 1):
+    if not t.is_cuda or str(t.dtype) != dtype or t.dim() != ndim or (t.numel() and t.shape[-1] > 1 and t.stride(-1) != 1):
         raise ValueError(f"{name} must be a CUDA {dtype} tensor of {ndim} dimension(s) with a contiguous last one")
     return t
+
+
+def _rows_inside(t, width: int) -> bool:
+    """Whether rows of ``width`` elements, the last one too, lie inside t's memory (lengths are clamped to whole rows)."""
+    return (t.storage_offset() + t.shape[0] * width) * t.element_size() <= t.untyped_storage().nbytes()
 
 
 class Rope:
@@ -492,8 +497,8 @@ class KVCache:
 
 class PagedBatch:
     """The sequences of one step: int32 device tables ``q_start`` [seqs + 1], ``kv_len`` [seqs] (the new tokens'
-    keys included) and ``page_table`` [seqs, entries], with the host's bounds.  Holds the tables, whose values may
-    change between calls (a captured graph reads them anew); see tq2_batch."""
+    keys included) and ``page_table`` [seqs, entries] (contiguous, or the first columns of a wider one), with the host's
+    bounds.  Holds the tables, whose values may change between calls (a captured graph reads them anew); see tq2_batch."""
 
     def __init__(self, q_start, kv_len, page_table, *, tokens: int, max_q: int, max_kv: int):
         _table(q_start, "q_start", "torch.int32", 1)
@@ -502,12 +507,12 @@ class PagedBatch:
         seqs = kv_len.numel()
         if q_start.numel() != seqs + 1 or page_table.shape[0] != seqs:
             raise ValueError(f"{seqs} sequences need q_start [{seqs + 1}] and page_table [{seqs}, entries]")
-        if seqs > 1 and page_table.stride(0) != page_table.shape[1]:
-            raise ValueError("page_table must be contiguous")
+        width = page_table.stride(0) if seqs > 1 else page_table.shape[1]
+        if width < page_table.shape[1] or (width > page_table.shape[1] and not _rows_inside(page_table, width)):
+            raise ValueError("page_table must be contiguous, or the first columns of a wider table")
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.seqs, self.tokens, self.max_q, self.max_kv = int(seqs), int(tokens), int(max_q), int(max_kv)
-        self.packed = tq2_batch(q_start, kv_len, page_table, self.seqs, self.tokens, self.max_q, self.max_kv,
-                                page_table.shape[1])
+        self.packed = tq2_batch(q_start, kv_len, page_table, self.seqs, self.tokens, self.max_q, self.max_kv, width)
 
 
 def rope_axes(q, k=None, v=None, *, positions, rope: Rope, out=None, inverse: bool = False, stream=None):

@@ -234,3 +234,22 @@ def test_an_uploaded_weight_belongs_to_its_stream(tq2):
     got = tq2.upload_weight(w, 64, 128, stream=side)
     side.synchronize()
     assert torch.equal(got, want) and pool_stream(got) == side.cuda_stream
+
+
+def test_first_columns_of_a_wider_table(tq2):
+    step = Step(tq2, [2, 3, 1], [30, 40, 17], 2, 64, 16, rest=0.0)
+    q = step.queries(4)
+    good = tq2.attention_paged(q, step.cache, step.batch)
+    wide = torch.full((3, 9), -1, dtype=torch.int32, device="cuda")
+    wide[:, :3] = step.tables[2]
+    got = tq2.attention_paged(q, step.cache, tq2.PagedBatch(*step.tables[:2], wide[:, :3], tokens=6, max_q=3, max_kv=40))
+    assert torch.equal(got, good)
+    with pytest.raises(ValueError):
+        tq2.PagedBatch(*step.tables[:2], wide[:, 6:], tokens=6, max_q=3, max_kv=40)
+    # one sequence, one entry: strides of single elements say nothing
+    one = Step(tq2, [1], [5], 2, 64, 16, rest=0.0)
+    q = one.queries(2)
+    tables = [t.repeat_interleave(2, -1)[..., ::2] for t in (one.tables[0], one.tables[1], one.tables[2])]
+    tables[0] = one.tables[0]
+    got = tq2.attention_paged(q, one.cache, tq2.PagedBatch(*tables, tokens=1, max_q=1, max_kv=5))
+    assert torch.equal(got, tq2.attention_paged(q, one.cache, one.batch))
