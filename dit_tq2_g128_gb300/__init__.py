@@ -349,7 +349,9 @@ def _on(stream):
     if stream is None:
         return contextlib.nullcontext()
     import torch
-    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream)))
+    if not isinstance(stream, torch.cuda.Stream):  # (ExternalStream(0) is not the default stream)
+        stream = torch.cuda.ExternalStream(_stream(stream)) if _stream(stream) else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _check_tensor(t, name, dtype, numel):

@@ -227,6 +227,15 @@ def test_results_belong_to_the_stream_that_writes_them(tq2, as_int):
     assert [pool_stream(t) for t in got] == [side.cuda_stream] * len(got)
 
 
+def test_results_of_the_default_stream_by_its_handle(tq2):
+    step = Step(tq2, [3], [40], 2, 64, 16, rest=0.0)
+    q = step.queries(4)
+    with torch.cuda.stream(torch.cuda.Stream()):
+        got = tq2.attention_paged(q, step.cache, step.batch, stream=0)
+    torch.cuda.synchronize()
+    assert pool_stream(got) == 0
+
+
 def test_an_uploaded_weight_belongs_to_its_stream(tq2):
     w = np.random.default_rng(0).integers(0, 256, tq2.tq2_soa_bytes(64, 128), dtype=np.uint8)
     want = tq2.upload_weight(w, 64, 128)
