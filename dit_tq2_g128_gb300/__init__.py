@@ -476,7 +476,7 @@ class Rope:
         if positions is None:
             return None
         if (positions.dtype is not self._int64 or not positions.is_cuda or not positions.is_contiguous()
-                or positions.numel() != tokens * self.axes):
+                or positions.numel() != tokens * self.axes or (self.axes > 1 and positions.shape[-1] != self.axes)):
             raise ValueError(f"positions must be a contiguous CUDA int64 tensor [{tokens}, {self.axes}]")
         return positions
 

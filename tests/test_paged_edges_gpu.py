@@ -262,3 +262,10 @@ def test_first_columns_of_a_wider_table(tq2):
     tables[0] = one.tables[0]
     got = tq2.attention_paged(q, one.cache, tq2.PagedBatch(*tables, tokens=1, max_q=1, max_kv=5))
     assert torch.equal(got, tq2.attention_paged(q, one.cache, one.batch))
+
+
+def test_positions_of_another_shape_are_refused(tq2):
+    rope = tq2.Rope([1.0, 0.1], axis=[0, 1], axes=2)
+    x = torch.zeros((3, 1, 4), device="cuda")
+    with pytest.raises(ValueError):
+        tq2.rope_axes(x, positions=torch.zeros((2, 3), dtype=torch.int64, device="cuda"), rope=rope)
