@@ -69,3 +69,42 @@ def test_views_that_share_nothing_are_taken_and_others_refused(tq2):  # noqa: F8
         assert refused(tq2, *views, tokens, dim) == meet, (views, tokens, dim)
         taken += not meet
     assert taken > 300
+
+
+# ---------------------------------------------------------------------------
+# the weights of the second product
+
+
+def remainder(w, dtype, terms):
+    """What is left of weights w (relative) after so many terms of the type, each the rounding of what the others leave."""
+    import torch
+    x = torch.as_tensor(w, dtype=torch.float64)
+    left = x * (128.0 if dtype == "f16" else 1.0)
+    for _ in range(terms):
+        left = left - left.to({"f16": torch.float16, "bf16": torch.bfloat16}[dtype]).double()
+    return (left.abs() / (x * (128.0 if dtype == "f16" else 1.0))).numpy()
+
+
+# kept terms and tolerance by type and kernel: half a step to the power of the terms, and 2^-20 for exponent, sums and division
+KEPT = {("f16", "few"): (2, 2.0 ** -20), ("bf16", "few"): (3, 2.0 ** -20),
+        ("f16", "many"): (2, 2.0 ** -20), ("bf16", "many"): (2, 2.0 ** -16 + 2.0 ** -20)}
+
+
+def telling_scores(dtype, rows):
+    """Scores s = -i/64 whose weight e^s tells whether its last term was kept: without it, it is off by three tolerances."""
+    terms, tol = KEPT[dtype, rows]
+    s = -np.arange(1, 65) / 64
+    return s[remainder(np.exp(s), dtype, terms - 1) > 3 * tol]
+
+
+@pytest.mark.parametrize("dtype,rows", KEPT, ids=str)
+def test_scores_that_tell_whether_a_term_was_kept(dtype, rows):
+    """Keys of score 0 and v = 0, every 16th of score s and v = 1: w / (15 + w) is off by more than the tolerance without
+    the last term, by less with it."""
+    terms, tol = KEPT[dtype, rows]
+    s = telling_scores(dtype, rows)
+    assert len(s) >= 16
+    w = np.exp(s)
+    off = 15 / (15 + w)   # d log(w / (15 + w)) / d log w
+    assert np.all(remainder(w, dtype, terms - 1) * off > 2 * tol)
+    assert np.all(remainder(w, dtype, terms) * off < tol)

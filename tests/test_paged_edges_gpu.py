@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import paged
+from test_paged_edges import KEPT, telling_scores
 from test_paged_gpu import DT, Step, attention_tol, check, frequencies, half_step, host, rope_tol
 
 torch = pytest.importorskip("torch")
@@ -269,3 +270,64 @@ def test_positions_of_another_shape_are_refused(tq2):
     x = torch.zeros((3, 1, 4), device="cuda")
     with pytest.raises(ValueError):
         tq2.rope_axes(x, positions=torch.zeros((2, 3), dtype=torch.int64, device="cuda"), rope=rope)
+
+
+COUNTS = [
+    # new tokens, kv lengths, heads, kv heads, dim, page, window
+    ([1], [20_011], 8, 1, 64, 16, 0),
+    ([1], [131_071], 16, 2, 128, 64, 0),
+    ([1] * 5, [4097, 63, 9000, 1, 513], 8, 2, 128, 48, 0),
+    ([4, 4], [9000, 77], 8, 1, 64, 1, 700),
+    ([1] * 70, [900 + 13 * i for i in range(70)], 4, 1, 40, 100, 0),
+    ([33], [7000], 4, 1, 64, 16, 0),
+    ([260, 5], [1500, 3000], 16, 2, 128, 16, 0),
+    ([300], [20_000], 8, 1, 64, 20, 3000),
+    ([300, 40] * 12, [900, 390] * 12, 24, 8, 128, 16, 0),
+    ([64], [131_000], 8, 1, 128, 64, 0),
+]
+
+
+@pytest.mark.parametrize("case", COUNTS, ids=lambda c: f"{c[0][0]}x{len(c[0])}-{max(c[1])}-{c[4]}-{c[5]}-{c[6]}")
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_every_key_counts_once(tq2, case, dtype):
+    """k = 0 and v = 1 in feature j % dim: every weight is the same and every sum a whole number below 2^24 times it, so a
+    result is the share of the visible keys with that remainder, to the roundings of 1 / l and of the product."""
+    q_len, kv_len, heads, kv_heads, dim, page, window = case
+    step = Step(tq2, q_len, kv_len, kv_heads, dim, page, "slots", dtype)
+    for b, n in enumerate(kv_len):
+        j = torch.arange(n, device="cuda")
+        p, o = torch.from_numpy(step.table[b].astype(np.int64)).cuda()[j // page], j % page
+        step.k[p, o] = 0
+        step.v[p, o] = torch.nn.functional.one_hot(j % dim, dim)[:, None].to(DT[dtype])
+    q = step.queries(heads)
+    got = torch.empty(q.shape, device="cuda")
+    tq2.attention_paged(q, step.cache, step.batch, out=got, window=window)
+    want = np.zeros((step.tokens, dim))
+    d = np.arange(dim)
+    for t, _, pos in paged.places(step.q_start, kv_len):
+        lo, hi = max(0, pos + 1 - window) if window else 0, pos + 1
+        if hi > lo:
+            want[t] = ((hi - 1 - d) // dim - (lo - 1 - d) // dim) / (hi - lo)
+    want = np.repeat(want[:, None], heads, 1)
+    check(got, want, 2.0 ** -22 * want + 1e-30)
+
+
+@pytest.mark.parametrize("dtype,rows", KEPT, ids=str)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_f32_outputs_keep_the_terms_of_the_weights(tq2, dtype, rows, dim):
+    """As the host's test of these scores: 64 keys of score 0 and v = 0, but every 16th of score s and v = 1."""
+    s = telling_scores(dtype, rows)
+    q_len = 1 if rows == "few" else 40
+    step = Step(tq2, [q_len] * len(s), [64] * len(s), 1, dim, 16, "slots", dtype, rest=0.0)
+    step.k.zero_()
+    step.v.zero_()
+    for b, x in enumerate(s):
+        for j in range(3, 64, 16):
+            step.k[(*step.slot(b, j), 0, 0)] = float(x)
+            step.v[step.slot(b, j)] = 1.0
+    q = torch.zeros((step.tokens, 4, dim), device="cuda", dtype=DT[dtype])
+    q[..., 0] = 1
+    got = torch.empty(q.shape, device="cuda")
+    tq2.attention_paged(q, step.cache, step.batch, out=got, scale=1.0, causal=False)
+    w = np.repeat(np.exp(s) / (15 + np.exp(s)), q_len)[:, None, None] + np.zeros(got.shape)
+    check(got, w, KEPT[dtype, rows][1] * w)
