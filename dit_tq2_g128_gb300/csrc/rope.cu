@@ -151,10 +151,10 @@ rope_kernel(const RopeArgs a, int units, int hpg, unsigned int *status) {
         bool bad = false;
         const SeqSpan sp = seq_span(a.batch, b, bad);
         report_bad(bad, status);
-        if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n) return;
+        if (t < sp.q0 || t >= int64_t(sp.q0) + sp.n || (bad && g.paged)) return;  // (clamped lengths would name the slots of older keys)
         key = int64_t(sp.kv) - sp.n + (t - sp.q0);
         if (g.paged) {
-            if (bad || key < 0) return;  // (clamped lengths would name the slots of older keys)
+            if (key < 0) return;
             const int in_table = int(key) / a.batch.page_size;
             const int64_t page = page_of(a.batch, b, in_table, bad);
             report_bad(bad, status);
