@@ -5,19 +5,22 @@
 // exp(i position[axis] inv_freq).  The angle is kept as a fraction of a turn in
 // 64-bit integers: phase = position * turns mod 2^64 is exact whatever the
 // position, and only the nearest quarter turn's remainder (32 bits of it) is
-// rounded to f32, at most an eighth of a turn with 24 bits: 2^-25 of a radian or
-// so, the rounding of the f32 sine itself.  (Its own short series: with the library's
-// sine the 16-bit forms were bound by instructions, 15 an element.)
+// rounded to f32: the angle is off by at most 2^-23.6 of a radian (an eighth of a turn
+// with 24 bits, times a rounded 2 pi) and a sine or cosine by 1e-7 (2^-23.2; every remainder
+// of a sample of four million, in a model of this arithmetic).  (Its own short series:
+// with the library's sine the 16-bit forms took 15 instructions an element.)
 //
-// Bound by memory (each element read once and written once).  A thread owns one
-// unit (VP pairs) of one token: it forms the unit's sines once and turns it in up
-// to `hpg` heads, four heads' loads in flight at a time, 16 bytes a load and lane.
+// Bound by memory (each element read once and written once): in f32 by its rate, at 16
+// bits by its latency too, as twice the arithmetic lies between one set of loads and the
+// next.  A thread owns one unit (VP pairs) of one token: it forms the unit's sines once
+// and turns it in up to `hpg` heads, the loads of two heads (four where a pack is less
+// than 16 bytes) in flight at a time.
 // Any strides: the vector width falls back to one element where the pointers,
 // strides or pair count do not allow 16 (8) bytes.
 //
 // Measured: q, k and v of 4608 tokens, 24 heads of 128 in f32, from rows to heads: 58.3 us,
 // 86 % of the copy rate.  Prompts of 16,580 tokens into a paged cache, 32 query and 8
-// key heads of 128 in bf16: 101 us, 72 % (16-bit units cost twice the instructions a byte).
+// key heads of 128 in bf16: 101 us, 72 % (32 % of the issue slots, 42 % of the warps, waiting for loads).
 // One token: 3.2 us on the GPU, its launch.
 #include <cuda_bf16.h>
 

@@ -331,3 +331,20 @@ def test_f32_outputs_keep_the_terms_of_the_weights(tq2, dtype, rows, dim):
     tq2.attention_paged(q, step.cache, step.batch, out=got, scale=1.0, causal=False)
     w = np.repeat(np.exp(s) / (15 + np.exp(s)), q_len)[:, None, None] + np.zeros(got.shape)
     check(got, w, KEPT[dtype, rows][1] * w)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("to", ["f32", "f16"])
+def test_f32_rotations_keep_f32s_bits(tq2, interleaved, to):
+    """Sines and cosines off by 1e-7, one product's rounding (2^-24) and the result's: together below 2^-22 of |a| + |b|."""
+    rng = np.random.default_rng(3)
+    f, _ = frequencies(64, 1, rng, False)
+    pos = np.concatenate([np.arange(200), rng.integers(-(1 << 20), 1 << 20, 200)]).reshape(400, 1)
+    x = torch.randn((400, 3, 128), device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    out = torch.empty(x.shape, device="cuda", dtype=DT[to])
+    tq2.rope_axes(x, positions=torch.from_numpy(pos).cuda(), rope=tq2.Rope(f, interleaved=interleaved), out=[out])
+    want = paged.rotate(host(x), pos, f, [0] * 64, interleaved)
+    near = np.abs(host(x)).reshape(400, 3, 64, 2) if interleaved else np.abs(host(x)).reshape(400, 3, 2, 64).swapaxes(2, 3)
+    near = near.sum(-1)
+    near = np.repeat(near, 2, -1) if interleaved else np.concatenate([near, near], -1)
+    check(out, want, 2.0 ** -22 * near + (half_step(to) * np.abs(want) * 1.001 + 2.0 ** -25 if to == "f16" else 0))
