@@ -520,7 +520,8 @@ class PagedBatch:
 def rope_axes(q, k=None, v=None, *, positions, rope: Rope, out=None, inverse: bool = False, stream=None):
     """Rotate q and k [tokens, heads, dim] by their positions and copy v, into ``out`` (a sequence of as many tensors,
     of any layout and another type if wanted; default: new contiguous ones).  Returns the outputs as a tuple.
-    ``inverse`` is the gradient: the gradients of the outputs go in, those of the inputs come out."""
+    ``inverse`` is the gradient: the gradients of the outputs go in, those of the inputs come out.  (Autograd does not
+    record the call: outputs of tensors that require a gradient have none, and the backward pass is that second call.)"""
     tokens, _, dim = q.shape
     ins = [t for t in (q, k, v) if t is not None]
     if out is None:

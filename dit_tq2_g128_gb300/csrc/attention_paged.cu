@@ -51,8 +51,8 @@ constexpr int kMinTiles = 4;    // units of a run, at least, where pairs may be 
 constexpr int kWholeKeys = 512; // up to so many keys a pair stays whole (a join costs more than a CTA saves)
 
 // Query rows per (sequence, key head) that this kernel takes; more go to the tcgen05
-// kernel.  The limit is where O and S of a warp's 16 keys stop fitting its registers (168
-// a thread at two CTAs an SM): 32 rows of 64 features, 16 of 128.  Measured, this kernel
+// kernel.  The limit is where O and S of a warp's 16 keys no longer fit its registers (168
+// a thread at two CTAs an SM): 32 rows of 64 features (2 to 5 words spilled), 16 of 128.  Measured, this kernel
 // against that one: 28 rows of 64, 16 sequences of 1000 keys 13.7 / 16.2 us, 32 rows, 64
 // of 2000 keys 90 / 100, 21 rows, 16 of 1000 11.5 / 16.2 (8 of 200 keys, 32 rows: 9.8 /
 // 8.9); 40 rows of 64, spilled, 64 of 2000 keys 126 / 100; 16 rows of 128, 64 of 2000

@@ -35,7 +35,8 @@
 //    256 + 128 w.  P overwrites S in the cache's type (32 columns); for an f32 output the
 //    weights' remainder follows as a second term in the other 32 (errors of 1.5e-6 of
 //    the result in binary16 and 2.5e-6 in bf16 at 500 keys; a third bf16 term, through
-//    shared memory, made that 1.5e-6 and the kernel 30 % slower).
+//    shared memory, made that 1.5e-6 and the kernel 30 % slower).  binary16 weights are
+//    lifted first (weight_lift).
 //  * V stays as it lies in the cache, [key][feature]: the second MMA's B operand is
 //    MN-major, with the feature halves 16 KB apart (leading offset) and 8-key groups 1 KB
 //    apart (stride offset).  No transposed copy of V exists.

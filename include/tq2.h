@@ -495,15 +495,18 @@ int tq2_kv_append(const tq2_heads *q, const tq2_heads *q_out, const tq2_heads *k
  * over the keys j of t's sequence in head h / (heads / cache->heads) that the
  * token sees.  With pos = its key index: causal, j <= pos; else every j <
  * kv_len; with window > 0 also j > pos - window.  A token that sees no key gets
- * zeros.  Slots that a token does not see have no influence, whatever they hold.
+ * zeros.  Slots that a token does not see have no influence, whatever they hold;
+ * an infinity in v that it sees makes that feature of its result an infinity or a NaN.
  *   q     : view of the cache's type, 16-byte aligned, strides multiples of 8;
  *           heads a multiple of cache->heads
  *   out   : view of the same heads, of the cache's type or f32, 16-byte aligned,
  *           strides multiples of 8
  *   scale : finite (usually 1/sqrt(dim))
  * Scores, softmax statistics and sums are f32; the weights enter the second
- * product in the cache's type, or, for an f32 out, as a sum of two such terms (of
- * three in bf16 where a sequence and key head have at most 16 query rows).
+ * product in the cache's type, or, for an f32 out, as a sum of two such terms, and of
+ * three in bf16 where the call has few rows: max_q (at most tokens) times the query
+ * heads of a key head up to 32 for dim <= 64, up to 16 above.  So a token's result
+ * may differ in its rounding with the max_q of the batch that it is in.
  * Memory: `workspace` holds partial results of long contexts
  * (tq2_attention_paged_workspace_bytes of the same arguments, 16-byte aligned);
  * if NULL, a temporary from the device's pool is taken instead. */
