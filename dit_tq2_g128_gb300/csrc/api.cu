@@ -611,7 +611,8 @@ tq2::BatchView batch_view(const tq2_batch *b, const tq2_kv_cache *c) {
     v.pages = c->pages;
     v.seqs = int(b->seqs);
     v.max_q = int(b->max_q < b->tokens ? b->max_q : b->tokens);
-    v.max_kv = int(b->max_kv);
+    const int64_t width = b->table_stride * c->page_size;  // (a loose max_kv sizes nothing beyond the table)
+    v.max_kv = int(b->max_kv < width ? b->max_kv : width);
     v.page_size = int(c->page_size);
     return v;
 }

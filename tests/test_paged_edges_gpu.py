@@ -348,3 +348,14 @@ def test_f32_rotations_keep_f32s_bits(tq2, interleaved, to):
     near = near.sum(-1)
     near = np.repeat(near, 2, -1) if interleaved else np.concatenate([near, near], -1)
     check(out, want, 2.0 ** -22 * near + (half_step(to) * np.abs(want) * 1.001 + 2.0 ** -25 if to == "f16" else 0))
+
+
+@pytest.mark.parametrize("q_len", [1, 40])
+def test_a_loose_bound_of_the_keys_is_no_size(tq2, q_len):
+    """max_kv may be far above what the tables hold: 2^30 keys for each of 300 sequences would be too many to share out."""
+    step = Step(tq2, [q_len] * 300, [41 + i % 50 for i in range(300)], 8, 64, 16)
+    q = step.queries(8)
+    good = tq2.attention_paged(q, step.cache, step.batch)
+    loose = tq2.PagedBatch(*step.tables, tokens=step.tokens, max_q=q_len, max_kv=1 << 30)
+    for workspace in (None, tq2.attention_paged_workspace(q, step.cache, loose)):
+        assert torch.equal(tq2.attention_paged(q, step.cache, loose, workspace=workspace), good)
