@@ -175,11 +175,11 @@ def test_a_wait_that_cannot_be_met_is_reported(tq2):
 
 def test_a_wait_of_few_rows_that_runs_out_is_reported(tq2):
     """The first of 24 tiles, where some rows see a key and others do not, holds nothing but infinities, which the
-    consumers hand to the rows one by one for tens of microseconds; the copies of the fourth tile wait for them."""
-    step = Step(tq2, [16], [2000], 1, 64, 16)
+    consumers hand to the rows one by one for half a millisecond; the copies of the fourth tile wait for them."""
+    step = Step(tq2, [32], [2000], 1, 64, 16)
     j = torch.arange(512, device="cuda")
     p, o = torch.from_numpy(step.table[0].astype(np.int64)).cuda()[j // 16], j % 16
-    q = step.queries(2)
+    q = step.queries(1)
     step.v[p, o] = float("inf")
     good = tq2.attention_paged(q, step.cache, step.batch, window=1500)
     torch.cuda.synchronize()
