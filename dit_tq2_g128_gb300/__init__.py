@@ -58,6 +58,7 @@ EXPORTS = (
     "tq2_act16_to_f32", "tq2_gemm_act16", "tq2_attention_f32",
     "tq2_rope_turns", "tq2_rope_axes", "tq2_kv_append", "tq2_attention_paged",
     "tq2_attention_paged_workspace_bytes",
+    "tq2_moe_route", "tq2_moe_swiglu", "tq2_moe_swiglu_workspace_bytes", "tq2_sample",
 )
 
 
@@ -128,6 +129,15 @@ def _load():
     L.tq2_attention_paged.argtypes = [ch, ch, ch, ch, ctypes.c_float, i64, i32, vp, ctypes.c_size_t, vp]
     L.tq2_attention_paged_workspace_bytes.restype = ctypes.c_size_t
     L.tq2_attention_paged_workspace_bytes.argtypes = [i64, ch, ch]
+    # tq2_experts and tq2_sampling go as packed bytes too
+    L.tq2_moe_route.restype = i32
+    L.tq2_moe_route.argtypes = [vp, i32, i64, vp, vp, i64, i64, i64, i32, i32, ctypes.c_float, vp]
+    L.tq2_moe_swiglu.restype = i32
+    L.tq2_moe_swiglu.argtypes = [ch, vp, vp, vp, vp, vp, i32, i64, i64, vp, ctypes.c_size_t, vp]
+    L.tq2_moe_swiglu_workspace_bytes.restype = ctypes.c_size_t
+    L.tq2_moe_swiglu_workspace_bytes.argtypes = [ch, i32, i64, i64]
+    L.tq2_sample.restype = i32
+    L.tq2_sample.argtypes = [vp, i32, i64, vp, ch, vp, vp, i64, i64, vp]
     L.tq2_gemm_noalloc.restype = i32
     L.tq2_gemm_noalloc.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp]
     return L
@@ -337,6 +347,39 @@ def tq2_attention_paged(q, out, cache: bytes, batch: bytes, scale: float, window
 
 def tq2_attention_paged_workspace_bytes(heads: int, cache: bytes, batch: bytes) -> int:
     return int(lib.tq2_attention_paged_workspace_bytes(heads, cache, batch))
+
+
+# ---------------------------------------------------------------------------
+# Mixtures of experts and sampling; tq2_experts(...) and tq2_sampling(...) return the C structs as packed bytes.
+
+
+def tq2_experts(gate_up, down, experts: int, width: int, ffn: int, _pack=struct.Struct("=qqqqq").pack) -> bytes:
+    return _pack(_ptr(gate_up) or 0, _ptr(down) or 0, experts, width, ffn)
+
+
+def tq2_sampling(temperature=None, top_k=None, top_p=None, min_p=None, _pack=struct.Struct("=qqqq").pack) -> bytes:
+    return _pack(_ptr(temperature) or 0, _ptr(top_k) or 0, _ptr(top_p) or 0, _ptr(min_p) or 0)
+
+
+def tq2_moe_route(logits, dtype: int, row_stride: int, experts, weights, tokens: int, n_experts: int, top_k: int,
+                  sigmoid: int = 0, normalize: int = 1, scale: float = 1.0, stream=None) -> None:
+    _check(lib.tq2_moe_route(_ptr(logits), dtype, row_stride, _ptr(experts), _ptr(weights), tokens, n_experts, top_k,
+                             sigmoid, normalize, scale, _stream(stream)), "tq2_moe_route")
+
+
+def tq2_moe_swiglu(w: bytes, x, expert, weight, residual, out, dtype: int, tokens: int, top_k: int, workspace=None,
+                   workspace_bytes: int = 0, stream=None) -> None:
+    _check(lib.tq2_moe_swiglu(w, _ptr(x), _ptr(expert), _ptr(weight), _ptr(residual), _ptr(out), dtype, tokens, top_k,
+                              _ptr(workspace), workspace_bytes, _stream(stream)), "tq2_moe_swiglu")
+
+
+def tq2_moe_swiglu_workspace_bytes(w: bytes, dtype: int, tokens: int, top_k: int) -> int:
+    return int(lib.tq2_moe_swiglu_workspace_bytes(w, dtype, tokens, top_k))
+
+
+def tq2_sample(logits, dtype: int, row_stride: int, u, filters, tokens, prob, rows: int, vocab: int, stream=None) -> None:
+    _check(lib.tq2_sample(_ptr(logits), dtype, row_stride, _ptr(u), filters, _ptr(tokens), _ptr(prob), rows, vocab,
+                          _stream(stream)), "tq2_sample")
 
 
 # ---------------------------------------------------------------------------
@@ -580,3 +623,112 @@ def attention_paged(q, cache: KVCache, batch: PagedBatch, *, out=None, scale: fl
                         dim ** -0.5 if scale is None else scale, window, int(causal), workspace,
                         0 if workspace is None else workspace.numel(), stream)
     return out
+
+
+# ---------------------------------------------------------------------------
+# Mixtures of experts and sampling on torch tensors.
+
+
+def _rows(t, name: str):
+    """(rows, columns, row stride, type) of a CUDA matrix with contiguous rows."""
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor of 2 dimensions, got {t.device} {tuple(shape)}")
+    if strides[1] != 1 and shape[1] != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return shape[0], shape[1], strides[0], _DTYPE[t.dtype] if t.dtype in _DTYPE else _dtype_of(t)
+
+
+def _given(t, name: str, dtype, shape) -> int:
+    """The pointer of a contiguous CUDA tensor of this type and shape."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor {tuple(shape)}, got {t.device} {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def moe_route(logits, top_k: int, *, sigmoid: bool = False, normalize: bool = True, scale: float = 1.0, experts=None,
+              weights=None, stream=None):
+    """The ``top_k`` experts of each token by the router's logits [tokens, experts] (float32, float16 or bfloat16; rows
+    of any stride), and their weights: softmax or ``sigmoid`` scores, over their sum if ``normalize``, times ``scale``.
+    Returns int32 and float32 tensors [tokens, top_k] (``experts`` and ``weights`` if given); see tq2_moe_route."""
+    import torch
+    tokens, n, stride, dtype = _rows(logits, "logits")
+    shape = (tokens, top_k)
+    if experts is None or weights is None:
+        with _on(stream):
+            if experts is None:
+                experts = torch.empty(shape, dtype=torch.int32, device=logits.device)
+            if weights is None:
+                weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
+    tq2_moe_route(logits.data_ptr(), dtype, stride, _given(experts, "experts", torch.int32, shape),
+                  _given(weights, "weights", torch.float32, shape), tokens, n, top_k, int(sigmoid), int(normalize), scale,
+                  stream)
+    return experts, weights
+
+
+class Experts:
+    """The ternary weights of a mixture's experts in the device layout (upload_weight): ``gate_up`` of experts * 2 * ffn
+    rows (each expert's gate projection, then its up projection) of ``width`` columns, ``down`` of experts * width rows
+    of ``ffn`` columns.  Holds the tensors; see tq2_experts in include/tq2.h."""
+
+    def __init__(self, gate_up, down, *, experts: int, width: int, ffn: int):
+        self.experts, self.width, self.ffn = int(experts), int(width), int(ffn)
+        for t, name, rows, cols in ((gate_up, "gate_up", self.experts * 2 * self.ffn, self.width),
+                                    (down, "down", self.experts * self.width, self.ffn)):
+            nbytes = tq2_soa_bytes(rows, cols)
+            if nbytes == 0:
+                raise TQ2Error(TQ2_ERR_BAD_K, "Experts")
+            _check_tensor(t, name, "torch.uint8", nbytes)
+        self.gate_up, self.down = gate_up, down
+        self.packed = tq2_experts(gate_up, down, self.experts, self.width, self.ffn)
+
+
+def moe_swiglu_workspace(experts: Experts, tokens: int, top_k: int, dtype):
+    """A device workspace for moe_swiglu of up to ``tokens`` tokens of this torch type (None if not needed)."""
+    import torch
+    nbytes = tq2_moe_swiglu_workspace_bytes(experts.packed, _dtype_of(torch.empty(0, dtype=dtype)), tokens, top_k)
+    return torch.empty(nbytes, dtype=torch.uint8, device=experts.down.device) if nbytes else None
+
+
+def moe_swiglu(layer: Experts, x, expert, weight, *, residual=None, out=None, workspace=None, stream=None):
+    """A mixture-of-experts layer on tokens x [tokens, width] (float32, float16 or bfloat16), routed to ``expert`` (int32
+    [tokens, top_k]; -1: none) with ``weight`` (float32): the weighted sum of their SwiGLU products (+ residual).
+    Returns ``out`` (default: a new tensor; it may be the residual)."""
+    import torch
+    tokens, width, stride, dtype = _rows(x, "x")
+    if width != layer.width or (stride != width and tokens > 1):
+        raise ValueError(f"x must be a contiguous tensor [tokens, {layer.width}], got {tuple(x.shape)}")
+    if expert.dim() != 2 or expert.shape[0] != tokens:
+        raise ValueError(f"expert must be [{tokens}, top_k], got {tuple(expert.shape)}")
+    if out is None:
+        with _on(stream):
+            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    tq2_moe_swiglu(layer.packed, x.data_ptr(), _given(expert, "expert", torch.int32, expert.shape),
+                   _given(weight, "weight", torch.float32, expert.shape),
+                   None if residual is None else _given(residual, "residual", x.dtype, x.shape),
+                   _given(out, "out", x.dtype, x.shape), dtype, tokens, expert.shape[1], workspace,
+                   0 if workspace is None else workspace.numel(), stream)
+    return out
+
+
+def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, out=None, prob=None, stream=None):
+    """One token of each row of logits [rows, vocab] (float32, float16 or bfloat16; rows of any stride) by random numbers
+    ``u`` (float32 [rows], in [0, 1)).  The filters are CUDA tensors [rows] (float32, top_k int32), None where off.
+    Returns int64 tokens and the float32 probabilities with which they were drawn, [rows] each (``out`` and ``prob`` if
+    given); see tq2_sample."""
+    import torch
+    rows, vocab, stride, dtype = _rows(logits, "logits")
+    shape, f32 = (rows,), torch.float32
+    if out is None or prob is None:
+        with _on(stream):
+            if out is None:
+                out = torch.empty(shape, dtype=torch.int64, device=logits.device)
+            if prob is None:
+                prob = torch.empty(shape, dtype=f32, device=logits.device)
+    filters = tq2_sampling(None if temperature is None else _given(temperature, "temperature", f32, shape),
+                           None if top_k is None else _given(top_k, "top_k", torch.int32, shape),
+                           None if top_p is None else _given(top_p, "top_p", f32, shape),
+                           None if min_p is None else _given(min_p, "min_p", f32, shape))
+    tq2_sample(logits.data_ptr(), dtype, stride, _given(u, "u", f32, shape), filters,
+               _given(out, "out", torch.int64, shape), _given(prob, "prob", f32, shape), rows, vocab, stream)
+    return out, prob

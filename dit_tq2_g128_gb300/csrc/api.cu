@@ -857,4 +857,159 @@ int tq2_attention_paged(const tq2_heads *q, const tq2_heads *out, const tq2_kv_c
     return finish(e != cudaSuccess ? e : f);
 }
 
+// ---------------------------------------------------------------------------
+// mixtures of experts, sampling
+
+namespace {
+
+constexpr int64_t kMaxExperts = 1024, kMaxTopK = 32, kMaxFeatures = 65536, kMaxPairs = int64_t(1) << 22;
+constexpr int64_t kMaxVocabulary = int64_t(1) << 18, kMaxRows = int64_t(1) << 24;
+
+// Rows of logits: [rows, n], row r from element r * stride on.
+int check_logits(const void *logits, int dtype, int64_t stride, int64_t rows, int64_t n) {
+    if (!logits || !dtype_ok(dtype)) return TQ2_ERR_INVALID_ARG;
+    if (rows > 1 && (stride < n || stride > kMaxStride)) return TQ2_ERR_INVALID_ARG;
+    return reinterpret_cast<uintptr_t>(logits) % dtype_bytes(dtype) ? TQ2_ERR_MISALIGNED : TQ2_OK;
+}
+size_t logits_bytes(int dtype, int64_t stride, int64_t rows, int64_t n) {
+    return size_t((rows - 1) * (rows > 1 ? stride : 0) + n) * dtype_bytes(dtype);
+}
+
+bool misaligned(const void *p, size_t to) { return reinterpret_cast<uintptr_t>(p) % to != 0; }
+
+int check_experts(const tq2_experts *w, int dtype, int64_t tokens, int64_t top_k) {
+    if (!w || !dtype_ok(dtype)) return TQ2_ERR_INVALID_ARG;
+    if (w->width <= 0 || w->width % tq2::kBlockW || w->ffn <= 0 || w->ffn % tq2::kBlockW) return TQ2_ERR_BAD_K;
+    if (w->width > kMaxFeatures || w->ffn > kMaxFeatures || w->experts < 1 || w->experts > kMaxExperts || top_k < 1 ||
+        top_k > kMaxTopK || tokens < 0 || tokens > kMaxPairs / top_k)
+        return TQ2_ERR_INVALID_ARG;
+    // rows of a weight are counted in 32 bits
+    if (w->experts * 2 * w->ffn > INT32_MAX || w->experts * w->width > INT32_MAX) return TQ2_ERR_INVALID_ARG;
+    return TQ2_OK;
+}
+
+}  // namespace
+
+int tq2_moe_route(const void *logits, int dtype, int64_t row_stride, int32_t *experts, float *weights, int64_t tokens,
+                  int64_t n_experts, int64_t top_k, int sigmoid, int normalize, float scale, void *stream) {
+    if (tokens < 0 || tokens > kMaxRows || n_experts < 1 || n_experts > kMaxExperts || top_k < 1 || top_k > kMaxTopK ||
+        top_k > n_experts || !std::isfinite(scale) || !dtype_ok(dtype))
+        return TQ2_ERR_INVALID_ARG;
+    if (tokens == 0) return TQ2_OK;
+    int st = check_logits(logits, dtype, row_stride, tokens, n_experts);
+    if (st != TQ2_OK) return st;
+    if (!experts || !weights) return TQ2_ERR_INVALID_ARG;
+    if (misaligned(experts, 4) || misaligned(weights, 4)) return TQ2_ERR_MISALIGNED;
+    const size_t lb = logits_bytes(dtype, row_stride, tokens, n_experts), ob = size_t(tokens) * size_t(top_k) * 4;
+    if (overlaps(experts, ob, logits, lb) || overlaps(weights, ob, logits, lb) || overlaps(experts, ob, weights, ob))
+        return TQ2_ERR_INVALID_ARG;
+    tq2::LaunchCtx ctx;
+    st = prepare(stream, &ctx, {logits, experts, weights});
+    if (st != TQ2_OK) return st;
+    tq2::RouteArgs a = {};
+    a.logits = logits;
+    a.row_stride = tokens > 1 ? row_stride : 0;
+    a.experts = experts;
+    a.weights = weights;
+    a.tokens = tokens;
+    a.n = int(n_experts);
+    a.top_k = int(top_k);
+    a.sigmoid = sigmoid != 0;
+    a.normalize = normalize != 0;
+    a.scale = scale;
+    return finish(tq2::launch_moe_route(a, dtype, ctx));
+}
+
+size_t tq2_moe_swiglu_workspace_bytes(const tq2_experts *w, int dtype, int64_t tokens, int64_t top_k) {
+    if (check_experts(w, dtype, tokens, top_k) != TQ2_OK || tokens == 0) return 0;
+    return tq2::moe_ws_bytes(tokens, top_k, w->experts, w->width, w->ffn, dtype);
+}
+
+int tq2_moe_swiglu(const tq2_experts *w, const void *x, const int32_t *expert, const float *weight,
+                   const void *residual, void *out, int dtype, int64_t tokens, int64_t top_k, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    int st = check_experts(w, dtype, tokens, top_k);
+    if (st != TQ2_OK || tokens == 0) return st;
+    if (!w->gate_up || !w->down || !x || !expert || !weight || !out) return TQ2_ERR_INVALID_ARG;
+    if (!aligned16(w->gate_up) || !aligned16(w->down) || !aligned16(x) || !aligned16(out) ||
+        (residual && !aligned16(residual)) || misaligned(expert, 4) || misaligned(weight, 4))
+        return TQ2_ERR_MISALIGNED;
+    const size_t xb = size_t(tokens) * size_t(w->width) * dtype_bytes(dtype), pb = size_t(tokens) * size_t(top_k) * 4;
+    const size_t gb = tq2_soa_bytes(w->experts * 2 * w->ffn, w->width), db = tq2_soa_bytes(w->experts * w->width, w->ffn);
+    const size_t need = tq2::moe_ws_bytes(tokens, top_k, w->experts, w->width, w->ffn, dtype);
+    if (workspace && workspace_bytes < need) return TQ2_ERR_INVALID_ARG;
+    if (workspace && !aligned16(workspace)) return TQ2_ERR_MISALIGNED;
+    const struct {
+        const void *p;
+        size_t n;
+    } in[] = {{x, xb}, {expert, pb}, {weight, pb}, {w->gate_up, gb}, {w->down, db}, {residual, residual ? xb : 0}};
+    for (const auto &i : in)
+        if ((i.p != residual || residual != out) && overlaps(out, xb, i.p, i.n)) return TQ2_ERR_INVALID_ARG;
+    if (workspace) {
+        if (overlaps(workspace, need, out, xb)) return TQ2_ERR_INVALID_ARG;
+        for (const auto &i : in)
+            if (overlaps(workspace, need, i.p, i.n)) return TQ2_ERR_INVALID_ARG;
+    }
+    tq2::LaunchCtx ctx;
+    st = prepare(stream, &ctx, {w->gate_up, w->down, x, expert, weight, residual, out, workspace});
+    if (st != TQ2_OK) return st;
+    tq2::MoeArgs a = {};
+    a.gate_up = w->gate_up;
+    a.down = w->down;
+    a.x = x;
+    a.residual = residual;
+    a.expert = expert;
+    a.weight = weight;
+    a.out = out;
+    a.tokens = tokens;
+    a.experts = int(w->experts);
+    a.width = int(w->width);
+    a.ffn = int(w->ffn);
+    a.top_k = int(top_k);
+    void *ws = workspace;
+    if (!ws && cudaMallocAsync(&ws, need, ctx.stream) != cudaSuccess) {
+        (void)cudaGetLastError();
+        return TQ2_ERR_CUDA;
+    }
+    const cudaError_t e = tq2::launch_moe(a, dtype, ws, ctx);
+    const cudaError_t f = ws != workspace ? cudaFreeAsync(ws, ctx.stream) : cudaSuccess;
+    return finish(e != cudaSuccess ? e : f);
+}
+
+int tq2_sample(const void *logits, int dtype, int64_t row_stride, const float *u, const tq2_sampling *filters,
+               int64_t *tokens, float *prob, int64_t rows, int64_t vocab, void *stream) {
+    if (rows < 0 || rows > kMaxRows || vocab < 1 || vocab > kMaxVocabulary || !dtype_ok(dtype)) return TQ2_ERR_INVALID_ARG;
+    if (rows == 0) return TQ2_OK;
+    int st = check_logits(logits, dtype, row_stride, rows, vocab);
+    if (st != TQ2_OK) return st;
+    if (!u || !tokens) return TQ2_ERR_INVALID_ARG;
+    const tq2_sampling off = {};
+    const tq2_sampling f = filters ? *filters : off;
+    const void *in[] = {u, f.temperature, f.top_k, f.top_p, f.min_p};
+    if (misaligned(tokens, 8) || misaligned(prob, 4)) return TQ2_ERR_MISALIGNED;
+    for (const void *p : in)
+        if (misaligned(p, 4)) return TQ2_ERR_MISALIGNED;
+    const size_t lb = logits_bytes(dtype, row_stride, rows, vocab), rb = size_t(rows) * 4;
+    if (overlaps(tokens, 2 * rb, logits, lb)) return TQ2_ERR_INVALID_ARG;
+    if (prob && (overlaps(prob, rb, logits, lb) || overlaps(prob, rb, tokens, 2 * rb))) return TQ2_ERR_INVALID_ARG;
+    for (const void *p : in)
+        if (p && (overlaps(tokens, 2 * rb, p, rb) || (prob && overlaps(prob, rb, p, rb)))) return TQ2_ERR_INVALID_ARG;
+    tq2::LaunchCtx ctx;
+    st = prepare(stream, &ctx, {logits, u, f.temperature, f.top_k, f.top_p, f.min_p, tokens, prob});
+    if (st != TQ2_OK) return st;
+    tq2::SampleArgs a = {};
+    a.logits = logits;
+    a.row_stride = rows > 1 ? row_stride : 0;
+    a.u = u;
+    a.temperature = f.temperature;
+    a.top_k = f.top_k;
+    a.top_p = f.top_p;
+    a.min_p = f.min_p;
+    a.tokens = tokens;
+    a.prob = prob;
+    a.rows = rows;
+    a.vocab = int(vocab);
+    return finish(tq2::launch_sample(a, dtype, ctx));
+}
+
 }  // extern "C"

@@ -1,0 +1,128 @@
+// Routing: the top_k experts of each token by its logits, and their weights.
+//
+// Order: logits descending, equal ones by index, NaN last; softmax and sigmoid do not change it, so the choice
+// is one of exact comparisons and no rounding decides it.  The weights are scores over the logits (softmax over all
+// experts, or a sigmoid each), divided by their sum over the chosen where asked.
+//
+// A warp takes a token: each lane holds NV logits as integers in the order of their values; top_k times the warp's
+// maximum (one redux) and the lowest index that holds it (another).
+#include <cstdint>
+
+#include "dtype.cuh"
+#include "tq2_internal.cuh"
+
+namespace tq2 {
+namespace {
+
+constexpr int kWarps = 8;  // tokens of a block
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(32 * kWarps)
+moe_route_kernel(const T *__restrict__ logits, int64_t row_stride, int32_t *__restrict__ experts,
+                 float *__restrict__ weights, int64_t tokens, int n, int top_k, int sigmoid, int normalize, float scale) {
+    const int lane = threadIdx.x & 31;
+    const int64_t t = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (t >= tokens) return;
+    const T *row = logits + t * row_stride;
+    uint32_t key[NV];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int i = j * 32 + lane;
+        key[j] = i < n ? order_key(to_f32(row[i])) : 0u;  // 0: none, or taken
+    }
+    uint32_t best = 0;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) best = max(best, key[j]);
+    const float top = key_value(__reduce_max_sync(0xffffffffu, best));
+    float z = 1.f;  // the softmax's denominator
+    if (!sigmoid && !normalize) {
+        float s = 0.f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (key[j]) s += expf(key_value(key[j]) - top);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        z = s;
+    }
+    int mine = 0;            // lane j: the j-th expert and its logit
+    float value = 0.f;
+    for (int k = 0; k < top_k; ++k) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+        int at = INT32_MAX;
+        if (best == m) {
+#pragma unroll
+            for (int j = NV - 1; j >= 0; --j)
+                if (key[j] == m) at = j * 32 + lane;
+        }
+        const int i = __reduce_min_sync(0xffffffffu, at);
+        if (at == i) {
+            best = 0;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                if (j * 32 + lane == i) key[j] = 0u;
+                best = max(best, key[j]);
+            }
+        }
+        if (lane == k) {
+            mine = i;
+            value = key_value(m);
+        }
+    }
+    // a row without a logit above -inf: weights of 0
+    float s = 0.f;
+    if (lane < top_k && top != -INFINITY) {
+        if (!sigmoid) {
+            s = expf(value - top);
+        } else if (!(value < 0.f)) {
+            s = 1.f / (1.f + expf(-value));
+        } else {  // (normalised, times exp(-top) where that is below 0 too: sigmoids that underflow have quotients all the same)
+            s = expf(normalize ? value - fminf(top, 0.f) : value) / (1.f + expf(value));
+        }
+    }
+    float sum = z;
+    if (normalize) {
+        sum = s;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane < top_k) {
+        experts[t * top_k + lane] = mine;
+        weights[t * top_k + lane] = s == 0.f ? 0.f : (sigmoid && !normalize ? s : s / sum) * scale;
+    }
+}
+
+template <typename T>
+cudaError_t launch(const RouteArgs &a, const LaunchCtx &ctx) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((a.tokens + kWarps - 1) / kWarps));
+    cfg.blockDim = dim3(32 * kWarps);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    auto go = [&](auto kern) {
+        return cudaLaunchKernelEx(&cfg, kern, static_cast<const T *>(a.logits), a.row_stride, a.experts, a.weights,
+                                  a.tokens, a.n, a.top_k, a.sigmoid, a.normalize, a.scale);
+    };
+    if (a.n <= 64) return go(moe_route_kernel<T, 2>);
+    if (a.n <= 128) return go(moe_route_kernel<T, 4>);
+    if (a.n <= 256) return go(moe_route_kernel<T, 8>);
+    if (a.n <= 512) return go(moe_route_kernel<T, 16>);
+    return go(moe_route_kernel<T, 32>);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_route(const RouteArgs &a, int dtype, const LaunchCtx &ctx) {
+    switch (dtype) {
+        case TQ2_F32: return launch<float>(a, ctx);
+        case TQ2_F16: return launch<__half>(a, ctx);
+        default: return launch<__nv_bfloat16>(a, ctx);
+    }
+}
+
+}  // namespace tq2

@@ -148,6 +148,45 @@ size_t attention_paged_chunk_ws_bytes(int64_t heads, int64_t kv_heads, int64_t d
                                       int64_t max_kv);
 cudaError_t launch_attention_paged_chunk(const PagedArgs &a, int dtype, bool out_f32, void *ws, const LaunchCtx &ctx);
 
+// Routing (moe_route.cu): the top_k of n logits of each token, and their weights.
+struct RouteArgs {
+    const void *logits;
+    int64_t row_stride;  // elements
+    int32_t *experts;
+    float *weights;
+    int64_t tokens;
+    int n, top_k, sigmoid, normalize;
+    float scale;
+};
+cudaError_t launch_moe_route(const RouteArgs &a, int dtype, const LaunchCtx &ctx);
+
+// Mixture of ternary experts (moe.cu): SoA weights of experts * 2 ffn rows of width, and experts * width rows of ffn.
+struct MoeArgs {
+    const void *gate_up, *down;
+    const void *x, *residual;
+    const int32_t *expert;
+    const float *weight;
+    void *out;
+    int64_t tokens;
+    int experts, width, ffn, top_k;
+};
+size_t moe_ws_bytes(int64_t tokens, int64_t top_k, int64_t experts, int64_t width, int64_t ffn, int dtype);
+cudaError_t launch_moe(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx);
+
+// Sampling (sample.cu): NULL filters are off.
+struct SampleArgs {
+    const void *logits;
+    int64_t row_stride;  // elements
+    const float *u, *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p;
+    int64_t *tokens;
+    float *prob;  // NULL: not wanted
+    int64_t rows;
+    int vocab;
+};
+cudaError_t launch_sample(const SampleArgs &a, int dtype, const LaunchCtx &ctx);
+
 // Skinny-M tensor-core kernel (2 <= m <= 32, k up to the shared-memory limit
 // of its K slices): one launch, no workspace.  cudaErrorNotSupported outside.
 bool skinny_mma_fits(int64_t m, int64_t n, int64_t k);

@@ -519,6 +519,101 @@ int tq2_attention_paged(const tq2_heads *q, const tq2_heads *out, const tq2_kv_c
  * max_q and max_kv (0: none is needed, or the arguments are not valid). */
 size_t tq2_attention_paged_workspace_bytes(int64_t heads, const tq2_kv_cache *cache, const tq2_batch *batch);
 
+/* ---------------------------------------------------------------------------
+ * Mixtures of ternary experts, and sampling (the rest of a decoder's step).
+ * The pages have no counterpart but `argmax` (a name only).  These serve: as of
+ * the ternary products above, no gradient of them is computed.
+ * ------------------------------------------------------------------------- */
+
+/* The experts of each token by the router's logits [tokens, n_experts], and their
+ * weights.  Experts are taken by their logits, descending, equal ones by index, NaN
+ * last: top_k different ones, in that order.  With s_i = exp(l_i) / sum_j exp(l_j)
+ * over all experts, or, if sigmoid, s_i = 1 / (1 + exp(-l_i)):
+ *     weights[t, j] = scale * s_i              (i = experts[t, j])
+ *     normalize != 0: divided by the sum of s over the token's top_k.
+ * A logit of -inf (a masked expert) has s = 0; where all of a token's are -inf its
+ * weights are 0.  A NaN or an infinite logit makes weights of its token NaN.
+ *   logits     : device, of type dtype (tq2_dtype), row t from element t * row_stride
+ *                on (row_stride >= n_experts; any for one token); aligned to its element
+ *   experts    : device int32 [tokens, top_k]
+ *   weights    : device f32 [tokens, top_k]
+ *   n_experts  : 1 .. 1024;  top_k : 1 .. min(n_experts, 32)
+ *   scale      : finite
+ * Scores and sums in f32.  No output may overlap another argument.  tokens == 0 is a
+ * no-op. */
+int tq2_moe_route(const void *logits, int dtype, int64_t row_stride, int32_t *experts, float *weights, int64_t tokens,
+                  int64_t n_experts, int64_t top_k, int sigmoid, int normalize, float scale, void *stream);
+
+/* The weights of a mixture's experts.  Expert e's gate projection is rows e * 2 ffn ..
+ * e * 2 ffn + ffn - 1 of gate_up, its up projection the ffn rows after them (of `width`
+ * columns each); its down projection is rows e * width .. of down (of `ffn` columns). */
+typedef struct {
+    const void *gate_up; /* device SoA weight of experts * 2 * ffn rows, k = width */
+    const void *down;    /* device SoA weight of experts * width rows, k = ffn */
+    int64_t experts;     /* 1 .. 1024 */
+    int64_t width;       /* a multiple of 128, up to 65536 */
+    int64_t ffn;         /* a multiple of 128, up to 65536 */
+} tq2_experts;
+
+/* A mixture-of-experts layer on routed tokens:
+ *     out[t] = residual[t] + sum_j weight[t, j] * Down_e (silu(Gate_e x_t) * (Up_e x_t)),
+ * e = expert[t, j]; j in ascending order.  An expert of -1 is none (a padded or dropped
+ * token); any other value outside 0 .. experts - 1 counts as none too, and
+ * TQ2_ERR_BAD_BATCH is then recorded in the device status word.  The same expert
+ * twice counts twice.  A token without experts gets its residual, or zeros.
+ *   x        : device [tokens, width] of type dtype (tq2_dtype)
+ *   expert   : device int32 [tokens, top_k] (from tq2_moe_route)
+ *   weight   : device f32 [tokens, top_k]
+ *   residual : device [tokens, width] of type dtype, or NULL; may equal out
+ *   out      : device [tokens, width] of type dtype
+ *   top_k    : 1 .. 32; tokens * top_k <= 2^22
+ * gate_up, down, x, residual and out are 16-byte aligned.
+ * Sums in f32, one rounding to the output's type.
+ * Memory: `workspace` holds the activations on their way
+ * (tq2_moe_swiglu_workspace_bytes of the same arguments, 16-byte aligned); if NULL, a
+ * temporary from the device's pool is taken instead.  Calls that share a workspace
+ * must be ordered.
+ * Errors: TQ2_ERR_BAD_K (width or ffn no positive multiple of 128), TQ2_ERR_INVALID_ARG,
+ * TQ2_ERR_MISALIGNED, TQ2_ERR_CUDA.  tokens == 0 is a no-op. */
+int tq2_moe_swiglu(const tq2_experts *w, const void *x, const int32_t *expert, const float *weight,
+                   const void *residual, void *out, int dtype, int64_t tokens, int64_t top_k, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/* Bytes of workspace that tq2_moe_swiglu uses: a function of the sizes alone (0: the
+ * arguments are not valid, or no token is there).  No call of fewer tokens needs more. */
+size_t tq2_moe_swiglu_workspace_bytes(const tq2_experts *w, int dtype, int64_t tokens, int64_t top_k);
+
+/* Filters of tq2_sample: device arrays of one value a row, NULL where a filter is off. */
+typedef struct {
+    const float *temperature; /* NULL: 1.  Not above 0 (or NaN): the likeliest token */
+    const int32_t *top_k;     /* not above 0: off */
+    const float *top_p;       /* 1 or more (or NaN): off; 0 or less: the likeliest token */
+    const float *min_p;       /* not above 0 (or NaN): off; 1 or more: tokens as likely as the likeliest */
+} tq2_sampling;
+
+/* One token of each row of logits [rows, vocab], by a given random number.  Tokens are
+ * ordered by their logits, descending, equal ones by index.  Token i's weight is
+ * w_i = exp((l_i - l_max) / temperature).  Of that order
+ *     top_k keeps the first top_k tokens,
+ *     top_p of these the shortest prefix that holds top_p of their weight,
+ *     min_p of these the tokens with w_i >= min_p;
+ * drawn is the first token whose cumulative weight is above u times what is kept.
+ * prob is its weight over what is kept.
+ * A logit of -inf or NaN has weight 0; where a row holds nothing else, its token is -1
+ * and prob 0.  Among infinite logits only these count.
+ *   logits : device, of type dtype (tq2_dtype), row r from element r * row_stride on
+ *            (row_stride >= vocab; any for one row); aligned to its element
+ *   u      : device f32 [rows], random numbers in [0, 1) (one outside is taken as the
+ *            nearest in it, NaN as 0)
+ *   tokens : device int64 [rows]
+ *   prob   : device f32 [rows], or NULL
+ *   vocab  : 1 .. 262144
+ * Weights are integers in units of 2^-45 (a smaller one is 0), each within 2^-30 of
+ * itself; their sums are exact, so that results do not depend on any order of summation.
+ * No output may overlap another argument.  rows == 0 is a no-op. */
+int tq2_sample(const void *logits, int dtype, int64_t row_stride, const float *u, const tq2_sampling *filters,
+               int64_t *tokens, float *prob, int64_t rows, int64_t vocab, void *stream);
+
 /* Bounded device-side waits.  Every spin-wait inside a kernel (on an mbarrier)
  * gives up after `ns` nanoseconds of %globaltimer time, records
  * TQ2_ERR_TIMEOUT in a device status word and lets the kernel exit cleanly
@@ -530,7 +625,7 @@ uint64_t tq2_set_wait_timeout_ns(uint64_t ns);
 
 /* Synchronises `stream`, then reads the device status word of the current
  * device: TQ2_OK, or TQ2_ERR_TIMEOUT if any kernel since the last check gave up
- * on a wait, or TQ2_ERR_BAD_BATCH if one found a batch's tables out of range;
+ * on a wait, or TQ2_ERR_BAD_BATCH if one found a batch's tables (or a routed expert) out of range;
  * TQ2_ERR_CUDA if the synchronisation itself failed.  What is returned is
  * cleared; where both happened the timeout comes first and the next call returns
  * the other. */
