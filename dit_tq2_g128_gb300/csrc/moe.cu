@@ -14,7 +14,7 @@
 namespace tq2 {
 namespace {
 
-constexpr int kPlanThreads = 1024, kPlanWarps = 32;
+constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanAhead = 8;
 
 // Exclusive sum over the block's threads of v; total: the sum.
 __device__ __forceinline__ int block_scan(int v, int *part, int *total) {
@@ -57,13 +57,28 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
     const int first = min(pairs, warp * per), last = min(pairs, first + per);
     int *mine = cnt + warp * experts;
     bool bad = false;
-    for (int p0 = first; p0 < last; p0 += 32) {
-        const int p = p0 + lane, e = p < last ? expert[p] : -1;
-        const bool there = e >= 0 && e < experts;
-        bad |= !there && e != -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, there ? e : -1);
-        if (there && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
+    // 8 x 32 of them in flight, and kept where they are all there are
+    int id[kPlanAhead];
+    auto load = [&](int p0) {
+#pragma unroll
+        for (int i = 0; i < kPlanAhead; ++i) {
+            const int p = p0 + 32 * i + lane;
+            id[i] = p < last ? expert[p] : -1;
+            if (id[i] < 0 || id[i] >= experts) {
+                bad |= id[i] != -1;
+                id[i] = -1;
+            }
+        }
+    };
+    for (int p0 = first; p0 < last; p0 += 32 * kPlanAhead) {
+        load(p0);
+#pragma unroll
+        for (int i = 0; i < kPlanAhead; ++i) {
+            if (p0 + 32 * i >= last) break;
+            const uint32_t same = __match_any_sync(0xffffffffu, id[i]);
+            if (id[i] >= 0 && lane == __ffs(same) - 1) mine[id[i]] += __popc(same);
+            __syncwarp();
+        }
     }
     report_bad(bad, status);
     __syncthreads();
@@ -88,19 +103,23 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
         plan.counts[1] = rows;
     }
     __syncthreads();
-    for (int p0 = first; p0 < last; p0 += 32) {
-        const int p = p0 + lane, x = p < last ? expert[p] : -1;
-        const bool there = x >= 0 && x < experts;
-        const uint32_t same = __match_any_sync(0xffffffffu, there ? x : -1);
-        int row = -1;
-        if (there) {
-            row = mine[x] + __popc(same & ((1u << lane) - 1));
-            plan.row_pair[row] = p;
+    for (int p0 = first; p0 < last; p0 += 32 * kPlanAhead) {
+        if (last - first > 32 * kPlanAhead) load(p0);
+#pragma unroll
+        for (int i = 0; i < kPlanAhead; ++i) {
+            if (p0 + 32 * i >= last) break;
+            const int p = p0 + 32 * i + lane, x = id[i];
+            const uint32_t same = __match_any_sync(0xffffffffu, x);
+            int row = -1;
+            if (x >= 0) {
+                row = mine[x] + __popc(same & ((1u << lane) - 1));
+                plan.row_pair[row] = p;
+            }
+            __syncwarp();
+            if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
+            __syncwarp();
+            if (p < last) plan.pair_row[p] = row;
         }
-        __syncwarp();
-        if (there && lane == __ffs(same) - 1) mine[x] += __popc(same);
-        __syncwarp();
-        if (p < last) plan.pair_row[p] = row;
     }
 }
 
@@ -210,11 +229,15 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(MoeArgs a, MoePlan
 
 size_t pad(size_t n) { return (n + 255) & ~size_t(255); }
 
+// Columns of a tile.  With 128 a tile's codes are decoded for twice the tokens; with 64 more warps decode, which is what
+// counts where experts have few.
+int tile_cols(int64_t pairs, int64_t experts, int terms) { return pairs * terms > 64 * std::min(pairs, experts) ? 128 : 64; }
+
 struct Workspace {
     MoePlan plan;
     __half *staged_x, *staged_h;
     float *scale_x, *scale_h, *h, *y;
-    int max_tiles;
+    int max_tiles, cols;
     size_t bytes;
 
     Workspace(char *base, int64_t pairs, int64_t experts, int64_t width, int64_t ffn, int terms) {
@@ -223,7 +246,8 @@ struct Workspace {
             p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(base + at);
             at += pad(n * sizeof(*p));
         };
-        const int64_t tile_rows = kMoeCols / terms;
+        cols = tile_cols(pairs, experts, terms);
+        const int64_t tile_rows = cols / terms;
         max_tiles = int(std::min(pairs, experts) + pairs / tile_rows);  // each expert leaves less than one unfilled
         take(plan.counts, 2);
         take(plan.tiles, size_t(max_tiles));
@@ -250,7 +274,7 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     cudaError_t e = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(plan_smem));
     if (e == cudaSuccess)
         e = launch_dependent(moe_plan_kernel, dim3(1), kPlanThreads, int(plan_smem), ctx.stream, a.expert, w.plan, int(pairs),
-                             a.experts, kMoeCols / terms, ctx.status);
+                             a.experts, w.cols / terms, ctx.status);
     if (e == cudaSuccess)
         e = launch_dependent(moe_stage_kernel<T, true>, dim3(unsigned(pairs)), kStageThreads, 0, ctx.stream,
                              static_cast<const T *>(a.x), w.plan, w.staged_x, w.scale_x, a.width, a.top_k, terms);
@@ -260,6 +284,7 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     g.pairs = pairs;
     g.experts = a.experts;
     g.terms = terms;
+    g.cols = w.cols;
     g.max_tiles = w.max_tiles;
     SoaView v = soa_view(a.gate_up, int64_t(a.experts) * 2 * a.ffn, a.width);
     g.qs = v.qs;

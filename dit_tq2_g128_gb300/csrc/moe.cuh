@@ -7,7 +7,6 @@
 
 namespace tq2 {
 
-constexpr int kMoeCols = 128;  // staged rows (MMA columns) of a tile
 
 // Some tokens of one expert: rows row0 .. row0 + n - 1 of those sorted by expert.
 struct alignas(16) MoeTile {
@@ -33,6 +32,7 @@ struct MoeGemm {
     int64_t pairs;
     int experts, rows, k;
     int terms;           // staged rows of a row
+    int cols;            // staged rows (MMA columns) of a tile, at most: 64 or 128
     int max_tiles;
 };
 // gate_up: rows holds gate then up rows, out the SwiGLU of rows / 2 features; else out is the product.

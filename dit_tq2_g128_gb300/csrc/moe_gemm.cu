@@ -15,8 +15,9 @@
 //    is rounded is the activations' staging and the sums.
 //  * Copies: codes by TMA, 512 weights of 128 rows a stage (64 KB in flight an SM); activations by TMA, 128 features of a
 //    tile's rows a stage.
-//  * Roles: warp 0 codes, warp 1 MMAs (owns tensor memory), warp 2 activations, warps 4-7 decode, warps 8-15 scale and
-//    sum (columns 0-63 and 64-127).  One persistent CTA an SM.  Every wait is bounded; a timeout sets the status word and the
+//  * Roles: warp 0 codes, warp 1 MMAs (owns tensor memory), warp 2 activations; two groups of four warps decode every other
+//    block; two groups scale and sum, each half of the columns, or, where tiles have 64 columns, every other item, so that
+//    one item's end runs under the next one's blocks.  One persistent CTA an SM.  Every wait is bounded; a timeout sets the status word and the
 //    CTA drains its copies and MMAs before it leaves.
 #include <cstdint>
 
@@ -26,26 +27,39 @@
 namespace tq2 {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4, W_SUM = 8;
-constexpr int kCodeStages = 4, kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
-constexpr int kActStages = 4, kActBytes = kMoeCols * kBlockW * 2;             // 32 KB: two halves of 64 features
-constexpr int kABufs = 4, kACols = kBlockW / 2, kDBufs = 2;
-constexpr uint32_t kTmemCols = 512, kACol = kDBufs * kMoeCols;
-static_assert(kACol + kABufs * kACols <= kTmemCols, "TMEM budget");
+constexpr int kThreads = 640;
+constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4, W_SUM = 12;
+// registers a thread at launch, and of the roles' warpgroups after it (one, two and two of them)
+constexpr int kRegs = 96, kRegsControl = 48, kRegsDecode = 72, kRegsSum = 144;
+static_assert(kRegsControl + 2 * kRegsDecode + 2 * kRegsSum <= 5 * kRegs, "registers");
+constexpr int kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
+constexpr int kABufs = 4, kACols = kBlockW / 2;
+constexpr uint32_t kTmemCols = 512;
+
+template <int COLS>
+struct Shape {
+    static constexpr int CODES = COLS == 64 ? 6 : 4;              // stages of codes
+    static constexpr int ACTS = COLS == 64 ? 8 : 4;               // stages of activations
+    static constexpr int ACT_BYTES = COLS * kBlockW * 2;          // two halves of 64 features
+    static constexpr int DBUFS = 256 / COLS;
+    static constexpr uint32_t A_COL = DBUFS * COLS;
+    static constexpr int OFF_ACT = CODES * kCodeBytes, OFF_CTL = OFF_ACT + ACTS * ACT_BYTES;
+    static_assert(A_COL + kABufs * kACols <= kTmemCols, "TMEM budget");
+};
 
 struct Ctl {
-    uint64_t c_full[kCodeStages], c_empty[kCodeStages];
-    uint64_t x_full[kActStages], x_empty[kActStages];
+    uint64_t c_full[6], c_empty[6];
+    uint64_t x_full[8], x_empty[8];
     uint64_t a_full[kABufs], a_empty[kABufs];
-    uint64_t d_full[kDBufs], d_empty[kDBufs];
+    uint64_t d_full[4], d_empty[4];
+    uint64_t turn[2];  // (64 columns) a summing group may begin its next item: the other has seen all blocks of the one before
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
 };
-constexpr int kOffAct = kCodeStages * kCodeBytes, kOffCtl = kOffAct + kActStages * kActBytes;
-constexpr int kSmem = kOffCtl + int(sizeof(Ctl)) + 1024;
-static_assert(kSmem <= 232448, "shared memory budget");
+template <int COLS>
+constexpr int kSmem = Shape<COLS>::OFF_CTL + int(sizeof(Ctl)) + 1024;
+static_assert(kSmem<64> <= 232448 && kSmem<128> <= 232448, "shared memory budget");
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {  // K-major, 128-byte swizzle: rows 128 B, 8-row groups 1024 B
     return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
@@ -94,6 +108,27 @@ __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32])
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+template <int N>
+__device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Two f32 at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float first(uint64_t p) { return __uint_as_float(uint32_t(p)); }
+__device__ __forceinline__ float second(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four words of 16 codes as 32 pairs of binary16 numbers code - 1: pair i of a word is its codes i and i + 8.  They stand at
@@ -129,24 +164,39 @@ __device__ __forceinline__ Item item_of(const MoeGemm &g, int i, int parts) {
     return it;
 }
 
+// MMA columns of this CTA's items, one read ahead.
+struct Columns {
+    const MoeGemm &g;
+    int parts, items, i, n;
+    __device__ __forceinline__ Columns(const MoeGemm &gemm, int p, int count) : g(gemm), parts(p), items(count), i(blockIdx.x) { read(); }
+    __device__ __forceinline__ void read() { n = i < items ? g.plan.tiles[i / parts].n : 0; }
+    __device__ __forceinline__ int take() {
+        const int cols = (n * g.terms + 15) & ~15;
+        i += gridDim.x;
+        read();
+        return cols;
+    }
+};
+
 // x / (1 + exp(-x)), with the fast exponential and quotient (relative error about 2^-21)
 __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
-template <bool GATE_UP>
+template <bool GATE_UP, int COLS>
 __global__ void __launch_bounds__(kThreads, 1)
-moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap xmap, const MoeGemm g,
-                unsigned int *status, uint64_t wait_ns) {
+moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap xmap,
+                const __grid_constant__ CUtensorMap xmap64, const MoeGemm g, unsigned int *status, uint64_t wait_ns) {
+    using L = Shape<COLS>;
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    Ctl *ctl = reinterpret_cast<Ctl *>(smem + kOffCtl);
+    Ctl *ctl = reinterpret_cast<Ctl *>(smem + L::OFF_CTL);
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     volatile int *abort_flag = &ctl->abort;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kCodeStages; ++s) {
+        for (int s = 0; s < L::CODES; ++s) {
             mbar_init(&ctl->c_full[s], 1);
-            mbar_init(&ctl->c_empty[s], 4);
+            mbar_init(&ctl->c_empty[s], 8);
         }
-        for (int s = 0; s < kActStages; ++s) {
+        for (int s = 0; s < L::ACTS; ++s) {
             mbar_init(&ctl->x_full[s], 1);
             mbar_init(&ctl->x_empty[s], 1);
         }
@@ -154,10 +204,11 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             mbar_init(&ctl->a_full[s], 4);
             mbar_init(&ctl->a_empty[s], 1);
         }
-        for (int s = 0; s < kDBufs; ++s) {
+        for (int s = 0; s < L::DBUFS; ++s) {
             mbar_init(&ctl->d_full[s], 1);
-            mbar_init(&ctl->d_empty[s], 8);
+            mbar_init(&ctl->d_empty[s], COLS / 16);
         }
+        for (int s = 0; s < 2; ++s) mbar_init(&ctl->turn[s], 4);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
         fence_mbarrier_init();
@@ -179,176 +230,206 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         return bool(__all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, wait_ns, status)));
     };
 
-    if (warp == W_CODES) {
-        int n = 0;  // stages filled
-        bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = item_of(g, i, parts);
-            const int row = it.tile.expert * g.rows;
-            const int y0 = row + (GATE_UP ? 64 : 128) * it.part, y1 = GATE_UP ? y0 + g.rows / 2 : y0 + 64;
-            for (int k = 0; k < g.k; k += kCodeK, ++n) {
-                const int s = n % kCodeStages;
-                if (n >= kCodeStages && !(ok = wait_on(&ctl->c_empty[s], (n / kCodeStages - 1) & 1))) break;
-                if (elect_one()) {
-                    mbar_expect_tx(&ctl->c_full[s], kCodeBytes);
-                    const uint32_t dst = smem_u32(smem) + uint32_t(s * kCodeBytes);
-                    tma_2d(dst, &cmap, k / 4, y0, &ctl->c_full[s]);
-                    tma_2d(dst + kCodeBytes / 2, &cmap, k / 4, y1, &ctl->c_full[s]);
+    if (warp < W_DECODE) {
+        regs_down<kRegsControl>();
+        if (warp == W_CODES) {
+            int n = 0;  // stages filled
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const Item it = item_of(g, i, parts);
+                const int row = it.tile.expert * g.rows;
+                const int y0 = row + (GATE_UP ? 64 : 128) * it.part, y1 = GATE_UP ? y0 + g.rows / 2 : y0 + 64;
+                for (int k = 0; k < g.k; k += kCodeK, ++n) {
+                    const int s = n % L::CODES;
+                    if (n >= L::CODES && !(ok = wait_on(&ctl->c_empty[s], (n / L::CODES - 1) & 1))) break;
+                    if (elect_one()) {
+                        mbar_expect_tx(&ctl->c_full[s], kCodeBytes);
+                        const uint32_t dst = smem_u32(smem) + uint32_t(s * kCodeBytes);
+                        tma_2d(dst, &cmap, k / 4, y0, &ctl->c_full[s]);
+                        tma_2d(dst + kCodeBytes / 2, &cmap, k / 4, y1, &ctl->c_full[s]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
-        if (lane == 0)  // every copy lands before the CTA ends
-            for (int j = max(0, n - kCodeStages); j < n; ++j)
-                mbar_wait_bounded(&ctl->c_full[j % kCodeStages], (j / kCodeStages) & 1, drain_ns(wait_ns), status);
-        __syncwarp();
-    } else if (warp == W_ACT) {
-        int n = 0;
-        bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = item_of(g, i, parts);
-            for (int b = 0; b < nb; ++b, ++n) {
-                const int s = n % kActStages;
-                if (n >= kActStages && !(ok = wait_on(&ctl->x_empty[s], (n / kActStages - 1) & 1))) break;
-                if (elect_one()) {
-                    mbar_expect_tx(&ctl->x_full[s], uint32_t(it.cols) * 256);
-                    const uint32_t dst = smem_u32(smem) + uint32_t(kOffAct + s * kActBytes);
-                    for (int c = 0; c < it.cols; c += 16)
+            if (lane == 0)  // every copy lands before the CTA ends
+                for (int j = max(0, n - L::CODES); j < n; ++j)
+                    mbar_wait_bounded(&ctl->c_full[j % L::CODES], (j / L::CODES) & 1, drain_ns(wait_ns), status);
+            __syncwarp();
+        } else if (warp == W_ACT) {
+            int n = 0;
+            bool ok = true;
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const Item it = item_of(g, i, parts);
+                for (int b = 0; b < nb; ++b, ++n) {
+                    const int s = n % L::ACTS;
+                    if (n >= L::ACTS && !(ok = wait_on(&ctl->x_empty[s], (n / L::ACTS - 1) & 1))) break;
+                    if (elect_one()) {
+                        // (boxes of 16 rows, or of 64: the rows after the tile's are other experts', whose columns nothing reads)
+                        const bool wide = it.cols > 32;
+                        const int step = wide ? 64 : 16, boxes = (it.cols + step - 1) / step;
+                        mbar_expect_tx(&ctl->x_full[s], uint32_t(boxes * step) * 256);
+                        const uint32_t dst = smem_u32(smem) + uint32_t(L::OFF_ACT + s * L::ACT_BYTES);
+                        for (int c = 0; c < boxes; ++c)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            tma_2d(dst + uint32_t(h * (kActBytes / 2) + c * 128), &xmap, b * kBlockW + 64 * h,
-                                   it.tile.row0 * g.terms + c, &ctl->x_full[s]);
+                            for (int h = 0; h < 2; ++h)
+                                tma_2d(dst + uint32_t(h * (L::ACT_BYTES / 2) + c * step * 128), wide ? &xmap64 : &xmap,
+                                       b * kBlockW + 64 * h, it.tile.row0 * g.terms + c * step, &ctl->x_full[s]);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
-        if (lane == 0)
-            for (int j = max(0, n - kActStages); j < n; ++j)
-                mbar_wait_bounded(&ctl->x_full[j % kActStages], (j / kActStages) & 1, drain_ns(wait_ns), status);
-        __syncwarp();
-    } else if (warp == W_MMA) {
-        int n = 0;  // blocks
-        bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            const Item it = item_of(g, i, parts);
-            const uint32_t idesc = uint32_t(uniform(int((1u << 4) | (uint32_t(it.cols >> 3) << 17) | (uint32_t(128 >> 4) << 24))));
-            for (int b = 0; b < nb; ++b, ++n) {
-                const int sx = n % kActStages, sa = n % kABufs, sd = n % kDBufs;
-                if (n >= kDBufs) ok = wait_on(&ctl->d_empty[sd], (n / kDBufs - 1) & 1);
-                ok = ok && wait_on(&ctl->x_full[sx], (n / kActStages) & 1) && wait_on(&ctl->a_full[sa], (n / kABufs) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    const uint64_t db = desc_k(smem_u32(smem) + uint32_t(kOffAct + sx * kActBytes));
-                    const uint32_t d = tmem + uint32_t(sd * kMoeCols), at = tmem + kACol + uint32_t(sa * kACols);
+            if (lane == 0)
+                for (int j = max(0, n - L::ACTS); j < n; ++j)
+                    mbar_wait_bounded(&ctl->x_full[j % L::ACTS], (j / L::ACTS) & 1, drain_ns(wait_ns), status);
+            __syncwarp();
+        } else if (warp == W_MMA) {
+            // (one lane takes the whole loop, from values that the compiler knows to be uniform)
+            if (elect_one()) {
+                const uint64_t x0 = desc_k(smem_u32(smem) + uint32_t(L::OFF_ACT));
+                auto wait_one = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, wait_ns, status); };
+                int n = 0;  // blocks
+                bool ok = true;
+                Columns next(g, parts, items);
+                for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                    const uint32_t idesc = (1u << 4) | (uint32_t(next.take() >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+                    for (int b = 0; b < nb; ++b, ++n) {
+                        const int sx = n % L::ACTS, sa = n % kABufs, sd = n % L::DBUFS;
+                        if (n >= L::DBUFS) ok = wait_one(&ctl->d_empty[sd], (n / L::DBUFS - 1) & 1);
+                        ok = ok && wait_one(&ctl->x_full[sx], (n / L::ACTS) & 1) && wait_one(&ctl->a_full[sa], (n / kABufs) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4));
+                        const uint32_t d = tmem + uint32_t(sd * COLS), at = tmem + L::A_COL + uint32_t(sa * kACols);
 #pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * (kActBytes / 2 >> 4) + 2 * (kk & 3)), idesc, kk > 0);
-                    tc_commit(&ctl->a_empty[sa]);
-                    tc_commit(&ctl->x_empty[sx]);
-                    tc_commit(&ctl->d_full[sd]);
+                        for (int kk = 0; kk < 8; ++kk)
+                            mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * (L::ACT_BYTES / 2 >> 4) + 2 * (kk & 3)), idesc,
+                                   kk > 0);
+                        tc_commit(&ctl->a_empty[sa]);
+                        tc_commit(&ctl->x_empty[sx]);
+                        tc_commit(&ctl->d_full[sd]);
+                    }
                 }
-                __syncwarp();
+                tc_commit(&ctl->drain);
             }
+            __syncwarp();
         }
-        if (elect_one()) tc_commit(&ctl->drain);
-        __syncwarp();
-    } else if (warp >= W_DECODE && warp < W_SUM) {
-        const int q = warp & 3;
+    } else if (warp < W_SUM) {
+        regs_down<kRegsDecode>();
+        const int q = warp & 3, group = (warp - W_DECODE) >> 2;
         // the row of this thread's lane among the stage's 128: gate rows in lanes 0-15, the up rows of the same features above
         const int r = GATE_UP ? (lane < 16 ? 16 * q + lane : 48 + 16 * q + lane) : 32 * q + lane;
-        int n = 0, stage = 0;
+        int n0 = 0, stage0 = 0;  // blocks and stages before the item
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-            for (int b = 0; b < nb; ++b, ++n) {
-                const int sc = stage % kCodeStages, sa = n % kABufs;
-                if ((b & 3) == 0 && !(ok = wait_on(&ctl->c_full[sc], (stage / kCodeStages) & 1))) break;
-                const uint8_t *row = smem + sc * kCodeBytes + r * 128;
-                uint4 w[2];
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x, n0 += nb, stage0 += (nb + 3) / 4) {
+            for (int b = 0; b < nb; ++b) {
+                const int stage = stage0 + b / 4, sc = stage % L::CODES, n = n0 + b, sa = n % kABufs;
+                const bool last = (b & 3) == 3 || b == nb - 1;
+                // (each group waits for every stage, so that none is ever two uses of a slot ahead of the other)
+                if ((b & 3) == 0 && !(ok = wait_on(&ctl->c_full[sc], (stage / L::CODES) & 1))) break;
+                if ((n & 1) == group) {
+                    const uint8_t *row = smem + sc * kCodeBytes + r * 128;
+                    uint4 w[2];
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    w[j] = *reinterpret_cast<const uint4 *>(row + (((2 * (b & 3) + j) ^ (r & 7)) << 4));
-                if ((b & 3) == 3 || b == nb - 1) {
+                    for (int j = 0; j < 2; ++j)
+                        w[j] = *reinterpret_cast<const uint4 *>(row + (((2 * (b & 3) + j) ^ (r & 7)) << 4));
+                    if (n >= kABufs && !(ok = wait_on(&ctl->a_empty[sa], (n / kABufs - 1) & 1))) break;
+                    tc_fence_after();
+                    const uint32_t at = tmem + L::A_COL + uint32_t(sa * kACols) + (uint32_t(q * 32) << 16);
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        uint32_t v[32];
+                        decode(w[j], v);
+                        tm_st32(at + uint32_t(32 * j), v);
+                    }
+                    tm_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&ctl->a_full[sa]);
+                }
+                if (last) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->c_empty[sc]);
-                    ++stage;
                 }
-                if (n >= kABufs && !(ok = wait_on(&ctl->a_empty[sa], (n / kABufs - 1) & 1))) break;
-                tc_fence_after();
-                const uint32_t at = tmem + kACol + uint32_t(sa * kACols) + (uint32_t(q * 32) << 16);
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    uint32_t v[32];
-                    decode(w[j], v);
-                    tm_st32(at + uint32_t(32 * j), v);
-                }
-                tm_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&ctl->a_full[sa]);
             }
         }
-    } else if (warp >= W_SUM) {
-        const int q = warp & 3, col0 = 64 * ((warp - W_SUM) >> 2);
-        int n = 0;
+    } else {
+        regs_up<kRegsSum>();
+        const int q = warp & 3, group = (warp - W_SUM) >> 2, col0 = COLS == 128 ? 64 * group : 0;
+        const int features = GATE_UP ? g.rows / 2 : g.rows;
+        const int step = COLS == 128 ? gridDim.x : 2 * gridDim.x;
+        int n0 = COLS == 128 ? 0 : group * nb, j = group;  // blocks and (64 columns) items of this CTA before the item
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+        for (int i = COLS == 128 ? blockIdx.x : blockIdx.x + group * gridDim.x; ok && i < items; i += step, n0 += COLS == 128 ? nb : 2 * nb, j += 2) {
             const Item it = item_of(g, i, parts);
             const int row = it.tile.expert * g.rows + (GATE_UP ? 64 * it.part + 16 * q + (lane & 15) + (lane < 16 ? 0 : g.rows / 2)
                                                               : 128 * it.part + 32 * q + lane);
             const __half *dp = g.d + int64_t(row) * nb;
-            float acc[64];
+            // the scales of this group's rows, two a lane
+            const int r0 = col0 / g.terms, left = it.tile.n - r0;
+            float scale[2];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) acc[c] = 0.f;
+            for (int j = 0; j < 2; ++j) scale[j] = g.scale[it.tile.row0 + min(r0 + 32 * j + lane, it.tile.n - 1)];
+            uint64_t acc[32];  // columns 2 c, 2 c + 1
+#pragma unroll
+            for (int c = 0; c < 32; ++c) acc[c] = 0;
             float dn = __half2float(dp[0]);
-            for (int b = 0; b < nb; ++b, ++n) {
-                const int sd = n % kDBufs;
-                const float d = dn;
+            // (in turn: a group that waited for a block two uses of its accumulator ahead would take the one before for it)
+            if (COLS == 64 && j > 0 && !(ok = wait_on(&ctl->turn[group], ((j - 1) >> 1) & 1))) break;
+            for (int b = 0; b < nb; ++b) {
+                const int n = n0 + b, sd = n % L::DBUFS;
+                const uint64_t d = pair(dn, dn);
                 if (b + 1 < nb) dn = __half2float(dp[b + 1]);
-                if (!(ok = wait_on(&ctl->d_full[sd], (n / kDBufs) & 1))) break;
+                if (!(ok = wait_on(&ctl->d_full[sd], (n / L::DBUFS) & 1))) break;
                 tc_fence_after();
-                const uint32_t at = tmem + uint32_t(sd * kMoeCols + col0) + (uint32_t(q * 32) << 16);
+                const uint32_t at = tmem + uint32_t(sd * COLS + col0) + (uint32_t(q * 32) << 16);
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     if (col0 + 32 * h < it.cols) {
                         uint32_t v[32];
                         tm_ld32(at + uint32_t(32 * h), v);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) acc[32 * h + c] = fmaf(d, __uint_as_float(v[c]), acc[32 * h + c]);
+                        for (int c = 0; c < 16; ++c)
+                            acc[16 * h + c] = fma2(d, uint64_t(v[2 * c]) | uint64_t(v[2 * c + 1]) << 32, acc[16 * h + c]);
                     }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->d_empty[sd]);
             }
             if (!ok) break;
-            // rows of this warp's columns (the staged terms of one side by side)
+            if (COLS == 64 && lane == 0) mbar_arrive(&ctl->turn[group ^ 1]);
+            float *out = g.out + int64_t(it.tile.row0 + r0) * features;
             auto finish = [&](auto two) {
                 constexpr int S = decltype(two)::value;
-                const int r0 = col0 / S, left = it.tile.n - r0;
-                const float *scale = g.scale + it.tile.row0 + r0;
-                const int features = GATE_UP ? g.rows / 2 : g.rows;
-                float *out = g.out + int64_t(it.tile.row0 + r0) * features;
-                if (S == 2) {
-#pragma unroll
-                    for (int c = 0; c < 32; ++c) acc[c] = acc[2 * c] + acc[2 * c + 1];
-                }
+                // row c of the group: column c, or the sum of columns 2 c and 2 c + 1 (terms)
+                auto sum = [&](int c) {
+                    return S == 2 ? first(acc[c]) + second(acc[c]) : c & 1 ? second(acc[c >> 1]) : first(acc[c >> 1]);
+                };
                 if (GATE_UP) {
                     out += 64 * it.part + 16 * q + (lane & 15);
-                    const bool up = lane >= 16;
+                    const int up = lane >= 16;
 #pragma unroll
-                    for (int c = 0; c < 64 / S; c += 2) {
-                        if (c >= left) break;
-                        // lanes 0-15 finish row c, lanes 16-31 row c + 1
-                        const float s = scale[min(c + up, left - 1)];
-                        const float other = __shfl_xor_sync(0xffffffffu, up ? acc[c] : acc[c + 1], 16);
-                        const float gate = (up ? other : acc[c]) * s, ups = (up ? acc[c + 1] : other) * s;
-                        if (c + up < left) out[int64_t(c + up) * features] = silu(gate) * ups;
-                    }
+                    for (int c0 = 0; c0 < 64 / S; c0 += 8)
+                        if (c0 < left) {
+#pragma unroll
+                            for (int c = c0; c < c0 + 8; c += 2) {
+                                // lanes 0-15 finish row c, lanes 16-31 row c + 1
+                                const float s = __shfl_sync(0xffffffffu, scale[c >> 5], (c & 31) + up);
+                                const float other = __shfl_xor_sync(0xffffffffu, up ? sum(c) : sum(c + 1), 16);
+                                const float gate = (up ? other : sum(c)) * s, ups = (up ? sum(c + 1) : other) * s;
+                                if (c + up < left) out[int64_t(c + up) * features] = silu(gate) * ups;
+                            }
+                        }
                 } else {
                     out += 128 * it.part + 32 * q + lane;
 #pragma unroll
-                    for (int c = 0; c < 64 / S; ++c)
-                        if (c < left) out[int64_t(c) * features] = acc[c] * scale[c];
+                    for (int c0 = 0; c0 < 64 / S; c0 += 8)
+                        if (c0 < left) {
+#pragma unroll
+                            for (int c = c0; c < c0 + 8; ++c) {
+                                const float s = __shfl_sync(0xffffffffu, scale[c >> 5], c & 31);
+                                if (c < left) out[int64_t(c) * features] = sum(c) * s;
+                            }
+                        }
                 }
             };
             if (g.terms == 2)
@@ -381,22 +462,29 @@ cudaError_t map_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base,
     return cudaSuccess;
 }
 
-}  // namespace
-
-cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
-    CUtensorMap cmap, xmap;
+template <int COLS>
+cudaError_t launch(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
+    CUtensorMap cmap, xmap, xmap64;
     cudaError_t e = map_2d(&cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.qs, g.k / 4, int64_t(g.experts) * g.rows, g.k / 4, 128, 64,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    if (e == cudaSuccess)
-        e = map_2d(&xmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, g.staged, g.k, g.pairs * g.terms, int64_t(g.k) * 2, 64, 16,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    for (int box : {16, 64})
+        if (e == cudaSuccess)
+            e = map_2d(box == 16 ? &xmap : &xmap64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, g.staged, g.k, g.pairs * g.terms,
+                       int64_t(g.k) * 2, 64, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
     if (e != cudaSuccess) return e;
-    auto kernel = gate_up ? moe_gemm_kernel<true> : moe_gemm_kernel<false>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    auto kernel = gate_up ? moe_gemm_kernel<true, COLS> : moe_gemm_kernel<false, COLS>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<COLS>);
     if (e != cudaSuccess) return e;
     const int64_t items = int64_t(g.max_tiles) * (g.rows / 128);
     const unsigned grid = unsigned(std::min<int64_t>(items, ctx.num_sms));
-    return launch_dependent(kernel, dim3(grid), kThreads, kSmem, ctx.stream, cmap, xmap, g, ctx.status, ctx.wait_ns);
+    return launch_dependent(kernel, dim3(grid), kThreads, kSmem<COLS>, ctx.stream, cmap, xmap, xmap64, g, ctx.status,
+                            ctx.wait_ns);
+}
+
+}  // namespace
+
+cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
+    return g.cols == 64 ? launch<64>(g, gate_up, ctx) : launch<128>(g, gate_up, ctx);
 }
 
 }  // namespace tq2

@@ -99,6 +99,14 @@ def test_tokens_of_one_expert(tq2, dtype, tokens):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts,width,ffn,tokens", [(40, 512, 768, 60), (64, 128, 1408, 130), (24, 2304, 640, 9),
+                                                      (3, 1664, 4096, 400)])
+def test_more_work_than_one_turn_of_the_gpu(tq2, dtype, experts, width, ffn, tokens):
+    """Several items a CTA, odd numbers of blocks, every ring wrapping."""
+    run(tq2, Layer(tq2, experts, width, ffn, seed=experts), dtype, tokens, 3)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_many_tokens_uneven(tq2, dtype):
     """Experts with hundreds of tokens beside experts with none or one."""
     layer, rng = Layer(tq2, 9, 384, 256, seed=3), np.random.default_rng(4)
