@@ -1,114 +1,597 @@
 // Sampling: one token of each row of logits, by a given random number.
 //
 // Tokens are ordered by their logits, descending, equal ones by index.  Weights w = exp((l - max) / temperature) are
-// integers in units of 2^-45, so that sums of them are exact in any order; temperature, top-k, top-p and min-p each keep
-// a prefix of the order, and the token drawn is the first whose cumulative weight passes u times the kept weight.
-// Every question is then one of counts or sums over a prefix.
+// integers in units of 2^-45 (sample_weight.cuh), so that sums of them are exact in any order; top-k, top-p and min-p
+// each keep a prefix of the order, and the token drawn is the first whose cumulative weight passes u times the kept
+// weight.  Every question is then one of a count or a sum over a prefix, and no sort of a row is needed.
 //
-// The plain form: a block a row, each question by bisection over the order's integers.
+// A cluster of CTAs takes a row and keeps it in shared memory: it is read from memory once.
+//  * The head: a bound that at least k (or some hundreds) of the threads' own maxima reach; the few elements above it go to
+//    the first CTA, which sorts them (bitonic, 1024 at most) and answers every question from their cumulative weights, if
+//    they reach that far: with a top-k always, without one where the distribution is as peaked as a model's usually is.
+//  * Else the whole order: a histogram of counts and weights over bins of 1/64 in log2 of the weight finds the bin that
+//    an answer lies in; its elements (at most 1024, or split further by their bits) are sorted as the head is.
+//
+// Bound by latency for one row (cluster barriers and the sort), by the pass over the row for many.
+#include <algorithm>
 #include <cstdint>
 
 #include "dtype.cuh"
+#include "paged_attention.cuh"
 #include "sample_weight.cuh"
 #include "tq2_internal.cuh"
 
 namespace tq2 {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kBinsPerUnit = 64, kBins = (kWeightBits + 1) * kBinsPerUnit;  // 2944
+constexpr int kList = 1024;
+constexpr int kHead = 512, kMostHeadK = 768;
+constexpr int kMaxCluster = 8;
 
-struct Sum {
-    uint64_t count, mass;
+enum Op { OP_DONE, OP_HISTOGRAM, OP_REFINE, OP_SPAN, OP_GATHER, OP_HEAVY, OP_TIE };
+// What the first CTA has the others do.
+struct Command {
+    int op, bin, shift;
+    uint32_t low, high;  // keys
+    uint32_t rank;       // OP_TIE: which of the elements `low`, from 0
 };
 
-__device__ Sum block_sum(Sum v, Sum *part) {
+struct Shared {
+    unsigned long long mass[kBins];
+    unsigned long long list[kList];  // key << 32 | ~index
+    unsigned long long cum[kList];
+    uint64_t table[64];
+    unsigned long long part[kWarps];
+    unsigned long long total, found_mass, found_before, kept;
+    uint32_t count[kBins];
+    uint32_t top[kMaxCluster], ties[kMaxCluster];
+    uint32_t n_list, low, high;
+    int found, bound;
+    Command cmd;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same place in CTA `rank`'s shared memory, as a generic pointer.
+template <typename P>
+__device__ __forceinline__ P *at_cta(P *p, uint32_t rank) {
+    uint64_t r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<P *>(r);
+}
+
+__device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        v.count += __shfl_xor_sync(0xffffffffu, v.count, o);
-        v.mass += __shfl_xor_sync(0xffffffffu, v.mass, o);
+    for (int o = 1; o < 32; o <<= 1) {
+        const unsigned long long x = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += x;
+    }
+    return v;
+}
+// Inclusive sums over the block's threads.
+__device__ __forceinline__ unsigned long long block_scan(unsigned long long v, Shared *sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    v = warp_scan(v);
+    __syncthreads();
+    if (lane == 31) sh->part[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+        const unsigned long long s = warp_scan(lane < kWarps ? sh->part[lane] : 0);
+        if (lane < kWarps) sh->part[lane] = s;
     }
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    return v + (warp ? sh->part[warp - 1] : 0);
+}
+
+// Descending bitonic sort of list[0, n) (n a power of two).
+__device__ void sort_list(unsigned long long *list, int n) {
+    for (int size = 2; size <= n; size <<= 1)
+        for (int step = size >> 1; step; step >>= 1) {
+            __syncthreads();
+            for (int i = threadIdx.x; i < n / 2; i += kThreads) {
+                const int a = 2 * i - (i & (step - 1)), b = a + step;
+                const unsigned long long x = list[a], y = list[b];
+                if ((x < y) == ((a & size) == 0)) {
+                    list[a] = y;
+                    list[b] = x;
+                }
+            }
+        }
     __syncthreads();
-    Sum s = {0, 0};
-    for (int w = 0; w < kThreads / 32; ++w) {
-        s.count += part[w].count;
-        s.mass += part[w].mass;
+}
+
+// A row's elements of this CTA, from `first` on, in shared memory.
+template <typename T>
+__device__ __forceinline__ uint32_t load_slice(const T *src, int n, float *x) {
+    constexpr int V = 16 / sizeof(T);
+    struct alignas(16) Pack {
+        T e[V];
+    };
+    uint32_t best = 0;
+    auto put = [&](int i, float v) {
+        x[i] = v;
+        best = max(best, order_key(v));
+    };
+    const int head = min(n, int((16 - (reinterpret_cast<uintptr_t>(src) & 15)) % 16 / sizeof(T)));
+    for (int i = threadIdx.x; i < head; i += kThreads) put(i, to_f32(src[i]));
+    const Pack *body = reinterpret_cast<const Pack *>(src + head);
+    const int packs = (n - head) / V;
+    for (int p0 = threadIdx.x; p0 < packs; p0 += 4 * kThreads) {
+        Pack v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (p0 + j * kThreads < packs) v[j] = body[p0 + j * kThreads];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (p0 + j * kThreads < packs)
+#pragma unroll
+                for (int i = 0; i < V; ++i) put(head + (p0 + j * kThreads) * V + i, to_f32(v[j].e[i]));
     }
-    return s;
+    for (int i = head + packs * V + threadIdx.x; i < n; i += kThreads) put(i, to_f32(src[i]));
+    return best;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a) {
-    __shared__ Sum part[kThreads / 32];
-    __shared__ uint64_t table[64];
-    __shared__ uint32_t highest[kThreads / 32];
-    const int64_t r = blockIdx.x;
-    const T *row = static_cast<const T *>(a.logits) + r * a.row_stride;
-    fill_weight_table(table);
-    uint32_t best = 0;
-    for (int i = threadIdx.x; i < a.vocab; i += kThreads) best = max(best, order_key(to_f32(row[i])));
-    best = __reduce_max_sync(0xffffffffu, best);
-    if ((threadIdx.x & 31) == 0) highest[threadIdx.x >> 5] = best;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) best = max(best, highest[w]);
-    const RowWeights rw(key_value(best), a.temperature ? a.temperature[r] : 1.f);
-    auto place = [&](int i) { return uint64_t(order_key(to_f32(row[i]))) << 18 | uint64_t(kMaxVocab - 1 - i); };
-    // of the prefix of the tokens whose place is `from` or more
-    auto prefix = [&](uint64_t from, uint64_t least) {
-        Sum s = {0, 0};
-        for (int i = threadIdx.x; i < a.vocab; i += kThreads)
-            if (place(i) >= from) {
-                const uint64_t w = rw.weight(to_f32(row[i]), table);
-                s.mass += w >= least ? w : 0;
-                ++s.count;
-            }
-        return block_sum(s, part);
-    };
-    // the last place whose prefix fulfils `enough`
-    auto find = [&](auto enough) {
-        uint64_t lo = 0, hi = uint64_t(1) << 50;  // enough at lo, not at hi
-        while (hi - lo > 1) {
-            const uint64_t mid = (lo + hi) / 2;
-            if (enough(prefix(mid, 0))) lo = mid;
-            else hi = mid;
+__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slice, int cluster) {
+    extern __shared__ __align__(16) uint8_t raw[];
+    Shared *sh = reinterpret_cast<Shared *>(raw);
+    float *x = reinterpret_cast<float *>(raw + sizeof(Shared));
+    const int tid = threadIdx.x, lane = tid & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t r = blockIdx.x / cluster;
+    Shared *lead = at_cta(sh, 0);
+    for (int i = tid; i < kBins; i += kThreads) sh->count[i] = 0;
+    fill_weight_table(sh->table);
+    if (tid == 0) {
+        sh->n_list = 0;
+        sh->total = 0;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    // ---- the row, and its largest logit
+    const int first = int(rank) * slice, n = max(0, min(slice, a.vocab - first));
+    const uint32_t mine = load_slice(static_cast<const T *>(a.logits) + r * a.row_stride + first, n, x);
+    {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, mine);
+        if (lane == 0) sh->part[tid >> 5] = m;
+        __syncthreads();
+        if (tid < cluster) {
+            uint32_t best = 0;
+            for (int w = 0; w < kWarps; ++w) best = max(best, uint32_t(sh->part[w]));
+            at_cta(sh, uint32_t(tid))->top[rank] = best;
         }
-        return lo;
-    };
-    if (best <= order_key(-INFINITY)) {
-        if (threadIdx.x == 0) {
+    }
+    cluster_sync();
+    uint32_t top = 0;
+    for (int c = 0; c < cluster; ++c) top = max(top, sh->top[c]);
+    if (top <= order_key(-INFINITY)) {  // nothing left
+        if (rank == 0 && tid == 0) {
             a.tokens[r] = -1;
             if (a.prob) a.prob[r] = 0.f;
         }
         return;
     }
-    uint64_t kept = prefix(0, 0).mass;
+    const RowWeights rw(key_value(top), a.temperature ? a.temperature[r] : 1.f);
     const int k = a.top_k ? a.top_k[r] : 0;
-    if (k > 0 && k < a.vocab) kept = prefix(find([&](Sum s) { return s.count >= uint64_t(k); }), 0).mass;
-    if (a.top_p && a.top_p[r] < 1.f) {
-        const uint64_t need = mass_needed(a.top_p[r], kept);
-        kept = prefix(find([&](Sum s) { return s.mass >= need; }), 0).mass;
+    const float p = a.top_p ? a.top_p[r] : 1.f;
+    const bool cut_k = k > 0 && k < a.vocab, cut_p = p < 1.f;
+
+    // ---- the head
+    const int want = cut_k ? k : kHead;
+    const bool try_head = !cut_k || k <= kMostHeadK;
+    if (try_head) {
+        if (a.vocab > kList) {  // (else all of it)
+            const int b = mine ? rw.bin(key_value(mine)) : -1;
+            if (b >= 0) atomicAdd(&lead->count[b], 1u);
+        }
+        unsigned long long sum = 0;
+        if (!cut_k)
+            for (int i = tid; i < n; i += kThreads) sum += rw.weight(x[i], sh->table);
+        cluster_sync();
+        if (rank == 0) {
+            int bound = kBins - 1;
+            if (a.vocab > kList) {
+                constexpr int per = (kBins + kThreads - 1) / kThreads;
+                uint32_t c[per], all = 0;
+#pragma unroll
+                for (int j = 0; j < per; ++j) {
+                    const int b = tid * per + j;
+                    c[j] = b < kBins ? sh->count[b] : 0;
+                    all += c[j];
+                }
+                if (tid == 0) sh->bound = kBins - 1;
+                unsigned long long before = block_scan(all, sh) - all;
+#pragma unroll
+                for (int j = 0; j < per; ++j) {
+                    if (before < uint32_t(want) && before + c[j] >= uint32_t(want)) sh->bound = tid * per + j;
+                    before += c[j];
+                }
+                __syncthreads();
+                bound = sh->bound;
+            }
+            if (tid < cluster) at_cta(sh, uint32_t(tid))->bound = bound;
+        }
+        if (!cut_k) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0 && sum) atomicAdd(&lead->total, sum);
+        }
+        cluster_sync();
+        const float limit = float(sh->bound + 1) * (1.f / kBinsPerUnit);
+        for (int i0 = 0; i0 < n; i0 += kThreads) {
+            const int i = i0 + tid;
+            const bool in = i < n && rw.above(x[i], limit);
+            const uint32_t m = __ballot_sync(0xffffffffu, in);
+            if (m) {
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(&lead->n_list, __popc(m));
+                at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+                if (in && at < kList) lead->list[at] = uint64_t(order_key(x[i])) << 32 | uint32_t(~(first + i));
+            }
+        }
+        cluster_sync();
     }
-    if (a.min_p) kept = min(kept, prefix(0, least_weight(a.min_p[r])).mass);
-    const uint64_t passed = drawn_mass(a.u[r], kept);
-    const uint64_t at = find([&](Sum s) { return s.mass > passed; });
-    if (threadIdx.x == 0) {
-        const int i = kMaxVocab - 1 - int(at & (kMaxVocab - 1));
-        a.tokens[r] = i;
-        if (a.prob) a.prob[r] = float(double(rw.weight(to_f32(row[i]), table)) / double(kept));
+
+    // (first CTA) Sorts the list's `count` elements; cumulative weights, from `before` on, in cum.
+    auto sort_and_sum = [&](int count, unsigned long long before) {
+        int size = 32;
+        while (size < count) size *= 2;
+        for (int i = count + tid; i < size; i += kThreads) sh->list[i] = 0;
+        sort_list(sh->list, size);
+        unsigned long long w[kList / kThreads], all = 0;
+#pragma unroll
+        for (int j = 0; j < kList / kThreads; ++j) {
+            const int i = tid * (kList / kThreads) + j;
+            w[j] = i < count ? rw.weight(key_value(uint32_t(sh->list[i] >> 32)), sh->table) : 0;
+            all += w[j];
+        }
+        unsigned long long c = before + block_scan(all, sh) - all;
+#pragma unroll
+        for (int j = 0; j < kList / kThreads; ++j) {
+            c += w[j];
+            sh->cum[tid * (kList / kThreads) + j] = c;
+        }
+        __syncthreads();
+    };
+    // (first CTA) The first of the `count` sorted elements whose cumulative weight is `mass` or more; -1: none.
+    auto first_of_mass = [&](unsigned long long mass, int count) {
+        if (tid == 0) sh->found = -1;
+        __syncthreads();
+        for (int i = tid; i < count; i += kThreads)
+            if (sh->cum[i] >= mass && (i == 0 || sh->cum[i - 1] < mass)) sh->found = i;
+        __syncthreads();
+        const int f = sh->found;
+        __syncthreads();
+        return f;
+    };
+    auto write = [&](uint32_t index, uint64_t weight, unsigned long long kept) {
+        a.tokens[r] = int64_t(index);
+        if (a.prob) a.prob[r] = float(double(weight) / double(kept));
+    };
+    const uint64_t least = a.min_p ? least_weight(a.min_p[r]) : 0;
+    const float u = a.u[r];
+    if (try_head && rank == 0) {
+        // ---- every answer from the head, if it holds them
+        const int count = int(min(sh->n_list, uint32_t(kList)));
+        bool ok = sh->n_list <= kList;
+        if (ok) {
+            sort_and_sum(count, 0);
+            const unsigned long long head = sh->cum[count - 1];
+            const bool whole = a.vocab <= kList || sh->bound == kBins - 1;  // no weight outside
+            unsigned long long kept = cut_k ? sh->cum[min(k, count) - 1] : sh->total;
+            if (cut_p) {
+                const unsigned long long need = mass_needed(p, kept);
+                ok = need <= head;
+                if (ok) kept = sh->cum[first_of_mass(need, count)];
+            }
+            if (ok && least) {
+                // the last that min_p keeps
+                if (tid == 0) sh->found = 0;
+                __syncthreads();
+                for (int i = tid; i < count; i += kThreads)
+                    if (rw.weight(key_value(uint32_t(sh->list[i] >> 32)), sh->table) >= least) atomicMax(&sh->found, i);
+                __syncthreads();
+                const unsigned long long heavy = sh->cum[sh->found];
+                ok = heavy >= kept || whole || sh->found + 1 < count;  // (lighter ones are in the head: all heavier are)
+                kept = min(kept, heavy);
+                __syncthreads();
+            }
+            const int f = ok ? first_of_mass(drawn_mass(u, kept) + 1, count) : -1;
+            ok = f >= 0;
+            if (ok && tid == 0)
+                write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
+        }
+        if (!cut_k || sh->n_list > kList)  // (the others wait for the word)
+            if (tid < cluster) at_cta(sh, uint32_t(tid))->cmd.op = ok ? OP_DONE : OP_HISTOGRAM;
     }
+    if (try_head) {
+        if (cut_k && lead->n_list <= kList) {
+            cluster_sync();  // (the first CTA's memory stays until all have read this)
+            return;
+        }
+        cluster_sync();
+        if (sh->cmd.op == OP_DONE) return;
+    }
+
+    // ---- the whole order
+    auto each = [&](auto f) {
+        for (int i = tid; i < n; i += kThreads) f(i, x[i]);
+    };
+    // Counts and weights of the bins slot(x) of all CTAs' elements (below 0: none), in the first CTA.
+    auto histogram = [&](auto slot) {
+        for (int i = tid; i < kBins; i += kThreads) {
+            sh->count[i] = 0;
+            sh->mass[i] = 0;
+        }
+        __syncthreads();
+        each([&](int, float v) {
+            const int b = slot(v);
+            if (b < 0) return;
+            atomicAdd(&sh->count[b], 1u);
+            atomicAdd(&sh->mass[b], static_cast<unsigned long long>(rw.weight(v, sh->table)));
+        });
+        cluster_sync();
+        for (int b = int(rank) + cluster * tid; b < kBins; b += cluster * kThreads) {
+            uint32_t c = 0;
+            unsigned long long m = 0;
+            for (int o = 0; o < cluster; ++o) {
+                c += at_cta(sh, uint32_t(o))->count[b];
+                m += at_cta(sh, uint32_t(o))->mass[b];
+            }
+            lead->count[b] = c;
+            lead->mass[b] = m;
+        }
+        cluster_sync();
+    };
+    // Has every CTA do `c` (first CTA: all its threads call it), up to the results' being there.
+    auto work = [&](const Command &c) {
+        if (c.op == OP_HISTOGRAM) {
+            histogram([&](float v) { return rw.bin(v); });
+        } else if (c.op == OP_REFINE) {
+            histogram([&](float v) {
+                const uint32_t key = order_key(v);
+                return key >= c.low && key <= c.high && rw.bin(v) == c.bin ? int((c.high - key) >> c.shift) : -1;
+            });
+        } else if (c.op == OP_SPAN) {  // the smallest and largest key of a bin
+            uint32_t lo = 0xffffffffu, hi = 0;
+            each([&](int, float v) {
+                if (rw.bin(v) == c.bin) {
+                    lo = min(lo, order_key(v));
+                    hi = max(hi, order_key(v));
+                }
+            });
+            lo = __reduce_min_sync(0xffffffffu, lo);
+            hi = __reduce_max_sync(0xffffffffu, hi);
+            if (lane == 0 && lo <= hi) {
+                atomicMin(&lead->low, lo);
+                atomicMax(&lead->high, hi);
+            }
+            cluster_sync();
+        } else if (c.op == OP_GATHER) {
+            each([&](int i, float v) {
+                const uint32_t key = order_key(v);
+                if (key >= c.low && key <= c.high && rw.bin(v) == c.bin) {
+                    const uint32_t at = atomicAdd(&lead->n_list, 1u);
+                    if (at < kList) lead->list[at] = uint64_t(key) << 32 | uint32_t(~(first + i));
+                }
+            });
+            cluster_sync();
+        } else if (c.op == OP_HEAVY) {  // the weight of what min_p keeps
+            unsigned long long sum = 0;
+            each([&](int, float v) {
+                const uint64_t w = rw.weight(v, sh->table);
+                sum += w >= least ? w : 0;
+            });
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0 && sum) atomicAdd(&lead->total, sum);
+            cluster_sync();
+        } else if (c.op == OP_TIE) {  // the CTA that holds the wanted one of the equal elements writes it
+            uint32_t same = 0;
+            const int per = (slice + kThreads - 1) / kThreads, i0 = tid * per, i1 = min(n, i0 + per);
+            for (int i = i0; i < i1; ++i) same += order_key(x[i]) == c.low;
+            const uint32_t upto = uint32_t(block_scan(same, sh));
+            if (tid == kThreads - 1)
+                for (int o = 0; o < cluster; ++o) at_cta(sh, uint32_t(o))->ties[rank] = upto;
+            cluster_sync();
+            uint32_t before = upto - same;
+            for (int o = 0; o < int(rank); ++o) before += sh->ties[o];
+            for (int i = i0; i < i1; ++i)
+                if (order_key(x[i]) == c.low && before++ == c.rank)
+                    write(uint32_t(first + i), rw.weight(x[i], sh->table), lead->kept);
+            cluster_sync();
+        }
+    };
+    if (rank != 0) {
+        for (;;) {
+            cluster_sync();
+            const Command c = sh->cmd;
+            if (c.op == OP_DONE) return;
+            work(c);
+        }
+    }
+    auto command = [&](const Command &c) {
+        if (tid < cluster) at_cta(sh, uint32_t(tid))->cmd = c;
+        cluster_sync();
+        if (c.op != OP_DONE) work(c);
+        __syncthreads();
+    };
+    bool fresh = false;  // the bins' histogram stands
+    struct Place {
+        unsigned long long before, mass;  // weight before the element, and up to it
+        uint32_t index;
+        bool tie;  // index: which of the elements `key`
+        uint32_t key;
+    };
+    // The first bin of the histogram in which the prefix reaches `target` (a count or a weight); what lies before it.
+    auto bin_of = [&](bool by_count, unsigned long long target, int bins, unsigned long long base_count,
+                      unsigned long long base_mass, unsigned long long *count, unsigned long long *mass) {
+        constexpr int per = (kBins + kThreads - 1) / kThreads;
+        unsigned long long c = 0, m = 0;
+        for (int j = 0; j < per; ++j) {
+            const int b = tid * per + j;
+            if (b < bins) {
+                c += sh->count[b];
+                m += sh->mass[b];
+            }
+        }
+        unsigned long long c0 = base_count + block_scan(c, sh) - c;
+        unsigned long long m0 = base_mass + block_scan(m, sh) - m;
+        if (tid == 0) sh->found = -1;
+        __syncthreads();
+        for (int j = 0; j < per; ++j) {
+            const int b = tid * per + j;
+            if (b >= bins) break;
+            const unsigned long long c1 = c0 + sh->count[b], m1 = m0 + sh->mass[b];
+            if (by_count ? c0 < target && c1 >= target : m0 < target && m1 >= target) {
+                sh->found = b;
+                sh->found_before = c0;
+                sh->found_mass = m0;
+            }
+            c0 = c1;
+            m0 = m1;
+        }
+        __syncthreads();
+        const int f = sh->found;
+        *count = sh->found_before;
+        *mass = sh->found_mass;
+        __syncthreads();
+        return f;
+    };
+    // The first element of the order whose prefix reaches `target`.
+    auto place_of = [&](bool by_count, unsigned long long target) {
+        if (!fresh) command(Command{OP_HISTOGRAM});
+        fresh = true;
+        unsigned long long count, mass;
+        const int bin = bin_of(by_count, target, kBins, 0, 0, &count, &mass);
+        uint32_t in = sh->count[bin], low = 0, high = 0xffffffffu;
+        if (in > kList) {
+            if (tid == 0) {
+                sh->low = 0xffffffffu;
+                sh->high = 0;
+            }
+            __syncthreads();
+            command(Command{OP_SPAN, bin});
+            low = sh->low;
+            high = sh->high;
+            while (in > kList && low < high) {
+                int shift = 0;
+                while ((high - low) >> shift >= kBins) ++shift;
+                command(Command{OP_REFINE, bin, shift, low, high});
+                fresh = false;
+                const int sub = bin_of(by_count, target, kBins, count, mass, &count, &mass);
+                in = sh->count[sub];
+                __syncthreads();
+                high -= uint32_t(sub) << shift;
+                low = max(low, high - ((1u << shift) - 1));
+            }
+        }
+        Place at = {};
+        if (in > kList) {  // equal elements
+            const uint64_t w = rw.weight(key_value(low), sh->table);
+            const unsigned long long which = by_count ? target - count - 1 : (target - mass - 1) / w;
+            at.tie = true;
+            at.key = low;
+            at.index = uint32_t(which);
+            at.before = mass + which * w;
+            at.mass = at.before + w;
+            return at;
+        }
+        if (tid == 0) sh->n_list = 0;
+        __syncthreads();
+        command(Command{OP_GATHER, bin, 0, low, high});
+        sort_and_sum(int(in), mass);
+        const int f = by_count ? int(target - count) - 1 : first_of_mass(target, int(in));
+        at.mass = sh->cum[f];
+        at.before = f ? sh->cum[f - 1] : mass;
+        at.index = ~uint32_t(sh->list[f]);
+        __syncthreads();
+        return at;
+    };
+    command(Command{OP_HISTOGRAM});
+    fresh = true;
+    unsigned long long kept;
+    uint32_t there;
+    {
+        unsigned long long c = 0, m = 0;
+        for (int b = tid; b < kBins; b += kThreads) {
+            c += sh->count[b];
+            m += sh->mass[b];
+        }
+        c = block_scan(c, sh);
+        if (tid == kThreads - 1) sh->found_before = c;
+        m = block_scan(m, sh);
+        if (tid == kThreads - 1) sh->found_mass = m;
+        __syncthreads();
+        there = uint32_t(sh->found_before);
+        kept = sh->found_mass;
+        __syncthreads();
+    }
+    if (cut_k && uint32_t(k) < there) kept = place_of(true, unsigned(k)).mass;
+    if (cut_p) kept = place_of(false, mass_needed(p, kept)).mass;
+    if (least > 1) {
+        if (tid == 0) sh->total = 0;
+        __syncthreads();
+        command(Command{OP_HEAVY});
+        kept = min(kept, sh->total);
+    }
+    const Place at = place_of(false, drawn_mass(u, kept) + 1);
+    if (at.tie) {
+        if (tid == 0) sh->kept = kept;
+        __syncthreads();
+        command(Command{OP_TIE, 0, 0, at.key, at.key, at.index});
+    } else if (tid == 0) {
+        write(at.index, at.mass - at.before, kept);
+    }
+    command(Command{OP_DONE});
+}
+
+template <typename T>
+cudaError_t launch(const SampleArgs &a, const LaunchCtx &ctx) {
+    // CTAs of a row: at least as many as its slices need to let two CTAs share an SM, more where rows are few
+    int cluster = 1;
+    while (cluster < kMaxCluster && int64_t(a.vocab) > int64_t(cluster) * 16384) cluster *= 2;
+    while (cluster < kMaxCluster && a.rows * cluster * 2 <= 2 * ctx.num_sms && a.vocab > cluster * 2048) cluster *= 2;
+    const int slice = ((a.vocab + cluster - 1) / cluster + 7) & ~7;
+    const size_t smem = sizeof(Shared) + size_t(slice) * 4;
+    auto kernel = sample_kernel<T>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(a.rows * cluster));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a, slice, cluster);
 }
 
 }  // namespace
 
 cudaError_t launch_sample(const SampleArgs &a, int dtype, const LaunchCtx &ctx) {
-    const dim3 grid(static_cast<unsigned>(a.rows));
     switch (dtype) {
-        case TQ2_F32: sample_kernel<float><<<grid, kThreads, 0, ctx.stream>>>(a); break;
-        case TQ2_F16: sample_kernel<__half><<<grid, kThreads, 0, ctx.stream>>>(a); break;
-        default: sample_kernel<__nv_bfloat16><<<grid, kThreads, 0, ctx.stream>>>(a); break;
+        case TQ2_F32: return launch<float>(a, ctx);
+        case TQ2_F16: return launch<__half>(a, ctx);
+        default: return launch<__nv_bfloat16>(a, ctx);
     }
-    return cudaGetLastError();
 }
 
 }  // namespace tq2

@@ -44,6 +44,19 @@ struct RowWeights {
         mode = !(temperature > 0.f) || s > 1e30 || top == INFINITY;
     }
 
+    // y rounded to f32: larger logits never have a larger one.  (Infinite or NaN: no weight.)
+    __device__ __forceinline__ float coarse(float l) const {
+        if (mode) return l == top ? 0.f : INFINITY;
+        return (top - l) * s_hi;
+    }
+    // Whether l's coarse y is below `limit` (at most kWeightBits + 1).
+    __device__ __forceinline__ bool above(float l, float limit) const { return coarse(l) < limit; }
+    // The bin of 1/64 that its coarse y lies in; -1: no weight.
+    __device__ __forceinline__ int bin(float l) const {
+        const float y = coarse(l);
+        return y < float(kWeightBits + 1) ? int(y * 64.f) : -1;
+    }
+
     __device__ __forceinline__ uint64_t weight(float l, const uint64_t *table) const {
         if (!(l > -INFINITY)) return 0;  // NaN too
         if (mode) return l == top ? uint64_t(1) << kWeightBits : 0;

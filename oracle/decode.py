@@ -47,17 +47,19 @@ def experts(gate_up, down, x, expert, weight, residual=None):
     f = down.shape[2]
     out = np.zeros(x.shape) if residual is None else residual.astype(np.float64).copy()
     hidden, sums = np.zeros(x.shape), np.abs(out)
-    for t in range(x.shape[0]):
-        for e, w in zip(expert[t], weight[t].astype(np.float64)):
-            if not 0 <= e < gate_up.shape[0]:
-                continue
-            gu, s = gate_up[e] @ x[t], np.abs(gate_up[e]) @ np.abs(x[t])
-            g, u = gu[:f], gu[f:]
-            h = silu(g) * u
-            out[t] += w * (down[e] @ h)
-            a = np.abs(w) * np.abs(down[e])
-            hidden[t] += a @ np.abs(h)
-            sums[t] += a @ (np.abs(h) + 1.1 * np.abs(u) * s[:f] + np.abs(silu(g)) * s[f:])  # |silu'| < 1.1
+    for e in range(gate_up.shape[0]):
+        t, j = np.nonzero(expert == e)
+        if not len(t):
+            continue
+        w = weight[t, j].astype(np.float64)[:, None]
+        gu, s = x[t] @ gate_up[e].T, np.abs(x[t]) @ np.abs(gate_up[e]).T
+        g, u = gu[:, :f], gu[:, f:]
+        h = silu(g) * u
+        np.add.at(out, t, w * (h @ down[e].T))
+        a = np.abs(down[e]).T
+        np.add.at(hidden, t, np.abs(w) * (np.abs(h) @ a))
+        # |silu'| < 1.1
+        np.add.at(sums, t, np.abs(w) * ((np.abs(h) + 1.1 * np.abs(u) * s[:, :f] + np.abs(silu(g)) * s[:, f:]) @ a))
     return out, hidden, sums
 
 
