@@ -9,7 +9,7 @@
 //  * The head: a bound that at least k (or some hundreds) of the threads' own maxima reach; the few elements above it go to
 //    the first CTA, which sorts them (bitonic, 1024 at most) and answers every question from their cumulative weights, if
 //    they reach that far: with a top-k always, without one where the distribution is as peaked as a model's usually is.
-//  * Else the whole order: a histogram of counts and weights over bins of 1/64 in log2 of the weight finds the bin that
+//  * Else the whole order: a histogram of counts and weights over bins of 1/32 in log2 of the weight finds the bin that
 //    an answer lies in; its elements (at most 1024, or split further by their bits) are sorted as the head is.
 //
 // Bound by latency for one row (cluster barriers and the sort), by the pass over the row for many.
@@ -25,7 +25,7 @@ namespace tq2 {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBinsPerUnit = 64, kBins = (kWeightBits + 1) * kBinsPerUnit;  // 2944
+constexpr int kBins = (kWeightBits + 1) * kBinsPerUnit;  // 1472
 constexpr int kList = 1024;
 constexpr int kHead = 512, kMostHeadK = 768;
 constexpr int kMaxCluster = 8;
@@ -39,7 +39,9 @@ struct Command {
 };
 
 struct Shared {
-    unsigned long long mass[kBins];
+    // Weights of bins.  While they are counted, in three pieces of 15 bits and more (a 64-bit atomic is a loop here, and
+    // 2^15 of a piece fit 32 bits); then, in the first CTA, the low and the high word of their sum over the CTAs.
+    uint32_t mass[3][kBins];
     unsigned long long list[kList];  // key << 32 | ~index
     unsigned long long cum[kList];
     uint64_t table[64];
@@ -92,12 +94,14 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, S
     return v + (warp ? sh->part[warp - 1] : 0);
 }
 
-// Descending bitonic sort of list[0, n) (n a power of two).
+// Descending bitonic sort of list[0, n) (n a power of two, at most 2 * kThreads): a thread a pair.  Steps of up to 32 stay
+// within the 64 elements of a warp's pairs, so that warps need not meet between them.
 __device__ void sort_list(unsigned long long *list, int n) {
+    const int i = threadIdx.x;
+    __syncthreads();
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step; step >>= 1) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < n / 2; i += kThreads) {
+            if (i < n / 2) {
                 const int a = 2 * i - (i & (step - 1)), b = a + step;
                 const unsigned long long x = list[a], y = list[b];
                 if ((x < y) == ((a & size) == 0)) {
@@ -105,46 +109,59 @@ __device__ void sort_list(unsigned long long *list, int n) {
                     list[b] = x;
                 }
             }
+            // (the next step is half of this one, or, after 1, of this size)
+            if (step > 32 || (step == 1 && size > 32))
+                __syncthreads();
+            else
+                __syncwarp();
         }
     __syncthreads();
 }
 
-// A row's elements of this CTA, from `first` on, in shared memory.
+// A pack of 16 bytes.
 template <typename T>
-__device__ __forceinline__ uint32_t load_slice(const T *src, int n, float *x) {
-    constexpr int V = 16 / sizeof(T);
-    struct alignas(16) Pack {
-        T e[V];
-    };
-    uint32_t best = 0;
-    auto put = [&](int i, float v) {
-        x[i] = v;
-        best = max(best, order_key(v));
-    };
-    const int head = min(n, int((16 - (reinterpret_cast<uintptr_t>(src) & 15)) % 16 / sizeof(T)));
-    for (int i = threadIdx.x; i < head; i += kThreads) put(i, to_f32(src[i]));
-    const Pack *body = reinterpret_cast<const Pack *>(src + head);
-    const int packs = (n - head) / V;
-    for (int p0 = threadIdx.x; p0 < packs; p0 += 4 * kThreads) {
-        Pack v[4];
+struct alignas(16) Pack {
+    static constexpr int N = 16 / sizeof(T);
+    T e[N];
+};
+// Elements src[0, n) to x[0, n), both at the same place in a pack.  Returns the thread's largest (-inf where it has none).
+template <typename T>
+__device__ __forceinline__ float load_slice(const T *src, int n, T *x) {
+    constexpr int V = Pack<T>::N, U = 4;
+    const int shift = int(reinterpret_cast<uintptr_t>(src) & 15) / int(sizeof(T));
+    const Pack<T> *from = reinterpret_cast<const Pack<T> *>(src - shift);
+    Pack<T> *to = reinterpret_cast<Pack<T> *>(x - shift);
+    const int packs = n > 0 ? (n + shift + V - 1) / V : 0;
+    const T nan = from_f32<T>(__uint_as_float(0x7fc00000u));
+    float best = -INFINITY;
+    for (int p0 = threadIdx.x; p0 < packs; p0 += U * kThreads) {
+        Pack<T> v[U];
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (p0 + j * kThreads < packs) v[j] = body[p0 + j * kThreads];
+        for (int j = 0; j < U; ++j) {
+            const int p = p0 + j * kThreads;
+            if (p > 0 && p < packs - 1)
+                v[j] = from[p];
+            else if (p < packs)  // (nothing outside the row is read)
+                for (int i = 0; i < V; ++i) {
+                    const int at = p * V + i - shift;
+                    v[j].e[i] = at >= 0 && at < n ? src[at] : nan;
+                }
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (p0 + j * kThreads < packs)
+        for (int j = 0; j < U; ++j)
+            if (p0 + j * kThreads < packs) {
+                to[p0 + j * kThreads] = v[j];
 #pragma unroll
-                for (int i = 0; i < V; ++i) put(head + (p0 + j * kThreads) * V + i, to_f32(v[j].e[i]));
+                for (int i = 0; i < V; ++i) best = fmaxf(best, to_f32(v[j].e[i]));
+            }
     }
-    for (int i = head + packs * V + threadIdx.x; i < n; i += kThreads) put(i, to_f32(src[i]));
     return best;
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slice, int cluster) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int slice, int cluster) {
     extern __shared__ __align__(16) uint8_t raw[];
     Shared *sh = reinterpret_cast<Shared *>(raw);
-    float *x = reinterpret_cast<float *>(raw + sizeof(Shared));
     const int tid = threadIdx.x, lane = tid & 31;
     const uint32_t rank = cluster_rank();
     const int64_t r = blockIdx.x / cluster;
@@ -160,9 +177,16 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
 
     // ---- the row, and its largest logit
     const int first = int(rank) * slice, n = max(0, min(slice, a.vocab - first));
-    const uint32_t mine = load_slice(static_cast<const T *>(a.logits) + r * a.row_stride + first, n, x);
+    const T *src = static_cast<const T *>(a.logits) + r * a.row_stride + first;
+    T *x = reinterpret_cast<T *>(raw + sizeof(Shared)) + int(reinterpret_cast<uintptr_t>(src) & 15) / int(sizeof(T));
+    const float mine = load_slice(src, n, x);
+    // f(index in the slice, value) for all elements, and some that are none (NaN); a warp's threads stay together
+    auto each = [&](auto f) {
+#pragma unroll 2
+        for (int i0 = 0; i0 < n; i0 += kThreads) f(i0 + tid, i0 + tid < n ? to_f32(x[i0 + tid]) : __uint_as_float(0x7fc00000u));
+    };
     {
-        const uint32_t m = __reduce_max_sync(0xffffffffu, mine);
+        const uint32_t m = __reduce_max_sync(0xffffffffu, order_key(mine));
         if (lane == 0) sh->part[tid >> 5] = m;
         __syncthreads();
         if (tid < cluster) {
@@ -191,12 +215,12 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
     const bool try_head = !cut_k || k <= kMostHeadK;
     if (try_head) {
         if (a.vocab > kList) {  // (else all of it)
-            const int b = mine ? rw.bin(key_value(mine)) : -1;
+            const int b = rw.bin(mine);
             if (b >= 0) atomicAdd(&lead->count[b], 1u);
         }
         unsigned long long sum = 0;
         if (!cut_k)
-            for (int i = tid; i < n; i += kThreads) sum += rw.weight(x[i], sh->table);
+            each([&](int, float v) { sum += rw.weight(v, sh->table); });
         cluster_sync();
         if (rank == 0) {
             int bound = kBins - 1;
@@ -228,17 +252,16 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
         }
         cluster_sync();
         const float limit = float(sh->bound + 1) * (1.f / kBinsPerUnit);
-        for (int i0 = 0; i0 < n; i0 += kThreads) {
-            const int i = i0 + tid;
-            const bool in = i < n && rw.above(x[i], limit);
+        each([&](int i, float v) {
+            const bool in = rw.above(v, limit);
             const uint32_t m = __ballot_sync(0xffffffffu, in);
             if (m) {
                 uint32_t at = 0;
                 if (lane == 0) at = atomicAdd(&lead->n_list, __popc(m));
                 at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
-                if (in && at < kList) lead->list[at] = uint64_t(order_key(x[i])) << 32 | uint32_t(~(first + i));
+                if (in && at < kList) lead->list[at] = uint64_t(order_key(v)) << 32 | uint32_t(~(first + i));
             }
-        }
+        });
         cluster_sync();
     }
 
@@ -324,35 +347,35 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
     }
 
     // ---- the whole order
-    auto each = [&](auto f) {
-        for (int i = tid; i < n; i += kThreads) f(i, x[i]);
-    };
     // Counts and weights of the bins slot(x) of all CTAs' elements (below 0: none), in the first CTA.
     auto histogram = [&](auto slot) {
-        for (int i = tid; i < kBins; i += kThreads) {
-            sh->count[i] = 0;
-            sh->mass[i] = 0;
-        }
+        for (int i = tid; i < kBins; i += kThreads) sh->count[i] = sh->mass[0][i] = sh->mass[1][i] = sh->mass[2][i] = 0;
         __syncthreads();
         each([&](int, float v) {
             const int b = slot(v);
             if (b < 0) return;
+            const uint64_t w = rw.weight(v, sh->table);
             atomicAdd(&sh->count[b], 1u);
-            atomicAdd(&sh->mass[b], static_cast<unsigned long long>(rw.weight(v, sh->table)));
+            atomicAdd(&sh->mass[0][b], uint32_t(w) & 0x7fffu);
+            atomicAdd(&sh->mass[1][b], uint32_t(w >> 15) & 0x7fffu);
+            atomicAdd(&sh->mass[2][b], uint32_t(w >> 30));
         });
         cluster_sync();
         for (int b = int(rank) + cluster * tid; b < kBins; b += cluster * kThreads) {
             uint32_t c = 0;
             unsigned long long m = 0;
             for (int o = 0; o < cluster; ++o) {
-                c += at_cta(sh, uint32_t(o))->count[b];
-                m += at_cta(sh, uint32_t(o))->mass[b];
+                const Shared *from = at_cta(sh, uint32_t(o));
+                c += from->count[b];
+                m += from->mass[0][b] + (uint64_t(from->mass[1][b]) << 15) + (uint64_t(from->mass[2][b]) << 30);
             }
             lead->count[b] = c;
-            lead->mass[b] = m;
+            lead->mass[0][b] = uint32_t(m);
+            lead->mass[1][b] = uint32_t(m >> 32);
         }
         cluster_sync();
     };
+    auto mass_of = [&](int b) { return sh->mass[0][b] | static_cast<unsigned long long>(sh->mass[1][b]) << 32; };
     // Has every CTA do `c` (first CTA: all its threads call it), up to the results' being there.
     auto work = [&](const Command &c) {
         if (c.op == OP_HISTOGRAM) {
@@ -399,7 +422,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
         } else if (c.op == OP_TIE) {  // the CTA that holds the wanted one of the equal elements writes it
             uint32_t same = 0;
             const int per = (slice + kThreads - 1) / kThreads, i0 = tid * per, i1 = min(n, i0 + per);
-            for (int i = i0; i < i1; ++i) same += order_key(x[i]) == c.low;
+            for (int i = i0; i < i1; ++i) same += order_key(to_f32(x[i])) == c.low;
             const uint32_t upto = uint32_t(block_scan(same, sh));
             if (tid == kThreads - 1)
                 for (int o = 0; o < cluster; ++o) at_cta(sh, uint32_t(o))->ties[rank] = upto;
@@ -407,8 +430,8 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
             uint32_t before = upto - same;
             for (int o = 0; o < int(rank); ++o) before += sh->ties[o];
             for (int i = i0; i < i1; ++i)
-                if (order_key(x[i]) == c.low && before++ == c.rank)
-                    write(uint32_t(first + i), rw.weight(x[i], sh->table), lead->kept);
+                if (order_key(to_f32(x[i])) == c.low && before++ == c.rank)
+                    write(uint32_t(first + i), rw.weight(to_f32(x[i]), sh->table), lead->kept);
             cluster_sync();
         }
     };
@@ -442,7 +465,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
             const int b = tid * per + j;
             if (b < bins) {
                 c += sh->count[b];
-                m += sh->mass[b];
+                m += mass_of(b);
             }
         }
         unsigned long long c0 = base_count + block_scan(c, sh) - c;
@@ -452,7 +475,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
         for (int j = 0; j < per; ++j) {
             const int b = tid * per + j;
             if (b >= bins) break;
-            const unsigned long long c1 = c0 + sh->count[b], m1 = m0 + sh->mass[b];
+            const unsigned long long c1 = c0 + sh->count[b], m1 = m0 + mass_of(b);
             if (by_count ? c0 < target && c1 >= target : m0 < target && m1 >= target) {
                 sh->found = b;
                 sh->found_before = c0;
@@ -526,7 +549,7 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a, int slic
         unsigned long long c = 0, m = 0;
         for (int b = tid; b < kBins; b += kThreads) {
             c += sh->count[b];
-            m += sh->mass[b];
+            m += mass_of(b);
         }
         c = block_scan(c, sh);
         if (tid == kThreads - 1) sh->found_before = c;
@@ -560,10 +583,10 @@ template <typename T>
 cudaError_t launch(const SampleArgs &a, const LaunchCtx &ctx) {
     // CTAs of a row: at least as many as its slices need to let two CTAs share an SM, more where rows are few
     int cluster = 1;
-    while (cluster < kMaxCluster && int64_t(a.vocab) > int64_t(cluster) * 16384) cluster *= 2;
+    while (cluster < kMaxCluster && int64_t(a.vocab) * int64_t(sizeof(T)) > int64_t(cluster) * 65536) cluster *= 2;
     while (cluster < kMaxCluster && a.rows * cluster * 2 <= 2 * ctx.num_sms && a.vocab > cluster * 2048) cluster *= 2;
     const int slice = ((a.vocab + cluster - 1) / cluster + 7) & ~7;
-    const size_t smem = sizeof(Shared) + size_t(slice) * 4;
+    const size_t smem = sizeof(Shared) + size_t(slice) * sizeof(T) + 32;
     auto kernel = sample_kernel<T>;
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     if (e != cudaSuccess) return e;

@@ -14,6 +14,7 @@ namespace tq2 {
 
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kWeightBits = 45;
+constexpr int kBinsPerUnit = 32;  // of log2 of the weight
 
 // 2^-(j/64) in units of 2^-62.
 __device__ __forceinline__ uint64_t weight_table_entry(int j) {
@@ -51,10 +52,10 @@ struct RowWeights {
     }
     // Whether l's coarse y is below `limit` (at most kWeightBits + 1).
     __device__ __forceinline__ bool above(float l, float limit) const { return coarse(l) < limit; }
-    // The bin of 1/64 that its coarse y lies in; -1: no weight.
+    // The bin that its coarse y lies in; -1: no weight.
     __device__ __forceinline__ int bin(float l) const {
         const float y = coarse(l);
-        return y < float(kWeightBits + 1) ? int(y * 64.f) : -1;
+        return y < float(kWeightBits + 1) ? int(y * float(kBinsPerUnit)) : -1;
     }
 
     __device__ __forceinline__ uint64_t weight(float l, const uint64_t *table) const {
