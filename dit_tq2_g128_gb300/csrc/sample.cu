@@ -6,13 +6,13 @@
 // weight.  Every question is then one of a count or a sum over a prefix, and no sort of a row is needed.
 //
 // A cluster of CTAs takes a row and keeps it in shared memory: it is read from memory once.
-//  * The head: a bound that at least k (or some hundreds) of the threads' own maxima reach; the few elements above it go to
-//    the first CTA, which sorts them (bitonic, 1024 at most) and answers every question from their cumulative weights, if
-//    they reach that far: with a top-k always, without one where the distribution is as peaked as a model's usually is.
-//  * Else the whole order: a histogram of counts and weights over bins of 1/32 in log2 of the weight finds the bin that
-//    an answer lies in; its elements (at most 1024, or split further by their bits) are sorted as the head is.
+//  * With a top-k (or a small vocabulary): a bound that at least k of the maxima of groups of threads reach; the few elements
+//    above it go to the first CTA, which sorts them (bitonic, 1024 at most) and answers every question from their cumulative
+//    weights.
+//  * Else: a histogram of counts and weights over bins of log2 of the weight finds the bin that an answer lies in; its
+//    elements (at most 1024, or split further by their bits) are sorted as above.
 //
-// Bound by latency for one row (cluster barriers and the sort), by the pass over the row for many.
+// Bound by latency for one row (cluster barriers and the sort), by the arithmetic of the weights and their atomics for many.
 #include <algorithm>
 #include <cstdint>
 
@@ -25,9 +25,9 @@ namespace tq2 {
 namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
-constexpr int kBins = (kWeightBits + 1) * kBinsPerUnit;  // 1472
+constexpr int kBins = 1472;  // of y: 32 or more in a unit (of log2 of the weight)
 constexpr int kList = 1024;
-constexpr int kHead = 512, kMostHeadK = 768;
+constexpr int kMostHeadK = 768;
 constexpr int kMaxCluster = 8;
 
 enum Op { OP_DONE, OP_HISTOGRAM, OP_REFINE, OP_SPAN, OP_GATHER, OP_HEAVY, OP_TIE };
@@ -49,8 +49,10 @@ struct Shared {
     unsigned long long total, found_mass, found_before, kept;
     uint32_t count[kBins];
     uint32_t top[kMaxCluster], ties[kMaxCluster];
+    float bottom[kMaxCluster];
     uint32_t n_list, low, high;
-    int found, bound;
+    int found;
+    float floor;  // the head: logits from here on
     Command cmd;
 };
 
@@ -124,16 +126,17 @@ struct alignas(16) Pack {
     static constexpr int N = 16 / sizeof(T);
     T e[N];
 };
-// Elements src[0, n) to x[0, n), both at the same place in a pack.  Returns the thread's largest (-inf where it has none).
+// Elements src[0, n) to x[0, n), both at the same place in a pack.  Returns the thread's largest (-inf where it has none);
+// lowest: its smallest above -inf (inf).
 template <typename T>
-__device__ __forceinline__ float load_slice(const T *src, int n, T *x) {
+__device__ __forceinline__ float load_slice(const T *src, int n, T *x, float *lowest) {
     constexpr int V = Pack<T>::N, U = 4;
     const int shift = int(reinterpret_cast<uintptr_t>(src) & 15) / int(sizeof(T));
     const Pack<T> *from = reinterpret_cast<const Pack<T> *>(src - shift);
     Pack<T> *to = reinterpret_cast<Pack<T> *>(x - shift);
     const int packs = n > 0 ? (n + shift + V - 1) / V : 0;
     const T nan = from_f32<T>(__uint_as_float(0x7fc00000u));
-    float best = -INFINITY;
+    float best = -INFINITY, least = INFINITY;
     for (int p0 = threadIdx.x; p0 < packs; p0 += U * kThreads) {
         Pack<T> v[U];
 #pragma unroll
@@ -152,9 +155,14 @@ __device__ __forceinline__ float load_slice(const T *src, int n, T *x) {
             if (p0 + j * kThreads < packs) {
                 to[p0 + j * kThreads] = v[j];
 #pragma unroll
-                for (int i = 0; i < V; ++i) best = fmaxf(best, to_f32(v[j].e[i]));
+                for (int i = 0; i < V; ++i) {
+                    const float f = to_f32(v[j].e[i]);
+                    best = fmaxf(best, f);
+                    least = f > -INFINITY ? fminf(least, f) : least;
+                }
             }
     }
+    *lowest = least;
     return best;
 }
 
@@ -170,7 +178,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     fill_weight_table(sh->table);
     if (tid == 0) {
         sh->n_list = 0;
-        sh->total = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -178,26 +185,33 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     // ---- the row, and its largest logit
     const int first = int(rank) * slice, n = max(0, min(slice, a.vocab - first));
     const T *src = static_cast<const T *>(a.logits) + r * a.row_stride + first;
-    T *x = reinterpret_cast<T *>(raw + sizeof(Shared)) + int(reinterpret_cast<uintptr_t>(src) & 15) / int(sizeof(T));
-    const float mine = load_slice(src, n, x);
-    // f(index in the slice, value) for all elements, and some that are none (NaN); a warp's threads stay together
-    auto each = [&](auto f) {
-#pragma unroll 2
-        for (int i0 = 0; i0 < n; i0 += kThreads) f(i0 + tid, i0 + tid < n ? to_f32(x[i0 + tid]) : __uint_as_float(0x7fc00000u));
-    };
+    constexpr int V = Pack<T>::N;
+    const int shift = int(reinterpret_cast<uintptr_t>(src) & 15) / int(sizeof(T));
+    T *x = reinterpret_cast<T *>(raw + sizeof(Shared)) + shift;
+    float lowest;
+    const float mine = load_slice(src, n, x, &lowest);
     {
         const uint32_t m = __reduce_max_sync(0xffffffffu, order_key(mine));
-        if (lane == 0) sh->part[tid >> 5] = m;
+        const uint32_t l = __reduce_min_sync(0xffffffffu, order_key(lowest));
+        if (lane == 0) sh->part[tid >> 5] = static_cast<unsigned long long>(l) << 32 | m;
         __syncthreads();
         if (tid < cluster) {
-            uint32_t best = 0;
-            for (int w = 0; w < kWarps; ++w) best = max(best, uint32_t(sh->part[w]));
+            uint32_t best = 0, least = 0xffffffffu;
+            for (int w = 0; w < kWarps; ++w) {
+                best = max(best, uint32_t(sh->part[w]));
+                least = min(least, uint32_t(sh->part[w] >> 32));
+            }
             at_cta(sh, uint32_t(tid))->top[rank] = best;
+            at_cta(sh, uint32_t(tid))->bottom[rank] = key_value(least);
         }
     }
     cluster_sync();
     uint32_t top = 0;
-    for (int c = 0; c < cluster; ++c) top = max(top, sh->top[c]);
+    float bottom = INFINITY;
+    for (int c = 0; c < cluster; ++c) {
+        top = max(top, sh->top[c]);
+        bottom = fminf(bottom, sh->bottom[c]);
+    }
     if (top <= order_key(-INFINITY)) {  // nothing left
         if (rank == 0 && tid == 0) {
             a.tokens[r] = -1;
@@ -206,65 +220,82 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         return;
     }
     const RowWeights rw(key_value(top), a.temperature ? a.temperature[r] : 1.f);
+    // The bin of a logit; -1: no weight.  The bins share out what y the row has.
+    const float most = fminf(rw.coarse(bottom), float(kWeightBits + 1));
+    const float per_unit = most > 0.f ? fminf(float(kBins - 1) / most, 1e6f) : 1.f;
+    auto bin_of_logit = [&](float l) {
+        const float y = rw.coarse(l);
+        return y < float(kWeightBits + 1) ? min(int(y * per_unit), kBins - 1) : -1;
+    };
     const int k = a.top_k ? a.top_k[r] : 0;
     const float p = a.top_p ? a.top_p[r] : 1.f;
     const bool cut_k = k > 0 && k < a.vocab, cut_p = p < 1.f;
 
     // ---- the head
-    const int want = cut_k ? k : kHead;
-    const bool try_head = !cut_k || k <= kMostHeadK;
+    const bool all = a.vocab <= kList, try_head = all || (cut_k && k <= kMostHeadK);
     if (try_head) {
-        if (a.vocab > kList) {  // (else all of it)
-            const int b = rw.bin(mine);
+        if (!all) {
+            // maxima of groups of four threads, or, for many, of each
+            float m = mine;
+            const bool fours = k <= kThreads / 8;
+            if (fours) {
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            }
+            const int b = !fours || (lane & 3) == 0 ? bin_of_logit(m) : -1;
             if (b >= 0) atomicAdd(&lead->count[b], 1u);
-        }
-        unsigned long long sum = 0;
-        if (!cut_k)
-            each([&](int, float v) { sum += rw.weight(v, sh->table); });
-        cluster_sync();
-        if (rank == 0) {
-            int bound = kBins - 1;
-            if (a.vocab > kList) {
+            cluster_sync();
+            if (rank == 0) {
                 constexpr int per = (kBins + kThreads - 1) / kThreads;
-                uint32_t c[per], all = 0;
+                uint32_t c[per], sum = 0;
 #pragma unroll
                 for (int j = 0; j < per; ++j) {
-                    const int b = tid * per + j;
-                    c[j] = b < kBins ? sh->count[b] : 0;
-                    all += c[j];
+                    c[j] = tid * per + j < kBins ? sh->count[tid * per + j] : 0;
+                    sum += c[j];
                 }
-                if (tid == 0) sh->bound = kBins - 1;
-                unsigned long long before = block_scan(all, sh) - all;
+                if (tid == 0) sh->found = kBins;
+                uint32_t before = uint32_t(block_scan(sum, sh)) - sum;
 #pragma unroll
                 for (int j = 0; j < per; ++j) {
-                    if (before < uint32_t(want) && before + c[j] >= uint32_t(want)) sh->bound = tid * per + j;
+                    if (before < uint32_t(k) && before + c[j] >= uint32_t(k)) sh->found = tid * per + j;
                     before += c[j];
                 }
                 __syncthreads();
-                bound = sh->bound;
+                // (none found: whatever has a weight)
+                if (tid < cluster)
+                    at_cta(sh, uint32_t(tid))->floor =
+                        rw.floor_of(sh->found == kBins ? float(kWeightBits + 1) : float(sh->found + 1) / per_unit);
             }
-            if (tid < cluster) at_cta(sh, uint32_t(tid))->bound = bound;
+            cluster_sync();
         }
-        if (!cut_k) {
+        const float floor = all ? -3.402823466e38f : sh->floor;
+        const Pack<T> *packed = reinterpret_cast<const Pack<T> *>(x - shift);
+        const int packs = n > 0 ? (n + shift + V - 1) / V : 0;
+        for (int q = tid; q < packs; q += kThreads) {
+            const Pack<T> v = packed[q];
+            bool any = false;
 #pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0 && sum) atomicAdd(&lead->total, sum);
-        }
-        cluster_sync();
-        const float limit = float(sh->bound + 1) * (1.f / kBinsPerUnit);
-        each([&](int i, float v) {
-            const bool in = rw.above(v, limit);
-            const uint32_t m = __ballot_sync(0xffffffffu, in);
-            if (m) {
-                uint32_t at = 0;
-                if (lane == 0) at = atomicAdd(&lead->n_list, __popc(m));
-                at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
-                if (in && at < kList) lead->list[at] = uint64_t(order_key(v)) << 32 | uint32_t(~(first + i));
+            for (int i = 0; i < V; ++i) any |= to_f32(v.e[i]) >= floor;
+            if (any) {
+#pragma unroll 1
+                for (int i = 0; i < V; ++i) {
+                    const int e = q * V + i - shift;
+                    const float f = e >= 0 && e < n ? to_f32(x[e]) : -INFINITY;
+                    if (f >= floor) {
+                        const uint32_t at = atomicAdd(&lead->n_list, 1u);
+                        if (at < kList) lead->list[at] = uint64_t(order_key(f)) << 32 | uint32_t(~(first + e));
+                    }
+                }
             }
-        });
+        }
         cluster_sync();
     }
 
+    // f(index in the slice, value) for all elements
+    auto each = [&](auto f) {
+#pragma unroll 2
+        for (int i = tid; i < n; i += kThreads) f(i, to_f32(x[i]));
+    };
     // (first CTA) Sorts the list's `count` elements; cumulative weights, from `before` on, in cum.
     auto sort_and_sum = [&](int count, unsigned long long before) {
         int size = 32;
@@ -303,47 +334,34 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     };
     const uint64_t least = a.min_p ? least_weight(a.min_p[r]) : 0;
     const float u = a.u[r];
-    if (try_head && rank == 0) {
-        // ---- every answer from the head, if it holds them
-        const int count = int(min(sh->n_list, uint32_t(kList)));
-        bool ok = sh->n_list <= kList;
-        if (ok) {
-            sort_and_sum(count, 0);
-            const unsigned long long head = sh->cum[count - 1];
-            const bool whole = a.vocab <= kList || sh->bound == kBins - 1;  // no weight outside
-            unsigned long long kept = cut_k ? sh->cum[min(k, count) - 1] : sh->total;
-            if (cut_p) {
-                const unsigned long long need = mass_needed(p, kept);
-                ok = need <= head;
-                if (ok) kept = sh->cum[first_of_mass(need, count)];
-            }
-            if (ok && least) {
-                // the last that min_p keeps
-                if (tid == 0) sh->found = 0;
-                __syncthreads();
-                for (int i = tid; i < count; i += kThreads)
-                    if (rw.weight(key_value(uint32_t(sh->list[i] >> 32)), sh->table) >= least) atomicMax(&sh->found, i);
-                __syncthreads();
-                const unsigned long long heavy = sh->cum[sh->found];
-                ok = heavy >= kept || whole || sh->found + 1 < count;  // (lighter ones are in the head: all heavier are)
-                kept = min(kept, heavy);
-                __syncthreads();
-            }
-            const int f = ok ? first_of_mass(drawn_mass(u, kept) + 1, count) : -1;
-            ok = f >= 0;
-            if (ok && tid == 0)
-                write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
-        }
-        if (!cut_k || sh->n_list > kList)  // (the others wait for the word)
-            if (tid < cluster) at_cta(sh, uint32_t(tid))->cmd.op = ok ? OP_DONE : OP_HISTOGRAM;
-    }
     if (try_head) {
-        if (cut_k && lead->n_list <= kList) {
+        if (rank != 0) {
+            const bool done = lead->n_list <= kList;
             cluster_sync();  // (the first CTA's memory stays until all have read this)
-            return;
+            if (done) return;
+        } else {
+            // every answer is in the head
+            const bool done = sh->n_list <= kList;
+            if (done) {
+                const int count = int(sh->n_list);
+                sort_and_sum(count, 0);
+                unsigned long long kept = sh->cum[(cut_k ? min(k, count) : count) - 1];
+                if (cut_p) kept = sh->cum[first_of_mass(mass_needed(p, kept), count)];
+                if (least > 1) {
+                    if (tid == 0) sh->found = 0;  // the last that min_p keeps
+                    __syncthreads();
+                    for (int i = tid; i < count; i += kThreads)
+                        if (sh->cum[i] - (i ? sh->cum[i - 1] : 0) >= least) atomicMax(&sh->found, i);
+                    __syncthreads();
+                    kept = min(kept, sh->cum[sh->found]);
+                    __syncthreads();
+                }
+                const int f = first_of_mass(drawn_mass(u, kept) + 1, count);
+                if (tid == 0) write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
+            }
+            cluster_sync();
+            if (done) return;
         }
-        cluster_sync();
-        if (sh->cmd.op == OP_DONE) return;
     }
 
     // ---- the whole order
@@ -379,16 +397,16 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     // Has every CTA do `c` (first CTA: all its threads call it), up to the results' being there.
     auto work = [&](const Command &c) {
         if (c.op == OP_HISTOGRAM) {
-            histogram([&](float v) { return rw.bin(v); });
+            histogram([&](float v) { return bin_of_logit(v); });
         } else if (c.op == OP_REFINE) {
             histogram([&](float v) {
                 const uint32_t key = order_key(v);
-                return key >= c.low && key <= c.high && rw.bin(v) == c.bin ? int((c.high - key) >> c.shift) : -1;
+                return key >= c.low && key <= c.high && bin_of_logit(v) == c.bin ? int((c.high - key) >> c.shift) : -1;
             });
         } else if (c.op == OP_SPAN) {  // the smallest and largest key of a bin
             uint32_t lo = 0xffffffffu, hi = 0;
             each([&](int, float v) {
-                if (rw.bin(v) == c.bin) {
+                if (bin_of_logit(v) == c.bin) {
                     lo = min(lo, order_key(v));
                     hi = max(hi, order_key(v));
                 }
@@ -403,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         } else if (c.op == OP_GATHER) {
             each([&](int i, float v) {
                 const uint32_t key = order_key(v);
-                if (key >= c.low && key <= c.high && rw.bin(v) == c.bin) {
+                if (key >= c.low && key <= c.high && bin_of_logit(v) == c.bin) {
                     const uint32_t at = atomicAdd(&lead->n_list, 1u);
                     if (at < kList) lead->list[at] = uint64_t(key) << 32 | uint32_t(~(first + i));
                 }

@@ -14,7 +14,6 @@ namespace tq2 {
 
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kWeightBits = 45;
-constexpr int kBinsPerUnit = 32;  // of log2 of the weight
 
 // 2^-(j/64) in units of 2^-62.
 __device__ __forceinline__ uint64_t weight_table_entry(int j) {
@@ -33,16 +32,19 @@ __device__ __forceinline__ void fill_weight_table(uint64_t *table) {
     if (threadIdx.x < 64) table[threadIdx.x] = weight_table_entry(threadIdx.x);
 }
 
+// A row's weights.  In f32 and integers throughout: 64-bit floating point, and conversions to and from it, run at a
+// thirtieth of their rate.
 struct RowWeights {
-    float top;       // the largest logit
+    float top;         // the largest logit
     float s_hi, s_lo;  // log2(e) / temperature
-    int mode;        // 0: as above, 1: the largest only (no temperature, or an infinite logit)
+    int mode;          // 0: as above, 1: the largest only (no temperature, or an infinite logit)
 
     __device__ __forceinline__ RowWeights(float largest, float temperature) : top(largest) {
-        const double s = 1.4426950408889634 / double(temperature);
-        s_hi = float(s);
-        s_lo = float(s - double(s_hi));
-        mode = !(temperature > 0.f) || s > 1e30 || top == INFINITY;
+        constexpr float e_hi = 1.44269502f, e_lo = 1.92596303e-8f;  // log2(e)
+        s_hi = e_hi / temperature;
+        s_lo = (fmaf(-s_hi, temperature, e_hi) + e_lo) / temperature;
+        mode = !(temperature > 0.f) || !(s_hi < 1e30f) || top == INFINITY;
+        if (!(temperature < INFINITY)) s_hi = s_lo = 0.f;
     }
 
     // y rounded to f32: larger logits never have a larger one.  (Infinite or NaN: no weight.)
@@ -50,12 +52,9 @@ struct RowWeights {
         if (mode) return l == top ? 0.f : INFINITY;
         return (top - l) * s_hi;
     }
-    // Whether l's coarse y is below `limit` (at most kWeightBits + 1).
-    __device__ __forceinline__ bool above(float l, float limit) const { return coarse(l) < limit; }
-    // The bin that its coarse y lies in; -1: no weight.
-    __device__ __forceinline__ int bin(float l) const {
-        const float y = coarse(l);
-        return y < float(kWeightBits + 1) ? int(y * float(kBinsPerUnit)) : -1;
+    // A logit below which no token has a coarse y below `limit`.
+    __device__ __forceinline__ float floor_of(float limit) const {
+        return mode ? top : fmaxf(top - limit * (1.f + 0x1p-18f) / s_hi, -3.402823466e38f);
     }
 
     __device__ __forceinline__ uint64_t weight(float l, const uint64_t *table) const {
@@ -67,33 +66,58 @@ struct RowWeights {
         const float p = hi * s_hi;
         if (!(p < float(kWeightBits + 1))) return 0;
         const float e = fmaf(hi, s_hi, -p) + fmaf(hi, s_lo, lo * s_hi);
-        const float n = rintf(p * 64.f);
-        const float t = fmaf(n, -1.f / 64.f, p) + e;
+        // n = 64 p to the nearest integer, in the low bits of its sum with 1.5 * 2^23
+        const float big = fmaf(p, 64.f, 12582912.f);
+        const int k = __float_as_int(big) - __float_as_int(12582912.f);
+        const float t = fmaf(big - 12582912.f, -1.f / 64.f, p) + e;
         // 2^-t - 1 = z + z^2/2 + z^3/6 + z^4/24, z = -t ln 2
         const float z = t * -0.69314718f;
         const float m = z * fmaf(z, fmaf(z, fmaf(z, 1.f / 24.f, 1.f / 6.f), 0.5f), 1.f);
-        const int k = int(n);
         const uint64_t base = table[k & 63];
-        const int64_t more = __float2ll_rn(__ull2float_rn(base) * m);
+        // base (2^-62) times m, below 2^-7: to 2^-38 in 32 bits
+        const float high = __uint2float_rn(uint32_t(base >> 32)) * m;
+        const int64_t more = int64_t(__float2int_rn(high * 256.f)) * (1 << 24);
         const int shift = 62 - kWeightBits + (k >> 6);
-        return (uint64_t(int64_t(base) + more) + (uint64_t(1) << (shift - 1))) >> shift;
+        return (base + uint64_t(more) + (uint64_t(1) << (shift - 1))) >> shift;
     }
 };
 
-// A prefix holds a share p of `total` when its mass is this or more (one token at least).
+// floor(f * total) for 0 <= f < 1, exactly; rest: whether anything was cut off.
+__device__ __forceinline__ uint64_t share(float f, uint64_t total, bool *rest) {
+    const uint32_t bits = __float_as_uint(f), e = bits >> 23;
+    const uint64_t m = e ? (bits & 0x7fffffu) | 0x800000u : bits & 0x7fffffu;  // f = m 2^-down
+    const uint32_t down = e ? 150 - e : 149;
+    const uint64_t lo = m * total, hi = __umul64hi(m, total);
+    *rest = f > 0.f;
+    if (down >= 128) return 0;
+    if (down >= 64) {
+        *rest = lo || (hi & ((uint64_t(1) << (down - 64)) - 1));
+        return hi >> (down - 64);
+    }
+    *rest = lo & ((uint64_t(1) << down) - 1);
+    return hi << (64 - down) | lo >> down;  // (f < 1: down is 24 or more)
+}
+// A prefix holds a share p < 1 of `total` when its mass is this or more (one token at least).
 __device__ __forceinline__ uint64_t mass_needed(float p, uint64_t total) {
-    const double need = ceil(double(p) * double(total));
-    return need >= 1.0 ? min(uint64_t(need), total) : 1;
+    if (!(p > 0.f)) return 1;
+    bool rest;
+    const uint64_t need = share(p, total, &rest) + rest;
+    return need ? need : 1;
 }
 // The smallest weight that min_p keeps; the likeliest token always stays.
 __device__ __forceinline__ uint64_t least_weight(float p) {
-    const double least = ceil(double(p) * double(uint64_t(1) << kWeightBits));
-    return least >= 1.0 ? min(uint64_t(least), uint64_t(1) << kWeightBits) : 0;
+    if (!(p > 0.f)) return 0;
+    if (p >= 1.f) return uint64_t(1) << kWeightBits;
+    bool rest;
+    const uint64_t least = share(p, uint64_t(1) << kWeightBits, &rest);
+    return least + rest;
 }
 // The mass that the drawn token's prefix passes: u of `total`, below it.
 __device__ __forceinline__ uint64_t drawn_mass(float u, uint64_t total) {
-    const double d = floor(double(u) * double(total));
-    return d >= 1.0 ? min(uint64_t(d), total - 1) : 0;
+    if (!(u > 0.f)) return 0;
+    if (u >= 1.f) return total - 1;
+    bool rest;
+    return share(u, total, &rest);
 }
 
 }  // namespace tq2
