@@ -6,11 +6,11 @@
 // weight.  Every question is then one of a count or a sum over a prefix, and no sort of a row is needed.
 //
 // A cluster of CTAs takes a row and keeps it in shared memory: it is read from memory once.
-//  * With a top-k (or a small vocabulary): a bound that at least k of the maxima of groups of threads reach; the few elements
-//    above it go to the first CTA, which sorts them (bitonic, 1024 at most) and answers every question from their cumulative
-//    weights.
+//  * The head: a bound that at least k (or a few hundred) of the maxima of groups of threads reach; the few elements above it go
+//    to the first CTA, which sorts them and answers every question from their cumulative weights, if they reach that far:
+//    with a top-k always, without one where the distribution is as peaked as a model's usually is.
 //  * Else: a histogram of counts and weights over bins of log2 of the weight finds the bin that an answer lies in; its
-//    elements (at most 1024, or split further by their bits) are sorted as above.
+//    elements (at most 1024, or split further by their bits) are sorted as the head is.
 //
 // Bound by latency for one row (cluster barriers and the sort), by the arithmetic of the weights and their atomics for many.
 #include <algorithm>
@@ -27,7 +27,8 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1472;  // of y: 32 or more in a unit (of log2 of the weight)
 constexpr int kList = 1024;
-constexpr int kMostHeadK = 768;
+constexpr int kHead = 256, kMostHeadK = 768, kRankSort = 256;
+constexpr int kEach = kList / kThreads;  // list elements of a thread
 constexpr int kMaxCluster = 8;
 
 enum Op { OP_DONE, OP_HISTOGRAM, OP_REFINE, OP_SPAN, OP_GATHER, OP_HEAVY, OP_TIE };
@@ -46,11 +47,11 @@ struct Shared {
     unsigned long long cum[kList];
     uint64_t table[64];
     unsigned long long part[kWarps];
-    unsigned long long total, found_mass, found_before, kept;
+    unsigned long long sum, total, found_mass, found_before, kept;
     uint32_t count[kBins];
     uint32_t top[kMaxCluster], ties[kMaxCluster];
     float bottom[kMaxCluster];
-    uint32_t n_list, low, high;
+    uint32_t n_list, n_mine, base, low, high;
     int found;
     float floor;  // the head: logits from here on
     Command cmd;
@@ -96,10 +97,28 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, S
     return v + (warp ? sh->part[warp - 1] : 0);
 }
 
-// Descending bitonic sort of list[0, n) (n a power of two, at most 2 * kThreads): a thread a pair.  Steps of up to 32 stay
-// within the 64 elements of a warp's pairs, so that warps need not meet between them.
-__device__ void sort_list(unsigned long long *list, int n) {
+// Sorts list[0, count) descending (all different).  Short ones by counting who is larger (a list of 100: 700 cycles, not
+// the 5000 of the network's 28 steps); others by a bitonic network, a thread a pair, whose steps of up to 32 stay within the
+// 64 elements of a warp's pairs, so that warps need not meet between them.
+__device__ void sort_list(unsigned long long *list, unsigned long long *spare, int count) {
     const int i = threadIdx.x;
+    if (count <= kRankSort) {
+        __syncthreads();
+        if (i < count) {
+            const unsigned long long mine = list[i];
+            int larger = 0;
+#pragma unroll 4
+            for (int j = 0; j < count; ++j) larger += list[j] > mine;
+            spare[larger] = mine;
+        }
+        __syncthreads();
+        if (i < count) list[i] = spare[i];
+        __syncthreads();
+        return;
+    }
+    int n = 32;
+    while (n < count) n *= 2;
+    for (int j = count + i; j < n; j += kThreads) list[j] = 0;
     __syncthreads();
     for (int size = 2; size <= n; size <<= 1)
         for (int step = size >> 1; step; step >>= 1) {
@@ -175,15 +194,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     const int64_t r = blockIdx.x / cluster;
     Shared *lead = at_cta(sh, 0);
     for (int i = tid; i < kBins; i += kThreads) sh->count[i] = 0;
-    fill_weight_table(sh->table);
+    if (tid < 64) sh->table[tid] = weight_table.e[tid];
     if (tid == 0) {
         sh->n_list = 0;
+        sh->n_mine = 0;
+        sh->sum = 0;
+        sh->total = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     // ---- the row, and its largest logit
     const int first = int(rank) * slice, n = max(0, min(slice, a.vocab - first));
+    const float temperature = a.temperature ? a.temperature[r] : 1.f, p = a.top_p ? a.top_p[r] : 1.f, u = a.u[r];
+    const int k = a.top_k ? a.top_k[r] : 0;
+    const uint64_t least = a.min_p ? least_weight(a.min_p[r]) : 0;
     const T *src = static_cast<const T *>(a.logits) + r * a.row_stride + first;
     constexpr int V = Pack<T>::N;
     const int shift = int(reinterpret_cast<uintptr_t>(src) & 15) / int(sizeof(T));
@@ -219,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         }
         return;
     }
-    const RowWeights rw(key_value(top), a.temperature ? a.temperature[r] : 1.f);
+    const RowWeights rw(key_value(top), temperature);
     // The bin of a logit; -1: no weight.  The bins share out what y the row has.
     const float most = fminf(rw.coarse(bottom), float(kWeightBits + 1));
     const float per_unit = most > 0.f ? fminf(float(kBins - 1) / most, 1e6f) : 1.f;
@@ -227,17 +252,44 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         const float y = rw.coarse(l);
         return y < float(kWeightBits + 1) ? min(int(y * per_unit), kBins - 1) : -1;
     };
-    const int k = a.top_k ? a.top_k[r] : 0;
-    const float p = a.top_p ? a.top_p[r] : 1.f;
     const bool cut_k = k > 0 && k < a.vocab, cut_p = p < 1.f;
 
+    // f(index in the slice, value) for all elements
+    auto each = [&](auto f) {
+#pragma unroll 2
+        for (int i = tid; i < n; i += kThreads) f(i, to_f32(x[i]));
+    };
+    // Elements on their way to the first CTA's list: in this CTA first, then all at once.
+    auto take = [&](int i, float v) {
+        const uint32_t at = atomicAdd(&sh->n_mine, 1u);
+        if (at < kList) sh->cum[at] = uint64_t(order_key(v)) << 32 | uint32_t(~(first + i));
+    };
+    auto hand_over = [&] {
+        __syncthreads();
+        const uint32_t count = sh->n_mine;
+        if (tid == 0 && count) sh->base = atomicAdd(&lead->n_list, count);
+        __syncthreads();
+        for (uint32_t i = tid; i < min(count, uint32_t(kList)) && sh->base + i < kList; i += kThreads)
+            lead->list[sh->base + i] = sh->cum[i];
+        if (tid == 0) sh->n_mine = 0;
+        cluster_sync();
+    };
+
     // ---- the head
-    const bool all = a.vocab <= kList, try_head = all || (cut_k && k <= kMostHeadK);
+    const bool all = a.vocab <= kList, try_head = all || !cut_k || k <= kMostHeadK;
     if (try_head) {
+        if (!cut_k) {  // the row's weight
+            unsigned long long sum = 0;
+            each([&](int, float v) { sum += rw.weight(v, sh->table); });
+#pragma unroll
+            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane == 0 && sum) atomicAdd(&sh->sum, sum);
+        }
         if (!all) {
             // maxima of groups of four threads, or, for many, of each
+            const int want = cut_k ? k : kHead;
             float m = mine;
-            const bool fours = k <= kThreads / 8;
+            const bool fours = want <= kThreads / 8 || (want <= kHead && cluster == kMaxCluster);
             if (fours) {
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -257,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
                 uint32_t before = uint32_t(block_scan(sum, sh)) - sum;
 #pragma unroll
                 for (int j = 0; j < per; ++j) {
-                    if (before < uint32_t(k) && before + c[j] >= uint32_t(k)) sh->found = tid * per + j;
+                    if (before < uint32_t(want) && before + c[j] >= uint32_t(want)) sh->found = tid * per + j;
                     before += c[j];
                 }
                 __syncthreads();
@@ -267,101 +319,94 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
                         rw.floor_of(sh->found == kBins ? float(kWeightBits + 1) : float(sh->found + 1) / per_unit);
             }
             cluster_sync();
+        } else if (!cut_k) {
+            __syncthreads();
         }
+        if (!cut_k && tid == 0) atomicAdd(&lead->total, sh->sum);
         const float floor = all ? -3.402823466e38f : sh->floor;
         const Pack<T> *packed = reinterpret_cast<const Pack<T> *>(x - shift);
         const int packs = n > 0 ? (n + shift + V - 1) / V : 0;
-        for (int q = tid; q < packs; q += kThreads) {
-            const Pack<T> v = packed[q];
-            bool any = false;
+        if (mine >= floor)  // (the packs that this thread brought)
+            for (int q = tid; q < packs; q += kThreads) {
+                const Pack<T> v = packed[q];
+                bool any = false;
 #pragma unroll
-            for (int i = 0; i < V; ++i) any |= to_f32(v.e[i]) >= floor;
-            if (any) {
+                for (int i = 0; i < V; ++i) any |= to_f32(v.e[i]) >= floor;
+                if (any) {
 #pragma unroll 1
-                for (int i = 0; i < V; ++i) {
-                    const int e = q * V + i - shift;
-                    const float f = e >= 0 && e < n ? to_f32(x[e]) : -INFINITY;
-                    if (f >= floor) {
-                        const uint32_t at = atomicAdd(&lead->n_list, 1u);
-                        if (at < kList) lead->list[at] = uint64_t(order_key(f)) << 32 | uint32_t(~(first + e));
+                    for (int i = 0; i < V; ++i) {
+                        const int e = q * V + i - shift;
+                        const float f = e >= 0 && e < n ? to_f32(x[e]) : -INFINITY;
+                        if (f >= floor) take(e, f);
                     }
                 }
             }
-        }
-        cluster_sync();
+        hand_over();
     }
 
-    // f(index in the slice, value) for all elements
-    auto each = [&](auto f) {
-#pragma unroll 2
-        for (int i = tid; i < n; i += kThreads) f(i, to_f32(x[i]));
-    };
-    // (first CTA) Sorts the list's `count` elements; cumulative weights, from `before` on, in cum.
+    // (first CTA) Sorts the list's `count` elements: this thread's weights and their cumulative ones, from `before` on (in
+    // sh->cum too).
+    unsigned long long w[kEach], cum[kEach];
     auto sort_and_sum = [&](int count, unsigned long long before) {
-        int size = 32;
-        while (size < count) size *= 2;
-        for (int i = count + tid; i < size; i += kThreads) sh->list[i] = 0;
-        sort_list(sh->list, size);
-        unsigned long long w[kList / kThreads], all = 0;
+        sort_list(sh->list, sh->cum, count);
+        unsigned long long sum = 0;
 #pragma unroll
-        for (int j = 0; j < kList / kThreads; ++j) {
-            const int i = tid * (kList / kThreads) + j;
+        for (int j = 0; j < kEach; ++j) {
+            const int i = tid * kEach + j;
             w[j] = i < count ? rw.weight(key_value(uint32_t(sh->list[i] >> 32)), sh->table) : 0;
-            all += w[j];
+            sum += w[j];
         }
-        unsigned long long c = before + block_scan(all, sh) - all;
+        unsigned long long c = before + block_scan(sum, sh) - sum;
 #pragma unroll
-        for (int j = 0; j < kList / kThreads; ++j) {
+        for (int j = 0; j < kEach; ++j) {
             c += w[j];
-            sh->cum[tid * (kList / kThreads) + j] = c;
+            cum[j] = c;
+            sh->cum[tid * kEach + j] = c;
         }
         __syncthreads();
     };
-    // (first CTA) The first of the `count` sorted elements whose cumulative weight is `mass` or more; -1: none.
+    // (first CTA) The first of the `count` sorted elements whose cumulative weight is `mass` or more; `count`: none.
     auto first_of_mass = [&](unsigned long long mass, int count) {
-        if (tid == 0) sh->found = -1;
-        __syncthreads();
-        for (int i = tid; i < count; i += kThreads)
-            if (sh->cum[i] >= mass && (i == 0 || sh->cum[i - 1] < mass)) sh->found = i;
-        __syncthreads();
-        const int f = sh->found;
-        __syncthreads();
-        return f;
+        int below = 0;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) below += __syncthreads_count(tid * kEach + j < count && cum[j] < mass);
+        return below;
     };
     auto write = [&](uint32_t index, uint64_t weight, unsigned long long kept) {
         a.tokens[r] = int64_t(index);
         if (a.prob) a.prob[r] = float(double(weight) / double(kept));
     };
-    const uint64_t least = a.min_p ? least_weight(a.min_p[r]) : 0;
-    const float u = a.u[r];
     if (try_head) {
-        if (rank != 0) {
-            const bool done = lead->n_list <= kList;
-            cluster_sync();  // (the first CTA's memory stays until all have read this)
-            if (done) return;
-        } else {
-            // every answer is in the head
-            const bool done = sh->n_list <= kList;
-            if (done) {
-                const int count = int(sh->n_list);
+        if (rank == 0) {
+            const int count = int(sh->n_list);
+            bool ok = count <= kList;
+            if (ok) {
                 sort_and_sum(count, 0);
-                unsigned long long kept = sh->cum[(cut_k ? min(k, count) : count) - 1];
-                if (cut_p) kept = sh->cum[first_of_mass(mass_needed(p, kept), count)];
-                if (least > 1) {
-                    if (tid == 0) sh->found = 0;  // the last that min_p keeps
-                    __syncthreads();
-                    for (int i = tid; i < count; i += kThreads)
-                        if (sh->cum[i] - (i ? sh->cum[i - 1] : 0) >= least) atomicMax(&sh->found, i);
-                    __syncthreads();
-                    kept = min(kept, sh->cum[sh->found]);
-                    __syncthreads();
+                const unsigned long long head = sh->cum[count - 1];
+                unsigned long long kept = cut_k ? sh->cum[min(k, count) - 1] : sh->total;
+                if (cut_p) {
+                    const unsigned long long need = mass_needed(p, kept);
+                    ok = need <= head;
+                    if (ok) kept = sh->cum[first_of_mass(need, count)];
                 }
-                const int f = first_of_mass(drawn_mass(u, kept) + 1, count);
-                if (tid == 0) write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
+                if (ok && least > 1) {
+                    int heavy = 0;  // those that min_p keeps
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) heavy += __syncthreads_count(w[j] >= least);
+                    ok = heavy < count || kept <= head;  // (else there may be more outside)
+                    kept = min(kept, sh->cum[heavy - 1]);
+                }
+                const unsigned long long passed = drawn_mass(u, kept);
+                ok = ok && passed < head;
+                if (ok) {
+                    const int f = first_of_mass(passed + 1, count);
+                    if (tid == 0) write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
+                }
             }
-            cluster_sync();
-            if (done) return;
+            if (tid < cluster) at_cta(sh, uint32_t(tid))->cmd.op = ok ? OP_DONE : OP_HISTOGRAM;
         }
+        cluster_sync();
+        if (sh->cmd.op == OP_DONE) return;
     }
 
     // ---- the whole order
@@ -421,12 +466,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         } else if (c.op == OP_GATHER) {
             each([&](int i, float v) {
                 const uint32_t key = order_key(v);
-                if (key >= c.low && key <= c.high && bin_of_logit(v) == c.bin) {
-                    const uint32_t at = atomicAdd(&lead->n_list, 1u);
-                    if (at < kList) lead->list[at] = uint64_t(key) << 32 | uint32_t(~(first + i));
-                }
+                if (key >= c.low && key <= c.high && bin_of_logit(v) == c.bin) take(i, v);
             });
-            cluster_sync();
+            hand_over();
         } else if (c.op == OP_HEAVY) {  // the weight of what min_p keeps
             unsigned long long sum = 0;
             each([&](int, float v) {

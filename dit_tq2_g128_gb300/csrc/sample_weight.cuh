@@ -15,22 +15,24 @@ namespace tq2 {
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kWeightBits = 45;
 
-// 2^-(j/64) in units of 2^-62.
-__device__ __forceinline__ uint64_t weight_table_entry(int j) {
+// 2^-(j/64) in units of 2^-62, to 53 bits.
+struct WeightTable {
+    uint64_t e[64];
+};
+constexpr WeightTable make_weight_table() {
     // 2^-(1/64), 2^-(1/32), .. 2^-(1/2)
     constexpr double root[6] = {0.98922801319397548, 0.97857206208770009, 0.95760328069857365,
                                 0.91700404320467122, 0.84089641525371454, 0.70710678118654752};
-    double v = 1.0;
-#pragma unroll
-    for (int b = 0; b < 6; ++b)
-        if (j >> b & 1) v *= root[b];
-    return uint64_t(v * 4611686018427387904.0);
+    WeightTable t = {};
+    for (int j = 0; j < 64; ++j) {
+        double v = 1.0;
+        for (int b = 0; b < 6; ++b)
+            if (j >> b & 1) v *= root[b];
+        t.e[j] = uint64_t(v * 4611686018427387904.0);
+    }
+    return t;
 }
-
-// Fills table[64] (shared memory); the caller synchronises the block.
-__device__ __forceinline__ void fill_weight_table(uint64_t *table) {
-    if (threadIdx.x < 64) table[threadIdx.x] = weight_table_entry(threadIdx.x);
-}
+__constant__ WeightTable weight_table = make_weight_table();
 
 // A row's weights.  In f32 and integers throughout: 64-bit floating point, and conversions to and from it, run at a
 // thirtieth of their rate.
