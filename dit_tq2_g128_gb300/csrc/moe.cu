@@ -14,7 +14,22 @@
 namespace tq2 {
 namespace {
 
-constexpr int kPlanThreads = 1024, kPlanWarps = 32, kPlanAhead = 8;
+constexpr int kPlanThreads = 1024, kPlanMaxCluster = 8, kPlanPairs = 4096;  // pairs of a CTA before there are more of them
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+template <typename P>
+__device__ __forceinline__ const P *at_cta(const P *p, uint32_t rank) {
+    uint64_t r;
+    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
+    return reinterpret_cast<const P *>(r);
+}
 
 // Exclusive sum over the block's threads of v; total: the sum.
 __device__ __forceinline__ int block_scan(int v, int *part, int *total) {
@@ -42,151 +57,169 @@ __device__ __forceinline__ int block_scan(int v, int *part, int *total) {
     return s - v + (warp ? part[warp - 1] : 0);
 }
 
-// The pairs sorted by expert (in their order within one), and the tiles.  One block: warp w counts and places the pairs of
-// the w-th part, 32 at a time.
+// The pairs sorted by expert, and the tiles.  One cluster, a part of the pairs a CTA.  (Counters place the pairs of one expert
+// in whatever order they come; no result depends on it.)
 __global__ void __launch_bounds__(kPlanThreads)
-moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int experts, int tile_rows, unsigned int *status) {
-    extern __shared__ int cnt[];  // [kPlanWarps][experts]
-    __shared__ int part[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int i = threadIdx.x; i < kPlanWarps * experts; i += kPlanThreads) cnt[i] = 0;
+moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int experts, int tile_rows, int cluster,
+                unsigned int *status) {
+    __shared__ int count[1024], next[1024], part[32];
+    const int tid = threadIdx.x, rank = int(cluster_rank());
+    count[tid] = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     __syncthreads();
-    const int per = ((pairs + kPlanWarps - 1) / kPlanWarps + 31) / 32 * 32;
-    const int first = min(pairs, warp * per), last = min(pairs, first + per);
-    int *mine = cnt + warp * experts;
+    const int per = (pairs + cluster - 1) / cluster, first = rank * per, last = min(pairs, first + per);
     bool bad = false;
-    // 8 x 32 of them in flight, and kept where they are all there are
-    int id[kPlanAhead];
-    auto load = [&](int p0) {
+    constexpr int U = 4;
+    for (int p0 = first + tid; p0 < last; p0 += U * kPlanThreads) {
+        int e[U];
 #pragma unroll
-        for (int i = 0; i < kPlanAhead; ++i) {
-            const int p = p0 + 32 * i + lane;
-            id[i] = p < last ? expert[p] : -1;
-            if (id[i] < 0 || id[i] >= experts) {
-                bad |= id[i] != -1;
-                id[i] = -1;
-            }
-        }
-    };
-    for (int p0 = first; p0 < last; p0 += 32 * kPlanAhead) {
-        load(p0);
+        for (int i = 0; i < U; ++i) e[i] = p0 + i * kPlanThreads < last ? expert[p0 + i * kPlanThreads] : -1;
 #pragma unroll
-        for (int i = 0; i < kPlanAhead; ++i) {
-            if (p0 + 32 * i >= last) break;
-            const uint32_t same = __match_any_sync(0xffffffffu, id[i]);
-            if (id[i] >= 0 && lane == __ffs(same) - 1) mine[id[i]] += __popc(same);
-            __syncwarp();
+        for (int i = 0; i < U; ++i) {
+            if (e[i] >= 0 && e[i] < experts)
+                atomicAdd(&count[e[i]], 1);
+            else
+                bad |= e[i] != -1;
         }
     }
     report_bad(bad, status);
-    __syncthreads();
-    const int e = threadIdx.x;
-    int total = 0;
-    if (e < experts)
-        for (int w = 0; w < kPlanWarps; ++w) {
-            const int c = cnt[w * experts + e];
-            cnt[w * experts + e] = total;
-            total += c;
+    cluster_sync();
+    // thread e: expert e's rows, those of the CTAs before this one first
+    int total = 0, before = 0;
+    if (tid < experts)
+        for (int c = 0; c < cluster; ++c) {
+            const int n = at_cta(count, uint32_t(c))[tid];
+            before += c < rank ? n : 0;
+            total += n;
         }
     int rows, tiles;
     const int at = block_scan(total, part, &rows);
     const int n_tiles = (total + tile_rows - 1) / tile_rows;
     const int tile0 = block_scan(n_tiles, part, &tiles);
-    if (e < experts)
-        for (int w = 0; w < kPlanWarps; ++w) cnt[w * experts + e] += at;
-    for (int i = 0; i < n_tiles; ++i)
-        plan.tiles[tile0 + i] = MoeTile{e, at + i * tile_rows, min(tile_rows, total - i * tile_rows), 0};
-    if (threadIdx.x == 0) {
-        plan.counts[0] = tiles;
-        plan.counts[1] = rows;
+    next[tid] = at + before;
+    if (rank == 0) {
+        for (int i = 0; i < n_tiles; ++i)
+            plan.tiles[tile0 + i] = MoeTile{tid, at + i * tile_rows, min(tile_rows, total - i * tile_rows), 0};
+        if (tid < experts) {
+            plan.expert_rows[tid] = total;
+            plan.bound[tid] = 0;
+        }
+        if (tid == 0) *plan.tile_count = tiles;
     }
     __syncthreads();
-    for (int p0 = first; p0 < last; p0 += 32 * kPlanAhead) {
-        if (last - first > 32 * kPlanAhead) load(p0);
+    for (int p0 = first + tid; p0 < last; p0 += U * kPlanThreads) {
+        int e[U];
 #pragma unroll
-        for (int i = 0; i < kPlanAhead; ++i) {
-            if (p0 + 32 * i >= last) break;
-            const int p = p0 + 32 * i + lane, x = id[i];
-            const uint32_t same = __match_any_sync(0xffffffffu, x);
-            int row = -1;
-            if (x >= 0) {
-                row = mine[x] + __popc(same & ((1u << lane) - 1));
-                plan.row_pair[row] = p;
-            }
-            __syncwarp();
-            if (x >= 0 && lane == __ffs(same) - 1) mine[x] += __popc(same);
-            __syncwarp();
-            if (p < last) plan.pair_row[p] = row;
-        }
+        for (int i = 0; i < U; ++i) e[i] = p0 + i * kPlanThreads < last ? expert[p0 + i * kPlanThreads] : -1;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (p0 + i * kPlanThreads < last)
+                plan.pair_row[p0 + i * kPlanThreads] = e[i] >= 0 && e[i] < experts ? min(atomicAdd(&next[e[i]], 1), pairs - 1) : -1;
     }
+    cluster_sync();  // (the counts stay until all CTAs have read them)
 }
 
-constexpr int kStageThreads = 128;
+constexpr int kStageThreads = 128, kBoundBlocks = 4;
 
-// Stages a row a block: binary16 terms of the row times the power of two that brings its largest value between 2^14 and
-// 2^15 (no value overflows, and one 2^-28 of the largest still has all its bits), in the products' order; scale is the
-// power that undoes it.  GATHER: row r is that of the token of pair row_pair[r]; else row r of the input.
-template <typename T, bool GATHER>
-__global__ void __launch_bounds__(kStageThreads)
-moe_stage_kernel(const T *__restrict__ in, MoePlan plan, __half *__restrict__ staged, float *__restrict__ scale, int k,
-                 int top_k, int terms) {
-    __shared__ float part[kStageThreads / 32];
-    const int r = blockIdx.x;
+struct StageArgs {
+    MoePlan plan;
+    __half *staged;  // [pairs][terms][k]
+    float *scale;    // [pairs]
+    float *sum;      // [pairs] of |x|, not below it
+    const __half *d;
+    int64_t d_count;  // of an expert
+    int64_t tokens;
+    int k, top_k, terms, experts;
+};
+
+// Stages a token a block: binary16 terms of its row times the power of two that brings its largest value between 2^14 and
+// 2^15 (no value overflows, and one 2^-28 of the largest still has all its bits), in the products' order, to the rows of all
+// its pairs; scale is the power that undoes it.  The blocks behind the tokens' take the largest block scales of the
+// experts that have tokens.
+template <typename T>
+__global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
+    __shared__ float part[2][kStageThreads / 32];
+    __shared__ int to[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (r >= plan.counts[1]) return;
-    const T *row = in + int64_t(GATHER ? plan.row_pair[r] / top_k : r) * k;
-    auto load = [&](int g, float (&v)[16]) {
-        struct alignas(16) Group {
-            T e[16];
-        };
-        const Group x = reinterpret_cast<const Group *>(row)[g];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = to_f32(x.e[i]);
+    if (blockIdx.x >= a.tokens) {
+        const int b = int(blockIdx.x - a.tokens), e = b / kBoundBlocks;
+        if (a.plan.expert_rows[e] == 0) return;
+        // (d_count is a multiple of 2: gate and up rows)
+        const uint32_t *d = reinterpret_cast<const uint32_t *>(a.d + int64_t(e) * a.d_count);
+        uint32_t top = 0;
+#pragma unroll 8
+        for (int64_t i = (b % kBoundBlocks) * kStageThreads + tid; i < a.d_count / 2; i += kBoundBlocks * kStageThreads) {
+            const uint32_t v = d[i] & 0x7fff7fffu;
+            top = max(top, max(v & 0xffffu, v >> 16));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) atomicMax(&a.plan.bound[e], __float_as_uint(__half2float(__ushort_as_half(uint16_t(top)))));
+        return;
+    }
+    const int64_t t = blockIdx.x;
+    if (tid < a.top_k) to[tid] = a.plan.pair_row[t * a.top_k + tid];
+    struct alignas(16) Group {
+        T e[16];
     };
-    float top = 0.f;
+    const Group *row = reinterpret_cast<const Group *>(x + t * a.k);
+    float top = 0.f, sum = 0.f;
     bool odd = false;  // an infinity or a NaN
-    for (int g = threadIdx.x; g < k / 16; g += kStageThreads) {
-        float v[16];
-        load(g, v);
+    for (int g = tid; g < a.k / 16; g += kStageThreads) {
+        const Group v = row[g];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            top = fmaxf(top, fabsf(v[i]));
-            odd |= !(fabsf(v[i]) < INFINITY);
+            const float f = fabsf(to_f32(v.e[i]));
+            top = fmaxf(top, f);
+            sum += f;
+            odd |= !(f < INFINITY);
         }
     }
     top = odd ? INFINITY : top;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = top;
+    for (int o = 16; o; o >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane == 0) {
+        part[0][warp] = top;
+        part[1][warp] = sum;
+    }
     __syncthreads();
+    sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kStageThreads / 32; ++w) top = fmaxf(top, part[w]);
-    // largest value 2^(e - 127) * [1, 2): times 2^(14 - (e - 127)), exponents kept to what f32 holds
-    const int e = int(__float_as_uint(top) >> 23);
-    const int up = top < INFINITY ? min(14 - (e - 127), 126) : 0;
-    const float by = __uint_as_float(uint32_t(up + 127) << 23);
-    if (threadIdx.x == 0) scale[r] = __uint_as_float(uint32_t(max(127 - up, 1)) << 23);
-    for (int g = threadIdx.x; g < k / 16; g += kStageThreads) {
-        float v[16];
-        load(g, v);
+    for (int w = 0; w < kStageThreads / 32; ++w) {
+        top = fmaxf(top, part[0][w]);
+        sum += part[1][w];
+    }
+    const int up = top < INFINITY ? min(14 - moe_log2(top), 126) : 0;
+    const float by = moe_power(up);
+    if (tid < a.top_k && to[tid] >= 0) {
+        a.scale[to[tid]] = moe_power(-up);
+        a.sum[to[tid]] = sum * (1.f + 0x1p-10f);  // (its rounding, at most 2^-24 an addition)
+    }
+    for (int g = tid; g < a.k / 16; g += kStageThreads) {
+        const Group v = row[g];
         __half2 hi[8], lo[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float a = v[i] * by, b = v[i + 8] * by;
-            hi[i] = __floats2half2_rn(a, b);
+            const float p = to_f32(v.e[i]) * by, q = to_f32(v.e[i + 8]) * by;
+            hi[i] = __floats2half2_rn(p, q);
             const float2 h = __half22float2(hi[i]);
-            lo[i] = __floats2half2_rn(a - h.x, b - h.y);
+            lo[i] = __floats2half2_rn(p - h.x, q - h.y);
         }
-        uint4 *to = reinterpret_cast<uint4 *>(staged + int64_t(r) * terms * k + 16 * g);
-        to[0] = reinterpret_cast<const uint4 *>(hi)[0];
-        to[1] = reinterpret_cast<const uint4 *>(hi)[1];
-        if (terms == 2) {
-            to = reinterpret_cast<uint4 *>(staged + (int64_t(r) * terms + 1) * k + 16 * g);
-            to[0] = reinterpret_cast<const uint4 *>(lo)[0];
-            to[1] = reinterpret_cast<const uint4 *>(lo)[1];
+        for (int j = 0; j < a.top_k; ++j) {
+            if (to[j] < 0) continue;
+            uint4 *dst = reinterpret_cast<uint4 *>(a.staged + int64_t(to[j]) * a.terms * a.k + 16 * g);
+            dst[0] = reinterpret_cast<const uint4 *>(hi)[0];
+            dst[1] = reinterpret_cast<const uint4 *>(hi)[1];
+            if (a.terms == 2) {
+                dst += a.k / 8;
+                dst[0] = reinterpret_cast<const uint4 *>(lo)[0];
+                dst[1] = reinterpret_cast<const uint4 *>(lo)[1];
+            }
         }
     }
 }
@@ -236,7 +269,7 @@ int tile_cols(int64_t pairs, int64_t experts, int terms) { return pairs * terms 
 struct Workspace {
     MoePlan plan;
     __half *staged_x, *staged_h;
-    float *scale_x, *scale_h, *h, *y;
+    float *scale_x, *scale_h, *sum_x, *y;
     int max_tiles, cols;
     size_t bytes;
 
@@ -249,14 +282,15 @@ struct Workspace {
         cols = tile_cols(pairs, experts, terms);
         const int64_t tile_rows = cols / terms;
         max_tiles = int(std::min(pairs, experts) + pairs / tile_rows);  // each expert leaves less than one unfilled
-        take(plan.counts, 2);
-        take(plan.tiles, size_t(max_tiles));
-        take(plan.row_pair, size_t(pairs));
+        take(plan.tile_count, 1);
+        take(plan.tiles, size_t(std::min(pairs, experts) + pairs / (64 / terms)));
         take(plan.pair_row, size_t(pairs));
+        take(plan.expert_rows, size_t(experts));
+        take(plan.bound, size_t(experts));
         take(scale_x, size_t(pairs));
         take(scale_h, size_t(pairs));
+        take(sum_x, size_t(pairs));
         take(staged_x, size_t(pairs * terms * width));
-        take(h, size_t(pairs * ffn));
         take(staged_h, size_t(pairs * terms * ffn));
         take(y, size_t(pairs * width));
         bytes = at;
@@ -265,19 +299,48 @@ struct Workspace {
 
 int terms_of(int dtype) { return dtype == TQ2_F32 ? 2 : 1; }
 
+cudaError_t launch_plan(const MoeArgs &a, const Workspace &w, int64_t pairs, int terms, const LaunchCtx &ctx) {
+    int cluster = 1;
+    while (cluster < kPlanMaxCluster && pairs > cluster * kPlanPairs) cluster *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(cluster));
+    cfg.blockDim = dim3(kPlanThreads);
+    cfg.stream = ctx.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, moe_plan_kernel, a.expert, w.plan, int(pairs), a.experts, w.cols / terms, cluster, ctx.status);
+}
+
 template <typename T>
 cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) {
     const int64_t pairs = a.tokens * a.top_k;
     const int terms = terms_of(dtype);
     const Workspace w(static_cast<char *>(ws), pairs, a.experts, a.width, a.ffn, terms);
-    const size_t plan_smem = size_t(kPlanWarps) * size_t(a.experts) * 4;
-    cudaError_t e = cudaFuncSetAttribute(moe_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(plan_smem));
-    if (e == cudaSuccess)
-        e = launch_dependent(moe_plan_kernel, dim3(1), kPlanThreads, int(plan_smem), ctx.stream, a.expert, w.plan, int(pairs),
-                             a.experts, w.cols / terms, ctx.status);
-    if (e == cudaSuccess)
-        e = launch_dependent(moe_stage_kernel<T, true>, dim3(unsigned(pairs)), kStageThreads, 0, ctx.stream,
-                             static_cast<const T *>(a.x), w.plan, w.staged_x, w.scale_x, a.width, a.top_k, terms);
+    const SoaView gate_up = soa_view(a.gate_up, int64_t(a.experts) * 2 * a.ffn, a.width);
+    const SoaView down = soa_view(a.down, int64_t(a.experts) * a.width, a.ffn);
+    cudaError_t e = launch_plan(a, w, pairs, terms, ctx);
+    if (e != cudaSuccess) return e;
+    StageArgs s = {};
+    s.plan = w.plan;
+    s.staged = w.staged_x;
+    s.scale = w.scale_x;
+    s.sum = w.sum_x;
+    s.d = gate_up.d;
+    s.d_count = int64_t(2) * a.ffn * (a.width / kBlockW);
+    s.tokens = a.tokens;
+    s.k = a.width;
+    s.top_k = a.top_k;
+    s.terms = terms;
+    s.experts = a.experts;
+    e = launch_dependent(moe_stage_kernel<T>, dim3(unsigned(a.tokens + a.experts * kBoundBlocks)), kStageThreads, 0, ctx.stream,
+                         static_cast<const T *>(a.x), s);
     if (e != cudaSuccess) return e;
     MoeGemm g = {};
     g.plan = w.plan;
@@ -286,21 +349,18 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     g.terms = terms;
     g.cols = w.cols;
     g.max_tiles = w.max_tiles;
-    SoaView v = soa_view(a.gate_up, int64_t(a.experts) * 2 * a.ffn, a.width);
-    g.qs = v.qs;
-    g.d = v.d;
+    g.qs = gate_up.qs;
+    g.d = gate_up.d;
     g.staged = w.staged_x;
     g.scale = w.scale_x;
-    g.out = w.h;
+    g.sum = w.sum_x;
+    g.staged_out = w.staged_h;
+    g.scale_out = w.scale_h;
     g.rows = 2 * a.ffn;
     g.k = a.width;
     if ((e = launch_moe_gemm(g, true, ctx)) != cudaSuccess) return e;
-    e = launch_dependent(moe_stage_kernel<float, false>, dim3(unsigned(pairs)), kStageThreads, 0, ctx.stream,
-                         static_cast<const float *>(w.h), w.plan, w.staged_h, w.scale_h, a.ffn, 1, terms);
-    if (e != cudaSuccess) return e;
-    v = soa_view(a.down, int64_t(a.experts) * a.width, a.ffn);
-    g.qs = v.qs;
-    g.d = v.d;
+    g.qs = down.qs;
+    g.d = down.d;
     g.staged = w.staged_h;
     g.scale = w.scale_h;
     g.out = w.y;

@@ -15,10 +15,11 @@ struct alignas(16) MoeTile {
 
 // Device tables of one call, from its routing: `rows` (token, expert) pairs sorted by expert, and their tiles.
 struct MoePlan {
-    int *counts;       // [2]: tiles, rows
+    int *tile_count;
     MoeTile *tiles;
-    int *row_pair;     // [pairs] pair of each row
-    int *pair_row;     // [pairs] row of each pair, -1: none
+    int *pair_row;        // [pairs] row of each pair, -1: none
+    int *expert_rows;     // [experts]
+    uint32_t *bound;      // [experts] largest |d| of the gate and up rows (the bits of an f32)
 };
 
 // One ternary product of the layer: of staged activations (see moe_stage_kernel) with the rows of each tile's expert.
@@ -27,18 +28,27 @@ struct MoeGemm {
     const uint8_t *qs;   // codes [experts * rows][k / 4]
     const __half *d;     // block scales [experts * rows][k / 128]
     const __half *staged;
-    const float *scale;  // of each row
-    float *out;          // [rows][features]
+    const float *scale;  // of each row: what its staged values are to be multiplied by
+    const float *sum;    // gate_up: of each row, the sum of |x|
+    float *out;          // down: [rows][features]
+    __half *staged_out;  // gate_up: the hidden values, staged
+    float *scale_out;    //          and each row's scale
     int64_t pairs;
     int experts, rows, k;
     int terms;           // staged rows of a row
     int cols;            // staged rows (MMA columns) of a tile, at most: 64 or 128
     int max_tiles;
 };
-// gate_up: rows holds gate then up rows, out the SwiGLU of rows / 2 features; else out is the product.
+// gate_up: rows counts gate then up rows, and the SwiGLU of rows / 2 features is staged; else out is the product.
 cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx);
 
 // Order of staged activations: a staged row holds elements i and i + 8 of each group of 16 at 2 i and 2 i + 1, as pairs of
 // codes are masked out of a word of 16 (the library's binary16 activation layout).
+__host__ __device__ constexpr int moe_place(int i) { return i < 8 ? 2 * i : 2 * (i - 8) + 1; }
+
+// 2^e with e kept to what f32 holds as a normal number.
+__device__ __forceinline__ float moe_power(int e) { return __uint_as_float(uint32_t(max(min(e, 127), -126) + 127) << 23); }
+// log2 of a positive finite f32, downwards (below 2^-126: -127).
+__device__ __forceinline__ int moe_log2(float x) { return int(__float_as_uint(x) >> 23) - 127; }
 
 }  // namespace tq2

@@ -225,7 +225,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(ctl->tmem_base)));
     const int parts = g.rows / 128, nb = uniform(g.k / kBlockW);
-    const int items = uniform(g.plan.counts[0] * parts);
+    const int items = uniform(*g.plan.tile_count * parts);
     auto wait_on = [&](uint64_t *bar, uint32_t parity) {
         return bool(__all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, wait_ns, status)));
     };
@@ -366,9 +366,19 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             const __half *dp = g.d + int64_t(row) * nb;
             // the scales of this group's rows, two a lane
             const int r0 = col0 / g.terms, left = it.tile.n - r0;
-            float scale[2];
+            float scale[2], up[2];  // up (gate_up): the power of two that the hidden values are staged with
 #pragma unroll
-            for (int j = 0; j < 2; ++j) scale[j] = g.scale[it.tile.row0 + min(r0 + 32 * j + lane, it.tile.n - 1)];
+            for (int j = 0; j < 2; ++j) {
+                const int at = it.tile.row0 + min(r0 + 32 * j + lane, it.tile.n - 1);
+                scale[j] = g.scale[at];
+                if (GATE_UP) {
+                    // |gate|, |up| <= bound * sum < 2^(e + 1), so that a hidden value times 2^(13 - 2 e) is below 2^15
+                    const float b = __uint_as_float(g.plan.bound[it.tile.expert]) * g.sum[at];
+                    const int e = b < INFINITY ? max(min(13 - 2 * moe_log2(b), 126), -126) : 0;
+                    up[j] = moe_power(e);
+                    if (it.part == 0 && q == 0) g.scale_out[at] = moe_power(-e);
+                }
+            }
             uint64_t acc[32];  // columns 2 c, 2 c + 1
 #pragma unroll
             for (int c = 0; c < 32; ++c) acc[c] = 0;
@@ -397,7 +407,6 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             }
             if (!ok) break;
             if (COLS == 64 && lane == 0) mbar_arrive(&ctl->turn[group ^ 1]);
-            float *out = g.out + int64_t(it.tile.row0 + r0) * features;
             auto finish = [&](auto two) {
                 constexpr int S = decltype(two)::value;
                 // row c of the group: column c, or the sum of columns 2 c and 2 c + 1 (terms)
@@ -405,22 +414,30 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                     return S == 2 ? first(acc[c]) + second(acc[c]) : c & 1 ? second(acc[c >> 1]) : first(acc[c >> 1]);
                 };
                 if (GATE_UP) {
-                    out += 64 * it.part + 16 * q + (lane & 15);
-                    const int up = lane >= 16;
+                    // this lane's place in a staged row
+                    __half *out = g.staged_out + int64_t(it.tile.row0 + r0) * S * features + 64 * it.part + 16 * q + moe_place(lane & 15);
+                    const int odd = lane >= 16;
 #pragma unroll
                     for (int c0 = 0; c0 < 64 / S; c0 += 8)
                         if (c0 < left) {
 #pragma unroll
                             for (int c = c0; c < c0 + 8; c += 2) {
                                 // lanes 0-15 finish row c, lanes 16-31 row c + 1
-                                const float s = __shfl_sync(0xffffffffu, scale[c >> 5], (c & 31) + up);
-                                const float other = __shfl_xor_sync(0xffffffffu, up ? sum(c) : sum(c + 1), 16);
-                                const float gate = (up ? other : sum(c)) * s, ups = (up ? sum(c + 1) : other) * s;
-                                if (c + up < left) out[int64_t(c + up) * features] = silu(gate) * ups;
+                                const float s = __shfl_sync(0xffffffffu, scale[c >> 5], (c & 31) + odd);
+                                const float by = __shfl_sync(0xffffffffu, up[c >> 5], (c & 31) + odd);
+                                const float other = __shfl_xor_sync(0xffffffffu, odd ? sum(c) : sum(c + 1), 16);
+                                const float gate = (odd ? other : sum(c)) * s, ups = (odd ? sum(c + 1) : other) * s;
+                                const float h = silu(gate) * ups * by;
+                                if (c + odd < left) {
+                                    const __half hi = __float2half_rn(h);
+                                    __half *to = out + int64_t(c + odd) * S * features;
+                                    to[0] = hi;
+                                    if (S == 2) to[features] = __float2half_rn(h - __half2float(hi));
+                                }
                             }
                         }
                 } else {
-                    out += 128 * it.part + 32 * q + lane;
+                    float *out = g.out + int64_t(it.tile.row0 + r0) * features + 128 * it.part + 32 * q + lane;
 #pragma unroll
                     for (int c0 = 0; c0 < 64 / S; c0 += 8)
                         if (c0 < left) {

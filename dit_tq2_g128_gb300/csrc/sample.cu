@@ -100,7 +100,7 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, S
 // Sorts list[0, count) descending (all different).  Short ones by counting who is larger (a list of 100: 700 cycles, not
 // the 5000 of the network's 28 steps); others by a bitonic network, a thread a pair, whose steps of up to 32 stay within the
 // 64 elements of a warp's pairs, so that warps need not meet between them.
-__device__ void sort_list(unsigned long long *list, unsigned long long *spare, int count) {
+__device__ __forceinline__ void sort_list(unsigned long long *list, unsigned long long *spare, int count) {
     const int i = threadIdx.x;
     if (count <= kRankSort) {
         __syncthreads();
@@ -296,6 +296,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
             }
             const int b = !fours || (lane & 3) == 0 ? bin_of_logit(m) : -1;
             if (b >= 0) atomicAdd(&lead->count[b], 1u);
+            if (!cut_k) {
+                __syncthreads();
+                if (tid == 0) atomicAdd(&lead->total, sh->sum);
+            }
             cluster_sync();
             if (rank == 0) {
                 constexpr int per = (kBins + kThreads - 1) / kThreads;
@@ -313,20 +317,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
                     before += c[j];
                 }
                 __syncthreads();
-                // (none found: whatever has a weight)
-                if (tid < cluster)
-                    at_cta(sh, uint32_t(tid))->floor =
-                        rw.floor_of(sh->found == kBins ? float(kWeightBits + 1) : float(sh->found + 1) / per_unit);
+                // (none found: whatever has a weight; no head at all where top_p wants more than one can weigh)
+                const float limit = sh->found == kBins ? float(kWeightBits + 1) : float(sh->found + 1) / per_unit;
+                const bool flat = !cut_k && cut_p && mass_needed(p, sh->total) >> kWeightBits > kHead;
+                if (tid < cluster) at_cta(sh, uint32_t(tid))->floor = flat ? INFINITY : rw.floor_of(limit);
             }
             cluster_sync();
         } else if (!cut_k) {
             __syncthreads();
+            if (tid == 0) atomicAdd(&lead->total, sh->sum);
         }
-        if (!cut_k && tid == 0) atomicAdd(&lead->total, sh->sum);
         const float floor = all ? -3.402823466e38f : sh->floor;
         const Pack<T> *packed = reinterpret_cast<const Pack<T> *>(x - shift);
         const int packs = n > 0 ? (n + shift + V - 1) / V : 0;
-        if (mine >= floor)  // (the packs that this thread brought)
+        if (mine >= floor && floor < INFINITY)  // (the packs that this thread brought)
             for (int q = tid; q < packs; q += kThreads) {
                 const Pack<T> v = packed[q];
                 bool any = false;
@@ -341,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
                     }
                 }
             }
-        hand_over();
+        if (floor < INFINITY) hand_over();
     }
 
     // (first CTA) Sorts the list's `count` elements: this thread's weights and their cumulative ones, from `before` on (in
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     if (try_head) {
         if (rank == 0) {
             const int count = int(sh->n_list);
-            bool ok = count <= kList;
+            bool ok = count > 0 && count <= kList;
             if (ok) {
                 sort_and_sum(count, 0);
                 const unsigned long long head = sh->cum[count - 1];
