@@ -120,7 +120,8 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
     cluster_sync();  // (the counts stay until all CTAs have read them)
 }
 
-constexpr int kStageThreads = 128, kBoundBlocks = 4;
+constexpr int kStageThreads = 128;
+constexpr int kBoundScales = 8192;  // block scales of a block that looks for the largest
 
 struct StageArgs {
     MoePlan plan;
@@ -129,6 +130,7 @@ struct StageArgs {
     float *sum;      // [pairs] of |x|, not below it
     const __half *d;
     int64_t d_count;  // of an expert
+    int bound_blocks;
     int64_t tokens;
     int k, top_k, terms, experts;
 };
@@ -145,15 +147,15 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (blockIdx.x >= a.tokens) {
-        const int b = int(blockIdx.x - a.tokens), e = b / kBoundBlocks;
+        const int b = int(blockIdx.x - a.tokens), e = b / a.bound_blocks, i0 = b % a.bound_blocks * (kBoundScales / 8);
         if (a.plan.expert_rows[e] == 0) return;
-        // (d_count is a multiple of 2: gate and up rows)
-        const uint32_t *d = reinterpret_cast<const uint32_t *>(a.d + int64_t(e) * a.d_count);
+        // (an expert has a multiple of 256 of them)
+        const uint4 *d = reinterpret_cast<const uint4 *>(a.d + e * a.d_count);
         uint32_t top = 0;
-#pragma unroll 8
-        for (int64_t i = (b % kBoundBlocks) * kStageThreads + tid; i < a.d_count / 2; i += kBoundBlocks * kStageThreads) {
-            const uint32_t v = d[i] & 0x7fff7fffu;
-            top = max(top, max(v & 0xffffu, v >> 16));
+#pragma unroll 4
+        for (int i = i0 + tid; i < min(i0 + kBoundScales / 8, int(a.d_count / 8)); i += kStageThreads) {
+            const uint4 v = d[i];
+            for (uint32_t w : {v.x, v.y, v.z, v.w}) top = max(top, max(w & 0x7fffu, w >> 16 & 0x7fffu));
         }
         top = __reduce_max_sync(0xffffffffu, top);
         if (lane == 0) atomicMax(&a.plan.bound[e], __float_as_uint(__half2float(__ushort_as_half(uint16_t(top)))));
@@ -334,12 +336,13 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     s.sum = w.sum_x;
     s.d = gate_up.d;
     s.d_count = int64_t(2) * a.ffn * (a.width / kBlockW);
+    s.bound_blocks = int((s.d_count + kBoundScales - 1) / kBoundScales);
     s.tokens = a.tokens;
     s.k = a.width;
     s.top_k = a.top_k;
     s.terms = terms;
     s.experts = a.experts;
-    e = launch_dependent(moe_stage_kernel<T>, dim3(unsigned(a.tokens + a.experts * kBoundBlocks)), kStageThreads, 0, ctx.stream,
+    e = launch_dependent(moe_stage_kernel<T>, dim3(unsigned(a.tokens + int64_t(a.experts) * s.bound_blocks)), kStageThreads, 0, ctx.stream,
                          static_cast<const T *>(a.x), s);
     if (e != cudaSuccess) return e;
     MoeGemm g = {};

@@ -149,6 +149,19 @@ __device__ __forceinline__ void decode(const uint4 &w, uint32_t (&r)[32]) {
     }
 }
 
+// Whether a phase is over, without waiting.
+__device__ __forceinline__ bool phase_over(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok;
+}
+
 // An item's place: its tile and its 128 weight rows.
 struct Item {
     MoeTile tile;
@@ -294,8 +307,13 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                     const uint32_t idesc = (1u << 4) | (uint32_t(next.take() >> 3) << 17) | (uint32_t(128 >> 4) << 24);
                     for (int b = 0; b < nb; ++b, ++n) {
                         const int sx = n % L::ACTS, sa = n % kABufs, sd = n % L::DBUFS;
-                        if (n >= L::DBUFS) ok = wait_one(&ctl->d_empty[sd], (n / L::DBUFS - 1) & 1);
-                        ok = ok && wait_one(&ctl->x_full[sx], (n / L::ACTS) & 1) && wait_one(&ctl->a_full[sa], (n / kABufs) & 1);
+                        // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
+                        // its first use counts as over)
+                        const uint32_t pd = ((n / L::DBUFS) & 1) ^ 1, px = (n / L::ACTS) & 1, pa = (n / kABufs) & 1;
+                        const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
+                                   a_there = phase_over(&ctl->a_full[sa], pa);
+                        ok = (d_free || wait_one(&ctl->d_empty[sd], pd)) && (x_there || wait_one(&ctl->x_full[sx], px)) &&
+                             (a_there || wait_one(&ctl->a_full[sa], pa));
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4));
@@ -318,37 +336,42 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         const int q = warp & 3, group = (warp - W_DECODE) >> 2;
         // the row of this thread's lane among the stage's 128: gate rows in lanes 0-15, the up rows of the same features above
         const int r = GATE_UP ? (lane < 16 ? 16 * q + lane : 48 + 16 * q + lane) : 32 * q + lane;
+        // This group's blocks are the even or the odd ones of all.  Each group waits for every stage, so that none is ever two
+        // uses of a slot ahead of the other.
         int n0 = 0, stage0 = 0;  // blocks and stages before the item
         bool ok = true;
         for (int i = blockIdx.x; ok && i < items; i += gridDim.x, n0 += nb, stage0 += (nb + 3) / 4) {
-            for (int b = 0; b < nb; ++b) {
-                const int stage = stage0 + b / 4, sc = stage % L::CODES, n = n0 + b, sa = n % kABufs;
-                const bool last = (b & 3) == 3 || b == nb - 1;
-                // (each group waits for every stage, so that none is ever two uses of a slot ahead of the other)
-                if ((b & 3) == 0 && !(ok = wait_on(&ctl->c_full[sc], (stage / L::CODES) & 1))) break;
-                if ((n & 1) == group) {
-                    const uint8_t *row = smem + sc * kCodeBytes + r * 128;
-                    uint4 w[2];
+            for (int b4 = 0; ok && b4 < nb; b4 += 4) {
+                const int stage = stage0 + b4 / 4, sc = stage % L::CODES;
+                if (!(ok = wait_on(&ctl->c_full[sc], (stage / L::CODES) & 1))) break;
+                const uint8_t *row = smem + sc * kCodeBytes + r * 128;
+                // the (up to two) blocks of this stage that are this group's
+                const int from = (n0 + b4 + group) & 1, count = b4 + from >= nb ? 0 : b4 + from + 2 >= nb || from + 2 > 3 ? 1 : 2;
+                uint4 w[2][2];
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        w[j] = *reinterpret_cast<const uint4 *>(row + (((2 * (b & 3) + j) ^ (r & 7)) << 4));
-                    if (n >= kABufs && !(ok = wait_on(&ctl->a_empty[sa], (n / kABufs - 1) & 1))) break;
+                        w[t][j] = *reinterpret_cast<const uint4 *>(row + (((2 * (from + 2 * t) + j) ^ (r & 7)) << 4));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->c_empty[sc]);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    if (t >= count) break;
+                    const int n = n0 + b4 + from + 2 * t, sa = n % kABufs;
+                    if (!(ok = wait_on(&ctl->a_empty[sa], ((n / kABufs) & 1) ^ 1))) break;
                     tc_fence_after();
                     const uint32_t at = tmem + L::A_COL + uint32_t(sa * kACols) + (uint32_t(q * 32) << 16);
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         uint32_t v[32];
-                        decode(w[j], v);
+                        decode(w[t][j], v);
                         tm_st32(at + uint32_t(32 * j), v);
                     }
                     tm_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&ctl->a_full[sa]);
-                }
-                if (last) {
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->c_empty[sc]);
                 }
             }
         }
@@ -357,9 +380,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         const int q = warp & 3, group = (warp - W_SUM) >> 2, col0 = COLS == 128 ? 64 * group : 0;
         const int features = GATE_UP ? g.rows / 2 : g.rows;
         const int step = COLS == 128 ? gridDim.x : 2 * gridDim.x;
-        int n0 = COLS == 128 ? 0 : group * nb, j = group;  // blocks and (64 columns) items of this CTA before the item
+        int n0 = COLS == 128 ? 0 : group * nb, turn = group;  // blocks and (64 columns) items of this CTA before the item
         bool ok = true;
-        for (int i = COLS == 128 ? blockIdx.x : blockIdx.x + group * gridDim.x; ok && i < items; i += step, n0 += COLS == 128 ? nb : 2 * nb, j += 2) {
+        for (int i = COLS == 128 ? blockIdx.x : blockIdx.x + group * gridDim.x; ok && i < items; i += step, n0 += COLS == 128 ? nb : 2 * nb, turn += 2) {
             const Item it = item_of(g, i, parts);
             const int row = it.tile.expert * g.rows + (GATE_UP ? 64 * it.part + 16 * q + (lane & 15) + (lane < 16 ? 0 : g.rows / 2)
                                                               : 128 * it.part + 32 * q + lane);
@@ -384,7 +407,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             for (int c = 0; c < 32; ++c) acc[c] = 0;
             float dn = __half2float(dp[0]);
             // (in turn: a group that waited for a block two uses of its accumulator ahead would take the one before for it)
-            if (COLS == 64 && j > 0 && !(ok = wait_on(&ctl->turn[group], ((j - 1) >> 1) & 1))) break;
+            if (COLS == 64 && turn > 0 && !(ok = wait_on(&ctl->turn[group], ((turn - 1) >> 1) & 1))) break;
             for (int b = 0; b < nb; ++b) {
                 const int n = n0 + b, sd = n % L::DBUFS;
                 const uint64_t d = pair(dn, dn);
