@@ -33,25 +33,27 @@ constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4, W_SUM = 12;
 constexpr int kRegs = 96, kRegsControl = 48, kRegsDecode = 72, kRegsSum = 144;
 static_assert(kRegsControl + 2 * kRegsDecode + 2 * kRegsSum <= 5 * kRegs, "registers");
 constexpr int kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
-constexpr int kABufs = 4, kACols = kBlockW / 2;
+constexpr int kRing = 4;  // blocks on their way: stages of activations, decoded weights
+constexpr int kACols = kBlockW / 2;
 constexpr uint32_t kTmemCols = 512;
 
 template <int COLS>
 struct Shape {
-    static constexpr int CODES = COLS == 64 ? 6 : 4;              // stages of codes
-    static constexpr int ACTS = COLS == 64 ? 8 : 4;               // stages of activations
+    static constexpr int CODES = COLS == 64 ? 8 : 4;              // stages of codes
     static constexpr int ACT_BYTES = COLS * kBlockW * 2;          // two halves of 64 features
     static constexpr int DBUFS = 256 / COLS;
     static constexpr uint32_t A_COL = DBUFS * COLS;
-    static constexpr int OFF_ACT = CODES * kCodeBytes, OFF_CTL = OFF_ACT + ACTS * ACT_BYTES;
-    static_assert(A_COL + kABufs * kACols <= kTmemCols, "TMEM budget");
+    static constexpr int OFF_ACT = CODES * kCodeBytes, OFF_CTL = OFF_ACT + kRing * ACT_BYTES;
+    static_assert(A_COL + kRing * kACols <= kTmemCols, "TMEM budget");
 };
 
 struct Ctl {
-    uint64_t c_full[6], c_empty[6];
-    uint64_t x_full[8], x_empty[8];
-    uint64_t a_full[kABufs], a_empty[kABufs];
-    uint64_t d_full[4], d_empty[4];
+    uint64_t c_full[8], c_empty[8];
+    uint64_t x_full[kRing], a_full[kRing];
+    // A block's MMAs have ended: its operands' slots are free and its accumulator is full.  (One commit a block: with one for
+    // each of the three the issuing lane stood still for 300 cycles.)
+    uint64_t done[kRing];
+    uint64_t d_empty[4];
     uint64_t turn[2];  // (64 columns) a summing group may begin its next item: the other has seen all blocks of the one before
     uint64_t drain;
     uint32_t tmem_base;
@@ -209,18 +211,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             mbar_init(&ctl->c_full[s], 1);
             mbar_init(&ctl->c_empty[s], 8);
         }
-        for (int s = 0; s < L::ACTS; ++s) {
+        for (int s = 0; s < kRing; ++s) {
             mbar_init(&ctl->x_full[s], 1);
-            mbar_init(&ctl->x_empty[s], 1);
-        }
-        for (int s = 0; s < kABufs; ++s) {
             mbar_init(&ctl->a_full[s], 4);
-            mbar_init(&ctl->a_empty[s], 1);
+            mbar_init(&ctl->done[s], 1);
         }
-        for (int s = 0; s < L::DBUFS; ++s) {
-            mbar_init(&ctl->d_full[s], 1);
-            mbar_init(&ctl->d_empty[s], COLS / 16);
-        }
+        for (int s = 0; s < L::DBUFS; ++s) mbar_init(&ctl->d_empty[s], COLS / 16);
         for (int s = 0; s < 2; ++s) mbar_init(&ctl->turn[s], 4);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
@@ -274,8 +270,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const Item it = item_of(g, i, parts);
                 for (int b = 0; b < nb; ++b, ++n) {
-                    const int s = n % L::ACTS;
-                    if (n >= L::ACTS && !(ok = wait_on(&ctl->x_empty[s], (n / L::ACTS - 1) & 1))) break;
+                    const int s = n % kRing;
+                    if (!(ok = wait_on(&ctl->done[s], ((n / kRing) & 1) ^ 1))) break;
                     if (elect_one()) {
                         // (boxes of 16 rows, or of 64: the rows after the tile's are other experts', whose columns nothing reads)
                         const bool wide = it.cols > 32;
@@ -292,8 +288,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 }
             }
             if (lane == 0)
-                for (int j = max(0, n - L::ACTS); j < n; ++j)
-                    mbar_wait_bounded(&ctl->x_full[j % L::ACTS], (j / L::ACTS) & 1, drain_ns(wait_ns), status);
+                for (int j = max(0, n - kRing); j < n; ++j)
+                    mbar_wait_bounded(&ctl->x_full[j % kRing], (j / kRing) & 1, drain_ns(wait_ns), status);
             __syncwarp();
         } else if (warp == W_MMA) {
             // (one lane takes the whole loop, from values that the compiler knows to be uniform)
@@ -306,25 +302,23 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                     const uint32_t idesc = (1u << 4) | (uint32_t(next.take() >> 3) << 17) | (uint32_t(128 >> 4) << 24);
                     for (int b = 0; b < nb; ++b, ++n) {
-                        const int sx = n % L::ACTS, sa = n % kABufs, sd = n % L::DBUFS;
+                        const int sx = n % kRing, sd = n % L::DBUFS;
                         // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
                         // its first use counts as over)
-                        const uint32_t pd = ((n / L::DBUFS) & 1) ^ 1, px = (n / L::ACTS) & 1, pa = (n / kABufs) & 1;
+                        const uint32_t pd = ((n / L::DBUFS) & 1) ^ 1, px = (n / kRing) & 1;
                         const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
-                                   a_there = phase_over(&ctl->a_full[sa], pa);
+                                   a_there = phase_over(&ctl->a_full[sx], px);
                         ok = (d_free || wait_one(&ctl->d_empty[sd], pd)) && (x_there || wait_one(&ctl->x_full[sx], px)) &&
-                             (a_there || wait_one(&ctl->a_full[sa], pa));
+                             (a_there || wait_one(&ctl->a_full[sx], px));
                         if (!ok) break;
                         tc_fence_after();
                         const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4));
-                        const uint32_t d = tmem + uint32_t(sd * COLS), at = tmem + L::A_COL + uint32_t(sa * kACols);
+                        const uint32_t d = tmem + uint32_t(sd * COLS), at = tmem + L::A_COL + uint32_t(sx * kACols);
 #pragma unroll
                         for (int kk = 0; kk < 8; ++kk)
                             mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * (L::ACT_BYTES / 2 >> 4) + 2 * (kk & 3)), idesc,
                                    kk > 0);
-                        tc_commit(&ctl->a_empty[sa]);
-                        tc_commit(&ctl->x_empty[sx]);
-                        tc_commit(&ctl->d_full[sd]);
+                        tc_commit(&ctl->done[sx]);
                     }
                 }
                 tc_commit(&ctl->drain);
@@ -358,8 +352,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (t >= count) break;
-                    const int n = n0 + b4 + from + 2 * t, sa = n % kABufs;
-                    if (!(ok = wait_on(&ctl->a_empty[sa], ((n / kABufs) & 1) ^ 1))) break;
+                    const int n = n0 + b4 + from + 2 * t, sa = n % kRing;
+                    if (!(ok = wait_on(&ctl->done[sa], ((n / kRing) & 1) ^ 1))) break;
                     tc_fence_after();
                     const uint32_t at = tmem + L::A_COL + uint32_t(sa * kACols) + (uint32_t(q * 32) << 16);
 #pragma unroll
@@ -412,7 +406,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 const int n = n0 + b, sd = n % L::DBUFS;
                 const uint64_t d = pair(dn, dn);
                 if (b + 1 < nb) dn = __half2float(dp[b + 1]);
-                if (!(ok = wait_on(&ctl->d_full[sd], (n / L::DBUFS) & 1))) break;
+                if (!(ok = wait_on(&ctl->done[n % kRing], (n / kRing) & 1))) break;
                 tc_fence_after();
                 const uint32_t at = tmem + uint32_t(sd * COLS + col0) + (uint32_t(q * 32) << 16);
 #pragma unroll
