@@ -11,12 +11,12 @@
 //    numbers, they would save nothing: the tensor core aligns products by the operands' exponents, and f32 sums lost ten
 //    bits.)
 //  * The block scale d stays out of the operands: each 128-weight block is a product of its own (eight MMAs) into one of
-//    two accumulators, and d times it is added to the running sums in registers (f32).  So operands are exact, and what
+//    two or four accumulators, and d times it is added to the running sums in registers (f32).  So operands are exact, and what
 //    is rounded is the activations' staging and the sums.
 //  * Copies: codes by TMA, 512 weights of 128 rows a stage (64 KB in flight an SM); activations by TMA, 128 features of a
 //    tile's rows a stage.
 //  * Roles: warp 0 codes, warp 1 MMAs (owns tensor memory), warp 2 activations; two groups of four warps decode every other
-//    block; two groups scale and sum, each half of the columns, or, where tiles have 64 columns, every other item, so that
+//    unit (of one block, or of two where tiles have 64 columns); two groups scale and sum, each half of the columns, or, where tiles have 64 columns, every other item, so that
 //    one item's end runs under the next one's blocks.  One persistent CTA an SM.  Every wait is bounded; a timeout sets the status word and the
 //    CTA drains its copies and MMAs before it leaves.
 #include <cstdint>
@@ -33,7 +33,7 @@ constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4, W_SUM = 12;
 constexpr int kRegs = 96, kRegsControl = 48, kRegsDecode = 72, kRegsSum = 144;
 static_assert(kRegsControl + 2 * kRegsDecode + 2 * kRegsSum <= 5 * kRegs, "registers");
 constexpr int kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
-constexpr int kRing = 4;  // blocks on their way: stages of activations, decoded weights
+constexpr int kBlocks = 4;  // 128-weight blocks on their way: stages of activations, decoded weights
 constexpr int kACols = kBlockW / 2;
 constexpr uint32_t kTmemCols = 512;
 
@@ -41,19 +41,21 @@ template <int COLS>
 struct Shape {
     static constexpr int CODES = COLS == 64 ? 8 : 4;              // stages of codes
     static constexpr int ACT_BYTES = COLS * kBlockW * 2;          // two halves of 64 features
-    static constexpr int DBUFS = 256 / COLS;
-    static constexpr uint32_t A_COL = DBUFS * COLS;
-    static constexpr int OFF_ACT = CODES * kCodeBytes, OFF_CTL = OFF_ACT + kRing * ACT_BYTES;
-    static_assert(A_COL + kRing * kACols <= kTmemCols, "TMEM budget");
+    // Blocks of a unit, what the roles hand to each other at a time: with few columns a block's work is less than the latency
+    // of handing it on.
+    static constexpr int UNIT = COLS == 64 ? 2 : 1;
+    static constexpr int RING = kBlocks / UNIT, DRING = 256 / COLS / UNIT;
+    static constexpr uint32_t A_COL = 256;
+    static constexpr int OFF_ACT = CODES * kCodeBytes, OFF_CTL = OFF_ACT + kBlocks * ACT_BYTES;
+    static_assert(A_COL + kBlocks * kACols <= kTmemCols && DRING * UNIT * COLS <= A_COL, "TMEM budget");
 };
 
 struct Ctl {
     uint64_t c_full[8], c_empty[8];
-    uint64_t x_full[kRing], a_full[kRing];
-    // A block's MMAs have ended: its operands' slots are free and its accumulator is full.  (One commit a block: with one for
-    // each of the three the issuing lane stood still for 300 cycles.)
-    uint64_t done[kRing];
-    uint64_t d_empty[4];
+    // by unit
+    uint64_t x_full[kBlocks], a_full[kBlocks];
+    uint64_t done[kBlocks];  // its MMAs have ended: its operands' slots are free and its accumulators are full
+    uint64_t d_empty[2];
     uint64_t turn[2];  // (64 columns) a summing group may begin its next item: the other has seen all blocks of the one before
     uint64_t drain;
     uint32_t tmem_base;
@@ -86,18 +88,26 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
-__device__ __forceinline__ void tm_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+// Accumulators to registers; they are there after tm_wait_ld, and tm_tie keeps their use behind it.
+__device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t (&r)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
         "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
           "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
           "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
           "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr)
         : "memory");
+}
+__device__ __forceinline__ void tm_ld(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
+__device__ __forceinline__ void tm_wait_ld() { tc_wait_ld(); }
+template <int N>
+__device__ __forceinline__ void tm_tie(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
 }
 __device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32]) {
     asm volatile(
@@ -211,12 +221,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             mbar_init(&ctl->c_full[s], 1);
             mbar_init(&ctl->c_empty[s], 8);
         }
-        for (int s = 0; s < kRing; ++s) {
+        for (int s = 0; s < L::RING; ++s) {
             mbar_init(&ctl->x_full[s], 1);
             mbar_init(&ctl->a_full[s], 4);
             mbar_init(&ctl->done[s], 1);
         }
-        for (int s = 0; s < L::DBUFS; ++s) mbar_init(&ctl->d_empty[s], COLS / 16);
+        for (int s = 0; s < L::DRING; ++s) mbar_init(&ctl->d_empty[s], COLS / 16);
         for (int s = 0; s < 2; ++s) mbar_init(&ctl->turn[s], 4);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
@@ -233,7 +243,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = uint32_t(uniform(int(ctl->tmem_base)));
-    const int parts = g.rows / 128, nb = uniform(g.k / kBlockW);
+    const int parts = g.rows / 128, nb = uniform(g.k / kBlockW), units = (nb + L::UNIT - 1) / L::UNIT;
     const int items = uniform(*g.plan.tile_count * parts);
     auto wait_on = [&](uint64_t *bar, uint32_t parity) {
         return bool(__all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, wait_ns, status)));
@@ -269,56 +279,65 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             bool ok = true;
             for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const Item it = item_of(g, i, parts);
-                for (int b = 0; b < nb; ++b, ++n) {
-                    const int s = n % kRing;
-                    if (!(ok = wait_on(&ctl->done[s], ((n / kRing) & 1) ^ 1))) break;
+                // (boxes of 16 rows, or of 64: the rows after the tile's are other experts', whose columns nothing reads)
+                const bool wide = it.cols > 32;
+                const int step = wide ? 64 : 16, boxes = (it.cols + step - 1) / step;
+                for (int u = 0; u < units; ++u, ++n) {
+                    const int s = n % L::RING, count = min(L::UNIT, nb - u * L::UNIT);
+                    if (!(ok = wait_on(&ctl->done[s], ((n / L::RING) & 1) ^ 1))) break;
                     if (elect_one()) {
-                        // (boxes of 16 rows, or of 64: the rows after the tile's are other experts', whose columns nothing reads)
-                        const bool wide = it.cols > 32;
-                        const int step = wide ? 64 : 16, boxes = (it.cols + step - 1) / step;
-                        mbar_expect_tx(&ctl->x_full[s], uint32_t(boxes * step) * 256);
-                        const uint32_t dst = smem_u32(smem) + uint32_t(L::OFF_ACT + s * L::ACT_BYTES);
-                        for (int c = 0; c < boxes; ++c)
+                        mbar_expect_tx(&ctl->x_full[s], uint32_t(count * boxes * step) * 256);
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)
-                                tma_2d(dst + uint32_t(h * (L::ACT_BYTES / 2) + c * step * 128), wide ? &xmap64 : &xmap,
-                                       b * kBlockW + 64 * h, it.tile.row0 * g.terms + c * step, &ctl->x_full[s]);
+                        for (int j = 0; j < L::UNIT; ++j) {
+                            if (j >= count) break;
+                            const uint32_t dst = smem_u32(smem) + uint32_t(L::OFF_ACT + (s * L::UNIT + j) * L::ACT_BYTES);
+                            for (int c = 0; c < boxes; ++c)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    tma_2d(dst + uint32_t(h * (L::ACT_BYTES / 2) + c * step * 128), wide ? &xmap64 : &xmap,
+                                           (u * L::UNIT + j) * kBlockW + 64 * h, it.tile.row0 * g.terms + c * step, &ctl->x_full[s]);
+                        }
                     }
                     __syncwarp();
                 }
             }
             if (lane == 0)
-                for (int j = max(0, n - kRing); j < n; ++j)
-                    mbar_wait_bounded(&ctl->x_full[j % kRing], (j / kRing) & 1, drain_ns(wait_ns), status);
+                for (int j = max(0, n - L::RING); j < n; ++j)
+                    mbar_wait_bounded(&ctl->x_full[j % L::RING], (j / L::RING) & 1, drain_ns(wait_ns), status);
             __syncwarp();
         } else if (warp == W_MMA) {
             // (one lane takes the whole loop, from values that the compiler knows to be uniform)
             if (elect_one()) {
                 const uint64_t x0 = desc_k(smem_u32(smem) + uint32_t(L::OFF_ACT));
                 auto wait_one = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, wait_ns, status); };
-                int n = 0;  // blocks
+                int n = 0;  // units
                 bool ok = true;
                 Columns next(g, parts, items);
                 for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                     const uint32_t idesc = (1u << 4) | (uint32_t(next.take() >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-                    for (int b = 0; b < nb; ++b, ++n) {
-                        const int sx = n % kRing, sd = n % L::DBUFS;
+                    for (int u = 0; u < units; ++u, ++n) {
+                        const int s = n % L::RING, sd = n % L::DRING;
                         // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
                         // its first use counts as over)
-                        const uint32_t pd = ((n / L::DBUFS) & 1) ^ 1, px = (n / kRing) & 1;
-                        const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
-                                   a_there = phase_over(&ctl->a_full[sx], px);
-                        ok = (d_free || wait_one(&ctl->d_empty[sd], pd)) && (x_there || wait_one(&ctl->x_full[sx], px)) &&
-                             (a_there || wait_one(&ctl->a_full[sx], px));
+                        const uint32_t pd = ((n / L::DRING) & 1) ^ 1, px = (n / L::RING) & 1;
+                        const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[s], px),
+                                   a_there = phase_over(&ctl->a_full[s], px);
+                        ok = (d_free || wait_one(&ctl->d_empty[sd], pd)) && (x_there || wait_one(&ctl->x_full[s], px)) &&
+                             (a_there || wait_one(&ctl->a_full[s], px));
                         if (!ok) break;
                         tc_fence_after();
-                        const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4));
-                        const uint32_t d = tmem + uint32_t(sd * COLS), at = tmem + L::A_COL + uint32_t(sx * kACols);
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * (L::ACT_BYTES / 2 >> 4) + 2 * (kk & 3)), idesc,
-                                   kk > 0);
-                        tc_commit(&ctl->done[sx]);
+                        for (int j = 0; j < L::UNIT; ++j) {
+                            if (u * L::UNIT + j >= nb) break;
+                            const uint64_t db = x0 + uint64_t(uint32_t(s * L::UNIT + j) * (L::ACT_BYTES >> 4));
+                            const uint32_t d = tmem + uint32_t((sd * L::UNIT + j) * COLS);
+                            const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols);
+#pragma unroll
+                            for (int kk = 0; kk < 8; ++kk)
+                                mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * (L::ACT_BYTES / 2 >> 4) + 2 * (kk & 3)),
+                                       idesc, kk > 0);
+                        }
+                        tc_commit(&ctl->done[s]);
                     }
                 }
                 tc_commit(&ctl->drain);
@@ -330,42 +349,49 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         const int q = warp & 3, group = (warp - W_DECODE) >> 2;
         // the row of this thread's lane among the stage's 128: gate rows in lanes 0-15, the up rows of the same features above
         const int r = GATE_UP ? (lane < 16 ? 16 * q + lane : 48 + 16 * q + lane) : 32 * q + lane;
-        // This group's blocks are the even or the odd ones of all.  Each group waits for every stage, so that none is ever two
-        // uses of a slot ahead of the other.
-        int n0 = 0, stage0 = 0;  // blocks and stages before the item
+        // This group's units are the even or the odd ones of all.  Each group waits for every stage of codes, so that none is
+        // ever two uses of a slot ahead of the other.
+        constexpr int PER = 4 / L::UNIT, MINE = PER / 2;  // units of a stage, and of them this group's
+        int n0 = 0, stage0 = 0;  // units and stages before the item
         bool ok = true;
-        for (int i = blockIdx.x; ok && i < items; i += gridDim.x, n0 += nb, stage0 += (nb + 3) / 4) {
-            for (int b4 = 0; ok && b4 < nb; b4 += 4) {
-                const int stage = stage0 + b4 / 4, sc = stage % L::CODES;
+        for (int i = blockIdx.x; ok && i < items; i += gridDim.x, n0 += units, stage0 += (nb + 3) / 4) {
+            for (int u0 = 0; ok && u0 < units; u0 += PER) {
+                const int stage = stage0 + u0 / PER, sc = stage % L::CODES;
                 if (!(ok = wait_on(&ctl->c_full[sc], (stage / L::CODES) & 1))) break;
                 const uint8_t *row = smem + sc * kCodeBytes + r * 128;
-                // the (up to two) blocks of this stage that are this group's
-                const int from = (n0 + b4 + group) & 1, count = b4 + from >= nb ? 0 : b4 + from + 2 >= nb || from + 2 > 3 ? 1 : 2;
-                uint4 w[2][2];
+                const int from = (n0 + u0 + group) & 1;  // this group's first unit of the stage
+                uint4 w[MINE][L::UNIT][2];
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
+                for (int t = 0; t < MINE; ++t)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
-                        w[t][j] = *reinterpret_cast<const uint4 *>(row + (((2 * (from + 2 * t) + j) ^ (r & 7)) << 4));
+                    for (int j = 0; j < L::UNIT; ++j)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c)
+                            w[t][j][c] = *reinterpret_cast<const uint4 *>(
+                                row + (((2 * ((from + 2 * t) * L::UNIT + j) + c) ^ (r & 7)) << 4));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->c_empty[sc]);
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    if (t >= count) break;
-                    const int n = n0 + b4 + from + 2 * t, sa = n % kRing;
-                    if (!(ok = wait_on(&ctl->done[sa], ((n / kRing) & 1) ^ 1))) break;
+                for (int t = 0; t < MINE; ++t) {
+                    const int u = u0 + from + 2 * t, n = n0 + u, s = n % L::RING;
+                    if (u >= units) break;
+                    if (!(ok = wait_on(&ctl->done[s], ((n / L::RING) & 1) ^ 1))) break;
                     tc_fence_after();
-                    const uint32_t at = tmem + L::A_COL + uint32_t(sa * kACols) + (uint32_t(q * 32) << 16);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        uint32_t v[32];
-                        decode(w[t][j], v);
-                        tm_st32(at + uint32_t(32 * j), v);
+                    for (int j = 0; j < L::UNIT; ++j) {
+                        if (u * L::UNIT + j >= nb) break;
+                        const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols) + (uint32_t(q * 32) << 16);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t v[32];
+                            decode(w[t][j][c], v);
+                            tm_st32(at + uint32_t(32 * c), v);
+                        }
                     }
                     tm_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&ctl->a_full[sa]);
+                    if (lane == 0) mbar_arrive(&ctl->a_full[s]);
                 }
             }
         }
@@ -374,9 +400,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         const int q = warp & 3, group = (warp - W_SUM) >> 2, col0 = COLS == 128 ? 64 * group : 0;
         const int features = GATE_UP ? g.rows / 2 : g.rows;
         const int step = COLS == 128 ? gridDim.x : 2 * gridDim.x;
-        int n0 = COLS == 128 ? 0 : group * nb, turn = group;  // blocks and (64 columns) items of this CTA before the item
+        int n0 = COLS == 128 ? 0 : group * units, turn = group;  // units and (64 columns) items of this CTA before the item
         bool ok = true;
-        for (int i = COLS == 128 ? blockIdx.x : blockIdx.x + group * gridDim.x; ok && i < items; i += step, n0 += COLS == 128 ? nb : 2 * nb, turn += 2) {
+        for (int i = COLS == 128 ? blockIdx.x : blockIdx.x + group * gridDim.x; ok && i < items; i += step, n0 += COLS == 128 ? units : 2 * units, turn += 2) {
             const Item it = item_of(g, i, parts);
             const int row = it.tile.expert * g.rows + (GATE_UP ? 64 * it.part + 16 * q + (lane & 15) + (lane < 16 ? 0 : g.rows / 2)
                                                               : 128 * it.part + 32 * q + lane);
@@ -399,24 +425,48 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             uint64_t acc[32];  // columns 2 c, 2 c + 1
 #pragma unroll
             for (int c = 0; c < 32; ++c) acc[c] = 0;
-            float dn = __half2float(dp[0]);
-            // (in turn: a group that waited for a block two uses of its accumulator ahead would take the one before for it)
+            float dn[L::UNIT];
+            auto scales_of = [&](int u) {
+#pragma unroll
+                for (int j = 0; j < L::UNIT; ++j) dn[j] = u * L::UNIT + j < nb ? __half2float(dp[u * L::UNIT + j]) : 0.f;
+            };
+            scales_of(0);
+            // (in turn: a group that waited for a unit two uses of its accumulator ahead would take the one before for it)
             if (COLS == 64 && turn > 0 && !(ok = wait_on(&ctl->turn[group], ((turn - 1) >> 1) & 1))) break;
-            for (int b = 0; b < nb; ++b) {
-                const int n = n0 + b, sd = n % L::DBUFS;
-                const uint64_t d = pair(dn, dn);
-                if (b + 1 < nb) dn = __half2float(dp[b + 1]);
-                if (!(ok = wait_on(&ctl->done[n % kRing], (n / kRing) & 1))) break;
+            for (int u = 0; u < units; ++u) {
+                const int n = n0 + u, sd = n % L::DRING;
+                uint64_t d[L::UNIT];
+#pragma unroll
+                for (int j = 0; j < L::UNIT; ++j) d[j] = pair(dn[j], dn[j]);
+                scales_of(u + 1);
+                if (!(ok = wait_on(&ctl->done[n % L::RING], (n / L::RING) & 1))) break;
                 tc_fence_after();
-                const uint32_t at = tmem + uint32_t(sd * COLS + col0) + (uint32_t(q * 32) << 16);
+                const uint32_t at = tmem + uint32_t(sd * L::UNIT * COLS + col0) + (uint32_t(q * 32) << 16);
+                const bool both = u * L::UNIT + L::UNIT <= nb;
+                // 32 values in flight: 32 columns of a block, or 16 of each of two
+                constexpr int W = 32 / L::UNIT;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (col0 + 32 * h < it.cols) {
-                        uint32_t v[32];
-                        tm_ld32(at + uint32_t(32 * h), v);
+                for (int h = 0; h < 64 / W; ++h)
+                    if (col0 + W * h < it.cols) {
+                        uint32_t v[L::UNIT][W];
 #pragma unroll
-                        for (int c = 0; c < 16; ++c)
-                            acc[16 * h + c] = fma2(d, uint64_t(v[2 * c]) | uint64_t(v[2 * c + 1]) << 32, acc[16 * h + c]);
+                        for (int j = 0; j < L::UNIT; ++j) {
+                            if (j > 0 && !both) {
+#pragma unroll
+                                for (int c = 0; c < W; ++c) v[j][c] = 0;
+                            } else {
+                                tm_ld(at + uint32_t(j * COLS + W * h), v[j]);
+                            }
+                        }
+                        tm_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < L::UNIT; ++j) {
+                            tm_tie(v[j]);
+#pragma unroll
+                            for (int c = 0; c < W / 2; ++c)
+                                acc[W / 2 * h + c] =
+                                    fma2(d[j], uint64_t(v[j][2 * c]) | uint64_t(v[j][2 * c + 1]) << 32, acc[W / 2 * h + c]);
+                        }
                     }
                 tc_fence_before();
                 __syncwarp();
