@@ -70,6 +70,13 @@ __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {  // K-major, 128-by
            (uint64_t(2) << 61);
 }
 
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
@@ -144,8 +151,16 @@ __device__ __forceinline__ float second(uint64_t p) { return __uint_as_float(uin
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four words of 16 codes as 32 pairs of binary16 numbers code - 1: pair i of a word is its codes i and i + 8.  They stand at
-// bits 2 i of each half; i < 5 within a binary16's mantissa, the others after a shift by 10.
-__device__ __forceinline__ void decode(const uint4 &w, uint32_t (&r)[32]) {
+// bits 2 i of each half; i < 5 within a binary16's mantissa, the others after a shift by 10.  The exponents are kept in
+// registers: as constants beside the masks they cost an instruction more for each pair.
+struct Exponents {
+    uint32_t e[5];  // of 2^(10 - 2 i), in both halves: a code at bit 2 i counts ones
+    __device__ __forceinline__ Exponents() {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) asm volatile("mov.b32 %0, %1;" : "=r"(e[i]) : "r"((uint32_t(25 - 2 * i) << 10) * 0x10001u));
+    }
+};
+__device__ __forceinline__ void decode(const uint4 &w, const Exponents &x, uint32_t (&r)[32]) {
     const uint32_t word[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -153,8 +168,7 @@ __device__ __forceinline__ void decode(const uint4 &w, uint32_t (&r)[32]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = i < 5 ? i : i - 5;
-            const uint32_t exponent = uint32_t(25 - 2 * e) << 10;  // of 2^(10 - 2 e): a code at bit 2 e counts ones
-            const uint32_t v = ((i < 5 ? word[j] : high) & (0x00030003u << (2 * e))) | exponent | exponent << 16;
+            const uint32_t v = ((i < 5 ? word[j] : high) & (0x00030003u << (2 * e))) | x.e[e];
             const __half2 s = __hsub2(*reinterpret_cast<const __half2 *>(&v), __float2half2_rn(float((1 << (10 - 2 * e)) + 1)));
             r[8 * j + i] = *reinterpret_cast<const uint32_t *>(&s);
         }
@@ -173,6 +187,12 @@ __device__ __forceinline__ bool phase_over(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok;
 }
+
+// Staged rows are copied (and multiplied) by boxes of 16, 32, 64 or 128: index, and rows, of the one that holds `cols`.
+__device__ __forceinline__ int box_of(int cols) { return cols <= 16 ? 0 : cols <= 32 ? 1 : cols <= 64 ? 2 : 3; }
+struct BoxMaps {
+    CUtensorMap map[4];
+};
 
 // An item's place: its tile and its 128 weight rows.
 struct Item {
@@ -208,8 +228,8 @@ __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __ex
 
 template <bool GATE_UP, int COLS>
 __global__ void __launch_bounds__(kThreads, 1)
-moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap xmap,
-                const __grid_constant__ CUtensorMap xmap64, const MoeGemm g, unsigned int *status, uint64_t wait_ns) {
+moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ BoxMaps xmaps, const MoeGemm g,
+                unsigned int *status, uint64_t wait_ns) {
     using L = Shape<COLS>;
     extern __shared__ __align__(1024) uint8_t raw[];
     uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -279,24 +299,16 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             bool ok = true;
             for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const Item it = item_of(g, i, parts);
-                // (boxes of 16 rows, or of 64: the rows after the tile's are other experts', whose columns nothing reads)
-                const bool wide = it.cols > 32;
-                const int step = wide ? 64 : 16, boxes = (it.cols + step - 1) / step;
+                // (one copy a unit, issued by one lane: its issue takes longer than the block's MMAs; the box's rows after the
+                // tile's are other experts', whose columns nothing reads)
+                const int box = uniform(box_of(it.cols)), bytes = (16 << box) * 256 * L::UNIT, row = it.tile.row0 * g.terms;
                 for (int u = 0; u < units; ++u, ++n) {
-                    const int s = n % L::RING, count = min(L::UNIT, nb - u * L::UNIT);
+                    const int s = n % L::RING;
                     if (!(ok = wait_on(&ctl->done[s], ((n / L::RING) & 1) ^ 1))) break;
                     if (elect_one()) {
-                        mbar_expect_tx(&ctl->x_full[s], uint32_t(count * boxes * step) * 256);
-#pragma unroll
-                        for (int j = 0; j < L::UNIT; ++j) {
-                            if (j >= count) break;
-                            const uint32_t dst = smem_u32(smem) + uint32_t(L::OFF_ACT + (s * L::UNIT + j) * L::ACT_BYTES);
-                            for (int c = 0; c < boxes; ++c)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h)
-                                    tma_2d(dst + uint32_t(h * (L::ACT_BYTES / 2) + c * step * 128), wide ? &xmap64 : &xmap,
-                                           (u * L::UNIT + j) * kBlockW + 64 * h, it.tile.row0 * g.terms + c * step, &ctl->x_full[s]);
-                        }
+                        mbar_expect_tx(&ctl->x_full[s], uint32_t(bytes));
+                        tma_3d(smem_u32(smem) + uint32_t(L::OFF_ACT + s * L::UNIT * L::ACT_BYTES), &xmaps.map[box], 0, row,
+                               u * L::UNIT * 2, &ctl->x_full[s]);
                     }
                     __syncwarp();
                 }
@@ -314,7 +326,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 bool ok = true;
                 Columns next(g, parts, items);
                 for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-                    const uint32_t idesc = (1u << 4) | (uint32_t(next.take() >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+                    const int cols = next.take();
+                    const uint32_t idesc = (1u << 4) | (uint32_t(cols >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+                    const uint32_t half = 128u << box_of(cols);  // (in 16 bytes) 64 features of the box's rows
                     for (int u = 0; u < units; ++u, ++n) {
                         const int s = n % L::RING, sd = n % L::DRING;
                         // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
@@ -329,13 +343,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
 #pragma unroll
                         for (int j = 0; j < L::UNIT; ++j) {
                             if (u * L::UNIT + j >= nb) break;
-                            const uint64_t db = x0 + uint64_t(uint32_t(s * L::UNIT + j) * (L::ACT_BYTES >> 4));
+                            const uint64_t db = x0 + uint64_t(uint32_t(s * L::UNIT) * (L::ACT_BYTES >> 4) + 2 * j * half);
                             const uint32_t d = tmem + uint32_t((sd * L::UNIT + j) * COLS);
                             const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols);
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
-                                mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * (L::ACT_BYTES / 2 >> 4) + 2 * (kk & 3)),
-                                       idesc, kk > 0);
+                                mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0);
                         }
                         tc_commit(&ctl->done[s]);
                     }
@@ -351,6 +364,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         const int r = GATE_UP ? (lane < 16 ? 16 * q + lane : 48 + 16 * q + lane) : 32 * q + lane;
         // This group's units are the even or the odd ones of all.  Each group waits for every stage of codes, so that none is
         // ever two uses of a slot ahead of the other.
+        const Exponents exponents;
         constexpr int PER = 4 / L::UNIT, MINE = PER / 2;  // units of a stage, and of them this group's
         int n0 = 0, stage0 = 0;  // units and stages before the item
         bool ok = true;
@@ -384,7 +398,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint32_t v[32];
-                            decode(w[t][j][c], v);
+                            decode(w[t][j][c], exponents, v);
                             tm_st32(at + uint32_t(32 * c), v);
                         }
                     }
@@ -534,13 +548,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
     }
 }
 
-cudaError_t map_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base, int64_t inner, int64_t rows, int64_t row_bytes,
-                   int box_inner, int box_rows, CUtensorMapL2promotion promote) {
+cudaError_t make_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, int rank, const cuuint64_t *dims,
+                     const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapL2promotion promote) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {cuuint64_t(inner), cuuint64_t(rows)}, strides[1] = {cuuint64_t(row_bytes)};
-    const cuuint32_t box[2] = {cuuint32_t(box_inner), cuuint32_t(box_rows)}, step[2] = {1, 1};
-    if (enc(map, type, 2, const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    const cuuint32_t step[3] = {1, 1, 1};
+    if (enc(map, type, cuuint32_t(rank), const_cast<void *>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
             CU_TENSOR_MAP_SWIZZLE_128B, promote, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     return cudaSuccess;
@@ -548,21 +561,26 @@ cudaError_t map_2d(CUtensorMap *map, CUtensorMapDataType type, const void *base,
 
 template <int COLS>
 cudaError_t launch(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
-    CUtensorMap cmap, xmap, xmap64;
-    cudaError_t e = map_2d(&cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.qs, g.k / 4, int64_t(g.experts) * g.rows, g.k / 4, 128, 64,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    for (int box : {16, 64})
-        if (e == cudaSuccess)
-            e = map_2d(box == 16 ? &xmap : &xmap64, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, g.staged, g.k, g.pairs * g.terms,
-                       int64_t(g.k) * 2, 64, box, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    CUtensorMap cmap;
+    BoxMaps xmaps = {};
+    const cuuint64_t cdims[2] = {cuuint64_t(g.k / 4), cuuint64_t(g.experts) * cuuint64_t(g.rows)}, cstrides[1] = {cuuint64_t(g.k / 4)};
+    const cuuint32_t cbox[2] = {128, 64};
+    cudaError_t e = make_map(&cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.qs, 2, cdims, cstrides, cbox, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
+    // [64-feature pieces][rows][64]: a unit's pieces in one copy, each a swizzled operand
+    const cuuint64_t xdims[3] = {64, cuuint64_t(g.pairs * g.terms), cuuint64_t(g.k / 64)};
+    const cuuint64_t xstrides[2] = {cuuint64_t(g.k) * 2, 128};
+    for (int i = 0; 16 << i <= COLS && e == cudaSuccess; ++i) {
+        const cuuint32_t xbox[3] = {64, cuuint32_t(16 << i), 2 * Shape<COLS>::UNIT};
+        e = make_map(&xmaps.map[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, g.staged, 3, xdims, xstrides, xbox,
+                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    }
     if (e != cudaSuccess) return e;
     auto kernel = gate_up ? moe_gemm_kernel<true, COLS> : moe_gemm_kernel<false, COLS>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<COLS>);
     if (e != cudaSuccess) return e;
     const int64_t items = int64_t(g.max_tiles) * (g.rows / 128);
     const unsigned grid = unsigned(std::min<int64_t>(items, ctx.num_sms));
-    return launch_dependent(kernel, dim3(grid), kThreads, kSmem<COLS>, ctx.stream, cmap, xmap, xmap64, g, ctx.status,
-                            ctx.wait_ns);
+    return launch_dependent(kernel, dim3(grid), kThreads, kSmem<COLS>, ctx.stream, cmap, xmaps, g, ctx.status, ctx.wait_ns);
 }
 
 }  // namespace
