@@ -264,9 +264,8 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(MoeArgs a, MoePlan
 
 size_t pad(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Columns of a tile.  With 128 a tile's codes are decoded for twice the tokens; with 64 more warps decode, which is what
-// counts where experts have few.
-int tile_cols(int64_t pairs, int64_t experts, int terms) { return pairs * terms > 64 * std::min(pairs, experts) ? 128 : 64; }
+// Columns of a tile: 96 where experts have more than 64 rows in the mean (fewer decodings), else 64 (units of two blocks).
+int tile_cols(int64_t pairs, int64_t experts, int terms) { return pairs * terms > 64 * std::min(pairs, experts) ? 96 : 64; }
 
 struct Workspace {
     MoePlan plan;

@@ -1,7 +1,7 @@
 // Grouped ternary product of a mixture of experts on the tcgen05 tensor cores:
 //     out[row, f] = sum_k x[row, k] W_e[f, k]   for the rows of each expert e, or silu(gate) * up of two such.
 //
-// Computed transposed, W x^T: an item is 128 weight rows of one expert (the MMA's M) times a tile of up to 128 staged
+// Computed transposed, W x^T: an item is 128 weight rows of one expert (the MMA's M) times a tile of up to 64 or 96 staged
 // rows of its tokens (N, any multiple of 16), so that the codes of an expert are read once for a tile of tokens however
 // few they are.
 //
@@ -13,12 +13,14 @@
 //  * The block scale d stays out of the operands: each 128-weight block is a product of its own (eight MMAs) into one of
 //    two or four accumulators, and d times it is added to the running sums in registers (f32).  So operands are exact, and what
 //    is rounded is the activations' staging and the sums.
-//  * Copies: codes by TMA, 512 weights of 128 rows a stage (64 KB in flight an SM); activations by TMA, 128 features of a
-//    tile's rows a stage.
+//  * Copies: codes by TMA, 512 weights of 128 rows a stage (96 KB in flight an SM); activations by TMA, a unit's features of a
+//    tile's rows in one copy.
 //  * Roles: warp 0 codes, warp 1 MMAs (owns tensor memory), warp 2 activations; two groups of four warps decode every other
-//    unit (of one block, or of two where tiles have 64 columns); two groups scale and sum, each half of the columns, or, where tiles have 64 columns, every other item, so that
-//    one item's end runs under the next one's blocks.  One persistent CTA an SM.  Every wait is bounded; a timeout sets the status word and the
-//    CTA drains its copies and MMAs before it leaves.
+//    unit; two groups scale and sum every other item, so that one item's end (128 rows' activation, staging and stores) runs
+//    under the next one's blocks (shared out by columns instead, the ends were a quarter of a prompt's time).  A unit is one block,
+//    or two where tiles have 64 columns: there the latency of handing a block on is more than its work.
+//    One persistent CTA an SM.  Every wait is bounded; a timeout sets the status word and the CTA drains its copies and
+//    MMAs before it leaves.
 #include <cstdint>
 
 #include "moe.cuh"
@@ -30,40 +32,40 @@ namespace {
 constexpr int kThreads = 640;
 constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4, W_SUM = 12;
 // registers a thread at launch, and of the roles' warpgroups after it (one, two and two of them)
-constexpr int kRegs = 96, kRegsControl = 48, kRegsDecode = 72, kRegsSum = 144;
-static_assert(kRegsControl + 2 * kRegsDecode + 2 * kRegsSum <= 5 * kRegs, "registers");
+constexpr int kRegs = 96;
 constexpr int kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
-constexpr int kBlocks = 4;  // 128-weight blocks on their way: stages of activations, decoded weights
+constexpr int kCodes = 6;   // stages of codes
+constexpr int kBlocks = 4;  // 128-weight blocks decoded, or being multiplied
 constexpr int kACols = kBlockW / 2;
-constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kTmemCols = 512, kACol = 256;
 
 template <int COLS>
 struct Shape {
-    static constexpr int CODES = COLS == 64 ? 8 : 4;              // stages of codes
-    static constexpr int ACT_BYTES = COLS * kBlockW * 2;          // two halves of 64 features
-    // Blocks of a unit, what the roles hand to each other at a time: with few columns a block's work is less than the latency
-    // of handing it on.
-    static constexpr int UNIT = COLS == 64 ? 2 : 1;
-    static constexpr int RING = kBlocks / UNIT, DRING = 256 / COLS / UNIT;
-    static constexpr uint32_t A_COL = 256;
-    static constexpr int OFF_ACT = CODES * kCodeBytes, OFF_CTL = OFF_ACT + kBlocks * ACT_BYTES;
-    static_assert(A_COL + kBlocks * kACols <= kTmemCols && DRING * UNIT * COLS <= A_COL, "TMEM budget");
+    static constexpr int UNIT = COLS == 64 ? 2 : 1;           // blocks that the roles hand to each other at a time
+    static constexpr int RING = kBlocks / UNIT, DRING = 2;    // units in tensor memory: decoded weights, accumulators
+    static constexpr int ACTS = COLS == 64 ? 4 : 5;           // units of activations
+    static constexpr int ACT_BYTES = COLS * kBlockW * 2 * UNIT;
+    static constexpr int REGS_CONTROL = 48, REGS_DECODE = COLS == 64 ? 72 : 56, REGS_SUM = COLS == 64 ? 144 : 160;
+    static constexpr int OFF_ACT = kCodes * kCodeBytes, OFF_CTL = OFF_ACT + ACTS * ACT_BYTES;
+    static_assert(kACol + kBlocks * kACols <= kTmemCols && DRING * UNIT * COLS <= kACol, "TMEM budget");
+    static_assert(REGS_CONTROL + 2 * REGS_DECODE + 2 * REGS_SUM <= 5 * kRegs, "registers");
 };
 
 struct Ctl {
-    uint64_t c_full[8], c_empty[8];
+    uint64_t c_full[kCodes], c_empty[kCodes];
     // by unit
-    uint64_t x_full[kBlocks], a_full[kBlocks];
-    uint64_t done[kBlocks];  // its MMAs have ended: its operands' slots are free and its accumulators are full
+    uint64_t x_full[5], x_empty[5];
+    uint64_t a_full[kBlocks];
+    uint64_t done[kBlocks];  // its MMAs have ended: its decoded weights' slot is free and its accumulators are full
     uint64_t d_empty[2];
-    uint64_t turn[2];  // (64 columns) a summing group may begin its next item: the other has seen all blocks of the one before
+    uint64_t turn[2];  // a summing group may begin its next item: the other has seen all blocks of the one before
     uint64_t drain;
     uint32_t tmem_base;
     int abort;
 };
 template <int COLS>
 constexpr int kSmem = Shape<COLS>::OFF_CTL + int(sizeof(Ctl)) + 1024;
-static_assert(kSmem<64> <= 232448 && kSmem<128> <= 232448, "shared memory budget");
+static_assert(kSmem<64> <= 232448 && kSmem<96> <= 232448, "shared memory budget");
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {  // K-major, 128-byte swizzle: rows 128 B, 8-row groups 1024 B
     return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
@@ -188,8 +190,9 @@ __device__ __forceinline__ bool phase_over(uint64_t *bar, uint32_t parity) {
     return ok;
 }
 
-// Staged rows are copied (and multiplied) by boxes of 16, 32, 64 or 128: index, and rows, of the one that holds `cols`.
+// Staged rows are copied by boxes of 16, 32, 64 or 96: index, and rows, of the one that holds `cols`.
 __device__ __forceinline__ int box_of(int cols) { return cols <= 16 ? 0 : cols <= 32 ? 1 : cols <= 64 ? 2 : 3; }
+__host__ __device__ constexpr int box_rows(int box) { return box < 3 ? 16 << box : 96; }
 struct BoxMaps {
     CUtensorMap map[4];
 };
@@ -237,16 +240,19 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
     const int warp = uniform(int(threadIdx.x >> 5)), lane = threadIdx.x & 31;
     volatile int *abort_flag = &ctl->abort;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < L::CODES; ++s) {
+        for (int s = 0; s < kCodes; ++s) {
             mbar_init(&ctl->c_full[s], 1);
             mbar_init(&ctl->c_empty[s], 8);
         }
-        for (int s = 0; s < L::RING; ++s) {
+        for (int s = 0; s < L::ACTS; ++s) {
             mbar_init(&ctl->x_full[s], 1);
+            mbar_init(&ctl->x_empty[s], 1);
+        }
+        for (int s = 0; s < L::RING; ++s) {
             mbar_init(&ctl->a_full[s], 4);
             mbar_init(&ctl->done[s], 1);
         }
-        for (int s = 0; s < L::DRING; ++s) mbar_init(&ctl->d_empty[s], COLS / 16);
+        for (int s = 0; s < L::DRING; ++s) mbar_init(&ctl->d_empty[s], 4);
         for (int s = 0; s < 2; ++s) mbar_init(&ctl->turn[s], 4);
         mbar_init(&ctl->drain, 1);
         ctl->abort = 0;
@@ -270,7 +276,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
     };
 
     if (warp < W_DECODE) {
-        regs_down<kRegsControl>();
+        regs_down<L::REGS_CONTROL>();
         if (warp == W_CODES) {
             int n = 0;  // stages filled
             bool ok = true;
@@ -279,8 +285,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 const int row = it.tile.expert * g.rows;
                 const int y0 = row + (GATE_UP ? 64 : 128) * it.part, y1 = GATE_UP ? y0 + g.rows / 2 : y0 + 64;
                 for (int k = 0; k < g.k; k += kCodeK, ++n) {
-                    const int s = n % L::CODES;
-                    if (n >= L::CODES && !(ok = wait_on(&ctl->c_empty[s], (n / L::CODES - 1) & 1))) break;
+                    const int s = n % kCodes;
+                    if (n >= kCodes && !(ok = wait_on(&ctl->c_empty[s], (n / kCodes - 1) & 1))) break;
                     if (elect_one()) {
                         mbar_expect_tx(&ctl->c_full[s], kCodeBytes);
                         const uint32_t dst = smem_u32(smem) + uint32_t(s * kCodeBytes);
@@ -291,8 +297,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 }
             }
             if (lane == 0)  // every copy lands before the CTA ends
-                for (int j = max(0, n - L::CODES); j < n; ++j)
-                    mbar_wait_bounded(&ctl->c_full[j % L::CODES], (j / L::CODES) & 1, drain_ns(wait_ns), status);
+                for (int j = max(0, n - kCodes); j < n; ++j)
+                    mbar_wait_bounded(&ctl->c_full[j % kCodes], (j / kCodes) & 1, drain_ns(wait_ns), status);
             __syncwarp();
         } else if (warp == W_ACT) {
             int n = 0;
@@ -301,21 +307,21 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 const Item it = item_of(g, i, parts);
                 // (one copy a unit, issued by one lane: its issue takes longer than the block's MMAs; the box's rows after the
                 // tile's are other experts', whose columns nothing reads)
-                const int box = uniform(box_of(it.cols)), bytes = (16 << box) * 256 * L::UNIT, row = it.tile.row0 * g.terms;
+                const int box = uniform(box_of(it.cols)), bytes = box_rows(box) * 256 * L::UNIT, row = it.tile.row0 * g.terms;
                 for (int u = 0; u < units; ++u, ++n) {
-                    const int s = n % L::RING;
-                    if (!(ok = wait_on(&ctl->done[s], ((n / L::RING) & 1) ^ 1))) break;
+                    const int s = n % L::ACTS;
+                    if (!(ok = wait_on(&ctl->x_empty[s], ((n / L::ACTS) & 1) ^ 1))) break;
                     if (elect_one()) {
                         mbar_expect_tx(&ctl->x_full[s], uint32_t(bytes));
-                        tma_3d(smem_u32(smem) + uint32_t(L::OFF_ACT + s * L::UNIT * L::ACT_BYTES), &xmaps.map[box], 0, row,
+                        tma_3d(smem_u32(smem) + uint32_t(L::OFF_ACT + s * L::ACT_BYTES), &xmaps.map[box], 0, row,
                                u * L::UNIT * 2, &ctl->x_full[s]);
                     }
                     __syncwarp();
                 }
             }
             if (lane == 0)
-                for (int j = max(0, n - L::RING); j < n; ++j)
-                    mbar_wait_bounded(&ctl->x_full[j % L::RING], (j / L::RING) & 1, drain_ns(wait_ns), status);
+                for (int j = max(0, n - L::ACTS); j < n; ++j)
+                    mbar_wait_bounded(&ctl->x_full[j % L::ACTS], (j / L::ACTS) & 1, drain_ns(wait_ns), status);
             __syncwarp();
         } else if (warp == W_MMA) {
             // (one lane takes the whole loop, from values that the compiler knows to be uniform)
@@ -328,29 +334,30 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                     const int cols = next.take();
                     const uint32_t idesc = (1u << 4) | (uint32_t(cols >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-                    const uint32_t half = 128u << box_of(cols);  // (in 16 bytes) 64 features of the box's rows
+                    const uint32_t half = uint32_t(box_rows(box_of(cols))) * 8;  // (in 16 bytes) 64 features of the box's rows
                     for (int u = 0; u < units; ++u, ++n) {
-                        const int s = n % L::RING, sd = n % L::DRING;
+                        const int s = n % L::RING, sx = n % L::ACTS, sd = n % L::DRING;
                         // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
                         // its first use counts as over)
-                        const uint32_t pd = ((n / L::DRING) & 1) ^ 1, px = (n / L::RING) & 1;
-                        const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[s], px),
-                                   a_there = phase_over(&ctl->a_full[s], px);
-                        ok = (d_free || wait_one(&ctl->d_empty[sd], pd)) && (x_there || wait_one(&ctl->x_full[s], px)) &&
-                             (a_there || wait_one(&ctl->a_full[s], px));
+                        const uint32_t pd = ((n / L::DRING) & 1) ^ 1, px = (n / L::ACTS) & 1, pa = (n / L::RING) & 1;
+                        const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
+                                   a_there = phase_over(&ctl->a_full[s], pa);
+                        ok = (d_free || wait_one(&ctl->d_empty[sd], pd)) && (x_there || wait_one(&ctl->x_full[sx], px)) &&
+                             (a_there || wait_one(&ctl->a_full[s], pa));
                         if (!ok) break;
                         tc_fence_after();
 #pragma unroll
                         for (int j = 0; j < L::UNIT; ++j) {
                             if (u * L::UNIT + j >= nb) break;
-                            const uint64_t db = x0 + uint64_t(uint32_t(s * L::UNIT) * (L::ACT_BYTES >> 4) + 2 * j * half);
+                            const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4) + 2 * j * half);
                             const uint32_t d = tmem + uint32_t((sd * L::UNIT + j) * COLS);
-                            const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols);
+                            const uint32_t at = tmem + kACol + uint32_t((s * L::UNIT + j) * kACols);
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
                                 mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0);
                         }
                         tc_commit(&ctl->done[s]);
+                        tc_commit(&ctl->x_empty[sx]);
                     }
                 }
                 tc_commit(&ctl->drain);
@@ -358,7 +365,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             __syncwarp();
         }
     } else if (warp < W_SUM) {
-        regs_down<kRegsDecode>();
+        regs_down<L::REGS_DECODE>();
         const int q = warp & 3, group = (warp - W_DECODE) >> 2;
         // the row of this thread's lane among the stage's 128: gate rows in lanes 0-15, the up rows of the same features above
         const int r = GATE_UP ? (lane < 16 ? 16 * q + lane : 48 + 16 * q + lane) : 32 * q + lane;
@@ -370,8 +377,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         bool ok = true;
         for (int i = blockIdx.x; ok && i < items; i += gridDim.x, n0 += units, stage0 += (nb + 3) / 4) {
             for (int u0 = 0; ok && u0 < units; u0 += PER) {
-                const int stage = stage0 + u0 / PER, sc = stage % L::CODES;
-                if (!(ok = wait_on(&ctl->c_full[sc], (stage / L::CODES) & 1))) break;
+                const int stage = stage0 + u0 / PER, sc = stage % kCodes;
+                if (!(ok = wait_on(&ctl->c_full[sc], (stage / kCodes) & 1))) break;
                 const uint8_t *row = smem + sc * kCodeBytes + r * 128;
                 const int from = (n0 + u0 + group) & 1;  // this group's first unit of the stage
                 uint4 w[MINE][L::UNIT][2];
@@ -394,7 +401,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < L::UNIT; ++j) {
                         if (u * L::UNIT + j >= nb) break;
-                        const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols) + (uint32_t(q * 32) << 16);
+                        const uint32_t at = tmem + kACol + uint32_t((s * L::UNIT + j) * kACols) + (uint32_t(q * 32) << 16);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             uint32_t v[32];
@@ -410,23 +417,22 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             }
         }
     } else {
-        regs_up<kRegsSum>();
-        const int q = warp & 3, group = (warp - W_SUM) >> 2, col0 = COLS == 128 ? 64 * group : 0;
+        regs_up<L::REGS_SUM>();
+        const int q = warp & 3, group = (warp - W_SUM) >> 2;
         const int features = GATE_UP ? g.rows / 2 : g.rows;
-        const int step = COLS == 128 ? gridDim.x : 2 * gridDim.x;
-        int n0 = COLS == 128 ? 0 : group * units, turn = group;  // units and (64 columns) items of this CTA before the item
+        int n0 = group * units, turn = group;  // units and items of this CTA before the item
         bool ok = true;
-        for (int i = COLS == 128 ? blockIdx.x : blockIdx.x + group * gridDim.x; ok && i < items; i += step, n0 += COLS == 128 ? units : 2 * units, turn += 2) {
+        for (int i = blockIdx.x + group * gridDim.x; ok && i < items; i += 2 * gridDim.x, n0 += 2 * units, turn += 2) {
             const Item it = item_of(g, i, parts);
             const int row = it.tile.expert * g.rows + (GATE_UP ? 64 * it.part + 16 * q + (lane & 15) + (lane < 16 ? 0 : g.rows / 2)
                                                               : 128 * it.part + 32 * q + lane);
             const __half *dp = g.d + int64_t(row) * nb;
-            // the scales of this group's rows, two a lane
-            const int r0 = col0 / g.terms, left = it.tile.n - r0;
-            float scale[2], up[2];  // up (gate_up): the power of two that the hidden values are staged with
+            // the scales of the tile's rows, some in each lane
+            const int left = it.tile.n;
+            float scale[COLS / 32], up[COLS / 32];  // up (gate_up): the power of two that the hidden values are staged with
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int at = it.tile.row0 + min(r0 + 32 * j + lane, it.tile.n - 1);
+            for (int j = 0; j < COLS / 32; ++j) {
+                const int at = it.tile.row0 + min(32 * j + lane, left - 1);
                 scale[j] = g.scale[at];
                 if (GATE_UP) {
                     // |gate|, |up| <= bound * sum < 2^(e + 1), so that a hidden value times 2^(13 - 2 e) is below 2^15
@@ -436,9 +442,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                     if (it.part == 0 && q == 0) g.scale_out[at] = moe_power(-e);
                 }
             }
-            uint64_t acc[32];  // columns 2 c, 2 c + 1
+            uint64_t acc[COLS / 2];  // columns 2 c, 2 c + 1
 #pragma unroll
-            for (int c = 0; c < 32; ++c) acc[c] = 0;
+            for (int c = 0; c < COLS / 2; ++c) acc[c] = 0;
             float dn[L::UNIT];
             auto scales_of = [&](int u) {
 #pragma unroll
@@ -446,7 +452,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             };
             scales_of(0);
             // (in turn: a group that waited for a unit two uses of its accumulator ahead would take the one before for it)
-            if (COLS == 64 && turn > 0 && !(ok = wait_on(&ctl->turn[group], ((turn - 1) >> 1) & 1))) break;
+            if (turn > 0 && !(ok = wait_on(&ctl->turn[group], ((turn - 1) >> 1) & 1))) break;
             for (int u = 0; u < units; ++u) {
                 const int n = n0 + u, sd = n % L::DRING;
                 uint64_t d[L::UNIT];
@@ -455,13 +461,13 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 scales_of(u + 1);
                 if (!(ok = wait_on(&ctl->done[n % L::RING], (n / L::RING) & 1))) break;
                 tc_fence_after();
-                const uint32_t at = tmem + uint32_t(sd * L::UNIT * COLS + col0) + (uint32_t(q * 32) << 16);
+                const uint32_t at = tmem + uint32_t(sd * L::UNIT * COLS) + (uint32_t(q * 32) << 16);
                 const bool both = u * L::UNIT + L::UNIT <= nb;
                 // 32 values in flight: 32 columns of a block, or 16 of each of two
                 constexpr int W = 32 / L::UNIT;
 #pragma unroll
-                for (int h = 0; h < 64 / W; ++h)
-                    if (col0 + W * h < it.cols) {
+                for (int h = 0; h < COLS / W; ++h)
+                    if (W * h < it.cols) {
                         uint32_t v[L::UNIT][W];
 #pragma unroll
                         for (int j = 0; j < L::UNIT; ++j) {
@@ -487,19 +493,19 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 if (lane == 0) mbar_arrive(&ctl->d_empty[sd]);
             }
             if (!ok) break;
-            if (COLS == 64 && lane == 0) mbar_arrive(&ctl->turn[group ^ 1]);
+            if (lane == 0) mbar_arrive(&ctl->turn[group ^ 1]);
             auto finish = [&](auto two) {
                 constexpr int S = decltype(two)::value;
-                // row c of the group: column c, or the sum of columns 2 c and 2 c + 1 (terms)
+                // row c of the tile: column c, or the sum of columns 2 c and 2 c + 1 (terms)
                 auto sum = [&](int c) {
                     return S == 2 ? first(acc[c]) + second(acc[c]) : c & 1 ? second(acc[c >> 1]) : first(acc[c >> 1]);
                 };
                 if (GATE_UP) {
                     // this lane's place in a staged row
-                    __half *out = g.staged_out + int64_t(it.tile.row0 + r0) * S * features + 64 * it.part + 16 * q + moe_place(lane & 15);
+                    __half *out = g.staged_out + int64_t(it.tile.row0) * S * features + 64 * it.part + 16 * q + moe_place(lane & 15);
                     const int odd = lane >= 16;
 #pragma unroll
-                    for (int c0 = 0; c0 < 64 / S; c0 += 8)
+                    for (int c0 = 0; c0 < COLS / S; c0 += 8)
                         if (c0 < left) {
 #pragma unroll
                             for (int c = c0; c < c0 + 8; c += 2) {
@@ -518,9 +524,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                             }
                         }
                 } else {
-                    float *out = g.out + int64_t(it.tile.row0 + r0) * features + 128 * it.part + 32 * q + lane;
+                    float *out = g.out + int64_t(it.tile.row0) * features + 128 * it.part + 32 * q + lane;
 #pragma unroll
-                    for (int c0 = 0; c0 < 64 / S; c0 += 8)
+                    for (int c0 = 0; c0 < COLS / S; c0 += 8)
                         if (c0 < left) {
 #pragma unroll
                             for (int c = c0; c < c0 + 8; ++c) {
@@ -569,8 +575,8 @@ cudaError_t launch(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
     // [64-feature pieces][rows][64]: a unit's pieces in one copy, each a swizzled operand
     const cuuint64_t xdims[3] = {64, cuuint64_t(g.pairs * g.terms), cuuint64_t(g.k / 64)};
     const cuuint64_t xstrides[2] = {cuuint64_t(g.k) * 2, 128};
-    for (int i = 0; 16 << i <= COLS && e == cudaSuccess; ++i) {
-        const cuuint32_t xbox[3] = {64, cuuint32_t(16 << i), 2 * Shape<COLS>::UNIT};
+    for (int i = 0; i < 4 && box_rows(i) <= COLS && e == cudaSuccess; ++i) {
+        const cuuint32_t xbox[3] = {64, cuuint32_t(box_rows(i)), 2 * Shape<COLS>::UNIT};
         e = make_map(&xmaps.map[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, g.staged, 3, xdims, xstrides, xbox,
                      CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
     }
@@ -586,7 +592,7 @@ cudaError_t launch(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
 }  // namespace
 
 cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
-    return g.cols == 64 ? launch<64>(g, gate_up, ctx) : launch<128>(g, gate_up, ctx);
+    return g.cols == 64 ? launch<64>(g, gate_up, ctx) : launch<96>(g, gate_up, ctx);
 }
 
 }  // namespace tq2
