@@ -45,7 +45,7 @@ struct Shape {
     static constexpr int RING = kBlocks / UNIT, DRING = 2;    // units in tensor memory: decoded weights, accumulators
     static constexpr int ACTS = COLS == 64 ? 4 : 5;           // units of activations
     static constexpr int ACT_BYTES = COLS * kBlockW * 2 * UNIT;
-    static constexpr int REGS_CONTROL = 48, REGS_DECODE = COLS == 64 ? 72 : 56, REGS_SUM = COLS == 64 ? 144 : 160;
+    static constexpr int REGS_CONTROL = 48, REGS_DECODE = COLS == 64 ? 88 : 56, REGS_SUM = COLS == 64 ? 128 : 160;
     static constexpr int OFF_ACT = kCodes * kCodeBytes, OFF_CTL = OFF_ACT + ACTS * ACT_BYTES;
     static_assert(kACol + kBlocks * kACols <= kTmemCols && DRING * UNIT * COLS <= kACol, "TMEM budget");
     static_assert(REGS_CONTROL + 2 * REGS_DECODE + 2 * REGS_SUM <= 5 * kRegs, "registers");
@@ -118,15 +118,12 @@ __device__ __forceinline__ void tm_tie(uint32_t (&r)[N]) {
     for (int i = 0; i < N; i += 8)
         asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
 }
-__device__ __forceinline__ void tm_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
 template <int N>
@@ -152,7 +149,7 @@ __device__ __forceinline__ float first(uint64_t p) { return __uint_as_float(uint
 __device__ __forceinline__ float second(uint64_t p) { return __uint_as_float(uint32_t(p >> 32)); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Four words of 16 codes as 32 pairs of binary16 numbers code - 1: pair i of a word is its codes i and i + 8.  They stand at
+// Two words of 16 codes as 16 pairs of binary16 numbers code - 1: pair i of a word is its codes i and i + 8.  They stand at
 // bits 2 i of each half; i < 5 within a binary16's mantissa, the others after a shift by 10.  The exponents are kept in
 // registers: as constants beside the masks they cost an instruction more for each pair.
 struct Exponents {
@@ -162,15 +159,16 @@ struct Exponents {
         for (int i = 0; i < 5; ++i) asm volatile("mov.b32 %0, %1;" : "=r"(e[i]) : "r"((uint32_t(25 - 2 * i) << 10) * 0x10001u));
     }
 };
-__device__ __forceinline__ void decode(const uint4 &w, const Exponents &x, uint32_t (&r)[32]) {
-    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+__device__ __forceinline__ void decode(uint32_t w0, uint32_t w1, const Exponents &x, uint32_t (&r)[16]) {
+    const uint32_t word[2] = {w0, w1};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
         const uint32_t high = word[j] >> 10;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int e = i < 5 ? i : i - 5;
-            const uint32_t v = ((i < 5 ? word[j] : high) & (0x00030003u << (2 * e))) | x.e[e];
+            uint32_t v;  // codes & mask | exponent
+            asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(i < 5 ? word[j] : high), "r"(0x00030003u << (2 * e)), "r"(x.e[e]));
             const __half2 s = __hsub2(*reinterpret_cast<const __half2 *>(&v), __float2half2_rn(float((1 << (10 - 2 * e)) + 1)));
             r[8 * j + i] = *reinterpret_cast<const uint32_t *>(&s);
         }
@@ -404,9 +402,12 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                         const uint32_t at = tmem + kACol + uint32_t((s * L::UNIT + j) * kACols) + (uint32_t(q * 32) << 16);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            uint32_t v[32];
-                            decode(w[t][j][c], exponents, v);
-                            tm_st32(at + uint32_t(32 * c), v);
+                            // (stores of 16 registers: of 32, the next ones waited for these to be read)
+                            uint32_t v[2][16];
+                            decode(w[t][j][c].x, w[t][j][c].y, exponents, v[0]);
+                            tm_st16(at + uint32_t(32 * c), v[0]);
+                            decode(w[t][j][c].z, w[t][j][c].w, exponents, v[1]);
+                            tm_st16(at + uint32_t(32 * c + 16), v[1]);
                         }
                     }
                     tm_wait_st();
