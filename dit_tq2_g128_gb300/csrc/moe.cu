@@ -264,8 +264,12 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(MoeArgs a, MoePlan
 
 size_t pad(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Columns of a tile: 96 where experts have more than 64 rows in the mean (fewer decodings), else 64 (units of two blocks).
-int tile_cols(int64_t pairs, int64_t experts, int terms) { return pairs * terms > 64 * std::min(pairs, experts) ? 96 : 64; }
+// Columns of a tile, by the rows that experts have in the mean: with more columns codes are decoded less often, with fewer
+// there is room for more decoded weights and more warps that decode.
+int tile_cols(int64_t pairs, int64_t experts, int terms) {
+    const int64_t rows = pairs * terms, active = std::min(pairs, experts);
+    return rows <= 16 * active ? 32 : rows <= 64 * active ? 64 : 96;
+}
 
 struct Workspace {
     MoePlan plan;
@@ -284,7 +288,7 @@ struct Workspace {
         const int64_t tile_rows = cols / terms;
         max_tiles = int(std::min(pairs, experts) + pairs / tile_rows);  // each expert leaves less than one unfilled
         take(plan.tile_count, 1);
-        take(plan.tiles, size_t(std::min(pairs, experts) + pairs / (64 / terms)));
+        take(plan.tiles, size_t(std::min(pairs, experts) + pairs / (32 / terms)));
         take(plan.pair_row, size_t(pairs));
         take(plan.expert_rows, size_t(experts));
         take(plan.bound, size_t(experts));

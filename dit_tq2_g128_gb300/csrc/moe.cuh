@@ -36,7 +36,7 @@ struct MoeGemm {
     int64_t pairs;
     int experts, rows, k;
     int terms;           // staged rows of a row
-    int cols;            // staged rows (MMA columns) of a tile, at most: 64 or 96
+    int cols;            // staged rows (MMA columns) of a tile, at most: 32, 64 or 96
     int max_tiles;
 };
 // gate_up: rows counts gate then up rows, and the SwiGLU of rows / 2 features is staged; else out is the product.

@@ -1,8 +1,8 @@
 // Grouped ternary product of a mixture of experts on the tcgen05 tensor cores:
 //     out[row, f] = sum_k x[row, k] W_e[f, k]   for the rows of each expert e, or silu(gate) * up of two such.
 //
-// Computed transposed, W x^T: an item is 128 weight rows of one expert (the MMA's M) times a tile of up to 64 or 96 staged
-// rows of its tokens (N, any multiple of 16), so that the codes of an expert are read once for a tile of tokens however
+// Computed transposed, W x^T: an item is 128 weight rows of one expert (the MMA's M) times a tile of up to 32, 64 or 96
+// staged rows of its tokens (N, any multiple of 16), so that the codes of an expert are read once for a tile of tokens however
 // few they are.
 //
 //  * The weights never touch shared memory decoded.  A thread takes one weight row, masks pairs of codes c out of its
@@ -15,10 +15,10 @@
 //    is rounded is the activations' staging and the sums.
 //  * Copies: codes by TMA, 512 weights of 128 rows a stage (96 KB in flight an SM); activations by TMA, a unit's features of a
 //    tile's rows in one copy.
-//  * Roles: warp 0 codes, warp 1 MMAs (owns tensor memory), warp 2 activations; two groups of four warps decode every other
-//    unit; two groups scale and sum every other item, so that one item's end (128 rows' activation, staging and stores) runs
+//  * Roles: warp 0 codes, warp 1 MMAs (owns tensor memory), warp 2 activations; two or three groups of four warps
+//    decode a unit each in turn; two groups scale and sum every other item, so that one item's end (128 rows' activation, staging and stores) runs
 //    under the next one's blocks (shared out by columns instead, the ends were a quarter of a prompt's time).  A unit is one block,
-//    or two where tiles have 64 columns: there the latency of handing a block on is more than its work.
+//    or two where tiles have few columns: there the latency of handing a block on is more than its work.
 //    One persistent CTA an SM.  Every wait is bounded; a timeout sets the status word and the CTA drains its copies and
 //    MMAs before it leaves.
 #include <cstdint>
@@ -29,34 +29,37 @@
 namespace tq2 {
 namespace {
 
-constexpr int kThreads = 640;
-constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4, W_SUM = 12;
-// registers a thread at launch, and of the roles' warpgroups after it (one, two and two of them)
-constexpr int kRegs = 96;
+constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4;
 constexpr int kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
 constexpr int kCodes = 6;   // stages of codes
-constexpr int kBlocks = 4;  // 128-weight blocks decoded, or being multiplied
 constexpr int kACols = kBlockW / 2;
-constexpr uint32_t kTmemCols = 512, kACol = 256;
+constexpr uint32_t kTmemCols = 512;
 
 template <int COLS>
 struct Shape {
-    static constexpr int UNIT = COLS == 64 ? 2 : 1;           // blocks that the roles hand to each other at a time
-    static constexpr int RING = kBlocks / UNIT, DRING = 2;    // units in tensor memory: decoded weights, accumulators
-    static constexpr int ACTS = COLS == 64 ? 4 : 5;           // units of activations
+    static constexpr int UNIT = COLS == 96 ? 1 : 2;          // blocks that the roles hand to each other at a time
+    static constexpr int RING = COLS == 32 ? 3 : 4 / UNIT;   // units decoded, or being multiplied
+    static constexpr int DRING = 2;                          // units of accumulators
+    static constexpr int ACTS = COLS == 32 ? 8 : COLS == 64 ? 4 : 5;  // units of activations
     static constexpr int ACT_BYTES = COLS * kBlockW * 2 * UNIT;
-    static constexpr int REGS_CONTROL = 48, REGS_DECODE = COLS == 64 ? 88 : 56, REGS_SUM = COLS == 64 ? 128 : 160;
+    static constexpr int DECODERS = COLS == 32 ? 3 : 2;      // groups of four warps
+    static constexpr int W_SUM = W_DECODE + 4 * DECODERS, THREADS = 32 * (W_SUM + 8);
+    // registers a thread at launch, and of the roles' warpgroups after it
+    static constexpr int REGS = COLS == 32 ? 80 : 96;
+    static constexpr int REGS_CONTROL = COLS == 32 ? 40 : 48, REGS_DECODE = COLS == 32 ? 80 : COLS == 64 ? 88 : 56;
+    static constexpr int REGS_SUM = COLS == 32 ? 96 : COLS == 64 ? 128 : 160;
     static constexpr int OFF_ACT = kCodes * kCodeBytes, OFF_CTL = OFF_ACT + ACTS * ACT_BYTES;
-    static_assert(kACol + kBlocks * kACols <= kTmemCols && DRING * UNIT * COLS <= kACol, "TMEM budget");
-    static_assert(REGS_CONTROL + 2 * REGS_DECODE + 2 * REGS_SUM <= 5 * kRegs, "registers");
+    static constexpr uint32_t A_COL = DRING * UNIT * COLS;
+    static_assert(A_COL + RING * UNIT * kACols <= kTmemCols, "TMEM budget");
+    static_assert(REGS_CONTROL + DECODERS * REGS_DECODE + 2 * REGS_SUM <= (3 + DECODERS) * REGS, "registers");
 };
 
 struct Ctl {
     uint64_t c_full[kCodes], c_empty[kCodes];
     // by unit
-    uint64_t x_full[5], x_empty[5];
-    uint64_t a_full[kBlocks];
-    uint64_t done[kBlocks];  // its MMAs have ended: its decoded weights' slot is free and its accumulators are full
+    uint64_t x_full[8], x_empty[8];
+    uint64_t a_full[4];
+    uint64_t done[4];  // its MMAs have ended: its decoded weights' slot is free and its accumulators are full
     uint64_t d_empty[2];
     uint64_t turn[2];  // a summing group may begin its next item: the other has seen all blocks of the one before
     uint64_t drain;
@@ -65,7 +68,7 @@ struct Ctl {
 };
 template <int COLS>
 constexpr int kSmem = Shape<COLS>::OFF_CTL + int(sizeof(Ctl)) + 1024;
-static_assert(kSmem<64> <= 232448 && kSmem<96> <= 232448, "shared memory budget");
+static_assert(kSmem<32> <= 232448 && kSmem<64> <= 232448 && kSmem<96> <= 232448, "shared memory budget");
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {  // K-major, 128-byte swizzle: rows 128 B, 8-row groups 1024 B
     return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
@@ -228,7 +231,7 @@ struct Columns {
 __device__ __forceinline__ float silu(float x) { return __fdividef(x, 1.f + __expf(-x)); }
 
 template <bool GATE_UP, int COLS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Shape<COLS>::THREADS, 1)
 moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ BoxMaps xmaps, const MoeGemm g,
                 unsigned int *status, uint64_t wait_ns) {
     using L = Shape<COLS>;
@@ -240,7 +243,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int s = 0; s < kCodes; ++s) {
             mbar_init(&ctl->c_full[s], 1);
-            mbar_init(&ctl->c_empty[s], 8);
+            mbar_init(&ctl->c_empty[s], 4 * L::DECODERS);
         }
         for (int s = 0; s < L::ACTS; ++s) {
             mbar_init(&ctl->x_full[s], 1);
@@ -349,7 +352,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                             if (u * L::UNIT + j >= nb) break;
                             const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4) + 2 * j * half);
                             const uint32_t d = tmem + uint32_t((sd * L::UNIT + j) * COLS);
-                            const uint32_t at = tmem + kACol + uint32_t((s * L::UNIT + j) * kACols);
+                            const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols);
 #pragma unroll
                             for (int kk = 0; kk < 8; ++kk)
                                 mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0);
@@ -362,15 +365,15 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             }
             __syncwarp();
         }
-    } else if (warp < W_SUM) {
+    } else if (warp < L::W_SUM) {
         regs_down<L::REGS_DECODE>();
         const int q = warp & 3, group = (warp - W_DECODE) >> 2;
         // the row of this thread's lane among the stage's 128: gate rows in lanes 0-15, the up rows of the same features above
         const int r = GATE_UP ? (lane < 16 ? 16 * q + lane : 48 + 16 * q + lane) : 32 * q + lane;
-        // This group's units are the even or the odd ones of all.  Each group waits for every stage of codes, so that none is
-        // ever two uses of a slot ahead of the other.
+        // This group's units are every other one, or third, of all.  Each group waits for every stage of codes, so that none is
+        // ever two uses of a slot ahead of another.
         const Exponents exponents;
-        constexpr int PER = 4 / L::UNIT, MINE = PER / 2;  // units of a stage, and of them this group's
+        constexpr int DEC = L::DECODERS, PER = 4 / L::UNIT, MINE = (PER + DEC - 1) / DEC;  // units of a stage, and of them a group's
         int n0 = 0, stage0 = 0;  // units and stages before the item
         bool ok = true;
         for (int i = blockIdx.x; ok && i < items; i += gridDim.x, n0 += units, stage0 += (nb + 3) / 4) {
@@ -378,7 +381,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 const int stage = stage0 + u0 / PER, sc = stage % kCodes;
                 if (!(ok = wait_on(&ctl->c_full[sc], (stage / kCodes) & 1))) break;
                 const uint8_t *row = smem + sc * kCodeBytes + r * 128;
-                const int from = (n0 + u0 + group) & 1;  // this group's first unit of the stage
+                const int from = (group + DEC - (n0 + u0) % DEC) % DEC;  // this group's first unit of the stage (or of a later one)
                 uint4 w[MINE][L::UNIT][2];
 #pragma unroll
                 for (int t = 0; t < MINE; ++t)
@@ -387,19 +390,19 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
 #pragma unroll
                         for (int c = 0; c < 2; ++c)
                             w[t][j][c] = *reinterpret_cast<const uint4 *>(
-                                row + (((2 * ((from + 2 * t) * L::UNIT + j) + c) ^ (r & 7)) << 4));
+                                row + (((2 * (min(from + DEC * t, PER - 1) * L::UNIT + j) + c) ^ (r & 7)) << 4));
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->c_empty[sc]);
 #pragma unroll
                 for (int t = 0; t < MINE; ++t) {
-                    const int u = u0 + from + 2 * t, n = n0 + u, s = n % L::RING;
-                    if (u >= units) break;
+                    const int u = u0 + from + DEC * t, n = n0 + u, s = n % L::RING;
+                    if (from + DEC * t >= PER || u >= units) break;
                     if (!(ok = wait_on(&ctl->done[s], ((n / L::RING) & 1) ^ 1))) break;
                     tc_fence_after();
 #pragma unroll
                     for (int j = 0; j < L::UNIT; ++j) {
                         if (u * L::UNIT + j >= nb) break;
-                        const uint32_t at = tmem + kACol + uint32_t((s * L::UNIT + j) * kACols) + (uint32_t(q * 32) << 16);
+                        const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols) + (uint32_t(q * 32) << 16);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
                             // (stores of 16 registers: of 32, the next ones waited for these to be read)
@@ -419,7 +422,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
         }
     } else {
         regs_up<L::REGS_SUM>();
-        const int q = warp & 3, group = (warp - W_SUM) >> 2;
+        const int q = warp & 3, group = (warp - L::W_SUM) >> 2;
         const int features = GATE_UP ? g.rows / 2 : g.rows;
         int n0 = group * units, turn = group;  // units and items of this CTA before the item
         bool ok = true;
@@ -587,13 +590,13 @@ cudaError_t launch(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
     if (e != cudaSuccess) return e;
     const int64_t items = int64_t(g.max_tiles) * (g.rows / 128);
     const unsigned grid = unsigned(std::min<int64_t>(items, ctx.num_sms));
-    return launch_dependent(kernel, dim3(grid), kThreads, kSmem<COLS>, ctx.stream, cmap, xmaps, g, ctx.status, ctx.wait_ns);
+    return launch_dependent(kernel, dim3(grid), Shape<COLS>::THREADS, kSmem<COLS>, ctx.stream, cmap, xmaps, g, ctx.status, ctx.wait_ns);
 }
 
 }  // namespace
 
 cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
-    return g.cols == 64 ? launch<64>(g, gate_up, ctx) : launch<96>(g, gate_up, ctx);
+    return g.cols == 32 ? launch<32>(g, gate_up, ctx) : g.cols == 64 ? launch<64>(g, gate_up, ctx) : launch<96>(g, gate_up, ctx);
 }
 
 }  // namespace tq2
