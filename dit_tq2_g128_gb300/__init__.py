@@ -156,10 +156,11 @@ def _ptr(t):
 
 _torch = None
 _current_raw_stream = None
+_current_device = None
 
 
 def _stream(stream):
-    global _torch, _current_raw_stream
+    global _torch, _current_raw_stream, _current_device
     if stream is None:
         if _torch is None:
             try:
@@ -167,13 +168,16 @@ def _stream(stream):
             except ImportError:  # pragma: no cover
                 return None
             _torch = torch
-            # the raw handle without a Stream object around it (4 us of a call otherwise)
-            _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if _current_device is None:
+            # the raw handle without a Stream object around it (4 us of a call otherwise), and the device without its own
+            # check of what is_initialized has said (1 us)
+            _current_raw_stream = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+            _current_device = getattr(_torch._C, "_cuda_getDevice", _torch.cuda.current_device)
         cuda = _torch.cuda
         if not cuda.is_initialized():
             return None
         if _current_raw_stream is not None:
-            return _current_raw_stream(cuda.current_device())
+            return _current_raw_stream(_current_device())
         return cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -646,23 +650,41 @@ def _given(t, name: str, dtype, shape) -> int:
     return t.data_ptr()
 
 
+def _made(t, name: str, dtype, shape, like, stream):
+    """(tensor, pointer): t, checked, or a new tensor of this type and shape."""
+    if t is not None:
+        return t, _given(t, name, dtype, shape)
+    if stream is None:
+        t = _torch.empty(shape, dtype=dtype, device=like.device)
+    else:
+        with _on(stream):
+            t = _torch.empty(shape, dtype=dtype, device=like.device)
+    return t, t.data_ptr()
+
+
+def _types():
+    """torch's int32, int64 and float32 (torch is imported by whoever holds tensors)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.int32, _torch.int64, _torch.float32
+
+
 def moe_route(logits, top_k: int, *, sigmoid: bool = False, normalize: bool = True, scale: float = 1.0, experts=None,
               weights=None, stream=None):
     """The ``top_k`` experts of each token by the router's logits [tokens, experts] (float32, float16 or bfloat16; rows
     of any stride), and their weights: softmax or ``sigmoid`` scores, over their sum if ``normalize``, times ``scale``.
     Returns int32 and float32 tensors [tokens, top_k] (``experts`` and ``weights`` if given); see tq2_moe_route."""
-    import torch
     tokens, n, stride, dtype = _rows(logits, "logits")
+    i32, _, f32 = _types()
     shape = (tokens, top_k)
-    if experts is None or weights is None:
-        with _on(stream):
-            if experts is None:
-                experts = torch.empty(shape, dtype=torch.int32, device=logits.device)
-            if weights is None:
-                weights = torch.empty(shape, dtype=torch.float32, device=logits.device)
-    tq2_moe_route(logits.data_ptr(), dtype, stride, _given(experts, "experts", torch.int32, shape),
-                  _given(weights, "weights", torch.float32, shape), tokens, n, top_k, int(sigmoid), int(normalize), scale,
-                  stream)
+    experts, ep = _made(experts, "experts", i32, shape, logits, stream)
+    weights, wp = _made(weights, "weights", f32, shape, logits, stream)
+    status = lib.tq2_moe_route(logits.data_ptr(), dtype, stride, ep, wp, tokens, n, top_k, sigmoid, normalize, scale,
+                               _stream(stream))
+    if status:
+        raise TQ2Error(status, "tq2_moe_route")
     return experts, weights
 
 
@@ -694,20 +716,21 @@ def moe_swiglu(layer: Experts, x, expert, weight, *, residual=None, out=None, wo
     """A mixture-of-experts layer on tokens x [tokens, width] (float32, float16 or bfloat16), routed to ``expert`` (int32
     [tokens, top_k]; -1: none) with ``weight`` (float32): the weighted sum of their SwiGLU products (+ residual).
     Returns ``out`` (default: a new tensor; it may be the residual)."""
-    import torch
     tokens, width, stride, dtype = _rows(x, "x")
     if width != layer.width or (stride != width and tokens > 1):
         raise ValueError(f"x must be a contiguous tensor [tokens, {layer.width}], got {tuple(x.shape)}")
-    if expert.dim() != 2 or expert.shape[0] != tokens:
-        raise ValueError(f"expert must be [{tokens}, top_k], got {tuple(expert.shape)}")
-    if out is None:
-        with _on(stream):
-            out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    tq2_moe_swiglu(layer.packed, x.data_ptr(), _given(expert, "expert", torch.int32, expert.shape),
-                   _given(weight, "weight", torch.float32, expert.shape),
-                   None if residual is None else _given(residual, "residual", x.dtype, x.shape),
-                   _given(out, "out", x.dtype, x.shape), dtype, tokens, expert.shape[1], workspace,
-                   0 if workspace is None else workspace.numel(), stream)
+    routed = expert.shape
+    if len(routed) != 2 or routed[0] != tokens:
+        raise ValueError(f"expert must be [{tokens}, top_k], got {tuple(routed)}")
+    i32, _, f32 = _types()
+    out, op = _made(out, "out", x.dtype, x.shape, x, stream)
+    status = lib.tq2_moe_swiglu(layer.packed, x.data_ptr(), _given(expert, "expert", i32, routed),
+                                _given(weight, "weight", f32, routed),
+                                None if residual is None else _given(residual, "residual", x.dtype, x.shape), op, dtype,
+                                tokens, routed[1], None if workspace is None else workspace.data_ptr(),
+                                0 if workspace is None else workspace.numel(), _stream(stream))
+    if status:
+        raise TQ2Error(status, "tq2_moe_swiglu")
     return out
 
 
@@ -716,19 +739,17 @@ def sample(logits, u, *, temperature=None, top_k=None, top_p=None, min_p=None, o
     ``u`` (float32 [rows], in [0, 1)).  The filters are CUDA tensors [rows] (float32, top_k int32), None where off.
     Returns int64 tokens and the float32 probabilities with which they were drawn, [rows] each (``out`` and ``prob`` if
     given); see tq2_sample."""
-    import torch
     rows, vocab, stride, dtype = _rows(logits, "logits")
-    shape, f32 = (rows,), torch.float32
-    if out is None or prob is None:
-        with _on(stream):
-            if out is None:
-                out = torch.empty(shape, dtype=torch.int64, device=logits.device)
-            if prob is None:
-                prob = torch.empty(shape, dtype=f32, device=logits.device)
+    i32, i64, f32 = _types()
+    shape = (rows,)
+    out, op = _made(out, "out", i64, shape, logits, stream)
+    prob, pp = _made(prob, "prob", f32, shape, logits, stream)
     filters = tq2_sampling(None if temperature is None else _given(temperature, "temperature", f32, shape),
-                           None if top_k is None else _given(top_k, "top_k", torch.int32, shape),
+                           None if top_k is None else _given(top_k, "top_k", i32, shape),
                            None if top_p is None else _given(top_p, "top_p", f32, shape),
                            None if min_p is None else _given(min_p, "min_p", f32, shape))
-    tq2_sample(logits.data_ptr(), dtype, stride, _given(u, "u", f32, shape), filters,
-               _given(out, "out", torch.int64, shape), _given(prob, "prob", f32, shape), rows, vocab, stream)
+    status = lib.tq2_sample(logits.data_ptr(), dtype, stride, _given(u, "u", f32, shape), filters, op, pp, rows, vocab,
+                            _stream(stream))
+    if status:
+        raise TQ2Error(status, "tq2_sample")
     return out, prob
