@@ -7,6 +7,8 @@
 // the same bits on every call.
 #include <cstdint>
 
+#include <cuda_fp8.h>
+
 #include "dtype.cuh"
 #include "moe.cuh"
 #include "paged_attention.cuh"
@@ -105,7 +107,10 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
             plan.expert_rows[tid] = total;
             plan.bound[tid] = 0;
         }
-        if (tid == 0) *plan.tile_count = tiles;
+        if (tid == 0) {
+            plan.tile_count[0] = tiles;
+            plan.tile_count[1] = rows;
+        }
     }
     __syncthreads();
     for (int p0 = first + tid; p0 < last; p0 += U * kPlanThreads) {
@@ -125,7 +130,7 @@ constexpr int kBoundScales = 8192;  // block scales of a block that looks for th
 
 struct StageArgs {
     MoePlan plan;
-    __half *staged;  // [pairs][terms][k]
+    void *staged;    // [pairs][terms][k]
     float *scale;    // [pairs]
     float *sum;      // [pairs] of |x|, not below it
     const __half *d;
@@ -135,11 +140,12 @@ struct StageArgs {
     int k, top_k, terms, experts;
 };
 
-// Stages a token a block: binary16 terms of its row times the power of two that brings its largest value between 2^14 and
-// 2^15 (no value overflows, and one 2^-28 of the largest still has all its bits), in the products' order, to the rows of all
-// its pairs; scale is the power that undoes it.  The blocks behind the tokens' take the largest block scales of the
-// experts that have tokens.
-template <typename T>
+// Stages a token a block: the terms of its row times the power of two that brings its largest value between 2^14 and 2^15
+// (no value overflows, and one 2^-28 of the largest still has all its bits; e4m3: between 2^7 and 2^8), in the products'
+// order, to the rows of all its pairs; scale is the power that undoes it.  Of a row with an infinity or a NaN, e4m3 terms
+// hold neither: its scale is NaN.  The blocks behind the tokens' take the largest block scales of the experts that have
+// tokens.  PAIRS: the rows are of pairs already (hidden values).
+template <typename T, bool F8, bool PAIRS>
 __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
     __shared__ float part[2][kStageThreads / 32];
     __shared__ int to[32];
@@ -162,7 +168,8 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
         return;
     }
     const int64_t t = blockIdx.x;
-    if (tid < a.top_k) to[tid] = a.plan.pair_row[t * a.top_k + tid];
+    if (PAIRS && t >= a.plan.tile_count[1]) return;
+    if (tid < a.top_k) to[tid] = PAIRS ? int(t) : a.plan.pair_row[t * a.top_k + tid];
     struct alignas(16) Group {
         T e[16];
     };
@@ -196,31 +203,51 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
         top = fmaxf(top, part[0][w]);
         sum += part[1][w];
     }
-    const int up = top < INFINITY ? min(14 - moe_log2(top), 126) : 0;
+    const int up = top < INFINITY ? min((F8 ? 7 : 14) - moe_log2(top), 126) : 0;
     const float by = moe_power(up);
     if (tid < a.top_k && to[tid] >= 0) {
-        a.scale[to[tid]] = moe_power(-up);
-        a.sum[to[tid]] = sum * (1.f + 0x1p-10f);  // (its rounding, at most 2^-24 an addition)
+        a.scale[to[tid]] = F8 && !(top < INFINITY) ? __uint_as_float(0x7fc00000u) : moe_power(-up);
+        if (!F8) a.sum[to[tid]] = sum * (1.f + 0x1p-10f);  // (its rounding, at most 2^-24 an addition)
     }
     for (int g = tid; g < a.k / 16; g += kStageThreads) {
         const Group v = row[g];
-        __half2 hi[8], lo[8];
+        if constexpr (F8) {
+            alignas(16) __nv_fp8_storage_t term[3][16];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float p = to_f32(v.e[i]) * by, q = to_f32(v.e[i + 8]) * by;
-            hi[i] = __floats2half2_rn(p, q);
-            const float2 h = __half22float2(hi[i]);
-            lo[i] = __floats2half2_rn(p - h.x, q - h.y);
-        }
-        for (int j = 0; j < a.top_k; ++j) {
-            if (to[j] < 0) continue;
-            uint4 *dst = reinterpret_cast<uint4 *>(a.staged + int64_t(to[j]) * a.terms * a.k + 16 * g);
-            dst[0] = reinterpret_cast<const uint4 *>(hi)[0];
-            dst[1] = reinterpret_cast<const uint4 *>(hi)[1];
-            if (a.terms == 2) {
-                dst += a.k / 8;
-                dst[0] = reinterpret_cast<const uint4 *>(lo)[0];
-                dst[1] = reinterpret_cast<const uint4 *>(lo)[1];
+            for (int i = 0; i < 16; ++i) {
+                float rest = to_f32(v.e[i]) * by;
+#pragma unroll
+                for (int j = 0; j < 3; ++j) {
+                    const __nv_fp8_storage_t b = __nv_cvt_float_to_fp8(rest, __NV_SATFINITE, __NV_E4M3);
+                    term[j][moe_place8(i)] = b;
+                    rest = (rest - __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)))) * 16.f;
+                }
+            }
+            for (int j = 0; j < a.top_k; ++j) {
+                if (to[j] < 0) continue;
+                uint8_t *dst = static_cast<uint8_t *>(a.staged) + int64_t(to[j]) * 3 * a.k + 16 * g;
+#pragma unroll
+                for (int i = 0; i < 3; ++i) *reinterpret_cast<uint4 *>(dst + int64_t(i) * a.k) = *reinterpret_cast<const uint4 *>(term[i]);
+            }
+        } else {
+            __half2 hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float p = to_f32(v.e[i]) * by, q = to_f32(v.e[i + 8]) * by;
+                hi[i] = __floats2half2_rn(p, q);
+                const float2 h = __half22float2(hi[i]);
+                lo[i] = __floats2half2_rn(p - h.x, q - h.y);
+            }
+            for (int j = 0; j < a.top_k; ++j) {
+                if (to[j] < 0) continue;
+                uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__half *>(a.staged) + int64_t(to[j]) * a.terms * a.k + 16 * g);
+                dst[0] = reinterpret_cast<const uint4 *>(hi)[0];
+                dst[1] = reinterpret_cast<const uint4 *>(hi)[1];
+                if (a.terms == 2) {
+                    dst += a.k / 8;
+                    dst[0] = reinterpret_cast<const uint4 *>(lo)[0];
+                    dst[1] = reinterpret_cast<const uint4 *>(lo)[1];
+                }
             }
         }
     }
@@ -264,47 +291,55 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(MoeArgs a, MoePlan
 
 size_t pad(size_t n) { return (n + 255) & ~size_t(255); }
 
-// Columns of a tile, by the rows that experts have in the mean: with more columns codes are decoded less often, with fewer
-// there is room for more decoded weights and more warps that decode.
-int tile_cols(int64_t pairs, int64_t experts, int terms) {
-    const int64_t rows = pairs * terms, active = std::min(pairs, experts);
-    return rows <= 16 * active ? 32 : rows <= 64 * active ? 64 : 96;
+// How a call of some size is computed: terms of an activation, columns of a tile.
+//  * 16-bit activations of at most 16 rows an expert in the mean: three e4m3 terms (see moe.cuh).
+//  * Else one binary16 term, or two of f32 activations, and columns by the staged rows that experts have in the mean: with
+//    more columns codes are decoded less often, with fewer there is room for more decoded weights and more warps that decode.
+struct Form {
+    int terms, cols;
+};
+Form form_of(int dtype, int64_t pairs, int64_t experts) {
+    const int64_t active = std::min(pairs, experts);
+    if (dtype != TQ2_F32 && pairs <= 16 * active) return {3, 48};
+    const int terms = dtype == TQ2_F32 ? 2 : 1;
+    const int64_t rows = pairs * terms;
+    return {terms, rows <= 16 * active ? 32 : rows <= 64 * active ? 64 : 96};
 }
 
 struct Workspace {
     MoePlan plan;
-    __half *staged_x, *staged_h;
-    float *scale_x, *scale_h, *sum_x, *y;
-    int max_tiles, cols;
+    uint8_t *staged_x, *staged_h;
+    float *scale_x, *scale_h, *sum_x, *h, *y;
+    int max_tiles;
     size_t bytes;
 
-    Workspace(char *base, int64_t pairs, int64_t experts, int64_t width, int64_t ffn, int terms) {
+    // (Sizes are the largest that any form of this many pairs, or of fewer, takes.)
+    Workspace(char *base, int64_t pairs, int64_t experts, int64_t width, int64_t ffn, int dtype) {
         size_t at = 0;
         auto take = [&](auto *&p, size_t n) {
             p = reinterpret_cast<std::remove_reference_t<decltype(p)>>(base + at);
             at += pad(n * sizeof(*p));
         };
-        cols = tile_cols(pairs, experts, terms);
-        const int64_t tile_rows = cols / terms;
-        max_tiles = int(std::min(pairs, experts) + pairs / tile_rows);  // each expert leaves less than one unfilled
-        take(plan.tile_count, 1);
-        take(plan.tiles, size_t(std::min(pairs, experts) + pairs / (32 / terms)));
+        const Form form = form_of(dtype, pairs, experts);
+        max_tiles = int(std::min(pairs, experts) + pairs / (form.cols / form.terms));  // each expert leaves less than one unfilled
+        const int64_t few = dtype == TQ2_F32 ? 0 : std::min(pairs, 16 * experts);  // pairs of the three-term form, at most
+        take(plan.tile_count, 2);
+        take(plan.tiles, size_t(std::min(pairs, experts) + pairs / 16));
         take(plan.pair_row, size_t(pairs));
         take(plan.expert_rows, size_t(experts));
         take(plan.bound, size_t(experts));
         take(scale_x, size_t(pairs));
         take(scale_h, size_t(pairs));
         take(sum_x, size_t(pairs));
-        take(staged_x, size_t(pairs * terms * width));
-        take(staged_h, size_t(pairs * terms * ffn));
+        take(staged_x, size_t(std::max(pairs * (dtype == TQ2_F32 ? 4 : 2), few * 3) * width));
+        take(staged_h, size_t(std::max(pairs * (dtype == TQ2_F32 ? 4 : 2), few * 3) * ffn));
+        take(h, size_t(few * ffn));
         take(y, size_t(pairs * width));
         bytes = at;
     }
 };
 
-int terms_of(int dtype) { return dtype == TQ2_F32 ? 2 : 1; }
-
-cudaError_t launch_plan(const MoeArgs &a, const Workspace &w, int64_t pairs, int terms, const LaunchCtx &ctx) {
+cudaError_t launch_plan(const MoeArgs &a, const Workspace &w, int64_t pairs, const Form &form, const LaunchCtx &ctx) {
     int cluster = 1;
     while (cluster < kPlanMaxCluster && pairs > cluster * kPlanPairs) cluster *= 2;
     cudaLaunchConfig_t cfg = {};
@@ -320,17 +355,19 @@ cudaError_t launch_plan(const MoeArgs &a, const Workspace &w, int64_t pairs, int
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, moe_plan_kernel, a.expert, w.plan, int(pairs), a.experts, w.cols / terms, cluster, ctx.status);
+    return cudaLaunchKernelEx(&cfg, moe_plan_kernel, a.expert, w.plan, int(pairs), a.experts, form.cols / form.terms, cluster,
+                              ctx.status);
 }
 
 template <typename T>
 cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) {
     const int64_t pairs = a.tokens * a.top_k;
-    const int terms = terms_of(dtype);
-    const Workspace w(static_cast<char *>(ws), pairs, a.experts, a.width, a.ffn, terms);
+    const Form form = form_of(dtype, pairs, a.experts);
+    const bool f8 = form.terms == 3;
+    const Workspace w(static_cast<char *>(ws), pairs, a.experts, a.width, a.ffn, dtype);
     const SoaView gate_up = soa_view(a.gate_up, int64_t(a.experts) * 2 * a.ffn, a.width);
     const SoaView down = soa_view(a.down, int64_t(a.experts) * a.width, a.ffn);
-    cudaError_t e = launch_plan(a, w, pairs, terms, ctx);
+    cudaError_t e = launch_plan(a, w, pairs, form, ctx);
     if (e != cudaSuccess) return e;
     StageArgs s = {};
     s.plan = w.plan;
@@ -339,32 +376,45 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     s.sum = w.sum_x;
     s.d = gate_up.d;
     s.d_count = int64_t(2) * a.ffn * (a.width / kBlockW);
-    s.bound_blocks = int((s.d_count + kBoundScales - 1) / kBoundScales);
+    s.bound_blocks = f8 ? 0 : int((s.d_count + kBoundScales - 1) / kBoundScales);
     s.tokens = a.tokens;
     s.k = a.width;
     s.top_k = a.top_k;
-    s.terms = terms;
+    s.terms = form.terms;
     s.experts = a.experts;
-    e = launch_dependent(moe_stage_kernel<T>, dim3(unsigned(a.tokens + int64_t(a.experts) * s.bound_blocks)), kStageThreads, 0, ctx.stream,
-                         static_cast<const T *>(a.x), s);
+    const T *x = static_cast<const T *>(a.x);
+    const dim3 stage_grid(unsigned(a.tokens + int64_t(a.experts) * s.bound_blocks));
+    e = f8 ? launch_dependent(moe_stage_kernel<T, true, false>, stage_grid, kStageThreads, 0, ctx.stream, x, s)
+           : launch_dependent(moe_stage_kernel<T, false, false>, stage_grid, kStageThreads, 0, ctx.stream, x, s);
     if (e != cudaSuccess) return e;
     MoeGemm g = {};
     g.plan = w.plan;
     g.pairs = pairs;
     g.experts = a.experts;
-    g.terms = terms;
-    g.cols = w.cols;
+    g.terms = form.terms;
+    g.cols = form.cols;
     g.max_tiles = w.max_tiles;
     g.qs = gate_up.qs;
     g.d = gate_up.d;
     g.staged = w.staged_x;
     g.scale = w.scale_x;
     g.sum = w.sum_x;
-    g.staged_out = w.staged_h;
+    g.out = w.h;
+    g.staged_out = reinterpret_cast<__half *>(w.staged_h);
     g.scale_out = w.scale_h;
     g.rows = 2 * a.ffn;
     g.k = a.width;
     if ((e = launch_moe_gemm(g, true, ctx)) != cudaSuccess) return e;
+    if (f8) {  // (e4m3 terms need the rows' largest values, not bounds of them)
+        s.staged = w.staged_h;
+        s.scale = w.scale_h;
+        s.tokens = pairs;
+        s.k = a.ffn;
+        s.top_k = 1;
+        e = launch_dependent(moe_stage_kernel<float, true, true>, dim3(unsigned(pairs)), kStageThreads, 0, ctx.stream,
+                             static_cast<const float *>(w.h), s);
+        if (e != cudaSuccess) return e;
+    }
     g.qs = down.qs;
     g.d = down.d;
     g.staged = w.staged_h;
@@ -381,7 +431,7 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
 }  // namespace
 
 size_t moe_ws_bytes(int64_t tokens, int64_t top_k, int64_t experts, int64_t width, int64_t ffn, int dtype) {
-    return Workspace(nullptr, tokens * top_k, experts, width, ffn, terms_of(dtype)).bytes;
+    return Workspace(nullptr, tokens * top_k, experts, width, ffn, dtype).bytes;
 }
 
 cudaError_t launch_moe(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) {

@@ -27,24 +27,33 @@ struct MoeGemm {
     MoePlan plan;
     const uint8_t *qs;   // codes [experts * rows][k / 4]
     const __half *d;     // block scales [experts * rows][k / 128]
-    const __half *staged;
+    const void *staged;  // binary16, or e4m3 where terms is 3
     const float *scale;  // of each row: what its staged values are to be multiplied by
     const float *sum;    // gate_up: of each row, the sum of |x|
-    float *out;          // down: [rows][features]
-    __half *staged_out;  // gate_up: the hidden values, staged
+    float *out;          // [rows][features]: of down the product, of gate_up, with three terms, the hidden values
+    __half *staged_out;  // gate_up, one or two terms: the hidden values, staged
     float *scale_out;    //          and each row's scale
     int64_t pairs;
     int experts, rows, k;
     int terms;           // staged rows of a row
-    int cols;            // staged rows (MMA columns) of a tile, at most: 32, 64 or 96
+    int cols;            // staged rows (MMA columns) of a tile, at most: 32, 64 or 96, or 48 with three terms
     int max_tiles;
 };
 // gate_up: rows counts gate then up rows, and the SwiGLU of rows / 2 features is staged; else out is the product.
 cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx);
 
-// Order of staged activations: a staged row holds elements i and i + 8 of each group of 16 at 2 i and 2 i + 1, as pairs of
-// codes are masked out of a word of 16 (the library's binary16 activation layout).
+// Terms of a staged value v, scaled by a power of two to below 2^15 (2^8 for e4m3):
+//   1: binary16(v).   2: also binary16(v - first).
+//   3: e4m3 numbers t0, t1, t2 with v = t0 + t1 / 16 + t2 / 256: each rounds to four bits what is left, so that they hold
+//      twelve: all of a binary16's or bf16's (down to 2^-25 of the largest), and others to 2^-12.
+// Three 8-bit terms where experts have few tokens: an MMA takes twice as many 8-bit weights as 16-bit ones in the same time,
+// 64 cycles for its A operand's 4 KB from tensor memory however few columns it has.
+//
+// Order of staged activations: a binary16 row holds elements i and i + 8 of each group of 16 at 2 i and 2 i + 1, as pairs of
+// codes are masked out of a word of 16 (the library's binary16 activation layout).  An e4m3 row holds the even and the odd elements
+// of each 8 after each other, as codes are looked up from a word four at a time.
 __host__ __device__ constexpr int moe_place(int i) { return i < 8 ? 2 * i : 2 * (i - 8) + 1; }
+__host__ __device__ constexpr int moe_place8(int i) { return (i & 8) + (i & 1) * 4 + (i & 7) / 2; }
 
 // 2^e with e kept to what f32 holds as a normal number.
 __device__ __forceinline__ float moe_power(int e) { return __uint_as_float(uint32_t(max(min(e, 127), -126) + 127) << 23); }

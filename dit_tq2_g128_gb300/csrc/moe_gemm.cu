@@ -32,25 +32,27 @@ namespace {
 constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4;
 constexpr int kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
 constexpr int kCodes = 6;   // stages of codes
-constexpr int kACols = kBlockW / 2;
 constexpr uint32_t kTmemCols = 512;
 
+// COLS: 32, 64 or 96 with one or two binary16 terms, 48 with three e4m3 terms.
 template <int COLS>
 struct Shape {
+    static constexpr bool F8 = COLS == 48, FEW = COLS <= 48;
     static constexpr int UNIT = COLS == 96 ? 1 : 2;          // blocks that the roles hand to each other at a time
-    static constexpr int RING = COLS == 32 ? 3 : 4 / UNIT;   // units decoded, or being multiplied
+    static constexpr int RING = FEW ? 3 : 4 / UNIT;          // units decoded, or being multiplied
     static constexpr int DRING = 2;                          // units of accumulators
-    static constexpr int ACTS = COLS == 32 ? 8 : COLS == 64 ? 4 : 5;  // units of activations
-    static constexpr int ACT_BYTES = COLS * kBlockW * 2 * UNIT;
-    static constexpr int DECODERS = COLS == 32 ? 3 : 2;      // groups of four warps
+    static constexpr int ACTS = FEW ? 8 : COLS == 64 ? 4 : 5;  // units of activations
+    static constexpr int ACT_BYTES = COLS * kBlockW * (F8 ? 1 : 2) * UNIT;
+    static constexpr int DECODERS = FEW ? 3 : 2;             // groups of four warps
     static constexpr int W_SUM = W_DECODE + 4 * DECODERS, THREADS = 32 * (W_SUM + 8);
     // registers a thread at launch, and of the roles' warpgroups after it
-    static constexpr int REGS = COLS == 32 ? 80 : 96;
-    static constexpr int REGS_CONTROL = COLS == 32 ? 40 : 48, REGS_DECODE = COLS == 32 ? 80 : COLS == 64 ? 88 : 56;
-    static constexpr int REGS_SUM = COLS == 32 ? 96 : COLS == 64 ? 128 : 160;
+    static constexpr int REGS = FEW ? 80 : 96;
+    static constexpr int REGS_CONTROL = FEW ? 40 : 48, REGS_DECODE = F8 ? 72 : FEW ? 80 : COLS == 64 ? 88 : 56;
+    static constexpr int REGS_SUM = F8 ? 112 : FEW ? 96 : COLS == 64 ? 128 : 160;
     static constexpr int OFF_ACT = kCodes * kCodeBytes, OFF_CTL = OFF_ACT + ACTS * ACT_BYTES;
+    static constexpr int A_COLS = F8 ? kBlockW / 4 : kBlockW / 2;  // of a block's decoded weights
     static constexpr uint32_t A_COL = DRING * UNIT * COLS;
-    static_assert(A_COL + RING * UNIT * kACols <= kTmemCols, "TMEM budget");
+    static_assert(A_COL + RING * UNIT * A_COLS <= kTmemCols, "TMEM budget");
     static_assert(REGS_CONTROL + DECODERS * REGS_DECODE + 2 * REGS_SUM <= (3 + DECODERS) * REGS, "registers");
 };
 
@@ -68,7 +70,7 @@ struct Ctl {
 };
 template <int COLS>
 constexpr int kSmem = Shape<COLS>::OFF_CTL + int(sizeof(Ctl)) + 1024;
-static_assert(kSmem<32> <= 232448 && kSmem<64> <= 232448 && kSmem<96> <= 232448, "shared memory budget");
+static_assert(kSmem<32> <= 232448 && kSmem<48> <= 232448 && kSmem<64> <= 232448 && kSmem<96> <= 232448, "shared memory budget");
 
 __device__ __forceinline__ uint64_t desc_k(uint32_t saddr) {  // K-major, 128-byte swizzle: rows 128 B, 8-row groups 1024 B
     return uint64_t((saddr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
@@ -121,6 +123,16 @@ __device__ __forceinline__ void tm_tie(uint32_t (&r)[N]) {
     for (int i = 0; i < N; i += 8)
         asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])::"memory");
 }
+// The same for e4m3 numbers: column c = elements 4c .. 4c + 3.
+__device__ __forceinline__ void mma_ts_f8(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
 __device__ __forceinline__ void tm_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -178,6 +190,21 @@ __device__ __forceinline__ void decode(uint32_t w0, uint32_t w1, const Exponents
     }
 }
 
+// Four words of 16 codes as e4m3 numbers code - 1, four in a register: of each word the codes 0, 2, 4, 6, then 1, 3, 5, 7, then
+// the same of its upper half, each looked up from -1, 0, 1, 2.
+__device__ __forceinline__ void decode_f8(const uint4 &w, uint32_t (&r)[16]) {
+    constexpr uint32_t values = 0x403800b8u;
+    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t even = word[j] & 0x33333333u, odd = (word[j] >> 2) & 0x33333333u;
+        r[4 * j] = __byte_perm(values, 0, even);
+        r[4 * j + 1] = __byte_perm(values, 0, odd);
+        r[4 * j + 2] = __byte_perm(values, 0, even >> 16);
+        r[4 * j + 3] = __byte_perm(values, 0, odd >> 16);
+    }
+}
+
 // Whether a phase is over, without waiting.
 __device__ __forceinline__ bool phase_over(uint64_t *bar, uint32_t parity) {
     uint32_t ok;
@@ -191,9 +218,11 @@ __device__ __forceinline__ bool phase_over(uint64_t *bar, uint32_t parity) {
     return ok;
 }
 
-// Staged rows are copied by boxes of 16, 32, 64 or 96: index, and rows, of the one that holds `cols`.
-__device__ __forceinline__ int box_of(int cols) { return cols <= 16 ? 0 : cols <= 32 ? 1 : cols <= 64 ? 2 : 3; }
-__host__ __device__ constexpr int box_rows(int box) { return box < 3 ? 16 << box : 96; }
+// Staged rows are copied by boxes of 16, 32, 64 or 96 (e4m3: 16, 32 or 48): index, and rows, of the one that holds `cols`.
+template <bool F8>
+__device__ __forceinline__ int box_of(int cols) { return cols <= 16 ? 0 : cols <= 32 ? 1 : F8 || cols <= 64 ? 2 : 3; }
+template <bool F8>
+__host__ __device__ constexpr int box_rows(int box) { return F8 ? 16 * (box + 1) : box < 3 ? 16 << box : 96; }
 struct BoxMaps {
     CUtensorMap map[4];
 };
@@ -308,14 +337,14 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 const Item it = item_of(g, i, parts);
                 // (one copy a unit, issued by one lane: its issue takes longer than the block's MMAs; the box's rows after the
                 // tile's are other experts', whose columns nothing reads)
-                const int box = uniform(box_of(it.cols)), bytes = box_rows(box) * 256 * L::UNIT, row = it.tile.row0 * g.terms;
+                const int box = uniform(box_of<L::F8>(it.cols)), bytes = box_rows<L::F8>(box) * (L::F8 ? 128 : 256) * L::UNIT, row = it.tile.row0 * g.terms;
                 for (int u = 0; u < units; ++u, ++n) {
                     const int s = n % L::ACTS;
                     if (!(ok = wait_on(&ctl->x_empty[s], ((n / L::ACTS) & 1) ^ 1))) break;
                     if (elect_one()) {
                         mbar_expect_tx(&ctl->x_full[s], uint32_t(bytes));
                         tma_3d(smem_u32(smem) + uint32_t(L::OFF_ACT + s * L::ACT_BYTES), &xmaps.map[box], 0, row,
-                               u * L::UNIT * 2, &ctl->x_full[s]);
+                               u * L::UNIT * (L::F8 ? 1 : 2), &ctl->x_full[s]);
                     }
                     __syncwarp();
                 }
@@ -335,7 +364,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
                     const int cols = next.take();
                     const uint32_t idesc = (1u << 4) | (uint32_t(cols >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-                    const uint32_t half = uint32_t(box_rows(box_of(cols))) * 8;  // (in 16 bytes) 64 features of the box's rows
+                    const uint32_t piece = uint32_t(box_rows<L::F8>(box_of<L::F8>(cols))) * 8;  // (in 16 bytes) 128 bytes of each of the box's rows
                     for (int u = 0; u < units; ++u, ++n) {
                         const int s = n % L::RING, sx = n % L::ACTS, sd = n % L::DRING;
                         // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
@@ -350,12 +379,15 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
 #pragma unroll
                         for (int j = 0; j < L::UNIT; ++j) {
                             if (u * L::UNIT + j >= nb) break;
-                            const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4) + 2 * j * half);
+                            const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4) + (L::F8 ? 1 : 2) * j * piece);
                             const uint32_t d = tmem + uint32_t((sd * L::UNIT + j) * COLS);
-                            const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols);
+                            const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * L::A_COLS);
 #pragma unroll
-                            for (int kk = 0; kk < 8; ++kk)
-                                mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * half + 2 * (kk & 3)), idesc, kk > 0);
+                            for (int kk = 0; kk < (L::F8 ? 4 : 8); ++kk)
+                                if (L::F8)
+                                    mma_ts_f8(d, at + uint32_t(kk * 8), db + uint64_t(2 * kk), idesc, kk > 0);
+                                else
+                                    mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * piece + 2 * (kk & 3)), idesc, kk > 0);
                         }
                         tc_commit(&ctl->done[s]);
                         tc_commit(&ctl->x_empty[sx]);
@@ -402,9 +434,15 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
 #pragma unroll
                     for (int j = 0; j < L::UNIT; ++j) {
                         if (u * L::UNIT + j >= nb) break;
-                        const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * kACols) + (uint32_t(q * 32) << 16);
+                        const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * L::A_COLS) + (uint32_t(q * 32) << 16);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
+                            if (L::F8) {
+                                uint32_t v[16];
+                                decode_f8(w[t][j][c], v);
+                                tm_st16(at + uint32_t(16 * c), v);
+                                continue;
+                            }
                             // (stores of 16 registers: of 32, the next ones waited for these to be read)
                             uint32_t v[2][16];
                             decode(w[t][j][c].x, w[t][j][c].y, exponents, v[0]);
@@ -438,7 +476,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             for (int j = 0; j < COLS / 32; ++j) {
                 const int at = it.tile.row0 + min(32 * j + lane, left - 1);
                 scale[j] = g.scale[at];
-                if (GATE_UP) {
+                if (GATE_UP && !L::F8) {
                     // |gate|, |up| <= bound * sum < 2^(e + 1), so that a hidden value times 2^(13 - 2 e) is below 2^15
                     const float b = __uint_as_float(g.plan.bound[it.tile.expert]) * g.sum[at];
                     const int e = b < INFINITY ? max(min(13 - 2 * moe_log2(b), 126), -126) : 0;
@@ -500,13 +538,16 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             if (lane == 0) mbar_arrive(&ctl->turn[group ^ 1]);
             auto finish = [&](auto two) {
                 constexpr int S = decltype(two)::value;
-                // row c of the tile: column c, or the sum of columns 2 c and 2 c + 1 (terms)
+                // row c of the tile: column c, or the sum of the columns of its terms
+                auto column = [&](int c) { return c & 1 ? second(acc[c >> 1]) : first(acc[c >> 1]); };
                 auto sum = [&](int c) {
-                    return S == 2 ? first(acc[c]) + second(acc[c]) : c & 1 ? second(acc[c >> 1]) : first(acc[c >> 1]);
+                    if (S == 3) return fmaf(fmaf(column(3 * c + 2), 0x1p-4f, column(3 * c + 1)), 0x1p-4f, column(3 * c));
+                    return S == 2 ? column(2 * c) + column(2 * c + 1) : column(c);
                 };
                 if (GATE_UP) {
                     // this lane's place in a staged row
                     __half *out = g.staged_out + int64_t(it.tile.row0) * S * features + 64 * it.part + 16 * q + moe_place(lane & 15);
+                    float *plain = g.out + int64_t(it.tile.row0) * features + 64 * it.part + 16 * q + (lane & 15);
                     const int odd = lane >= 16;
 #pragma unroll
                     for (int c0 = 0; c0 < COLS / S; c0 += 8)
@@ -515,11 +556,13 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                             for (int c = c0; c < c0 + 8; c += 2) {
                                 // lanes 0-15 finish row c, lanes 16-31 row c + 1
                                 const float s = __shfl_sync(0xffffffffu, scale[c >> 5], (c & 31) + odd);
-                                const float by = __shfl_sync(0xffffffffu, up[c >> 5], (c & 31) + odd);
+                                const float by = S == 3 ? 1.f : __shfl_sync(0xffffffffu, up[c >> 5], (c & 31) + odd);
                                 const float other = __shfl_xor_sync(0xffffffffu, odd ? sum(c) : sum(c + 1), 16);
                                 const float gate = (odd ? other : sum(c)) * s, ups = (odd ? sum(c + 1) : other) * s;
                                 const float h = silu(gate) * ups * by;
-                                if (c + odd < left) {
+                                if (S == 3) {
+                                    if (c + odd < left) plain[int64_t(c + odd) * features] = h;
+                                } else if (c + odd < left) {
                                     const __half hi = __float2half_rn(h);
                                     __half *to = out + int64_t(c + odd) * S * features;
                                     to[0] = hi;
@@ -540,7 +583,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                         }
                 }
             };
-            if (g.terms == 2)
+            if (L::F8)
+                finish(std::integral_constant<int, 3>{});
+            else if (g.terms == 2)
                 finish(std::integral_constant<int, 2>{});
             else
                 finish(std::integral_constant<int, 1>{});
@@ -576,13 +621,15 @@ cudaError_t launch(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
     const cuuint64_t cdims[2] = {cuuint64_t(g.k / 4), cuuint64_t(g.experts) * cuuint64_t(g.rows)}, cstrides[1] = {cuuint64_t(g.k / 4)};
     const cuuint32_t cbox[2] = {128, 64};
     cudaError_t e = make_map(&cmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, g.qs, 2, cdims, cstrides, cbox, CU_TENSOR_MAP_L2_PROMOTION_L2_256B);
-    // [64-feature pieces][rows][64]: a unit's pieces in one copy, each a swizzled operand
-    const cuuint64_t xdims[3] = {64, cuuint64_t(g.pairs * g.terms), cuuint64_t(g.k / 64)};
-    const cuuint64_t xstrides[2] = {cuuint64_t(g.k) * 2, 128};
-    for (int i = 0; i < 4 && box_rows(i) <= COLS && e == cudaSuccess; ++i) {
-        const cuuint32_t xbox[3] = {64, cuuint32_t(box_rows(i)), 2 * Shape<COLS>::UNIT};
-        e = make_map(&xmaps.map[i], CU_TENSOR_MAP_DATA_TYPE_FLOAT16, g.staged, 3, xdims, xstrides, xbox,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
+    // [128-byte pieces of a row][rows][a piece]: a unit's pieces in one copy, each a swizzled operand
+    constexpr bool F8 = Shape<COLS>::F8;
+    constexpr int size = F8 ? 1 : 2, piece = 128 / size;
+    const cuuint64_t xdims[3] = {piece, cuuint64_t(g.pairs * g.terms), cuuint64_t(g.k / piece)};
+    const cuuint64_t xstrides[2] = {cuuint64_t(g.k) * size, 128};
+    for (int i = 0; i < 4 && box_rows<F8>(i) <= COLS && e == cudaSuccess; ++i) {
+        const cuuint32_t xbox[3] = {piece, cuuint32_t(box_rows<F8>(i)), cuuint32_t(kBlockW / piece * Shape<COLS>::UNIT)};
+        e = make_map(&xmaps.map[i], F8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, g.staged, 3, xdims, xstrides,
+                     xbox, CU_TENSOR_MAP_L2_PROMOTION_L2_128B);
     }
     if (e != cudaSuccess) return e;
     auto kernel = gate_up ? moe_gemm_kernel<true, COLS> : moe_gemm_kernel<false, COLS>;
@@ -596,7 +643,12 @@ cudaError_t launch(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
 }  // namespace
 
 cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx) {
-    return g.cols == 32 ? launch<32>(g, gate_up, ctx) : g.cols == 64 ? launch<64>(g, gate_up, ctx) : launch<96>(g, gate_up, ctx);
+    switch (g.cols) {
+        case 32: return launch<32>(g, gate_up, ctx);
+        case 48: return launch<48>(g, gate_up, ctx);
+        case 64: return launch<64>(g, gate_up, ctx);
+        default: return launch<96>(g, gate_up, ctx);
+    }
 }
 
 }  // namespace tq2

@@ -568,7 +568,13 @@ typedef struct {
  *   out      : device [tokens, width] of type dtype
  *   top_k    : 1 .. 32; tokens * top_k <= 2^22
  * gate_up, down, x, residual and out are 16-byte aligned.
- * Sums in f32, one rounding to the output's type.
+ * Arithmetic: weights exact; activations as sums of terms that the tensor cores
+ * multiply: of f32 ones two in binary16 (2^-22 of a value), of 16-bit ones one in binary16
+ * or, where experts have 16 rows or fewer in the mean, three in e4m3 (which hold all bits of
+ * those that are not below 2^-25 of their row's largest); so too the hidden values
+ * silu(.) * (.), to 2^-11 of themselves (f32: 2^-22).  Any magnitudes are in range.  Sums in f32,
+ * one rounding to the output's type.  A token's result may differ in its rounding with the
+ * number of tokens of the call.
  * Memory: `workspace` holds the activations on their way
  * (tq2_moe_swiglu_workspace_bytes of the same arguments, 16-byte aligned); if NULL, a
  * temporary from the device's pool is taken instead.  Calls that share a workspace

