@@ -39,7 +39,7 @@ template <int COLS>
 struct Shape {
     static constexpr bool F8 = COLS == 48, FEW = COLS <= 48;
     static constexpr int UNIT = COLS == 96 ? 1 : 2;          // blocks that the roles hand to each other at a time
-    static constexpr int RING = FEW ? 3 : 4 / UNIT;          // units decoded, or being multiplied
+    static constexpr int RING = F8 ? 4 : FEW ? 3 : 4 / UNIT;          // units decoded, or being multiplied
     static constexpr int DRING = 2;                          // units of accumulators
     static constexpr int ACTS = FEW ? 8 : COLS == 64 ? 4 : 5;  // units of activations
     static constexpr int ACT_BYTES = COLS * kBlockW * (F8 ? 1 : 2) * UNIT;
@@ -354,47 +354,49 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                     mbar_wait_bounded(&ctl->x_full[j % L::ACTS], (j / L::ACTS) & 1, drain_ns(wait_ns), status);
             __syncwarp();
         } else if (warp == W_MMA) {
-            // (one lane takes the whole loop, from values that the compiler knows to be uniform)
-            if (elect_one()) {
-                const uint64_t x0 = desc_k(smem_u32(smem) + uint32_t(L::OFF_ACT));
-                auto wait_one = [&](uint64_t *bar, uint32_t parity) { return wait_phase(bar, parity, abort_flag, wait_ns, status); };
-                int n = 0;  // units
-                bool ok = true;
-                Columns next(g, parts, items);
-                for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
-                    const int cols = next.take();
-                    const uint32_t idesc = (1u << 4) | (uint32_t(cols >> 3) << 17) | (uint32_t(128 >> 4) << 24);
-                    const uint32_t piece = uint32_t(box_rows<L::F8>(box_of<L::F8>(cols))) * 8;  // (in 16 bytes) 128 bytes of each of the box's rows
-                    for (int u = 0; u < units; ++u, ++n) {
-                        const int s = n % L::RING, sx = n % L::ACTS, sd = n % L::DRING;
-                        // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
-                        // its first use counts as over)
-                        const uint32_t pd = ((n / L::DRING) & 1) ^ 1, px = (n / L::ACTS) & 1, pa = (n / L::RING) & 1;
-                        const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
-                                   a_there = phase_over(&ctl->a_full[s], pa);
-                        ok = (d_free || wait_one(&ctl->d_empty[sd], pd)) && (x_there || wait_one(&ctl->x_full[sx], px)) &&
-                             (a_there || wait_one(&ctl->a_full[s], pa));
-                        if (!ok) break;
-                        tc_fence_after();
+            // (the whole warp takes the loop, from values that the compiler knows to be uniform, and one lane issues)
+            const uint64_t x0 = desc_k(smem_u32(smem) + uint32_t(L::OFF_ACT));
+            int n = 0;  // units
+            bool ok = true;
+            Columns next(g, parts, items);
+            for (int i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const int cols = uniform(next.take());
+                const uint32_t idesc = (1u << 4) | (uint32_t(cols >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+                const uint32_t piece = uint32_t(box_rows<L::F8>(box_of<L::F8>(cols))) * 8;  // (in 16 bytes) 128 bytes of each of the box's rows
+                for (int u = 0; u < units; ++u, ++n) {
+                    const int s = n % L::RING, sx = n % L::ACTS, sd = n % L::DRING;
+                    // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
+                    // its first use counts as over)
+                    const uint32_t pd = ((n / L::DRING) & 1) ^ 1, px = (n / L::ACTS) & 1, pa = (n / L::RING) & 1;
+                    const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
+                               a_there = phase_over(&ctl->a_full[s], pa);
+                    if (!__all_sync(0xffffffffu, d_free && x_there && a_there))
+                        ok = wait_on(&ctl->d_empty[sd], pd) && wait_on(&ctl->x_full[sx], px) && wait_on(&ctl->a_full[s], pa);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t dx = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4));
+                    const uint32_t d = tmem + uint32_t(sd * L::UNIT * COLS), at = tmem + L::A_COL + uint32_t(s * L::UNIT * L::A_COLS);
+                    const bool both = u * L::UNIT + L::UNIT <= nb;
+                    if (elect_one()) {
 #pragma unroll
                         for (int j = 0; j < L::UNIT; ++j) {
-                            if (u * L::UNIT + j >= nb) break;
-                            const uint64_t db = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4) + (L::F8 ? 1 : 2) * j * piece);
-                            const uint32_t d = tmem + uint32_t((sd * L::UNIT + j) * COLS);
-                            const uint32_t at = tmem + L::A_COL + uint32_t((s * L::UNIT + j) * L::A_COLS);
+                            if (j > 0 && !both) break;
+                            const uint64_t db = dx + uint64_t((L::F8 ? 1 : 2) * j * piece);
 #pragma unroll
                             for (int kk = 0; kk < (L::F8 ? 4 : 8); ++kk)
                                 if (L::F8)
-                                    mma_ts_f8(d, at + uint32_t(kk * 8), db + uint64_t(2 * kk), idesc, kk > 0);
+                                    mma_ts_f8(d + j * COLS, at + uint32_t(j * L::A_COLS + kk * 8), db + uint64_t(2 * kk), idesc, kk > 0);
                                 else
-                                    mma_ts(d, at + uint32_t(kk * 8), db + uint64_t((kk >> 2) * piece + 2 * (kk & 3)), idesc, kk > 0);
+                                    mma_ts(d + j * COLS, at + uint32_t(j * L::A_COLS + kk * 8),
+                                           db + uint64_t((kk >> 2) * piece + 2 * (kk & 3)), idesc, kk > 0);
                         }
                         tc_commit(&ctl->done[s]);
                         tc_commit(&ctl->x_empty[sx]);
                     }
+                    __syncwarp();
                 }
-                tc_commit(&ctl->drain);
             }
+            if (elect_one()) tc_commit(&ctl->drain);
             __syncwarp();
         }
     } else if (warp < L::W_SUM) {
