@@ -33,15 +33,16 @@ constexpr int W_CODES = 0, W_MMA = 1, W_ACT = 2, W_DECODE = 4;
 constexpr int kCodeK = 512, kCodeBytes = 128 * kCodeK / 4;  // 16 KB
 constexpr int kCodes = 6;   // stages of codes
 constexpr uint32_t kTmemCols = 512;
+constexpr int kMostActs = 8, kMostUnits = 4;
 
 // COLS: 32, 64 or 96 with one or two binary16 terms, 48 with three e4m3 terms.
 template <int COLS>
 struct Shape {
     static constexpr bool F8 = COLS == 48, FEW = COLS <= 48;
-    static constexpr int UNIT = COLS == 96 ? 1 : 2;          // blocks that the roles hand to each other at a time
-    static constexpr int RING = F8 ? 4 : FEW ? 3 : 4 / UNIT;          // units decoded, or being multiplied
-    static constexpr int DRING = 2;                          // units of accumulators
-    static constexpr int ACTS = FEW ? 8 : COLS == 64 ? 4 : 5;  // units of activations
+    static constexpr int UNIT = FEW ? 2 : 1;                 // blocks that the roles hand to each other at a time
+    static constexpr int RING = COLS == 64 ? 4 : 3;          // units decoded, or being multiplied
+    static constexpr int DRING = COLS == 32 ? 2 : RING;      // units of accumulators: with two a unit took 400 cycles of waits
+    static constexpr int ACTS = COLS == 96 ? 5 : 8;          // units of activations
     static constexpr int ACT_BYTES = COLS * kBlockW * (F8 ? 1 : 2) * UNIT;
     static constexpr int DECODERS = FEW ? 3 : 2;             // groups of four warps
     static constexpr int W_SUM = W_DECODE + 4 * DECODERS, THREADS = 32 * (W_SUM + 8);
@@ -53,16 +54,18 @@ struct Shape {
     static constexpr int A_COLS = F8 ? kBlockW / 4 : kBlockW / 2;  // of a block's decoded weights
     static constexpr uint32_t A_COL = DRING * UNIT * COLS;
     static_assert(A_COL + RING * UNIT * A_COLS <= kTmemCols, "TMEM budget");
+    // (a unit's accumulators are read before its place among the units decoded is used again: no phase of `done` is missed)
+    static_assert(DRING <= RING && RING <= kMostUnits && ACTS <= kMostActs);
     static_assert(REGS_CONTROL + DECODERS * REGS_DECODE + 2 * REGS_SUM <= (3 + DECODERS) * REGS, "registers");
 };
 
 struct Ctl {
     uint64_t c_full[kCodes], c_empty[kCodes];
     // by unit
-    uint64_t x_full[8], x_empty[8];
-    uint64_t a_full[4];
-    uint64_t done[4];  // its MMAs have ended: its decoded weights' slot is free and its accumulators are full
-    uint64_t d_empty[2];
+    uint64_t x_full[kMostActs], x_empty[kMostActs];
+    uint64_t a_full[kMostUnits];
+    uint64_t done[kMostUnits];  // its MMAs have ended: its decoded weights' slot is free and its accumulators are full
+    uint64_t d_empty[kMostUnits];
     uint64_t turn[2];  // a summing group may begin its next item: the other has seen all blocks of the one before
     uint64_t drain;
     uint32_t tmem_base;
@@ -368,10 +371,14 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                     // (asked for together: one after the other the answers took 300 cycles a block; a slot's phase before
                     // its first use counts as over)
                     const uint32_t pd = ((n / L::DRING) & 1) ^ 1, px = (n / L::ACTS) & 1, pa = (n / L::RING) & 1;
-                    const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
-                               a_there = phase_over(&ctl->a_full[s], pa);
-                    if (!__all_sync(0xffffffffu, d_free && x_there && a_there))
-                        ok = wait_on(&ctl->d_empty[sd], pd) && wait_on(&ctl->x_full[sx], px) && wait_on(&ctl->a_full[s], pa);
+                    for (int polls = 0; ok; ++polls) {
+                        const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
+                                   a_there = phase_over(&ctl->a_full[s], pa);
+                        if (__all_sync(0xffffffffu, d_free && x_there && a_there)) break;
+                        if (polls == 256)  // (some 20 us)
+                            ok = wait_on(&ctl->d_empty[sd], pd) && wait_on(&ctl->x_full[sx], px) && wait_on(&ctl->a_full[s], pa);
+                        if (polls == 256) break;
+                    }
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t dx = x0 + uint64_t(uint32_t(sx) * (L::ACT_BYTES >> 4));
