@@ -33,7 +33,8 @@ __device__ __forceinline__ const P *at_cta(const P *p, uint32_t rank) {
     return reinterpret_cast<const P *>(r);
 }
 
-// Exclusive sum over the block's threads of v; total: the sum.
+// Exclusive sum over the block's threads (of WARPS warps) of v; total: the sum.
+template <int WARPS>
 __device__ __forceinline__ int block_scan(int v, int *part, int *total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int s = v;
@@ -46,7 +47,7 @@ __device__ __forceinline__ int block_scan(int v, int *part, int *total) {
     if (lane == 31) part[warp] = s;
     __syncthreads();
     if (warp == 0) {
-        int x = part[lane];
+        int x = lane < WARPS ? part[lane] : 0;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, x, o);
@@ -96,9 +97,9 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
             total += n;
         }
     int rows, tiles;
-    const int at = block_scan(total, part, &rows);
+    const int at = block_scan<kPlanThreads / 32>(total, part, &rows);
     const int n_tiles = (total + tile_rows - 1) / tile_rows;
-    const int tile0 = block_scan(n_tiles, part, &tiles);
+    const int tile0 = block_scan<kPlanThreads / 32>(n_tiles, part, &tiles);
     next[tid] = at + before;
     if (rank == 0) {
         for (int i = 0; i < n_tiles; ++i)
@@ -126,6 +127,7 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
 }
 
 constexpr int kStageThreads = 128;
+constexpr int kFewPairs = 1024;     // that are sorted by the blocks that stage them
 constexpr int kBoundScales = 8192;  // block scales of a block that looks for the largest
 
 struct StageArgs {
@@ -138,6 +140,10 @@ struct StageArgs {
     int bound_blocks;
     int64_t tokens;
     int k, top_k, terms, experts;
+    // where the pairs are not sorted yet
+    const int32_t *expert;
+    int tile_rows;
+    unsigned int *status;
 };
 
 // Stages a token a block: the terms of its row times the power of two that brings its largest value between 2^14 and 2^15
@@ -145,14 +151,63 @@ struct StageArgs {
 // order, to the rows of all its pairs; scale is the power that undoes it.  Of a row with an infinity or a NaN, e4m3 terms
 // hold neither: its scale is NaN.  The blocks behind the tokens' take the largest block scales of the experts that have
 // tokens.  PAIRS: the rows are of pairs already (hidden values).
-template <typename T, bool F8, bool PAIRS>
+// ROUTE: the pairs (at most kFewPairs) are not sorted yet: each token's block finds the rows of its pairs by counting those
+// before them, and the block behind the tokens' writes the tiles.
+template <typename T, bool F8, bool PAIRS, bool ROUTE>
 __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
     __shared__ float part[2][kStageThreads / 32];
     __shared__ int to[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (blockIdx.x >= a.tokens) {
+    if constexpr (ROUTE) {
+        __shared__ int id[kFewPairs], count[1024], sums[32];
+        const int pairs = int(a.tokens) * a.top_k;
+        for (int i = tid; i < pairs; i += kStageThreads) id[i] = a.expert[i];
+        if (blockIdx.x == a.tokens) {
+            for (int e = tid; e < 1024; e += kStageThreads) count[e] = 0;
+            __syncthreads();
+            for (int i = tid; i < pairs; i += kStageThreads) {
+                const bool there = id[i] >= 0 && id[i] < a.experts;
+                if (there) atomicAdd(&count[id[i]], 1);
+                report_bad(!there && id[i] != -1, a.status);
+            }
+            __syncthreads();
+            // experts 8 tid .. 8 tid + 7
+            int rows = 0, tiles = 0;
+            for (int e = 8 * tid; e < 8 * tid + 8; ++e) {
+                rows += count[e];
+                tiles += (count[e] + a.tile_rows - 1) / a.tile_rows;
+            }
+            int all_rows, all_tiles;
+            int row = block_scan<kStageThreads / 32>(rows, sums, &all_rows), tile = block_scan<kStageThreads / 32>(tiles, sums, &all_tiles);
+            for (int e = 8 * tid; e < 8 * tid + 8; ++e) {
+                for (int i = 0; i < count[e]; i += a.tile_rows)
+                    a.plan.tiles[tile++] = MoeTile{e, row + i, min(a.tile_rows, count[e] - i), 0};
+                row += count[e];
+            }
+            if (tid == 0) {
+                a.plan.tile_count[0] = all_tiles;
+                a.plan.tile_count[1] = all_rows;
+            }
+            return;
+        }
+        if (tid < a.top_k) to[tid] = 0;
+        __syncthreads();
+        for (int j = 0; j < a.top_k; ++j) {
+            const int p = int(blockIdx.x) * a.top_k + j, e = id[p];
+            int before = 0;
+            for (int i = tid; i < pairs; i += kStageThreads) before += id[i] >= 0 && (id[i] < e || (id[i] == e && i < p));
+            before = __reduce_add_sync(0xffffffffu, before);
+            if (lane == 0) atomicAdd(&to[j], before);
+        }
+        __syncthreads();
+        if (tid < a.top_k) {
+            const int p = int(blockIdx.x) * a.top_k + tid, e = id[p];
+            if (e < 0 || e >= a.experts) to[tid] = -1;
+            a.plan.pair_row[p] = to[tid];
+        }
+    } else if (blockIdx.x >= a.tokens) {
         const int b = int(blockIdx.x - a.tokens), e = b / a.bound_blocks, i0 = b % a.bound_blocks * (kBoundScales / 8);
         if (a.plan.expert_rows[e] == 0) return;
         // (an expert has a multiple of 256 of them)
@@ -169,7 +224,7 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
     }
     const int64_t t = blockIdx.x;
     if (PAIRS && t >= a.plan.tile_count[1]) return;
-    if (tid < a.top_k) to[tid] = PAIRS ? int(t) : a.plan.pair_row[t * a.top_k + tid];
+    if (!ROUTE && tid < a.top_k) to[tid] = PAIRS ? int(t) : a.plan.pair_row[t * a.top_k + tid];
     struct alignas(16) Group {
         T e[16];
     };
@@ -272,16 +327,28 @@ __global__ void __launch_bounds__(kSumThreads) moe_sum_kernel(MoeArgs a, MoePlan
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[j] = to_f32(r.e[j]);
     }
-    for (int j = 0; j < a.top_k; ++j) {
-        const int64_t p = t * a.top_k + j;
-        const int row = plan.pair_row[p];
-        if (row < 0) continue;
-        const float w = a.weight[p];
-        const float4 v = *reinterpret_cast<const float4 *>(y + int64_t(row) * a.width + c);
-        s[0] = fmaf(w, v.x, s[0]);
-        s[1] = fmaf(w, v.y, s[1]);
-        s[2] = fmaf(w, v.z, s[2]);
-        s[3] = fmaf(w, v.w, s[3]);
+    constexpr int U = 8;  // pairs whose loads are in flight together
+    for (int j0 = 0; j0 < a.top_k; j0 += U) {
+        int row[U];
+        float w[U];
+        float4 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int64_t p = t * a.top_k + min(j0 + j, a.top_k - 1);
+            row[j] = j0 + j < a.top_k ? plan.pair_row[p] : -1;
+            w[j] = a.weight[p];
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (row[j] >= 0) v[j] = *reinterpret_cast<const float4 *>(y + int64_t(row[j]) * a.width + c);
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+            if (row[j] >= 0) {
+                s[0] = fmaf(w[j], v[j].x, s[0]);
+                s[1] = fmaf(w[j], v[j].y, s[1]);
+                s[2] = fmaf(w[j], v[j].z, s[2]);
+                s[3] = fmaf(w[j], v[j].w, s[3]);
+            }
     }
     Four o;
 #pragma unroll
@@ -367,9 +434,13 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     const Workspace w(static_cast<char *>(ws), pairs, a.experts, a.width, a.ffn, dtype);
     const SoaView gate_up = soa_view(a.gate_up, int64_t(a.experts) * 2 * a.ffn, a.width);
     const SoaView down = soa_view(a.down, int64_t(a.experts) * a.width, a.ffn);
-    cudaError_t e = launch_plan(a, w, pairs, form, ctx);
+    const bool route = f8 && pairs <= kFewPairs;  // sorted by the blocks that stage them
+    cudaError_t e = route ? cudaSuccess : launch_plan(a, w, pairs, form, ctx);
     if (e != cudaSuccess) return e;
     StageArgs s = {};
+    s.expert = a.expert;
+    s.tile_rows = form.cols / form.terms;
+    s.status = ctx.status;
     s.plan = w.plan;
     s.staged = w.staged_x;
     s.scale = w.scale_x;
@@ -383,9 +454,10 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     s.terms = form.terms;
     s.experts = a.experts;
     const T *x = static_cast<const T *>(a.x);
-    const dim3 stage_grid(unsigned(a.tokens + int64_t(a.experts) * s.bound_blocks));
-    e = f8 ? launch_dependent(moe_stage_kernel<T, true, false>, stage_grid, kStageThreads, 0, ctx.stream, x, s)
-           : launch_dependent(moe_stage_kernel<T, false, false>, stage_grid, kStageThreads, 0, ctx.stream, x, s);
+    const dim3 stage_grid(unsigned(a.tokens + (route ? 1 : int64_t(a.experts) * s.bound_blocks)));
+    auto stage = route ? moe_stage_kernel<T, true, false, true>
+                       : f8 ? moe_stage_kernel<T, true, false, false> : moe_stage_kernel<T, false, false, false>;
+    e = launch_dependent(stage, stage_grid, kStageThreads, 0, ctx.stream, x, s);
     if (e != cudaSuccess) return e;
     MoeGemm g = {};
     g.plan = w.plan;
@@ -411,7 +483,7 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
         s.tokens = pairs;
         s.k = a.ffn;
         s.top_k = 1;
-        e = launch_dependent(moe_stage_kernel<float, true, true>, dim3(unsigned(pairs)), kStageThreads, 0, ctx.stream,
+        e = launch_dependent(moe_stage_kernel<float, true, true, false>, dim3(unsigned(pairs)), kStageThreads, 0, ctx.stream,
                              static_cast<const float *>(w.h), s);
         if (e != cudaSuccess) return e;
     }
