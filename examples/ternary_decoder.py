@@ -6,8 +6,10 @@ Every projection is a TQ2_0_g128 matmul; between them lie the rotary positions, 
     cache <- rotated k, v; q rotated         tq2.kv_append
     a = attention of q over the cache        tq2.attention_paged (f32 out, straight into the next projection)
     x += a Wo; x += swiglu(x Wgu) Wd         tq2.matmul, tq2.tq2_gate_up_swiglu
+    or, with experts: x += mixture of them   tq2.moe_route (of a ternary router's logits), tq2.moe_swiglu
+    the next token of the logits             argmax, or tq2.sample
 
-A batch of prompts of different lengths is read in chunks, then decoded greedily, one token a sequence a step, each
+A batch of prompts of different lengths is read in chunks, then decoded, one token a sequence a step, each
 step one replay of a captured graph whose device tables (lengths, tokens) change between replays.  ``joint_tokens``
 is the image model's use of the same rotation: q, k and v of one fused projection, rotated by (text, row, column)
 positions into the head-major operands of the joint attention.
@@ -45,14 +47,21 @@ def norm(x):
 
 
 class Decoder:
-    def __init__(self, layers=4, heads=8, kv_heads=2, dim=64, ffn=1024, vocab=1024, seed=0):
+    def __init__(self, layers=4, heads=8, kv_heads=2, dim=64, ffn=1024, vocab=1024, seed=0, experts=0, top_k=2):
+        """experts: how many of ffn features each layer mixes, top_k of them a token (0: one MLP for all)."""
         gen = torch.Generator(device="cuda").manual_seed(seed)
         self.heads, self.kv_heads, self.dim, self.width, self.vocab, self.ffn = heads, kv_heads, dim, heads * dim, vocab, ffn
         self.embed = torch.randn((vocab, self.width), device="cuda", generator=gen)
         rows = (heads + 2 * kv_heads) * dim
+        self.experts, self.top_k = experts, top_k
+        many = max(1, experts)
         self.layers = [tuple(TernaryLinear(n, k, gen) for n, k in ((rows, self.width), (self.width, self.width),
-                                                                  (2 * ffn, self.width), (self.width, ffn)))
+                                                                  (many * 2 * ffn, self.width), (many * self.width, ffn)))
                        for _ in range(layers)]
+        if experts:
+            self.routers = [TernaryLinear(experts, self.width, gen) for _ in range(layers)]
+            self.mixtures = [tq2.Experts(gate_up.w, down.w, experts=experts, width=self.width, ffn=ffn)
+                             for _, _, gate_up, down in self.layers]
         self.head = TernaryLinear(vocab, self.width, gen)
         self.rope = tq2.Rope([10_000.0 ** (-2 * i / dim) for i in range(dim // 2)])
 
@@ -65,11 +74,16 @@ class Decoder:
         """Logits [tokens, vocab] of a step's new tokens (int64 on the device), whose keys join the caches."""
         x = self.embed[tokens]
         h, g, d = self.heads, self.kv_heads, self.dim
-        for (qkv, out, gate_up, down), cache in zip(self.layers, caches):
+        for i, ((qkv, out, gate_up, down), cache) in enumerate(zip(self.layers, caches)):
             q, k, v = (t.unflatten(-1, (-1, d)) for t in qkv(norm(x)).split([h * d, g * d, g * d], -1))
             q = tq2.kv_append(k, v, cache, batch, rope=self.rope, q=q)
             a = tq2.attention_paged(q, cache, batch, out=torch.empty((len(x), h, d), device="cuda"))
             x = out(a.view(len(x), -1), x)
+            if self.experts:
+                y = norm(x)
+                expert, weight = tq2.moe_route(self.routers[i](y), self.top_k)
+                x = tq2.moe_swiglu(self.mixtures[i], y, expert, weight, residual=x)
+                continue
             act = torch.empty((len(x), self.ffn), device="cuda")
             tq2.tq2_gate_up_swiglu(gate_up.w, norm(x), act, len(x), self.ffn, self.width)
             x = down(act, x)
@@ -94,8 +108,15 @@ class Sequences:
                               max_kv=self.room)
 
 
-def generate(model, prompts, new, chunk=64):
-    """Greedy continuation [sequences, new] of prompts (lists of token ids), and the caches' last logits."""
+def generate(model, prompts, new, chunk=64, sampling=None):
+    """Continuation [sequences, new] of prompts (lists of token ids), and a step's milliseconds: greedy, or drawn with the
+    filters of ``sampling`` (keyword arguments of tq2.sample)."""
+
+    def choose(logits):
+        if sampling is None:
+            return logits.argmax(-1)
+        return tq2.sample(logits, torch.rand(len(logits), device="cuda"), **sampling)[0]
+
     seqs = Sequences(len(prompts), max(map(len, prompts)) + new)
     caches = model.new_caches(seqs.pages)
     last = [None] * len(prompts)
@@ -107,7 +128,7 @@ def generate(model, prompts, new, chunk=64):
             end += len(p)
             if p:
                 last[b] = logits[end - 1]
-    token = torch.stack(last).argmax(-1)
+    token = choose(torch.stack(last))
     # decoding: one graph, replayed with the lengths and tokens that the last replay left
     step = seqs.batch([1] * len(prompts))
     out = torch.empty((new, len(prompts)), dtype=torch.int64, device="cuda")
@@ -115,7 +136,7 @@ def generate(model, prompts, new, chunk=64):
 
     def one():
         out.index_copy_(0, row, token[None])
-        token.copy_(model.step(token, caches, step).argmax(-1))
+        token.copy_(choose(model.step(token, caches, step)))
         seqs.kv_len.add_(1)
         row.add_(1)
 
@@ -162,6 +183,12 @@ def main():
     tokens, ms = generate(model, prompts, 64)
     for p, row in zip(prompts, tokens.tolist()):
         print(f"{len(p):4d} tokens -> {row[:12]} ...")
+    print(f"{ms:.3f} ms a step, {len(prompts) / ms * 1e3:.0f} tokens/s")
+    mixture = Decoder(ffn=512, experts=8)
+    each = lambda v, t=torch.float32: torch.full((len(prompts),), v, dtype=t, device="cuda")  # noqa: E731
+    tokens, ms = generate(mixture, prompts, 64, sampling=dict(temperature=each(0.8), top_k=each(40, torch.int32), top_p=each(0.95)))
+    for p, row in zip(prompts, tokens.tolist()):
+        print(f"{len(p):4d} tokens -> {row[:12]} ... (8 experts, sampled)")
     print(f"{ms:.3f} ms a step, {len(prompts) / ms * 1e3:.0f} tokens/s")
     print("joint attention:", tuple(joint_tokens(torch.randn(77 + 256, 3 * 4 * 64, device="cuda"), 4, 64, 77, 16).shape))
     assert tq2.tq2_device_status() == tq2.TQ2_OK

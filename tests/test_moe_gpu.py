@@ -339,3 +339,49 @@ def test_uploaded_weights(tq2, dtype):
         tq2.moe_swiglu(layer.dev, x, torch.from_numpy(expert).cuda(), torch.from_numpy(weight[:3]).cuda())
     with pytest.raises(ValueError):
         tq2.moe_swiglu(layer.dev, x, torch.from_numpy(expert).cuda().long(), torch.from_numpy(weight).cuda())
+
+
+@pytest.mark.parametrize("dtype,tokens", [("f32", 5), ("bf16", 5), ("f16", 300), ("f32", 300)])
+def test_a_wait_that_runs_out_is_reported_and_the_context_goes_on(tq2, dtype, tokens):
+    layer = Layer(tq2, 4, 512, 384, seed=30)
+    x, r, expert, weight, good = run(tq2, layer, dtype, tokens, 2, seed=31)
+    e, w = torch.from_numpy(expert).cuda(), torch.from_numpy(weight).cuda()
+    limit = tq2.tq2_set_wait_timeout_ns(0)
+    try:
+        for _ in range(3):
+            tq2.moe_swiglu(layer.dev, x, e, w, residual=r)
+        assert tq2.tq2_device_status() in (tq2.TQ2_ERR_TIMEOUT, tq2.TQ2_OK)  # (a wait may find its phase in time)
+    finally:
+        tq2.tq2_set_wait_timeout_ns(limit)
+    again = tq2.moe_swiglu(layer.dev, x, e, w, residual=r)
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
+    assert torch.equal(again, good)
+
+
+def test_a_decoder_with_experts_and_sampling(tq2):
+    """Greedy decoding by graph replays follows the logits of one pass; sampling at temperature 0 is greedy decoding, and with
+    a top-k draws from the k best."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "ternary_decoder.py")
+    spec = importlib.util.spec_from_file_location("ternary_decoder", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    model = ex.Decoder(layers=2, ffn=256, vocab=256, experts=6)
+    rng = np.random.default_rng(0)
+    prompts = [rng.integers(0, 256, n).tolist() for n in (70, 5, 33)]
+    each = lambda v, t=torch.float32: torch.full((3,), v, dtype=t, device="cuda")  # noqa: E731
+    greedy, _ = ex.generate(model, prompts, 6, chunk=32)
+    cold, _ = ex.generate(model, prompts, 6, chunk=32, sampling=dict(temperature=each(0.0)))
+    assert torch.equal(greedy, cold)
+    drawn, _ = ex.generate(model, prompts, 6, chunk=32, sampling=dict(top_k=each(3, torch.int32)))
+    for rows, most in ((greedy.tolist(), 1), (drawn.tolist(), 3)):
+        for p, row in zip(prompts, rows):
+            text = p + row
+            seqs = ex.Sequences(1, len(text))
+            logits = model.step(torch.tensor(text, device="cuda"), model.new_caches(seqs.pages), seqs.batch([len(text)]))
+            for i, got in enumerate(row):
+                at = logits[len(p) - 1 + i].double()
+                # (near ties: activations in binary16, a cache in bf16, and experts chosen by logits that those move)
+                assert at.topk(most).values[-1] - at[got] <= 0.25 * at.std(), (len(p), i)
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
