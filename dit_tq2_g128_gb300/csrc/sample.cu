@@ -9,7 +9,7 @@
 //  * The head: a bound that at least k (or a few hundred) of the maxima of groups of threads reach; the few elements above it go
 //    to the first CTA, which sorts them and answers every question from their cumulative weights, if they reach that far:
 //    with a top-k always, without one where the distribution is as peaked as a model's usually is.
-//  * Else: a histogram of counts and weights over bins of log2 of the weight finds the bin that an answer lies in; its
+//  * Else: a histogram of counts and weights over bins of log2 of the weight (its shared atomics are most of the work) finds the bin that an answer lies in; its
 //    elements (at most 1024, or split further by their bits) are sorted as the head is.
 //
 // Bound by latency for one row (cluster barriers and the sort), by the arithmetic of the weights and their atomics for many.
@@ -39,7 +39,7 @@ struct Command {
     uint32_t rank;       // OP_TIE: which of the elements `low`, from 0
 };
 
-struct Shared {
+struct alignas(16) Shared {  // (the row follows it, in packs of 16 bytes)
     // Weights of bins.  While they are counted, in three pieces of 15 bits and more (a 64-bit atomic is a loop here, and
     // 2^15 of a piece fit 32 bits); then, in the first CTA, the low and the high word of their sum over the CTAs.
     uint32_t mass[3][kBins];
