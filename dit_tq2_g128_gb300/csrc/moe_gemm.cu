@@ -375,9 +375,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                         const bool d_free = phase_over(&ctl->d_empty[sd], pd), x_there = phase_over(&ctl->x_full[sx], px),
                                    a_there = phase_over(&ctl->a_full[s], pa);
                         if (__all_sync(0xffffffffu, d_free && x_there && a_there)) break;
-                        if (polls == 256)  // (some 20 us)
+                        if (polls == 4)
                             ok = wait_on(&ctl->d_empty[sd], pd) && wait_on(&ctl->x_full[sx], px) && wait_on(&ctl->a_full[s], pa);
-                        if (polls == 256) break;
+                        if (polls == 4) break;
                     }
                     if (!ok) break;
                     tc_fence_after();
