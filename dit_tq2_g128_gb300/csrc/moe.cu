@@ -104,10 +104,7 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
     if (rank == 0) {
         for (int i = 0; i < n_tiles; ++i)
             plan.tiles[tile0 + i] = MoeTile{tid, at + i * tile_rows, min(tile_rows, total - i * tile_rows), 0};
-        if (tid < experts) {
-            plan.expert_rows[tid] = total;
-            plan.bound[tid] = 0;
-        }
+        if (tid < experts) plan.expert_rows[tid] = total;
         if (tid == 0) {
             plan.tile_count[0] = tiles;
             plan.tile_count[1] = rows;
@@ -149,10 +146,10 @@ struct StageArgs {
 // Stages a token a block: the terms of its row times the power of two that brings its largest value between 2^14 and 2^15
 // (no value overflows, and one 2^-28 of the largest still has all its bits; e4m3: between 2^7 and 2^8), in the products'
 // order, to the rows of all its pairs; scale is the power that undoes it.  Of a row with an infinity or a NaN, e4m3 terms
-// hold neither: its scale is NaN.  The blocks behind the tokens' take the largest block scales of the experts that have
-// tokens.  PAIRS: the rows are of pairs already (hidden values).
+// hold neither: its scale is NaN.  The blocks behind the tokens' take the largest of some of the block scales of an expert
+// that has tokens.  PAIRS: the rows are of pairs already (hidden values).
 // ROUTE: the pairs (at most kFewPairs) are not sorted yet: each token's block finds the rows of its pairs by counting those
-// before them, and the block behind the tokens' writes the tiles.
+// before them, and the first block behind the tokens' writes the tiles.
 template <typename T, bool F8, bool PAIRS, bool ROUTE>
 __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
     __shared__ float part[2][kStageThreads / 32];
@@ -160,11 +157,37 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __shared__ int id[ROUTE ? kFewPairs : 1];
+    const int pairs = ROUTE ? int(a.tokens) * a.top_k : 0;
     if constexpr (ROUTE) {
-        __shared__ int id[kFewPairs], count[1024], sums[32];
-        const int pairs = int(a.tokens) * a.top_k;
         for (int i = tid; i < pairs; i += kStageThreads) id[i] = a.expert[i];
-        if (blockIdx.x == a.tokens) {
+    }
+    if (blockIdx.x >= a.tokens + ROUTE) {
+        const int b = int(blockIdx.x - a.tokens - ROUTE), e = b / a.bound_blocks, i0 = b % a.bound_blocks * (kBoundScales / 8);
+        bool there = !ROUTE && a.plan.expert_rows[e] > 0;
+        for (int i = tid; i < pairs; i += kStageThreads) there |= id[i] == e;  // (this thread's own)
+        if (!__syncthreads_or(there)) return;
+        // (an expert has a multiple of 256 of them)
+        const uint4 *d = reinterpret_cast<const uint4 *>(a.d + e * a.d_count);
+        uint32_t top = 0;
+#pragma unroll 4
+        for (int i = i0 + tid; i < min(i0 + kBoundScales / 8, int(a.d_count / 8)); i += kStageThreads) {
+            const uint4 v = d[i];
+            for (uint32_t w : {v.x, v.y, v.z, v.w}) top = max(top, max(w & 0x7fffu, w >> 16 & 0x7fffu));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        if (lane == 0) part[0][warp] = __half2float(__ushort_as_half(uint16_t(top)));
+        __syncthreads();
+        if (tid == 0) {
+            uint32_t most = 0;  // (of bits: a NaN is above all)
+            for (int w = 0; w < kStageThreads / 32; ++w) most = max(most, __float_as_uint(part[0][w]));
+            a.plan.bound[b] = most;
+        }
+        return;
+    }
+    if constexpr (ROUTE) {
+        __shared__ int count[1024], sums[32];
+        if (int64_t(blockIdx.x) == a.tokens) {
             for (int e = tid; e < 1024; e += kStageThreads) count[e] = 0;
             __syncthreads();
             for (int i = tid; i < pairs; i += kStageThreads) {
@@ -207,20 +230,6 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
             if (e < 0 || e >= a.experts) to[tid] = -1;
             a.plan.pair_row[p] = to[tid];
         }
-    } else if (blockIdx.x >= a.tokens) {
-        const int b = int(blockIdx.x - a.tokens), e = b / a.bound_blocks, i0 = b % a.bound_blocks * (kBoundScales / 8);
-        if (a.plan.expert_rows[e] == 0) return;
-        // (an expert has a multiple of 256 of them)
-        const uint4 *d = reinterpret_cast<const uint4 *>(a.d + e * a.d_count);
-        uint32_t top = 0;
-#pragma unroll 4
-        for (int i = i0 + tid; i < min(i0 + kBoundScales / 8, int(a.d_count / 8)); i += kStageThreads) {
-            const uint4 v = d[i];
-            for (uint32_t w : {v.x, v.y, v.z, v.w}) top = max(top, max(w & 0x7fffu, w >> 16 & 0x7fffu));
-        }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) atomicMax(&a.plan.bound[e], __float_as_uint(__half2float(__ushort_as_half(uint16_t(top)))));
-        return;
     }
     const int64_t t = blockIdx.x;
     if (PAIRS && t >= a.plan.tile_count[1]) return;
@@ -377,7 +386,7 @@ struct Workspace {
     MoePlan plan;
     uint8_t *staged_x, *staged_h;
     float *scale_x, *scale_h, *sum_x, *h, *y;
-    int max_tiles;
+    int max_tiles, bound_blocks;  // bound_blocks: of an expert's block scales
     size_t bytes;
 
     // (Sizes are the largest that any form of this many pairs, or of fewer, takes.)
@@ -394,7 +403,8 @@ struct Workspace {
         take(plan.tiles, size_t(std::min(pairs, experts) + pairs / 16));
         take(plan.pair_row, size_t(pairs));
         take(plan.expert_rows, size_t(experts));
-        take(plan.bound, size_t(experts));
+        bound_blocks = int((2 * ffn * (width / kBlockW) + kBoundScales - 1) / kBoundScales);
+        take(plan.bound, size_t(experts * bound_blocks));
         take(scale_x, size_t(pairs));
         take(scale_h, size_t(pairs));
         take(sum_x, size_t(pairs));
@@ -434,7 +444,7 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     const Workspace w(static_cast<char *>(ws), pairs, a.experts, a.width, a.ffn, dtype);
     const SoaView gate_up = soa_view(a.gate_up, int64_t(a.experts) * 2 * a.ffn, a.width);
     const SoaView down = soa_view(a.down, int64_t(a.experts) * a.width, a.ffn);
-    const bool route = f8 && pairs <= kFewPairs;  // sorted by the blocks that stage them
+    const bool route = pairs <= kFewPairs;  // sorted by the blocks that stage them
     cudaError_t e = route ? cudaSuccess : launch_plan(a, w, pairs, form, ctx);
     if (e != cudaSuccess) return e;
     StageArgs s = {};
@@ -447,16 +457,16 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     s.sum = w.sum_x;
     s.d = gate_up.d;
     s.d_count = int64_t(2) * a.ffn * (a.width / kBlockW);
-    s.bound_blocks = f8 ? 0 : int((s.d_count + kBoundScales - 1) / kBoundScales);
+    s.bound_blocks = f8 ? 0 : w.bound_blocks;
     s.tokens = a.tokens;
     s.k = a.width;
     s.top_k = a.top_k;
     s.terms = form.terms;
     s.experts = a.experts;
     const T *x = static_cast<const T *>(a.x);
-    const dim3 stage_grid(unsigned(a.tokens + (route ? 1 : int64_t(a.experts) * s.bound_blocks)));
-    auto stage = route ? moe_stage_kernel<T, true, false, true>
-                       : f8 ? moe_stage_kernel<T, true, false, false> : moe_stage_kernel<T, false, false, false>;
+    const dim3 stage_grid(unsigned(a.tokens + route + int64_t(a.experts) * s.bound_blocks));
+    auto stage = f8 ? route ? moe_stage_kernel<T, true, false, true> : moe_stage_kernel<T, true, false, false>
+                    : route ? moe_stage_kernel<T, false, false, true> : moe_stage_kernel<T, false, false, false>;
     e = launch_dependent(stage, stage_grid, kStageThreads, 0, ctx.stream, x, s);
     if (e != cudaSuccess) return e;
     MoeGemm g = {};
@@ -466,6 +476,7 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     g.terms = form.terms;
     g.cols = form.cols;
     g.max_tiles = w.max_tiles;
+    g.bound_blocks = w.bound_blocks;
     g.qs = gate_up.qs;
     g.d = gate_up.d;
     g.staged = w.staged_x;

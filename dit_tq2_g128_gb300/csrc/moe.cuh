@@ -19,7 +19,7 @@ struct MoePlan {
     MoeTile *tiles;
     int *pair_row;        // [pairs] row of each pair, -1: none
     int *expert_rows;     // [experts]
-    uint32_t *bound;      // [experts] largest |d| of the gate and up rows (the bits of an f32)
+    uint32_t *bound;      // [experts][bound_blocks] largest |d| among some of an expert's gate and up rows (the bits of an f32)
 };
 
 // One ternary product of the layer: of staged activations (see moe_stage_kernel) with the rows of each tile's expert.
@@ -37,7 +37,7 @@ struct MoeGemm {
     int experts, rows, k;
     int terms;           // staged rows of a row
     int cols;            // staged rows (MMA columns) of a tile, at most: 32, 64 or 96, or 48 with three terms
-    int max_tiles;
+    int max_tiles, bound_blocks;
 };
 // gate_up: rows counts gate then up rows, and the SwiGLU of rows / 2 features is staged; else out is the product.
 cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx);

@@ -480,6 +480,11 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             const __half *dp = g.d + int64_t(row) * nb;
             // the scales of the tile's rows, some in each lane
             const int left = it.tile.n;
+            uint32_t bound = 0;
+            if (GATE_UP && !L::F8) {
+                for (int j = lane; j < g.bound_blocks; j += 32) bound = max(bound, g.plan.bound[it.tile.expert * g.bound_blocks + j]);
+                bound = __reduce_max_sync(0xffffffffu, bound);
+            }
             float scale[COLS / 32], up[COLS / 32];  // up (gate_up): the power of two that the hidden values are staged with
 #pragma unroll
             for (int j = 0; j < COLS / 32; ++j) {
@@ -487,7 +492,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 scale[j] = g.scale[at];
                 if (GATE_UP && !L::F8) {
                     // |gate|, |up| <= bound * sum < 2^(e + 1), so that a hidden value times 2^(13 - 2 e) is below 2^15
-                    const float b = __uint_as_float(g.plan.bound[it.tile.expert]) * g.sum[at];
+                    const float b = __uint_as_float(bound) * g.sum[at];
                     const int e = b < INFINITY ? max(min(13 - 2 * moe_log2(b), 126), -126) : 0;
                     up[j] = moe_power(e);
                     if (it.part == 0 && q == 0) g.scale_out[at] = moe_power(-e);
