@@ -7,7 +7,6 @@
 
 namespace tq2 {
 
-
 // Some tokens of one expert: rows row0 .. row0 + n - 1 of those sorted by expert.
 struct alignas(16) MoeTile {
     int expert, row0, n, unused;
@@ -15,7 +14,7 @@ struct alignas(16) MoeTile {
 
 // Device tables of one call, from its routing: `rows` (token, expert) pairs sorted by expert, and their tiles.
 struct MoePlan {
-    int *tile_count;
+    int *tile_count;      // [2]: tiles, rows
     MoeTile *tiles;
     int *pair_row;        // [pairs] row of each pair, -1: none
     int *expert_rows;     // [experts]
@@ -45,9 +44,9 @@ cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx
 // Terms of a staged value v, scaled by a power of two to below 2^15 (2^8 for e4m3):
 //   1: binary16(v).   2: also binary16(v - first).
 //   3: e4m3 numbers t0, t1, t2 with v = t0 + t1 / 16 + t2 / 256: each rounds to four bits what is left, so that they hold
-//      twelve: all of a binary16's or bf16's (down to 2^-25 of the largest), and others to 2^-12.
-// Three 8-bit terms where experts have few tokens: an MMA takes twice as many 8-bit weights as 16-bit ones in the same time,
-// 64 cycles for its A operand's 4 KB from tensor memory however few columns it has.
+//      twelve: all of a binary16's or bf16's (down to 2^-25 of the largest value), and others to 2^-12.
+// Three 8-bit terms where experts have few tokens: an MMA of few columns takes as long for 32 weights of a row in 8 bits as
+// for 16 in 16 bits, and decoding to 8 bits is half the stores and no subtraction.
 //
 // Order of staged activations: a binary16 row holds elements i and i + 8 of each group of 16 at 2 i and 2 i + 1, as pairs of
 // codes are masked out of a word of 16 (the library's binary16 activation layout).  An e4m3 row holds the even and the odd elements

@@ -532,7 +532,7 @@ size_t tq2_attention_paged_workspace_bytes(int64_t heads, const tq2_kv_cache *ca
  *     weights[t, j] = scale * s_i              (i = experts[t, j])
  *     normalize != 0: divided by the sum of s over the token's top_k.
  * A logit of -inf (a masked expert) has s = 0; where all of a token's are -inf its
- * weights are 0.  A NaN or an infinite logit makes weights of its token NaN.
+ * weights are 0.  NaN and +inf go through the formulas: what they enter is NaN.
  *   logits     : device, of type dtype (tq2_dtype), row t from element t * row_stride
  *                on (row_stride >= n_experts; any for one token); aligned to its element
  *   experts    : device int32 [tokens, top_k]
@@ -570,8 +570,8 @@ typedef struct {
  * gate_up, down, x, residual and out are 16-byte aligned.
  * Arithmetic: weights exact; activations as sums of terms that the tensor cores
  * multiply: of f32 ones two in binary16 (2^-22 of a value), of 16-bit ones one in binary16
- * or, where experts have 16 rows or fewer in the mean, three in e4m3 (which hold all bits of
- * those that are not below 2^-25 of their row's largest); so too the hidden values
+ * or, where experts have 16 rows or fewer in the mean, three in e4m3 (which hold their bits
+ * down to 2^-25 of the row's largest value); so too the hidden values
  * silu(.) * (.), to 2^-11 of themselves (f32: 2^-22).  Any magnitudes are in range.  Sums in f32,
  * one rounding to the output's type.  A token's result may differ in its rounding with the
  * number of tokens of the call.
