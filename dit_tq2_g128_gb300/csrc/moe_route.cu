@@ -7,7 +7,7 @@
 // A warp takes a token: each lane holds NV logits as integers in the order of their values; top_k times the warp's
 // maximum (one redux) and the lowest index that holds it (another).
 //
-// Bound by issue slots: 8 of 256 bf16 logits of 8191 tokens (4.2 MB read) take 10.1 us, some 900 instructions a token; one
+// Bound by issue slots: 8 of 256 bf16 logits of 8191 tokens (4.2 MB read) take 10.1 us, 793 warp instructions a token, 57 % of the issue slots; one
 // token 1.9 us, its launch.  Calls from Python take 13 us (two new tensors, the checks and the launch).
 #include <cstdint>
 
