@@ -7,8 +7,8 @@
 // A warp takes a token: each lane holds NV logits as integers in the order of their values; top_k times the warp's
 // maximum (one redux) and the lowest index that holds it (another).
 //
-// Bound by issue slots: 8 of 256 bf16 logits of 8191 tokens (4.2 MB read) take 10.1 us, 793 warp instructions a token, 57 % of the issue slots; one
-// token 1.9 us, its launch.  Calls from Python take 13 us (two new tensors, the checks and the launch).
+// Bound by issue slots: 8 of 256 bf16 logits of 8191 tokens (4.2 MB read) take 10.1 us, 793 warp instructions a token, 57 %
+// of the issue slots; one token 1.9 us, its launch.  Calls from Python take 15 us (two new tensors, the checks and the launch).
 #include <cstdint>
 
 #include "dtype.cuh"
@@ -36,8 +36,13 @@ moe_route_kernel(const T *__restrict__ logits, int64_t row_stride, int32_t *__re
         key[j] = i < n ? order_key(to_f32(row[i])) : 0u;  // 0: none, or taken
     }
     uint32_t best = 0;
+    bool nan = false;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) best = max(best, key[j]);
+    for (int j = 0; j < NV; ++j) {
+        best = max(best, key[j]);
+        nan |= key[j] == order_key(__uint_as_float(0x7fc00000u));
+    }
+    nan = __any_sync(0xffffffffu, nan);
     const float top = key_value(__reduce_max_sync(0xffffffffu, best));
     float z = 1.f;  // the softmax's denominator
     if (!sigmoid && !normalize) {
@@ -73,9 +78,8 @@ moe_route_kernel(const T *__restrict__ logits, int64_t row_stride, int32_t *__re
             value = key_value(m);
         }
     }
-    // a row without a logit above -inf: weights of 0
     float s = 0.f;
-    if (lane < top_k && top != -INFINITY) {
+    if (lane < top_k && value != -INFINITY) {
         if (!sigmoid) {
             s = expf(value - top);
         } else if (!(value < 0.f)) {
@@ -92,7 +96,10 @@ moe_route_kernel(const T *__restrict__ logits, int64_t row_stride, int32_t *__re
     }
     if (lane < top_k) {
         experts[t * top_k + lane] = mine;
-        weights[t * top_k + lane] = s == 0.f ? 0.f : (sigmoid && !normalize ? s : s / sum) * scale;
+        float w = s == 0.f && !(sum != sum) ? 0.f : (sigmoid && !normalize ? s : s / sum) * scale;
+        if (top == -INFINITY && !nan) w = 0.f;                            // nothing but -inf
+        if (!sigmoid && (nan || top == INFINITY)) w = __uint_as_float(0x7fc00000u);  // (in the softmax's sum, chosen or not)
+        weights[t * top_k + lane] = w;
     }
 }
 

@@ -532,13 +532,16 @@ size_t tq2_attention_paged_workspace_bytes(int64_t heads, const tq2_kv_cache *ca
  *     weights[t, j] = scale * s_i              (i = experts[t, j])
  *     normalize != 0: divided by the sum of s over the token's top_k.
  * A logit of -inf (a masked expert) has s = 0; where all of a token's are -inf its
- * weights are 0.  NaN and +inf go through the formulas: what they enter is NaN.
+ * weights are 0 (of sigmoids, where all that are chosen are).  NaN and +inf go through the
+ * formulas: a softmax with one makes all of its token's weights NaN; a sigmoid of NaN is NaN
+ * (if normalised, with all that it is chosen with), of +inf 1.
  *   logits     : device, of type dtype (tq2_dtype), row t from element t * row_stride
  *                on (row_stride >= n_experts; any for one token); aligned to its element
  *   experts    : device int32 [tokens, top_k]
  *   weights    : device f32 [tokens, top_k]
  *   n_experts  : 1 .. 1024;  top_k : 1 .. min(n_experts, 32)
  *   scale      : finite
+ *   tokens     : up to 2^24
  * Scores and sums in f32.  No output may overlap another argument.  tokens == 0 is a
  * no-op. */
 int tq2_moe_route(const void *logits, int dtype, int64_t row_stride, int32_t *experts, float *weights, int64_t tokens,
@@ -564,16 +567,18 @@ typedef struct {
  *   x        : device [tokens, width] of type dtype (tq2_dtype)
  *   expert   : device int32 [tokens, top_k] (from tq2_moe_route)
  *   weight   : device f32 [tokens, top_k]
- *   residual : device [tokens, width] of type dtype, or NULL; may equal out
+ *   residual : device [tokens, width] of type dtype, or NULL; may equal out, and x
  *   out      : device [tokens, width] of type dtype
  *   top_k    : 1 .. 32; tokens * top_k <= 2^22
- * gate_up, down, x, residual and out are 16-byte aligned.
+ * gate_up, down, x, residual and out are 16-byte aligned.  out overlaps nothing else.
  * Arithmetic: weights exact; activations as sums of terms that the tensor cores
- * multiply: of f32 ones two in binary16 (2^-22 of a value), of 16-bit ones one in binary16
- * or, where experts have 16 rows or fewer in the mean, three in e4m3 (which hold their bits
- * down to 2^-25 of the row's largest value); so too the hidden values
- * silu(.) * (.), to 2^-11 of themselves (f32: 2^-22).  Any magnitudes are in range.  Sums in f32,
- * one rounding to the output's type.  A token's result may differ in its rounding with the
+ * multiply: of f32 ones two in binary16 (2^-22 of a value, or 2^-39 of the row's largest), of
+ * 16-bit ones one in binary16 (which holds their bits down to 2^-38 of the row's largest value)
+ * or, where experts have 16 rows or fewer in the mean, three in e4m3 (to 2^-25 of it).
+ * So too the hidden values h = silu(.) * (.): to 2^-11 of themselves (f32: 2^-22), or, where more,
+ * 2^-38 of (the largest block scale of the expert's gate_up times sum |x|)^2; of few rows an
+ * expert, 2^-12 of themselves or 2^-25 of the pair's largest.  No magnitude overflows on its
+ * way that the formula in f32 does not.  Sums in f32, one rounding to the output's type.  A token's result may differ in its rounding with the
  * number of tokens of the call.
  * Memory: `workspace` holds the activations on their way
  * (tq2_moe_swiglu_workspace_bytes of the same arguments, 16-byte aligned); if NULL, a
@@ -605,7 +610,8 @@ typedef struct {
  *     min_p of these the tokens with w_i >= min_p;
  * drawn is the first token whose cumulative weight is above u times what is kept.
  * prob is its weight over what is kept.
- * A logit of -inf or NaN has weight 0; where a row holds nothing else, its token is -1
+ * A logit of -inf or NaN has weight 0 (and one so far below that l_max - l is not an f32);
+ * where a row holds nothing else, its token is -1
  * and prob 0.  Among infinite logits only these count.
  *   logits : device, of type dtype (tq2_dtype), row r from element r * row_stride on
  *            (row_stride >= vocab; any for one row); aligned to its element
@@ -613,7 +619,7 @@ typedef struct {
  *            nearest in it, NaN as 0)
  *   tokens : device int64 [rows]
  *   prob   : device f32 [rows], or NULL
- *   vocab  : 1 .. 262144
+ *   vocab  : 1 .. 262144;  rows : up to 2^24
  * Weights are integers in units of 2^-45 (a smaller one is 0), each within 2^-30 of
  * itself; their sums are exact, so that results do not depend on any order of summation.
  * No output may overlap another argument.  rows == 0 is a no-op. */

@@ -22,7 +22,10 @@ def route(logits, top_k, sigmoid=False, normalize=True, scale=1.0):
         s = np.take_along_axis(s, experts.astype(np.int64), 1)
         if normalize:
             s = s / s.sum(1, keepdims=True)
-    s[np.all(logits == -np.inf, axis=1)] = 0.0
+    none = np.all(logits == -np.inf, axis=1)
+    if sigmoid:
+        none |= np.all(np.take_along_axis(logits, experts.astype(np.int64), 1) == -np.inf, axis=1)
+    s[none] = 0.0
     return experts, s * scale
 
 

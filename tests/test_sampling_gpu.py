@@ -82,6 +82,23 @@ def test_route_nan_comes_last(tq2):
     assert np.array_equal(np.isnan(w), np.isnan(np.take_along_axis(x, e.cpu().numpy().astype(int), 1)))
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("k", [1, 2, 4])
+def test_route_nan_and_infinity_go_through_the_formulas(tq2, sigmoid, normalize, k):
+    """A softmax has them in its sum, chosen or not; sigmoids only where they are chosen."""
+    x = np.random.default_rng(17).standard_normal((9, 40)).astype(np.float32)
+    x[0, 7] = NAN
+    x[1, 39] = INF
+    x[2, :2] = INF
+    x[3], x[3, 5] = -INF, NAN
+    x[4], x[4, 38:] = -INF, (INF, NAN)
+    x[5], x[5, 3] = NAN, 1.0
+    x[6] = NAN
+    x[7], x[7, 4:7] = -INF, NAN
+    check_route(tq2, torch.from_numpy(x).cuda(), k, sigmoid, normalize, 1.5)
+
+
 def test_route_given_outputs_stream_and_replay(tq2):
     rng = np.random.default_rng(6)
     x = logits_of(rng, 40, 100, "bf16")
