@@ -204,6 +204,10 @@ def test_in_place_residual_no_workspace_and_same_bits(tq2, dtype, tokens):
         place = r.clone()
         assert tq2.moe_swiglu(layer.dev, x, e, w, residual=place, out=place) is place
         assert torch.equal(place, out)
+    own = tq2.moe_swiglu(layer.dev, x, e, w, residual=x)
+    place = x.clone()
+    tq2.moe_swiglu(layer.dev, place, e, w, residual=place, out=place)
+    assert torch.equal(place, own)
 
 
 @pytest.mark.parametrize("dtype,tokens", [("f16", 3), ("f16", 32), ("bf16", 3), ("bf16", 32), ("f32", 3), ("f32", 150)])
@@ -291,6 +295,92 @@ def test_larger_workspace_serves_fewer_tokens(tq2):
         expert, weight = routed(rng, tokens, 4, 2)
         out = tq2.moe_swiglu(layer.dev, x, torch.from_numpy(expert).cuda(), torch.from_numpy(weight).cuda(), workspace=ws)
         check(layer, out, "bf16", x, expert, weight)
+
+
+class Drawn:
+    """A layer of random bytes drawn on the device; some experts' matrices for the oracle."""
+
+    def __init__(self, tq2, experts, width, ffn, held):
+        g = torch.Generator(device="cuda").manual_seed(experts)
+        self.n, self.width, self.ffn, self.gu, self.dn = experts, width, ffn, {}, {}
+        dev = []
+        for rows, cols, to in ((2 * ffn, width, self.gu), (width, ffn, self.dn)):
+            codes, blocks = rows * cols // 4, rows * cols // 128
+            w = torch.empty(experts * (codes + 2 * blocks), dtype=torch.uint8, device="cuda")
+            w[:experts * codes].random_(0, 256, generator=g)
+            d = w[experts * codes:].view(torch.float16)
+            d.uniform_(0.3 * cols ** -0.5, 1.2 * cols ** -0.5, generator=g)
+            for e in held:
+                one = torch.cat([w[e * codes:(e + 1) * codes], d[e * blocks:(e + 1) * blocks].view(torch.uint8)])
+                to[e] = decode.matrices(one.cpu().numpy(), 1, rows, cols)[0]
+            dev.append(w)
+        self.dev = tq2.Experts(*dev, experts=experts, width=width, ffn=ffn)
+
+    def some(self, expert):
+        """The experts that `expert` names, and `expert` counting among these."""
+        held = sorted(self.gu)
+        part = type("Part", (), dict(gu=np.stack([self.gu[e] for e in held]), dn=np.stack([self.dn[e] for e in held]), ffn=self.ffn))
+        return part, np.searchsorted(held, expert)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_weights_past_32_bits(tq2, dtype):
+    """Codes of more than 2^32 bytes: the first and the last experts."""
+    layer, rng = Drawn(tq2, 1024, 2048, 4096, (0, 511, 1000, 1023)), np.random.default_rng(28)
+    x = torch.from_numpy(rng.standard_normal((6, 2048))).to(DTYPES[dtype]).cuda()
+    expert = np.array([[0, 1023], [1023, 511], [1000, 1023], [511, 0], [1023, 1000], [1000, 0]], np.int32)
+    weight = rng.uniform(0, 1, expert.shape).astype(np.float32)
+    out = tq2.moe_swiglu(layer.dev, x, torch.from_numpy(expert).cuda(), torch.from_numpy(weight).cuda())
+    part, among = layer.some(expert)
+    check(part, out, dtype, x, among, weight)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_activations_past_32_bits(tq2, dtype):
+    """Pairs times features of more than 2^31: the first and the last tokens."""
+    tokens, width = 300_000, 4096
+    layer = Layer(tq2, 2, width, 128, seed=29)
+    g = torch.Generator(device="cuda").manual_seed(30)
+    x = torch.empty((tokens, width), dtype=DTYPES[dtype], device="cuda").normal_(generator=g)
+    expert = torch.randint(0, 2, (tokens, 2), dtype=torch.int32, device="cuda", generator=g)
+    weight = torch.rand((tokens, 2), device="cuda", generator=g)
+    out = tq2.moe_swiglu(layer.dev, x, expert, weight)
+    at = [0, 1, 131_072, tokens // 2, tokens - 2, tokens - 1]
+    check(layer, out[at], dtype, x[at], expert[at].cpu().numpy(), weight[at].cpu().numpy())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_most_pairs_of_most_experts(tq2, dtype):
+    tokens, top_k, n = 1 << 17, 32, 1024
+    layer, rng = Layer(tq2, n, 128, 128, seed=31), np.random.default_rng(32)
+    x = torch.from_numpy(rng.standard_normal((tokens, 128)).astype(np.float32)).to(DTYPES[dtype]).cuda()
+    expert = ((rng.integers(0, n, (tokens, 1)) + rng.integers(0, n // 2, (tokens, 1)) * 2 * np.arange(top_k) + np.arange(top_k)) % n).astype(np.int32)
+    weight = rng.uniform(0, 1 / 16, (tokens, top_k)).astype(np.float32)
+    out = tq2.moe_swiglu(layer.dev, x, torch.from_numpy(expert).cuda(), torch.from_numpy(weight).cuda())
+    at = rng.integers(0, tokens, 60).tolist() + [0, tokens - 1]
+    check(layer, out[at], dtype, x[at], expert[at], weight[at])
+    assert bool(torch.isfinite(out).all()) and tq2.tq2_device_status() == tq2.TQ2_OK
+
+
+def test_calls_on_two_streams_at_once(tq2):
+    layers = [Layer(tq2, 8, 512, 256, seed=33), Layer(tq2, 4, 256, 640, seed=34)]
+    rng, streams = np.random.default_rng(35), [torch.cuda.Stream(), torch.cuda.Stream()]
+    calls = []
+    for layer, dtype, tokens in ((layers[0], "bf16", 30), (layers[1], "f32", 200)):
+        x = torch.from_numpy(rng.standard_normal((tokens, layer.width))).to(DTYPES[dtype]).cuda()
+        expert, weight = (torch.from_numpy(a).cuda() for a in routed(rng, tokens, layer.n, 2))
+        logits, u = torch.from_numpy(rng.standard_normal((tokens, 20_000))).cuda().float(), torch.rand(tokens, device="cuda")
+        want = tq2.moe_swiglu(layer.dev, x, expert, weight), *tq2.moe_route(x, 8), *tq2.sample(logits, u)
+        calls.append((layer, x, expert, weight, logits, u, want, []))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, (layer, x, expert, weight, logits, u, _, got) in zip(streams, calls):
+            got.append((tq2.moe_swiglu(layer.dev, x, expert, weight, stream=s), *tq2.moe_route(x, 8, stream=s),
+                        *tq2.sample(logits, u, stream=s)))
+    torch.cuda.synchronize()
+    for *_, want, got in calls:
+        for one in got:
+            assert all(torch.equal(a, b) for a, b in zip(one, want))
 
 
 def test_router_experts_sampling_together(tq2):
