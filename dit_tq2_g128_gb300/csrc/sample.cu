@@ -257,17 +257,49 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     };
     const bool cut_k = k > 0 && k < a.vocab, cut_p = p < 1.f;
 
-    // f(index in the slice, value) for all elements
+    // f(value) for all elements, a pack at a time (and for the NaNs that fill the first and last packs)
+    const Pack<T> *packed = reinterpret_cast<const Pack<T> *>(x - shift);
+    const int packs = n > 0 ? (n + shift + V - 1) / V : 0;
     auto each = [&](auto f) {
+        for (int q = tid; q < packs; q += kThreads) {
+            const Pack<T> v = packed[q];
+#pragma unroll
+            for (int i = 0; i < V; ++i) f(to_f32(v.e[i]));
+        }
+    };
+    // The elements that are `wanted` to the first CTA's list: marked, placed in this CTA's own by one count a warp, and handed
+    // over all at once.  (Taken one by one, with a count each, they were a third of a row's time.)
+    auto collect = [&](bool look, auto wanted) {
+        for (int q0 = 0; q0 < packs; q0 += 64 / V * kThreads) {
+            unsigned long long hits = 0;
+            if (look) {
 #pragma unroll 2
-        for (int i = tid; i < n; i += kThreads) f(i, to_f32(x[i]));
-    };
-    // Elements on their way to the first CTA's list: in this CTA first, then all at once.
-    auto take = [&](int i, float v) {
-        const uint32_t at = atomicAdd(&sh->n_mine, 1u);
-        if (at < kList) sh->cum[at] = uint64_t(order_key(v)) << 32 | uint32_t(~(first + i));
-    };
-    auto hand_over = [&] {
+                for (int j = 0; j < 64 / V; ++j) {
+                    const int q = q0 + j * kThreads + tid;
+                    if (q >= packs) break;
+                    const Pack<T> v = packed[q];
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int i = 0; i < V; ++i) m |= wanted(to_f32(v.e[i])) ? 1u << i : 0u;
+                    hits |= static_cast<unsigned long long>(m) << (j * V);
+                }
+            }
+            const int mine = __popcll(hits);
+            if (!__any_sync(0xffffffffu, mine)) continue;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += y;
+            }
+            uint32_t base = 0;
+            if (lane == 31) base = atomicAdd(&sh->n_mine, uint32_t(upto));
+            uint32_t at = __shfl_sync(0xffffffffu, base, 31) + uint32_t(upto - mine);
+            for (; hits && at < kList; hits &= hits - 1, ++at) {
+                const int b = __ffsll(static_cast<long long>(hits)) - 1, e = (q0 + b / V * kThreads + tid) * V + b % V - shift;
+                sh->cum[at] = uint64_t(order_key(to_f32(x[e]))) << 32 | uint32_t(~(first + e));
+            }
+        }
         __syncthreads();
         const uint32_t count = sh->n_mine;
         if (tid == 0 && count) sh->base = atomicAdd(&lead->n_list, count);
@@ -283,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     if (try_head) {
         if (!cut_k) {  // the row's weight
             unsigned long long sum = 0;
-            each([&](int, float v) { sum += rw.weight(v, sh->table); });
+            each([&](float v) { sum += rw.weight(v, sh->table); });
 #pragma unroll
             for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0 && sum) atomicAdd(&sh->sum, sum);
@@ -331,24 +363,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
             if (tid == 0) atomicAdd(&lead->total, sh->sum);
         }
         const float floor = all ? -3.402823466e38f : sh->floor;
-        const Pack<T> *packed = reinterpret_cast<const Pack<T> *>(x - shift);
-        const int packs = n > 0 ? (n + shift + V - 1) / V : 0;
-        if (mine >= floor && floor < INFINITY)  // (the packs that this thread brought)
-            for (int q = tid; q < packs; q += kThreads) {
-                const Pack<T> v = packed[q];
-                bool any = false;
-#pragma unroll
-                for (int i = 0; i < V; ++i) any |= to_f32(v.e[i]) >= floor;
-                if (any) {
-#pragma unroll 1
-                    for (int i = 0; i < V; ++i) {
-                        const int e = q * V + i - shift;
-                        const float f = e >= 0 && e < n ? to_f32(x[e]) : -INFINITY;
-                        if (f >= floor) take(e, f);
-                    }
-                }
-            }
-        if (floor < INFINITY) hand_over();
+        // (only of the packs that this thread brought, if any is there)
+        if (floor < INFINITY) collect(mine >= floor, [&](float v) { return v >= floor; });
     }
 
     // (first CTA) Sorts the list's `count` elements: this thread's weights and their cumulative ones, from `before` on (in
@@ -387,6 +403,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         if (rank == 0) {
             const int count = int(sh->n_list);
             bool ok = count > 0 && count <= kList;
+            if (ok && !cut_k && !all && least <= 1) {  // whether the head reaches as far as the answer lies, before it is sorted
+                unsigned long long sum = 0;
+                for (int i = tid; i < count; i += kThreads) sum += rw.weight(key_value(uint32_t(sh->list[i] >> 32)), sh->table);
+                sum = block_scan(sum, sh);
+                if (tid == kThreads - 1) sh->found_mass = sum;
+                __syncthreads();
+                ok = (cut_p ? mass_needed(p, sh->total) : drawn_mass(u, sh->total) + 1) <= sh->found_mass;
+            }
             if (ok) {
                 sort_and_sum(count, 0);
                 const unsigned long long head = sh->cum[count - 1];
@@ -421,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     auto histogram = [&](auto slot) {
         for (int i = tid; i < kBins; i += kThreads) sh->count[i] = sh->mass[0][i] = sh->mass[1][i] = sh->mass[2][i] = 0;
         __syncthreads();
-        each([&](int, float v) {
+        each([&](float v) {
             const int b = slot(v);
             if (b < 0) return;
             const uint64_t w = rw.weight(v, sh->table);
@@ -457,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
             });
         } else if (c.op == OP_SPAN) {  // the smallest and largest key of a bin
             uint32_t lo = 0xffffffffu, hi = 0;
-            each([&](int, float v) {
+            each([&](float v) {
                 if (bin_of_logit(v) == c.bin) {
                     lo = min(lo, order_key(v));
                     hi = max(hi, order_key(v));
@@ -471,14 +495,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
             }
             cluster_sync();
         } else if (c.op == OP_GATHER) {
-            each([&](int i, float v) {
+            collect(true, [&](float v) {
                 const uint32_t key = order_key(v);
-                if (key >= c.low && key <= c.high && bin_of_logit(v) == c.bin) take(i, v);
+                return key >= c.low && key <= c.high && bin_of_logit(v) == c.bin;
             });
-            hand_over();
         } else if (c.op == OP_HEAVY) {  // the weight of what min_p keeps
             unsigned long long sum = 0;
-            each([&](int, float v) {
+            each([&](float v) {
                 const uint64_t w = rw.weight(v, sh->table);
                 sum += w >= least ? w : 0;
             });
