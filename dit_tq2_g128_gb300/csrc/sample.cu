@@ -445,15 +445,27 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     auto histogram = [&](auto slot) {
         for (int i = tid; i < kBins; i += kThreads) sh->count[i] = sh->mass[0][i] = sh->mass[1][i] = sh->mass[2][i] = 0;
         __syncthreads();
-        each([&](float v) {
-            const int b = slot(v);
-            if (b < 0) return;
-            const uint64_t w = rw.weight(v, sh->table);
-            atomicAdd(&sh->count[b], 1u);
-            atomicAdd(&sh->mass[0][b], uint32_t(w) & 0x7fffu);
-            atomicAdd(&sh->mass[1][b], uint32_t(w >> 15) & 0x7fffu);
-            atomicAdd(&sh->mass[2][b], uint32_t(w >> 30));
-        });
+        for (int q = tid; q < packs; q += kThreads) {
+            const Pack<T> v = packed[q];
+#pragma unroll
+            for (int i0 = 0; i0 < V; i0 += 4) {
+                int b[4];
+                uint64_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    b[i] = slot(to_f32(v.e[i0 + i]));
+                    w[i] = rw.weight(to_f32(v.e[i0 + i]), sh->table);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (b[i] >= 0) {
+                        atomicAdd(&sh->count[b[i]], 1u);
+                        atomicAdd(&sh->mass[0][b[i]], uint32_t(w[i]) & 0x7fffu);
+                        atomicAdd(&sh->mass[1][b[i]], uint32_t(w[i] >> 15) & 0x7fffu);
+                        atomicAdd(&sh->mass[2][b[i]], uint32_t(w[i] >> 30));
+                    }
+            }
+        }
         cluster_sync();
         for (int b = int(rank) + cluster * tid; b < kBins; b += cluster * kThreads) {
             uint32_t c = 0;
@@ -477,15 +489,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         } else if (c.op == OP_REFINE) {
             histogram([&](float v) {
                 const uint32_t key = order_key(v);
-                return key >= c.low && key <= c.high && bin_of_logit(v) == c.bin ? int((c.high - key) >> c.shift) : -1;
+                return (key >= c.low) & (key <= c.high) & (bin_of_logit(v) == c.bin) ? int((c.high - key) >> c.shift) : -1;
             });
         } else if (c.op == OP_SPAN) {  // the smallest and largest key of a bin
             uint32_t lo = 0xffffffffu, hi = 0;
             each([&](float v) {
-                if (bin_of_logit(v) == c.bin) {
-                    lo = min(lo, order_key(v));
-                    hi = max(hi, order_key(v));
-                }
+                const bool in = bin_of_logit(v) == c.bin;
+                lo = min(lo, in ? order_key(v) : 0xffffffffu);
+                hi = max(hi, in ? order_key(v) : 0u);
             });
             lo = __reduce_min_sync(0xffffffffu, lo);
             hi = __reduce_max_sync(0xffffffffu, hi);
@@ -497,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         } else if (c.op == OP_GATHER) {
             collect(true, [&](float v) {
                 const uint32_t key = order_key(v);
-                return key >= c.low && key <= c.high && bin_of_logit(v) == c.bin;
+                return (key >= c.low) & (key <= c.high) & (bin_of_logit(v) == c.bin);
             });
         } else if (c.op == OP_HEAVY) {  // the weight of what min_p keeps
             unsigned long long sum = 0;

@@ -35,38 +35,39 @@ constexpr WeightTable make_weight_table() {
 __constant__ WeightTable weight_table = make_weight_table();
 
 // A row's weights.  In f32 and integers throughout: 64-bit floating point, and conversions to and from it, run at a
-// thirtieth of their rate.
+// thirtieth of their rate.  No branches: a weight is a chain of some 60 instructions, and several have to be under way (with
+// branches between them a pass over 49 elements a thread took 15,000 cycles).
 struct RowWeights {
     float top;         // the largest logit
     float s_hi, s_lo;  // log2(e) / temperature
-    int mode;          // 0: as above, 1: the largest only (no temperature, or an infinite logit)
+    bool only;         // the largest only (no temperature, or an infinite logit): s_hi is infinite
 
     __device__ __forceinline__ RowWeights(float largest, float temperature) : top(largest) {
         constexpr float e_hi = 1.44269502f, e_lo = 1.92596303e-8f;  // log2(e)
         s_hi = e_hi / temperature;
         s_lo = (fmaf(-s_hi, temperature, e_hi) + e_lo) / temperature;
-        mode = !(temperature > 0.f) || !(s_hi < 1e30f) || top == INFINITY;
+        only = !(temperature > 0.f) || !(s_hi < 1e30f) || top == INFINITY;
         if (!(temperature < INFINITY)) s_hi = s_lo = 0.f;
+        if (only) {
+            s_hi = INFINITY;
+            s_lo = 0.f;
+        }
     }
 
     // y rounded to f32: larger logits never have a larger one.  (Infinite or NaN: no weight.)
     __device__ __forceinline__ float coarse(float l) const {
-        if (mode) return l == top ? 0.f : INFINITY;
-        return (top - l) * s_hi;
+        return l == top ? 0.f : (top - l) * s_hi;
     }
     // A logit below which no token has a coarse y below `limit`.
     __device__ __forceinline__ float floor_of(float limit) const {
-        return mode ? top : fmaxf(top - limit * (1.f + 0x1p-18f) / s_hi, -3.402823466e38f);
+        return only ? top : fmaxf(top - limit * (1.f + 0x1p-18f) / s_hi, -3.402823466e38f);
     }
 
     __device__ __forceinline__ uint64_t weight(float l, const uint64_t *table) const {
-        if (!(l > -INFINITY)) return 0;  // NaN too
-        if (mode) return l == top ? uint64_t(1) << kWeightBits : 0;
         // max - l as hi + lo, exactly
         const float hi = top - l, v = hi - top;
         const float lo = (top - (hi - v)) - (l + v);
-        const float p = hi * s_hi;
-        if (!(p < float(kWeightBits + 1))) return 0;
+        const float y = hi * s_hi, p = fminf(y, float(kWeightBits + 1));  // (of -inf and NaN: infinite or NaN, and no weight)
         const float e = fmaf(hi, s_hi, -p) + fmaf(hi, s_lo, lo * s_hi);
         // n = 64 p to the nearest integer, in the low bits of its sum with 1.5 * 2^23
         const float big = fmaf(p, 64.f, 12582912.f);
@@ -80,7 +81,8 @@ struct RowWeights {
         const float high = __uint2float_rn(uint32_t(base >> 32)) * m;
         const int64_t more = int64_t(__float2int_rn(high * 256.f)) * (1 << 24);
         const int shift = 62 - kWeightBits + (k >> 6);
-        return (base + uint64_t(more) + (uint64_t(1) << (shift - 1))) >> shift;
+        const uint64_t w = (base + uint64_t(more) + (uint64_t(1) << (shift - 1))) >> shift;
+        return l == top ? uint64_t(1) << kWeightBits : y < float(kWeightBits + 1) ? w : 0;
     }
 };
 
