@@ -29,10 +29,12 @@ namespace {
 
 constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1472;  // of y: 32 or more in a unit (of log2 of the weight)
+constexpr int kFine = 4 * kBins;  // of y in a guess, in the same memory
 constexpr int kList = 1024;
 constexpr int kHead = 256, kMostHeadK = 768, kRankSort = 256;
 constexpr int kEach = kList / kThreads;  // list elements of a thread
 constexpr int kMaxCluster = 8;
+static_assert(kBins % (4 * kMaxCluster) == 0);
 
 enum Op { OP_DONE, OP_HISTOGRAM, OP_REFINE, OP_SPAN, OP_GATHER, OP_HEAVY, OP_TIE };
 // What the first CTA has the others do.
@@ -45,13 +47,16 @@ struct Command {
 struct alignas(16) Shared {  // (the row follows it, in packs of 16 bytes)
     // Weights of bins.  While they are counted, in three pieces of 15 bits and more (a 64-bit atomic is a loop here, and
     // 2^15 of a piece fit 32 bits); then, in the first CTA, the low and the high word of their sum over the CTAs.
-    uint32_t mass[3][kBins];
+    uint32_t mass[3][kBins], count[kBins];
     unsigned long long list[kList];  // key << 32 | ~index
     unsigned long long cum[kList];
     uint64_t table[64];
     unsigned long long part[kWarps];
     unsigned long long sum, total, found_mass, found_before, kept;
-    uint32_t count[kBins];
+    unsigned long long sums[4], my_sums[4];  // of a guess: all weights, those min_p keeps, those above each range; this CTA's
+    float range[2][2];  // logits from and to which answers are looked for
+    int edge[4];
+    uint32_t until[4];
     uint32_t top[kMaxCluster], ties[kMaxCluster];
     float bottom[kMaxCluster];
     uint32_t n_list, n_mine, base, low, high;
@@ -101,8 +106,8 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, S
 }
 
 // Sorts list[0, count) descending (all different).  Short ones by counting who is larger (a list of 100: 700 cycles, not
-// the 5000 of the network's 28 steps); others by a bitonic network, a thread a pair, whose steps of up to 32 stay within the
-// 64 elements of a warp's pairs, so that warps need not meet between them.
+// the 5000 of a network's 28 steps through shared memory); others by a bitonic network of one or two elements a thread, in
+// registers, whose steps within a warp are shuffles (of 400: 3,000 cycles, not 11,000 through shared memory).
 __device__ __forceinline__ void sort_list(unsigned long long *list, unsigned long long *spare, int count) {
     const int i = threadIdx.x;
     if (count <= kRankSort) {
@@ -119,26 +124,33 @@ __device__ __forceinline__ void sort_list(unsigned long long *list, unsigned lon
         __syncthreads();
         return;
     }
-    int n = 32;
-    while (n < count) n *= 2;
-    for (int j = count + i; j < n; j += kThreads) list[j] = 0;
-    __syncthreads();
-    for (int size = 2; size <= n; size <<= 1)
+    const bool two = count > kThreads;  // elements a thread: i, and i + kThreads
+    unsigned long long v[2] = {i < count ? list[i] : 0, i + kThreads < count ? list[i + kThreads] : 0};
+    bool odd = false;
+    for (int size = 2; size <= (two ? 2 : 1) * kThreads; size <<= 1)
         for (int step = size >> 1; step; step >>= 1) {
-            if (i < n / 2) {
-                const int a = 2 * i - (i & (step - 1)), b = a + step;
-                const unsigned long long x = list[a], y = list[b];
-                if ((x < y) == ((a & size) == 0)) {
-                    list[a] = y;
-                    list[b] = x;
-                }
-            }
-            // (the next step is half of this one, or, after 1, of this size)
-            if (step > 32 || (step == 1 && size > 32))
+            unsigned long long o[2] = {v[1], v[0]};
+            if (step < 32) {
+                o[0] = __shfl_xor_sync(0xffffffffu, v[0], step);
+                o[1] = __shfl_xor_sync(0xffffffffu, v[1], step);
+            } else if (step < kThreads) {
+                unsigned long long *to = odd ? spare : list;  // (in turn, so that one barrier a step is enough)
+                odd = !odd;
+                to[i] = v[0];
+                if (two) to[i + kThreads] = v[1];
                 __syncthreads();
-            else
-                __syncwarp();
+                o[0] = to[i ^ step];
+                if (two) o[1] = to[(i ^ step) + kThreads];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int at = i + j * kThreads;
+                v[j] = ((at & step) == 0) == ((at & size) == 0) ? max(v[j], o[j]) : min(v[j], o[j]);
+            }
         }
+    __syncthreads();
+    list[i] = v[0];
+    if (two) list[i + kThreads] = v[1];
     __syncthreads();
 }
 
@@ -196,7 +208,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     const uint32_t rank = cluster_rank();
     const int64_t r = blockIdx.x / cluster;
     Shared *lead = at_cta(sh, 0);
-    for (int i = tid; i < kBins; i += kThreads) sh->count[i] = 0;
+    uint32_t *fine = sh->mass[0];
+    for (int i = tid; i < kFine; i += kThreads) fine[i] = 0;
+    if (tid < 4) sh->sums[tid] = sh->my_sums[tid] = 0;
     if (tid < 64) sh->table[tid] = weight_table.e[tid];
     if (tid == 0) {
         sh->n_list = 0;
@@ -310,8 +324,25 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         cluster_sync();
     };
 
+    // (after a cluster barrier) The first CTA's bins[0, count) become the sums over all CTAs'.  Each CTA takes some that follow one
+    // another: every eighth of them took eight times as long.
+    auto sum_bins = [&](uint32_t *bins, int count) {
+        const int some = count / cluster;  // (a multiple of 4)
+        for (int b = int(rank) * some + 4 * tid; b < int(rank + 1) * some; b += 4 * kThreads) {
+            uint4 c = make_uint4(0, 0, 0, 0);
+#pragma unroll 4
+            for (int o = 0; o < cluster; ++o) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(at_cta(bins, uint32_t(o)) + b);
+                c = make_uint4(c.x + v.x, c.y + v.y, c.z + v.z, c.w + v.w);
+            }
+            *reinterpret_cast<uint4 *>(at_cta(bins, 0) + b) = c;
+        }
+        cluster_sync();
+    };
+
     // ---- the head
-    const bool all = a.vocab <= kList, try_head = all || !cut_k || k <= kMostHeadK;
+    const bool all = a.vocab <= kList, guess = !all && !cut_k && !rw.only && rw.s_hi > 0.f;
+    const bool try_head = !guess && (all || !cut_k || k <= kMostHeadK);
     if (try_head) {
         if (!cut_k) {  // the row's weight
             unsigned long long sum = 0;
@@ -440,6 +471,149 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         if (sh->cmd.op == OP_DONE) return;
     }
 
+    // ---- a guess
+    if (guess) {
+        const float fine_per_unit = 4.f * per_unit;
+        each([&](float v) {
+            const float y = rw.coarse(v);
+            if (y < float(kWeightBits + 1)) atomicAdd(&fine[min(int(y * fine_per_unit), kFine - 1)], 1u);
+        });
+        cluster_sync();
+        sum_bins(fine, kFine);
+        if (rank == 0) {
+            // Cumulative weights of the bins, as if all their elements lay in the middle.  (Scanned in 2^-26, with the counts from
+            // bit 45 on.)
+            constexpr int per = (kFine + kThreads - 1) / kThreads;
+            constexpr unsigned long long mask = (1ull << 45) - 1;
+            const float unit = 1.f / fine_per_unit;
+            auto of_bin = [&](int b) { return float(fine[b]) * exp2f(26.f - (float(b) + 0.5f) * unit); };
+            const int b0 = min(tid * per, kFine), b1 = min(b0 + per, kFine);
+            float weight = 0.f;
+            uint32_t count = 0;
+            for (int b = b0; b < b1; ++b) {
+                weight += of_bin(b);
+                count += fine[b];
+            }
+            const unsigned long long mine = static_cast<unsigned long long>(count) << 45 | static_cast<unsigned long long>(weight);
+            const unsigned long long upto = block_scan(mine, sh), whole = sh->part[kWarps - 1];
+            const float row = float(whole & mask), first = float((upto - mine) & mask), last = float(upto & mask);
+            const uint32_t before = uint32_t((upto - mine) >> 45);
+            if (tid < 4) {
+                sh->edge[tid] = kFine;
+                sh->until[tid] = uint32_t(whole >> 45);
+            }
+            if (tid == 0) sh->floor = row;
+            __syncthreads();
+            float kept = cut_p ? row * fmaxf(p, 0.f) : row;
+            const float target1 = kept;
+            if (least > 1) {
+                const int b = min(int((float(kWeightBits) - log2f(float(least))) * fine_per_unit), kFine - 1);
+                if (b >= b0 && b < b1) {
+                    float c = first;
+                    for (int j = b0; j <= b; ++j) c += of_bin(j);
+                    sh->floor = c;
+                }
+                __syncthreads();
+                kept = fminf(kept, sh->floor);
+            }
+            const float target2 = kept * fminf(fmaxf(u, 0.f), 1.f);
+            // three times what the places of elements within their bins may add up to (their standard deviation, with the sum of
+            // squared weights at most the sum), twice that where what is kept is a guess too
+            const float slack = 0.6f * unit * sqrtf(row * 0x1p26f);
+            const float at[4] = {target1 - slack, target1 + slack, target2 - 2.f * slack, target2 + 2.f * slack};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (tid == 0 && !(at[i] >= 0.f)) {
+                    sh->edge[i] = 0;
+                    sh->until[i] = 0;
+                }
+                if (!(first > at[i]) && last > at[i]) {
+                    float c = first;
+                    uint32_t n = before;
+                    int b = b0;
+                    for (; b < b1 - 1 && !((c += of_bin(b)) > at[i]); ++b) n += fine[b];
+                    sh->edge[i] = b + (i & 1);  // (whole bins: elements may be few, or lie on a grid as coarse as the bins)
+                    sh->until[i] = n + (i & 1 ? fine[b] : 0);
+                }
+            }
+            __syncthreads();
+            if (tid < cluster) {
+                Shared *to = at_cta(sh, uint32_t(tid));
+                to->found = (cut_p ? sh->until[1] - sh->until[0] : 0) + sh->until[3] - sh->until[2] <= kList;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool off = i == 0 && !cut_p;
+                    to->range[i][0] = off ? INFINITY : rw.top - float(sh->edge[2 * i + 1]) * unit / rw.s_hi;
+                    to->range[i][1] = off ? INFINITY : rw.top - float(sh->edge[2 * i]) * unit / rw.s_hi;
+                }
+            }
+        }
+        cluster_sync();
+        if (sh->found) {
+            const float lo1 = sh->range[0][0], hi1 = sh->range[0][1], lo2 = sh->range[1][0], hi2 = sh->range[1][1];
+            unsigned long long sums[4] = {};
+            for (int q = tid; q < packs; q += kThreads) {
+                const Pack<T> v = packed[q];
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float f = to_f32(v.e[i]);
+                    const unsigned long long w = rw.weight(f, sh->table);
+                    sums[0] += w;
+                    sums[1] += w >= least ? w : 0;
+                    sums[2] += f > hi1 ? w : 0;
+                    sums[3] += f > hi2 ? w : 0;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sums[j] += __shfl_xor_sync(0xffffffffu, sums[j], o);
+                if (lane == 0 && sums[j]) atomicAdd(&sh->my_sums[j], sums[j]);
+            }
+            __syncthreads();
+            if (tid < 4) atomicAdd(&lead->sums[tid], sh->my_sums[tid]);
+            collect(true, [&](float v) { return ((v >= lo1) & (v <= hi1)) | ((v >= lo2) & (v <= hi2)); });
+        }
+        if (rank == 0) {
+            const int count = int(sh->n_list);
+            bool ok = sh->found && count > 0 && count <= kList;
+            if (ok) {
+                sort_and_sum(count, 0);
+                // The list's element at which the prefix reaches `target`, if it lies in range i; *skip: what is to be added to
+                // the list's cumulative weights there.
+                auto find = [&](unsigned long long target, int i, unsigned long long *skip) {
+                    const float lo = sh->range[i][0], hi = sh->range[i][1];
+                    int from = 0, to = 0;
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) {
+                        const int e = tid * kEach + j;
+                        const float v = e < count ? key_value(uint32_t(sh->list[e] >> 32)) : -INFINITY;
+                        from += __syncthreads_count(v > hi);
+                        to += __syncthreads_count(v >= lo);
+                    }
+                    const unsigned long long above = sh->sums[2 + i], before = from ? sh->cum[from - 1] : 0;
+                    *skip = above - before;  // (modulo 2^64)
+                    if (target <= above) return -1;
+                    const int f = first_of_mass(target - *skip, count);
+                    return f < to ? f : -1;
+                };
+                unsigned long long kept = sh->sums[0], skip;
+                if (cut_p) {
+                    const int f = find(mass_needed(p, kept), 0, &skip);
+                    ok = f >= 0;
+                    if (ok) kept = sh->cum[f] + skip;
+                }
+                if (least > 1) kept = min(kept, sh->sums[1]);
+                const int f = ok ? find(drawn_mass(u, kept) + 1, 1, &skip) : -1;
+                ok = f >= 0;
+                if (ok && tid == 0) write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
+            }
+            if (tid < cluster) at_cta(sh, uint32_t(tid))->cmd.op = ok ? OP_DONE : OP_HISTOGRAM;
+        }
+        cluster_sync();
+        if (sh->cmd.op == OP_DONE) return;
+    }
+
     // ---- the whole order
     // Counts and weights of the bins slot(x) of all CTAs' elements (below 0: none), in the first CTA.
     auto histogram = [&](auto slot) {
@@ -467,7 +641,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
             }
         }
         cluster_sync();
-        for (int b = int(rank) + cluster * tid; b < kBins; b += cluster * kThreads) {
+        const int some = kBins / cluster;
+        for (int b = int(rank) * some + tid; b < int(rank + 1) * some; b += kThreads) {
             uint32_t c = 0;
             unsigned long long m = 0;
             for (int o = 0; o < cluster; ++o) {
