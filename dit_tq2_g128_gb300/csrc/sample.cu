@@ -6,16 +6,21 @@
 // weight.  Every question is then one of a count or a sum over a prefix, and no sort of a row is needed.
 //
 // A cluster of CTAs takes a row and keeps it in shared memory: it is read from memory once.
-//  * The head: a bound that at least k (or a few hundred) of the maxima of groups of threads reach; the few elements above it go
-//    to the first CTA, which sorts them and answers every question from their cumulative weights, if they reach that far:
-//    with a top-k always, without one where the distribution is as peaked as a model's usually is.
-//  * Else: a histogram of counts and weights over bins of log2 of the weight finds the bin that an answer lies in; its
-//    elements (at most 1024, or split further by their bits) are sorted as the head is.
+//  * With a top-k of up to 768 (and of rows of up to 1024 logits, or of which only the largest weigh anything), the head: a
+//    bound that at least k of the maxima of groups of threads reach; the few elements above it go to the first CTA, which
+//    sorts them and answers every question from their cumulative weights.
+//  * Without a top-k, a guess: a histogram of counts (5888 bins of log2 of the weight, their elements taken to lie in the middle)
+//    says within some elements where top_p's border and the drawn token lie.  One pass then adds up the exact weights of all
+//    elements and of those above either place, and collects the few about them, which are sorted; if the exact prefixes pass
+//    their targets among these, they are the answer.
+//  * Else (a larger k, many equal logits, a guess that failed): a histogram of counts and exact weights finds the bin that an
+//    answer lies in; its elements (at most 1024, or split further by their bits) are sorted as the head is.
 //
-// Bound by latency: for one row (32,000 logits: 9.0 us) and, with two CTAs an SM, for many: a row with a top-k passes through
-// loading, four cluster barriers, the gathering and the sort in 20 us, in which 27 % of its SMs' issue slots are used (256 rows of
-// 100,003 bf16 logits: 74 us).  Without a top-k, where the head does not reach, the histogram's shared atomics (four an
-// element) are most of it: 16 flat rows of 200,000: 86 us, 64 rows of 128,000 f32, a quarter without a top-k: 78 us.
+// Bound by latency for one row (32,000 logits: 8.1 us) and by a row's chain for many: with a top-k 28,000 cycles (loading 9,
+// four cluster barriers with the bound 6, collecting 5, sorting 5, the answer 3), two CTAs an SM (256 rows of 100,003
+// bf16 logits: 63 us); without one 55,000, of which the exact sums are a third, some 60 instructions a weight (16 flat rows of
+// 200,000: 40 us; 64 rows of 128,000 f32, a quarter without a top-k: 54 us).  The exact histogram in place of the guess, with
+// four shared atomics an element and two passes to collect, took 81 and 75 us.
 #include <algorithm>
 #include <cstdint>
 
@@ -105,9 +110,55 @@ __device__ __forceinline__ unsigned long long block_scan(unsigned long long v, S
     return v + (warp ? sh->part[warp - 1] : 0);
 }
 
+// A bitonic network of E elements a thread in registers (i, and i + kThreads), whose steps within a warp are shuffles.
+template <int E>
+__device__ __forceinline__ void sort_network(unsigned long long *list, unsigned long long *spare, int count) {
+    const int i = threadIdx.x;
+    unsigned long long v[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[j] = i + j * kThreads < count ? list[i + j * kThreads] : 0;
+    auto keep = [&](int j, unsigned long long other, int step, bool falling) {
+        v[j] = ((i & step) == 0) == falling ? max(v[j], other) : min(v[j], other);
+    };
+    auto within = [&](int step, int size) {
+#pragma unroll
+        for (int j = 0; j < E; ++j) keep(j, __shfl_xor_sync(0xffffffffu, v[j], step), step, ((i + j * kThreads) & size) == 0);
+    };
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int step = size >> 1; step; step >>= 1) within(step, size);
+    bool odd = false;
+#pragma unroll 1
+    for (int size = 64; size <= E * kThreads; size <<= 1) {
+        int step = size >> 1;
+        if (E == 2 && step == kThreads) {
+            const unsigned long long top = max(v[0], v[E - 1]), low = min(v[0], v[E - 1]);
+            v[0] = top;
+            v[E - 1] = low;
+            step >>= 1;
+        }
+#pragma unroll 1
+        for (; step >= 32; step >>= 1) {
+            unsigned long long *to = odd ? spare : list;  // (in turn, so that one barrier a step is enough)
+            odd = !odd;
+#pragma unroll
+            for (int j = 0; j < E; ++j) to[i + j * kThreads] = v[j];
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < E; ++j) keep(j, to[(i ^ step) + j * kThreads], step, ((i + j * kThreads) & size) == 0);
+        }
+#pragma unroll
+        for (step = 16; step; step >>= 1) within(step, size);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < E; ++j) list[i + j * kThreads] = v[j];
+    __syncthreads();
+}
 // Sorts list[0, count) descending (all different).  Short ones by counting who is larger (a list of 100: 700 cycles, not
 // the 5000 of a network's 28 steps through shared memory); others by a bitonic network of one or two elements a thread, in
-// registers, whose steps within a warp are shuffles (of 400: 3,000 cycles, not 11,000 through shared memory).
+// registers, whose steps within a warp are shuffles (of 400: 7,000 cycles, not 11,000 through shared memory).
 __device__ __forceinline__ void sort_list(unsigned long long *list, unsigned long long *spare, int count) {
     const int i = threadIdx.x;
     if (count <= kRankSort) {
@@ -124,34 +175,10 @@ __device__ __forceinline__ void sort_list(unsigned long long *list, unsigned lon
         __syncthreads();
         return;
     }
-    const bool two = count > kThreads;  // elements a thread: i, and i + kThreads
-    unsigned long long v[2] = {i < count ? list[i] : 0, i + kThreads < count ? list[i + kThreads] : 0};
-    bool odd = false;
-    for (int size = 2; size <= (two ? 2 : 1) * kThreads; size <<= 1)
-        for (int step = size >> 1; step; step >>= 1) {
-            unsigned long long o[2] = {v[1], v[0]};
-            if (step < 32) {
-                o[0] = __shfl_xor_sync(0xffffffffu, v[0], step);
-                o[1] = __shfl_xor_sync(0xffffffffu, v[1], step);
-            } else if (step < kThreads) {
-                unsigned long long *to = odd ? spare : list;  // (in turn, so that one barrier a step is enough)
-                odd = !odd;
-                to[i] = v[0];
-                if (two) to[i + kThreads] = v[1];
-                __syncthreads();
-                o[0] = to[i ^ step];
-                if (two) o[1] = to[(i ^ step) + kThreads];
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const int at = i + j * kThreads;
-                v[j] = ((at & step) == 0) == ((at & size) == 0) ? max(v[j], o[j]) : min(v[j], o[j]);
-            }
-        }
-    __syncthreads();
-    list[i] = v[0];
-    if (two) list[i + kThreads] = v[1];
-    __syncthreads();
+    if (count <= kThreads)
+        sort_network<1>(list, spare, count);
+    else
+        sort_network<2>(list, spare, count);
 }
 
 // A pack of 16 bytes.
