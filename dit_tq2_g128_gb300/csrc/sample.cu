@@ -36,7 +36,7 @@ constexpr int kThreads = 512, kWarps = kThreads / 32;
 constexpr int kBins = 1472;  // of y: 32 or more in a unit (of log2 of the weight)
 constexpr int kFine = 4 * kBins;  // of y in a guess, in the same memory
 constexpr int kList = 1024;
-constexpr int kHead = 256, kMostHeadK = 768, kRankSort = 256;
+constexpr int kMostHeadK = 768, kRankSort = 256;
 constexpr int kEach = kList / kThreads;  // list elements of a thread
 constexpr int kMaxCluster = 8;
 static_assert(kBins % (4 * kMaxCluster) == 0);
@@ -57,7 +57,7 @@ struct alignas(16) Shared {  // (the row follows it, in packs of 16 bytes)
     unsigned long long cum[kList];
     uint64_t table[64];
     unsigned long long part[kWarps];
-    unsigned long long sum, total, found_mass, found_before, kept;
+    unsigned long long total, found_mass, found_before, kept;
     unsigned long long sums[4], my_sums[4];  // of a guess: all weights, those min_p keeps, those above each range; this CTA's
     float range[2][2];  // logits from and to which answers are looked for
     int edge[4];
@@ -242,8 +242,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     if (tid == 0) {
         sh->n_list = 0;
         sh->n_mine = 0;
-        sh->sum = 0;
-        sh->total = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -369,30 +367,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
 
     // ---- the head
     const bool all = a.vocab <= kList, guess = !all && !cut_k && !rw.only && rw.s_hi > 0.f;
-    const bool try_head = !guess && (all || !cut_k || k <= kMostHeadK);
+    const bool try_head = all || rw.only || (cut_k && k <= kMostHeadK);
     if (try_head) {
-        if (!cut_k) {  // the row's weight
-            unsigned long long sum = 0;
-            each([&](float v) { sum += rw.weight(v, sh->table); });
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane == 0 && sum) atomicAdd(&sh->sum, sum);
-        }
         if (!all) {
             // maxima of groups of four threads, or, for many, of each
-            const int want = cut_k ? k : kHead;
+            const int want = cut_k ? k : 1;
             float m = mine;
-            const bool fours = want <= kThreads / 8 || (want <= kHead && cluster == kMaxCluster);
+            const bool fours = want <= kThreads / 8 || (want <= kRankSort && cluster == kMaxCluster);
             if (fours) {
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
             }
             const int b = !fours || (lane & 3) == 0 ? bin_of_logit(m) : -1;
             if (b >= 0) atomicAdd(&lead->count[b], 1u);
-            if (!cut_k) {
-                __syncthreads();
-                if (tid == 0) atomicAdd(&lead->total, sh->sum);
-            }
             cluster_sync();
             if (rank == 0) {
                 constexpr int per = (kBins + kThreads - 1) / kThreads;
@@ -410,19 +397,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
                     before += c[j];
                 }
                 __syncthreads();
-                // (none found: whatever has a weight; no head at all where top_p wants more than one can weigh)
+                // (none found: whatever has a weight)
                 const float limit = sh->found == kBins ? float(kWeightBits + 1) : float(sh->found + 1) / per_unit;
-                const bool flat = !cut_k && cut_p && mass_needed(p, sh->total) >> kWeightBits > kHead;
-                if (tid < cluster) at_cta(sh, uint32_t(tid))->floor = flat ? INFINITY : rw.floor_of(limit);
+                if (tid < cluster) at_cta(sh, uint32_t(tid))->floor = rw.floor_of(limit);
             }
             cluster_sync();
-        } else if (!cut_k) {
-            __syncthreads();
-            if (tid == 0) atomicAdd(&lead->total, sh->sum);
         }
         const float floor = all ? -3.402823466e38f : sh->floor;
         // (only of the packs that this thread brought, if any is there)
-        if (floor < INFINITY) collect(mine >= floor, [&](float v) { return v >= floor; });
+        collect(mine >= floor, [&](float v) { return v >= floor; });
     }
 
     // (first CTA) Sorts the list's `count` elements: this thread's weights and their cumulative ones, from `before` on (in
@@ -460,37 +443,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     if (try_head) {
         if (rank == 0) {
             const int count = int(sh->n_list);
-            bool ok = count > 0 && count <= kList;
-            if (ok && !cut_k && !all && least <= 1) {  // whether the head reaches as far as the answer lies, before it is sorted
-                unsigned long long sum = 0;
-                for (int i = tid; i < count; i += kThreads) sum += rw.weight(key_value(uint32_t(sh->list[i] >> 32)), sh->table);
-                sum = block_scan(sum, sh);
-                if (tid == kThreads - 1) sh->found_mass = sum;
-                __syncthreads();
-                ok = (cut_p ? mass_needed(p, sh->total) : drawn_mass(u, sh->total) + 1) <= sh->found_mass;
-            }
-            if (ok) {
+            const bool ok = count <= kList;
+            if (ok) {  // (all that is kept is there)
                 sort_and_sum(count, 0);
-                const unsigned long long head = sh->cum[count - 1];
-                unsigned long long kept = cut_k ? sh->cum[min(k, count) - 1] : sh->total;
-                if (cut_p) {
-                    const unsigned long long need = mass_needed(p, kept);
-                    ok = need <= head;
-                    if (ok) kept = sh->cum[first_of_mass(need, count)];
-                }
-                if (ok && least > 1) {
+                unsigned long long kept = sh->cum[(cut_k ? min(k, count) : count) - 1];
+                if (cut_p) kept = sh->cum[first_of_mass(mass_needed(p, kept), count)];
+                if (least > 1) {
                     int heavy = 0;  // those that min_p keeps
 #pragma unroll
                     for (int j = 0; j < kEach; ++j) heavy += __syncthreads_count(w[j] >= least);
-                    ok = heavy < count || kept <= head;  // (else there may be more outside)
                     kept = min(kept, sh->cum[heavy - 1]);
                 }
-                const unsigned long long passed = drawn_mass(u, kept);
-                ok = ok && passed < head;
-                if (ok) {
-                    const int f = first_of_mass(passed + 1, count);
-                    if (tid == 0) write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
-                }
+                const int f = first_of_mass(drawn_mass(u, kept) + 1, count);
+                if (tid == 0) write(~uint32_t(sh->list[f]), sh->cum[f] - (f ? sh->cum[f - 1] : 0), kept);
             }
             if (tid < cluster) at_cta(sh, uint32_t(tid))->cmd.op = ok ? OP_DONE : OP_HISTOGRAM;
         }

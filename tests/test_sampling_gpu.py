@@ -208,6 +208,23 @@ def test_sample(tq2, dtype, rows, vocab, sharp, filters):
     assert near <= 1 + rows // 100
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,vocab", [(200, 30_011), (150, 1025), (40, 131_000)])
+def test_sample_without_top_k(tq2, dtype, rows, vocab):
+    """Rows from nearly flat to nearly decided, with every mix of the other filters."""
+    rng = np.random.default_rng(vocab)
+    x = rng.standard_normal((rows, vocab)) * np.exp(rng.uniform(-4, 2, (rows, 1)))
+    x[::5] = np.round(x[::5] * 4) / 4          # many equal
+    x[1::7, vocab // 3:] = -INF
+    x[2::9, :3] += 12.0                        # a few that outweigh the rest
+    logits = torch.from_numpy(x).to(DTYPES[dtype]).cuda()
+    f = dict(temperature=np.exp(rng.uniform(-1, 1, rows)).tolist(),
+             top_p=np.where(rng.random(rows) < 0.7, 1 - rng.uniform(0, 1, rows) ** 3, 1.0).tolist(),
+             min_p=np.where(rng.random(rows) < 0.3, rng.uniform(0, 0.05, rows), 0.0).tolist())
+    near = check_sample(tq2, logits, rng.random(rows).tolist(), **f)
+    assert near <= 1 + rows // 100
+
+
 @pytest.mark.parametrize("vocab", [5, 1003, 70_000])
 def test_every_token_by_its_share(tq2, vocab):
     """u steps through the whole order: equal weights' tokens come in the order of their indices."""
