@@ -286,6 +286,29 @@ def test_stream_and_replay(tq2, dtype):
     assert tq2.tq2_device_status() == tq2.TQ2_OK
 
 
+@pytest.mark.parametrize("tokens", [5, 600])
+def test_captured_without_a_workspace_and_beside_another_graph(tq2, tokens):
+    """A temporary of the graph's own in one graph, a workspace that both an eager call and another graph use in the other."""
+    layer, rng = Layer(tq2, 4, 256, 128, seed=36), np.random.default_rng(37)
+    x = torch.from_numpy(rng.standard_normal((tokens, 256))).to(torch.bfloat16).cuda()
+    expert, weight = (torch.from_numpy(a).cuda() for a in routed(rng, tokens, 4, 2))
+    want, outs, graphs = tq2.moe_swiglu(layer.dev, x, expert, weight), [], []
+    ws = tq2.moe_swiglu_workspace(layer.dev, tokens, 2, x.dtype)
+    for workspace in (None, ws):
+        outs.append(torch.empty_like(x))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            tq2.moe_swiglu(layer.dev, x, expert, weight, out=outs[-1], workspace=workspace)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(NAN)
+        graphs[0].replay()
+        graphs[1].replay()
+        eager = tq2.moe_swiglu(layer.dev, x, expert, weight, workspace=ws)
+        graphs[0].replay()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and torch.equal(eager, want)
+
+
 def test_larger_workspace_serves_fewer_tokens(tq2):
     layer = Layer(tq2, 4, 256, 256, seed=24)
     ws = tq2.moe_swiglu_workspace(layer.dev, 300, 2, torch.bfloat16)
