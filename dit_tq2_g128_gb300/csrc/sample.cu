@@ -61,6 +61,7 @@ struct alignas(16) Shared {  // (the row follows it, in packs of 16 bytes)
     unsigned long long total, found_mass, found_before, kept;
     unsigned long long sums[4], my_sums[4];  // of a guess: all weights, those min_p keeps, those above each range; this CTA's
     float range[2][2];  // logits from and to which answers are looked for
+    float heavy[2];  // what min_p keeps, without and with the bin it ends in
     int edge[4];
     uint32_t until[4];
     uint32_t top[kMaxCluster], ties[kMaxCluster];
@@ -495,40 +496,45 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
                 sh->edge[tid] = kFine;
                 sh->until[tid] = uint32_t(whole >> 45);
             }
-            if (tid == 0) sh->floor = row;
+            if (tid < 2) sh->heavy[tid] = row;
             __syncthreads();
-            float kept = cut_p ? row * fmaxf(p, 0.f) : row;
-            const float target1 = kept;
+            // Edge i: the bin in which the cumulative weight passes `at`.
+            auto find_edge = [&](int i, float at) {
+                if (tid == 0 && !(at >= 0.f)) {
+                    sh->edge[i] = 0;
+                    sh->until[i] = 0;
+                }
+                if (!(first > at) && last > at) {
+                    float c = first;
+                    uint32_t n = before;
+                    int b = b0;
+                    for (; b < b1 - 1 && !((c += of_bin(b)) > at); ++b) n += fine[b];
+                    sh->edge[i] = b + (i & 1);  // (whole bins: elements may be few, or lie on a grid as coarse as the bins)
+                    sh->until[i] = n + (i & 1 ? fine[b] : 0);
+                }
+            };
             if (least > 1) {
                 const int b = min(int((float(kWeightBits) - log2f(float(least))) * fine_per_unit), kFine - 1);
                 if (b >= b0 && b < b1) {
                     float c = first;
-                    for (int j = b0; j <= b; ++j) c += of_bin(j);
-                    sh->floor = c;
+                    for (int j = b0; j < b; ++j) c += of_bin(j);
+                    sh->heavy[0] = c;
+                    sh->heavy[1] = c + of_bin(b);
                 }
-                __syncthreads();
-                kept = fminf(kept, sh->floor);
             }
-            const float target2 = kept * fminf(fmaxf(u, 0.f), 1.f);
             // three times what the places of elements within their bins may add up to (their standard deviation, with the sum of
             // squared weights at most the sum), twice that where what is kept is a guess too
             const float slack = 0.6f * unit * sqrtf(row * 0x1p26f);
-            const float at[4] = {target1 - slack, target1 + slack, target2 - 2.f * slack, target2 + 2.f * slack};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (tid == 0 && !(at[i] >= 0.f)) {
-                    sh->edge[i] = 0;
-                    sh->until[i] = 0;
-                }
-                if (!(first > at[i]) && last > at[i]) {
-                    float c = first;
-                    uint32_t n = before;
-                    int b = b0;
-                    for (; b < b1 - 1 && !((c += of_bin(b)) > at[i]); ++b) n += fine[b];
-                    sh->edge[i] = b + (i & 1);  // (whole bins: elements may be few, or lie on a grid as coarse as the bins)
-                    sh->until[i] = n + (i & 1 ? fine[b] : 0);
-                }
+            const float target = cut_p ? row * fmaxf(p, 0.f) : row;
+            if (cut_p) {
+                find_edge(0, target - slack);
+                find_edge(1, target + slack);
             }
+            __syncthreads();
+            // (top_p keeps the element that it ends in, and so up to the weight of one at its range's upper end more)
+            const float over = cut_p ? exp2f(26.f - float(sh->edge[0]) * unit) : 0.f, part = fminf(fmaxf(u, 0.f), 1.f);
+            find_edge(2, part * fminf(target, sh->heavy[0]) - 2.f * slack);
+            find_edge(3, part * fminf(target + over, sh->heavy[1]) + 2.f * slack);
             __syncthreads();
             if (tid < cluster) {
                 Shared *to = at_cta(sh, uint32_t(tid));
