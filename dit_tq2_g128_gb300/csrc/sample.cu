@@ -19,7 +19,7 @@
 // Bound by latency for one row (32,000 logits: 8.1 us) and by a row's chain for many: with a top-k 28,000 cycles (loading 9,
 // four cluster barriers with the bound 6, collecting 5, sorting 5, the answer 3), two CTAs an SM (256 rows of 100,003
 // bf16 logits: 63 us); without one 55,000, of which the exact sums are a third, some 60 instructions a weight (16 flat rows of
-// 200,000: 40 us; 64 rows of 128,000 f32, a quarter without a top-k: 54 us, all: 71, of bf16 53, all with one of 2000: 92; one
+// 200,000: 40 us; 64 rows of 128,000 f32, a quarter without a top-k: 49 us, all: 71, of bf16 53, all with one of 2000: 92; one
 // such row 22).  The exact histogram in place of the guess, with
 // four shared atomics an element and two passes to collect, took 81 and 75 us.
 #include <algorithm>
