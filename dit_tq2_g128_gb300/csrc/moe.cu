@@ -15,6 +15,7 @@
 
 #include <cuda_fp8.h>
 
+#include "cluster.cuh"
 #include "dtype.cuh"
 #include "moe.cuh"
 #include "paged_attention.cuh"
@@ -23,21 +24,6 @@ namespace tq2 {
 namespace {
 
 constexpr int kPlanThreads = 1024, kPlanMaxCluster = 8, kPlanPairs = 4096;  // pairs of a CTA before there are more of them
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-template <typename P>
-__device__ __forceinline__ const P *at_cta(const P *p, uint32_t rank) {
-    uint64_t r;
-    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-    return reinterpret_cast<const P *>(r);
-}
 
 // Exclusive sum over the block's threads (of WARPS warps) of v; total: the sum.
 template <int WARPS>

@@ -25,6 +25,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "cluster.cuh"
 #include "dtype.cuh"
 #include "paged_attention.cuh"
 #include "sample_weight.cuh"
@@ -71,22 +72,6 @@ struct alignas(16) Shared {  // (the row follows it, in packs of 16 bytes)
     float floor;  // the head: logits from here on
     Command cmd;
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The same place in CTA `rank`'s shared memory, as a generic pointer.
-template <typename P>
-__device__ __forceinline__ P *at_cta(P *p, uint32_t rank) {
-    uint64_t r;
-    asm volatile("mapa.u64 %0, %1, %2;" : "=l"(r) : "l"(reinterpret_cast<uint64_t>(p)), "r"(rank));
-    return reinterpret_cast<P *>(r);
-}
 
 __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) {
     const int lane = threadIdx.x & 31;
