@@ -222,6 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     const uint32_t rank = cluster_rank();
     const int64_t r = blockIdx.x / cluster;
     Shared *lead = at_cta(sh, 0);
+    cluster_arrive();  // (begun; waited for before another CTA's memory is written, behind the row's load)
     uint32_t *fine = sh->mass[0];
     for (int i = tid; i < kFine; i += kThreads) fine[i] = 0;
     if (tid < 4) sh->sums[tid] = sh->my_sums[tid] = 0;
@@ -249,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
         const uint32_t l = __reduce_min_sync(0xffffffffu, order_key(lowest));
         if (lane == 0) sh->part[tid >> 5] = static_cast<unsigned long long>(l) << 32 | m;
         __syncthreads();
+        cluster_wait();  // every CTA has begun
         if (tid < cluster) {
             uint32_t best = 0, least = 0xffffffffu;
             for (int w = 0; w < kWarps; ++w) {
