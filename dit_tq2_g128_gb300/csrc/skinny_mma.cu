@@ -36,6 +36,7 @@
 #include <climits>
 #include <cstring>
 
+#include "cluster.cuh"
 #include "tq2_internal.cuh"
 
 namespace tq2 {
@@ -72,10 +73,6 @@ __device__ __forceinline__ void sk_tma_2d(uint32_t dst, const CUtensorMap *map, 
         : "memory");
 }
 
-__device__ __forceinline__ void sk_cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // Shared-memory address of the same offset in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t sk_mapa(uint32_t addr, uint32_t rank) {
     uint32_t r;
@@ -105,6 +102,7 @@ skinny_mma_kernel(const __grid_constant__ CUtensorMap qmap, const __half *__rest
     extern __shared__ __align__(1024) uint8_t sk_raw[];
     uint8_t *base = sk_raw + ((1024u - (smem_u32(sk_raw) & 1023u)) & 1023u);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    cluster_arrive();  // begun: waited for before the partial sums are pushed
     const int S = P.S;
     const int rank = int(blockIdx.x) % S, tile = int(blockIdx.x) / S;
     const int b0 = int(int64_t(rank) * P.nb / S), b1 = int(int64_t(rank + 1) * P.nb / S);
@@ -222,6 +220,7 @@ skinny_mma_kernel(const __grid_constant__ CUtensorMap qmap, const __half *__rest
         }
     }
     __syncthreads();
+    cluster_wait();  // every CTA of the cluster has begun, so that its receive buffer may be written
 
     // ---- contraction: warp w owns weight rows 16w + g and 16w + g + 8 of the tile
     const int g = lane >> 2, q = lane & 3;
@@ -318,7 +317,7 @@ skinny_mma_kernel(const __grid_constant__ CUtensorMap qmap, const __half *__rest
         push(rb, n0, acc[t][2]);
         push(rb, n0 + 1, acc[t][3]);
     }
-    sk_cluster_sync();
+    cluster_sync();
     for (int it = tid; it < P.M * rpr; it += SK_THREADS) {
         const int nrow = it / rpr, rl = it - nrow * rpr;
         const int grow = row0 + rank * rpr + rl;

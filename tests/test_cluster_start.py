@@ -11,7 +11,7 @@ import pytest
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "dit_tq2_g128_gb300", "csrc")
 # an access by a mapped address (`lead` is one kept as a pointer), and what ends a thread's wait for the whole cluster
 ACCESS = re.compile(r"at_cta\([^;]*?\)(?:->|\[)|\*at_cta\(|\blead->|sk_mapa\(")
-BARRIER = re.compile(r"\b(?:sk_)?cluster_(?:sync|wait)\(\);")
+BARRIER = re.compile(r"\bcluster_(?:sync|wait)\(\);")
 
 
 def kernels(text):
@@ -33,13 +33,13 @@ def early(body):
 
 def test_the_check_itself():
     assert early("int a; at_cta(sh, 1)->x = 2; cluster_sync();")
-    assert early("push(sk_mapa(p, 1)); sk_cluster_sync();")
+    assert early("push(sk_mapa(p, 1)); cluster_sync();")
     assert not early("Shared *lead = at_cta(sh, 0); cluster_arrive(); cluster_wait(); lead->x = 1;")
     assert early("cluster_arrive(); lead->x = 1; cluster_wait();")
     assert not early("cluster_sync();")
 
 
-@pytest.mark.parametrize("source", ["sample.cu", "moe.cu"])
+@pytest.mark.parametrize("source", ["sample.cu", "moe.cu", "skinny_mma.cu"])
 def test_all_ctas_have_begun(source):
     with open(os.path.join(CSRC, source)) as f:
         bodies = list(kernels(f.read()))
