@@ -841,6 +841,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(SampleArgs a, int s
     command(Command{OP_DONE});
 }
 
+// Shared memory of a CTA that holds `slice` logits: at most those of the largest vocabulary over the most CTAs, as more CTAs take
+// a row as long as a slice has more than 64 KB.
+template <typename T>
+constexpr size_t shared_bytes(int slice) {
+    return sizeof(Shared) + size_t(slice) * sizeof(T) + 32;
+}
+static_assert(kMaxVocab / kMaxCluster * 2 >= 65536 && shared_bytes<float>(kMaxVocab / kMaxCluster) <= 232448);
+
 template <typename T>
 cudaError_t launch(const SampleArgs &a, const LaunchCtx &ctx) {
     // CTAs of a row: at least as many as its slices need to let two CTAs share an SM, more where rows are few
@@ -848,9 +856,11 @@ cudaError_t launch(const SampleArgs &a, const LaunchCtx &ctx) {
     while (cluster < kMaxCluster && int64_t(a.vocab) * int64_t(sizeof(T)) > int64_t(cluster) * 65536) cluster *= 2;
     while (cluster < kMaxCluster && a.rows * cluster * 2 <= 2 * ctx.num_sms && a.vocab > cluster * 2048) cluster *= 2;
     const int slice = ((a.vocab + cluster - 1) / cluster + 7) & ~7;
-    const size_t smem = sizeof(Shared) + size_t(slice) * sizeof(T) + 32;
+    const size_t smem = shared_bytes<T>(slice);
     auto kernel = sample_kernel<T>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // (the process's, so that calls of several threads all ask for the same: a smaller one could come between another's and its
+    // launch)
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(shared_bytes<T>(kMaxVocab / kMaxCluster)));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(a.rows * cluster));

@@ -1,0 +1,65 @@
+"""Two host threads, each on a stream of its own, call the same entry point with sizes that need different amounts of shared
+memory: what one thread's call asks of a kernel must not fail the other's launch."""
+
+import threading
+
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tq2():
+    import dit_tq2_g128_gb300 as m
+    return m
+
+
+def at_once(calls, times):
+    """Runs each of `calls` (functions of a stream) `times` times in a thread of its own; what they raised."""
+    errors, begin = [], threading.Barrier(len(calls))
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+
+    def work(call, stream):
+        try:
+            begin.wait()
+            for i in range(times):
+                call(stream)
+                if i % 64 == 63:
+                    stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(calls, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return errors
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_sampling_of_two_vocabularies(tq2, dtype):
+    torch_type, kind = {"f32": (torch.float32, tq2.TQ2_F32), "bf16": (torch.bfloat16, tq2.TQ2_BF16)}[dtype]
+    calls, results = [], []
+    for rows, vocab in ((1, 200_000), (2, 32_000), (1, 3000), (1, 260_000)):
+        gen = torch.Generator(device="cuda").manual_seed(vocab)
+        x = torch.randn((rows, vocab), device="cuda", generator=gen).to(torch_type)
+        u, k = torch.rand(rows, device="cuda", generator=gen), torch.full((rows,), 30, dtype=torch.int32, device="cuda")
+        want = tq2.sample(x, u, top_k=k)
+        out = torch.empty_like(want[0]), torch.empty_like(want[1])
+        results.append((want, out, x, u, k))
+        # (the C entry point with its arguments at hand, so that most of a call is spent in it)
+        at = x.data_ptr(), kind, vocab, u.data_ptr(), tq2.tq2_sampling(top_k=k), out[0].data_ptr(), out[1].data_ptr(), rows, vocab
+
+        def call(stream, at=at):
+            status = tq2.lib.tq2_sample(*at, stream.cuda_stream)
+            if status:
+                raise tq2.TQ2Error(status, "tq2_sample")
+
+        calls.append(call)
+    assert at_once(calls, 5000) == []
+    for want, out, *_ in results:
+        assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
