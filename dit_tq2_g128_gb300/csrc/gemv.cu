@@ -1033,7 +1033,7 @@ cudaError_t launch_gemv_stream(const void *w_soa, const float *x, const float *r
     P.xbox_rows = wide ? int(k / kGwLaneW) : (((xrows + P.nxbox - 1) / P.nxbox) + 7) & ~7;
     const size_t x_bytes = size_t(P.nxbox) * P.xbox_rows * 128;
     // two CTAs per SM: 2 * (this + 1 KB reserved per CTA) within 228 KB
-    const size_t budget = 112 * 1024;
+    constexpr size_t budget = 112 * 1024;
     const size_t fixed = 1024 + x_bytes + partial_bytes + 64 * 16 + 32;
     if (fixed + stage_bytes > budget) return cudaErrorNotSupported;
     // ring: enough slots for all of a CTA's stages if shared memory allows (no
@@ -1095,8 +1095,9 @@ cudaError_t launch_gemv_stream(const void *w_soa, const float *x, const float *r
         default: TQ2_GV_KERN(8); break;
     }
 #undef TQ2_GV_KERN
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    // (the process's, so that calls of several threads all ask for the same: a smaller one could come between another's
+    // and its launch)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(budget));
     if (e != cudaSuccess) return e;
     // the largest shared-memory carve-out, so that two CTAs fit on an SM
     e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100);

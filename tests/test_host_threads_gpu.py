@@ -63,3 +63,27 @@ def test_sampling_of_two_vocabularies(tq2, dtype):
     assert at_once(calls, 5000) == []
     for want, out, *_ in results:
         assert torch.equal(want[0], out[0]) and torch.equal(want[1], out[1])
+
+
+def products(tq2, kernel, shapes, times):
+    """The same kernel's products of several shapes (m, n, k) at once."""
+    calls, results = [], []
+    for m, n, k in shapes:
+        gen = torch.Generator(device="cuda").manual_seed(n + k)
+        w = torch.randint(0, 256, (tq2.tq2_soa_bytes(n, k),), dtype=torch.uint8, device="cuda", generator=gen)
+        w[n * k // 4:].view(torch.float16).uniform_(0.5 * k ** -0.5, 1.5 * k ** -0.5, generator=gen)
+        x = torch.randn((m, k), device="cuda", generator=gen)
+        want, out = (torch.empty((m, n), device="cuda") for _ in range(2))
+        call = lambda s, o, w=w, x=x, m=m, n=n, k=k: tq2.tq2_gemm_with(kernel, w, x, None, o, m, n, k, stream=s)  # noqa: E731
+        call(None, want)
+        results.append((want, out))
+        calls.append(lambda s, call=call, out=out: call(s, out))
+    assert at_once(calls, times) == []
+    for want, out in results:
+        assert torch.equal(want, out)
+
+
+# (the pairs share a kernel: as many rows a stage)
+@pytest.mark.parametrize("shapes", [[(1, 12_288, 4096), (1, 4096, 4096)], [(1, 12_288, 5120), (1, 12_288, 1024)]])
+def test_gemv_of_two_sizes(tq2, shapes):
+    products(tq2, tq2.TQ2_KERNEL_GEMV, shapes, 2000)
