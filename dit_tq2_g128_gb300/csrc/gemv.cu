@@ -208,7 +208,7 @@ cudaError_t launch_tpl(const void *w_soa, const float *x, const float *residual,
     const int64_t target_ctas = int64_t(ctx.num_sms) * 3;
     int64_t rps = (n + S * target_ctas - 1) / (S * target_ctas);
     rps = std::max<int64_t>(1, std::min<int64_t>(rps, 16));
-    const int64_t max_smem = 200 * 1024;
+    constexpr int64_t max_smem = 200 * 1024;
     while (rps > 1 && S * rps * C * MR * 4 > max_smem) --rps;
     const int64_t R = S * rps;
     const size_t smem = size_t(R) * C * MR * 4;
@@ -216,8 +216,8 @@ cudaError_t launch_tpl(const void *w_soa, const float *x, const float *residual,
     if (int64_t(k) > INT32_MAX || n > INT32_MAX || m > INT32_MAX) return cudaErrorInvalidValue;
     auto kern = smallm_kernel<MR, WPL>;
     if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+        // (always the most: the attribute is the process's, and another thread's launch may need more than this one)
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(max_smem));
         if (e != cudaSuccess) return e;
     }
     const SoaView v = soa_view(w_soa, n, k);

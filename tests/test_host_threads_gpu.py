@@ -87,3 +87,7 @@ def products(tq2, kernel, shapes, times):
 @pytest.mark.parametrize("shapes", [[(1, 12_288, 4096), (1, 4096, 4096)], [(1, 12_288, 5120), (1, 12_288, 1024)]])
 def test_gemv_of_two_sizes(tq2, shapes):
     products(tq2, tq2.TQ2_KERNEL_GEMV, shapes, 2000)
+
+
+def test_small_products_of_two_lengths(tq2):
+    products(tq2, tq2.TQ2_KERNEL_SKINNY, [(4, 7296, 262_144), (4, 7296, 131_072)], 200)
