@@ -416,7 +416,8 @@ cudaError_t launch_skinny_mma(const void *w_soa, const float *x, const float *re
         case 3: kern = skinny_mma_kernel<3>; break;
         default: kern = skinny_mma_kernel<4>; break;
     }
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    // (always the most: the attribute is the process's, and another thread's launch may need more than this one)
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(SK_SMEM_BUDGET));
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(tiles * S));

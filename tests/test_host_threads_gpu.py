@@ -91,3 +91,7 @@ def test_gemv_of_two_sizes(tq2, shapes):
 
 def test_small_products_of_two_lengths(tq2):
     products(tq2, tq2.TQ2_KERNEL_SKINNY, [(4, 7296, 262_144), (4, 7296, 131_072)], 200)
+
+
+def test_skinny_products_of_two_sizes(tq2):
+    products(tq2, tq2.TQ2_KERNEL_SKINNY_MMA, [(8, 4096, 4096), (8, 1024, 1024), (7, 9728, 8192)], 2000)
