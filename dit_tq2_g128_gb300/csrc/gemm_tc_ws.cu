@@ -863,15 +863,24 @@ uint8_t *g_noalloc_ptr[64];  // device address of the scratch array, per device
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static PFN_cuCtxGetCurrent_v4000 current = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+        auto find = [](const char *name, unsigned int version) {
+            void *p = nullptr;
+            cudaDriverEntryPointQueryResult q;
+            const bool there = cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) == cudaSuccess &&
+                               q == cudaDriverEntryPointSuccess;
+            return there ? p : nullptr;
+        };
+        current = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(find("cuCtxGetCurrent", 4000));
+        fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(find("cuTensorMapEncodeTiled", 12000));
     });
+    // The encoder wants a context, and a host thread that has launched nothing yet has none: it gets its device's.
+    CUcontext ctx = nullptr;
+    int dev = 0;
+    if (current && (current(&ctx) != CUDA_SUCCESS || !ctx) && (cudaGetDevice(&dev) != cudaSuccess || cudaSetDevice(dev) != cudaSuccess))
+        return nullptr;
     return fn;
 }
 

@@ -95,3 +95,60 @@ def test_small_products_of_two_lengths(tq2):
 
 def test_skinny_products_of_two_sizes(tq2):
     products(tq2, tq2.TQ2_KERNEL_SKINNY_MMA, [(8, 4096, 4096), (8, 1024, 1024), (7, 9728, 8192)], 2000)
+
+
+def first_calls(tq2):
+    """Functions of an output, one for each kernel that copies by tensor maps, and the outputs' shapes and types."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def weight(n, k):
+        w = torch.randint(0, 256, (tq2.tq2_soa_bytes(n, k),), dtype=torch.uint8, device="cuda", generator=gen)
+        w[n * k // 4:].view(torch.float16).uniform_(0.5 * k ** -0.5, 1.5 * k ** -0.5, generator=gen)
+        return w
+
+    w = weight(256, 1024)
+    rows = torch.randn((300, 1024), device="cuda", generator=gen)
+    ws = torch.empty(tq2.tq2_gemm_workspace_bytes(300, 256, 1024), dtype=torch.uint8, device="cuda")
+    heads = torch.randn((3, 2, 70, 64), device="cuda", generator=gen)
+    pages = torch.randn((2, 12, 16, 1, 64), device="cuda", generator=gen).to(torch.bfloat16)
+    q = torch.randn((140, 4, 64), device="cuda", generator=gen).to(torch.bfloat16)
+    ints = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    table = torch.arange(10, dtype=torch.int32, device="cuda")[None]
+    cache = tq2.KVCache(pages[0], pages[1])
+    batch = {t: tq2.PagedBatch(ints(0, t), ints(140), table, tokens=t, max_q=t, max_kv=140) for t in (1, 140)}
+    layer = tq2.Experts(weight(512, 256), weight(512, 128), experts=2, width=256, ffn=128)
+    expert, scale = torch.zeros((9, 1), dtype=torch.int32, device="cuda"), torch.ones((9, 1), device="cuda")
+    moe_ws = tq2.moe_swiglu_workspace(layer, 9, 1, torch.float32)
+    s = 0  # (the default stream, by its handle)
+    f32, bf16 = torch.float32, torch.bfloat16
+    return {
+        "gemv": (lambda o: tq2.tq2_gemv(w, rows, None, o, 256, 1024, stream=s), (256,), f32),
+        "skinny": (lambda o: tq2.tq2_gemm_with(tq2.TQ2_KERNEL_SKINNY_MMA, w, rows, None, o, 8, 256, 1024, stream=s), (8, 256), f32),
+        "rows": (lambda o: tq2.tq2_gemm_ws(w, rows, None, o, 300, 256, 1024, ws, ws.numel(), stream=s), (300, 256), f32),
+        "joint attention": (lambda o: tq2.tq2_attention_f32(*heads, o, 2, 70, 64, stream=s), (70, 128), f32),
+        "paged, few rows": (lambda o: tq2.attention_paged(q[:1], cache, batch[1], out=o, stream=s), (1, 4, 64), bf16),
+        "paged, many rows": (lambda o: tq2.attention_paged(q, cache, batch[140], out=o, stream=s), (140, 4, 64), bf16),
+        "experts": (lambda o: tq2.moe_swiglu(layer, rows.view(-1, 256)[:9], expert, scale, out=o, workspace=moe_ws, stream=s), (9, 256), f32),
+    }
+
+
+@pytest.mark.parametrize("name", ["gemv", "skinny", "rows", "joint attention", "paged, few rows", "paged, many rows", "experts"])
+def test_the_first_call_of_a_host_thread(tq2, name):
+    """A thread that has made no CUDA call yet gets what others get."""
+    call, shape, dtype = first_calls(tq2)[name]
+    want, got, errors = torch.empty(shape, dtype=dtype, device="cuda"), torch.empty(shape, dtype=dtype, device="cuda"), []
+
+    def work():
+        try:
+            call(got)
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    call(want)
+    torch.cuda.synchronize()
+    thread = threading.Thread(target=work)
+    thread.start()
+    thread.join()
+    torch.cuda.synchronize()
+    assert errors == []
+    assert torch.equal(want, got)
