@@ -497,8 +497,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 const int at = it.tile.row0 + min(32 * j + lane, left - 1);
                 scale[j] = g.scale[at];
                 if (GATE_UP && !L::F8) {
-                    // |gate|, |up| <= bound * sum < 2^(e + 1), so that a hidden value times 2^(13 - 2 e) is below 2^15
-                    const float b = __uint_as_float(bound) * g.sum[at];
+                    // |gate|, |up| <= 2 bound * sum < 2^(e + 1) (2: code 3), so that a hidden value times 2^(13 - 2 e) is below 2^15
+                    const float b = 2.f * __uint_as_float(bound) * g.sum[at];
                     const int e = b < INFINITY ? max(min(13 - 2 * moe_log2(b), 126), -126) : 0;
                     up[j] = moe_power(e);
                     if (it.part == 0 && q == 0) g.scale_out[at] = moe_power(-e);

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 
 from oracle import decode
+from test_moe_gpu import check
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -33,3 +34,47 @@ def test_sampling_by_clusters_of_every_size(tq2, rows, vocab):
         assert margin < 4e-9 or (int(got[0][0][r]) == want and abs(float(got[0][1][r]) - wp) <= wp * 2.0 ** -23)
     for t, p in got[1:]:
         assert torch.equal(t, got[0][0]) and torch.equal(p, got[0][1])
+
+
+# ---------------------------------------------------------------------------
+# hidden values of a mixture: staged by a bound of them
+
+
+class Scaled:
+    """A layer of given codes (or of random ones below 3) and scales d(rng, rows, blocks); matrices for the oracle."""
+
+    def __init__(self, tq2, experts, width, ffn, gate_up_scales, code=None, seed=0):
+        rng = np.random.default_rng(seed)
+        self.n, self.width, self.ffn = experts, width, ffn
+
+        def soa(rows, cols, d, code):
+            c = rng.integers(0, 3, (4, rows * cols // 4), dtype=np.uint8) if code is None else np.full((4, rows * cols // 4), code, np.uint8)
+            q = c[0] | c[1] << 2 | c[2] << 4 | c[3] << 6
+            return np.concatenate([q, d.astype(np.float16).reshape(-1).view(np.uint8)])
+
+        gu = soa(experts * 2 * ffn, width, gate_up_scales(rng, experts * 2 * ffn, width // 128), code)
+        dn = soa(experts * width, ffn, rng.uniform(0.5, 1.5, (experts * width, ffn // 128)) * ffn ** -0.5, None)
+        self.gu, self.dn = decode.matrices(gu, experts, 2 * ffn, width), decode.matrices(dn, experts, width, ffn)
+        self.dev = tq2.Experts(torch.from_numpy(gu).cuda(), torch.from_numpy(dn).cuda(), experts=experts, width=width, ffn=ffn)
+
+    def run(self, tq2, x, dtype):
+        """All tokens at expert 0, against the oracle."""
+        xt = torch.from_numpy(x).to(DTYPES[dtype]).cuda()
+        expert, weight = np.zeros((len(x), 1), np.int32), np.linspace(0.5, 1.0, len(x), dtype=np.float32)[:, None]
+        out = tq2.moe_swiglu(self.dev, xt, torch.from_numpy(expert).cuda(), torch.from_numpy(weight).cuda())
+        assert tq2.tq2_device_status() == tq2.TQ2_OK
+        return xt, expert, weight, out
+
+
+@pytest.mark.parametrize("dtype,tokens", [("f32", 3), ("f32", 150), ("f16", 3), ("f16", 40), ("bf16", 3), ("bf16", 150)])
+@pytest.mark.parametrize("scale", [1.0, 1.5])
+def test_hidden_values_at_their_bound(tq2, dtype, tokens, scale):
+    """Code 3 is +2: gate and up reach twice the largest scale times the sum of |x|, in rows that one element outweighs and
+    in rows of one sign.  Sums from just above a power of two to just below the next."""
+    layer = Scaled(tq2, 1, 256, 128, lambda rng, r, b: np.full((r, b), scale), code=3)
+    rng = np.random.default_rng(tokens)
+    total = np.array([15.96, 8.01, 10.7, 1.0, 0.52, 3.97, 31.0, 0.1245])[np.arange(tokens) % 8] / scale
+    x = np.zeros((tokens, 256))
+    x[np.arange(tokens), rng.integers(0, 256, tokens)] = total
+    x[1::3] = total[1::3, None] / 256
+    check(layer, *(lambda xt, e, w, out: (out, dtype, xt, e, w))(*layer.run(tq2, x, dtype)))
