@@ -4,7 +4,7 @@
 // The (token, expert) pairs are sorted by expert, so that an expert's codes are read once for all its tokens; each pair's
 // activations are staged as terms that the tensor cores multiply (moe.cuh; moe_stage_kernel, which also sorts up to 1024
 // pairs; more are sorted by moe_plan_kernel).  The first product (moe_gemm.cu) ends in the SwiGLU and stages its hidden values
-// itself, scaled by a bound of them (largest block scale times sum of |x|, squared); of few tokens it leaves them in f32, as
+// itself, scaled by a bound of them (moe.cuh); of few tokens it leaves them in f32, as
 // e4m3 terms want the rows' largest values, and they are staged like the activations.  Each token's pairs of the second
 // product are summed in their order (moe_sum_kernel): the same bits on every call.
 //
@@ -117,16 +117,17 @@ moe_plan_kernel(const int32_t *__restrict__ expert, MoePlan plan, int pairs, int
 
 constexpr int kStageThreads = 128;
 constexpr int kFewPairs = 1024;     // that are sorted by the blocks that stage them
-constexpr int kBoundScales = 8192;  // block scales of a block that looks for the largest
+constexpr int kBoundScales = 1024;  // gate scales, and as many up scales, of a block that bounds an expert's hidden values
 
 struct StageArgs {
     MoePlan plan;
     void *staged;    // [pairs][terms][k]
     float *scale;    // [pairs]
     float *sum;      // [pairs] of |x|, not below it
-    const __half *d;
-    int64_t d_count;  // of an expert
-    int bound_blocks;
+    float *peak;     // [pairs] the largest sum of |x| in a block of 128, not below it
+    const __half *d;  // of gate and up
+    int ffn;
+    int bound_blocks, bound_rows, bound_lanes;  // of an expert; features of one; threads that share a feature
     int64_t tokens;
     int k, top_k, terms, experts;
     // where the pairs are not sorted yet
@@ -138,13 +139,14 @@ struct StageArgs {
 // Stages a token a block: the terms of its row times the power of two that brings its largest value between 2^14 and 2^15
 // (no value overflows, and one 2^-28 of the largest still has all its bits; e4m3: between 2^7 and 2^8), in the products'
 // order, to the rows of all its pairs; scale is the power that undoes it.  Of a row with an infinity or a NaN, e4m3 terms
-// hold neither: its scale is NaN.  The blocks behind the tokens' take the largest of some of the block scales of an expert
-// that has tokens.  PAIRS: the rows are of pairs already (hidden values).
+// hold neither: its scale is NaN.  The blocks behind the tokens' bound some hidden values of an expert that has tokens (see
+// moe.cuh).  PAIRS: the rows are of pairs already (hidden values).
 // ROUTE: the pairs (at most kFewPairs) are not sorted yet: each token's block finds the rows of its pairs by counting those
 // before them, and the first block behind the tokens' writes the tiles.
 template <typename T, bool F8, bool PAIRS, bool ROUTE>
 __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
-    __shared__ float part[2][kStageThreads / 32];
+    extern __shared__ uint4 bound_scales[];
+    __shared__ float part[3][kStageThreads / 32];
     __shared__ int to[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -155,25 +157,55 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
         for (int i = tid; i < pairs; i += kStageThreads) id[i] = a.expert[i];
     }
     if (blockIdx.x >= a.tokens + ROUTE) {
-        const int b = int(blockIdx.x - a.tokens - ROUTE), e = b / a.bound_blocks, i0 = b % a.bound_blocks * (kBoundScales / 8);
+        const int b = int(blockIdx.x - a.tokens - ROUTE), e = b / a.bound_blocks, f0 = b % a.bound_blocks * a.bound_rows;
         bool there = !ROUTE && a.plan.expert_rows[e] > 0;
         for (int i = tid; i < pairs; i += kStageThreads) there |= id[i] == e;  // (this thread's own)
         if (!__syncthreads_or(there)) return;
-        // (an expert has a multiple of 256 of them)
-        const uint4 *d = reinterpret_cast<const uint4 *>(a.d + e * a.d_count);
-        uint32_t top = 0;
+        // |d| of the features' gate rows, then of their up rows (features in multiples of 8: whole packs)
+        const int nb = a.k / kBlockW, n = min(a.bound_rows, a.ffn - f0), packs = n * nb / 8;
+        const uint4 *gate = reinterpret_cast<const uint4 *>(a.d + (int64_t(e) * 2 * a.ffn + f0) * nb);
+        const uint4 *up = reinterpret_cast<const uint4 *>(a.d + (int64_t(e) * 2 * a.ffn + a.ffn + f0) * nb);
 #pragma unroll 4
-        for (int i = i0 + tid; i < min(i0 + kBoundScales / 8, int(a.d_count / 8)); i += kStageThreads) {
-            const uint4 v = d[i];
-            for (uint32_t w : {v.x, v.y, v.z, v.w}) top = max(top, max(w & 0x7fffu, w >> 16 & 0x7fffu));
+        for (int i = tid; i < 2 * packs; i += kStageThreads) {
+            const uint4 v = i < packs ? gate[i] : up[i - packs];
+            bound_scales[i] = make_uint4(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu, v.z & 0x7fff7fffu, v.w & 0x7fff7fffu);
         }
-        top = __reduce_max_sync(0xffffffffu, top);
-        if (lane == 0) part[0][warp] = __half2float(__ushort_as_half(uint16_t(top)));
+        __syncthreads();
+        const __half *d = reinterpret_cast<const __half *>(bound_scales);
+        float most = 0.f, whole = 0.f;  // of a feature's products: of its rows' largest scales, of their sums
+        for (int f1 = 0; f1 < n; f1 += kStageThreads / a.bound_lanes) {
+            const int f = f1 + tid / a.bound_lanes;
+            float mg = 0.f, mu = 0.f, sg = 0.f, su = 0.f;
+            if (f < n)
+                for (int i = f * nb + tid % a.bound_lanes; i < (f + 1) * nb; i += a.bound_lanes) {
+                    const float g = __half2float(d[i]), u = __half2float(d[8 * packs + i]);
+                    mg = fmaxf(mg, g);
+                    mu = fmaxf(mu, u);
+                    sg += g;
+                    su += u;
+                }
+            for (int o = a.bound_lanes / 2; o; o >>= 1) {
+                mg = fmaxf(mg, __shfl_xor_sync(0xffffffffu, mg, o));
+                mu = fmaxf(mu, __shfl_xor_sync(0xffffffffu, mu, o));
+                sg += __shfl_xor_sync(0xffffffffu, sg, o);
+                su += __shfl_xor_sync(0xffffffffu, su, o);
+            }
+            most = fmaxf(most, mg * mu);  // (a NaN is left out: all that its expert gives is NaN)
+            whole = fmaxf(whole, sg * su);
+        }
+        most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+        whole = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(whole)));
+        if (lane == 0) {
+            part[0][warp] = most;
+            part[1][warp] = whole;
+        }
         __syncthreads();
         if (tid == 0) {
-            uint32_t most = 0;  // (of bits: a NaN is above all)
-            for (int w = 0; w < kStageThreads / 32; ++w) most = max(most, __float_as_uint(part[0][w]));
-            a.plan.bound[b] = most;
+            for (int w = 0; w < kStageThreads / 32; ++w) {
+                most = fmaxf(most, part[0][w]);
+                whole = fmaxf(whole, part[1][w]);
+            }
+            a.plan.bound[b] = make_float2(sqrtf(most), sqrtf(whole));
         }
         return;
     }
@@ -230,27 +262,37 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
         T e[16];
     };
     const Group *row = reinterpret_cast<const Group *>(x + t * a.k);
-    float top = 0.f, sum = 0.f;
+    float top = 0.f, sum = 0.f, peak = 0.f;
     bool odd = false;  // an infinity or a NaN
-    for (int g = tid; g < a.k / 16; g += kStageThreads) {
-        const Group v = row[g];
+    for (int g0 = 0; g0 < a.k / 16; g0 += kStageThreads) {
+        float mine = 0.f;
+        if (g0 + tid < a.k / 16) {
+            const Group v = row[g0 + tid];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const float f = fabsf(to_f32(v.e[i]));
-            top = fmaxf(top, f);
-            sum += f;
-            odd |= !(f < INFINITY);
+            for (int i = 0; i < 16; ++i) {
+                const float f = fabsf(to_f32(v.e[i]));
+                top = fmaxf(top, f);
+                mine += f;
+                odd |= !(f < INFINITY);
+            }
         }
+        if (F8) continue;
+        sum += mine;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);  // (a block of 128: eight groups)
+        peak = fmaxf(peak, mine);
     }
     top = odd ? INFINITY : top;
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        peak = fmaxf(peak, __shfl_xor_sync(0xffffffffu, peak, o));
     }
     if (lane == 0) {
         part[0][warp] = top;
         part[1][warp] = sum;
+        part[2][warp] = peak;
     }
     __syncthreads();
     sum = 0.f;
@@ -258,12 +300,16 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
     for (int w = 0; w < kStageThreads / 32; ++w) {
         top = fmaxf(top, part[0][w]);
         sum += part[1][w];
+        peak = fmaxf(peak, part[2][w]);
     }
     const int up = top < INFINITY ? min((F8 ? 7 : 14) - moe_log2(top), 126) : 0;
     const float by = moe_power(up);
     if (tid < a.top_k && to[tid] >= 0) {
         a.scale[to[tid]] = F8 && !(top < INFINITY) ? __uint_as_float(0x7fc00000u) : moe_power(-up);
-        if (!F8) a.sum[to[tid]] = sum * (1.f + 0x1p-10f);  // (its rounding, at most 2^-24 an addition)
+        if (!F8) {  // (more by what sums of these and of the scales may have been rounded down, 2^-24 an addition)
+            a.sum[to[tid]] = sum * (1.f + 0x1p-10f);
+            a.peak[to[tid]] = peak * (1.f + 0x1p-10f);
+        }
     }
     for (int g = tid; g < a.k / 16; g += kStageThreads) {
         const Group v = row[g];
@@ -377,8 +423,8 @@ Form form_of(int dtype, int64_t pairs, int64_t experts) {
 struct Workspace {
     MoePlan plan;
     uint8_t *staged_x, *staged_h;
-    float *scale_x, *scale_h, *sum_x, *h, *y;
-    int max_tiles, bound_blocks;  // bound_blocks: of an expert's block scales
+    float *scale_x, *scale_h, *sum_x, *peak_x, *h, *y;
+    int max_tiles, bound_rows, bound_blocks;  // features that a block bounds, blocks of an expert
     size_t bytes;
 
     // (Sizes are the largest that any form of this many pairs, or of fewer, takes.)
@@ -395,11 +441,13 @@ struct Workspace {
         take(plan.tiles, size_t(std::min(pairs, experts) + pairs / 16));
         take(plan.pair_row, size_t(pairs));
         take(plan.expert_rows, size_t(experts));
-        bound_blocks = int((2 * ffn * (width / kBlockW) + kBoundScales - 1) / kBoundScales);
+        bound_rows = std::max(8, int(kBoundScales / (width / kBlockW)) & ~7);
+        bound_blocks = int((ffn + bound_rows - 1) / bound_rows);
         take(plan.bound, size_t(experts * bound_blocks));
         take(scale_x, size_t(pairs));
         take(scale_h, size_t(pairs));
         take(sum_x, size_t(pairs));
+        take(peak_x, size_t(pairs));
         take(staged_x, size_t(std::max(pairs * (dtype == TQ2_F32 ? 4 : 2), few * 3) * width));
         take(staged_h, size_t(std::max(pairs * (dtype == TQ2_F32 ? 4 : 2), few * 3) * ffn));
         take(h, size_t(few * ffn));
@@ -447,9 +495,13 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     s.staged = w.staged_x;
     s.scale = w.scale_x;
     s.sum = w.sum_x;
+    s.peak = w.peak_x;
     s.d = gate_up.d;
-    s.d_count = int64_t(2) * a.ffn * (a.width / kBlockW);
+    s.ffn = a.ffn;
     s.bound_blocks = f8 ? 0 : w.bound_blocks;
+    s.bound_rows = w.bound_rows;
+    s.bound_lanes = 1;
+    while (s.bound_lanes < 16 && s.bound_lanes * 2 * w.bound_rows <= kStageThreads) s.bound_lanes *= 2;
     s.tokens = a.tokens;
     s.k = a.width;
     s.top_k = a.top_k;
@@ -459,7 +511,8 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     const dim3 stage_grid(unsigned(a.tokens + route + int64_t(a.experts) * s.bound_blocks));
     auto stage = f8 ? route ? moe_stage_kernel<T, true, false, true> : moe_stage_kernel<T, true, false, false>
                     : route ? moe_stage_kernel<T, false, false, true> : moe_stage_kernel<T, false, false, false>;
-    e = launch_dependent(stage, stage_grid, kStageThreads, 0, ctx.stream, x, s);
+    const int bound_bytes = f8 ? 0 : 2 * w.bound_rows * (a.width / kBlockW) * int(sizeof(__half));  // (16 KB at most)
+    e = launch_dependent(stage, stage_grid, kStageThreads, bound_bytes, ctx.stream, x, s);
     if (e != cudaSuccess) return e;
     MoeGemm g = {};
     g.plan = w.plan;
@@ -474,6 +527,7 @@ cudaError_t launch(const MoeArgs &a, int dtype, void *ws, const LaunchCtx &ctx) 
     g.staged = w.staged_x;
     g.scale = w.scale_x;
     g.sum = w.sum_x;
+    g.peak = w.peak_x;
     g.out = w.h;
     g.staged_out = reinterpret_cast<__half *>(w.staged_h);
     g.scale_out = w.scale_h;

@@ -18,7 +18,7 @@ struct MoePlan {
     MoeTile *tiles;
     int *pair_row;        // [pairs] row of each pair, -1: none
     int *expert_rows;     // [experts]
-    uint32_t *bound;      // [experts][bound_blocks] largest |d| among some of an expert's gate and up rows (the bits of an f32)
+    float2 *bound;        // [experts][bound_blocks] of some of an expert's features (see below)
 };
 
 // One ternary product of the layer: of staged activations (see moe_stage_kernel) with the rows of each tile's expert.
@@ -29,6 +29,7 @@ struct MoeGemm {
     const void *staged;  // binary16, or e4m3 where terms is 3
     const float *scale;  // of each row: what its staged values are to be multiplied by
     const float *sum;    // gate_up: of each row, the sum of |x|
+    const float *peak;   //          and the largest of a block of 128
     float *out;          // [rows][features]: of down the product, of gate_up, with three terms, the hidden values
     __half *staged_out;  // gate_up, one or two terms: the hidden values, staged
     float *scale_out;    //          and each row's scale
@@ -49,6 +50,13 @@ cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx
 // for 16 in 16 bits, and decoding to 8 bits is half the stores and no subtraction.  Measured against one binary16 term, the
 // whole call: 7 tokens, 2 of 8 experts of 4096 x 6144: 55.5 against 59.8 us; 64 tokens, 8 of 128 of 2048 x 768: 66.7 against
 // 67.7; one token of 6 of 64 of 2048 x 1408: 19.3 against 18.9.
+//
+// Scale of staged hidden values, which the first product stages before any of its row is known to all: a bound of them.
+// |Gate_f x| and |Up_f x| are at most 2 (code 3) times the sum over blocks of |d| times the block's sum of |x|, so that
+//   |h_f| <= (2 S)^2 P, P the largest over f of a product of a number of the gate row and one of the up row:
+// with S the sum of |x| of the row, their largest |d|; with S that of the block where it is largest, their sums of |d|.  The
+// smaller of both is taken (the second where few scales are large, the first where few elements are).  By a product over the
+// same feature, a large gate row counts once.
 //
 // Order of staged activations: a binary16 row holds elements i and i + 8 of each group of 16 at 2 i and 2 i + 1, as pairs of
 // codes are masked out of a word of 16 (the library's binary16 activation layout).  An e4m3 row holds the even and the odd elements

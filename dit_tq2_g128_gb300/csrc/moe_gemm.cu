@@ -486,10 +486,15 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             const __half *dp = g.d + int64_t(row) * nb;
             // the scales of the tile's rows, some in each lane
             const int left = it.tile.n;
-            uint32_t bound = 0;
+            uint32_t most = 0, whole = 0;
             if (GATE_UP && !L::F8) {
-                for (int j = lane; j < g.bound_blocks; j += 32) bound = max(bound, g.plan.bound[it.tile.expert * g.bound_blocks + j]);
-                bound = __reduce_max_sync(0xffffffffu, bound);
+                for (int j = lane; j < g.bound_blocks; j += 32) {
+                    const float2 b = g.plan.bound[it.tile.expert * g.bound_blocks + j];
+                    most = max(most, __float_as_uint(b.x));
+                    whole = max(whole, __float_as_uint(b.y));
+                }
+                most = __reduce_max_sync(0xffffffffu, most);
+                whole = __reduce_max_sync(0xffffffffu, whole);
             }
             float scale[COLS / 32], up[COLS / 32];  // up (gate_up): the power of two that the hidden values are staged with
 #pragma unroll
@@ -497,8 +502,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 const int at = it.tile.row0 + min(32 * j + lane, left - 1);
                 scale[j] = g.scale[at];
                 if (GATE_UP && !L::F8) {
-                    // |gate|, |up| <= 2 bound * sum < 2^(e + 1) (2: code 3), so that a hidden value times 2^(13 - 2 e) is below 2^15
-                    const float b = 2.f * __uint_as_float(bound) * g.sum[at];
+                    // |h| <= b^2 < 2^(2 e + 2) (see moe.cuh), so that times 2^(13 - 2 e) it is below 2^15
+                    const float b = 2.f * fminf(__uint_as_float(most) * g.sum[at], __uint_as_float(whole) * g.peak[at]);
                     const int e = b < INFINITY ? max(min(13 - 2 * moe_log2(b), 126), -126) : 0;
                     up[j] = moe_power(e);
                     if (it.part == 0 && q == 0) g.scale_out[at] = moe_power(-e);

@@ -575,10 +575,12 @@ typedef struct {
  * multiply: of f32 ones two in binary16 (2^-22 of a value, or 2^-39 of the row's largest), of
  * 16-bit ones one in binary16 (which holds their bits down to 2^-38 of the row's largest value)
  * or, where experts have 16 rows or fewer in the mean, three in e4m3 (to 2^-25 of it).
- * So too the hidden values h = silu(.) * (.): to 2^-11 of themselves (f32: 2^-22), or, where more,
- * 2^-36 of (the largest block scale of the expert's gate_up times sum |x|)^2; of few rows an
- * expert, 2^-12 of themselves or 2^-25 of the pair's largest.  No magnitude overflows on its
- * way that the formula in f32 does not.  Sums in f32, one rounding to the output's type.  A token's result may differ in its rounding with the
+ * So too the hidden values h = silu(.) * (.): to 2^-11 of themselves (f32: 2^-22) or, where more, 2^-36 of S^2 P:
+ * S = sum |x| and P the largest product, over the expert's features, of the largest block scales of the gate row and
+ * of the up row, or, if that is less, S the largest sum |x| of a block of 128 and P the largest product of the
+ * rows' sums of block scales; of few rows an expert, 2^-12 of themselves or 2^-25 of the pair's largest.  No
+ * magnitude overflows on its way that the formula in f32 does not.  Sums in f32, one rounding to the
+ * output's type.  A token's result may differ in its rounding with the
  * number of tokens of the call.
  * Memory: `workspace` holds the activations on their way
  * (tq2_moe_swiglu_workspace_bytes of the same arguments, 16-byte aligned); if NULL, a

@@ -78,3 +78,30 @@ def test_hidden_values_at_their_bound(tq2, dtype, tokens, scale):
     x[np.arange(tokens), rng.integers(0, 256, tokens)] = total
     x[1::3] = total[1::3, None] / 256
     check(layer, *(lambda xt, e, w, out: (out, dtype, xt, e, w))(*layer.run(tq2, x, dtype)))
+
+
+def spike(rng, rows, blocks, by):
+    """All scales equal but one."""
+    d = np.full((rows, blocks), (128 * blocks) ** -0.5)
+    d[rng.integers(rows), rng.integers(blocks)] *= by
+    return d
+
+
+SPREADS = {
+    "one 100 times the rest": lambda rng, r, b: spike(rng, r, b, 100.0),
+    "one 1000 times the rest": lambda rng, r, b: spike(rng, r, b, 1000.0),
+    "log-normal": lambda rng, r, b: np.exp(1.3 * rng.standard_normal((r, b))) * (128 * b) ** -0.5,
+    "a gate row 300 times the rest": lambda rng, r, b: np.where(np.arange(r)[:, None] == r // 3, 300.0, 1.0) * np.full((r, b), (128 * b) ** -0.5),
+}
+
+
+@pytest.mark.parametrize("dtype,tokens", [("f32", 4), ("f32", 40), ("f16", 40), ("bf16", 40), ("bf16", 4)])
+@pytest.mark.parametrize("spread", SPREADS)
+@pytest.mark.parametrize("width", [256, 1280, 4096])
+def test_scales_of_a_wide_spread(tq2, dtype, tokens, spread, width):
+    """Hidden values that a few of an expert's scales put far below their bound keep their bits (check's mean error; its bound
+    for single elements counts the sums' roundings at their worst and is wider for wide layers)."""
+    layer = Scaled(tq2, 1, width, 256, SPREADS[spread], seed=width)
+    x = np.random.default_rng(tokens).standard_normal((tokens, width))
+    xt, e, w, out = layer.run(tq2, x, dtype)
+    check(layer, out, dtype, xt, e, w)
