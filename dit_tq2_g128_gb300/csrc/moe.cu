@@ -143,8 +143,10 @@ struct StageArgs {
 // moe.cuh).  PAIRS: the rows are of pairs already (hidden values).
 // ROUTE: the pairs (at most kFewPairs) are not sorted yet: each token's block finds the rows of its pairs by counting those
 // before them, and the first block behind the tokens' writes the tiles.
+// At most 32 registers where tokens are few: beside a product's CTA an SM has 4096 left, so that blocks begin while the kernel before ends, and
+// the next product's CTAs beside them (with 36, 7 tokens of 8 experts of 4096 x 6144 took 65 us, not 55).
 template <typename T, bool F8, bool PAIRS, bool ROUTE>
-__global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
+__global__ void __launch_bounds__(kStageThreads, ROUTE || F8 ? 16 : 12) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
     extern __shared__ uint4 bound_scales[];
     __shared__ float part[3][kStageThreads / 32];
     __shared__ int to[32];
@@ -156,7 +158,7 @@ __global__ void __launch_bounds__(kStageThreads) moe_stage_kernel(const T *__res
     if constexpr (ROUTE) {
         for (int i = tid; i < pairs; i += kStageThreads) id[i] = a.expert[i];
     }
-    if (blockIdx.x >= a.tokens + ROUTE) {
+    if (!F8 && blockIdx.x >= a.tokens + ROUTE) {
         const int b = int(blockIdx.x - a.tokens - ROUTE), e = b / a.bound_blocks, f0 = b % a.bound_blocks * a.bound_rows;
         bool there = !ROUTE && a.plan.expert_rows[e] > 0;
         for (int i = tid; i < pairs; i += kStageThreads) there |= id[i] == e;  // (this thread's own)

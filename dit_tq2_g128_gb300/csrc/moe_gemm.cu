@@ -486,8 +486,20 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
             const __half *dp = g.d + int64_t(row) * nb;
             // the scales of the tile's rows, some in each lane
             const int left = it.tile.n;
-            uint32_t most = 0, whole = 0;
-            if (GATE_UP && !L::F8) {
+            float scale[COLS / 32], up[COLS / 32];  // up (gate_up): the power of two that the hidden values are staged with
+            float sum_x[COLS / 32], peak_x[COLS / 32];
+            constexpr bool STAGES = GATE_UP && !L::F8;
+#pragma unroll
+            for (int j = 0; j < COLS / 32; ++j) {
+                const int at = it.tile.row0 + min(32 * j + lane, left - 1);
+                scale[j] = g.scale[at];
+                if (STAGES) {
+                    sum_x[j] = g.sum[at];
+                    peak_x[j] = g.peak[at];
+                }
+            }
+            if (STAGES) {
+                uint32_t most = 0, whole = 0;
                 for (int j = lane; j < g.bound_blocks; j += 32) {
                     const float2 b = g.plan.bound[it.tile.expert * g.bound_blocks + j];
                     most = max(most, __float_as_uint(b.x));
@@ -495,18 +507,13 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 }
                 most = __reduce_max_sync(0xffffffffu, most);
                 whole = __reduce_max_sync(0xffffffffu, whole);
-            }
-            float scale[COLS / 32], up[COLS / 32];  // up (gate_up): the power of two that the hidden values are staged with
 #pragma unroll
-            for (int j = 0; j < COLS / 32; ++j) {
-                const int at = it.tile.row0 + min(32 * j + lane, left - 1);
-                scale[j] = g.scale[at];
-                if (GATE_UP && !L::F8) {
+                for (int j = 0; j < COLS / 32; ++j) {
                     // |h| <= b^2 < 2^(2 e + 2) (see moe.cuh), so that times 2^(13 - 2 e) it is below 2^15
-                    const float b = 2.f * fminf(__uint_as_float(most) * g.sum[at], __uint_as_float(whole) * g.peak[at]);
+                    const float b = 2.f * fminf(__uint_as_float(most) * sum_x[j], __uint_as_float(whole) * peak_x[j]);
                     const int e = b < INFINITY ? max(min(13 - 2 * moe_log2(b), 126), -126) : 0;
                     up[j] = moe_power(e);
-                    if (it.part == 0 && q == 0) g.scale_out[at] = moe_power(-e);
+                    if (it.part == 0 && q == 0) g.scale_out[it.tile.row0 + min(32 * j + lane, left - 1)] = moe_power(-e);
                 }
             }
             uint64_t acc[COLS / 2];  // columns 2 c, 2 c + 1
