@@ -137,7 +137,7 @@ struct StageArgs {
 };
 
 // Stages a token a block: the terms of its row times the power of two that brings its largest value between 2^14 and 2^15
-// (no value overflows, and one 2^-28 of the largest still has all its bits; e4m3: between 2^7 and 2^8), in the products'
+// (no value overflows, and one 2^-28 of the largest still has all bits of a binary16; e4m3: between 2^7 and 2^8), in the products'
 // order, to the rows of all its pairs; scale is the power that undoes it.  Of a row with an infinity or a NaN, e4m3 terms
 // hold neither: its scale is NaN.  The blocks behind the tokens' bound some hidden values of an expert that has tokens (see
 // moe.cuh).  PAIRS: the rows are of pairs already (hidden values).
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(kStageThreads, ROUTE || F8 ? 16 : 12) moe_stag
                 const float p = to_f32(v.e[i]) * by, q = to_f32(v.e[i + 8]) * by;
                 hi[i] = __floats2half2_rn(p, q);
                 const float2 h = __half22float2(hi[i]);
-                lo[i] = __floats2half2_rn(p - h.x, q - h.y);
+                lo[i] = __floats2half2_rn((p - h.x) * kLowScale, (q - h.y) * kLowScale);
             }
             for (int j = 0; j < a.top_k; ++j) {
                 if (to[j] < 0) continue;

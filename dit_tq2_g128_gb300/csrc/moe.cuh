@@ -43,7 +43,8 @@ struct MoeGemm {
 cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx);
 
 // Terms of a staged value v, scaled by a power of two to below 2^15 (2^8 for e4m3):
-//   1: binary16(v).   2: also binary16(v - first).
+//   1: binary16(v).   2: also binary16((v - first) 2^12), at most 2^15: what is left of v has 11 bits as long as v is 2^-14 or
+//      more, 2^-29 of the most (as it is it would lose bits from 2^-2 on, below 2^-17 of the most).
 //   3: e4m3 numbers t0, t1, t2 with v = t0 + t1 / 16 + t2 / 256: each rounds to four bits what is left, so that they hold
 //      twelve: all of a binary16's or bf16's (down to 2^-25 of the largest value), and others to 2^-12.
 // Three 8-bit terms where experts have few tokens: an MMA of few columns takes as long for 32 weights of a row in 8 bits as
@@ -63,6 +64,8 @@ cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx
 // of each 8 after each other, as codes are looked up from a word four at a time.
 __host__ __device__ constexpr int moe_place(int i) { return i < 8 ? 2 * i : 2 * (i - 8) + 1; }
 __host__ __device__ constexpr int moe_place8(int i) { return (i & 8) + (i & 1) * 4 + (i & 7) / 2; }
+
+constexpr float kLowScale = 4096.f;  // of the second of two terms
 
 // 2^e with e kept to what f32 holds as a normal number.
 __device__ __forceinline__ float moe_power(int e) { return __uint_as_float(uint32_t(max(min(e, 127), -126) + 127) << 23); }

@@ -574,7 +574,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 auto column = [&](int c) { return c & 1 ? second(acc[c >> 1]) : first(acc[c >> 1]); };
                 auto sum = [&](int c) {
                     if (S == 3) return fmaf(fmaf(column(3 * c + 2), 0x1p-4f, column(3 * c + 1)), 0x1p-4f, column(3 * c));
-                    return S == 2 ? column(2 * c) + column(2 * c + 1) : column(c);
+                    return S == 2 ? fmaf(column(2 * c + 1), 1.f / kLowScale, column(2 * c)) : column(c);
                 };
                 if (GATE_UP) {
                     // this lane's place in a staged row
@@ -598,7 +598,7 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                                     const __half hi = __float2half_rn(h);
                                     __half *to = out + int64_t(c + odd) * S * features;
                                     to[0] = hi;
-                                    if (S == 2) to[features] = __float2half_rn(h - __half2float(hi));
+                                    if (S == 2) to[features] = __float2half_rn((h - __half2float(hi)) * kLowScale);
                                 }
                             }
                         }

@@ -572,10 +572,10 @@ typedef struct {
  *   top_k    : 1 .. 32; tokens * top_k <= 2^22
  * gate_up, down, x, residual and out are 16-byte aligned.  out overlaps nothing else.
  * Arithmetic: weights exact; activations as sums of terms that the tensor cores
- * multiply: of f32 ones two in binary16 (2^-22 of a value, or 2^-39 of the row's largest), of
+ * multiply: of f32 ones two in binary16 (2^-22 of a value, or 2^-51 of the row's largest), of
  * 16-bit ones one in binary16 (which holds their bits down to 2^-38 of the row's largest value)
  * or, where experts have 16 rows or fewer in the mean, three in e4m3 (to 2^-25 of it).
- * So too the hidden values h = silu(.) * (.): to 2^-11 of themselves (f32: 2^-22) or, where more, 2^-36 of S^2 P:
+ * So too the hidden values h = silu(.) * (.): to 2^-11 of themselves (f32: 2^-22) or, where more, 2^-36 (f32: 2^-48) of S^2 P:
  * S = sum |x| and P the largest product, over the expert's features, of the largest block scales of the gate row and
  * of the up row, or, if that is less, S the largest sum |x| of a block of 128 and P the largest product of the
  * rows' sums of block scales; of few rows an expert, 2^-12 of themselves or 2^-25 of the pair's largest.  No

@@ -105,3 +105,16 @@ def test_scales_of_a_wide_spread(tq2, dtype, tokens, spread, width):
     x = np.random.default_rng(tokens).standard_normal((tokens, width))
     xt, e, w, out = layer.run(tq2, x, dtype)
     check(layer, out, dtype, xt, e, w)
+
+
+@pytest.mark.parametrize("dtype,tokens,by", [("f32", 4, 300.0), ("f32", 40, 300.0), ("f32", 40, 10_000.0), ("f16", 40, 300.0),
+                                             ("bf16", 40, 300.0), ("bf16", 40, 10_000.0)])
+@pytest.mark.parametrize("width", [256, 4096])
+def test_a_large_gate_that_is_shut(tq2, dtype, tokens, by, width):
+    """A gate row far above the others that every token holds below 0: it bounds the hidden values, and gives none of them."""
+    layer = Scaled(tq2, 1, width, 256, lambda rng, r, b: np.where(np.arange(r)[:, None] == 100, by, 1.0) * np.full((r, b), (128 * b) ** -0.5),
+                   seed=width)
+    x = np.random.default_rng(tokens).standard_normal((tokens, width))
+    x *= -np.sign(x @ layer.gu[0, 100])[:, None]
+    xt, e, w, out = layer.run(tq2, x, dtype)
+    check(layer, out, dtype, xt, e, w)
