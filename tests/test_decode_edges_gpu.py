@@ -118,3 +118,32 @@ def test_a_large_gate_that_is_shut(tq2, dtype, tokens, by, width):
     x *= -np.sign(x @ layer.gu[0, 100])[:, None]
     xt, e, w, out = layer.run(tq2, x, dtype)
     check(layer, out, dtype, xt, e, w)
+
+
+@pytest.mark.parametrize("tokens", [4, 60])
+def test_the_activation_of_closed_gates_in_f32(tq2, tokens):
+    """silu to a few units in the last place where it is an exponential's, gates of -14 to -2: gate_f = d_f x_0, up_f = x_1 = 1,
+    and down the identity, all exact.
+
+    Relative roundings: the exponential 2^-22 (2 units in the last place at most), 1 + e, the quotient and the terms' sum
+    2^-24 each, the two terms 2^-23: 4.5 * 2^-23; and the staging's floor, 2^-50 of b^2 = (2 (|x_0| + 1))^2 max d."""
+    ffn = 128
+    d = (1.0 + np.arange(ffn) / 256).astype(np.float16)
+    codes = np.ones((2 * ffn, 128), np.uint8)  # 1: zero
+    codes[:ffn, 0], codes[ffn:, 1] = 2, 2
+
+    def soa(codes, d):
+        c = codes.reshape(len(codes), -1, 4)
+        return torch.from_numpy(np.concatenate([(c[..., 0] | c[..., 1] << 2 | c[..., 2] << 4 | c[..., 3] << 6).reshape(-1),
+                                                d.view(np.uint8)])).cuda()
+
+    dev = tq2.Experts(soa(codes, np.concatenate([d, np.ones(ffn, np.float16)])),
+                      soa(np.ones((128, 128), np.uint8) + np.eye(128, dtype=np.uint8), np.ones(128, np.float16)), experts=1, width=128, ffn=ffn)
+    x = np.zeros((tokens, 128), np.float32)
+    x[:, 0], x[:, 1] = -2 - np.round(np.linspace(0, 7, tokens) * 64) / 64, 1.0
+    out = tq2.moe_swiglu(dev, torch.from_numpy(x).cuda(), torch.zeros((tokens, 1), dtype=torch.int32, device="cuda"),
+                         torch.ones((tokens, 1), device="cuda"))
+    want = decode.silu(x[:, :1].astype(np.float64) * d.astype(np.float64))
+    floor = 2.0 ** -50 * (2 * (np.abs(x[:, :1]) + 1)) ** 2 * float(d.max())
+    err = np.abs(out.double().cpu().numpy() - want)
+    assert np.all(err <= 4.5 * 2.0 ** -23 * np.abs(want) + floor), np.max((err - floor) / np.abs(want)) * 2.0 ** 23
