@@ -452,6 +452,9 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                         for (int c = 0; c < 2; ++c)
                             w[t][j][c] = *reinterpret_cast<const uint4 *>(
                                 row + (((2 * (min(from + DEC * t, PER - 1) * L::UNIT + j) + c) ^ (r & 7)) << 4));
+                // (read before the next copy may write there: without it loads were put off to where the codes are decoded, behind
+                // the wait for a slot, and where codes came late from memory some rows had the next stage's)
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctl->c_empty[sc]);
 #pragma unroll

@@ -147,3 +147,58 @@ def test_the_activation_of_closed_gates_in_f32(tq2, tokens):
     floor = 2.0 ** -50 * (2 * (np.abs(x[:, :1]) + 1)) ** 2 * float(d.max())
     err = np.abs(out.double().cpu().numpy() - want)
     assert np.all(err <= 4.5 * 2.0 ** -23 * np.abs(want) + floor), np.max((err - floor) / np.abs(want)) * 2.0 ** 23
+
+
+# ---------------------------------------------------------------------------
+# layers larger than the L2
+
+
+def large(tq2, tokens, dtype, seed, experts=8, width=8192, ffn=4096):
+    """A layer of 142 + 71 MB, tokens of it with two experts each."""
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+
+    def weight(rows, cols):
+        w = torch.randint(0, 256, (tq2.tq2_soa_bytes(rows, cols),), dtype=torch.uint8, device="cuda", generator=gen)
+        w[rows * cols // 4:].view(torch.float16).uniform_(0.5 * cols ** -0.5, 1.5 * cols ** -0.5, generator=gen)
+        return w
+
+    layer = tq2.Experts(weight(experts * 2 * ffn, width), weight(experts * width, ffn), experts=experts, width=width, ffn=ffn)
+    x = torch.randn((tokens, width), device="cuda", generator=gen).to(DTYPES[dtype])
+    expert = ((torch.arange(tokens, device="cuda")[:, None] * 2 + torch.tensor([[0, 1]], device="cuda")) % experts).int().contiguous()
+    return layer, x, expert, torch.ones((tokens, 2), device="cuda")
+
+
+def in_64_bits(layer, x, expert, scale):
+    """The layer's output by the formula, an expert's matrices at a time."""
+    out = torch.zeros(x.shape, dtype=torch.float64, device="cuda")
+
+    def matrix(soa, e, rows, cols):
+        at, n = layer.experts * rows * cols // 4, rows * cols // 4
+        q = soa[e * n:(e + 1) * n].view(rows, cols // 4)
+        c = torch.stack([q >> 2 * j & 3 for j in range(4)], -1).view(rows, cols).double() - 1.0
+        d = soa[at:].view(torch.float16).view(layer.experts, rows, cols // 128)[e].double()
+        return c.view(rows, cols // 128, 128).mul_(d[:, :, None]).view(rows, cols)
+
+    for e in range(layer.experts):
+        t, j = (expert == e).nonzero(as_tuple=True)
+        z = x[t].double() @ matrix(layer.gate_up, e, 2 * layer.ffn, layer.width).T
+        h = torch.nn.functional.silu(z[:, :layer.ffn]) * z[:, layer.ffn:]
+        out.index_add_(0, t, (h @ matrix(layer.down, e, layer.width, layer.ffn).T) * scale[t, j].double()[:, None])
+    return out
+
+
+@pytest.mark.parametrize("dtype,tokens", [("f32", 6), ("bf16", 6), ("f16", 150), ("f32", 300), ("bf16", 700)])
+def test_codes_that_come_late_from_memory(tq2, dtype, tokens):
+    """The same bits on every call, and the formula's values, where codes are awaited row by row from memory: a decoder that
+    gave a stage back before it had read it took the next one's in its place.  (Mean errors as in test_moe_gpu.check.)"""
+    layer, x, expert, scale = large(tq2, tokens, dtype, tokens)
+    rest = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")
+    good = tq2.moe_swiglu(layer, x, expert, scale)
+    ref = in_64_bits(layer, x, expert, scale)
+    typical = {"f32": 2.0 ** -20, "f16": 2.0 ** -11, "bf16": 2.0 ** -8.5}[dtype]
+    assert float((good.double() - ref).norm()) <= typical * 2 ** 0.5 * float(ref.norm())
+    for i in range(30):
+        if i % 2:
+            rest.fill_(i)  # (nothing of the layer is in the L2)
+        assert torch.equal(tq2.moe_swiglu(layer, x, expert, scale), good), i
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
