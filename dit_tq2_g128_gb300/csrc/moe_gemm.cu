@@ -324,8 +324,8 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
     const uint32_t tmem = uint32_t(uniform(int(ctl->tmem_base)));
     const int parts = g.rows / 128, nb = uniform(g.k / kBlockW), units = (nb + L::UNIT - 1) / L::UNIT;
     const int items = uniform(*g.plan.tile_count * parts);
-    auto wait_on = [&](uint64_t *bar, uint32_t parity) {
-        return bool(__all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, wait_ns, status)));
+    auto wait_on = [&](uint64_t *bar, uint32_t parity, uint32_t first_poll = 0) {
+        return bool(__all_sync(0xffffffffu, wait_phase(bar, parity, abort_flag, wait_ns, status, first_poll)));
     };
 
     if (warp < W_DECODE) {
@@ -542,8 +542,10 @@ moe_gemm_kernel(const __grid_constant__ CUtensorMap cmap, const __grid_constant_
                 for (int j = 0; j < L::UNIT; ++j) dn[j] = u * L::UNIT + j < nb ? __half2float(dp[u * L::UNIT + j]) : 0.f;
             };
             scales_of(0);
-            // (in turn: a group that waited for a unit two uses of its accumulator ahead would take the one before for it)
-            if (turn > 0 && !(ok = wait_on(&ctl->turn[group], ((turn - 1) >> 1) & 1))) break;
+            // (in turn: a group that waited for a unit two uses of its accumulator ahead would take the one before for it; the
+            // longest wait of all, which a limit of 0 gives up after one poll: looked at in all of them, that took a prompt
+            // from 530 to 534 us)
+            if (turn > 0 && !(ok = wait_on(&ctl->turn[group], ((turn - 1) >> 1) & 1, wait_ns ? 0 : 63))) break;
             for (int u = 0; u < units; ++u) {
                 const int n = n0 + u, sd = n % L::DRING;
                 uint64_t d[L::UNIT];

@@ -53,12 +53,13 @@ __device__ __forceinline__ bool elect_one() {
 // Bounded wait that also ends when another role of the CTA has given up; false (with
 // the flag set) then.  The flag and the timer are read at every 64th poll only (read
 // at each one, 512 tokens over 32768 keys took 208 us, not 198): a poll that fails
-// sleeps for 3.7 us, so a limit is kept to a quarter of a millisecond.
+// sleeps for 3.7 us, so a limit is kept to a quarter of a millisecond.  first: the number of the first poll (63: one
+// that fails is looked at at once).
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, volatile int *abort_flag, uint64_t wait_ns,
-                                           unsigned int *status) {
+                                           unsigned int *status, uint32_t first = 0) {
     const uint32_t addr = smem_u32(bar);
     uint64_t t0 = 0;
-    for (uint32_t it = 0;; ++it) {
+    for (uint32_t it = first;; ++it) {
         uint32_t ok;
         asm volatile(
             "{\n\t.reg .pred p;\n\t"

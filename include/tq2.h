@@ -633,8 +633,10 @@ int tq2_sample(const void *logits, int dtype, int64_t row_stride, const float *u
  * gives up after `ns` nanoseconds of %globaltimer time, records
  * TQ2_ERR_TIMEOUT in a device status word and lets the kernel exit cleanly
  * (draining its own in-flight work first).  Default 2e9 (2 s).  Applies to
- * launches issued after the call.  The paged attention looks at the limit about
- * four times a millisecond: a shorter wait does not run out, whatever the limit.
+ * launches issued after the call.  The paged attention and the experts' products look
+ * at the limit about four times a millisecond: a shorter wait does not run out, whatever
+ * the limit (but for one of the experts' products: with a limit of 0, that of one half of
+ * the sums for the other gives up after some microseconds).
  * Returns the previous value. */
 uint64_t tq2_set_wait_timeout_ns(uint64_t ns);
 

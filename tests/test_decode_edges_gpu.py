@@ -202,3 +202,37 @@ def test_codes_that_come_late_from_memory(tq2, dtype, tokens):
             rest.fill_(i)  # (nothing of the layer is in the L2)
         assert torch.equal(tq2.moe_swiglu(layer, x, expert, scale), good), i
     assert tq2.tq2_device_status() == tq2.TQ2_OK
+
+
+# ---------------------------------------------------------------------------
+# waits
+
+
+class Limit:
+    """A limit on the device's waits, put back at the end."""
+
+    def __init__(self, tq2, ns):
+        self.tq2, self.ns = tq2, ns
+
+    def __enter__(self):
+        torch.cuda.synchronize()
+        self.before = self.tq2.tq2_set_wait_timeout_ns(self.ns)
+
+    def __exit__(self, *_):
+        self.tq2.tq2_set_wait_timeout_ns(self.before)
+
+
+@pytest.mark.parametrize("dtype,tokens", [("f32", 6), ("bf16", 6), ("f16", 150), ("f32", 300)])
+def test_a_wait_of_the_experts_that_runs_out_is_reported(tq2, dtype, tokens):
+    """Three items and more a CTA, of 64 blocks: the second group of sums waits for all of the first one's, some 10 us and more,
+    which is longer than a poll sleeps."""
+    layer, x, expert, scale = large(tq2, tokens, dtype, tokens)
+    good = tq2.moe_swiglu(layer, x, expert, scale)
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
+    for _ in range(5):
+        with Limit(tq2, 0):
+            tq2.moe_swiglu(layer, x, expert, scale)
+            assert tq2.tq2_device_status() == tq2.TQ2_ERR_TIMEOUT
+        assert tq2.tq2_device_status() == tq2.TQ2_OK
+        assert torch.equal(tq2.moe_swiglu(layer, x, expert, scale), good)
+    assert tq2.tq2_device_status() == tq2.TQ2_OK
