@@ -455,7 +455,7 @@ paged_rows_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constan
                         if constexpr (THIRD) mma_16x8<T>(o[t][j], va, pt[t][0], pt[t][1]);
                     }
                 }
-                if (!clean) fence_proxy_async_smem();  // this warp wrote where the next copies land
+                fence_proxy_async_smem();  // (this warp read, and may have written, where the next copies land)
             }
             __syncwarp();
             if (it + 1 < tiles && lane == 0) mbar_arrive(&ctl->empty[s]);  // the last tile's slot is kept for the exchange
