@@ -564,6 +564,7 @@ tc_ws_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ C
                                  : "=r"(code.x), "=r"(code.y), "=r"(code.z), "=r"(code.w)
                                  : "r"(stage_c(cs) + uint32_t(pr) * 16)
                                  : "memory");
+                fence_proxy_async_smem();  // (read before the next copy may write there)
                 mbar_arrive(&ctl->codes_empty[cs]);
                 // decode into registers first, then wait for the slot
                 const __half2 d2 =
