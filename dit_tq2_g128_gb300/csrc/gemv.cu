@@ -562,7 +562,10 @@ gemv_stream_kernel(const __grid_constant__ CUtensorMap xmap, const uint8_t *__re
             // Release this chunk's share of the slot once all its reads are
             // done: right here when the block scales come from global memory,
             // after the scale reads below when they travel in the slot.
-            if (!dbulk) mbar_arrive(&empty[slot]);
+            if (!dbulk) {
+                fence_proxy_async_smem();  // (read before the next copy may write there)
+                mbar_arrive(&empty[slot]);
+            }
             // Per row: T = sum_i (c_i - 1) X_i over the lane's 32 weights, exact
             // in int32 (|T| <= 2^28).  Codes of weights t, t+4, t+8, t+12 of a
             // word are the bytes of (w >> 2t) & 0x03030303; each dp4a multiplies
@@ -620,7 +623,10 @@ gemv_stream_kernel(const __grid_constant__ CUtensorMap xmap, const uint8_t *__re
                                : __half2float(__ushort_as_half(ldg_u16(dpl + int64_t(real_row(r0 + uu)) * kb + dcol)));
                 fv[i] = active ? float(tv[i]) * (sc * dd) : 0.f;
             }
-            if (dbulk) mbar_arrive(&empty[slot]);
+            if (dbulk) {
+                fence_proxy_async_smem();
+                mbar_arrive(&empty[slot]);
+            }
             // float halving levels at offsets 4, 8, ... until one value is left, then full levels
 #pragma unroll
             for (int lv = 0; (VH >> lv) > 1; ++lv) {
@@ -895,7 +901,10 @@ gemv_wide_kernel(const __grid_constant__ CUtensorMap xmap, const uint8_t *__rest
 #pragma unroll
             for (int uu = 0; uu < RS; ++uu)
                 cw[uu] = *reinterpret_cast<const uint4 *>(sb + code_off + uint32_t(uu) * kq32);
-            if (!dbulk) mbar_arrive(&empty[slot]);
+            if (!dbulk) {
+                fence_proxy_async_smem();  // (read before the next copy may write there)
+                mbar_arrive(&empty[slot]);
+            }
             constexpr int V = RS <= 2 ? 2 : RS <= 4 ? 4 : 8;
             int tv[V];
 #pragma unroll
@@ -939,7 +948,10 @@ gemv_wide_kernel(const __grid_constant__ CUtensorMap xmap, const uint8_t *__rest
                                : __half2float(__ushort_as_half(ldg_u16(dpl + int64_t(real_row(r0 + uu)) * kb + dcol)));
                 fv[i] = float(tv[i]) * (sc * dd);
             }
-            if (dbulk) mbar_arrive(&empty[slot]);
+            if (dbulk) {
+                fence_proxy_async_smem();
+                mbar_arrive(&empty[slot]);
+            }
             // float halving levels at offsets 2, 4, ... until one value is left
 #pragma unroll
             for (int lv = 0; (VH >> lv) > 1; ++lv) {

@@ -31,7 +31,7 @@ def test_the_check_itself():
     assert not unfenced("x = *p;\nfence_proxy_async_smem();\nmbar_arrive(&ctl->empty[s]);", RINGS["attention_paged.cu"])
 
 
-SOURCES = ["moe_gemm.cu", "attention_paged.cu", "gemm_tc_ws.cu"]
+SOURCES = list(RINGS)
 
 
 @pytest.mark.parametrize("source", SOURCES)
