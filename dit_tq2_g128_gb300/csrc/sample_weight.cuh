@@ -1,8 +1,9 @@
 // The weight of a token in sampling, as an integer in units of 2^-45 of the likeliest token's.
 //
 // w = 2^-y, y = (max - l) log2(e) / temperature.  y is kept as a sum of two f32 (its error is 2^-46 of it), split into
-// n / 64 + t with |t| <= 1/128: 2^-(n/64) from a table, 2^-t - 1 by a short series in f32.  The series' rounding is
-// 2^-24 of a value below 0.0055, so that a weight is off by 2^-31 of itself: where a prefix's sum or a border falls
+// n / 64 + t with |t| <= 1/128: 2^-(n/64) from a table, 2^-t - 1 by a short series in f32.  The roundings of t, of the series
+// and of its product with the table's entry are half a step each of values below 0.0055: at most 5.5 * 2^-32 together, so that a
+// weight is within 2^-29.5 of itself (2^-31 as a rule) and half a unit.  Where a prefix's sum or a border falls
 // between two of a hundred thousand tokens is then what exact weights would say but for one case in some 10^5 (f32
 // weights would be off in one of hundreds).  The likeliest token's weight is exactly 2^45, and 2^18 of it fit 64 bits.
 #pragma once

@@ -623,8 +623,8 @@ typedef struct {
  *   tokens : device int64 [rows]
  *   prob   : device f32 [rows], or NULL
  *   vocab  : 1 .. 262144;  rows : up to 2^24
- * Weights are integers in units of 2^-45 (a smaller one is 0), each within 2^-30 of
- * itself; their sums are exact, so that results do not depend on any order of summation.
+ * Weights are integers in units of 2^-45 of the likeliest token's, each within 2^-29 of itself or, below 2^-17,
+ * within a unit; their sums are exact, so that results do not depend on any order of summation.
  * No output may overlap another argument.  rows == 0 is a no-op. */
 int tq2_sample(const void *logits, int dtype, int64_t row_stride, const float *u, const tq2_sampling *filters,
                int64_t *tokens, float *prob, int64_t rows, int64_t vocab, void *stream);
