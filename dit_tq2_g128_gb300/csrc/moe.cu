@@ -9,7 +9,7 @@
 // product are summed in their order (moe_sum_kernel): the same bits on every call.
 //
 // Bound by launches where tokens are few (one token of 6 experts: 19 us, five launches, of which the products are 10 + 8); of a
-// prompt of 4096 tokens (537 us) staging writes 134 MB in 35 us, the sum reads 268 MB in 62 us (what the product before it
+// prompt of 4096 tokens (531 us) staging writes 134 MB in 35 us, the sum reads 268 MB in 60 us (what the product before it
 // wrote is still on its way to memory), the products are the rest.
 #include <cstdint>
 
@@ -411,6 +411,17 @@ size_t pad(size_t n) { return (n + 255) & ~size_t(255); }
 //  * 16-bit activations of at most 16 rows an expert in the mean: three e4m3 terms (see moe.cuh).
 //  * Else one binary16 term, or two of f32 activations, and columns by the staged rows that experts have in the mean: with
 //    more columns codes are decoded less often, with fewer there is room for more decoded weights and more warps that decode.
+// Measured (us a call in a graph; e4m3 / 32 / 64 / 96 columns of binary16; A: 8 of 128 experts of 2048 x 768, bf16,
+// B: 2 of 8 of 4096 x 6144, f16, C: 2 of 16 of 1280 x 2816, f32):
+//   rows    1 (16 tokens, 4)          4                       8                       12                      16
+//   A   45 /  50 /  57 /  59    66 /  70 /  81 /  83    81 /  81 /  91 /  95    96 /  86 /  95 /  99   111 /  97 / 102 / 105
+//   B   60 /  66 /  79 /  80    74 /  81 /  98 / 100    78 /  83 /  99 / 100    87 /  85 / 100 / 101   102 /  87 / 101 / 103
+//   rows   24                         32                      48                      64                      96
+//   A  140 / 111 / 111 / 115   172 / 131 / 124 / 125   231 / 165 / 147 / 147   292 / 204 / 173 / 169   420 / 282 / 229 / 219
+//   B  147 /  97 / 105 / 107   171 / 116 / 108 / 110   223 / 154 / 122 / 120   277 / 171 / 146 / 132   378 / 238 / 197 / 173
+//   C (two terms)  1: 26 / 29 / 29   8: 39 / 40 / 41   16: 47 / 47 / 46   24: 59 / 53 / 54   32: 67 / 58 / 60   64: 104 / 83 / 80
+// Three terms pay up to 8 rows and cost 10 to 17 % at 12 to 16, where experts of more than 16 have a second tile; the border
+// stands at 16, up to which a token's result is then the same whatever the tokens beside it.
 struct Form {
     int terms, cols;
 };

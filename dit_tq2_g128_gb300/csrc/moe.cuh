@@ -48,9 +48,8 @@ cudaError_t launch_moe_gemm(const MoeGemm &g, bool gate_up, const LaunchCtx &ctx
 //   3: e4m3 numbers t0, t1, t2 with v = t0 + t1 / 16 + t2 / 256: each rounds to four bits what is left, so that they hold
 //      twelve: all of a binary16's or bf16's (down to 2^-25 of the largest value), and others to 2^-12.
 // Three 8-bit terms where experts have few tokens: an MMA of few columns takes as long for 32 weights of a row in 8 bits as
-// for 16 in 16 bits, and decoding to 8 bits is half the stores and no subtraction.  Measured against one binary16 term, the
-// whole call: 7 tokens, 2 of 8 experts of 4096 x 6144: 55.5 against 59.8 us; 64 tokens, 8 of 128 of 2048 x 768: 66.7 against
-// 67.7; one token of 6 of 64 of 2048 x 1408: 19.3 against 18.9.
+// for 16 in 16 bits, and decoding to 8 bits is half the stores and no subtraction.  Measured against one binary16 term: see
+// form_of in moe.cu (one token of 6 of 64 experts of 2048 x 1408: 19.3 against 18.9 us, a launch more).
 //
 // Scale of staged hidden values, which the first product stages before any of its row is known to all: a bound of them.
 // |Gate_f x| and |Up_f x| are at most 2 (code 3) times the sum over blocks of |d| times the block's sum of |x|, so that

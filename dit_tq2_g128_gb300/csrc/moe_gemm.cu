@@ -11,8 +11,10 @@
 //    by a byte permutation.  (Left as they are masked out, as subnormal binary16 numbers, codes would cost one instruction
 //    less a pair, but the tensor core aligns products by the operands' exponents: f32 sums were off by 1e-5.)
 //  * The block scale d stays out of the operands: each 128-weight block is a product of its own into an accumulator of its
-//    own, and d times it is added to the running sums in registers (f32).  So operands are exact, and what is rounded is
-//    the activations' staging and the sums.
+//    own, and d times it is added to the running sums in registers (f32).  e4m3 operands could not hold it; binary16 ones
+//    could ((c - 1) d is exact for any finite d, and for code 3 below 32768, as in the dense product, which sums all of K in tensor
+//    memory with 256 columns and reaches 1.2 PFLOP/s): one design serves both here, at the price of the summing groups, whose
+//    registers keep a tile to 96 columns.
 //  * Copies: codes by TMA, 512 weights of 128 rows a stage (96 KB in flight an SM); activations by TMA, a unit's features of a
 //    tile's rows in one copy (several, of 16 rows each, took their issuing lane longer than the block's MMAs).
 //  * Roles: warp 0 codes, warp 1 MMAs (owns tensor memory), warp 2 activations; two or three groups of four warps decode a
@@ -23,10 +25,10 @@
 //    MMAs before it leaves.
 //
 // Bound by the roles' turns: with every copy, decoding, MMA and sum taken out, what waits and hands on still takes 175 of a
-// prompt's 420 us (4096 tokens, 8 of 64 experts of 2048 x 1024, both products), and warps that poll for their turn take the
+// prompt's 410 us (4096 tokens, 8 of 64 experts of 2048 x 1024, both products), and warps that poll for their turn take the
 // others' issue slots (half of which are used: decoding is five instructions for eight weights of a thread's row and block
-// sums are one for two).  Measured, both products: 64 tokens, 8 of 128 experts of 2048 x 768 (160 MB): 34 + 22 us, 2.9 TB/s;
-// 7 tokens, 2 of 8 experts of 4096 x 6144 (160 MB): 30 + 23 us, 3.0 TB/s; the prompt 272 + 138 us, 1.0 PFLOP/s.
+// sums are one for two).  Measured, both products: 64 tokens, 8 of 128 experts of 2048 x 768 (160 MB): 35 + 23 us, 2.7 TB/s;
+// 7 tokens, 2 of 8 experts of 4096 x 6144 (160 MB): 30 + 24 us, 2.9 TB/s; the prompt 263 + 140 us, 1.02 PFLOP/s.
 #include <cstdint>
 
 #include "moe.cuh"

@@ -21,8 +21,8 @@
 // bf16 logits: 63 us); without one 55,000, of which the exact sums are a third, some 60 instructions a weight (16 flat rows of
 // 200,000: 40 us; 64 rows of 128,000 f32, a quarter without a top-k: 49 us, all: 71, of bf16 53, all with one of 2000: 92; one
 // such row 22).  The exact histogram in place of the guess, with
-// four shared atomics an element and two passes to collect, took 81 and 75 us.  64 registers a thread (two CTAs an SM), of which 1 to 13
-// are spilled, about the head and the guess.
+// four shared atomics an element and two passes to collect, took 81 and 75 us.  64 registers a thread, so that two CTAs share
+// an SM: 4 bytes a thread are spilled and read 32 times (bf16: 52 bytes, 42 times; by the compiler's count).
 #include <algorithm>
 #include <cstdint>
 

@@ -579,7 +579,7 @@ typedef struct {
  * S = sum |x| and P the largest product, over the expert's features, of the largest block scales of the gate row and
  * of the up row, or, if that is less, S the largest sum |x| of a block of 128 and P the largest product of the
  * rows' sums of block scales; of few rows an expert, 2^-12 of themselves or 2^-25 of the pair's largest.  (The
- * activation is within 2^-21 of itself in f32, and within 2^-18 for gates above -24 else.)  No
+ * activation is within 2^-21 of itself in f32 for gates above -87, and within 2^-18 for gates above -24 else.)  No
  * magnitude overflows on its way that the formula in f32 does not.  Sums in f32, one rounding to the
  * output's type.  A token's result may differ in its rounding with the
  * number of tokens of the call.
