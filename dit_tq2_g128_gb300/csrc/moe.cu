@@ -4,8 +4,7 @@
 // The (token, expert) pairs are sorted by expert, so that an expert's codes are read once for all its tokens; each pair's
 // activations are staged as terms that the tensor cores multiply (moe.cuh; moe_stage_kernel, which also sorts up to 1024
 // pairs; more are sorted by moe_plan_kernel).  The first product (moe_gemm.cu) ends in the SwiGLU and stages its hidden values
-// itself, scaled by a bound of them (moe.cuh); of few tokens it leaves them in f32, as
-// e4m3 terms want the rows' largest values, and they are staged like the activations.  Each token's pairs of the second
+// itself, scaled by a bound of them (moe.cuh); of few tokens it leaves them in f32, as e4m3 terms want the rows' largest values, and they are staged like the activations.  Each token's pairs of the second
 // product are summed in their order (moe_sum_kernel): the same bits on every call.
 //
 // Bound by launches where tokens are few (one token of 6 experts: 19 us, five launches, of which the products are 10 + 8); of a
@@ -143,8 +142,8 @@ struct StageArgs {
 // moe.cuh).  PAIRS: the rows are of pairs already (hidden values).
 // ROUTE: the pairs (at most kFewPairs) are not sorted yet: each token's block finds the rows of its pairs by counting those
 // before them, and the first block behind the tokens' writes the tiles.
-// At most 32 registers where tokens are few: beside a product's CTA an SM has 4096 left, so that blocks begin while the kernel before ends, and
-// the next product's CTAs beside them (with 36, 7 tokens of 8 experts of 4096 x 6144 took 65 us, not 55).
+// At most 32 registers where tokens are few: beside a product's CTA an SM has 4096 left, so that blocks begin while the kernel
+// before ends, and the next product's CTAs beside them (with 36, 7 tokens of 8 experts of 4096 x 6144 took 65 us, not 55).
 template <typename T, bool F8, bool PAIRS, bool ROUTE>
 __global__ void __launch_bounds__(kStageThreads, ROUTE || F8 ? 16 : 12) moe_stage_kernel(const T *__restrict__ x, const StageArgs a) {
     extern __shared__ uint4 bound_scales[];
