@@ -4,8 +4,9 @@
 // The (token, expert) pairs are sorted by expert, so that an expert's codes are read once for all its tokens; each pair's
 // activations are staged as terms that the tensor cores multiply (moe.cuh; moe_stage_kernel, which also sorts up to 1024
 // pairs; more are sorted by moe_plan_kernel).  The first product (moe_gemm.cu) ends in the SwiGLU and stages its hidden values
-// itself, scaled by a bound of them (moe.cuh); of few tokens it leaves them in f32, as e4m3 terms want the rows' largest values, and they are staged like the activations.  Each token's pairs of the second
-// product are summed in their order (moe_sum_kernel): the same bits on every call.
+// itself, scaled by a bound of them (moe.cuh); of few tokens it leaves them in f32, as e4m3 terms want the rows' largest
+// values, and they are staged like the activations.  Each token's pairs of the second product are summed in their order
+// (moe_sum_kernel): the same bits on every call.
 //
 // Bound by launches where tokens are few (one token of 6 experts: 19 us, five launches, of which the products are 10 + 8); of a
 // prompt of 4096 tokens (531 us) staging writes 134 MB in 35 us, the sum reads 268 MB in 60 us (what the product before it
